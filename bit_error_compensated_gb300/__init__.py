@@ -10,7 +10,8 @@ _BINDING_NAMES = (
     "echo_comp_bytes", "echo_wire_bytes", "echo_wire_layout", "echo_get_status",
     "echo_debug_wire", "echo_plan_destroy", "echo_strerror", "echo_set_fused",
     "echo_set_timing", "echo_set_quantizer", "echo_allreduce_noalloc", "Plan", "EchoError",
-    "COMP_DEFAULT",
+    "COMP_DEFAULT", "echo_norm_plan", "echo_norm_plan_destroy", "echo_norm", "echo_norm_backward",
+    "echo_quantize_tokens", "echo_matmul_int8", "echo_linear_int8", "NormPlan", "NormParams",
 )
 
 

@@ -19,12 +19,18 @@ ROOT = PKG.parent
 CSRC = PKG / "csrc"
 LIBDIR = PKG / "lib"
 LIB = LIBDIR / "libecho.so"
-# (source, group size it is compiled for, or None).  Every kernel source is
-# compiled once per supported group size; the objects compile in parallel.
+# (source, suffix and definition it is compiled with, or None).  Every kernel
+# source of the all-reduce is compiled once per supported group size, those of
+# the residual join once per element type (the ECHO_F32, ECHO_BF16, ECHO_F16
+# numbers); the objects compile in parallel.
 GROUPS = (64, 128, 256)
-SOURCES = [("echo_api.cu", None), ("echo_noalloc.cu", None)] + [
-    (src, g) for src in ("k_push.cu", "k_reduce.cu", "k_gather.cu", "k_call.cu", "k_tile.cu")
-    for g in GROUPS]
+TYPES = (0, 1, 2)
+SOURCES = [(src, None) for src in ("echo_api.cu", "echo_noalloc.cu", "norm_api.cu", "int8_api.cu",
+                                   "int8_quantize.cu", "int8_product.cu")] + [
+    (src, (f"_g{g}", f"-DECHO_G={g}"))
+    for src in ("k_push.cu", "k_reduce.cu", "k_gather.cu", "k_call.cu", "k_tile.cu")
+    for g in GROUPS] + [
+    (src, (f"_t{t}", f"-DECHO_T={t}")) for src in ("norm_fwd.cu", "norm_bwd.cu") for t in TYPES]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -62,10 +68,10 @@ def build_library(force: bool = False, ptxas_verbose: bool = False) -> Path:
     objdir.mkdir(parents=True, exist_ok=True)
     LIBDIR.mkdir(exist_ok=True)
     procs = []
-    for src, g in SOURCES:
-        stem = Path(src).stem + ("" if g is None else f"_g{g}")
+    for src, variant in SOURCES:
+        stem = Path(src).stem + (variant[0] if variant else "")
         obj = objdir / (stem + ".o")
-        defs = [] if g is None else [f"-DECHO_G={g}"]
+        defs = [variant[1]] if variant else []
         cmd = [cc, *_flags(ptxas_verbose), *defs, "-c", str(CSRC / src), "-o", str(obj)]
         procs.append((stem, obj, subprocess.Popen(cmd, stdout=subprocess.PIPE,
                                                  stderr=subprocess.STDOUT, text=True)))

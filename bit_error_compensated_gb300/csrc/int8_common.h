@@ -1,0 +1,42 @@
+// int8_common.h -- launch arguments of the 8-bit product and its token
+// quantizer (int8_*.cu).  The operators are described in include/echo.h.
+#pragma once
+
+#include "ops_common.h"
+
+namespace echo {
+
+struct QuantArgs {
+  const void* x;
+  int64_t ld_x, rank_x;
+  int8_t* codes;
+  int64_t ld_codes, rank_codes;
+  float* scales;                 // [ranks][tokens]
+  int64_t ranks, tokens, depth;
+};
+
+struct ProductArgs {
+  const int8_t* a;               // [ranks][tokens][depth]
+  int64_t ld_a, rank_a;
+  const float* a_scales;
+  int64_t rank_a_scales;
+  const int8_t* w;               // [ranks][channels][depth]
+  int64_t ld_w, rank_w;
+  const float* w_scales;
+  int64_t rank_w_scales;
+  void* out;                     // [ranks][tokens][channels]
+  int64_t ld_out, rank_out;
+  int64_t ranks, tokens, channels, depth;
+  int out_dtype;
+};
+
+// The value of an exact sum: fp32 products by the token's, then the channel's
+// scale, in this order everywhere, so that every kernel gives the same bits.
+__device__ __forceinline__ float scaled_sum(int sum, float token, float channel) {
+  return __fmul_rn(__fmul_rn(__int2float_rn(sum), token), channel);
+}
+
+cudaError_t launch_quantize(const QuantArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_product(const ProductArgs& a, cudaStream_t s);
+
+}  // namespace echo

@@ -1,0 +1,91 @@
+// int8_quantize.cu -- echo_quantize_tokens: one int8 scale a token
+// (include/echo.h).
+//
+//     amax = max(2^-110, max |x|),  codes = rint(x * (127 / amax)),  scale = amax / 127
+//
+// One block a row.  The row is read once: its elements wait for the maximum in
+// registers; a row longer than the block's registers is read again instead.
+// It is bound by those bytes.
+#include "int8_common.h"
+
+namespace echo {
+namespace {
+
+constexpr int kPieces = 4;             // 16-byte pieces (or elements) a thread holds
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(1024)
+quantize_kernel(const QuantArgs a) {
+  __shared__ uint32_t maxima[32];
+  const int64_t row = blockIdx.x;
+  const int64_t rank = row / a.tokens, token = row - rank * a.tokens;
+  const T* x = static_cast<const T*>(a.x) + rank * a.rank_x + token * a.ld_x;
+  int8_t* codes = a.codes + rank * a.rank_codes + token * a.ld_codes;
+  const int64_t step = (int64_t)blockDim.x * VEC;
+  const int64_t col0 = (int64_t)threadIdx.x * VEC;
+  pdl_wait();
+
+  Pack<T, VEC> held[kPieces];
+  uint32_t amax = __float_as_uint(kTinyAmax);
+  auto take = [&](const Pack<T, VEC>& p) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) amax = max(amax, abs_bits(to_float(p.v[i])));
+  };
+#pragma unroll
+  for (int j = 0; j < kPieces; ++j)
+    if (col0 + j * step < a.depth) held[j] = load_pack<T, VEC>(x + col0 + j * step);
+#pragma unroll
+  for (int j = 0; j < kPieces; ++j)
+    if (col0 + j * step < a.depth) take(held[j]);
+  for (int64_t c = col0 + kPieces * step; c < a.depth; c += step) take(load_pack<T, VEC>(x + c));
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
+  if ((threadIdx.x & 31) == 0) maxima[threadIdx.x >> 5] = amax;
+  __syncthreads();
+  for (int i = 0; i < (int)blockDim.x / 32; ++i) amax = max(amax, maxima[i]);
+  const float top = __uint_as_float(amax), inv = __fdiv_rn(127.f, top);
+
+  auto put = [&](int64_t c, const Pack<T, VEC>& p) {
+    Pack<int8_t, VEC> q;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) q.v[i] = (int8_t)quantize_code(to_float(p.v[i]), inv);
+    if constexpr (VEC == 8) *reinterpret_cast<uint2*>(codes + c) = *reinterpret_cast<const uint2*>(&q);
+    else if constexpr (VEC == 4)
+      *reinterpret_cast<uint32_t*>(codes + c) = *reinterpret_cast<const uint32_t*>(&q);
+    else codes[c] = q.v[0];
+  };
+#pragma unroll
+  for (int j = 0; j < kPieces; ++j)
+    if (col0 + j * step < a.depth) put(col0 + j * step, held[j]);
+  for (int64_t c = col0 + kPieces * step; c < a.depth; c += step) put(c, load_pack<T, VEC>(x + c));
+  if (threadIdx.x == 0) a.scales[row] = __fdiv_rn(top, 127.f);
+}
+
+template <typename T, int VEC>
+cudaError_t launch(const QuantArgs& a, cudaStream_t s) {
+  int64_t threads = (a.depth + 2 * VEC - 1) / (2 * VEC);
+  threads = threads > 1024 ? 1024 : threads < 32 ? 32 : (threads + 31) / 32 * 32;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.ranks * a.tokens));
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = s;
+  return cudaLaunchKernelEx(&cfg, quantize_kernel<T, VEC>, a);
+}
+
+template <typename T>
+cudaError_t pick(const QuantArgs& a, cudaStream_t s) {
+  constexpr int V = 16 / sizeof(T);
+  const int64_t size = sizeof(T);
+  const bool vec = on_boundary(a.x, 16) && on_boundary(a.codes, V) && a.depth % V == 0 &&
+                   (a.tokens == 1 || (a.ld_x * size % 16 == 0 && a.ld_codes % V == 0)) &&
+                   (a.ranks == 1 || (a.rank_x * size % 16 == 0 && a.rank_codes % V == 0));
+  return vec ? launch<T, V>(a, s) : launch<T, 1>(a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_quantize(const QuantArgs& a, int dtype, cudaStream_t s) {
+  return dtype == ECHO_F32 ? pick<float>(a, s) : dtype == ECHO_BF16 ? pick<__nv_bfloat16>(a, s) : pick<__half>(a, s);
+}
+
+}  // namespace echo

@@ -1,0 +1,88 @@
+// norm_common.h -- launch arguments of the residual join (norm_fwd.cu,
+// norm_bwd.cu) and its block-wide sums.  The operator is described in
+// include/echo.h (echo_norm_plan).
+#pragma once
+
+#include "ops_common.h"
+
+namespace echo {
+
+struct NormArgs {
+  int64_t rows;
+  int width;
+  const void *x, *y, *gate;
+  int64_t ld_x, ld_y;
+  int64_t gate_span;             // rows that share a gate row
+  const void *w_post, *b_post, *w_pre, *b_pre;
+  void *r, *h;
+  int64_t ld_r, ld_h;
+  int8_t* codes;
+  int64_t ld_codes;
+  float *scales, *stats;
+  float eps, scale;
+  int gate_scalar;               // one gate value a row instead of `width`
+  int post;                      // the norm after the block is there (and y is)
+  int params_f32;                // parameters and gate are fp32 (else the rows' type)
+};
+
+struct NormGradArgs {
+  int64_t rows;
+  int width;
+  const void *x, *y, *gate;
+  int64_t ld_x, ld_y;
+  int64_t gate_span;
+  const void *w_post, *b_post, *w_pre;
+  const float* stats;
+  const void *dr, *dh;
+  int64_t ld_dr, ld_dh;
+  void *dx, *dy, *dgate;
+  int64_t ld_dx, ld_dy;
+  void* dparam[4];               // w_post, b_post, w_pre, b_pre
+  float* partial[4];             // [workers][width] sums of each, or nullptr
+  float* gate_partial;           // [workers][2][width or 1], see norm_bwd.cu
+  int64_t span;                  // rows a worker takes
+  int64_t workers;
+  float scale;
+  int gate_scalar, post, params_f32;
+};
+
+// N floats of a parameter vector (or gate row) of either type, from element
+// `col`; `missing` where there is none.
+template <typename T, int N>
+__device__ __forceinline__ void load_param(const void* p, int f32, int64_t col, float missing,
+                                           float (&out)[N]) {
+  if (p == nullptr) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) out[i] = missing;
+  } else if (sizeof(T) == 4 || f32) {
+    const Pack<float, N> v = load_pack<float, N>(static_cast<const float*>(p) + col);
+#pragma unroll
+    for (int i = 0; i < N; ++i) out[i] = v.v[i];
+  } else {
+    const Pack<T, N> v = load_pack<T, N>(static_cast<const T*>(p) + col);
+#pragma unroll
+    for (int i = 0; i < N; ++i) out[i] = to_float(v.v[i]);
+  }
+}
+
+// Launchers, one instantiation per element type (norm_fwd.cu and norm_bwd.cu
+// are compiled once for each).  `vec`: 16-byte accesses are possible.
+template <typename T>
+cudaError_t launch_norm(const NormArgs& a, int layer, bool vec, int sms, cudaStream_t s);
+template <typename T>
+cudaError_t launch_norm_grad(NormGradArgs a, int layer, bool vec, int sms, cudaStream_t s);
+// Workers (row ranges with their own partial sums) a backward call may have:
+// two blocks an SM, of up to 4 rows at once where a row takes less than 128 threads.
+inline int64_t norm_grad_max_workers(int width, int sms) {
+  return (int64_t)2 * sms * (width <= 128 * 16 ? 4 : 1);
+}
+
+}  // namespace echo
+
+#if ECHO_T == 0
+#define ECHO_ELEM float
+#elif ECHO_T == 1
+#define ECHO_ELEM __nv_bfloat16
+#elif ECHO_T == 2
+#define ECHO_ELEM __half
+#endif

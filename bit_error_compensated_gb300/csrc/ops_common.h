@@ -1,0 +1,139 @@
+// ops_common.h -- shared by the operators around the all-reduce (norm_*.cu,
+// int8_*.cu): element types, vector accesses, block sums, argument checks.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <cstdlib>
+
+#include "../../include/echo.h"
+
+namespace echo {
+
+int note_cuda_error(cudaError_t e);    // echo_api.cu
+
+#define ECHO_OPS_CUDA(call)                                    \
+  do {                                                         \
+    cudaError_t e_ = (call);                                   \
+    if (e_ != cudaSuccess) {                                   \
+      cudaGetLastError();   /* the caller's next check is not this call's */ \
+      return echo::note_cuda_error(e_);                        \
+    }                                                          \
+  } while (0)
+
+// ------------------------------------------------------------------ device
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
+template <typename T> __device__ __forceinline__ T from_float(float v);
+template <> __device__ __forceinline__ float from_float<float>(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) {
+  return __float2bfloat16_rn(v);
+}
+template <> __device__ __forceinline__ __half from_float<__half>(float v) {
+  return __float2half_rn(v);
+}
+
+// N contiguous elements as they lie in memory, moved in 16-byte pieces (N * size a
+// multiple of 16, 16-byte aligned) or, for N == 1, as one element.
+template <typename T, int N>
+struct __align__(sizeof(T) * N >= 16 ? 16 : sizeof(T) * N) Pack {
+  T v[N];
+};
+
+template <typename T, int N>
+__device__ __forceinline__ Pack<T, N> load_pack(const T* p) {
+  Pack<T, N> out;
+  if constexpr (N * sizeof(T) >= 16) {
+    const uint4* src = reinterpret_cast<const uint4*>(p);
+    uint4* dst = reinterpret_cast<uint4*>(&out);
+#pragma unroll
+    for (int i = 0; i < (int)(N * sizeof(T) / 16); ++i) dst[i] = src[i];
+  } else {
+    static_assert(N == 1, "packs are 16-byte pieces or single elements");
+    out.v[0] = p[0];
+  }
+  return out;
+}
+
+template <typename T, int N>
+__device__ __forceinline__ void store_pack(T* p, const Pack<T, N>& in) {
+  if constexpr (N * sizeof(T) >= 16) {
+    const uint4* src = reinterpret_cast<const uint4*>(&in);
+#pragma unroll
+    for (int i = 0; i < (int)(N * sizeof(T) / 16); ++i) reinterpret_cast<uint4*>(p)[i] = src[i];
+  } else {
+    p[0] = in.v[0];
+  }
+}
+
+template <typename T, int N>
+__device__ __forceinline__ void store_floats(T* p, const float (&v)[N]) {
+  Pack<T, N> out;
+#pragma unroll
+  for (int i = 0; i < N; ++i) out.v[i] = from_float<T>(v[i]);
+  store_pack<T, N>(p, out);
+}
+
+// Programmatic dependent launch: wait for the kernels this launch depends on,
+// and let the next kernel's blocks be placed.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_trigger() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// The smallest amax a quantized row is scaled by.
+constexpr float kTinyAmax = 7.703719777548943e-34f;   // 2^-110
+// The largest |v| of a row as the bits of a float: unlike fmaxf this keeps
+// NaNs (their bits are above infinity's).
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+// rint(v * inv) for |v| * inv <= 127 (with inv = 127 / amax, rounded); 0 for NaN.
+__device__ __forceinline__ int quantize_code(float v, float inv) {
+  return __float2int_rn(__fmul_rn(v, inv));
+}
+
+// -------------------------------------------------------------------- host
+inline int elem_size(int dtype) { return dtype == ECHO_F32 ? 4 : 2; }
+inline bool known_dtype(int dtype) {
+  return dtype == ECHO_F32 || dtype == ECHO_BF16 || dtype == ECHO_F16;
+}
+inline bool on_boundary(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+// A strided matrix in memory: `rows` rows of `bytes` bytes, `pitch` bytes apart.
+struct Region {
+  uintptr_t at = 0;
+  int64_t rows = 0, bytes = 0, pitch = 0;
+};
+inline Region region(const void* p, int64_t rows, int64_t cols, int64_t ld, int size) {
+  Region r;
+  if (p == nullptr || rows <= 0 || cols <= 0) return r;
+  r.at = (uintptr_t)p;
+  r.rows = rows;
+  r.bytes = cols * size;
+  r.pitch = ld * size;
+  return r;
+}
+// Whether two matrices may share a byte.  Columns of one matrix, or rows of
+// different tensors that alternate, do not: exact where the pitches are equal,
+// by the whole ranges otherwise.
+inline bool overlaps(const Region& a, const Region& b) {
+  if (a.rows == 0 || b.rows == 0) return false;
+  const uintptr_t ea = a.at + (uintptr_t)((a.rows - 1) * a.pitch + a.bytes);
+  const uintptr_t eb = b.at + (uintptr_t)((b.rows - 1) * b.pitch + b.bytes);
+  if (ea <= b.at || eb <= a.at) return false;
+  if (a.pitch == b.pitch && a.pitch > 0) {
+    const bool first = a.at <= b.at;
+    const int64_t d = (int64_t)((first ? b.at - a.at : a.at - b.at) % (uintptr_t)a.pitch);
+    const int64_t low = first ? a.bytes : b.bytes, high = first ? b.bytes : a.bytes;
+    if (d >= low && a.pitch - d >= high) return false;
+  }
+  return true;
+}
+inline bool same(const Region& a, const Region& b) {
+  return a.at == b.at && a.rows == b.rows && a.bytes == b.bytes && (a.pitch == b.pitch || a.rows == 1);
+}
+
+}  // namespace echo

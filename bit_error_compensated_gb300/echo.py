@@ -39,8 +39,39 @@ ECHO_STATE_F32 = 0
 ECHO_STATE_BF16 = 1
 ECHO_STATE_F16 = 2
 COMP_DEFAULT = ctypes.c_void_p(-1 & (2 ** 64 - 1))   # ECHO_COMP_DEFAULT
+ECHO_F32 = 0
+ECHO_BF16 = 1
+ECHO_F16 = 2
+ECHO_NORM_RMS = 0
+ECHO_NORM_LAYER = 1
+ECHO_NORM_MAX_WIDTH = 16384
+ECHO_MATMUL_MAX_DEPTH = 131071
 
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+
+
+class _NormParams(ctypes.Structure):           # echo_norm_params
+    _fields_ = [(n, _vp) for n in ("w_post", "b_post", "w_pre", "b_pre")]
+
+
+class _NormIo(ctypes.Structure):               # echo_norm_io
+    _fields_ = [("rows", _i64), ("x", _vp), ("ld_x", _i64), ("y", _vp), ("ld_y", _i64),
+                ("gate", _vp), ("gate_rows", _i64), ("gate_cols", _i64),
+                ("r", _vp), ("ld_r", _i64), ("h", _vp), ("ld_h", _i64),
+                ("codes", _vp), ("ld_codes", _i64), ("scales", _vp), ("stats", _vp)]
+
+
+class _NormGradIo(ctypes.Structure):           # echo_norm_grad_io
+    _fields_ = [("rows", _i64), ("x", _vp), ("ld_x", _i64), ("y", _vp), ("ld_y", _i64),
+                ("gate", _vp), ("gate_rows", _i64), ("gate_cols", _i64), ("stats", _vp),
+                ("dr", _vp), ("ld_dr", _i64), ("dh", _vp), ("ld_dh", _i64),
+                ("dx", _vp), ("ld_dx", _i64), ("dy", _vp), ("ld_dy", _i64), ("dgate", _vp)]
+
+
+class _Matrix(ctypes.Structure):               # echo_matrix
+    _fields_ = [("data", _vp), ("ld", _i64), ("rank_stride", _i64)]
+
+
 _SIGS = {
     "echo_plan": (_i32, [_i32, _i64, _i32, _i32, ctypes.POINTER(_vp)]),
     "echo_allreduce": (_i32, [_vp, ctypes.POINTER(_vp), ctypes.POINTER(_vp), _vp, _vp]),
@@ -63,6 +94,20 @@ _SIGS = {
     "echo_allreduce_noalloc": (_i32, [_i32, _i64, _i32, ctypes.POINTER(_vp), ctypes.POINTER(_vp),
                                       _vp, _vp]),
     "echo_plan_destroy": (None, [_vp]),
+    "echo_norm_plan": (_i32, [_i64, _i32, _i32, _i32, _i32, ctypes.c_float, ctypes.c_float,
+                              ctypes.POINTER(_vp)]),
+    "echo_norm_plan_destroy": (None, [_vp]),
+    "echo_norm": (_i32, [_vp, ctypes.POINTER(_NormParams), ctypes.POINTER(_NormIo), _vp]),
+    "echo_norm_backward": (_i32, [_vp, ctypes.POINTER(_NormParams), ctypes.POINTER(_NormGradIo),
+                                  ctypes.POINTER(_NormParams), _vp]),
+    "echo_quantize_tokens": (_i32, [_i64, _i64, _i64, _i32, ctypes.POINTER(_Matrix),
+                                    ctypes.POINTER(_Matrix), _vp, _vp]),
+    "echo_matmul_int8": (_i32, [_i64, _i64, _i64, _i64, ctypes.POINTER(_Matrix), _vp, _i64,
+                                ctypes.POINTER(_Matrix), _vp, _i64, _i32,
+                                ctypes.POINTER(_Matrix), _vp]),
+    "echo_linear_int8": (_i32, [_i64, _i64, _i64, _i64, _i32, ctypes.POINTER(_Matrix),
+                                ctypes.POINTER(_Matrix), _vp, _i64, ctypes.POINTER(_Matrix), _vp,
+                                ctypes.POINTER(_Matrix), _vp]),
     "echo_strerror": (ctypes.c_char_p, [_i32]),
 }
 for _name, (_res, _args) in _SIGS.items():
@@ -308,6 +353,277 @@ def echo_plan_destroy(plan: Plan) -> None:
     h, plan.handle = plan.handle, None
     if h:
         _lib.echo_plan_destroy(h)
+
+
+# ---------------------------------------------------------------------------
+# The operators on either side of the all-reduce.  Their arguments are tensors
+# (strides and sizes are read from them); outputs are the caller's buffers.
+
+def _dtype_code(dtype) -> int:
+    import torch
+    code = {torch.float32: ECHO_F32, torch.bfloat16: ECHO_BF16, torch.float16: ECHO_F16}.get(dtype)
+    if code is None:
+        raise ValueError(f"dtype {dtype}, expected float32, bfloat16 or float16")
+    return code
+
+
+def _expect(t, what: str, dtype, shape) -> None:
+    """dtype, shape and unit stride along the last dimension."""
+    if t.dtype != dtype:
+        raise ValueError(f"{what}: dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {shape}")
+    if shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{what}: elements of a row must be contiguous")
+
+
+def _expect_contiguous(t, what: str, dtype, shape) -> None:
+    _expect(t, what, dtype, shape)
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: tensor must be contiguous")
+
+
+def _on_device(device: int | None, *tensors) -> None:
+    """Every tensor on the device that the call runs on: the current one."""
+    import torch
+    for t in tensors:
+        if t is not None and not t.is_cuda:
+            raise ValueError("tensor must be on a CUDA device")
+    current = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != current:
+            raise ValueError(f"tensor on cuda:{t.get_device()}, but the current device is cuda:{current}")
+    if device is not None and device != current:
+        raise ValueError(f"the plan belongs to cuda:{device}, but the current device is cuda:{current}")
+
+
+def _at(t) -> tuple:
+    """(address, row distance) of a matrix, or (None, 0)."""
+    return (None, 0) if t is None else (t.data_ptr(), t.stride(0))
+
+
+class NormPlan:
+    """Owning handle of an echo_norm_plan_t; frees the plan when collected."""
+
+    def __init__(self, handle, width, dtype, param_dtype, kind, post, device):
+        self.handle = handle
+        self.width, self.dtype, self.param_dtype = width, dtype, param_dtype
+        self.kind, self.post, self.device = kind, post, device
+
+    def __del__(self):
+        h, self.handle = getattr(self, "handle", None), None
+        if h:
+            _lib.echo_norm_plan_destroy(h)
+
+    @property
+    def _as_parameter_(self):
+        return ctypes.c_void_p(self.handle)
+
+
+def echo_norm_plan(width: int, dtype, param_dtype=None, kind: int = ECHO_NORM_RMS, post: bool = True,
+                   eps: float = 1e-6, scale: float = 1.0) -> NormPlan:
+    """A residual join (include/echo.h): rows of `width` elements of `dtype`,
+    parameters and gate of `param_dtype` (dtype if None, or torch.float32)."""
+    import torch
+    param_dtype = dtype if param_dtype is None else param_dtype
+    h = _vp()
+    _check(_lib.echo_norm_plan(width, _dtype_code(dtype), _dtype_code(param_dtype), kind, int(post),
+                               eps, scale, ctypes.byref(h)), "echo_norm_plan")
+    return NormPlan(h.value, width, dtype, param_dtype, kind, bool(post), torch.cuda.current_device())
+
+
+def echo_norm_plan_destroy(plan: NormPlan) -> None:
+    h, plan.handle = plan.handle, None
+    if h:
+        _lib.echo_norm_plan_destroy(h)
+
+
+class NormParams:
+    """The weights and biases of a plan's norms (or their gradients), checked
+    once: contiguous tensors of `width` elements of the plan's param_dtype, or
+    None.  Keeps the tensors; their addresses are taken once."""
+
+    __slots__ = ("_keep", "_struct")
+
+    def __init__(self, plan: NormPlan, w_post=None, b_post=None, w_pre=None, b_pre=None):
+        self._keep = (w_post, b_post, w_pre, b_pre)
+        for t, what in zip(self._keep, ("w_post", "b_post", "w_pre", "b_pre")):
+            if t is not None:
+                _expect_contiguous(t, what, plan.param_dtype, (plan.width,))
+        if any(t is not None for t in self._keep):
+            _on_device(plan.device, *self._keep)
+        self._struct = _NormParams(*[None if t is None else t.data_ptr() for t in self._keep])
+
+
+def _norm_gate(plan: NormPlan, gate, dgate, rows: int) -> tuple:
+    """(address, rows, columns) of a gate of [rows or fewer][width or 1]."""
+    if gate is None:
+        if dgate is not None:
+            raise ValueError("dgate without gate")
+        return None, 0, 0
+    shape = tuple(gate.shape)
+    if len(shape) != 2 or shape[1] not in (plan.width, 1) or shape[0] < 1 or rows % shape[0]:
+        raise ValueError(f"gate: shape {shape}, expected (rows of which {rows} is a multiple, "
+                         f"{plan.width} or 1)")
+    _expect_contiguous(gate, "gate", plan.param_dtype, shape)
+    if dgate is not None:
+        _expect_contiguous(dgate, "dgate", plan.param_dtype, shape)
+    return gate.data_ptr(), shape[0], shape[1]
+
+
+def echo_norm(plan: NormPlan, params: NormParams | None, x, y=None, r=None, h=None, gate=None,
+              codes=None, scales=None, stats=None, stream=None) -> None:
+    """x, y, r, h: [rows][width] tensors of the plan's dtype, any row distance
+    (y, r, h may be None); gate: [gate rows][width or 1]; codes int8
+    [rows][width] with scales fp32 [rows]; stats fp32 [rows][4]."""
+    if x.dim() != 2:
+        raise ValueError(f"x: shape {tuple(x.shape)}, expected (rows, {plan.width})")
+    rows = x.shape[0]
+    shape, dtype = (rows, plan.width), plan.dtype
+    _expect(x, "x", dtype, shape)
+    if y is not None:
+        _expect(y, "y", dtype, shape)
+    if r is not None:
+        _expect(r, "r", dtype, shape)
+    if h is not None:
+        _expect(h, "h", dtype, shape)
+    if (codes is None) != (scales is None):
+        raise ValueError("codes and scales belong together")
+    if codes is not None:
+        import torch
+        _expect(codes, "codes", torch.int8, shape)
+        _expect_contiguous(scales, "scales", torch.float32, (rows,))
+    if stats is not None:
+        import torch
+        _expect_contiguous(stats, "stats", torch.float32, (rows, 4))
+    gate_args = _norm_gate(plan, gate, None, rows)
+    _on_device(plan.device, x, y, r, h, gate, codes, scales, stats)
+    io = _NormIo(rows, *_at(x), *_at(y), *gate_args, *_at(r), *_at(h), *_at(codes), _ptr(scales),
+                 _ptr(stats))
+    _check(_lib.echo_norm(plan, None if params is None else params._struct, io, _stream(stream)),
+           "echo_norm")
+
+
+def echo_norm_backward(plan: NormPlan, params: NormParams | None, x, y, stats, dr, dh, dx=None,
+                       dy=None, grads: NormParams | None = None, gate=None, dgate=None,
+                       stream=None) -> None:
+    """x, y, gate, stats as in the forward call; dr, dh: gradients of r and h
+    (either may be None); dx, dy, dgate and grads (a NormParams of the plan
+    holding the tensors to write) receive the gradients."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError(f"x: shape {tuple(x.shape)}, expected (rows, {plan.width})")
+    rows = x.shape[0]
+    shape = (rows, plan.width)
+    for t, what in ((x, "x"), (y, "y"), (dr, "dr"), (dh, "dh"), (dx, "dx"), (dy, "dy")):
+        if t is not None:
+            _expect(t, what, plan.dtype, shape)
+    if stats is not None:
+        _expect_contiguous(stats, "stats", torch.float32, (rows, 4))
+    gate_args = _norm_gate(plan, gate, dgate, rows)
+    _on_device(plan.device, x, y, stats, dr, dh, dx, dy, gate, dgate)
+    io = _NormGradIo(rows, *_at(x), *_at(y), *gate_args, _ptr(stats), *_at(dr), *_at(dh), *_at(dx),
+                     *_at(dy), _ptr(dgate))
+    _check(_lib.echo_norm_backward(plan, None if params is None else params._struct, io,
+                                   None if grads is None else grads._struct, _stream(stream)),
+           "echo_norm_backward")
+
+
+def _matrix(t, ranks: int) -> _Matrix:
+    """A [ranks][rows][cols] tensor, or a [rows][cols] one that all ranks share."""
+    if t.dim() == 2:
+        return _Matrix(t.data_ptr(), t.stride(0), 0)
+    return _Matrix(t.data_ptr(), t.stride(1), t.stride(0) if ranks > 1 else 0)
+
+
+def _batch(t, what: str) -> tuple:
+    """(ranks or None, rows, columns) of a two- or three-dimensional tensor."""
+    if t.dim() == 2:
+        return (None, *t.shape)
+    if t.dim() == 3:
+        return tuple(t.shape)
+    raise ValueError(f"{what}: shape {tuple(t.shape)}, expected two or three dimensions")
+
+
+def _with_ranks(t, shape: tuple) -> tuple:
+    """The shape expected of an input that may be shared by the ranks."""
+    return shape if t.dim() == len(shape) else shape[1:]
+
+
+def _check_product(codes_like, w, w_scales, out) -> tuple:
+    """(ranks, tokens, channels, depth) of a product, its tensors checked
+    (those of the tokens' side apart from their last dimension's type)."""
+    import torch
+    ranks, tokens, channels = _batch(out, "out")
+    ranks = 1 if ranks is None else ranks
+    depth = w.shape[-1]
+    full = (ranks, tokens, depth)
+    if tuple(codes_like.shape) not in (full, full[1:]):
+        raise ValueError(f"tokens: shape {tuple(codes_like.shape)}, expected {full} or {full[1:]}")
+    _batch(w, "w")
+    _expect(w, "w", torch.int8, _with_ranks(w, (ranks, channels, depth)))
+    if w_scales.dim() not in (1, 2):
+        raise ValueError(f"w_scales: shape {tuple(w_scales.shape)}, expected one or two dimensions")
+    _expect(w_scales, "w_scales", torch.float32,
+            (ranks, channels) if w_scales.dim() == 2 else (channels,))
+    _expect(out, "out", out.dtype, (ranks, tokens, channels) if out.dim() == 3 else (tokens, channels))
+    return ranks, tokens, channels, depth
+
+
+def echo_quantize_tokens(x, codes, scales, stream=None) -> None:
+    """x [ranks][tokens][depth] (or [tokens][depth]) to int8 codes of the same
+    shape and one fp32 scale a token, [ranks][tokens] contiguous."""
+    import torch
+    ranks, tokens, depth = _batch(x, "x")
+    shape = tuple(x.shape)
+    _expect(x, "x", x.dtype, shape)
+    _expect(codes, "codes", torch.int8, shape)
+    _expect_contiguous(scales, "scales", torch.float32, shape[:-1])
+    dtype = _dtype_code(x.dtype)
+    _on_device(None, x, codes, scales)
+    ranks = 1 if ranks is None else ranks
+    _check(_lib.echo_quantize_tokens(ranks, tokens, depth, dtype, _matrix(x, ranks),
+                                     _matrix(codes, ranks), scales.data_ptr(), _stream(stream)),
+           "echo_quantize_tokens")
+
+
+def echo_matmul_int8(codes, scales, w, w_scales, out, stream=None) -> None:
+    """out[p][t][c] = sum_k codes[p][t][k] w[p][c][k] * scales[p][t] * w_scales[p][c].
+    out: [ranks][tokens][channels], or without ranks; codes with scales, w and
+    w_scales: with the ranks' dimension, or without it where all ranks share
+    them (codes and scales both)."""
+    import torch
+    ranks, tokens, channels, depth = _check_product(codes, w, w_scales, out)
+    _expect(codes, "codes", torch.int8, tuple(codes.shape))
+    _expect_contiguous(scales, "scales", torch.float32, tuple(codes.shape[:-1]))
+    dtype = _dtype_code(out.dtype)
+    _on_device(None, codes, scales, w, w_scales, out)
+    _check(_lib.echo_matmul_int8(ranks, tokens, channels, depth, _matrix(codes, ranks),
+                                 scales.data_ptr(), tokens if codes.dim() == 3 else 0,
+                                 _matrix(w, ranks), w_scales.data_ptr(),
+                                 w_scales.stride(0) if w_scales.dim() == 2 else 0, dtype,
+                                 _matrix(out, ranks), _stream(stream)), "echo_matmul_int8")
+
+
+def echo_linear_int8(x, w, w_scales, out, codes, scales, stream=None) -> None:
+    """echo_quantize_tokens(x, codes, scales), then echo_matmul_int8 of them:
+    x [ranks][tokens][depth] (or without ranks) and out of one dtype; codes
+    and scales are the caller's buffers for the quantized tokens."""
+    import torch
+    ranks, tokens, channels, depth = _check_product(x, w, w_scales, out)
+    shape = tuple(x.shape)
+    if len(shape) != out.dim():
+        raise ValueError(f"x: shape {shape}, expected the {out.dim()} dimensions of out")
+    _expect(x, "x", out.dtype, shape)
+    _expect(codes, "codes", torch.int8, shape)
+    _expect_contiguous(scales, "scales", torch.float32, shape[:-1])
+    dtype = _dtype_code(x.dtype)
+    _on_device(None, x, w, w_scales, out, codes, scales)
+    _check(_lib.echo_linear_int8(ranks, tokens, channels, depth, dtype, _matrix(x, ranks),
+                                 _matrix(w, ranks), w_scales.data_ptr(),
+                                 w_scales.stride(0) if w_scales.dim() == 2 else 0,
+                                 _matrix(codes, ranks), scales.data_ptr(), _matrix(out, ranks),
+                                 _stream(stream)), "echo_linear_int8")
 
 
 def echo_strerror(status: int) -> str:

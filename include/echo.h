@@ -367,6 +367,178 @@ int echo_debug_check_guards(echo_plan_t plan, int* intact);
 /* Free everything the plan allocated.  NULL is accepted. */
 void echo_plan_destroy(echo_plan_t plan);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The operators on either side of the all-reduce in a tensor-parallel block:
+ * the join of the reduced output with the residual stream, with the norms
+ * before and after it, and the 8-bit product that makes the partial sums.
+ * Status codes, streams and ownership are as above.  All of them only enqueue
+ * work on `stream`; none allocates or synchronizes.
+ * ---------------------------------------------------------------------------
+ */
+
+/* Element types (the same numbers as the ECHO_STATE_* formats). */
+#define ECHO_F32  0
+#define ECHO_BF16 1
+#define ECHO_F16  2
+
+#define ECHO_NORM_RMS   0   /* v / sqrt(mean(v^2) + eps) */
+#define ECHO_NORM_LAYER 1   /* (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) */
+#define ECHO_NORM_MAX_WIDTH 16384
+
+typedef struct echo_norm_plan_s* echo_norm_plan_t;
+
+/*
+ * echo_norm_plan -- a residual join of one width and type:
+ *     n = norm(y) * w_post + b_post       (n = y if post is 0)
+ *     r = x + scale * gate * n            the residual stream after the block
+ *     h = norm(r) * w_pre + b_pre         the next block's input
+ * for each row (token) of `width` elements; all arithmetic, the sums of the
+ * norms included, in fp32, rounded once per output.  h is computed from the
+ * unrounded r.
+ *   width        1..ECHO_NORM_MAX_WIDTH (ECHO_ERR_UNSUPPORTED above)
+ *   dtype        ECHO_* type of x, y, r, h and their gradients
+ *   param_dtype  type of weights, biases and gate and of their gradients:
+ *                dtype or ECHO_F32
+ *   kind         ECHO_NORM_RMS (no biases) or ECHO_NORM_LAYER, for both norms
+ *   post         1: with the norm after the block, 0: without
+ *   eps, scale   finite, eps >= 0
+ * Allocates (cudaMalloc, on the current device) the workspace of
+ * echo_norm_backward: the plan serves one stream at a time.
+ */
+int echo_norm_plan(int64_t width, int dtype, int param_dtype, int kind, int post,
+                   float eps, float scale, echo_norm_plan_t* out);
+
+/* Free the plan and its workspace.  NULL is accepted. */
+void echo_norm_plan_destroy(echo_norm_plan_t plan);
+
+/* The parameters (or, for echo_norm_backward, their gradients): device
+ * pointers to `width` contiguous elements of param_dtype.  A NULL weight is
+ * one, a NULL bias zero, a NULL gradient is not computed.  ECHO_ERR_ARG for
+ * w_post or b_post without post, for biases with ECHO_NORM_RMS. */
+typedef struct {
+  void *w_post, *b_post, *w_pre, *b_pre;
+} echo_norm_params;
+
+/* One call of echo_norm.  Row t of a tensor starts ld elements after row
+ * t - 1, ld >= width; pointers are aligned to their element.  Tensors whose
+ * rows and parameters are all 16-byte aligned are moved in 16-byte pieces,
+ * others element by element. */
+typedef struct {
+  int64_t rows;
+  const void* x;           /* residual stream */
+  int64_t ld_x;
+  const void* y;           /* the block's output; NULL: r = x (no post norm, no gate) */
+  int64_t ld_y;
+  const void* gate;        /* [gate_rows][gate_cols] of param_dtype, contiguous; NULL: 1 */
+  int64_t gate_rows;       /* divides rows: each gate row serves rows / gate_rows */
+                           /* consecutive rows (1: a layer scale; rows: one per token) */
+  int64_t gate_cols;       /* width, or 1 for a scalar per gate row */
+  void* r;                 /* NULL: not written */
+  int64_t ld_r;
+  void* h;                 /* NULL: not written */
+  int64_t ld_h;
+  int8_t* codes;           /* h quantized as by echo_quantize_tokens (from its fp32 */
+  int64_t ld_codes;        /* values), with its scales; NULL: not written */
+  float* scales;           /* [rows] */
+  float* stats;            /* [rows][4]: mean and 1/sqrt(var + eps) of y, then of r, for */
+                           /* echo_norm_backward (mean 0 for RMS; 0 and 1 where there is */
+                           /* no norm); 16-byte aligned; NULL: not written */
+} echo_norm_io;
+
+/*
+ * echo_norm -- one forward call.  r may be x, and h may be y, with the same
+ * row distance; any other overlap of an output with an input or output is
+ * rejected (ECHO_ERR_ARG).  `p` NULL: no parameters.  Rows with a non-finite
+ * element give what the formula gives (NaN in h, and codes 0 with a
+ * non-finite scale).
+ */
+int echo_norm(echo_norm_plan_t plan, const echo_norm_params* p, const echo_norm_io* io,
+              void* stream);
+
+/* One call of echo_norm_backward: x, y, gate and stats of the forward call
+ * (inputs as they were then: x is the residual stream before the join), and
+ * the gradients of r and h (either may be NULL: zero). */
+typedef struct {
+  int64_t rows;
+  const void* x;
+  int64_t ld_x;
+  const void* y;
+  int64_t ld_y;
+  const void* gate;
+  int64_t gate_rows, gate_cols;
+  const float* stats;
+  const void* dr;
+  int64_t ld_dr;
+  const void* dh;
+  int64_t ld_dh;
+  void* dx;                /* NULL: not written */
+  int64_t ld_dx;
+  void* dy;                /* NULL: not written; must be NULL if y is */
+  int64_t ld_dy;
+  void* dgate;             /* as gate, summed over the rows (and, for gate_cols 1, the */
+                           /* columns) that share an element; NULL: not written */
+} echo_norm_grad_io;
+
+/*
+ * echo_norm_backward -- gradients of one echo_norm call.  Those of the
+ * parameters and the gate are written (not added to), summed over the rows in
+ * fp32 in an order that depends on the shapes only: a repeated call gives the
+ * same bits.  dx may be dr or dh, dy may be dr, dh or y, each with the same
+ * row distance; other overlaps are rejected (ECHO_ERR_ARG).
+ */
+int echo_norm_backward(echo_norm_plan_t plan, const echo_norm_params* p,
+                       const echo_norm_grad_io* io, const echo_norm_params* grads, void* stream);
+
+/* A batch of `ranks` matrices of rows x cols elements: element (p, i, j) at
+ * data + p * rank_stride + i * ld + j (in elements). */
+typedef struct {
+  void* data;
+  int64_t ld;
+  int64_t rank_stride;     /* 0: every rank reads the same matrix (inputs only) */
+} echo_matrix;
+
+/*
+ * echo_quantize_tokens -- x[ranks][tokens][depth] to int8, one scale a token:
+ *     amax = max over the row of |x|, at least 2^-110
+ *     codes = rint(x * fl32(127 / amax)),   scales[ranks][tokens] = fl32(amax / 127)
+ * A row with an infinity or a NaN gets codes 0 and a scale that is infinite or
+ * NaN, so that every product with it is NaN.
+ */
+int echo_quantize_tokens(int64_t ranks, int64_t tokens, int64_t depth, int dtype,
+                         const echo_matrix* x, const echo_matrix* codes, float* scales,
+                         void* stream);
+
+/*
+ * echo_matmul_int8 -- for each rank p, token t, channel c:
+ *     out[p][t][c] = (sum over k of a[p][t][k] * w[p][c][k]) * a_scales[p][t] * w_scales[p][c]
+ * The sum is exact for any codes (int32; depth at most ECHO_MATMUL_MAX_DEPTH),
+ * so a token's result does not depend on how many tokens the call has; it is
+ * converted to fp32, multiplied by the token's scale and then the channel's,
+ * and rounded once to out's type.
+ *   a_scales  fp32, rank p's tokens at a_scales + p * a_scale_stride (a stride
+ *             of 0 shares them between the ranks)
+ *   w_scales  fp32, rank p's channels at w_scales + p * w_scale_stride
+ *   out       out_dtype ECHO_F32, ECHO_BF16 or ECHO_F16; must not overlap the
+ *             inputs, nor one rank's rows another's (ECHO_ERR_ARG)
+ * Laid out like echo_allreduce's inputs, out + p * rank_stride is rank p's
+ * partial tensor.
+ */
+#define ECHO_MATMUL_MAX_DEPTH 131071
+int echo_matmul_int8(int64_t ranks, int64_t tokens, int64_t channels, int64_t depth,
+                     const echo_matrix* a, const float* a_scales, int64_t a_scale_stride,
+                     const echo_matrix* w, const float* w_scales, int64_t w_scale_stride,
+                     int out_dtype, const echo_matrix* out, void* stream);
+
+/*
+ * echo_linear_int8 -- echo_quantize_tokens of x into codes and a_scales
+ * ([ranks][tokens], contiguous), then echo_matmul_int8: the same bits.  x and out have the type dtype.
+ */
+int echo_linear_int8(int64_t ranks, int64_t tokens, int64_t channels, int64_t depth, int dtype,
+                     const echo_matrix* x, const echo_matrix* w, const float* w_scales,
+                     int64_t w_scale_stride, const echo_matrix* codes, float* a_scales,
+                     const echo_matrix* out, void* stream);
+
 /* A static description of a status code; for ECHO_ERR_CUDA, of the last CUDA
  * error seen by the library in this thread. */
 const char* echo_strerror(int status);
