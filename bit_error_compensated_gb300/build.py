@@ -21,8 +21,8 @@ LIBDIR = PKG / "lib"
 LIB = LIBDIR / "libecho.so"
 # (source, suffix and definition it is compiled with, or None).  Every kernel
 # source of the all-reduce is compiled once per supported group size, those of
-# the residual join once per element type (the ECHO_F32, ECHO_BF16, ECHO_F16
-# numbers); the objects compile in parallel.
+# the operators around it once per element type (the ECHO_F32, ECHO_BF16,
+# ECHO_F16 numbers); the objects compile in parallel.
 GROUPS = (64, 128, 256)
 TYPES = (0, 1, 2)
 SOURCES = [(src, None) for src in ("echo_api.cu", "echo_noalloc.cu", "norm_api.cu", "int8_api.cu",
@@ -30,7 +30,9 @@ SOURCES = [(src, None) for src in ("echo_api.cu", "echo_noalloc.cu", "norm_api.c
     (src, (f"_g{g}", f"-DECHO_G={g}"))
     for src in ("k_push.cu", "k_reduce.cu", "k_gather.cu", "k_call.cu", "k_tile.cu")
     for g in GROUPS] + [
-    (src, (f"_t{t}", f"-DECHO_T={t}")) for src in ("norm_fwd.cu", "norm_bwd.cu") for t in TYPES]
+    (src, (f"_t{t}", f"-DECHO_T={t}"))
+    for src in ("norm_fwd.cu", "norm_bwd.cu", "int8_pair.cu")
+    for t in TYPES]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

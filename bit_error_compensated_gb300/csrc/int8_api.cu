@@ -160,6 +160,18 @@ int echo_matmul_int8(int64_t ranks, int64_t tokens, int64_t channels, int64_t de
   return ECHO_OK;
 }
 
+int echo_matmul_status(void* stream, int* status) {
+  if (status == nullptr) return ECHO_ERR_ARG;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int word[3] = {0, 0, 0};
+  ECHO_OPS_CUDA(take_gave_up<float>(word, s));
+  ECHO_OPS_CUDA(take_gave_up<__nv_bfloat16>(word + 1, s));
+  ECHO_OPS_CUDA(take_gave_up<__half>(word + 2, s));
+  ECHO_OPS_CUDA(cudaStreamSynchronize(s));
+  *status = word[0] | word[1] | word[2] ? ECHO_ERR_TIMEOUT : ECHO_OK;
+  return ECHO_OK;
+}
+
 int echo_linear_int8(int64_t ranks, int64_t tokens, int64_t channels, int64_t depth, int dtype,
                      const echo_matrix* x, const echo_matrix* w, const float* w_scales,
                      int64_t w_scale_stride, const echo_matrix* codes, float* a_scales,

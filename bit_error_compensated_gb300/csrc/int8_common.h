@@ -36,7 +36,27 @@ __device__ __forceinline__ float scaled_sum(int sum, float token, float channel)
   return __fmul_rn(__fmul_rn(__int2float_rn(sum), token), channel);
 }
 
+// What a call's addresses and distances allow.
+struct ProductLayout {
+  bool aligned;                  // rows of codes start on 16-byte boundaries
+  bool wide;                     // rows of out do
+  int sms;
+};
+
 cudaError_t launch_quantize(const QuantArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_product(const ProductArgs& a, cudaStream_t s);
+// One instantiation per type of out (the sources are compiled once for each).
+template <typename T>
+cudaError_t launch_pair(const ProductArgs& p, const ProductLayout& l, cudaStream_t s);
+// Reads and clears the word that a wait that gave up has set.
+template <typename T> cudaError_t take_gave_up(int* word, cudaStream_t s);
 
 }  // namespace echo
+
+#if ECHO_T == 0
+#define ECHO_ELEM float
+#elif ECHO_T == 1
+#define ECHO_ELEM __nv_bfloat16
+#elif ECHO_T == 2
+#define ECHO_ELEM __half
+#endif

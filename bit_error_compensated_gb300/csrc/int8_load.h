@@ -1,0 +1,50 @@
+// int8_load.h -- 16 codes of a row at a time, and their conversion to f16.
+#pragma once
+
+#include "int8_common.h"
+
+namespace echo {
+
+// Codes k..k+15 of a row of `depth` codes, zeros behind its end (k a multiple
+// of 16; `row` nullptr: zeros).  ALIGNED: rows start on 16-byte boundaries, so
+// all but a ragged last piece is one load.  Otherwise a piece inside the row
+// is put together from the aligned words around it, all of them inside the row
+// too, and only a row's ends go byte by byte.
+template <bool ALIGNED>
+__device__ __forceinline__ uint4 load_codes(const int8_t* row, int64_t k, int64_t depth) {
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (row == nullptr || k >= depth) return v;
+  const int8_t* p = row + k;
+  if (ALIGNED && k + 16 <= depth) return __ldg(reinterpret_cast<const uint4*>(p));
+  if (!ALIGNED && k >= 3 && k + 19 <= depth) {
+    const uint32_t shift = (uint32_t)((uintptr_t)p & 3) * 8;
+    const uint32_t* w = reinterpret_cast<const uint32_t*>((uintptr_t)p & ~(uintptr_t)3);
+    const uint32_t a = __ldg(w), b = __ldg(w + 1), c = __ldg(w + 2), d = __ldg(w + 3);
+    const uint32_t e = shift ? __ldg(w + 4) : 0;
+    v.x = __funnelshift_r(a, b, shift);
+    v.y = __funnelshift_r(b, c, shift);
+    v.z = __funnelshift_r(c, d, shift);
+    v.w = __funnelshift_r(d, e, shift);
+    return v;
+  }
+  uint32_t word[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if (k + i < depth) word[i / 4] |= (uint32_t)(uint8_t)__ldg(p + i) << (8 * (i % 4));
+  return make_uint4(word[0], word[1], word[2], word[3]);
+}
+
+// Four codes as two pairs of f16, exactly: with the sign bit turned a code is
+// 128 more than it was, and behind the byte 0x64 it is the significand of
+// 1024 + (code + 128); 1152 is then taken off.
+__device__ __forceinline__ void codes_to_f16(uint32_t four, uint32_t& low, uint32_t& high) {
+  const uint32_t u = four ^ 0x80808080u;
+  const __half2 bias = __half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));   // 1152
+  const uint32_t l = __byte_perm(u, 0x64646464u, 0x4140), h = __byte_perm(u, 0x64646464u, 0x4342);
+  const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&l), bias);
+  const __half2 b = __hsub2(*reinterpret_cast<const __half2*>(&h), bias);
+  low = *reinterpret_cast<const uint32_t*>(&a);
+  high = *reinterpret_cast<const uint32_t*>(&b);
+}
+
+}  // namespace echo

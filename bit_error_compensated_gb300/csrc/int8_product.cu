@@ -62,6 +62,18 @@ cudaError_t launch(const ProductArgs& p, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_product(const ProductArgs& p, cudaStream_t s) {
+  ProductLayout l;
+  cudaError_t e = device_sms(&l.sms);
+  if (e != cudaSuccess) return e;
+  const int64_t size = elem_size(p.out_dtype);
+  l.aligned = on_boundary(p.a, 16) && on_boundary(p.w, 16) && (p.tokens == 1 || p.ld_a % 16 == 0) &&
+              (p.channels == 1 || p.ld_w % 16 == 0) &&
+              (p.ranks == 1 || (p.rank_a % 16 == 0 && p.rank_w % 16 == 0));
+  l.wide = on_boundary(p.out, 16) && (p.tokens == 1 || p.ld_out * size % 16 == 0) &&
+           (p.ranks == 1 || p.rank_out * size % 16 == 0);
+  if (p.tokens > 32)
+    return p.out_dtype == ECHO_F32    ? launch_pair<float>(p, l, s)
+           : p.out_dtype == ECHO_BF16 ? launch_pair<__nv_bfloat16>(p, l, s) : launch_pair<__half>(p, l, s);
   return p.out_dtype == ECHO_F32    ? launch<float>(p, s)
          : p.out_dtype == ECHO_BF16 ? launch<__nv_bfloat16>(p, s) : launch<__half>(p, s);
 }

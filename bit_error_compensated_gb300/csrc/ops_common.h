@@ -7,7 +7,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <cstdlib>
+#include <atomic>
 
 #include "../../include/echo.h"
 
@@ -101,6 +101,36 @@ inline bool known_dtype(int dtype) {
   return dtype == ECHO_F32 || dtype == ECHO_BF16 || dtype == ECHO_F16;
 }
 inline bool on_boundary(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+// Work done once per device by the first call that needs it (a kernel's
+// attributes); calls that race do the same work twice.
+struct OncePerDevice {
+  std::atomic<uint64_t> done{0};
+  template <typename F>
+  cudaError_t run(F&& work) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = (uint64_t)1 << (dev & 63);
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = work();
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+  }
+};
+
+// SMs of the current device.
+inline cudaError_t device_sms(int* sms) {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  *sms = known[dev & 63].load(std::memory_order_relaxed);
+  if (*sms) return cudaSuccess;
+  e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) known[dev & 63].store(*sms, std::memory_order_relaxed);
+  return e;
+}
 
 // A strided matrix in memory: `rows` rows of `bytes` bytes, `pitch` bytes apart.
 struct Region {

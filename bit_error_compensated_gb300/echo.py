@@ -105,6 +105,7 @@ _SIGS = {
     "echo_matmul_int8": (_i32, [_i64, _i64, _i64, _i64, ctypes.POINTER(_Matrix), _vp, _i64,
                                 ctypes.POINTER(_Matrix), _vp, _i64, _i32,
                                 ctypes.POINTER(_Matrix), _vp]),
+    "echo_matmul_status": (_i32, [_vp, ctypes.POINTER(_i32)]),
     "echo_linear_int8": (_i32, [_i64, _i64, _i64, _i64, _i32, ctypes.POINTER(_Matrix),
                                 ctypes.POINTER(_Matrix), _vp, _i64, ctypes.POINTER(_Matrix), _vp,
                                 ctypes.POINTER(_Matrix), _vp]),
@@ -603,6 +604,12 @@ def echo_matmul_int8(codes, scales, w, w_scales, out, stream=None) -> None:
                                  _matrix(w, ranks), w_scales.data_ptr(),
                                  w_scales.stride(0) if w_scales.dim() == 2 else 0, dtype,
                                  _matrix(out, ranks), _stream(stream)), "echo_matmul_int8")
+
+
+def echo_matmul_status(stream=None) -> int:
+    st = _i32(0)
+    _check(_lib.echo_matmul_status(_stream(stream), ctypes.byref(st)), "echo_matmul_status")
+    return st.value
 
 
 def echo_linear_int8(x, w, w_scales, out, codes, scales, stream=None) -> None:

@@ -531,6 +531,14 @@ int echo_matmul_int8(int64_t ranks, int64_t tokens, int64_t channels, int64_t de
                      int out_dtype, const echo_matrix* out, void* stream);
 
 /*
+ * echo_matmul_status -- read and clear the current device's status word of the
+ * products: synchronizes `stream`, then writes ECHO_OK, or ECHO_ERR_TIMEOUT if
+ * a device-side wait of an earlier echo_matmul_int8 or echo_linear_int8 gave
+ * up (after 1 s; that call's results are unspecified).
+ */
+int echo_matmul_status(void* stream, int* status);
+
+/*
  * echo_linear_int8 -- echo_quantize_tokens of x into codes and a_scales
  * ([ranks][tokens], contiguous), then echo_matmul_int8: the same bits.  x and out have the type dtype.
  */
