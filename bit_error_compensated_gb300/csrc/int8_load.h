@@ -6,17 +6,16 @@
 namespace echo {
 
 // Codes k..k+15 of a row of `depth` codes, zeros behind its end (k a multiple
-// of 16; `row` nullptr: zeros).  ALIGNED: rows start on 16-byte boundaries, so
-// all but a ragged last piece is one load.  Otherwise a piece inside the row
-// is put together from the aligned words around it, all of them inside the row
-// too, and only a row's ends go byte by byte.
+// of 16).  ALIGNED: rows start on 16-byte boundaries, so all but a ragged last
+// piece is one load.  Otherwise a piece inside the row is put together from
+// the aligned words around it, all of them inside the row too, and only a
+// row's ends go byte by byte.
 template <bool ALIGNED>
 __device__ __forceinline__ uint4 load_codes(const int8_t* row, int64_t k, int64_t depth) {
-  uint4 v = make_uint4(0, 0, 0, 0);
-  if (row == nullptr || k >= depth) return v;
   const int8_t* p = row + k;
   if (ALIGNED && k + 16 <= depth) return __ldg(reinterpret_cast<const uint4*>(p));
   if (!ALIGNED && k >= 3 && k + 19 <= depth) {
+    uint4 v;
     const uint32_t shift = (uint32_t)((uintptr_t)p & 3) * 8;
     const uint32_t* w = reinterpret_cast<const uint32_t*>((uintptr_t)p & ~(uintptr_t)3);
     const uint32_t a = __ldg(w), b = __ldg(w + 1), c = __ldg(w + 2), d = __ldg(w + 3);
@@ -27,11 +26,13 @@ __device__ __forceinline__ uint4 load_codes(const int8_t* row, int64_t k, int64_
     v.w = __funnelshift_r(d, e, shift);
     return v;
   }
-  uint32_t word[4] = {0, 0, 0, 0};
-#pragma unroll
-  for (int i = 0; i < 16; ++i)
-    if (k + i < depth) word[i / 4] |= (uint32_t)(uint8_t)__ldg(p + i) << (8 * (i % 4));
-  return make_uint4(word[0], word[1], word[2], word[3]);
+  uint64_t low = 0, high = 0;
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i) {
+    if (k + i < depth) low |= (uint64_t)(uint8_t)__ldg(p + i) << (8 * i);
+    if (k + i + 8 < depth) high |= (uint64_t)(uint8_t)__ldg(p + i + 8) << (8 * i);
+  }
+  return make_uint4((uint32_t)low, (uint32_t)(low >> 32), (uint32_t)high, (uint32_t)(high >> 32));
 }
 
 // Four codes as two pairs of f16, exactly: with the sign bit turned a code is

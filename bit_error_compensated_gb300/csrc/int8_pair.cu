@@ -88,12 +88,28 @@ __device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile 
   }
 }
 
-// Arrives on a barrier of the pair's first block.
+// Arrives on a barrier of this block; what its threads wrote is visible to
+// the block's waiters.
+__device__ __forceinline__ void arrive_here(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
+}
+
+// Arrives on a barrier of the pair's first block.  Releasing to the cluster
+// waits for the thread's loads in flight, so only the issuing warps do it.
 __device__ __forceinline__ void arrive_first(uint32_t bar) {
   asm volatile(
       "{\n\t.reg .b32 at;\n\t"
       "mapa.shared::cluster.u32 at, %0, 0;\n\t"
       "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [at];\n\t}"
+      :: "r"(bar) : "memory");
+}
+
+// The same for a thread that has nothing in memory to publish.
+__device__ __forceinline__ void arrive_first_relaxed(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .b32 at;\n\t"
+      "mapa.shared::cluster.u32 at, %0, 0;\n\t"
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [at];\n\t}"
       :: "r"(bar) : "memory");
 }
 
@@ -174,7 +190,7 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide) {
   if (tid == 0) {
     give_up = 0;
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(full + 8 * s, 2 * kWorkers);
+      mbar_init(full + 8 * s, kWorkers + (half == 0 ? 1 : 0));   // and the second block's word
       mbar_init(empty + 8 * s, 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -235,34 +251,51 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide) {
         give_up = 1;
       }
     }
+    if (warp == kWorkers && half == 1 && lane == 0) {
+      // Tells the first block of each stage that this block has stored.
+      int slot = 0;
+      uint32_t phase = 0;
+      for (int64_t g = 0; g < mine * stages; ++g) {
+        if (!wait_on(full + 8 * slot, phase, &give_up)) break;
+        arrive_first(full + 8 * slot);
+        if (++slot == kStages) {
+          slot = 0;
+          phase ^= 1;
+        }
+      }
+    }
     __syncwarp();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kWorkerRegs));
     const int seg = tid & 3, r0 = tid >> 2;              // this thread's piece of rows r0, r0 + 64
+    const uint32_t put0 = (uint32_t)(r0 * 128 + (((2 * seg) ^ (r0 & 7)) << 4));    // its two halves'
+    const uint32_t put1 = (uint32_t)(r0 * 128 + (((2 * seg + 1) ^ (r0 & 7)) << 4));  // swizzled places
     // The stage to load next: its tile, its depth, its rows.
     int64_t load_tile = pair, load_k = 0;
     const int8_t* row[2 + kPieces];
+    // Rows past the last token or channel repeat it: their results are dropped.
     auto find_rows = [&]() {
-      if (load_tile >= tiles.total) {
-#pragma unroll
-        for (int i = 0; i < 2 + kPieces; ++i) row[i] = nullptr;
-        return;
-      }
-      const Place at = place_of(tiles, load_tile);
+      const Place at = place_of(tiles, load_tile < tiles.total ? load_tile : pair);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int64_t t = at.row * 256 + half * kRows + r0 + 64 * i;
-        row[i] = t < p.tokens ? p.a + at.rank * p.rank_a + t * p.ld_a : nullptr;
+        row[i] = p.a + at.rank * p.rank_a + (t < p.tokens ? t : p.tokens - 1) * p.ld_a;
       }
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
         const int64_t c = at.col * BN + half * (BN / 2) + r0 + 64 * i;
-        row[2 + i] = c < p.channels ? p.w + at.rank * p.rank_w + c * p.ld_w : nullptr;
+        row[2 + i] = p.w + at.rank * p.rank_w + (c < p.channels ? c : p.channels - 1) * p.ld_w;
       }
     };
     auto load_stage = [&](uint4 (&v)[2 + kPieces]) {
+      const int64_t k = load_k + 16 * seg;
+      if (ALIGNED && k + 16 <= p.depth) {
 #pragma unroll
-      for (int i = 0; i < 2 + kPieces; ++i) v[i] = load_codes<ALIGNED>(row[i], load_k + 16 * seg, p.depth);
+        for (int i = 0; i < 2 + kPieces; ++i) v[i] = __ldg(reinterpret_cast<const uint4*>(row[i] + k));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2 + kPieces; ++i) v[i] = load_codes<ALIGNED>(row[i], k, p.depth);
+      }
       load_k += kStageDepth;
       if (load_k >= p.depth) {
         load_k = 0;
@@ -308,7 +341,7 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide) {
       if (++step == kSteps) {
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncwarp();
-        if (lane == 0) arrive_first(sums_empty + 8 * b);
+        if (lane == 0) arrive_first_relaxed(sums_empty + 8 * b);   // the loads from TMEM are done
       }
     };
 
@@ -329,22 +362,20 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide) {
         const uint32_t base = ring + slot * stage_bytes<BN>();
 #pragma unroll
         for (int i = 0; i < 2 + kPieces; ++i) {
-          const int r = r0 + 64 * (i < 2 ? i : i - 2);
-          const uint32_t at = base + (i < 2 ? 0 : kRows * 128) + r * 128;
+          const uint32_t at = base + (uint32_t)(i < 2 ? 64 * i : kRows + 64 * (i - 2)) * 128;
           uint32_t h[8];
           codes_to_f16(held[u][i].x, h[0], h[1]);
           codes_to_f16(held[u][i].y, h[2], h[3]);
           codes_to_f16(held[u][i].z, h[4], h[5]);
           codes_to_f16(held[u][i].w, h[6], h[7]);
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
-                         :: "r"(at + (uint32_t)(((2 * seg + c) ^ (r & 7)) << 4)), "r"(h[4 * c]), "r"(h[4 * c + 1]),
-                            "r"(h[4 * c + 2]), "r"(h[4 * c + 3]) : "memory");
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                       :: "r"(at + put0), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                       :: "r"(at + put1), "r"(h[4]), "r"(h[5]), "r"(h[6]), "r"(h[7]) : "memory");
         }
         fence_proxy_async();
         __syncwarp();
-        if (lane == 0) arrive_first(full + 8 * slot);
+        if (lane == 0) arrive_here(full + 8 * slot);
         load_stage(held[u]);
         if (++slot == kStages) {
           slot = 0;
