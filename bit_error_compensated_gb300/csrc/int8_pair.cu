@@ -10,10 +10,10 @@
 // Two SMs (a cluster of two blocks) share one tile of 256 tokens x BN channels
 // (tcgen05 cta_group::2): each block turns 128 rows of tokens and BN / 2 rows
 // of channels, which halves what goes through its shared memory per product.
-// In a block, eight warps load 16-byte pieces of codes two stages ahead into
+// In a block, eight warps load 16-byte pieces of codes a stage ahead into
 // registers, turn and store them (the 128-byte-swizzled K-major layout the
 // matrix instruction reads), and in between take the last chunk's sums out of
-// TMEM, 16 columns a stage; one thread of the first block issues the matrix
+// TMEM, 32 columns a stage; one thread of the first block issues the matrix
 // instructions.  TMEM holds two chunks' sums, so one is taken out while the
 // next is computed.
 //
@@ -26,18 +26,18 @@ namespace echo {
 namespace {
 
 constexpr int kRows = 128;              // tokens a block holds of the pair's 256
-constexpr int kStageDepth = 64;         // codes of a row per stage: 128 bytes of f16
-constexpr int kStages = 6;
-constexpr int kChunkStages = 16;        // 1024 codes: exact in fp32
+constexpr int kStageDepth = 128;        // codes of a row per stage: two swizzle atoms of f16
+constexpr int kStages = 3;
+constexpr int kChunkStages = 8;         // 1024 codes: exact in fp32
 constexpr int kWorkers = 8;             // warps that convert and store results
 constexpr int kThreads = 32 * (kWorkers + 4);   // three warpgroups; of the last, one warp works
 // Registers: the block starts with 168 a thread (three warpgroups of 504 in
 // all); a worker holds 128 sums, two stages' codes and 16 columns.
 constexpr int kWorkerRegs = 224, kIssuerRegs = 40;
 static_assert(2 * kWorkerRegs + kIssuerRegs <= 3 * 168, "a split above the launch's registers never ends");
-constexpr int kStep = 16;               // columns taken out of TMEM at a time
+constexpr int kStep = 32;               // columns taken out of TMEM after a stage
 
-template <int BN> constexpr int stage_bytes() { return (kRows + BN / 2) * 128; }
+template <int BN> constexpr int stage_bytes() { return (kRows + BN / 2) * 2 * kStageDepth; }
 template <int BN> constexpr int smem_bytes() { return kStages * stage_bytes<BN>() + 1024; }
 
 // Set by a block whose wait gave up, until echo_matmul_status clears it.
@@ -169,7 +169,8 @@ __device__ __forceinline__ void store_results(const ProductArgs& p, int64_t rank
 template <typename T, int BN, bool ALIGNED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide) {
-  constexpr int kPieces = BN / 128;                     // of the channels' rows, a thread and stage
+  constexpr int kPieces = 4 + BN / 64;                  // a thread loads of a stage: tokens', channels' rows
+  constexpr uint32_t kAtomA = kRows * 128, kAtomB = BN / 2 * 128;         // 64 codes of every row
   constexpr int kSteps = BN / 2 / kStep;                // to take out a chunk's sums
   constexpr uint32_t kInstr = (1u << 4) | ((uint32_t)(BN / 8) << 17) | (16u << 24);  // f16, fp32 sums, 256 x BN
   extern __shared__ uint8_t raw[];
@@ -231,10 +232,12 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide) {
             if (!ok) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t at = ring + slot * stage_bytes<BN>();
-            const uint64_t da = smem_desc(at), db = smem_desc(at + kRows * 128);
 #pragma unroll
-            for (int k = 0; k < kStageDepth / 16; ++k)          // 16 codes: 32 bytes on
-              mma_pair(tmem + b * BN, da + 2 * k, db + 2 * k, kInstr, s > 0 || k > 0);
+            for (int k = 0; k < kStageDepth / 16; ++k) {        // 16 codes: 32 bytes on
+              const uint64_t da = smem_desc(at + (k / 4) * kAtomA) + 2 * (k % 4);
+              const uint64_t db = smem_desc(at + 2 * kAtomA + (k / 4) * kAtomB) + 2 * (k % 4);
+              mma_pair(tmem + b * BN, da, db, kInstr, s > 0 || k > 0);
+            }
             commit_pair(empty + 8 * slot);
             if (++slot == kStages) {
               slot = 0;
@@ -267,34 +270,39 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide) {
     __syncwarp();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kWorkerRegs));
-    const int seg = tid & 3, r0 = tid >> 2;              // this thread's piece of rows r0, r0 + 64
-    const uint32_t put0 = (uint32_t)(r0 * 128 + (((2 * seg) ^ (r0 & 7)) << 4));    // its two halves'
-    const uint32_t put1 = (uint32_t)(r0 * 128 + (((2 * seg + 1) ^ (r0 & 7)) << 4));  // swizzled places
+    // This thread's pieces: 16 codes from 16 * seg of rows r0 + 32 i.  A
+    // quarter of a warp stores four pieces of two rows of one atom: swizzled,
+    // they lie in different banks; a row's eight pieces are one 128-byte line.
+    const int seg = (lane & 3) + 4 * ((lane >> 3) & 1);
+    const int r0 = warp * 4 + ((lane >> 2) & 1) + 2 * (lane >> 4);
+    const uint32_t put = (uint32_t)(r0 * 128 + (((2 * (seg & 3)) ^ (r0 & 7)) << 4));
+    const uint32_t put_a = put + (seg >> 2) * kAtomA, put_b = put + 2 * kAtomA + (seg >> 2) * kAtomB;
     // The stage to load next: its tile, its depth, its rows.
     int64_t load_tile = pair, load_k = 0;
-    const int8_t* row[2 + kPieces];
+    const int8_t* row[kPieces];
     // Rows past the last token or channel repeat it: their results are dropped.
     auto find_rows = [&]() {
       const Place at = place_of(tiles, load_tile < tiles.total ? load_tile : pair);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int64_t t = at.row * 256 + half * kRows + r0 + 64 * i;
-        row[i] = p.a + at.rank * p.rank_a + (t < p.tokens ? t : p.tokens - 1) * p.ld_a;
-      }
-#pragma unroll
       for (int i = 0; i < kPieces; ++i) {
-        const int64_t c = at.col * BN + half * (BN / 2) + r0 + 64 * i;
-        row[2 + i] = p.w + at.rank * p.rank_w + (c < p.channels ? c : p.channels - 1) * p.ld_w;
+        if (i < 4) {
+          const int64_t t = at.row * 256 + half * kRows + r0 + 32 * i;
+          row[i] = p.a + at.rank * p.rank_a + (t < p.tokens ? t : p.tokens - 1) * p.ld_a;
+        } else {
+          const int64_t c = at.col * BN + half * (BN / 2) + r0 + 32 * (i - 4);
+          row[i] = p.w + at.rank * p.rank_w + (c < p.channels ? c : p.channels - 1) * p.ld_w;
+        }
       }
     };
-    auto load_stage = [&](uint4 (&v)[2 + kPieces]) {
+    uint4 held[kPieces];
+    auto load_stage = [&]() {
       const int64_t k = load_k + 16 * seg;
       if (ALIGNED && k + 16 <= p.depth) {
 #pragma unroll
-        for (int i = 0; i < 2 + kPieces; ++i) v[i] = __ldg(reinterpret_cast<const uint4*>(row[i] + k));
+        for (int i = 0; i < kPieces; ++i) held[i] = __ldg(reinterpret_cast<const uint4*>(row[i] + k));
       } else {
 #pragma unroll
-        for (int i = 0; i < 2 + kPieces; ++i) v[i] = load_codes<ALIGNED>(row[i], k, p.depth);
+        for (int i = 0; i < kPieces; ++i) held[i] = load_codes<ALIGNED>(row[i], k, p.depth);
       }
       load_k += kStageDepth;
       if (load_k >= p.depth) {
@@ -306,7 +314,7 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide) {
 
     // The chunk whose sums are being taken out.
     int sum[BN / 2];
-    int step = kSteps, delay = 0;       // next 16 columns; stages to wait before the first
+    int step = kSteps, delay = 0;       // next columns; stages to wait before the first
     int64_t drained = 0;                // chunks taken out, or being so
     bool first = false, final = false;
     Place place = {0, 0, 0};
@@ -323,19 +331,22 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide) {
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
         if (s != step) continue;
-        float v[16];
-        tmem_load16(my_tmem + b * BN + s * kStep, v);
 #pragma unroll
-        for (int i = 0; i < kStep; ++i) {
-          const int x = __float2int_rn(v[i]);
-          sum[s * kStep + i] = first ? x : sum[s * kStep + i] + x;
-        }
-        if (final) {
-          const int64_t t = place.row * 256 + half * kRows + (warp & 3) * 32 + lane;
-          const int64_t c = place.col * BN + (warp >> 2) * (BN / 2) + s * kStep;
-          if (t < p.tokens && c < p.channels)
-            store_results<T>(p, place.rank, static_cast<T*>(p.out) + place.rank * p.rank_out + t * p.ld_out, c,
-                             sum + s * kStep, __ldg(p.a_scales + place.rank * p.rank_a_scales + t), wide);
+        for (int j = s * kStep; j < (s + 1) * kStep; j += 16) {
+          float v[16];
+          tmem_load16(my_tmem + b * BN + j, v);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int x = __float2int_rn(v[i]);
+            sum[j + i] = first ? x : sum[j + i] + x;
+          }
+          if (final) {
+            const int64_t t = place.row * 256 + half * kRows + (warp & 3) * 32 + lane;
+            const int64_t c = place.col * BN + (warp >> 2) * (BN / 2) + j;
+            if (t < p.tokens && c < p.channels)
+              store_results<T>(p, place.rank, static_cast<T*>(p.out) + place.rank * p.rank_out + t * p.ld_out,
+                               c, sum + j, __ldg(p.a_scales + place.rank * p.rank_a_scales + t), wide);
+          }
         }
       }
       if (++step == kSteps) {
@@ -346,66 +357,61 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide) {
     };
 
     find_rows();
-    uint4 held[2][2 + kPieces];
-    load_stage(held[0]);
-    load_stage(held[1]);
+    load_stage();
     int slot = 0;
     uint32_t phase = 0;
     int64_t tile = pair, s_tile = 0, s_chunk = 0;         // the stage being stored
-    const int64_t total = mine * stages;
-    for (int64_t g0 = 0; g0 < total && ok; g0 += 2) {
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        if (g0 + u >= total || !ok) break;
+    for (int64_t left = mine * stages; ok; --left) {      // and once more, for the last sums
+      if (left > 0) {
         ok = __all_sync(0xFFFFFFFFu, wait_on(empty + 8 * slot, phase ^ 1u, &give_up));
         if (!ok) break;
         const uint32_t base = ring + slot * stage_bytes<BN>();
 #pragma unroll
-        for (int i = 0; i < 2 + kPieces; ++i) {
-          const uint32_t at = base + (uint32_t)(i < 2 ? 64 * i : kRows + 64 * (i - 2)) * 128;
+        for (int i = 0; i < kPieces; ++i) {
+          const uint32_t at = base + (i < 4 ? put_a + 4096 * i : put_b + 4096 * (i - 4));   // 32 rows on
           uint32_t h[8];
-          codes_to_f16(held[u][i].x, h[0], h[1]);
-          codes_to_f16(held[u][i].y, h[2], h[3]);
-          codes_to_f16(held[u][i].z, h[4], h[5]);
-          codes_to_f16(held[u][i].w, h[6], h[7]);
+          codes_to_f16(held[i].x, h[0], h[1]);
+          codes_to_f16(held[i].y, h[2], h[3]);
+          codes_to_f16(held[i].z, h[4], h[5]);
+          codes_to_f16(held[i].w, h[6], h[7]);
           asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
-                       :: "r"(at + put0), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
+                       :: "r"(at), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
           asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
-                       :: "r"(at + put1), "r"(h[4]), "r"(h[5]), "r"(h[6]), "r"(h[7]) : "memory");
+                       :: "r"(at ^ 16u), "r"(h[4]), "r"(h[5]), "r"(h[6]), "r"(h[7]) : "memory");
         }
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) arrive_here(full + 8 * slot);
-        load_stage(held[u]);
+        load_stage();
         if (++slot == kStages) {
           slot = 0;
           phase ^= 1;
         }
-        // A chunk is complete in the ring: the one before it must be out of
-        // TMEM now, as the chunk after this one goes where it was.
         ++s_chunk;
         ++s_tile;
-        if (s_chunk == chunk_stages || s_tile == stages) {
-          while (step < kSteps && ok) take_step();
-          first = s_tile <= chunk_stages;
-          final = s_tile == stages;
-          if (final) place = place_of(tiles, tile);
-          ++drained;
-          step = 0;
-          delay = kStages + 1;        // until the matrix instructions have caught up
-          s_chunk = 0;
-          if (final) {
-            s_tile = 0;
-            tile += pairs;
-          }
-        } else if (delay > 0) {
-          --delay;
-        } else if (step < kSteps) {
-          take_step();
+      }
+      // A chunk is complete in the ring: the one before it must be out of
+      // TMEM now, as the chunk after this one goes where it was.
+      const bool end = left > 0 && (s_chunk == chunk_stages || s_tile == stages);
+      int take = 1;
+      if (end || left == 0) take = kSteps;
+      else if (delay > 0) --delay, take = 0;
+      for (; take > 0 && step < kSteps && ok; --take) take_step();
+      if (left == 0) break;
+      if (end) {
+        first = s_tile <= chunk_stages;
+        final = s_tile == stages;
+        if (final) place = place_of(tiles, tile);
+        ++drained;
+        step = 0;
+        delay = kStages;                // until the matrix instructions have caught up
+        s_chunk = 0;
+        if (final) {
+          s_tile = 0;
+          tile += pairs;
         }
       }
     }
-    while (step < kSteps && ok) take_step();
     if (!ok && lane == 0) atomicOr(&g_gave_up, 1);
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
