@@ -12,6 +12,7 @@ _BINDING_NAMES = (
     "echo_set_timing", "echo_set_quantizer", "echo_allreduce_noalloc", "Plan", "EchoError",
     "COMP_DEFAULT", "echo_norm_plan", "echo_norm_plan_destroy", "echo_norm", "echo_norm_backward",
     "echo_quantize_tokens", "echo_matmul_int8", "echo_matmul_status",
+    "echo_matmul_workspace_bytes",
     "echo_linear_int8", "NormPlan", "NormParams",
 )
 

@@ -103,14 +103,22 @@ int check_product(int64_t ranks, int64_t tokens, int64_t channels, int64_t depth
   return clear_of(out, ranks, tokens, channels, size, in, n) ? ECHO_OK : ECHO_ERR_ARG;
 }
 
+int check_workspace(int64_t ranks, int64_t tokens, int64_t depth, const void* workspace, size_t bytes) {
+  const size_t need = product_workspace(ranks, tokens, depth);
+  if (need == 0) return ECHO_OK;
+  if (workspace == nullptr || bytes < need) return ECHO_ERR_TOO_LARGE;
+  return on_boundary(workspace, 16) ? ECHO_OK : ECHO_ERR_ALIGN;
+}
+
 QuantArgs quant_args(int64_t ranks, int64_t tokens, int64_t depth, const echo_matrix* x,
-                     const echo_matrix* codes, float* scales) {
+                     const echo_matrix* codes, float* scales, void* wide) {
   QuantArgs a;
   std::memset(&a, 0, sizeof(a));
   a.x = x->data; a.ld_x = x->ld; a.rank_x = x->rank_stride;
   a.codes = static_cast<int8_t*>(codes->data);
   a.ld_codes = codes->ld; a.rank_codes = codes->rank_stride;
   a.scales = scales;
+  a.wide = static_cast<uint8_t*>(wide);
   a.ranks = ranks; a.tokens = tokens; a.depth = depth;
   return a;
 }
@@ -118,7 +126,7 @@ QuantArgs quant_args(int64_t ranks, int64_t tokens, int64_t depth, const echo_ma
 ProductArgs product_args(int64_t ranks, int64_t tokens, int64_t channels, int64_t depth,
                          const echo_matrix* a, const float* a_scales, int64_t a_scale_stride,
                          const echo_matrix* w, const float* w_scales, int64_t w_scale_stride,
-                         int out_dtype, const echo_matrix* out) {
+                         int out_dtype, const echo_matrix* out, void* wide) {
   ProductArgs p;
   std::memset(&p, 0, sizeof(p));
   p.a = static_cast<const int8_t*>(a->data); p.ld_a = a->ld; p.rank_a = a->rank_stride;
@@ -128,6 +136,7 @@ ProductArgs product_args(int64_t ranks, int64_t tokens, int64_t channels, int64_
   p.out = out->data; p.ld_out = out->ld; p.rank_out = out->rank_stride;
   p.ranks = ranks; p.tokens = tokens; p.channels = channels; p.depth = depth;
   p.out_dtype = out_dtype;
+  p.wide = static_cast<uint8_t*>(wide);
   return p;
 }
 
@@ -141,7 +150,7 @@ int echo_quantize_tokens(int64_t ranks, int64_t tokens, int64_t depth, int dtype
   ECHO_TRY(check_sizes(ranks, tokens, 0, depth));
   ECHO_TRY(check_quantize(ranks, tokens, depth, dtype, x, codes, scales));
   if (tokens == 0) return ECHO_OK;
-  ECHO_OPS_CUDA(launch_quantize(quant_args(ranks, tokens, depth, x, codes, scales), dtype,
+  ECHO_OPS_CUDA(launch_quantize(quant_args(ranks, tokens, depth, x, codes, scales, nullptr), dtype,
                                 static_cast<cudaStream_t>(stream)));
   return ECHO_OK;
 }
@@ -149,15 +158,21 @@ int echo_quantize_tokens(int64_t ranks, int64_t tokens, int64_t depth, int dtype
 int echo_matmul_int8(int64_t ranks, int64_t tokens, int64_t channels, int64_t depth,
                      const echo_matrix* a, const float* a_scales, int64_t a_scale_stride,
                      const echo_matrix* w, const float* w_scales, int64_t w_scale_stride,
-                     int out_dtype, const echo_matrix* out, void* stream) {
+                     int out_dtype, const echo_matrix* out, void* workspace, size_t workspace_bytes,
+                     void* stream) {
   ECHO_TRY(check_sizes(ranks, tokens, channels, depth));
   ECHO_TRY(check_product(ranks, tokens, channels, depth, a, a_scales, a_scale_stride, w, w_scales,
                          w_scale_stride, out_dtype, out));
   if (tokens == 0 || channels == 0) return ECHO_OK;
+  ECHO_TRY(check_workspace(a->rank_stride == 0 ? 1 : ranks, tokens, depth, workspace, workspace_bytes));
   ECHO_OPS_CUDA(launch_product(product_args(ranks, tokens, channels, depth, a, a_scales, a_scale_stride, w,
-                                            w_scales, w_scale_stride, out_dtype, out),
-                               static_cast<cudaStream_t>(stream)));
+                                            w_scales, w_scale_stride, out_dtype, out, workspace),
+                               false, static_cast<cudaStream_t>(stream)));
   return ECHO_OK;
+}
+
+size_t echo_matmul_workspace_bytes(int64_t ranks, int64_t tokens, int64_t depth) {
+  return check_sizes(ranks, tokens, 0, depth) == ECHO_OK ? product_workspace(ranks, tokens, depth) : 0;
 }
 
 int echo_matmul_status(void* stream, int* status) {
@@ -175,17 +190,20 @@ int echo_matmul_status(void* stream, int* status) {
 int echo_linear_int8(int64_t ranks, int64_t tokens, int64_t channels, int64_t depth, int dtype,
                      const echo_matrix* x, const echo_matrix* w, const float* w_scales,
                      int64_t w_scale_stride, const echo_matrix* codes, float* a_scales,
-                     const echo_matrix* out, void* stream) {
+                     const echo_matrix* out, void* workspace, size_t workspace_bytes, void* stream) {
   ECHO_TRY(check_sizes(ranks, tokens, channels, depth));
   ECHO_TRY(check_quantize(ranks, tokens, depth, dtype, x, codes, a_scales));
   ECHO_TRY(check_product(ranks, tokens, channels, depth, codes, a_scales, tokens, w, w_scales,
                          w_scale_stride, dtype, out));
   if (tokens == 0) return ECHO_OK;
+  const bool many = channels > 0 && product_workspace(ranks, tokens, depth) > 0;
+  if (many) ECHO_TRY(check_workspace(ranks, tokens, depth, workspace, workspace_bytes));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  ECHO_OPS_CUDA(launch_quantize(quant_args(ranks, tokens, depth, x, codes, a_scales), dtype, s));
+  ECHO_OPS_CUDA(launch_quantize(quant_args(ranks, tokens, depth, x, codes, a_scales, many ? workspace : nullptr),
+                                dtype, s));
   if (channels == 0) return ECHO_OK;
   ECHO_OPS_CUDA(launch_product(product_args(ranks, tokens, channels, depth, codes, a_scales, tokens, w,
-                                            w_scales, w_scale_stride, dtype, out), s));
+                                            w_scales, w_scale_stride, dtype, out, workspace), many, s));
   return ECHO_OK;
 }
 

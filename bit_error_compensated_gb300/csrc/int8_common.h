@@ -12,6 +12,7 @@ struct QuantArgs {
   int8_t* codes;
   int64_t ld_codes, rank_codes;
   float* scales;                 // [ranks][tokens]
+  uint8_t* wide;                 // the codes as f16 too (int8_load.h), or nullptr
   int64_t ranks, tokens, depth;
 };
 
@@ -28,7 +29,15 @@ struct ProductArgs {
   int64_t ld_out, rank_out;
   int64_t ranks, tokens, channels, depth;
   int out_dtype;
+  uint8_t* wide;                 // the tokens' codes as f16 (int8_load.h): many tokens only
 };
+
+// Products of more tokens than this run on the tensor cores' tiles, from f16
+// codes in a workspace.
+constexpr int64_t kFewTokens = 32;
+// Ranks of the tokens' codes: one where all share them.
+inline int64_t token_ranks(const ProductArgs& p) { return p.rank_a == 0 ? 1 : p.ranks; }
+size_t product_workspace(int64_t ranks, int64_t tokens, int64_t depth);
 
 // The value of an exact sum: fp32 products by the token's, then the channel's
 // scale, in this order everywhere, so that every kernel gives the same bits.
@@ -44,7 +53,10 @@ struct ProductLayout {
 };
 
 cudaError_t launch_quantize(const QuantArgs& a, int dtype, cudaStream_t s);
-cudaError_t launch_product(const ProductArgs& a, cudaStream_t s);
+// The f16 codes of tokens that are in int8 already.
+cudaError_t launch_widen(const ProductArgs& p, bool aligned, cudaStream_t s);
+// `widened`: the workspace already holds the tokens' f16 codes.
+cudaError_t launch_product(const ProductArgs& a, bool widened, cudaStream_t s);
 // One instantiation per type of out (the sources are compiled once for each).
 template <typename T>
 cudaError_t launch_pair(const ProductArgs& p, const ProductLayout& l, cudaStream_t s);

@@ -1,4 +1,5 @@
-// int8_load.h -- 16 codes of a row at a time, and their conversion to f16.
+// int8_load.h -- 16 codes of a row at a time, their conversion to f16, and the
+// layout of the tokens' f16 codes in the workspace of a product.
 #pragma once
 
 #include "int8_common.h"
@@ -46,6 +47,22 @@ __device__ __forceinline__ void codes_to_f16(uint32_t four, uint32_t& low, uint3
   const __half2 b = __hsub2(*reinterpret_cast<const __half2*>(&h), bias);
   low = *reinterpret_cast<const uint32_t*>(&a);
   high = *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// The workspace of a product of many tokens holds their codes as f16 in the
+// blocks that a copy takes to shared memory whole: 128 tokens x 128 codes, two
+// halves of 64 codes, each row's 128 bytes in eight 16-byte pieces that are
+// swizzled (piece ^ row % 8), as the matrix instruction reads them.
+constexpr int kBlockTokens = 128, kBlockCodes = 128;
+constexpr int kBlockBytes = kBlockTokens * kBlockCodes * 2;
+
+__host__ __device__ inline int64_t wide_blocks(int64_t extent) { return (extent + 127) / 128; }
+
+// Where code k (a multiple of 8) of token t of a rank lies: its byte offset.
+__device__ __forceinline__ int64_t wide_offset(int64_t rank, int64_t t, int64_t k, int64_t tokens, int64_t depth) {
+  const int64_t block = (rank * wide_blocks(tokens) + (t >> 7)) * wide_blocks(depth) + (k >> 7);
+  const uint32_t r = (uint32_t)t & 127u, c = (uint32_t)k & 127u;
+  return block * kBlockBytes + (c >> 6) * (kBlockBytes / 2) + r * 128 + ((((c & 63u) >> 3) ^ (r & 7u)) << 4);
 }
 
 }  // namespace echo

@@ -1,7 +1,7 @@
 // int8_product.cu -- echo_matmul_int8 (include/echo.h): a plain tile kernel.
 // A block computes 64 tokens x 64 channels; 64 codes of each row at a time
 // pass through shared memory and every thread sums 4 x 4 results with dp4a.
-#include "int8_common.h"
+#include "int8_load.h"
 
 namespace echo {
 namespace {
@@ -61,7 +61,12 @@ cudaError_t launch(const ProductArgs& p, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_product(const ProductArgs& p, cudaStream_t s) {
+size_t product_workspace(int64_t ranks, int64_t tokens, int64_t depth) {
+  if (tokens <= kFewTokens || depth == 0) return 0;
+  return (size_t)(ranks * wide_blocks(tokens) * wide_blocks(depth)) * kBlockBytes;
+}
+
+cudaError_t launch_product(const ProductArgs& p, bool widened, cudaStream_t s) {
   ProductLayout l;
   cudaError_t e = device_sms(&l.sms);
   if (e != cudaSuccess) return e;
@@ -71,9 +76,11 @@ cudaError_t launch_product(const ProductArgs& p, cudaStream_t s) {
               (p.ranks == 1 || (p.rank_a % 16 == 0 && p.rank_w % 16 == 0));
   l.wide = on_boundary(p.out, 16) && (p.tokens == 1 || p.ld_out * size % 16 == 0) &&
            (p.ranks == 1 || p.rank_out * size % 16 == 0);
-  if (p.tokens > 32)
+  if (p.tokens > kFewTokens && p.depth > 0) {
+    if (!widened && (e = launch_widen(p, l.aligned, s)) != cudaSuccess) return e;
     return p.out_dtype == ECHO_F32    ? launch_pair<float>(p, l, s)
            : p.out_dtype == ECHO_BF16 ? launch_pair<__nv_bfloat16>(p, l, s) : launch_pair<__half>(p, l, s);
+  }
   return p.out_dtype == ECHO_F32    ? launch<float>(p, s)
          : p.out_dtype == ECHO_BF16 ? launch<__nv_bfloat16>(p, s) : launch<__half>(p, s);
 }

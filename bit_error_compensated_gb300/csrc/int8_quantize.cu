@@ -6,7 +6,7 @@
 // One block a row.  The row is read once: its elements wait for the maximum in
 // registers; a row longer than the block's registers is read again instead.
 // It is bound by those bytes.
-#include "int8_common.h"
+#include "int8_load.h"
 
 namespace echo {
 namespace {
@@ -53,12 +53,46 @@ quantize_kernel(const QuantArgs a) {
     else if constexpr (VEC == 4)
       *reinterpret_cast<uint32_t*>(codes + c) = *reinterpret_cast<const uint32_t*>(&q);
     else codes[c] = q.v[0];
+    if (a.wide) {
+      Pack<__half, VEC> h;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) h.v[i] = __int2half_rn(q.v[i]);
+      uint8_t* to = a.wide + wide_offset(rank, token, c & ~(int64_t)7, a.tokens, a.depth) + 2 * (c & 7);
+      if constexpr (VEC == 8) *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(&h);
+      else if constexpr (VEC == 4) *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(&h);
+      else *reinterpret_cast<__half*>(to) = h.v[0];
+    }
   };
 #pragma unroll
   for (int j = 0; j < kPieces; ++j)
     if (col0 + j * step < a.depth) put(col0 + j * step, held[j]);
   for (int64_t c = col0 + kPieces * step; c < a.depth; c += step) put(c, load_pack<T, VEC>(x + c));
+  if (a.wide)                          // zeros up to the last block's end
+    for (int64_t c = a.depth + threadIdx.x; c < wide_blocks(a.depth) * kBlockCodes; c += blockDim.x)
+      *reinterpret_cast<uint16_t*>(a.wide + wide_offset(rank, token, c & ~(int64_t)7, a.tokens, a.depth) + 2 * (c & 7)) = 0;
   if (threadIdx.x == 0) a.scales[row] = __fdiv_rn(top, 127.f);
+}
+
+// Codes that are in int8 already, as f16: a thread turns 16 of a row.
+template <bool ALIGNED>
+__global__ void __launch_bounds__(256)
+widen_kernel(const ProductArgs p) {
+  pdl_wait();
+  const int64_t pieces = wide_blocks(p.depth) * (kBlockCodes / 16);
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t row = i / pieces, k = (i - row * pieces) * 16;
+  const int64_t rank = row / p.tokens, token = row - rank * p.tokens;
+  if (rank >= (p.rank_a == 0 ? 1 : p.ranks)) return;
+  const uint4 v = k < p.depth ? load_codes<ALIGNED>(p.a + rank * p.rank_a + token * p.ld_a, k, p.depth)
+                              : make_uint4(0, 0, 0, 0);
+  uint32_t h[8];
+  codes_to_f16(v.x, h[0], h[1]);
+  codes_to_f16(v.y, h[2], h[3]);
+  codes_to_f16(v.z, h[4], h[5]);
+  codes_to_f16(v.w, h[6], h[7]);
+  uint8_t* base = p.wide;
+  *reinterpret_cast<uint4*>(base + wide_offset(rank, token, k, p.tokens, p.depth)) = make_uint4(h[0], h[1], h[2], h[3]);
+  *reinterpret_cast<uint4*>(base + wide_offset(rank, token, k + 8, p.tokens, p.depth)) = make_uint4(h[4], h[5], h[6], h[7]);
 }
 
 template <typename T, int VEC>
@@ -83,6 +117,15 @@ cudaError_t pick(const QuantArgs& a, cudaStream_t s) {
 }
 
 }  // namespace
+
+cudaError_t launch_widen(const ProductArgs& p, bool aligned, cudaStream_t s) {
+  const int64_t pieces = token_ranks(p) * p.tokens * wide_blocks(p.depth) * (kBlockCodes / 16);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((pieces + 255) / 256));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  return aligned ? cudaLaunchKernelEx(&cfg, widen_kernel<true>, p) : cudaLaunchKernelEx(&cfg, widen_kernel<false>, p);
+}
 
 cudaError_t launch_quantize(const QuantArgs& a, int dtype, cudaStream_t s) {
   return dtype == ECHO_F32 ? pick<float>(a, s) : dtype == ECHO_BF16 ? pick<__nv_bfloat16>(a, s) : pick<__half>(a, s);

@@ -104,11 +104,12 @@ _SIGS = {
                                     ctypes.POINTER(_Matrix), _vp, _vp]),
     "echo_matmul_int8": (_i32, [_i64, _i64, _i64, _i64, ctypes.POINTER(_Matrix), _vp, _i64,
                                 ctypes.POINTER(_Matrix), _vp, _i64, _i32,
-                                ctypes.POINTER(_Matrix), _vp]),
+                                ctypes.POINTER(_Matrix), _vp, _sz, _vp]),
+    "echo_matmul_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "echo_matmul_status": (_i32, [_vp, ctypes.POINTER(_i32)]),
     "echo_linear_int8": (_i32, [_i64, _i64, _i64, _i64, _i32, ctypes.POINTER(_Matrix),
                                 ctypes.POINTER(_Matrix), _vp, _i64, ctypes.POINTER(_Matrix), _vp,
-                                ctypes.POINTER(_Matrix), _vp]),
+                                ctypes.POINTER(_Matrix), _vp, _sz, _vp]),
     "echo_strerror": (ctypes.c_char_p, [_i32]),
 }
 for _name, (_res, _args) in _SIGS.items():
@@ -571,6 +572,27 @@ def _check_product(codes_like, w, w_scales, out) -> tuple:
     return ranks, tokens, channels, depth
 
 
+def _workspace(ranks: int, tokens: int, depth: int, device, stream) -> tuple:
+    """(tensor or None, address, bytes) of a product's workspace, from torch's
+    allocator: ordered by the stream that the call runs on."""
+    nbytes = int(_lib.echo_matmul_workspace_bytes(ranks, tokens, depth))
+    if nbytes == 0:
+        return None, None, 0
+    import torch
+    buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if stream is not None:
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=device)
+        if stream != torch.cuda.current_stream():
+            stream.wait_stream(torch.cuda.current_stream())   # the memory's last use lies on this one
+            buf.record_stream(stream)
+    return buf, buf.data_ptr(), nbytes
+
+
+def echo_matmul_workspace_bytes(ranks: int, tokens: int, depth: int) -> int:
+    return int(_lib.echo_matmul_workspace_bytes(ranks, tokens, depth))
+
+
 def echo_quantize_tokens(x, codes, scales, stream=None) -> None:
     """x [ranks][tokens][depth] (or [tokens][depth]) to int8 codes of the same
     shape and one fp32 scale a token, [ranks][tokens] contiguous."""
@@ -599,11 +621,13 @@ def echo_matmul_int8(codes, scales, w, w_scales, out, stream=None) -> None:
     _expect_contiguous(scales, "scales", torch.float32, tuple(codes.shape[:-1]))
     dtype = _dtype_code(out.dtype)
     _on_device(None, codes, scales, w, w_scales, out)
+    keep, at, nbytes = _workspace(ranks if codes.dim() == 3 and codes.stride(0) else 1, tokens, depth,
+                                  codes.device, stream)
     _check(_lib.echo_matmul_int8(ranks, tokens, channels, depth, _matrix(codes, ranks),
                                  scales.data_ptr(), tokens if codes.dim() == 3 else 0,
                                  _matrix(w, ranks), w_scales.data_ptr(),
                                  w_scales.stride(0) if w_scales.dim() == 2 else 0, dtype,
-                                 _matrix(out, ranks), _stream(stream)), "echo_matmul_int8")
+                                 _matrix(out, ranks), at, nbytes, _stream(stream)), "echo_matmul_int8")
 
 
 def echo_matmul_status(stream=None) -> int:
@@ -626,11 +650,12 @@ def echo_linear_int8(x, w, w_scales, out, codes, scales, stream=None) -> None:
     _expect_contiguous(scales, "scales", torch.float32, shape[:-1])
     dtype = _dtype_code(x.dtype)
     _on_device(None, x, w, w_scales, out, codes, scales)
+    keep, at, nbytes = _workspace(ranks, tokens, depth, x.device, stream)
     _check(_lib.echo_linear_int8(ranks, tokens, channels, depth, dtype, _matrix(x, ranks),
                                  _matrix(w, ranks), w_scales.data_ptr(),
                                  w_scales.stride(0) if w_scales.dim() == 2 else 0,
                                  _matrix(codes, ranks), scales.data_ptr(), _matrix(out, ranks),
-                                 _stream(stream)), "echo_linear_int8")
+                                 at, nbytes, _stream(stream)), "echo_linear_int8")
 
 
 def echo_strerror(status: int) -> str:

@@ -65,7 +65,8 @@ extern "C" {
 #define ECHO_ERR_CUDA        5  /* a CUDA runtime call failed */
 #define ECHO_ERR_OVERFLOW    6  /* (status word) a non-finite input or an fp16 step overflow */
 #define ECHO_ERR_TIMEOUT     7  /* (status word) a device-side wait gave up */
-#define ECHO_ERR_TOO_LARGE   8  /* echo_allreduce_noalloc: beyond its fixed scratch area */
+#define ECHO_ERR_TOO_LARGE   8  /* echo_allreduce_noalloc: beyond its fixed scratch area;
+                                   a product: its workspace is too small */
 
 #define ECHO_MAX_RANKS 16
 
@@ -521,6 +522,9 @@ int echo_quantize_tokens(int64_t ranks, int64_t tokens, int64_t depth, int dtype
  *   w_scales  fp32, rank p's channels at w_scales + p * w_scale_stride
  *   out       out_dtype ECHO_F32, ECHO_BF16 or ECHO_F16; must not overlap the
  *             inputs, nor one rank's rows another's (ECHO_ERR_ARG)
+ *   workspace  16-byte-aligned device memory of at least
+ *             echo_matmul_workspace_bytes bytes, overlapping nothing else
+ *             (ECHO_ERR_TOO_LARGE if NULL or smaller); one call at a time
  * Laid out like echo_allreduce's inputs, out + p * rank_stride is rank p's
  * partial tensor.
  */
@@ -528,7 +532,16 @@ int echo_quantize_tokens(int64_t ranks, int64_t tokens, int64_t depth, int dtype
 int echo_matmul_int8(int64_t ranks, int64_t tokens, int64_t channels, int64_t depth,
                      const echo_matrix* a, const float* a_scales, int64_t a_scale_stride,
                      const echo_matrix* w, const float* w_scales, int64_t w_scale_stride,
-                     int out_dtype, const echo_matrix* out, void* stream);
+                     int out_dtype, const echo_matrix* out,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * echo_matmul_workspace_bytes -- bytes of the device workspace that
+ * echo_matmul_int8 and echo_linear_int8 need for these sizes (2 a code of the
+ * tokens, whose f16 forms it holds during the call, rows and columns rounded
+ * up to 128; 0 for few tokens).  Ranks that share their tokens count as one.
+ */
+size_t echo_matmul_workspace_bytes(int64_t ranks, int64_t tokens, int64_t depth);
 
 /*
  * echo_matmul_status -- read and clear the current device's status word of the
@@ -545,7 +558,8 @@ int echo_matmul_status(void* stream, int* status);
 int echo_linear_int8(int64_t ranks, int64_t tokens, int64_t channels, int64_t depth, int dtype,
                      const echo_matrix* x, const echo_matrix* w, const float* w_scales,
                      int64_t w_scale_stride, const echo_matrix* codes, float* a_scales,
-                     const echo_matrix* out, void* stream);
+                     const echo_matrix* out, void* workspace, size_t workspace_bytes,
+                     void* stream);
 
 /* A static description of a status code; for ECHO_ERR_CUDA, of the last CUDA
  * error seen by the library in this thread. */
