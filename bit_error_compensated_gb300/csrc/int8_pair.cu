@@ -10,20 +10,25 @@
 // Two SMs (a cluster of two blocks) share one tile of 256 tokens x BN channels
 // (tcgen05 cta_group::2), 128 rows of tokens and BN / 2 of channels in each
 // block's shared memory, which halves what goes through it per product.  The
-// tokens' codes come as f16 from the workspace, a block of 128 x 128 per copy
-// (cp.async.bulk); turning those of the tokens once instead of in every tile
-// costs 2 bytes a code, turning the larger weights ahead would cost as much as
-// the product of a thousand tokens.  The channels' codes are loaded as int8
-// and turned by two groups of eight warps, which take the stages (128 codes
-// deep) in turn: storing for the tensor cores needs a proxy fence, which also
-// waits for the warp's loads in flight, so no warp can load ahead of its
-// stores, and the second group works while the first waits.  In between, the
-// warps take the last chunk's sums out of TMEM; one thread of the first block
-// issues the matrix instructions.  TMEM holds two chunks' sums, so one is
-// taken out while the next is computed.
+// tokens' codes come as f16 from the workspace, a block of 128 x 128 per copy;
+// turning those of the tokens once instead of in every tile costs 2 bytes a
+// code, while turning the larger weights ahead would cost as much as the
+// product of a thousand tokens.  So the channels' codes come as int8 by TMA,
+// and warps turn them in shared memory.  A block's warps:
+//   8  take chunks' sums out of TMEM, add them up and store the results;
+//   8  turn codes, in two groups that take the stages (128 codes deep) in turn,
+//      so that one group's fences and waits overlap the other's work;
+//   3  issue: matrix instructions (first block), the tokens' copies, the
+//      channels' copies.
+// TMEM holds two chunks' sums, so one is taken out while the next is computed.
+// Shared memory moves 160 KB a stage (32 KB of tokens written and read, 16 KB
+// of int8 codes written and read, 32 KB of their f16 written and read): 1280
+// cycles at 128 bytes a cycle, for 1024 of matrix instructions.
 //
 // Every wait is bounded; one that gives up ends the call with a status
 // (echo_matmul_status).
+#include <cuda.h>
+
 #include "int8_load.h"
 #include "tma.cuh"
 
@@ -34,16 +39,20 @@ constexpr int kRows = kBlockTokens;     // tokens a block holds of the pair's 25
 constexpr int kStageDepth = kBlockCodes;
 constexpr int kStages = 3;
 constexpr int kChunkStages = 8;         // 1024 codes: exact in fp32
-constexpr int kGroups = 2, kGroupWarps = 8, kWorkers = kGroups * kGroupWarps;
-constexpr int kThreads = 32 * (kWorkers + 4);   // five warpgroups; of the last, two warps work
-constexpr int kStep = 16;               // columns taken out of TMEM at a time
+constexpr int kTakers = 8, kGroups = 2, kGroupWarps = 4, kTurners = kGroups * kGroupWarps;
+constexpr int kIssuer = kTakers + kTurners;     // the first of the issuing warps
+constexpr int kThreads = 32 * (kIssuer + 4);    // five warpgroups; of the last, three warps work
 // Registers: the block starts with 96 a thread (five warpgroups of 480 in
-// all); a worker holds up to 64 sums, a stage's codes and 16 columns.
-constexpr int kWorkerRegs = 112, kIssuerRegs = 32;
-static_assert(4 * kWorkerRegs + kIssuerRegs <= 5 * 96, "a split above the launch's registers never ends");
+// all); a taker holds up to 128 sums, a turner a stage's codes.
+constexpr int kTakerRegs = 160, kTurnerRegs = 64, kIssuerRegs = 32;
+static_assert(2 * kTakerRegs + 2 * kTurnerRegs + kIssuerRegs <= 5 * 96,
+              "a split above the launch's registers never ends");
 
-template <int BN> constexpr int stage_bytes() { return kBlockBytes + BN / 2 * 2 * kStageDepth; }
-template <int BN> constexpr int smem_bytes() { return kStages * stage_bytes<BN>() + 1024; }
+template <int BN> constexpr int code_bytes() { return BN / 2 * kStageDepth; }        // int8, one stage
+template <int BN> constexpr int stage_bytes() { return kBlockBytes + 2 * code_bytes<BN>(); }
+template <int BN> constexpr int smem_bytes() {
+  return kStages * stage_bytes<BN>() + kGroups * code_bytes<BN>() + 1024;
+}
 
 // Set by a block whose wait gave up, until echo_matmul_status clears it.
 __device__ int g_gave_up;
@@ -93,6 +102,11 @@ __device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile 
   }
 }
 
+// Arrives on a barrier of this block.
+__device__ __forceinline__ void arrive_here(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
+}
+
 // Arrives on a barrier of the pair's first block, without a release to the
 // cluster (which waits for everything the SM has in flight, over a thousand
 // cycles).  What the arrival reports needs none: rows in this block's shared
@@ -127,15 +141,25 @@ __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uin
       :: "r"(d), "l"(a), "l"(b), "r"(desc), "r"(add) : "memory");
 }
 
-__device__ __forceinline__ void tmem_load8(uint32_t at, float (&v)[8]) {
-  uint32_t r[8];
+__device__ __forceinline__ void tmem_load16(uint32_t at, float (&v)[16]) {
+  uint32_t r[16];
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(at) : "memory");
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// A box of the channels' codes: 128 codes from k of the rows from c of a rank.
+__device__ __forceinline__ void load_box(uint32_t to, const CUtensorMap* map, int k, int c, int rank, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];"
+      :: "r"(to), "l"(map), "r"(k), "r"(c), "r"(rank), "r"(bar) : "memory");
 }
 
 __device__ __forceinline__ void cluster_sync() {
@@ -166,19 +190,19 @@ __device__ __forceinline__ void store_results(const ProductArgs& p, int64_t rank
 
 template <typename T, int BN, bool ALIGNED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide_out) {
-  constexpr int kPieces = BN / 64;                      // a worker loads of a stage
-  constexpr int kCols = BN / 4;                         // of a chunk's sums, a worker takes out
-  constexpr int kSteps = kCols / kStep;
+product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide_out,
+                    const __grid_constant__ CUtensorMap codes_map) {
+  constexpr int kCols = BN / 2;                         // of a chunk's sums, a taker's
   constexpr uint32_t kAtomA = kRows * 128, kAtomB = BN / 2 * 128;         // 64 codes of every row
   constexpr uint32_t kInstr = (1u << 4) | ((uint32_t)(BN / 8) << 17) | (16u << 24);  // f16, fp32 sums, 256 x BN
   extern __shared__ uint8_t raw[];
-  __shared__ __align__(8) uint64_t bars[3 * kStages + 5];
+  __shared__ __align__(8) uint64_t bars[3 * kStages + 2 * kGroups + 5];
   __shared__ uint32_t tmem_at;
   __shared__ volatile int give_up;
-  const uint32_t ring = (smem_addr(raw) + 1023u) & ~1023u;
+  const uint32_t ring = (smem_addr(raw) + 1023u) & ~1023u, codes = ring + kStages * stage_bytes<BN>();
   const uint32_t full = smem_addr(bars), landed = full + 8 * kStages, empty = landed + 8 * kStages,
-                 sums_full = empty + 8 * kStages, sums_empty = sums_full + 16, last = sums_empty + 16;
+                 codes_full = empty + 8 * kStages, codes_free = codes_full + 8 * kGroups,
+                 sums_full = codes_free + 8 * kGroups, sums_empty = sums_full + 16, last = sums_empty + 16;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int half = (int)(blockIdx.x & 1);               // of the pair
   const int pair = (int)(blockIdx.x >> 1), pairs = (int)(gridDim.x >> 1);
@@ -194,14 +218,18 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide_out) 
       mbar_init(landed + 8 * s, 1);
       mbar_init(empty + 8 * s, 1);
     }
+    for (int g = 0; g < kGroups; ++g) {
+      mbar_init(codes_full + 8 * g, 1);
+      mbar_init(codes_free + 8 * g, kGroupWarps);
+    }
     for (int b = 0; b < 2; ++b) {
       mbar_init(sums_full + 8 * b, 1);
-      mbar_init(sums_empty + 8 * b, 2 * kWorkers);
+      mbar_init(sums_empty + 8 * b, 2 * kTakers);
     }
     mbar_init(last, 1);
     fence_barrier_init();
   }
-  if (warp == kWorkers) {
+  if (warp == kIssuer) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
                  :: "r"(smem_addr(&tmem_at)), "r"(2 * BN) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
@@ -213,7 +241,7 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide_out) 
   const uint32_t tmem = tmem_at;
   pdl_wait();
 
-  if (warp >= kWorkers) {
+  if (warp >= kIssuer) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kIssuerRegs));
     int slot = 0;
     uint32_t phase = 0;
@@ -223,8 +251,8 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide_out) 
         phase ^= 1;
       }
     };
-    if (warp == kWorkers && half == 0) {
-      // Issues the matrix instructions of the pair (one lane; the warp stays
+    if (warp == kIssuer && half == 0) {
+      // The pair's matrix instructions (one lane issues; the warp stays
       // together, so that addresses are uniform).
       const bool one = elect_one();
       uint32_t chunk = 0;
@@ -257,8 +285,8 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide_out) 
         wait_on(last, 0, &give_up);
         give_up = 1;
       }
-    } else if (warp == kWorkers + 1 && lane == 0) {
-      // Copies the tokens' f16 codes.
+    } else if (warp == kIssuer + 1 && lane == 0) {
+      // The tokens' copies.
       const int64_t blocks = wide_blocks(p.tokens);
       const uint64_t policy = policy_evict_normal();
       int64_t issued = 0;
@@ -277,167 +305,143 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide_out) 
           next();
         }
       }
-      if (!ok) {                       // no copy outlives the block
-        for (int n = 0; n < kStages && issued > 0; ++n, --issued) {
-          slot = slot == 0 ? kStages - 1 : slot - 1;
-          if (slot == kStages - 1) phase ^= 1;
-          give_up = 0;
-          wait_on(landed + 8 * slot, phase, &give_up);
-          give_up = 1;
+      for (int n = 0; !ok && n < kStages && issued > 0; ++n, --issued) {  // no copy outlives the block
+        slot = slot == 0 ? kStages - 1 : slot - 1;
+        if (slot == kStages - 1) phase ^= 1;
+        give_up = 0;
+        wait_on(landed + 8 * slot, phase, &give_up);
+        give_up = 1;
+      }
+    } else if (ALIGNED && warp == kIssuer + 2 && lane == 0) {
+      // The channels' copies, a slot for each group of turners.
+      int64_t g = 0;
+      bool ok = true;
+      for (int tile = pair; tile < tiles.total && ok; tile += pairs) {
+        const Place at = place_of(tiles, tile);
+        for (int s = 0; s < stages; ++s, ++g) {
+          const uint32_t bar = codes_full + 8 * (uint32_t)(g & 1);
+          ok = wait_on(codes_free + 8 * (uint32_t)(g & 1), (uint32_t)((g >> 1) & 1) ^ 1u, &give_up);
+          if (!ok) break;
+          mbar_expect_tx(bar, code_bytes<BN>());
+          load_box(codes + (uint32_t)(g & 1) * code_bytes<BN>(), &codes_map, s * kStageDepth,
+                   at.col * BN + half * (BN / 2), p.rank_w == 0 ? 0 : at.rank, bar);
         }
+      }
+      for (int n = 0; !ok && n < kGroups && g > 0; ++n) {                 // no copy outlives the block
+        --g;
+        give_up = 0;
+        wait_on(codes_full + 8 * (uint32_t)(g & 1), (uint32_t)((g >> 1) & 1), &give_up);
+        give_up = 1;
       }
     }
     __syncwarp();
-  } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kWorkerRegs));
-    // This thread's pieces: 16 codes from 16 * seg of rows r0 + 32 i of the
-    // channels.  A quarter of a warp stores four pieces of two rows of one
-    // atom: swizzled, they lie in different banks; a row's eight pieces are
-    // one 128-byte line.
-    const int group = warp / kGroupWarps;
-    const int seg = (lane & 3) + 4 * ((lane >> 3) & 1);
-    const int r0 = (warp % kGroupWarps) * 4 + ((lane >> 2) & 1) + 2 * (lane >> 4);
-    const uint32_t put = 2 * kAtomA + (seg >> 2) * kAtomB +
-                         (uint32_t)(r0 * 128 + (((2 * (seg & 3)) ^ (r0 & 7)) << 4));
-    // The group's next stage: its tile and place in it; and the rows.
-    int tile = pair;
+  } else if (warp >= kTakers) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kTurnerRegs));
+    // This thread's pieces: 16 codes from 16 * seg of a row.  Eight lanes
+    // that load or store together have eight rows and one seg: swizzled, they
+    // lie in different banks.
+    constexpr int kPieces = BN / 32;                    // a thread turns of a stage
+    const int group = (warp - kTakers) / kGroupWarps;
+    const int r0 = (warp % kGroupWarps) * (BN / 8) + (lane & 7), seg0 = lane >> 3;
+    const uint32_t from = codes + (uint32_t)group * code_bytes<BN>() + (uint32_t)r0 * 128;
+    const uint32_t from0 = from + (uint32_t)((seg0 ^ (lane & 7)) << 4), from1 = from + (uint32_t)(((seg0 + 4) ^ (lane & 7)) << 4);
+    const uint32_t put = 2 * kAtomA + (uint32_t)(r0 * 128 + (((2 * seg0) ^ (lane & 7)) << 4));
+    int slot = group;
+    uint32_t phase = 0, codes_phase = 0;
     int stage = group;
-    const int8_t* row[kPieces];
-    // Rows past the last channel repeat it: their results are dropped.
-    auto find_rows = [&]() {
-      const Place at = place_of(tiles, tile < tiles.total ? tile : pair);
-#pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
-        const int64_t c = (int64_t)at.col * BN + half * (BN / 2) + r0 + 32 * i;
-        row[i] = p.w + at.rank * p.rank_w + (c < p.channels ? c : p.channels - 1) * p.ld_w + 16 * seg;
-      }
-    };
-    // The chunk (of this pair's, in order) that stage belongs to, and its place there.
-    int chunk = 0, in_chunk = group;
-    auto settle = [&]() {               // after a step: into the next chunk or tile
-      bool moved = false;
-      while (tile < tiles.total) {
-        const int rest = stages - (stage - in_chunk);           // of the tile, from the chunk's first
-        const int here = rest < chunk_stages ? rest : chunk_stages;
-        if (in_chunk < here) break;
-        in_chunk -= here;
-        ++chunk;
-        if (here == rest) {
-          stage = in_chunk;
-          tile += pairs;
-          moved = true;
-        }
-      }
-      if (moved) find_rows();
-    };
-    uint4 held[kPieces];
-    auto load_stage = [&]() {
-      const int64_t k = (int64_t)stage * kStageDepth;
-      if (ALIGNED && k + 16 * seg + 16 <= p.depth) {
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) held[i] = __ldg(reinterpret_cast<const uint4*>(row[i] + k));
-      } else {
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i)
-          held[i] = load_codes<ALIGNED>(row[i] - 16 * seg, k + 16 * seg, p.depth);
-      }
-    };
-
-    // Chunks' sums: those of chunk `taken` (of this pair's, in order) are the
-    // next to be taken out, 16 columns a step.
-    int sum[kCols];
-    int taken = 0;
-    int take_tile = pair;
-    int step = 0, take_chunk = 0;       // of the tile
     bool ok = true;
-    const uint32_t my_tmem = tmem + ((uint32_t)(warp & 3) << 21) + (uint32_t)(warp >> 2) * kCols;
-    auto take_step = [&]() {
-      const uint32_t b = (uint32_t)(taken & 1);
-      const bool first = take_chunk == 0, final = take_chunk == chunks - 1;
-      if (step == 0) {
-        ok = __all_sync(0xFFFFFFFFu, wait_on(sums_full + 8 * b, (uint32_t)((taken >> 1) & 1), &give_up));
-        if (!ok) return;
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      }
+    for (int tile = pair; tile < tiles.total && ok; tile += pairs, stage -= stages) {
+      const Place at = place_of(tiles, tile);
+      for (; stage < stages; stage += kGroups) {
+        uint4 held[kPieces];
+        if (ALIGNED) {
+          ok = __all_sync(0xFFFFFFFFu, wait_on(codes_full + 8 * group, codes_phase, &give_up));
+          if (!ok) break;
+          codes_phase ^= 1;
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        if (s != step) continue;
+          for (int i = 0; i < kPieces; ++i)             // two pieces of each eighth row
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(held[i].x), "=r"(held[i].y), "=r"(held[i].z), "=r"(held[i].w)
+                         : "r"((i & 1 ? from1 : from0) + (i >> 1) * 1024) : "memory");
+        } else {
 #pragma unroll
-        for (int j = s * kStep; j < (s + 1) * kStep; j += 8) {
-          float v[8];
-          tmem_load8(my_tmem + b * BN + j, v);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int x = __float2int_rn(v[i]);
-            sum[j + i] = first ? x : sum[j + i] + x;
+          for (int i = 0; i < kPieces; ++i) {           // rows past the last repeat it: dropped
+            const int64_t c = (int64_t)at.col * BN + half * (BN / 2) + r0 + 8 * (i >> 1);
+            const int8_t* row = p.w + at.rank * p.rank_w + (c < p.channels ? c : p.channels - 1) * p.ld_w;
+            const int64_t k = (int64_t)stage * kStageDepth + 16 * (seg0 + 4 * (i & 1));
+            held[i] = k < p.depth ? load_codes<false>(row, k, p.depth) : make_uint4(0, 0, 0, 0);
           }
         }
-        if (final) {
-          const Place at = place_of(tiles, take_tile);
-          const int64_t t = (int64_t)at.row * 256 + half * kRows + (warp & 3) * 32 + lane;
-          const int64_t c = (int64_t)at.col * BN + (warp >> 2) * kCols + s * kStep;
-          if (t < p.tokens && c < p.channels)
-            store_results<T>(p, at.rank, static_cast<T*>(p.out) + at.rank * p.rank_out + t * p.ld_out, c,
-                             sum + s * kStep, __ldg(p.a_scales + at.rank * p.rank_a_scales + t), wide_out);
+        ok = __all_sync(0xFFFFFFFFu, wait_on(empty + 8 * slot, phase ^ 1u, &give_up));
+        if (!ok) break;
+        const uint32_t base = ring + slot * stage_bytes<BN>() + put;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+          const uint32_t to = base + (i >> 1) * 1024 + (i & 1 ? kAtomB : 0);
+          uint32_t h[8];
+          codes_to_f16(held[i].x, h[0], h[1]);
+          codes_to_f16(held[i].y, h[2], h[3]);
+          codes_to_f16(held[i].z, h[4], h[5]);
+          codes_to_f16(held[i].w, h[6], h[7]);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                       :: "r"(to), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                       :: "r"(to ^ 16u), "r"(h[4]), "r"(h[5]), "r"(h[6]), "r"(h[7]) : "memory");
+        }
+        fence_proxy_async();
+        if (ALIGNED) {                  // all of this warp's pieces are in registers and turned
+          __syncwarp();
+          if (lane == 0) arrive_here(codes_free + 8 * group);
+        }
+        if (warp % kGroupWarps == 0)    // one warp vouches for the tokens' copy too
+          ok = __all_sync(0xFFFFFFFFu, wait_on(landed + 8 * slot, phase, &give_up));
+        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) arrive_first(full + 8 * slot);
+        slot += kGroups;
+        if (slot >= kStages) {
+          slot -= kStages;
+          phase ^= 1;
         }
       }
-      if (++step == kSteps) {
+    }
+    if (!ok && lane == 0) atomicOr(&g_gave_up, 1);
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kTakerRegs));
+    int sum[kCols];
+    uint32_t chunk = 0;
+    bool ok = true;
+    const uint32_t my_tmem = tmem + ((uint32_t)(warp & 3) << 21) + (uint32_t)(warp >> 2) * kCols;
+    for (int tile = pair; tile < tiles.total && ok; tile += pairs) {
+      for (int c = 0; c < chunks; ++c, ++chunk) {
+        const uint32_t b = chunk & 1;
+        ok = __all_sync(0xFFFFFFFFu, wait_on(sums_full + 8 * b, (chunk >> 1) & 1, &give_up));
+        if (!ok) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+#pragma unroll
+        for (int j = 0; j < kCols; j += 16) {
+          float v[16];
+          tmem_load16(my_tmem + b * BN + j, v);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int x = __float2int_rn(v[i]);
+            sum[j + i] = c == 0 ? x : sum[j + i] + x;
+          }
+        }
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncwarp();
         if (lane == 0) arrive_first(sums_empty + 8 * b);
-        step = 0;
-        ++taken;
-        if (++take_chunk == chunks) {
-          take_chunk = 0;
-          take_tile += pairs;
-        }
       }
-    };
-
-    settle();
-    find_rows();
-    if (tile < tiles.total) load_stage();
-    int slot = group, complete = 0;
-    uint32_t phase = 0;
-    for (;;) {
-      const bool more = tile < tiles.total;
-      if (!more) chunk = mine * chunks + 1;
-      // The chunk two before this stage's must be out of TMEM now, as this
-      // one's sums go where it was; of one that is known to be complete, half.
-      for (int take = kSteps / 2; ok && (taken <= chunk - 2 || (take > 0 && taken < complete)); --take) take_step();
-      if (!more || !ok) break;
-      ok = __all_sync(0xFFFFFFFFu, wait_on(empty + 8 * slot, phase ^ 1u, &give_up));
       if (!ok) break;
-      const uint32_t base = ring + slot * stage_bytes<BN>() + put;
+      const Place at = place_of(tiles, tile);
+      const int64_t t = (int64_t)at.row * 256 + half * kRows + (warp & 3) * 32 + lane;
+      const int64_t c0 = (int64_t)at.col * BN + (warp >> 2) * kCols;
+      if (t < p.tokens) {
+        T* row = static_cast<T*>(p.out) + at.rank * p.rank_out + t * p.ld_out;
+        const float token = __ldg(p.a_scales + at.rank * p.rank_a_scales + t);
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
-        const uint32_t at = base + 4096 * i;             // 32 rows on
-        uint32_t h[8];
-        codes_to_f16(held[i].x, h[0], h[1]);
-        codes_to_f16(held[i].y, h[2], h[3]);
-        codes_to_f16(held[i].z, h[4], h[5]);
-        codes_to_f16(held[i].w, h[6], h[7]);
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
-                     :: "r"(at), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
-                     :: "r"(at ^ 16u), "r"(h[4]), "r"(h[5]), "r"(h[6]), "r"(h[7]) : "memory");
-      }
-      fence_proxy_async();
-      if (warp % kGroupWarps == 0)      // one warp vouches for the tokens' copy too
-        ok = __all_sync(0xFFFFFFFFu, wait_on(landed + 8 * slot, phase, &give_up));
-      __syncwarp();
-      if (lane == 0 && ok) arrive_first(full + 8 * slot);
-      // Where this stage went, one of this chunk was before: the last chunk's
-      // matrix instructions have ended.
-      if (in_chunk >= kStages) complete = chunk;
-      stage += kGroups;
-      in_chunk += kGroups;
-      settle();
-      if (tile < tiles.total) load_stage();
-      slot += kGroups;
-      if (slot >= kStages) {
-        slot -= kStages;
-        phase ^= 1;
+        for (int j = 0; j < kCols; j += 16)
+          if (c0 + j < p.channels) store_results<T>(p, at.rank, row, c0 + j, sum + j, token, wide_out);
       }
     }
     if (!ok && lane == 0) atomicOr(&g_gave_up, 1);
@@ -446,8 +450,44 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide_out) 
   __syncthreads();
   cluster_sync();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-  if (warp == kWorkers)
+  if (warp == kIssuer)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(2 * BN) : "memory");
+}
+
+// The driver's encoder of tensor maps, looked up once.
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+cudaError_t encoder(EncodeTiled* out) {
+  static std::atomic<void*> known{nullptr};
+  void* f = known.load(std::memory_order_acquire);
+  if (f == nullptr) {
+    cudaDriverEntryPointQueryResult found;
+    cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found);
+    if (e != cudaSuccess) return e;
+    if (found != cudaDriverEntryPointSuccess || f == nullptr) return cudaErrorNotSupported;
+    known.store(f, std::memory_order_release);
+  }
+  *out = reinterpret_cast<EncodeTiled>(f);
+  return cudaSuccess;
+}
+
+// The channels' codes as a tensor of depth x channels x ranks, taken in boxes
+// of 128 codes x BN / 2 channels, rows swizzled; zeros outside.
+template <int BN>
+cudaError_t channels_map(const ProductArgs& p, CUtensorMap* map) {
+  EncodeTiled encode = nullptr;
+  cudaError_t e = encoder(&encode);
+  if (e != cudaSuccess) return e;
+  const int64_t ranks = p.rank_w == 0 ? 1 : p.ranks;
+  const int64_t ld = p.channels > 1 ? p.ld_w : (p.depth + 15) / 16 * 16;
+  const cuuint64_t dims[3] = {(cuuint64_t)p.depth, (cuuint64_t)p.channels, (cuuint64_t)ranks};
+  const cuuint64_t strides[2] = {(cuuint64_t)ld, (cuuint64_t)(ranks > 1 ? p.rank_w : ld)};
+  const cuuint32_t box[3] = {kStageDepth, BN / 2, 1}, every[3] = {1, 1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<int8_t*>(p.w), dims, strides, box, every,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 template <typename T, int BN, bool ALIGNED>
@@ -458,6 +498,8 @@ cudaError_t launch(const ProductArgs& p, const ProductLayout& l, cudaStream_t s)
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<BN>());
   });
   if (e != cudaSuccess) return e;
+  CUtensorMap map = {};
+  if (ALIGNED && (e = channels_map<BN>(p, &map)) != cudaSuccess) return e;
   Tiles t;
   t.rows = (int)((p.tokens + 255) / 256);
   t.cols = (int)((p.channels + BN - 1) / BN);
@@ -470,7 +512,7 @@ cudaError_t launch(const ProductArgs& p, const ProductLayout& l, cudaStream_t s)
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem_bytes<BN>();
   cfg.stream = s;
-  return cudaLaunchKernelEx(&cfg, product_pair_kernel<T, BN, ALIGNED>, p, t, (int)l.wide);
+  return cudaLaunchKernelEx(&cfg, product_pair_kernel<T, BN, ALIGNED>, p, t, (int)l.wide, map);
 }
 
 }  // namespace
