@@ -26,7 +26,7 @@ LIB = LIBDIR / "libecho.so"
 GROUPS = (64, 128, 256)
 TYPES = (0, 1, 2)
 SOURCES = [(src, None) for src in ("echo_api.cu", "echo_noalloc.cu", "norm_api.cu", "int8_api.cu",
-                                   "int8_quantize.cu", "int8_product.cu")] + [
+                                   "int8_quantize.cu", "int8_product.cu", "int8_few.cu")] + [
     (src, (f"_g{g}", f"-DECHO_G={g}"))
     for src in ("k_push.cu", "k_reduce.cu", "k_gather.cu", "k_call.cu", "k_tile.cu")
     for g in GROUPS] + [

@@ -196,6 +196,18 @@ int echo_linear_int8(int64_t ranks, int64_t tokens, int64_t channels, int64_t de
   ECHO_TRY(check_product(ranks, tokens, channels, depth, codes, a_scales, tokens, w, w_scales,
                          w_scale_stride, dtype, out));
   if (tokens == 0) return ECHO_OK;
+  {
+    // The quantizer must not write what the product takes as given.
+    Region given[2 * ECHO_MAX_RANKS];
+    int n = 0;
+    const echo_matrix wt = {const_cast<float*>(w_scales), channels, w_scale_stride};
+    add_regions(w, ranks, channels, depth, 1, given, &n);
+    add_regions(&wt, ranks, 1, channels, 4, given, &n);
+    const Region scales = region(a_scales, 1, ranks * tokens, ranks * tokens, 4);
+    if (!clear_of(codes, ranks, tokens, depth, 1, given, n)) return ECHO_ERR_ARG;
+    for (int i = 0; i < n; ++i)
+      if (overlaps(scales, given[i])) return ECHO_ERR_ARG;
+  }
   const bool many = channels > 0 && product_workspace(ranks, tokens, depth) > 0;
   if (many) ECHO_TRY(check_workspace(ranks, tokens, depth, workspace, workspace_bytes));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -203,7 +215,7 @@ int echo_linear_int8(int64_t ranks, int64_t tokens, int64_t channels, int64_t de
                                 dtype, s));
   if (channels == 0) return ECHO_OK;
   ECHO_OPS_CUDA(launch_product(product_args(ranks, tokens, channels, depth, codes, a_scales, tokens, w,
-                                            w_scales, w_scale_stride, dtype, out, workspace), many, s));
+                                            w_scales, w_scale_stride, dtype, out, workspace), true, s));
   return ECHO_OK;
 }
 

@@ -32,9 +32,9 @@ struct ProductArgs {
   uint8_t* wide;                 // the tokens' codes as f16 (int8_load.h): many tokens only
 };
 
-// Products of more tokens than this run on the tensor cores' tiles, from f16
+// Products of more tokens than this run in tiles (int8_pair.cu), from f16
 // codes in a workspace.
-constexpr int64_t kFewTokens = 32;
+constexpr int64_t kFewTokens = 64;
 // Ranks of the tokens' codes: one where all share them.
 inline int64_t token_ranks(const ProductArgs& p) { return p.rank_a == 0 ? 1 : p.ranks; }
 size_t product_workspace(int64_t ranks, int64_t tokens, int64_t depth);
@@ -55,8 +55,11 @@ struct ProductLayout {
 cudaError_t launch_quantize(const QuantArgs& a, int dtype, cudaStream_t s);
 // The f16 codes of tokens that are in int8 already.
 cudaError_t launch_widen(const ProductArgs& p, bool aligned, cudaStream_t s);
-// `widened`: the workspace already holds the tokens' f16 codes.
-cudaError_t launch_product(const ProductArgs& a, bool widened, cudaStream_t s);
+// `quantized`: this call's quantizer ran just before, and has left the tokens'
+// f16 codes in the workspace where the product needs them.
+cudaError_t launch_product(const ProductArgs& a, bool quantized, cudaStream_t s);
+// `early`: the kernel before is this call's quantizer, see int8_few.cu.
+cudaError_t launch_few(const ProductArgs& p, bool aligned, bool early, cudaStream_t s);
 // One instantiation per type of out (the sources are compiled once for each).
 template <typename T>
 cudaError_t launch_pair(const ProductArgs& p, const ProductLayout& l, cudaStream_t s);

@@ -240,6 +240,7 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide_out,
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = tmem_at;
   pdl_wait();
+  pdl_trigger();
 
   if (warp >= kIssuer) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kIssuerRegs));
@@ -389,7 +390,7 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide_out,
                        :: "r"(to ^ 16u), "r"(h[4]), "r"(h[5]), "r"(h[6]), "r"(h[7]) : "memory");
         }
         fence_proxy_async();
-        if (ALIGNED) {                  // all of this warp's pieces are in registers and turned
+        if (ALIGNED) {                  // only now: a copy can overtake loads that no one has used yet
           __syncwarp();
           if (lane == 0) arrive_here(codes_free + 8 * group);
         }
@@ -512,6 +513,9 @@ cudaError_t launch(const ProductArgs& p, const ProductLayout& l, cudaStream_t s)
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem_bytes<BN>();
   cfg.stream = s;
+  cudaLaunchAttribute overlapped = overlapped_launch();
+  cfg.attrs = &overlapped;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, product_pair_kernel<T, BN, ALIGNED>, p, t, (int)l.wide, map);
 }
 

@@ -24,6 +24,7 @@ quantize_kernel(const QuantArgs a) {
   const int64_t step = (int64_t)blockDim.x * VEC;
   const int64_t col0 = (int64_t)threadIdx.x * VEC;
   pdl_wait();
+  pdl_trigger();
 
   Pack<T, VEC> held[kPieces];
   uint32_t amax = __float_as_uint(kTinyAmax);
@@ -78,6 +79,7 @@ template <bool ALIGNED>
 __global__ void __launch_bounds__(256)
 widen_kernel(const ProductArgs p) {
   pdl_wait();
+  pdl_trigger();
   const int64_t pieces = wide_blocks(p.depth) * (kBlockCodes / 16);
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t row = i / pieces, k = (i - row * pieces) * 16;
@@ -103,6 +105,9 @@ cudaError_t launch(const QuantArgs& a, cudaStream_t s) {
   cfg.gridDim = dim3((unsigned)(a.ranks * a.tokens));
   cfg.blockDim = dim3((unsigned)threads);
   cfg.stream = s;
+  cudaLaunchAttribute overlapped = overlapped_launch();
+  cfg.attrs = &overlapped;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, quantize_kernel<T, VEC>, a);
 }
 
@@ -124,6 +129,9 @@ cudaError_t launch_widen(const ProductArgs& p, bool aligned, cudaStream_t s) {
   cfg.gridDim = dim3((unsigned)((pieces + 255) / 256));
   cfg.blockDim = dim3(256);
   cfg.stream = s;
+  cudaLaunchAttribute overlapped = overlapped_launch();
+  cfg.attrs = &overlapped;
+  cfg.numAttrs = 1;
   return aligned ? cudaLaunchKernelEx(&cfg, widen_kernel<true>, p) : cudaLaunchKernelEx(&cfg, widen_kernel<false>, p);
 }
 

@@ -89,6 +89,7 @@ norm_grad_kernel(const NormGradArgs a, int blocks, int block_cols) {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
                  "barrier.cluster.wait.acquire.aligned;" ::: "memory");
   pdl_wait();
+  pdl_trigger();
 
   bool in[NV];
 #pragma unroll
@@ -312,6 +313,7 @@ __global__ void __launch_bounds__(32 * kFinishRows)
 norm_grad_finish(const NormGradArgs a) {
   __shared__ float part[kFinishRows][33];
   pdl_wait();
+  pdl_trigger();
   const int64_t col = (int64_t)blockIdx.x * 32 + threadIdx.x;
   const int which = blockIdx.y;
   auto put = [&](void* to, int64_t at, float v) {
@@ -360,12 +362,12 @@ cudaError_t launch(NormGradArgs a, int sms, cudaStream_t s) {
   cfg.gridDim = dim3((unsigned)((a.workers + rows - 1) / rows * blocks));
   cfg.blockDim = dim3(threads, rows);
   cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = blocks;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute at[2] = {overlapped_launch()};
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = blocks;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = blocks > 1 ? 1 : 0;
+  cfg.numAttrs = blocks > 1 ? 2 : 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, norm_grad_kernel<T, VEC, NV, LAYER, GATE>, a, blocks, block_cols);
   bool any = a.dgate && a.workers > 1;
   for (int k = 0; k < 4; ++k) any = any || a.dparam[k];
@@ -374,6 +376,8 @@ cudaError_t launch(NormGradArgs a, int sms, cudaStream_t s) {
   fin.gridDim = dim3((unsigned)((a.width + 31) / 32), 5);
   fin.blockDim = dim3(32, kFinishRows);
   fin.stream = s;
+  fin.attrs = at;
+  fin.numAttrs = 1;
   return cudaLaunchKernelEx(&fin, norm_grad_finish<T>, a);
 }
 

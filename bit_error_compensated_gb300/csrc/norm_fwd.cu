@@ -63,6 +63,7 @@ norm_kernel(const NormArgs a) {
   RowReduce red{slots, (int)threadIdx.y * (threads / 32), threads / 32, tid >> 5, tid & 31, 0};
   const float inv_width = 1.0f / (float)a.width;
   pdl_wait();
+  pdl_trigger();
 
   for (int64_t base = (int64_t)blockIdx.x * blockDim.y; base < a.rows;
        base += (int64_t)gridDim.x * blockDim.y) {
@@ -188,6 +189,9 @@ cudaError_t launch(const NormArgs& a, int layer, int sms, cudaStream_t s) {
   cfg.gridDim = dim3((unsigned)(blocks < most ? blocks : most));
   cfg.blockDim = dim3(threads, rows);
   cfg.stream = s;
+  cudaLaunchAttribute overlapped = overlapped_launch();
+  cfg.attrs = &overlapped;
+  cfg.numAttrs = 1;
   return layer ? cudaLaunchKernelEx(&cfg, norm_kernel<T, VEC, NV, true>, a)
                : cudaLaunchKernelEx(&cfg, norm_kernel<T, VEC, NV, false>, a);
 }

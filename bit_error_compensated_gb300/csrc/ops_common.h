@@ -78,8 +78,7 @@ __device__ __forceinline__ void store_floats(T* p, const float (&v)[N]) {
   store_pack<T, N>(p, out);
 }
 
-// Programmatic dependent launch: wait for the kernels this launch depends on,
-// and let the next kernel's blocks be placed.
+// See overlapped_launch below.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -130,6 +129,17 @@ inline cudaError_t device_sms(int* sms) {
   e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
   if (e == cudaSuccess) known[dev & 63].store(*sms, std::memory_order_relaxed);
   return e;
+}
+
+// Programmatic dependent launch: the kernel's blocks may be placed while the
+// one before it in the stream still runs; each of these kernels waits
+// (pdl_wait) before it touches memory, and lets the next one's blocks be
+// placed (pdl_trigger) once it runs itself.
+inline cudaLaunchAttribute overlapped_launch() {
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  return at;
 }
 
 // A strided matrix in memory: `rows` rows of `bytes` bytes, `pitch` bytes apart.
