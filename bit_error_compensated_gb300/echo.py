@@ -9,6 +9,7 @@ this module raises if the library has not been built
 from __future__ import annotations
 
 import ctypes
+import struct
 from pathlib import Path
 
 _LIB_PATH = Path(__file__).resolve().parent / "lib" / "libecho.so"
@@ -50,27 +51,13 @@ ECHO_MATMUL_MAX_DEPTH = 131071
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
 
 
-class _NormParams(ctypes.Structure):           # echo_norm_params
-    _fields_ = [(n, _vp) for n in ("w_post", "b_post", "w_pre", "b_pre")]
-
-
-class _NormIo(ctypes.Structure):               # echo_norm_io
-    _fields_ = [("rows", _i64), ("x", _vp), ("ld_x", _i64), ("y", _vp), ("ld_y", _i64),
-                ("gate", _vp), ("gate_rows", _i64), ("gate_cols", _i64),
-                ("r", _vp), ("ld_r", _i64), ("h", _vp), ("ld_h", _i64),
-                ("codes", _vp), ("ld_codes", _i64), ("scales", _vp), ("stats", _vp)]
-
-
-class _NormGradIo(ctypes.Structure):           # echo_norm_grad_io
-    _fields_ = [("rows", _i64), ("x", _vp), ("ld_x", _i64), ("y", _vp), ("ld_y", _i64),
-                ("gate", _vp), ("gate_rows", _i64), ("gate_cols", _i64), ("stats", _vp),
-                ("dr", _vp), ("ld_dr", _i64), ("dh", _vp), ("ld_dh", _i64),
-                ("dx", _vp), ("ld_dx", _i64), ("dy", _vp), ("ld_dy", _i64), ("dgate", _vp)]
-
-
-class _Matrix(ctypes.Structure):               # echo_matrix
-    _fields_ = [("data", _vp), ("ld", _i64), ("rank_stride", _i64)]
-
+# The C structures of the block operators: nothing but 64-bit integers and
+# pointers, packed into bytes (cheaper than a ctypes.Structure per call).
+_NORM_PARAMS = struct.Struct("4q")        # echo_norm_params: w_post, b_post, w_pre, b_pre
+_NORM_IO = struct.Struct("16q")           # echo_norm_io
+_NORM_GRAD_IO = struct.Struct("18q")      # echo_norm_grad_io
+_MATRIX = struct.Struct("3q")             # echo_matrix: data, ld, rank_stride
+_FEW_TOKENS = 64                          # up to here no product needs a workspace
 
 _SIGS = {
     "echo_plan": (_i32, [_i32, _i64, _i32, _i32, ctypes.POINTER(_vp)]),
@@ -97,19 +84,15 @@ _SIGS = {
     "echo_norm_plan": (_i32, [_i64, _i32, _i32, _i32, _i32, ctypes.c_float, ctypes.c_float,
                               ctypes.POINTER(_vp)]),
     "echo_norm_plan_destroy": (None, [_vp]),
-    "echo_norm": (_i32, [_vp, ctypes.POINTER(_NormParams), ctypes.POINTER(_NormIo), _vp]),
-    "echo_norm_backward": (_i32, [_vp, ctypes.POINTER(_NormParams), ctypes.POINTER(_NormGradIo),
-                                  ctypes.POINTER(_NormParams), _vp]),
-    "echo_quantize_tokens": (_i32, [_i64, _i64, _i64, _i32, ctypes.POINTER(_Matrix),
-                                    ctypes.POINTER(_Matrix), _vp, _vp]),
-    "echo_matmul_int8": (_i32, [_i64, _i64, _i64, _i64, ctypes.POINTER(_Matrix), _vp, _i64,
-                                ctypes.POINTER(_Matrix), _vp, _i64, _i32,
-                                ctypes.POINTER(_Matrix), _vp, _sz, _vp]),
+    "echo_norm": (_i32, [_vp, _vp, _vp, _vp]),
+    "echo_norm_backward": (_i32, [_vp, _vp, _vp, _vp, _vp]),
+    "echo_quantize_tokens": (_i32, [_i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp]),
+    "echo_matmul_int8": (_i32, [_i64, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _i32, _vp,
+                                _vp, _sz, _vp]),
     "echo_matmul_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "echo_matmul_status": (_i32, [_vp, ctypes.POINTER(_i32)]),
-    "echo_linear_int8": (_i32, [_i64, _i64, _i64, _i64, _i32, ctypes.POINTER(_Matrix),
-                                ctypes.POINTER(_Matrix), _vp, _i64, ctypes.POINTER(_Matrix), _vp,
-                                ctypes.POINTER(_Matrix), _vp, _sz, _vp]),
+    "echo_linear_int8": (_i32, [_i64, _i64, _i64, _i64, _i32, _vp, _vp, _vp, _i64, _vp, _vp, _vp,
+                                _vp, _sz, _vp]),
     "echo_strerror": (ctypes.c_char_p, [_i32]),
 }
 for _name, (_res, _args) in _SIGS.items():
@@ -188,6 +171,9 @@ def _state_dtypes(fmt: int):
 def _stream(stream) -> int | None:
     if stream is None:
         import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:                       # without making a Stream object: 0.1 us, not 3
+            return raw(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -360,6 +346,9 @@ def echo_plan_destroy(plan: Plan) -> None:
 # ---------------------------------------------------------------------------
 # The operators on either side of the all-reduce.  Their arguments are tensors
 # (strides and sizes are read from them); outputs are the caller's buffers.
+# A decode loop makes these calls once a token and layer, so the checks are one
+# cheap test of each tensor (_fits); only a tensor that fails it goes through
+# _refuse, which says what is wrong.
 
 def _dtype_code(dtype) -> int:
     import torch
@@ -369,39 +358,45 @@ def _dtype_code(dtype) -> int:
     return code
 
 
-def _expect(t, what: str, dtype, shape) -> None:
-    """dtype, shape and unit stride along the last dimension."""
+def _fits(t, dtype, shape, device) -> bool:
+    """Of this dtype, shape and device, the elements of a row contiguous."""
+    return (t.dtype is dtype and t.shape == shape and t.get_device() == device
+            and (t.stride()[-1] == 1 or shape[-1] <= 1))
+
+
+def _refuse(t, what: str, dtype, shape, device) -> None:
     if t.dtype != dtype:
         raise ValueError(f"{what}: dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {shape}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{what}: elements of a row must be contiguous")
+    if not t.is_cuda:
+        raise ValueError(f"{what}: tensor must be on a CUDA device")
+    raise ValueError(f"{what}: tensor on cuda:{t.get_device()}, but the call runs on cuda:{device}")
 
 
-def _expect_contiguous(t, what: str, dtype, shape) -> None:
-    _expect(t, what, dtype, shape)
+def _expect(t, what: str, dtype, shape, device) -> None:
+    if not _fits(t, dtype, shape, device):
+        _refuse(t, what, dtype, shape, device)
+
+
+def _expect_contiguous(t, what: str, dtype, shape, device) -> None:
+    if not _fits(t, dtype, shape, device):
+        _refuse(t, what, dtype, shape, device)
     if not t.is_contiguous():
         raise ValueError(f"{what}: tensor must be contiguous")
 
 
-def _on_device(device: int | None, *tensors) -> None:
-    """Every tensor on the device that the call runs on: the current one."""
+def _call_device(t, plan=None) -> int:
+    """The device that a call runs on: the current one, and the plan's."""
+    if not t.is_cuda:
+        raise ValueError("tensor must be on a CUDA device")
     import torch
-    for t in tensors:
-        if t is not None and not t.is_cuda:
-            raise ValueError("tensor must be on a CUDA device")
-    current = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != current:
-            raise ValueError(f"tensor on cuda:{t.get_device()}, but the current device is cuda:{current}")
-    if device is not None and device != current:
-        raise ValueError(f"the plan belongs to cuda:{device}, but the current device is cuda:{current}")
-
-
-def _at(t) -> tuple:
-    """(address, row distance) of a matrix, or (None, 0)."""
-    return (None, 0) if t is None else (t.data_ptr(), t.stride(0))
+    device = torch.cuda.current_device()
+    if plan is not None and plan.device != device:
+        raise ValueError(f"the plan belongs to cuda:{plan.device}, but the current device is cuda:{device}")
+    return device
 
 
 class NormPlan:
@@ -416,10 +411,6 @@ class NormPlan:
         h, self.handle = getattr(self, "handle", None), None
         if h:
             _lib.echo_norm_plan_destroy(h)
-
-    @property
-    def _as_parameter_(self):
-        return ctypes.c_void_p(self.handle)
 
 
 def echo_norm_plan(width: int, dtype, param_dtype=None, kind: int = ECHO_NORM_RMS, post: bool = True,
@@ -445,16 +436,31 @@ class NormParams:
     once: contiguous tensors of `width` elements of the plan's param_dtype, or
     None.  Keeps the tensors; their addresses are taken once."""
 
-    __slots__ = ("_keep", "_struct")
+    __slots__ = ("_keep", "_plan", "_packed")
 
     def __init__(self, plan: NormPlan, w_post=None, b_post=None, w_pre=None, b_pre=None):
         self._keep = (w_post, b_post, w_pre, b_pre)
+        self._plan = plan
         for t, what in zip(self._keep, ("w_post", "b_post", "w_pre", "b_pre")):
             if t is not None:
-                _expect_contiguous(t, what, plan.param_dtype, (plan.width,))
-        if any(t is not None for t in self._keep):
-            _on_device(plan.device, *self._keep)
-        self._struct = _NormParams(*[None if t is None else t.data_ptr() for t in self._keep])
+                _expect_contiguous(t, what, plan.param_dtype, (plan.width,), plan.device)
+        self._packed = _NORM_PARAMS.pack(*[0 if t is None else t.data_ptr() for t in self._keep])
+
+
+def _packed_params(plan: NormPlan, params):
+    if params is None:
+        return None
+    if params._plan is not plan:
+        raise ValueError("these parameters were checked for another plan")
+    return params._packed
+
+
+def _norm_rows(plan: NormPlan, x) -> int:
+    if plan.handle is None:
+        raise ValueError("the plan was destroyed")
+    if x.dim() != 2:
+        raise ValueError(f"x: shape {tuple(x.shape)}, expected (rows, {plan.width})")
+    return x.shape[0]
 
 
 def _norm_gate(plan: NormPlan, gate, dgate, rows: int) -> tuple:
@@ -462,14 +468,14 @@ def _norm_gate(plan: NormPlan, gate, dgate, rows: int) -> tuple:
     if gate is None:
         if dgate is not None:
             raise ValueError("dgate without gate")
-        return None, 0, 0
+        return 0, 0, 0
     shape = tuple(gate.shape)
     if len(shape) != 2 or shape[1] not in (plan.width, 1) or shape[0] < 1 or rows % shape[0]:
         raise ValueError(f"gate: shape {shape}, expected (rows of which {rows} is a multiple, "
                          f"{plan.width} or 1)")
-    _expect_contiguous(gate, "gate", plan.param_dtype, shape)
+    _expect_contiguous(gate, "gate", plan.param_dtype, shape, plan.device)
     if dgate is not None:
-        _expect_contiguous(dgate, "dgate", plan.param_dtype, shape)
+        _expect_contiguous(dgate, "dgate", plan.param_dtype, shape, plan.device)
     return gate.data_ptr(), shape[0], shape[1]
 
 
@@ -478,32 +484,37 @@ def echo_norm(plan: NormPlan, params: NormParams | None, x, y=None, r=None, h=No
     """x, y, r, h: [rows][width] tensors of the plan's dtype, any row distance
     (y, r, h may be None); gate: [gate rows][width or 1]; codes int8
     [rows][width] with scales fp32 [rows]; stats fp32 [rows][4]."""
-    if x.dim() != 2:
-        raise ValueError(f"x: shape {tuple(x.shape)}, expected (rows, {plan.width})")
-    rows = x.shape[0]
-    shape, dtype = (rows, plan.width), plan.dtype
-    _expect(x, "x", dtype, shape)
+    rows = _norm_rows(plan, x)
+    shape, dtype, device = (rows, plan.width), plan.dtype, plan.device
+    _expect(x, "x", dtype, shape, device)
+    _call_device(x, plan)
+    at_y = at_r = at_h = at_codes = at_scales = at_stats = ld_y = ld_r = ld_h = ld_codes = 0
     if y is not None:
-        _expect(y, "y", dtype, shape)
+        _expect(y, "y", dtype, shape, device)
+        at_y, ld_y = y.data_ptr(), y.stride()[0]
     if r is not None:
-        _expect(r, "r", dtype, shape)
+        _expect(r, "r", dtype, shape, device)
+        at_r, ld_r = r.data_ptr(), r.stride()[0]
     if h is not None:
-        _expect(h, "h", dtype, shape)
+        _expect(h, "h", dtype, shape, device)
+        at_h, ld_h = h.data_ptr(), h.stride()[0]
     if (codes is None) != (scales is None):
         raise ValueError("codes and scales belong together")
     if codes is not None:
         import torch
-        _expect(codes, "codes", torch.int8, shape)
-        _expect_contiguous(scales, "scales", torch.float32, (rows,))
+        _expect(codes, "codes", torch.int8, shape, device)
+        _expect_contiguous(scales, "scales", torch.float32, (rows,), device)
+        at_codes, ld_codes, at_scales = codes.data_ptr(), codes.stride()[0], scales.data_ptr()
     if stats is not None:
         import torch
-        _expect_contiguous(stats, "stats", torch.float32, (rows, 4))
-    gate_args = _norm_gate(plan, gate, None, rows)
-    _on_device(plan.device, x, y, r, h, gate, codes, scales, stats)
-    io = _NormIo(rows, *_at(x), *_at(y), *gate_args, *_at(r), *_at(h), *_at(codes), _ptr(scales),
-                 _ptr(stats))
-    _check(_lib.echo_norm(plan, None if params is None else params._struct, io, _stream(stream)),
-           "echo_norm")
+        _expect_contiguous(stats, "stats", torch.float32, (rows, 4), device)
+        at_stats = stats.data_ptr()
+    at_gate, gate_rows, gate_cols = _norm_gate(plan, gate, None, rows)
+    io = _NORM_IO.pack(rows, x.data_ptr(), x.stride()[0], at_y, ld_y, at_gate, gate_rows, gate_cols,
+                       at_r, ld_r, at_h, ld_h, at_codes, ld_codes, at_scales, at_stats)
+    status = _lib.echo_norm(plan.handle, _packed_params(plan, params), io, _stream(stream))
+    if status:
+        raise EchoError(status, "echo_norm")
 
 
 def echo_norm_backward(plan: NormPlan, params: NormParams | None, x, y, stats, dr, dh, dx=None,
@@ -513,69 +524,69 @@ def echo_norm_backward(plan: NormPlan, params: NormParams | None, x, y, stats, d
     (either may be None); dx, dy, dgate and grads (a NormParams of the plan
     holding the tensors to write) receive the gradients."""
     import torch
-    if x.dim() != 2:
-        raise ValueError(f"x: shape {tuple(x.shape)}, expected (rows, {plan.width})")
-    rows = x.shape[0]
-    shape = (rows, plan.width)
+    rows = _norm_rows(plan, x)
+    shape, device = (rows, plan.width), plan.device
+    at = []
     for t, what in ((x, "x"), (y, "y"), (dr, "dr"), (dh, "dh"), (dx, "dx"), (dy, "dy")):
-        if t is not None:
-            _expect(t, what, plan.dtype, shape)
+        if t is None:
+            at += (0, 0)
+        else:
+            _expect(t, what, plan.dtype, shape, device)
+            at += (t.data_ptr(), t.stride()[0])
+    _call_device(x, plan)
     if stats is not None:
-        _expect_contiguous(stats, "stats", torch.float32, (rows, 4))
+        _expect_contiguous(stats, "stats", torch.float32, (rows, 4), device)
     gate_args = _norm_gate(plan, gate, dgate, rows)
-    _on_device(plan.device, x, y, stats, dr, dh, dx, dy, gate, dgate)
-    io = _NormGradIo(rows, *_at(x), *_at(y), *gate_args, _ptr(stats), *_at(dr), *_at(dh), *_at(dx),
-                     *_at(dy), _ptr(dgate))
-    _check(_lib.echo_norm_backward(plan, None if params is None else params._struct, io,
-                                   None if grads is None else grads._struct, _stream(stream)),
-           "echo_norm_backward")
+    io = _NORM_GRAD_IO.pack(rows, *at[:4], *gate_args, 0 if stats is None else stats.data_ptr(), *at[4:],
+                            0 if dgate is None else dgate.data_ptr())
+    status = _lib.echo_norm_backward(plan.handle, _packed_params(plan, params), io,
+                                     _packed_params(plan, grads), _stream(stream))
+    if status:
+        raise EchoError(status, "echo_norm_backward")
 
 
-def _matrix(t, ranks: int) -> _Matrix:
+def _matrix(t) -> bytes:
     """A [ranks][rows][cols] tensor, or a [rows][cols] one that all ranks share."""
-    if t.dim() == 2:
-        return _Matrix(t.data_ptr(), t.stride(0), 0)
-    return _Matrix(t.data_ptr(), t.stride(1), t.stride(0) if ranks > 1 else 0)
+    stride = t.stride()
+    if len(stride) == 2:
+        return _MATRIX.pack(t.data_ptr(), stride[0], 0)
+    return _MATRIX.pack(t.data_ptr(), stride[1], stride[0] if t.shape[0] > 1 else 0)
 
 
 def _batch(t, what: str) -> tuple:
-    """(ranks or None, rows, columns) of a two- or three-dimensional tensor."""
-    if t.dim() == 2:
-        return (None, *t.shape)
-    if t.dim() == 3:
-        return tuple(t.shape)
-    raise ValueError(f"{what}: shape {tuple(t.shape)}, expected two or three dimensions")
+    """(ranks, rows, columns) of a two- or three-dimensional tensor."""
+    shape = t.shape
+    if len(shape) == 2:
+        return 1, shape[0], shape[1]
+    if len(shape) == 3:
+        return shape
+    raise ValueError(f"{what}: shape {tuple(shape)}, expected two or three dimensions")
 
 
-def _with_ranks(t, shape: tuple) -> tuple:
-    """The shape expected of an input that may be shared by the ranks."""
-    return shape if t.dim() == len(shape) else shape[1:]
-
-
-def _check_product(codes_like, w, w_scales, out) -> tuple:
-    """(ranks, tokens, channels, depth) of a product, its tensors checked
-    (those of the tokens' side apart from their last dimension's type)."""
+def _check_product(tokens_of, what: str, dtype, scales, w, w_scales, out, device: int) -> tuple:
+    """(ranks, tokens, channels, depth) of a product whose tensors fit: out
+    [ranks][tokens][channels] or without ranks, the tokens' tensor and scales,
+    w and w_scales each with the ranks' dimension or without it."""
     import torch
     ranks, tokens, channels = _batch(out, "out")
-    ranks = 1 if ranks is None else ranks
     depth = w.shape[-1]
-    full = (ranks, tokens, depth)
-    if tuple(codes_like.shape) not in (full, full[1:]):
-        raise ValueError(f"tokens: shape {tuple(codes_like.shape)}, expected {full} or {full[1:]}")
-    _batch(w, "w")
-    _expect(w, "w", torch.int8, _with_ranks(w, (ranks, channels, depth)))
-    if w_scales.dim() not in (1, 2):
-        raise ValueError(f"w_scales: shape {tuple(w_scales.shape)}, expected one or two dimensions")
+    if len(tokens_of.shape) == 3:
+        _expect(tokens_of, what, dtype, (ranks, tokens, depth), device)
+        _expect_contiguous(scales, "scales", torch.float32, (ranks, tokens), device)
+    else:
+        _expect(tokens_of, what, dtype, (tokens, depth), device)
+        _expect_contiguous(scales, "scales", torch.float32, (tokens,), device)
+    _expect(w, "w", torch.int8, (ranks, channels, depth) if len(w.shape) == 3 else (channels, depth), device)
     _expect(w_scales, "w_scales", torch.float32,
-            (ranks, channels) if w_scales.dim() == 2 else (channels,))
-    _expect(out, "out", out.dtype, (ranks, tokens, channels) if out.dim() == 3 else (tokens, channels))
+            (ranks, channels) if len(w_scales.shape) == 2 else (channels,), device)
+    _expect(out, "out", out.dtype, out.shape, device)
     return ranks, tokens, channels, depth
 
 
 def _workspace(ranks: int, tokens: int, depth: int, device, stream) -> tuple:
     """(tensor or None, address, bytes) of a product's workspace, from torch's
     allocator: ordered by the stream that the call runs on."""
-    nbytes = int(_lib.echo_matmul_workspace_bytes(ranks, tokens, depth))
+    nbytes = _lib.echo_matmul_workspace_bytes(ranks, tokens, depth)
     if nbytes == 0:
         return None, None, 0
     import torch
@@ -598,16 +609,15 @@ def echo_quantize_tokens(x, codes, scales, stream=None) -> None:
     shape and one fp32 scale a token, [ranks][tokens] contiguous."""
     import torch
     ranks, tokens, depth = _batch(x, "x")
-    shape = tuple(x.shape)
-    _expect(x, "x", x.dtype, shape)
-    _expect(codes, "codes", torch.int8, shape)
-    _expect_contiguous(scales, "scales", torch.float32, shape[:-1])
-    dtype = _dtype_code(x.dtype)
-    _on_device(None, x, codes, scales)
-    ranks = 1 if ranks is None else ranks
-    _check(_lib.echo_quantize_tokens(ranks, tokens, depth, dtype, _matrix(x, ranks),
-                                     _matrix(codes, ranks), scales.data_ptr(), _stream(stream)),
-           "echo_quantize_tokens")
+    dtype, shape = _dtype_code(x.dtype), x.shape
+    device = _call_device(x)
+    _expect(x, "x", x.dtype, shape, device)
+    _expect(codes, "codes", torch.int8, shape, device)
+    _expect_contiguous(scales, "scales", torch.float32, shape[:-1], device)
+    status = _lib.echo_quantize_tokens(ranks, tokens, depth, dtype, _matrix(x), _matrix(codes),
+                                       scales.data_ptr(), _stream(stream))
+    if status:
+        raise EchoError(status, "echo_quantize_tokens")
 
 
 def echo_matmul_int8(codes, scales, w, w_scales, out, stream=None) -> None:
@@ -616,18 +626,19 @@ def echo_matmul_int8(codes, scales, w, w_scales, out, stream=None) -> None:
     w_scales: with the ranks' dimension, or without it where all ranks share
     them (codes and scales both)."""
     import torch
-    ranks, tokens, channels, depth = _check_product(codes, w, w_scales, out)
-    _expect(codes, "codes", torch.int8, tuple(codes.shape))
-    _expect_contiguous(scales, "scales", torch.float32, tuple(codes.shape[:-1]))
-    dtype = _dtype_code(out.dtype)
-    _on_device(None, codes, scales, w, w_scales, out)
-    keep, at, nbytes = _workspace(ranks if codes.dim() == 3 and codes.stride(0) else 1, tokens, depth,
-                                  codes.device, stream)
-    _check(_lib.echo_matmul_int8(ranks, tokens, channels, depth, _matrix(codes, ranks),
-                                 scales.data_ptr(), tokens if codes.dim() == 3 else 0,
-                                 _matrix(w, ranks), w_scales.data_ptr(),
-                                 w_scales.stride(0) if w_scales.dim() == 2 else 0, dtype,
-                                 _matrix(out, ranks), at, nbytes, _stream(stream)), "echo_matmul_int8")
+    device = _call_device(out)
+    ranks, tokens, channels, depth = _check_product(codes, "codes", torch.int8, scales, w, w_scales, out, device)
+    stride = codes.stride()
+    own = len(stride) == 3               # each rank has its own tokens, unless they are expanded
+    keep, at, nbytes = (None, None, 0)
+    if tokens > _FEW_TOKENS:
+        keep, at, nbytes = _workspace(ranks if own and stride[0] else 1, tokens, depth, out.device, stream)
+    status = _lib.echo_matmul_int8(ranks, tokens, channels, depth, _matrix(codes), scales.data_ptr(),
+                                   tokens if own else 0, _matrix(w), w_scales.data_ptr(),
+                                   w_scales.stride()[0] if len(w_scales.shape) == 2 else 0,
+                                   _dtype_code(out.dtype), _matrix(out), at, nbytes, _stream(stream))
+    if status:
+        raise EchoError(status, "echo_matmul_int8")
 
 
 def echo_matmul_status(stream=None) -> int:
@@ -641,21 +652,21 @@ def echo_linear_int8(x, w, w_scales, out, codes, scales, stream=None) -> None:
     x [ranks][tokens][depth] (or without ranks) and out of one dtype; codes
     and scales are the caller's buffers for the quantized tokens."""
     import torch
-    ranks, tokens, channels, depth = _check_product(x, w, w_scales, out)
-    shape = tuple(x.shape)
-    if len(shape) != out.dim():
-        raise ValueError(f"x: shape {shape}, expected the {out.dim()} dimensions of out")
-    _expect(x, "x", out.dtype, shape)
-    _expect(codes, "codes", torch.int8, shape)
-    _expect_contiguous(scales, "scales", torch.float32, shape[:-1])
-    dtype = _dtype_code(x.dtype)
-    _on_device(None, x, w, w_scales, out, codes, scales)
-    keep, at, nbytes = _workspace(ranks, tokens, depth, x.device, stream)
-    _check(_lib.echo_linear_int8(ranks, tokens, channels, depth, dtype, _matrix(x, ranks),
-                                 _matrix(w, ranks), w_scales.data_ptr(),
-                                 w_scales.stride(0) if w_scales.dim() == 2 else 0,
-                                 _matrix(codes, ranks), scales.data_ptr(), _matrix(out, ranks),
-                                 at, nbytes, _stream(stream)), "echo_linear_int8")
+    device = _call_device(out)
+    ranks, tokens, channels, depth = _check_product(codes, "codes", torch.int8, scales, w, w_scales, out, device)
+    shape = x.shape
+    if len(shape) != len(out.shape):
+        raise ValueError(f"x: shape {tuple(shape)}, expected the {len(out.shape)} dimensions of out")
+    _expect(x, "x", out.dtype, codes.shape, device)
+    keep, at, nbytes = (None, None, 0)
+    if tokens > _FEW_TOKENS:
+        keep, at, nbytes = _workspace(ranks, tokens, depth, out.device, stream)
+    status = _lib.echo_linear_int8(ranks, tokens, channels, depth, _dtype_code(x.dtype), _matrix(x), _matrix(w),
+                                   w_scales.data_ptr(),
+                                   w_scales.stride()[0] if len(w_scales.shape) == 2 else 0,
+                                   _matrix(codes), scales.data_ptr(), _matrix(out), at, nbytes, _stream(stream))
+    if status:
+        raise EchoError(status, "echo_linear_int8")
 
 
 def echo_strerror(status: int) -> str:
