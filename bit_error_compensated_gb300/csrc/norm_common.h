@@ -46,23 +46,24 @@ struct NormGradArgs {
   int gate_scalar, post, params_f32;
 };
 
-// N floats of a parameter vector (or gate row) of either type, from element
-// `col`; `missing` where there is none.
+// N floats of a parameter vector (or gate row) of either type, from element `col`.
 template <typename T, int N>
-__device__ __forceinline__ void load_param(const void* p, int f32, int64_t col, float missing,
-                                           float (&out)[N]) {
-  if (p == nullptr) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) out[i] = missing;
-  } else if (sizeof(T) == 4 || f32) {
+__device__ __forceinline__ void load_param(const void* p, int f32, int64_t col, float (&out)[N]) {
+  if (sizeof(T) == 4 || f32) {
     const Pack<float, N> v = load_pack<float, N>(static_cast<const float*>(p) + col);
 #pragma unroll
     for (int i = 0; i < N; ++i) out[i] = v.v[i];
   } else {
-    const Pack<T, N> v = load_pack<T, N>(static_cast<const T*>(p) + col);
-#pragma unroll
-    for (int i = 0; i < N; ++i) out[i] = to_float(v.v[i]);
+    to_floats<T, N>(load_pack<T, N>(static_cast<const T*>(p) + col), out);
   }
+}
+// The same, `missing` where there is no vector.
+template <typename T, int N>
+__device__ __forceinline__ void load_param(const void* p, int f32, int64_t col, float missing,
+                                           float (&out)[N]) {
+  if (p != nullptr) return load_param<T, N>(p, f32, col, out);
+#pragma unroll
+  for (int i = 0; i < N; ++i) out[i] = missing;
 }
 
 // Launchers, one instantiation per element type (norm_fwd.cu and norm_bwd.cu

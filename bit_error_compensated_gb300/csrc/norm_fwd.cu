@@ -7,6 +7,14 @@
 // the stores of r and h, so each is read or written once; the statistics are
 // sums over the row's threads, the variance in a second pass over the
 // registers (no cancellation).  It is bound by those bytes.
+//
+// norm_stream_kernel takes rows of 16-byte pieces up to 8192 elements.  A
+// 16-bit element leaves an SM only 3.4 of its four instructions a cycle's
+// worth of time (32 KB a row of 4096 at the memory's rate are 1400 cycles), so
+// what can be done once is: a thread keeps its eight columns' parameters in
+// registers over all its rows, the scale, a shared gate and the post norm's
+// weight multiplied into one factor.  Rows come through a ring of asynchronous
+// copies, several ahead.  norm_kernel takes any other row.
 #include "norm_common.h"
 
 namespace echo {
@@ -26,7 +34,8 @@ struct MaxBits {
 // Sums and maxima over the threads of a row (a whole number of warps of the
 // block).  Each uses one of two sets of slots in turn, so one barrier is
 // enough: a set is written again only after the next sum's barrier, which its
-// readers have passed.  Slots past a row's warps stay 0, neutral to both.
+// readers have passed.  Slots past a row's warps stay 0, neutral to both, so
+// that four are read at a time.
 struct RowReduce {
   uint32_t (*slots)[kMaxWarps];      // [2][kMaxWarps]
   int first, count, warp, lane;      // the row's slots, this thread's place in them
@@ -40,151 +49,395 @@ struct RowReduce {
     which ^= 1;
     if (lane == 0) s[warp] = v;
     __syncthreads();
-    v = s[0];
-    for (int i = 1; i < count; ++i) v = op(v, s[i]);
+    struct __align__(16) Four { V v[4]; };
+    const Four* f = reinterpret_cast<const Four*>(s);
+    v = op(op(f[0].v[0], f[0].v[1]), op(f[0].v[2], f[0].v[3]));
+#pragma unroll
+    for (int i = 1; i < kMaxWarps / 4; ++i)
+      if (4 * i < count) v = op(v, op(op(f[i].v[0], f[i].v[1]), op(f[i].v[2], f[i].v[3])));
     return v;
   }
 };
 
-template <typename T, int VEC, int NV>
-constexpr int norm_max_threads() {
-  return VEC == 1 ? (NV == 4 ? 256 : 1024) : NV == 1 ? 256 : NV == 2 ? 512 : VEC == 4 ? 1024 : 512;
+// v[i] op= parameters i of the vector at `p` (nothing where there is none).
+template <typename T, int VEC>
+__device__ __forceinline__ void scale_by(const void* p, int f32, int64_t col, float (&v)[VEC]) {
+  if (p == nullptr) return;
+  float w[VEC];
+  load_param<T, VEC>(p, f32, col, w);
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) v[i] *= w[i];
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void shift_by(const void* p, int f32, int64_t col, float (&v)[VEC]) {
+  if (p == nullptr) return;
+  float b[VEC];
+  load_param<T, VEC>(p, f32, col, b);
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) v[i] += b[i];
 }
 
 template <typename T, int VEC, int NV, bool LAYER>
-__global__ void __launch_bounds__(norm_max_threads<T, VEC, NV>())
+__global__ void __launch_bounds__(1024)
 norm_kernel(const NormArgs a) {
-  __shared__ uint32_t slots[2][kMaxWarps];
-  constexpr int E = VEC * NV;
+  __shared__ __align__(16) uint32_t slots[2][kMaxWarps];
   const int tid = threadIdx.x, threads = blockDim.x;
+  const int64_t step = (int64_t)gridDim.x * blockDim.y;
+  int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   for (int i = threadIdx.y * threads + tid; i < 2 * kMaxWarps; i += threads * blockDim.y)
     slots[i / kMaxWarps][i % kMaxWarps] = 0;
   __syncthreads();
-  RowReduce red{slots, (int)threadIdx.y * (threads / 32), threads / 32, tid >> 5, tid & 31, 0};
+  RowReduce red{slots, (int)threadIdx.y * 4, threads / 32, tid >> 5, tid & 31, 0};
   const float inv_width = 1.0f / (float)a.width;
+  bool in[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) in[j] = (j * threads + tid) * VEC < a.width;
+  auto col = [&](int j) { return (j * threads + tid) * VEC; };
   pdl_wait();
   pdl_trigger();
 
-  for (int64_t base = (int64_t)blockIdx.x * blockDim.y; base < a.rows;
-       base += (int64_t)gridDim.x * blockDim.y) {
-    const int64_t row = base + threadIdx.y;
+  Pack<T, VEC> next_x[NV], next_y[NV];
+  auto load_row = [&](int64_t at) {
+    if (at >= a.rows) return;
+    const T* x = static_cast<const T*>(a.x) + at * a.ld_x;
+    const T* y = static_cast<const T*>(a.y) + at * a.ld_y;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (in[j]) {
+        if (a.y) next_y[j] = load_pack<T, VEC>(y + col(j));
+        next_x[j] = load_pack<T, VEC>(x + col(j));
+      }
+  };
+  load_row(row);
+  // The gate row of a row, kept up as the rows advance by `step`.
+  int64_t gate_row = 0, gate_pos = 0, gate_step = 0, gate_rest = 0;
+  if (a.gate && a.gate_span < a.rows) {
+    gate_row = row / a.gate_span;
+    gate_pos = row - gate_row * a.gate_span;
+    gate_step = step / a.gate_span;
+    gate_rest = step - gate_step * a.gate_span;
+  }
+  // All rows of a block take the same number of turns, as its sums' barriers need.
+  for (int64_t base = row - threadIdx.y; base < a.rows; base += step, row += step) {
     const bool active = row < a.rows;
-    bool on[NV];
-    Pack<T, VEC> px[NV], py[NV];
+    Pack<T, VEC> px[NV];
+    float v[NV][VEC];      // y, then n, then r, then h; 0 outside the row
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int col = (j * threads + tid) * VEC;
-      on[j] = active && col < a.width;
-      if (on[j]) {
-        if (a.y) py[j] = load_pack<T, VEC>(static_cast<const T*>(a.y) + row * a.ld_y + col);
-        px[j] = load_pack<T, VEC>(static_cast<const T*>(a.x) + row * a.ld_x + col);
+      px[j] = next_x[j];
+      if (a.y && active && in[j]) {
+        to_floats<T, VEC>(next_y[j], v[j]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[j][i] = 0.f;
       }
     }
-    float v[E];            // y, then n, then r, then h; 0 outside the row
+    load_row(row + step);
     float mean1 = 0.f, rstd1 = 1.f, mean2 = 0.f, rstd2 = 1.f;
-
     // Centres v (layer norm) and returns 1 / sqrt(var + eps).
     auto centre = [&](float& mean) {
       float s = 0.f;
       if (LAYER) {
 #pragma unroll
-        for (int i = 0; i < E; ++i) s += v[i];
-        mean = red.all(s, Add()) * inv_width;
+        for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int i = 0; i < E; ++i) v[i] = on[i / VEC] ? v[i] - mean : 0.f;
+          for (int i = 0; i < VEC; ++i) s += v[j][i];
+        mean = red.all(s, Add()) * inv_width;
         s = 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+          if (active && in[j])
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) v[j][i] -= mean;
       }
 #pragma unroll
-      for (int i = 0; i < E; ++i) s += v[i] * v[i];
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) s += v[j][i] * v[j][i];
       return rsqrtf(red.all(s, Add()) * inv_width + a.eps);
     };
 
-#pragma unroll
-    for (int i = 0; i < E; ++i)
-      v[i] = a.y && on[i / VEC] ? to_float(py[i / VEC].v[i % VEC]) : 0.f;
     if (a.post) rstd1 = centre(mean1);
-    const int64_t gate_row = a.gate ? row / a.gate_span : 0;
+    float factor = a.scale * rstd1;
+    if (a.gate && a.gate_scalar && active) {
+      float g[1];
+      load_param<T, 1>(a.gate, a.params_f32, gate_row, g);
+      factor *= g[0];
+    }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int col = (j * threads + tid) * VEC;
-      if (on[j]) {
-        float w[VEC], b[VEC];
+      if (!active || !in[j]) continue;
+      if (a.y) {
         if (a.post) {
-          load_param<T, VEC>(a.w_post, a.params_f32, col, 1.f, w);
-          load_param<T, VEC>(a.b_post, a.params_f32, col, 0.f, b);
+          scale_by<T, VEC>(a.w_post, a.params_f32, col(j), v[j]);
+          if (LAYER && a.b_post) {             // n / rstd, so that one factor is left
+            const float std1 = 1.f / rstd1;
+            float b[VEC];
+            load_param<T, VEC>(a.b_post, a.params_f32, col(j), b);
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) v[j * VEC + i] = v[j * VEC + i] * rstd1 * w[i] + b[i];
-        }
-        if (a.gate && !a.gate_scalar) {
-          load_param<T, VEC>(a.gate, a.params_f32, gate_row * a.width + col, 1.f, w);
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) v[j * VEC + i] *= w[i];
-        } else if (a.gate) {
-          float g[1];
-          load_param<T, 1>(a.gate, a.params_f32, gate_row, 1.f, g);
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) v[j * VEC + i] *= g[0];
-        }
-        Pack<T, VEC> out;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          float& r = v[j * VEC + i];
-          r = a.y ? to_float(px[j].v[i]) + a.scale * r : to_float(px[j].v[i]);
-          out.v[i] = from_float<T>(r);
-        }
-        if (a.r) store_pack<T, VEC>(static_cast<T*>(a.r) + row * a.ld_r + col, out);
-      }
-    }
-    if (a.h || a.codes || a.stats) rstd2 = centre(mean2);
-    uint32_t amax = __float_as_uint(kTinyAmax);
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int col = (j * threads + tid) * VEC;
-      if (on[j] && (a.h || a.codes)) {
-        float w[VEC], b[VEC], h[VEC];
-        load_param<T, VEC>(a.w_pre, a.params_f32, col, 1.f, w);
-        load_param<T, VEC>(a.b_pre, a.params_f32, col, 0.f, b);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          h[i] = v[j * VEC + i] * rstd2 * w[i] + b[i];
-          v[j * VEC + i] = h[i];
-          amax = max(amax, abs_bits(h[i]));
-        }
-        if (a.h) store_floats<T, VEC>(static_cast<T*>(a.h) + row * a.ld_h + col, h);
-      }
-    }
-    if (a.codes) {
-      const float top = __uint_as_float(red.all(amax, MaxBits()));
-      const float inv = __fdiv_rn(127.f, top);
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int col = (j * threads + tid) * VEC;
-        if (on[j]) {
-          Pack<int8_t, VEC> q;
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) q.v[i] = (int8_t)quantize_code(v[j * VEC + i], inv);
-          int8_t* to = a.codes + row * a.ld_codes + col;
-          if constexpr (VEC == 8) {
-            *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(&q);
-          } else if constexpr (VEC == 4) {
-            *reinterpret_cast<uint32_t*>(to) = *reinterpret_cast<const uint32_t*>(&q);
-          } else {
-            *to = q.v[0];
+            for (int i = 0; i < VEC; ++i) v[j][i] += b[i] * std1;
           }
         }
+        if (a.gate && !a.gate_scalar)
+          scale_by<T, VEC>(a.gate, a.params_f32, gate_row * a.width + col(j), v[j]);
       }
-      if (tid == 0 && active) a.scales[row] = __fdiv_rn(top, 127.f);
+      float x[VEC];
+      to_floats<T, VEC>(px[j], x);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) v[j][i] = a.y ? fmaf(factor, v[j][i], x[i]) : x[i];
+      if (a.r) store_floats<T, VEC>(static_cast<T*>(a.r) + row * a.ld_r + col(j), v[j]);
+    }
+    if (a.h || a.codes || a.stats) rstd2 = centre(mean2);
+    if (a.h || a.codes) {
+      uint32_t amax = __float_as_uint(kTinyAmax);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        if (!active || !in[j]) continue;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[j][i] *= rstd2;
+        scale_by<T, VEC>(a.w_pre, a.params_f32, col(j), v[j]);
+        if (LAYER) shift_by<T, VEC>(a.b_pre, a.params_f32, col(j), v[j]);
+        if (a.h) store_floats<T, VEC>(static_cast<T*>(a.h) + row * a.ld_h + col(j), v[j]);
+        if (a.codes)
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) amax = max(amax, abs_bits(v[j][i]));
+      }
+      if (a.codes) {
+        const float top = __uint_as_float(red.all(amax, MaxBits()));
+        const float inv = __fdiv_rn(127.f, top);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          if (!active || !in[j]) continue;
+          Pack<int8_t, VEC> q;
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) q.v[i] = (int8_t)quantize_code(v[j][i], inv);
+          int8_t* to = a.codes + row * a.ld_codes + col(j);
+          if constexpr (VEC == 8) *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(&q);
+          else if constexpr (VEC == 4) *reinterpret_cast<uint32_t*>(to) = *reinterpret_cast<const uint32_t*>(&q);
+          else *to = q.v[0];
+        }
+        if (tid == 0 && active) a.scales[row] = __fdiv_rn(top, 127.f);
+      }
+    }
+    gate_row += gate_step;
+    gate_pos += gate_rest;
+    if (gate_pos >= a.gate_span) {
+      gate_pos -= a.gate_span;
+      ++gate_row;
     }
     if (a.stats && tid == 0 && active)
       *reinterpret_cast<float4*>(a.stats + 4 * row) = make_float4(mean1, rstd1, mean2, rstd2);
   }
 }
 
+// Rows ahead in the ring of asynchronous copies: 64 (fp32: 96) bytes a thread.
+template <typename T> constexpr int rows_ahead() { return sizeof(T) == 2 ? 4 : 3; }
+
+// GATE: 0 none, or one row for all (multiplied into `mul` and `add`); 1 a row
+// of gates, 2 a gate, for each row or several.
+template <typename T, int NV, bool LAYER, bool POST, int GATE>
+__global__ void __launch_bounds__(1024)
+norm_stream_kernel(const NormArgs a) {
+  constexpr int VEC = 16 / sizeof(T), kAhead = rows_ahead<T>();
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ __align__(16) uint32_t slots[2][kMaxWarps];
+  const int tid = threadIdx.x, threads = blockDim.x;
+  const int64_t step = (int64_t)gridDim.x * blockDim.y;
+  int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  for (int i = threadIdx.y * threads + tid; i < 2 * kMaxWarps; i += threads * blockDim.y)
+    slots[i / kMaxWarps][i % kMaxWarps] = 0;
+  __syncthreads();
+  RowReduce red{slots, (int)threadIdx.y * 4, threads / 32, tid >> 5, tid & 31, 0};
+  const float inv_width = 1.0f / (float)a.width;
+  bool in[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) in[j] = (j * threads + tid) * VEC < a.width;
+  // This thread's pieces of the ring: x and y of piece j of slot s.
+  const uint32_t piece = 16u * threads * blockDim.y, slot_bytes = 2 * NV * piece;
+  const uint32_t mine = (uint32_t)__cvta_generic_to_shared(ring) + 16u * (threadIdx.y * threads + tid);
+  pdl_wait();
+  pdl_trigger();
+
+  const char* from_x = static_cast<const char*>(a.x) + row * a.ld_x * sizeof(T) + 16 * tid;
+  const char* from_y = static_cast<const char*>(a.y) + row * a.ld_y * sizeof(T) + 16 * tid;
+  const int64_t far_x = step * a.ld_x * sizeof(T), far_y = step * a.ld_y * sizeof(T);
+  int64_t fetch = row;
+  auto copy_row = [&](uint32_t slot) {
+    if (fetch < a.rows) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (in[j]) {
+          copy16_async(mine + slot * slot_bytes + 2 * j * piece, from_x + 16 * j * threads);
+          if (a.y) copy16_async(mine + slot * slot_bytes + (2 * j + 1) * piece, from_y + 16 * j * threads);
+        }
+    }
+    copies_commit();
+    fetch += step;
+    from_x += far_x;
+    from_y += far_y;
+  };
+#pragma unroll
+  for (int s = 0; s < kAhead; ++s) copy_row(s);
+
+  // The columns' parameters: n = hat1 * mul + add (times the row's gate), h = hat2 * w + b.
+  float mul[NV][VEC], add[LAYER ? NV : 1][VEC], w[NV][VEC], b[LAYER ? NV : 1][VEC];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int col = (j * threads + tid) * VEC;
+    float g[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      g[i] = a.scale;
+      mul[j][i] = w[j][i] = 1.f;
+      if (LAYER) add[j][i] = b[j][i] = 0.f;
+    }
+    if (!in[j]) continue;
+    if (GATE == 0) scale_by<T, VEC>(a.gate, a.params_f32, col, g);
+    load_param<T, VEC>(a.w_pre, a.params_f32, col, 1.f, w[j]);
+    if (POST) load_param<T, VEC>(a.w_post, a.params_f32, col, 1.f, mul[j]);
+    if (LAYER) {
+      load_param<T, VEC>(a.b_pre, a.params_f32, col, 0.f, b[j]);
+      if (POST) load_param<T, VEC>(a.b_post, a.params_f32, col, 0.f, add[j]);
+    }
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      mul[j][i] *= g[i];
+      if (LAYER) add[j][i] *= g[i];
+    }
+  }
+  // The gate row of a row, kept up as the rows advance by `step`.
+  int64_t gate_row = 0, gate_pos = 0, gate_step = 0, gate_rest = 0;
+  if (GATE != 0) {
+    gate_row = row / a.gate_span;
+    gate_pos = row - gate_row * a.gate_span;
+    gate_step = step / a.gate_span;
+    gate_rest = step - gate_step * a.gate_span;
+  }
+  char* to_r = static_cast<char*>(a.r) + row * a.ld_r * sizeof(T) + 16 * tid;
+  char* to_h = static_cast<char*>(a.h) + row * a.ld_h * sizeof(T) + 16 * tid;
+  const int64_t far_r = step * a.ld_r * sizeof(T), far_h = step * a.ld_h * sizeof(T);
+  uint32_t slot = 0;
+
+  // All rows of a block take the same number of turns, as its sums' barriers need.
+  for (int64_t base = row - threadIdx.y; base < a.rows; base += step, row += step) {
+    const bool active = row < a.rows;
+    copies_wait<kAhead - 1>();
+    float v[NV][VEC];      // y, then r, then h; 0 outside the row
+    float mean1 = 0.f, rstd1 = 1.f, mean2 = 0.f, rstd2 = 1.f;
+    auto centre = [&](float& mean) {
+      float s = 0.f;
+      if (LAYER) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) s += v[j][i];
+        mean = red.all(s, Add()) * inv_width;
+        s = 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+          if (active && in[j])
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) v[j][i] -= mean;
+      }
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) s = fmaf(v[j][i], v[j][i], s);
+      return rsqrtf(red.all(s, Add()) * inv_width + a.eps);
+    };
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (a.y && active && in[j]) {
+        to_floats<T, VEC>(load_shared16<T, VEC>(mine + slot * slot_bytes + (2 * j + 1) * piece), v[j]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[j][i] = 0.f;
+      }
+    }
+    if (POST) rstd1 = centre(mean1);
+    float factor = rstd1, gate = 1.f;
+    if (GATE == 2 && active) {
+      float one[1];
+      load_param<T, 1>(a.gate, a.params_f32, gate_row, one);
+      gate = one[0];
+      factor *= gate;
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (!active || !in[j]) continue;
+      float x[VEC];
+      to_floats<T, VEC>(load_shared16<T, VEC>(mine + slot * slot_bytes + 2 * j * piece), x);
+      if (a.y) {
+        float g[VEC];
+        if (GATE == 1) load_param<T, VEC>(a.gate, a.params_f32, gate_row * a.width + (j * threads + tid) * VEC, g);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          float n = POST ? v[j][i] * factor : GATE == 2 ? v[j][i] * gate : v[j][i];
+          if (LAYER && GATE == 2) n = fmaf(n, mul[j][i], add[j][i] * gate);
+          else if (LAYER) n = fmaf(n, mul[j][i], add[j][i]);
+          if (GATE == 1) v[j][i] = LAYER ? fmaf(n, g[i], x[i]) : fmaf(n * mul[j][i], g[i], x[i]);
+          else v[j][i] = LAYER ? n + x[i] : fmaf(n, mul[j][i], x[i]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[j][i] = x[i];
+      }
+      if (a.r) store_floats<T, VEC>(reinterpret_cast<T*>(to_r + 16 * j * threads), v[j]);
+    }
+    copy_row(slot);                     // this thread has read its pieces of the slot
+    slot = slot == kAhead - 1 ? 0 : slot + 1;
+    if (a.h || a.codes || a.stats) rstd2 = centre(mean2);
+    if (a.h || a.codes) {
+      uint32_t amax = __float_as_uint(kTinyAmax);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        if (!active || !in[j]) continue;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+          v[j][i] = LAYER ? fmaf(v[j][i] * rstd2, w[j][i], b[j][i]) : v[j][i] * rstd2 * w[j][i];
+        if (a.h) store_floats<T, VEC>(reinterpret_cast<T*>(to_h + 16 * j * threads), v[j]);
+        if (a.codes)
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) amax = max(amax, abs_bits(v[j][i]));
+      }
+      if (a.codes) {
+        const float top = __uint_as_float(red.all(amax, MaxBits()));
+        const float inv = __fdiv_rn(127.f, top);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          if (!active || !in[j]) continue;
+          Pack<int8_t, VEC> q;
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) q.v[i] = (int8_t)quantize_code(v[j][i], inv);
+          int8_t* to = a.codes + row * a.ld_codes + (j * threads + tid) * VEC;
+          if constexpr (VEC == 8) *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(&q);
+          else *reinterpret_cast<uint32_t*>(to) = *reinterpret_cast<const uint32_t*>(&q);
+        }
+        if (tid == 0 && active) a.scales[row] = __fdiv_rn(top, 127.f);
+      }
+    }
+    if (a.stats && tid == 0 && active)
+      *reinterpret_cast<float4*>(a.stats + 4 * row) = make_float4(mean1, rstd1, mean2, rstd2);
+    to_r += far_r;
+    to_h += far_h;
+    if (GATE != 0) {
+      gate_row += gate_step;
+      gate_pos += gate_rest;
+      if (gate_pos >= a.gate_span) {
+        gate_pos -= a.gate_span;
+        ++gate_row;
+      }
+    }
+  }
+  copies_wait<0>();
+}
+
 template <typename T, int VEC, int NV>
 cudaError_t launch(const NormArgs& a, int layer, int sms, cudaStream_t s) {
   const int threads = ((a.width + VEC * NV - 1) / (VEC * NV) + 31) / 32 * 32;
   const int rows = threads < 128 ? 128 / threads : 1;
-  const int64_t blocks = (a.rows + rows - 1) / rows, most = (int64_t)sms * 64;
+  // As many blocks as 64 registers a thread let run at once.
+  const int64_t blocks = (a.rows + rows - 1) / rows, most = (int64_t)sms * (1024 / (threads * rows));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(blocks < most ? blocks : most));
   cfg.blockDim = dim3(threads, rows);
@@ -196,16 +449,53 @@ cudaError_t launch(const NormArgs& a, int layer, int sms, cudaStream_t s) {
                : cudaLaunchKernelEx(&cfg, norm_kernel<T, VEC, NV, false>, a);
 }
 
+template <typename T, bool LAYER, bool POST, int GATE>
+cudaError_t launch_stream(const NormArgs& a, int sms, cudaStream_t s) {
+  constexpr int VEC = 16 / sizeof(T), NV = 8 / VEC, kAhead = rows_ahead<T>();
+  const int threads = ((a.width + 7) / 8 + 31) / 32 * 32;
+  const int rows = threads < 128 ? 128 / threads : 1;
+  const int smem = kAhead * 2 * NV * 16 * threads * rows;
+  static OncePerDevice prepared;
+  cudaError_t e = prepared.run([] {
+    return cudaFuncSetAttribute(norm_stream_kernel<T, NV, LAYER, POST, GATE>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, kAhead * 2 * NV * 16 * 1024);
+  });
+  if (e != cudaSuccess) return e;
+  const int64_t blocks = (a.rows + rows - 1) / rows;
+  int at_once = 1024 / (threads * rows);               // by registers; and by shared memory
+  if (at_once > 200 * 1024 / smem) at_once = 200 * 1024 / smem;
+  if (at_once < 1) at_once = 1;
+  const int64_t most = (int64_t)sms * at_once;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(blocks < most ? blocks : most));
+  cfg.blockDim = dim3(threads, rows);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute overlapped = overlapped_launch();
+  cfg.attrs = &overlapped;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, norm_stream_kernel<T, NV, LAYER, POST, GATE>, a);
+}
+
+template <typename T, bool LAYER, bool POST>
+cudaError_t pick_stream(const NormArgs& a, int sms, cudaStream_t s) {
+  if (!a.gate || (!a.gate_scalar && a.gate_span >= a.rows)) return launch_stream<T, LAYER, POST, 0>(a, sms, s);
+  return a.gate_scalar ? launch_stream<T, LAYER, POST, 2>(a, sms, s) : launch_stream<T, LAYER, POST, 1>(a, sms, s);
+}
+
 }  // namespace
 
 template <>
 cudaError_t launch_norm<ECHO_ELEM>(const NormArgs& a, int layer, bool vec, int sms, cudaStream_t s) {
   using T = ECHO_ELEM;
   constexpr int V = 16 / sizeof(T);
-  if (!vec) return a.width <= 1024 ? launch<T, 1, 4>(a, layer, sms, s) : launch<T, 1, 16>(a, layer, sms, s);
-  if (a.width <= 256 * V) return launch<T, V, 1>(a, layer, sms, s);
-  if (a.width <= 1024 * V) return launch<T, V, 2>(a, layer, sms, s);
-  return launch<T, V, 4>(a, layer, sms, s);
+  if (!vec) {
+    if (a.width <= 4096) return launch<T, 1, 4>(a, layer, sms, s);
+    return a.width <= 8192 ? launch<T, 1, 8>(a, layer, sms, s) : launch<T, 1, 16>(a, layer, sms, s);
+  }
+  if (a.width > 8192) return launch<T, V, 16 / V>(a, layer, sms, s);
+  if (layer) return a.post ? pick_stream<T, true, true>(a, sms, s) : pick_stream<T, true, false>(a, sms, s);
+  return a.post ? pick_stream<T, false, true>(a, sms, s) : pick_stream<T, false, false>(a, sms, s);
 }
 
 }  // namespace echo

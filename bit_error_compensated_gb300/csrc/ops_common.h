@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "../../include/echo.h"
 
@@ -70,12 +71,71 @@ __device__ __forceinline__ void store_pack(T* p, const Pack<T, N>& in) {
   }
 }
 
+// The elements of a pack as floats, and back, two at a time.
+template <typename T, int N>
+__device__ __forceinline__ void to_floats(const Pack<T, N>& in, float (&v)[N]) {
+  if constexpr (sizeof(T) == 2 && N % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const uint32_t two = reinterpret_cast<const uint32_t*>(&in)[i / 2];
+      if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        v[i] = __uint_as_float(two << 16);
+        v[i + 1] = __uint_as_float(two & 0xFFFF0000u);
+      } else {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&two));
+        v[i] = f.x;
+        v[i + 1] = f.y;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = to_float(in.v[i]);
+  }
+}
+
+template <typename T, int N>
+__device__ __forceinline__ Pack<T, N> from_floats(const float (&v)[N]) {
+  Pack<T, N> out;
+  if constexpr (sizeof(T) == 2 && N % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        const __nv_bfloat162 two = __floats2bfloat162_rn(v[i], v[i + 1]);
+        reinterpret_cast<uint32_t*>(&out)[i / 2] = *reinterpret_cast<const uint32_t*>(&two);
+      } else {
+        const __half2 two = __floats2half2_rn(v[i], v[i + 1]);
+        reinterpret_cast<uint32_t*>(&out)[i / 2] = *reinterpret_cast<const uint32_t*>(&two);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) out.v[i] = from_float<T>(v[i]);
+  }
+  return out;
+}
+
 template <typename T, int N>
 __device__ __forceinline__ void store_floats(T* p, const float (&v)[N]) {
-  Pack<T, N> out;
-#pragma unroll
-  for (int i = 0; i < N; ++i) out.v[i] = from_float<T>(v[i]);
-  store_pack<T, N>(p, out);
+  store_pack<T, N>(p, from_floats<T, N>(v));
+}
+
+// Copies of 16 bytes into shared memory that a thread reads back itself (no
+// barrier between): in flight while it works, without registers.
+__device__ __forceinline__ void copy16_async(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" :: "n"(PENDING) : "memory");
+}
+template <typename T, int N>
+__device__ __forceinline__ Pack<T, N> load_shared16(uint32_t at) {
+  static_assert(sizeof(T) * N == 16, "one 16-byte piece");
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return *reinterpret_cast<const Pack<T, N>*>(&v);
 }
 
 // See overlapped_launch below.
