@@ -268,7 +268,8 @@ int echo_norm_backward(echo_norm_plan_t plan, const echo_norm_params* params,
   const int64_t stride = plan->workers * W;
   for (int k = 0; k < 4; ++k) {
     a.dparam[k] = dparam[k];
-    a.partial[k] = dparam[k] ? plan->workspace + k * stride : nullptr;
+    // the first two are dgate's too
+    a.partial[k] = dparam[k] || (k < 2 && io->dgate) ? plan->workspace + k * stride : nullptr;
   }
   a.gate_partial = plan->workspace + 4 * stride;
   a.scale = plan->scale;

@@ -8,12 +8,20 @@
 //     dw_pre = sum dh b, db_pre = sum dh, dw_post = sum dn a, db_post = sum dn
 //
 // ([.] for layer norms only).  A worker (a row's worth of threads) takes a
-// contiguous range of rows, keeps each row in registers from its four loads
-// to its two stores, and keeps the column sums of the parameters' gradients
-// in registers over all its rows; a second, small kernel adds the workers'
-// sums in a fixed order.  Rows wider than one block's registers are split by
-// columns over a cluster, whose blocks exchange the row sums through
+// contiguous range of rows and keeps the column sums of the parameters'
+// gradients in registers over all of them; a second, small kernel adds the
+// workers' sums in a fixed order.  Rows wider than one block's threads are
+// split by columns over a cluster, whose blocks exchange the row sums through
 // distributed shared memory.
+//
+// norm_grad_stream_kernel takes rows of 16-byte pieces.  Its time is that of
+// its bytes (12 a 16-bit element) as long as it stays under 5 instructions an
+// element, warp and cycle's share, so: rows come through a ring of
+// asynchronous copies; scale, gate and weight are multiplied once (one gate row
+// for all) or once a row; and with one gate row for all, or while a gate row
+// lasts, only A = sum D a (and sum D) are kept, of which dw_post is
+// scale gate A and dgate is scale (w_post A + b_post sum D).
+// norm_grad_kernel takes any other row.
 #include "norm_common.h"
 
 namespace echo {
@@ -304,8 +312,432 @@ norm_grad_kernel(const NormGradArgs a, int blocks, int block_cols) {
                  "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// Sums of N values over a row's threads, as RowSums above, four slots read at
+// a time (slots past a row's warps stay 0).
+constexpr int kStreamThreads = 512, kStreamSlots = kStreamThreads / 32 * kMaxCluster;
+
+struct StreamSums {
+  float (*slots)[3][kStreamSlots];     // [2]
+  int first, count, warp, lane, blocks;
+  int which;
+  template <int N>
+  __device__ __forceinline__ void all(float (&v)[N]) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+#pragma unroll
+      for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], d);
+    if (count == 1) return;
+    float(*s)[kStreamSlots] = slots[which];
+    which ^= 1;
+    if (blocks > 1) {
+      if (lane < blocks) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          uint32_t at;
+          asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                       : "=r"(at) : "r"(smem_u32(&s[k][first + warp])), "r"(lane));
+          asm volatile("st.shared::cluster.f32 [%0], %1;" :: "r"(at), "f"(v[k]) : "memory");
+        }
+      }
+      asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
+                   "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    } else {
+      if (lane == 0)
+#pragma unroll
+        for (int k = 0; k < N; ++k) s[k][first + warp] = v[k];
+      __syncthreads();
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const float4* f = reinterpret_cast<const float4*>(&s[k][first]);
+      v[k] = (f[0].x + f[0].y) + (f[0].z + f[0].w);
+    }
+    for (int i = 1; 4 * i < count; ++i)
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const float4 f = reinterpret_cast<const float4*>(&s[k][first])[i];
+        v[k] += (f.x + f.y) + (f.z + f.w);
+      }
+  }
+};
+
+// Rows ahead in the ring of asynchronous copies: 128 KB at 4096 columns.
+template <typename T> constexpr int rows_ahead() { return sizeof(T) == 2 ? 4 : 2; }
+// 16-byte pieces of shared memory a thread has: the ring's (x, y, dr, dh) and
+// its columns' fp32 parameters (mul, w, and for layer norms add).
+template <typename T, bool LAYER>
+constexpr int grad_pieces() { return rows_ahead<T>() * 4 * (8 * (int)sizeof(T) / 16) + (LAYER ? 6 : 4); }
+// Warps an SM: at 128 registers a thread.  (64 and twice the warps spill, and
+// take 143 us where this takes GRAD_US, 8192 x 4096 bf16.)
+constexpr int kStreamWarps = 16;
+
+// GATE: 0 none, or one row for all; 1 a row of gates, 2 a gate, for each row
+// or several.
+template <typename T, bool LAYER, bool POST, int GATE>
+__global__ void __launch_bounds__(kStreamThreads, 1)
+norm_grad_stream_kernel(const NormGradArgs a, int blocks, int block_cols) {
+  constexpr int VEC = 16 / sizeof(T), NV = 8 / VEC, kAhead = rows_ahead<T>();
+  constexpr bool SUM0 = LAYER && POST;                  // sum D is needed (db_post, dgate)
+  extern __shared__ __align__(16) uint8_t room[];
+  __shared__ __align__(16) float slots[2][3][kStreamSlots];
+  const int tid = threadIdx.x, threads = blockDim.x, all_threads = threads * blockDim.y;
+  const int me = threadIdx.y * threads + tid;
+  const int part = (int)blockIdx.x % blocks;            // of the row's columns
+  const int64_t worker = (int64_t)(blockIdx.x / blocks) * blockDim.y + threadIdx.y;
+  const int col0 = part * block_cols, warps = threads / 32;
+  StreamSums sums{slots, blockDim.y > 1 ? (int)threadIdx.y * 4 : 0, warps * blocks, part * warps + (tid >> 5),
+                  tid & 31, blocks, 0};
+  for (int i = me; i < 6 * kStreamSlots; i += all_threads) (&slots[0][0][0])[i] = 0.f;
+  __syncthreads();
+  if (blocks > 1)                      // every block's slots are ready before the first is written
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
+                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  const float inv_width = 1.0f / (float)a.width;
+  bool in[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) in[j] = (j * threads + tid) * VEC < block_cols && col0 + (j * threads + tid) * VEC < a.width;
+  const int my_col = col0 + tid * VEC;                  // of piece j: + j * threads * VEC
+  pdl_wait();
+  pdl_trigger();
+
+  const int64_t row0 = worker * a.span;
+  const int64_t row1 = row0 + a.span < a.rows ? row0 + a.span : a.rows;
+  const uint32_t piece = 16u * all_threads;
+  const uint32_t mine = smem_u32(room) + 16u * me, slot_bytes = 4 * NV * piece;
+  const uint32_t params = mine + kAhead * slot_bytes;
+  auto start = [&](const void* p, int64_t ld) {
+    return static_cast<const char*>(p) + (row0 * ld + my_col) * (int64_t)sizeof(T);
+  };
+  const char* from[4] = {start(a.x, a.ld_x), start(a.y, a.ld_y), start(a.dr, a.ld_dr), start(a.dh, a.ld_dh)};
+  int64_t fetch = row0;
+  auto copy_row = [&](uint32_t slot) {
+    if (fetch < row1) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (in[j]) {
+          const uint32_t to = mine + slot * slot_bytes + 4 * j * piece;
+          copy16_async(to, from[0] + 16 * j * threads);
+          if (a.y) copy16_async(to + piece, from[1] + 16 * j * threads);
+          if (a.dr) copy16_async(to + 2 * piece, from[2] + 16 * j * threads);
+          if (a.dh) copy16_async(to + 3 * piece, from[3] + 16 * j * threads);
+        }
+    }
+    copies_commit();
+    ++fetch;
+    from[0] += a.ld_x * sizeof(T);
+    from[1] += a.ld_y * sizeof(T);
+    from[2] += a.ld_dr * sizeof(T);
+    from[3] += a.ld_dh * sizeof(T);
+  };
+#pragma unroll
+  for (int s = 0; s < kAhead; ++s) copy_row(s);
+
+  // The columns' parameters, as fp32 in this thread's shared memory: mul and
+  // add of n * scale (times the gate, if it is one row) = hat1 * mul + add,
+  // and w of the norm of r.
+  auto put = [&](int at, int j, const float (&v)[VEC]) {
+#pragma unroll
+    for (int i = 0; i < VEC; i += 4)
+      asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};"
+                   :: "r"(params + (uint32_t)(at * 2 + j * (VEC / 4) + i / 4) * piece), "f"(v[i]), "f"(v[i + 1]),
+                      "f"(v[i + 2]), "f"(v[i + 3]) : "memory");
+  };
+  auto get = [&](int at, int j, float (&v)[VEC]) {
+#pragma unroll
+    for (int i = 0; i < VEC; i += 4)
+      asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(v[i]), "=f"(v[i + 1]), "=f"(v[i + 2]), "=f"(v[i + 3])
+                   : "r"(params + (uint32_t)(at * 2 + j * (VEC / 4) + i / 4) * piece) : "memory");
+  };
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int col = my_col + j * threads * VEC;
+    float g[VEC], m[VEC], w[VEC], b[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      g[i] = a.scale;
+      m[i] = w[i] = 1.f;
+      b[i] = 0.f;
+    }
+    if (in[j]) {
+      if (GATE == 0 && a.gate) {
+        load_param<T, VEC>(a.gate, a.params_f32, col, g);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) g[i] *= a.scale;
+      }
+      load_param<T, VEC>(a.w_pre, a.params_f32, col, 1.f, w);
+      if (POST) load_param<T, VEC>(a.w_post, a.params_f32, col, 1.f, m);
+      if (SUM0) load_param<T, VEC>(a.b_post, a.params_f32, col, 0.f, b);
+    }
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      m[i] *= g[i];
+      b[i] *= g[i];
+    }
+    put(0, j, m);
+    put(1, j, w);
+    if (LAYER) put(2, j, b);
+  }
+
+  float sum_a[NV][VEC], sum_d[SUM0 ? NV : 1][VEC];      // of D a, D: all rows, or the gate row's
+  float sum_wpost[GATE == 1 ? NV : 1][VEC], sum_bpost[GATE == 1 && SUM0 ? NV : 1][VEC];
+  float sum_wpre[NV][VEC], sum_bpre[LAYER ? NV : 1][VEC];
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      sum_a[j][i] = sum_wpre[j][i] = 0.f;
+      if (SUM0) sum_d[j][i] = 0.f;
+      if (GATE == 1) sum_wpost[j][i] = 0.f;
+      if (GATE == 1 && SUM0) sum_bpost[j][i] = 0.f;
+      if (LAYER) sum_bpre[j][i] = 0.f;
+    }
+  float sum_scalar = 0.f;
+  int64_t gate_row = 0, gate_left = 0;
+  bool gate_whole = false;             // the gate row's first row is this worker's
+  if (GATE != 0) {
+    gate_row = row0 / a.gate_span;
+    gate_left = a.gate_span - (row0 - gate_row * a.gate_span);
+    gate_whole = gate_left == a.gate_span;
+  }
+  char* to_dx = static_cast<char*>(a.dx) + (row0 * a.ld_dx + my_col) * (int64_t)sizeof(T);
+  char* to_dy = static_cast<char*>(a.dy) + (row0 * a.ld_dy + my_col) * (int64_t)sizeof(T);
+  const float4 no_stats = make_float4(0.f, 1.f, 0.f, 1.f);
+  const float4* stats = reinterpret_cast<const float4*>(a.stats) + row0;
+  float4 next_stats = a.stats && row0 < row1 ? __ldg(stats) : no_stats;
+  uint32_t slot = 0;
+
+  for (int64_t step = 0; step < a.span; ++step) {
+    const int64_t row = row0 + step;
+    const bool active = row < row1;
+    const float4 st = next_stats;
+    ++stats;
+    if (a.stats && row + 1 < row1) next_stats = __ldg(stats);
+    float gate = 1.f;
+    if (GATE == 2 && active) {
+      float one[1];
+      load_param<T, 1>(a.gate, a.params_f32, gate_row, one);
+      gate = one[0];
+    }
+    copies_wait<kAhead - 1>();
+    const uint32_t here = mine + slot * slot_bytes;
+    float hat1[NV][VEC], hat2[NV][VEC], g[NV][VEC];     // g: dh w, then f
+    float s[LAYER ? 2 : 1] = {};
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (!active || !in[j]) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) hat1[j][i] = hat2[j][i] = g[j][i] = 0.f;
+        continue;
+      }
+      float x[VEC], m[VEC];
+      to_floats<T, VEC>(load_shared16<T, VEC>(here + 4 * j * piece), x);
+      if (a.y) {
+        to_floats<T, VEC>(load_shared16<T, VEC>(here + (4 * j + 1) * piece), hat1[j]);
+        if (POST)
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) hat1[j][i] = LAYER ? (hat1[j][i] - st.x) * st.y : hat1[j][i] * st.y;
+        get(0, j, m);
+        if (GATE == 1) {
+          float q[VEC];
+          load_param<T, VEC>(a.gate, a.params_f32, gate_row * a.width + my_col + j * threads * VEC, q);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) m[i] *= q[i];
+          if (SUM0) {
+            float b[VEC];
+            get(2, j, b);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) x[i] = fmaf(b[i], q[i], x[i]);
+          }
+        } else if (SUM0) {
+          float b[VEC];
+          get(2, j, b);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) x[i] = GATE == 2 ? fmaf(b[i], gate, x[i]) : x[i] + b[i];
+        }
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) x[i] = fmaf(hat1[j][i], GATE == 2 ? m[i] * gate : m[i], x[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) hat1[j][i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) hat2[j][i] = LAYER ? (x[i] - st.z) * st.w : x[i] * st.w;
+      if (a.dh) {
+        float w[VEC];
+        to_floats<T, VEC>(load_shared16<T, VEC>(here + (4 * j + 3) * piece), g[j]);
+        get(1, j, w);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          sum_wpre[j][i] = fmaf(g[j][i], hat2[j][i], sum_wpre[j][i]);
+          if (LAYER) sum_bpre[j][i] += g[j][i];
+          g[j][i] *= w[i];
+          s[0] = fmaf(g[j][i], hat2[j][i], s[0]);
+          if (LAYER) s[1] += g[j][i];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) g[j][i] = 0.f;
+      }
+    }
+    if (a.dh) {
+      sums.all(s);
+#pragma unroll
+      for (float& v : s) v *= inv_width;
+    }
+    float t[(LAYER ? 2 : 1) + (GATE == 2 ? 1 : 0)] = {};
+    constexpr int kScalar = LAYER ? 2 : 1;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (!active || !in[j]) continue;
+      float d[VEC];
+      if (a.dr) {
+        to_floats<T, VEC>(load_shared16<T, VEC>(here + (4 * j + 2) * piece), d);
+      } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) d[i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        const float back = fmaf(-s[0], hat2[j][i], LAYER ? g[j][i] - s[LAYER ? 1 : 0] : g[j][i]);
+        d[i] = fmaf(st.w, back, d[i]);
+      }
+      if (a.dx) store_floats<T, VEC>(reinterpret_cast<T*>(to_dx + 16 * j * threads), d);
+      if (!a.y) continue;
+      float m[VEC];
+      get(0, j, m);
+      if (GATE == 1) {
+        float q[VEC];
+        load_param<T, VEC>(a.gate, a.params_f32, gate_row * a.width + my_col + j * threads * VEC, q);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) m[i] *= q[i];
+      }
+      if (GATE == 2) {
+        const float k = a.scale * gate;
+        float b[VEC];
+        if (SUM0) get(2, j, b);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          const float n = SUM0 ? fmaf(hat1[j][i], m[i], b[i]) : hat1[j][i] * m[i];
+          t[kScalar < (int)(sizeof(t) / sizeof(float)) ? kScalar : 0] += d[i] * n;
+          m[i] *= gate;
+          sum_a[j][i] = fmaf(d[i] * k, hat1[j][i], sum_a[j][i]);
+          if (SUM0) sum_d[j][i] = fmaf(d[i], k, sum_d[j][i]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          sum_a[j][i] = fmaf(d[i], hat1[j][i], sum_a[j][i]);
+          if (SUM0) sum_d[j][i] += d[i];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        g[j][i] = d[i] * m[i];
+        if (POST) {
+          t[0] = fmaf(g[j][i], hat1[j][i], t[0]);
+          if (LAYER) t[LAYER ? 1 : 0] += g[j][i];
+        }
+      }
+    }
+    copy_row(slot);                     // this thread has read its pieces of the slot
+    slot = slot == kAhead - 1 ? 0 : slot + 1;
+    if (POST || GATE == 2) {
+      sums.all(t);
+      t[0] *= inv_width;
+      if (LAYER) t[LAYER ? 1 : 0] *= inv_width;
+    }
+    if (a.dy) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        if (!active || !in[j]) continue;
+        if (POST)
+#pragma unroll
+          for (int i = 0; i < VEC; ++i)
+            g[j][i] = st.y * fmaf(-t[0], hat1[j][i], LAYER ? g[j][i] - t[LAYER ? 1 : 0] : g[j][i]);
+        store_floats<T, VEC>(reinterpret_cast<T*>(to_dy + 16 * j * threads), g[j]);
+      }
+    }
+    to_dx += a.ld_dx * sizeof(T);
+    to_dy += a.ld_dy * sizeof(T);
+    // A gate row ends, or this worker's part of it: a gate row whose rows are
+    // all this worker's is written; of the others, the part of one that began
+    // before its range goes to the worker's first slot, of one that goes on
+    // behind it to the second, for norm_grad_finish.
+    if (GATE != 0 && active) {
+      if (GATE == 2) sum_scalar += t[kScalar < (int)(sizeof(t) / sizeof(float)) ? kScalar : 0];
+      if (--gate_left == 0 || row + 1 == row1) {
+        const bool direct = gate_whole && gate_left == 0;
+        const int64_t cols = GATE == 1 ? a.width : 1;
+        float* part_of = a.gate_partial + (2 * worker + (gate_whole ? 1 : 0)) * cols;
+        if (GATE == 1) {
+#pragma unroll
+          for (int j = 0; j < NV; ++j) {
+            if (!in[j]) continue;
+            const int col = my_col + j * threads * VEC;
+            float m[VEC], q[VEC];
+            get(0, j, m);
+            load_param<T, VEC>(a.gate, a.params_f32, gate_row * a.width + col, q);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+              m[i] *= sum_a[j][i];
+              sum_wpost[j][i] = fmaf(a.scale * q[i], sum_a[j][i], sum_wpost[j][i]);
+              sum_a[j][i] = 0.f;
+            }
+            if (SUM0) {
+              float b[VEC];
+              get(2, j, b);
+#pragma unroll
+              for (int i = 0; i < VEC; ++i) {
+                m[i] = fmaf(b[i], sum_d[j][i], m[i]);
+                sum_bpost[j][i] = fmaf(a.scale * q[i], sum_d[j][i], sum_bpost[j][i]);
+                sum_d[j][i] = 0.f;
+              }
+            }
+            if (!a.dgate) continue;
+            const int64_t at = gate_row * a.width + col;
+            if (!direct) store_floats<float, VEC>(part_of + col, m);
+            else if (a.params_f32) store_floats<float, VEC>(static_cast<float*>(a.dgate) + at, m);
+            else store_floats<T, VEC>(static_cast<T*>(a.dgate) + at, m);
+          }
+        } else {
+          if (a.dgate && tid == 0 && part == 0) {
+            if (!direct) part_of[0] = sum_scalar;
+            else if (a.params_f32) static_cast<float*>(a.dgate)[gate_row] = sum_scalar;
+            else static_cast<T*>(a.dgate)[gate_row] = from_float<T>(sum_scalar);
+          }
+          sum_scalar = 0.f;
+        }
+        if (gate_left == 0) {
+          ++gate_row;
+          gate_left = a.gate_span;
+          gate_whole = true;
+        }
+      }
+    }
+  }
+  copies_wait<0>();
+
+  if (worker < a.workers) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (!in[j]) continue;
+      const int64_t at = worker * a.width + my_col + j * threads * VEC;
+      if (a.partial[0]) store_floats<float, VEC>(a.partial[0] + at, GATE == 1 ? sum_wpost[GATE == 1 ? j : 0] : sum_a[j]);
+      if (SUM0 && a.partial[1])
+        store_floats<float, VEC>(a.partial[1] + at, GATE == 1 ? sum_bpost[GATE == 1 && SUM0 ? j : 0] : sum_d[SUM0 ? j : 0]);
+      if (a.partial[2]) store_floats<float, VEC>(a.partial[2] + at, sum_wpre[j]);
+      if (LAYER && a.partial[3]) store_floats<float, VEC>(a.partial[3] + at, sum_bpre[LAYER ? j : 0]);
+    }
+  }
+  // No block of a cluster may end while another can still write to its slots.
+  if (blocks > 1)
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
+                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // Adds the workers' column sums: blockIdx.y 0..3 a parameter each, 4 the gate
-// rows that more than one worker shares.
+// (with folded sums), or its rows that more than one worker shares.
 constexpr int kFinishRows = 32;
 
 template <typename T>
@@ -320,19 +752,39 @@ norm_grad_finish(const NormGradArgs a) {
     if (a.params_f32) static_cast<float*>(to)[at] = v;
     else static_cast<T*>(to)[at] = from_float<T>(v);
   };
-  if (which < 4) {
-    if (!a.dparam[which]) return;
+  auto parameter = [&](const void* p, float missing) {
+    if (!p) return missing;
+    return a.params_f32 ? static_cast<const float*>(p)[col] : to_float(static_cast<const T*>(p)[col]);
+  };
+  // The sum of one of the partials' columns (the block's, threads y = 0).
+  auto total = [&](const float* partial) {
     float s = 0.f;
-    if (col < a.width)
-      for (int64_t w = threadIdx.y; w < a.workers; w += kFinishRows)
-        s += a.partial[which][w * a.width + col];
+    if (col < a.width && partial)
+      for (int64_t w = threadIdx.y; w < a.workers; w += kFinishRows) s += partial[w * a.width + col];
+    __syncthreads();
     part[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
-    if (threadIdx.y == 0 && col < a.width) {
+    if (threadIdx.y == 0) {
       s = part[0][threadIdx.x];
       for (int i = 1; i < kFinishRows; ++i) s += part[i][threadIdx.x];
+    }
+    return s;
+  };
+  if (which < 4) {
+    if (!a.dparam[which]) return;
+    float s = total(a.partial[which]);
+    if (threadIdx.y == 0 && col < a.width) {
+      if (a.folded && which < 2) s *= a.scale * parameter(a.gate, 1.f);
       put(a.dparam[which], col, s);
     }
+    return;
+  }
+  if (a.folded) {                      // one gate row: scale (w_post sum D a + b_post sum D)
+    if (!a.dgate) return;
+    const float da = total(a.partial[0]), d = total(a.partial[1]);
+    if (threadIdx.y == 0 && col < a.width)
+      put(a.dgate, col, a.scale * fmaf(a.post ? parameter(a.w_post, 1.f) : 1.f, da,
+                                       a.post ? parameter(a.b_post, 0.f) * d : 0.f));
     return;
   }
   const int64_t cols = a.gate_scalar ? 1 : a.width;
@@ -347,6 +799,65 @@ norm_grad_finish(const NormGradArgs a) {
       s += a.gate_partial[2 * w * cols + col];
     put(a.dgate, g * cols + col, s);
   }
+}
+
+template <typename T>
+cudaError_t launch_finish(const NormGradArgs& a, cudaStream_t s) {
+  bool any = a.dgate && (a.folded || a.workers > 1);
+  for (int k = 0; k < 4; ++k) any = any || a.dparam[k];
+  if (!any) return cudaSuccess;
+  cudaLaunchConfig_t fin = {};
+  fin.gridDim = dim3((unsigned)((a.width + 31) / 32), 5);
+  fin.blockDim = dim3(32, kFinishRows);
+  fin.stream = s;
+  cudaLaunchAttribute overlapped = overlapped_launch();
+  fin.attrs = &overlapped;
+  fin.numAttrs = 1;
+  return cudaLaunchKernelEx(&fin, norm_grad_finish<T>, a);
+}
+
+template <typename T, bool LAYER, bool POST, int GATE>
+cudaError_t launch_stream(NormGradArgs a, int sms, cudaStream_t s) {
+  const int blocks = (a.width + 8 * kStreamThreads - 1) / (8 * kStreamThreads);
+  const int block_cols = ((a.width + blocks - 1) / blocks + 7) / 8 * 8;
+  const int threads = norm_grad_threads(block_cols);
+  const int rows = threads < 128 ? 128 / threads : 1;
+  const int smem = grad_pieces<T, LAYER>() * 16 * threads * rows;
+  static OncePerDevice prepared;
+  cudaError_t e = prepared.run([] {
+    return cudaFuncSetAttribute(norm_grad_stream_kernel<T, LAYER, POST, GATE>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                grad_pieces<T, LAYER>() * 16 * kStreamThreads);
+  });
+  if (e != cudaSuccess) return e;
+  int at_once = kStreamWarps * 32 / (threads * rows);          // by registers; by shared memory
+  if (at_once > 216 * 1024 / smem) at_once = 216 * 1024 / smem;
+  if (at_once < 1) at_once = 1;
+  int64_t most = (int64_t)(at_once * sms / blocks) * rows;
+  if (most < 1) most = 1;
+  a.span = (a.rows + most - 1) / most;
+  a.workers = (a.rows + a.span - 1) / a.span;
+  a.folded = GATE == 0;
+  if (!(LAYER && POST)) a.partial[1] = nullptr;        // no b_post, no sum of D
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((a.workers + rows - 1) / rows * blocks));
+  cfg.blockDim = dim3(threads, rows);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2] = {overlapped_launch()};
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = blocks;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = blocks > 1 ? 2 : 1;
+  e = cudaLaunchKernelEx(&cfg, norm_grad_stream_kernel<T, LAYER, POST, GATE>, a, blocks, block_cols);
+  return e != cudaSuccess ? e : launch_finish<T>(a, s);
+}
+
+template <typename T, bool LAYER, bool POST>
+cudaError_t pick_stream(const NormGradArgs& a, int sms, cudaStream_t s) {
+  if (!a.gate || (!a.gate_scalar && a.gate_span >= a.rows)) return launch_stream<T, LAYER, POST, 0>(a, sms, s);
+  return a.gate_scalar ? launch_stream<T, LAYER, POST, 2>(a, sms, s) : launch_stream<T, LAYER, POST, 1>(a, sms, s);
 }
 
 template <typename T, int VEC, int NV, bool LAYER, bool GATE>
@@ -369,16 +880,7 @@ cudaError_t launch(NormGradArgs a, int sms, cudaStream_t s) {
   cfg.attrs = at;
   cfg.numAttrs = blocks > 1 ? 2 : 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, norm_grad_kernel<T, VEC, NV, LAYER, GATE>, a, blocks, block_cols);
-  bool any = a.dgate && a.workers > 1;
-  for (int k = 0; k < 4; ++k) any = any || a.dparam[k];
-  if (e != cudaSuccess || !any) return e;
-  cudaLaunchConfig_t fin = {};
-  fin.gridDim = dim3((unsigned)((a.width + 31) / 32), 5);
-  fin.blockDim = dim3(32, kFinishRows);
-  fin.stream = s;
-  fin.attrs = at;
-  fin.numAttrs = 1;
-  return cudaLaunchKernelEx(&fin, norm_grad_finish<T>, a);
+  return e != cudaSuccess ? e : launch_finish<T>(a, s);
 }
 
 template <typename T, int VEC, int NV>
@@ -393,10 +895,11 @@ cudaError_t pick(const NormGradArgs& a, int layer, int sms, cudaStream_t s) {
 template <>
 cudaError_t launch_norm_grad<ECHO_ELEM>(NormGradArgs a, int layer, bool vec, int sms, cudaStream_t s) {
   using T = ECHO_ELEM;
-  constexpr int V = 16 / sizeof(T);
-  const bool narrow = a.width <= 8 * kThreads;
-  if (!vec) return narrow ? pick<T, 1, 8>(a, layer, sms, s) : pick<T, 1, 16>(a, layer, sms, s);
-  return narrow ? pick<T, V, 8 / V>(a, layer, sms, s) : pick<T, V, 16 / V>(a, layer, sms, s);
+  if (vec) {
+    if (layer) return a.post ? pick_stream<T, true, true>(a, sms, s) : pick_stream<T, true, false>(a, sms, s);
+    return a.post ? pick_stream<T, false, true>(a, sms, s) : pick_stream<T, false, false>(a, sms, s);
+  }
+  return a.width <= 8 * kThreads ? pick<T, 1, 8>(a, layer, sms, s) : pick<T, 1, 16>(a, layer, sms, s);
 }
 
 }  // namespace echo

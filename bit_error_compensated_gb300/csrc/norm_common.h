@@ -44,6 +44,7 @@ struct NormGradArgs {
   int64_t workers;
   float scale;
   int gate_scalar, post, params_f32;
+  int folded;                    // partial[0], [1] are without scale and gate (norm_bwd.cu)
 };
 
 // N floats of a parameter vector (or gate row) of either type, from element `col`.
@@ -72,10 +73,13 @@ template <typename T>
 cudaError_t launch_norm(const NormArgs& a, int layer, bool vec, int sms, cudaStream_t s);
 template <typename T>
 cudaError_t launch_norm_grad(NormGradArgs a, int layer, bool vec, int sms, cudaStream_t s);
-// Workers (row ranges with their own partial sums) a backward call may have:
-// two blocks an SM, of up to 4 rows at once where a row takes less than 128 threads.
+// Threads that norm_grad_stream_kernel gives a row of `cols` columns of a block.
+inline int norm_grad_threads(int cols) { return ((cols + 7) / 8 + 31) / 32 * 32; }
+// Workers (row ranges with their own partial sums) a backward call may have at most.
 inline int64_t norm_grad_max_workers(int width, int sms) {
-  return (int64_t)2 * sms * (width <= 128 * 16 ? 4 : 1);
+  const int threads = norm_grad_threads(width < 4096 ? width : 4096);
+  const int stream = 1024 / threads > 1 ? 1024 / threads : 1, plain = width <= 2048 ? 8 : 2;
+  return (int64_t)sms * (stream > plain ? stream : plain);
 }
 
 }  // namespace echo
