@@ -14,307 +14,33 @@
 // split by columns over a cluster, whose blocks exchange the row sums through
 // distributed shared memory.
 //
-// norm_grad_stream_kernel takes rows of 16-byte pieces.  Its time is that of
-// its bytes (12 a 16-bit element) as long as it stays under 5 instructions an
-// element, warp and cycle's share, so: rows come through a ring of
-// asynchronous copies; scale, gate and weight are multiplied once (one gate row
-// for all) or once a row; and with one gate row for all, or while a gate row
-// lasts, only A = sum D a (and sum D) are kept, of which dw_post is
-// scale gate A and dgate is scale (w_post A + b_post sum D).
-// norm_grad_kernel takes any other row.
+// The bytes (12 a 16-bit element) leave an SM 2090 cycles a row of 4096, so
+// instructions count: rows of 16-byte pieces come through a ring of
+// asynchronous copies (others element by element, a row ahead in registers);
+// scale, gate and weight are multiplied once (one gate row for all) or once a
+// row; and with one gate row for all, or while a gate row lasts, only
+// A = sum D a (and sum D) are kept, of which dw_post is scale gate A and dgate
+// is scale (w_post A + b_post sum D).
 #include "norm_common.h"
 
 namespace echo {
 namespace {
 
-constexpr int kThreads = 256;          // of a block at most
-constexpr int kBlocksPerSm = 2;        // of a call's grid
-constexpr int kMaxCluster = 4;         // ECHO_NORM_MAX_WIDTH / (16 * kThreads)
-constexpr int kSlots = kThreads / 32 * kMaxCluster;
+constexpr int kMaxCluster = 8;         // ECHO_NORM_MAX_WIDTH / 2048
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return (uint32_t)__cvta_generic_to_shared(p);
 }
 
-// Sums over a row's threads: those of its warps of this block and, in a
-// cluster, of the other blocks'.  A warp writes its sum to the slot that
+// Sums of N values over a row's threads: those of its warps of this block and,
+// in a cluster, of the other blocks'.  A warp writes its sum to the slot that
 // belongs to it in every block; then one barrier (of the cluster, or of the
-// block) and everyone adds the slots in the same order.  Two sets of slots in
-// turn, as a set is written again only behind the next sum's barrier.
-template <int N>
-struct RowSums {
-  float (*slots)[kSlots][N];           // [2]
-  int first, count, warp, lane;        // the row's slots; this warp's among them
-  int blocks;                          // of the cluster
-  int which;
-  __device__ __forceinline__ void all(float (&v)[N]) {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
-#pragma unroll
-      for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], d);
-    if (count == 1) return;
-    float(*s)[N] = slots[which];
-    which ^= 1;
-    if (blocks > 1) {
-      if (lane < blocks) {
-        uint32_t at;
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                     : "=r"(at) : "r"(smem_u32(&s[first + warp][0])), "r"(lane));
-#pragma unroll
-        for (int k = 0; k < N; ++k)
-          asm volatile("st.shared::cluster.f32 [%0], %1;" :: "r"(at + 4 * k), "f"(v[k]) : "memory");
-      }
-      asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
-                   "barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    } else {
-      if (lane == 0)
-#pragma unroll
-        for (int k = 0; k < N; ++k) s[first + warp][k] = v[k];
-      __syncthreads();
-    }
-#pragma unroll
-    for (int k = 0; k < N; ++k) v[k] = s[first][k];
-    for (int i = 1; i < count; ++i)
-#pragma unroll
-      for (int k = 0; k < N; ++k) v[k] += s[first + i][k];
-  }
-};
-
-template <typename T, int VEC, int NV, bool LAYER, bool GATE>
-__global__ void __launch_bounds__(kThreads)
-norm_grad_kernel(const NormGradArgs a, int blocks, int block_cols) {
-  constexpr int E = VEC * NV;
-  __shared__ float slots[2][kSlots][3];
-  const int tid = threadIdx.x, threads = blockDim.x;
-  const int part = (int)blockIdx.x % blocks;             // of the row's columns
-  const int64_t worker = (int64_t)(blockIdx.x / blocks) * blockDim.y + threadIdx.y;
-  const int col0 = part * block_cols;
-  const int warps = threads / 32;
-  RowSums<3> sums{slots, (int)threadIdx.y * warps, warps * blocks, part * warps + (tid >> 5),
-                  tid & 31, blocks, 0};
-  const float inv_width = 1.0f / (float)a.width;
-  if (blocks > 1)                      // every block's slots exist before the first is written
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
-                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  pdl_wait();
-  pdl_trigger();
-
-  bool in[NV];
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int c = (j * threads + tid) * VEC;
-    in[j] = c < block_cols && col0 + c < a.width;
-  }
-  auto col_of = [&](int j) { return col0 + (j * threads + tid) * VEC; };
-
-  float sum_wpost[E], sum_bpost[LAYER ? E : 1], sum_wpre[E], sum_bpre[LAYER ? E : 1];
-  float sum_gate[GATE ? E : 1];
-#pragma unroll
-  for (int i = 0; i < E; ++i) {
-    sum_wpost[i] = sum_wpre[i] = 0.f;
-    if (LAYER) sum_bpost[i] = sum_bpre[i] = 0.f;
-    if (GATE) sum_gate[i] = 0.f;
-  }
-  float sum_scalar = 0.f;
-
-  const int64_t row0 = worker * a.span;
-  const int64_t row1 = row0 + a.span < a.rows ? row0 + a.span : a.rows;
-  int64_t gate_row = a.gate ? row0 / a.gate_span : 0;
-  int64_t gate_left = a.gate ? a.gate_span - (row0 - gate_row * a.gate_span) : 0;
-  bool gate_whole = a.gate && gate_left == a.gate_span;   // its first row is this worker's
-
-  for (int64_t step = 0; step < a.span; ++step) {
-    const int64_t row = row0 + step;
-    const bool active = row < row1;
-    bool on[NV];
-    float hat1[E], hat2[E], g[E], d[E];
-    float4 st = make_float4(0.f, 1.f, 0.f, 1.f);
-    if (active && a.stats) st = __ldg(reinterpret_cast<const float4*>(a.stats) + row);
-    float s[3] = {0.f, 0.f, 0.f};
-    float gate_value = 1.f;
-    if (a.gate && a.gate_scalar && active) {
-      float one[1];
-      load_param<T, 1>(a.gate, a.params_f32, gate_row, 1.f, one);
-      gate_value = one[0];
-    }
-    // n and gate of vector j, from a
-    auto n_of = [&](int j, float (&n)[VEC], float (&gate)[VEC]) {
-      float w[VEC], b[VEC];
-      if (a.post) {
-        load_param<T, VEC>(a.w_post, a.params_f32, col_of(j), 1.f, w);
-        load_param<T, VEC>(a.b_post, a.params_f32, col_of(j), 0.f, b);
-      }
-      if (GATE) load_param<T, VEC>(a.gate, a.params_f32, gate_row * a.width + col_of(j), 1.f, gate);
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        n[i] = a.post ? hat1[j * VEC + i] * w[i] + b[i] : hat1[j * VEC + i];
-        if (!GATE) gate[i] = gate_value;
-      }
-    };
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      on[j] = active && in[j];
-      Pack<T, VEC> px, py, pr, ph;
-      if (on[j]) {
-        px = load_pack<T, VEC>(static_cast<const T*>(a.x) + row * a.ld_x + col_of(j));
-        if (a.y) py = load_pack<T, VEC>(static_cast<const T*>(a.y) + row * a.ld_y + col_of(j));
-        if (a.dr) pr = load_pack<T, VEC>(static_cast<const T*>(a.dr) + row * a.ld_dr + col_of(j));
-        if (a.dh) ph = load_pack<T, VEC>(static_cast<const T*>(a.dh) + row * a.ld_dh + col_of(j));
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          const float y = a.y ? to_float(py.v[i]) : 0.f;
-          hat1[j * VEC + i] = a.post ? (y - st.x) * st.y : y;
-        }
-        float n[VEC], gate[VEC], w[VEC];
-        n_of(j, n, gate);
-        load_param<T, VEC>(a.w_pre, a.params_f32, col_of(j), 1.f, w);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          const int k = j * VEC + i;
-          const float r = a.y ? to_float(px.v[i]) + a.scale * (gate[i] * n[i]) : to_float(px.v[i]);
-          hat2[k] = (r - st.z) * st.w;
-          const float dh = a.dh ? to_float(ph.v[i]) : 0.f;
-          sum_wpre[k] += dh * hat2[k];
-          if (LAYER) sum_bpre[k] += dh;
-          g[k] = dh * w[i];
-          d[k] = a.dr ? to_float(pr.v[i]) : 0.f;
-          s[0] += g[k] * hat2[k];
-          if (LAYER) s[1] += g[k];
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i)
-          hat1[j * VEC + i] = hat2[j * VEC + i] = g[j * VEC + i] = d[j * VEC + i] = 0.f;
-      }
-    }
-    if (a.dh) {
-      sums.all(s);
-      s[0] *= inv_width;
-      s[1] *= inv_width;
-    }
-    float t[3] = {0.f, 0.f, 0.f};
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      if (!on[j]) continue;
-      if (a.dh) {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          const int k = j * VEC + i;
-          d[k] += st.w * (g[k] - (LAYER ? s[1] : 0.f) - hat2[k] * s[0]);
-        }
-      }
-      float dx[VEC];
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) dx[i] = d[j * VEC + i];
-      if (a.dx) store_floats<T, VEC>(static_cast<T*>(a.dx) + row * a.ld_dx + col_of(j), dx);
-      if (!a.y) continue;
-      float n[VEC], gate[VEC], w[VEC];
-      n_of(j, n, gate);
-      if (a.post) load_param<T, VEC>(a.w_post, a.params_f32, col_of(j), 1.f, w);
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const int k = j * VEC + i;
-        const float sd = a.scale * d[k];
-        if (GATE) sum_gate[k] += sd * n[i];
-        else t[2] += sd * n[i];
-        float dn = sd * gate[i];
-        if (a.post) {
-          sum_wpost[k] += dn * hat1[k];
-          if (LAYER) sum_bpost[k] += dn;
-          dn *= w[i];
-          t[0] += dn * hat1[k];
-          if (LAYER) t[1] += dn;
-        }
-        g[k] = dn;
-      }
-    }
-    if (a.post || a.gate_scalar) {
-      sums.all(t);
-      t[0] *= inv_width;
-      t[1] *= inv_width;
-    }
-    if (a.y && a.dy) {
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        if (!on[j]) continue;
-        float dy[VEC];
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          const int k = j * VEC + i;
-          dy[i] = a.post ? st.y * (g[k] - (LAYER ? t[1] : 0.f) - hat1[k] * t[0]) : g[k];
-        }
-        store_floats<T, VEC>(static_cast<T*>(a.dy) + row * a.ld_dy + col_of(j), dy);
-      }
-    }
-    // The gate's gradient: a gate row whose rows are all this worker's is
-    // written; one that began before its range goes to the worker's first
-    // slot, one that goes on behind it to the second, for norm_grad_finish.
-    if (a.gate && active) --gate_left;
-    if (a.dgate && active) {
-      sum_scalar += t[2];
-      if (gate_left == 0 || row + 1 == row1) {
-        const bool direct = gate_whole && gate_left == 0;
-        const int64_t cols = GATE ? a.width : 1;
-        float* slot = a.gate_partial + (2 * worker + (gate_whole ? 1 : 0)) * cols;
-        if (GATE) {
-#pragma unroll
-          for (int j = 0; j < NV; ++j) {
-            if (!in[j]) continue;
-            float v[VEC];
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-              v[i] = sum_gate[j * VEC + i];
-              sum_gate[j * VEC + i] = 0.f;
-            }
-            const int64_t at = gate_row * a.width + col_of(j);
-            if (!direct) store_floats<float, VEC>(slot + col_of(j), v);
-            else if (a.params_f32) store_floats<float, VEC>(static_cast<float*>(a.dgate) + at, v);
-            else store_floats<T, VEC>(static_cast<T*>(a.dgate) + at, v);
-          }
-        } else {
-          if (tid == 0 && part == 0) {
-            if (!direct) slot[0] = sum_scalar;
-            else if (a.params_f32) static_cast<float*>(a.dgate)[gate_row] = sum_scalar;
-            else static_cast<T*>(a.dgate)[gate_row] = from_float<T>(sum_scalar);
-          }
-          sum_scalar = 0.f;
-        }
-      }
-    }
-    if (a.gate && active && gate_left == 0) {
-      ++gate_row;
-      gate_left = a.gate_span;
-      gate_whole = true;
-    }
-  }
-
-  if (worker < a.workers) {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      if (!in[j]) continue;
-      const int64_t at = worker * a.width + col_of(j);
-      auto put = [&](float* to, const float* from) {
-        if (!to) return;
-        float v[VEC];
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) v[i] = from[j * VEC + i];
-        store_floats<float, VEC>(to + at, v);
-      };
-      put(a.partial[0], sum_wpost);
-      if (LAYER) put(a.partial[1], sum_bpost);
-      put(a.partial[2], sum_wpre);
-      if (LAYER) put(a.partial[3], sum_bpre);
-    }
-  }
-  // No block of a cluster may end while another can still write to its slots.
-  if (blocks > 1)
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
-                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// Sums of N values over a row's threads, as RowSums above, four slots read at
-// a time (slots past a row's warps stay 0).
-constexpr int kStreamThreads = 512, kStreamSlots = kStreamThreads / 32 * kMaxCluster;
+// block) and everyone adds the slots in the same order, four at a time (those
+// past a row's warps stay 0).  Two sets of slots in turn, as a set is written
+// again only behind the next sum's barrier.
+constexpr int kStreamThreads = 512;
+constexpr int kStreamSlots = 64;       // 16 warps of one block, or 8 of each of 8
+static_assert(kStreamSlots >= kStreamThreads / 32 && kStreamSlots >= 8 * kMaxCluster, "a slot for every warp");
 
 struct StreamSums {
   float (*slots)[3][kStreamSlots];     // [2]
@@ -365,18 +91,20 @@ struct StreamSums {
 template <typename T> constexpr int rows_ahead() { return sizeof(T) == 2 ? 4 : 2; }
 // 16-byte pieces of shared memory a thread has: the ring's (x, y, dr, dh) and
 // its columns' fp32 parameters (mul, w, and for layer norms add).
-template <typename T, bool LAYER>
-constexpr int grad_pieces() { return rows_ahead<T>() * 4 * (8 * (int)sizeof(T) / 16) + (LAYER ? 6 : 4); }
+template <typename T, int VEC, bool LAYER>
+constexpr int grad_pieces() {
+  return (VEC == 1 ? 0 : rows_ahead<T>() * 4 * (8 * (int)sizeof(T) / 16)) + (LAYER ? 6 : 4);
+}
 // Warps an SM: at 128 registers a thread.  (64 and twice the warps spill, and
 // take 143 us where this takes GRAD_US, 8192 x 4096 bf16.)
 constexpr int kStreamWarps = 16;
 
 // GATE: 0 none, or one row for all; 1 a row of gates, 2 a gate, for each row
 // or several.
-template <typename T, bool LAYER, bool POST, int GATE>
+template <typename T, int VEC, bool LAYER, bool POST, int GATE>
 __global__ void __launch_bounds__(kStreamThreads, 1)
-norm_grad_stream_kernel(const NormGradArgs a, int blocks, int block_cols) {
-  constexpr int VEC = 16 / sizeof(T), NV = 8 / VEC, kAhead = rows_ahead<T>();
+norm_grad_kernel(const NormGradArgs a, int blocks, int block_cols) {
+  constexpr int NV = 8 / VEC, kAhead = VEC == 1 ? 1 : rows_ahead<T>();
   constexpr bool SUM0 = LAYER && POST;                  // sum D is needed (db_post, dgate)
   extern __shared__ __align__(16) uint8_t room[];
   __shared__ __align__(16) float slots[2][3][kStreamSlots];
@@ -404,50 +132,65 @@ norm_grad_stream_kernel(const NormGradArgs a, int blocks, int block_cols) {
   const int64_t row1 = row0 + a.span < a.rows ? row0 + a.span : a.rows;
   const uint32_t piece = 16u * all_threads;
   const uint32_t mine = smem_u32(room) + 16u * me, slot_bytes = 4 * NV * piece;
-  const uint32_t params = mine + kAhead * slot_bytes;
+  const uint32_t params = VEC == 1 ? smem_u32(room) + 4u * me : mine + kAhead * slot_bytes;
   auto start = [&](const void* p, int64_t ld) {
     return static_cast<const char*>(p) + (row0 * ld + my_col) * (int64_t)sizeof(T);
   };
   const char* from[4] = {start(a.x, a.ld_x), start(a.y, a.ld_y), start(a.dr, a.ld_dr), start(a.dh, a.ld_dh)};
+  const bool there[4] = {true, a.y != nullptr, a.dr != nullptr, a.dh != nullptr};
+  const int64_t far[4] = {a.ld_x * (int64_t)sizeof(T), a.ld_y * (int64_t)sizeof(T), a.ld_dr * (int64_t)sizeof(T),
+                          a.ld_dh * (int64_t)sizeof(T)};
+  // Whole pieces wait in the ring; single elements, which asynchronous copies
+  // do not take, in registers.
+  T held[VEC == 1 ? 4 : 1][VEC == 1 ? NV : 1];
   int64_t fetch = row0;
-  auto copy_row = [&](uint32_t slot) {
-    if (fetch < row1) {
+  auto fetch_array = [&](int k, uint32_t slot) {
+    if (fetch < row1 && there[k]) {
 #pragma unroll
       for (int j = 0; j < NV; ++j)
         if (in[j]) {
-          const uint32_t to = mine + slot * slot_bytes + 4 * j * piece;
-          copy16_async(to, from[0] + 16 * j * threads);
-          if (a.y) copy16_async(to + piece, from[1] + 16 * j * threads);
-          if (a.dr) copy16_async(to + 2 * piece, from[2] + 16 * j * threads);
-          if (a.dh) copy16_async(to + 3 * piece, from[3] + 16 * j * threads);
+          if constexpr (VEC == 1) held[k][j] = *reinterpret_cast<const T*>(from[k] + j * threads * (int)sizeof(T));
+          else copy16_async(mine + slot * slot_bytes + (4 * j + k) * piece, from[k] + 16 * j * threads);
         }
     }
-    copies_commit();
-    ++fetch;
-    from[0] += a.ld_x * sizeof(T);
-    from[1] += a.ld_y * sizeof(T);
-    from[2] += a.ld_dr * sizeof(T);
-    from[3] += a.ld_dh * sizeof(T);
+    from[k] += far[k];
+  };
+  auto take = [&](int k, int j, uint32_t slot, float (&v)[VEC]) {
+    if constexpr (VEC == 1) v[0] = to_float(held[k][j]);
+    else to_floats<T, VEC>(load_shared16<T, VEC>(mine + slot * slot_bytes + (4 * j + k) * piece), v);
   };
 #pragma unroll
-  for (int s = 0; s < kAhead; ++s) copy_row(s);
+  for (int s = 0; s < kAhead; ++s) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) fetch_array(k, s);
+    if (VEC > 1) copies_commit();
+    ++fetch;
+  }
 
   // The columns' parameters, as fp32 in this thread's shared memory: mul and
   // add of n * scale (times the gate, if it is one row) = hat1 * mul + add,
   // and w of the norm of r.
   auto put = [&](int at, int j, const float (&v)[VEC]) {
+    if constexpr (VEC == 1) {
+      asm volatile("st.shared.f32 [%0], %1;" :: "r"(params + (uint32_t)(at * 8 + j) * (piece / 4)), "f"(v[0]) : "memory");
+    } else {
 #pragma unroll
-    for (int i = 0; i < VEC; i += 4)
-      asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};"
-                   :: "r"(params + (uint32_t)(at * 2 + j * (VEC / 4) + i / 4) * piece), "f"(v[i]), "f"(v[i + 1]),
-                      "f"(v[i + 2]), "f"(v[i + 3]) : "memory");
+      for (int i = 0; i < VEC; i += 4)
+        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};"
+                     :: "r"(params + (uint32_t)(at * 2 + j * (VEC / 4) + i / 4) * piece), "f"(v[i]), "f"(v[i + 1]),
+                        "f"(v[i + 2]), "f"(v[i + 3]) : "memory");
+    }
   };
   auto get = [&](int at, int j, float (&v)[VEC]) {
+    if constexpr (VEC == 1) {
+      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[0]) : "r"(params + (uint32_t)(at * 8 + j) * (piece / 4)) : "memory");
+    } else {
 #pragma unroll
-    for (int i = 0; i < VEC; i += 4)
-      asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                   : "=f"(v[i]), "=f"(v[i + 1]), "=f"(v[i + 2]), "=f"(v[i + 3])
-                   : "r"(params + (uint32_t)(at * 2 + j * (VEC / 4) + i / 4) * piece) : "memory");
+      for (int i = 0; i < VEC; i += 4)
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(v[i]), "=f"(v[i + 1]), "=f"(v[i + 2]), "=f"(v[i + 3])
+                     : "r"(params + (uint32_t)(at * 2 + j * (VEC / 4) + i / 4) * piece) : "memory");
+    }
   };
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
@@ -519,8 +262,7 @@ norm_grad_stream_kernel(const NormGradArgs a, int blocks, int block_cols) {
       load_param<T, 1>(a.gate, a.params_f32, gate_row, one);
       gate = one[0];
     }
-    copies_wait<kAhead - 1>();
-    const uint32_t here = mine + slot * slot_bytes;
+    if (VEC > 1) copies_wait<kAhead - 1>();
     float hat1[NV][VEC], hat2[NV][VEC], g[NV][VEC];     // g: dh w, then f
     float s[LAYER ? 2 : 1] = {};
 #pragma unroll
@@ -531,9 +273,9 @@ norm_grad_stream_kernel(const NormGradArgs a, int blocks, int block_cols) {
         continue;
       }
       float x[VEC], m[VEC];
-      to_floats<T, VEC>(load_shared16<T, VEC>(here + 4 * j * piece), x);
+      take(0, j, slot, x);
       if (a.y) {
-        to_floats<T, VEC>(load_shared16<T, VEC>(here + (4 * j + 1) * piece), hat1[j]);
+        take(1, j, slot, hat1[j]);
         if (POST)
 #pragma unroll
           for (int i = 0; i < VEC; ++i) hat1[j][i] = LAYER ? (hat1[j][i] - st.x) * st.y : hat1[j][i] * st.y;
@@ -565,7 +307,7 @@ norm_grad_stream_kernel(const NormGradArgs a, int blocks, int block_cols) {
       for (int i = 0; i < VEC; ++i) hat2[j][i] = LAYER ? (x[i] - st.z) * st.w : x[i] * st.w;
       if (a.dh) {
         float w[VEC];
-        to_floats<T, VEC>(load_shared16<T, VEC>(here + (4 * j + 3) * piece), g[j]);
+        take(3, j, slot, g[j]);
         get(1, j, w);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
@@ -580,6 +322,11 @@ norm_grad_stream_kernel(const NormGradArgs a, int blocks, int block_cols) {
         for (int i = 0; i < VEC; ++i) g[j][i] = 0.f;
       }
     }
+    if (VEC == 1) {                     // what has been read makes room for the next row's
+      fetch_array(0, 0);
+      fetch_array(1, 0);
+      fetch_array(3, 0);
+    }
     if (a.dh) {
       sums.all(s);
 #pragma unroll
@@ -592,7 +339,7 @@ norm_grad_stream_kernel(const NormGradArgs a, int blocks, int block_cols) {
       if (!active || !in[j]) continue;
       float d[VEC];
       if (a.dr) {
-        to_floats<T, VEC>(load_shared16<T, VEC>(here + (4 * j + 2) * piece), d);
+        take(2, j, slot, d);
       } else {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) d[i] = 0.f;
@@ -602,7 +349,7 @@ norm_grad_stream_kernel(const NormGradArgs a, int blocks, int block_cols) {
         const float back = fmaf(-s[0], hat2[j][i], LAYER ? g[j][i] - s[LAYER ? 1 : 0] : g[j][i]);
         d[i] = fmaf(st.w, back, d[i]);
       }
-      if (a.dx) store_floats<T, VEC>(reinterpret_cast<T*>(to_dx + 16 * j * threads), d);
+      if (a.dx) store_floats<T, VEC>(reinterpret_cast<T*>(to_dx) + j * threads * VEC, d);
       if (!a.y) continue;
       float m[VEC];
       get(0, j, m);
@@ -640,8 +387,15 @@ norm_grad_stream_kernel(const NormGradArgs a, int blocks, int block_cols) {
         }
       }
     }
-    copy_row(slot);                     // this thread has read its pieces of the slot
-    slot = slot == kAhead - 1 ? 0 : slot + 1;
+    if (VEC == 1) {
+      fetch_array(2, 0);
+    } else {                            // this thread has read its pieces of the slot
+#pragma unroll
+      for (int k = 0; k < 4; ++k) fetch_array(k, slot);
+      copies_commit();
+      slot = slot == kAhead - 1 ? 0 : slot + 1;
+    }
+    ++fetch;
     if (POST || GATE == 2) {
       sums.all(t);
       t[0] *= inv_width;
@@ -655,7 +409,7 @@ norm_grad_stream_kernel(const NormGradArgs a, int blocks, int block_cols) {
 #pragma unroll
           for (int i = 0; i < VEC; ++i)
             g[j][i] = st.y * fmaf(-t[0], hat1[j][i], LAYER ? g[j][i] - t[LAYER ? 1 : 0] : g[j][i]);
-        store_floats<T, VEC>(reinterpret_cast<T*>(to_dy + 16 * j * threads), g[j]);
+        store_floats<T, VEC>(reinterpret_cast<T*>(to_dy) + j * threads * VEC, g[j]);
       }
     }
     to_dx += a.ld_dx * sizeof(T);
@@ -716,7 +470,7 @@ norm_grad_stream_kernel(const NormGradArgs a, int blocks, int block_cols) {
       }
     }
   }
-  copies_wait<0>();
+  if (VEC > 1) copies_wait<0>();
 
   if (worker < a.workers) {
 #pragma unroll
@@ -816,18 +570,20 @@ cudaError_t launch_finish(const NormGradArgs& a, cudaStream_t s) {
   return cudaLaunchKernelEx(&fin, norm_grad_finish<T>, a);
 }
 
-template <typename T, bool LAYER, bool POST, int GATE>
+template <typename T, int VEC, bool LAYER, bool POST, int GATE>
 cudaError_t launch_stream(NormGradArgs a, int sms, cudaStream_t s) {
-  const int blocks = (a.width + 8 * kStreamThreads - 1) / (8 * kStreamThreads);
+  // Past 4096 columns, blocks of 2048: two clusters an SM, so that one works
+  // while the other's barrier is on its way.
+  const int blocks = a.width <= 8 * kStreamThreads ? 1 : (a.width + 2047) / 2048;
   const int block_cols = ((a.width + blocks - 1) / blocks + 7) / 8 * 8;
   const int threads = norm_grad_threads(block_cols);
   const int rows = threads < 128 ? 128 / threads : 1;
-  const int smem = grad_pieces<T, LAYER>() * 16 * threads * rows;
+  const int smem = grad_pieces<T, VEC, LAYER>() * 16 * threads * rows;
   static OncePerDevice prepared;
   cudaError_t e = prepared.run([] {
-    return cudaFuncSetAttribute(norm_grad_stream_kernel<T, LAYER, POST, GATE>,
+    return cudaFuncSetAttribute(norm_grad_kernel<T, VEC, LAYER, POST, GATE>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                grad_pieces<T, LAYER>() * 16 * kStreamThreads);
+                                grad_pieces<T, VEC, LAYER>() * 16 * kStreamThreads);
   });
   if (e != cudaSuccess) return e;
   int at_once = kStreamWarps * 32 / (threads * rows);          // by registers; by shared memory
@@ -850,44 +606,21 @@ cudaError_t launch_stream(NormGradArgs a, int sms, cudaStream_t s) {
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = blocks > 1 ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, norm_grad_stream_kernel<T, LAYER, POST, GATE>, a, blocks, block_cols);
+  e = cudaLaunchKernelEx(&cfg, norm_grad_kernel<T, VEC, LAYER, POST, GATE>, a, blocks, block_cols);
   return e != cudaSuccess ? e : launch_finish<T>(a, s);
 }
 
-template <typename T, bool LAYER, bool POST>
-cudaError_t pick_stream(const NormGradArgs& a, int sms, cudaStream_t s) {
-  if (!a.gate || (!a.gate_scalar && a.gate_span >= a.rows)) return launch_stream<T, LAYER, POST, 0>(a, sms, s);
-  return a.gate_scalar ? launch_stream<T, LAYER, POST, 2>(a, sms, s) : launch_stream<T, LAYER, POST, 1>(a, sms, s);
+template <typename T, int VEC, bool LAYER, bool POST>
+cudaError_t pick_gate(const NormGradArgs& a, int sms, cudaStream_t s) {
+  if (!a.gate || (!a.gate_scalar && a.gate_span >= a.rows)) return launch_stream<T, VEC, LAYER, POST, 0>(a, sms, s);
+  return a.gate_scalar ? launch_stream<T, VEC, LAYER, POST, 2>(a, sms, s)
+                       : launch_stream<T, VEC, LAYER, POST, 1>(a, sms, s);
 }
 
-template <typename T, int VEC, int NV, bool LAYER, bool GATE>
-cudaError_t launch(NormGradArgs a, int sms, cudaStream_t s) {
-  const int blocks = (a.width + VEC * NV * kThreads - 1) / (VEC * NV * kThreads);
-  const int block_cols = ((a.width + blocks - 1) / blocks + VEC - 1) / VEC * VEC;
-  const int threads = ((block_cols + VEC * NV - 1) / (VEC * NV) + 31) / 32 * 32;
-  const int rows = threads < 128 ? 128 / threads : 1;
-  const int64_t most = (int64_t)(kBlocksPerSm * sms / blocks) * rows;
-  a.span = (a.rows + most - 1) / most;
-  a.workers = (a.rows + a.span - 1) / a.span;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((a.workers + rows - 1) / rows * blocks));
-  cfg.blockDim = dim3(threads, rows);
-  cfg.stream = s;
-  cudaLaunchAttribute at[2] = {overlapped_launch()};
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = blocks;
-  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = blocks > 1 ? 2 : 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, norm_grad_kernel<T, VEC, NV, LAYER, GATE>, a, blocks, block_cols);
-  return e != cudaSuccess ? e : launch_finish<T>(a, s);
-}
-
-template <typename T, int VEC, int NV>
-cudaError_t pick(const NormGradArgs& a, int layer, int sms, cudaStream_t s) {
-  const bool gate = a.gate && !a.gate_scalar;
-  if (layer) return gate ? launch<T, VEC, NV, true, true>(a, sms, s) : launch<T, VEC, NV, true, false>(a, sms, s);
-  return gate ? launch<T, VEC, NV, false, true>(a, sms, s) : launch<T, VEC, NV, false, false>(a, sms, s);
+template <typename T, int VEC>
+cudaError_t pick_norm(const NormGradArgs& a, int layer, int sms, cudaStream_t s) {
+  if (layer) return a.post ? pick_gate<T, VEC, true, true>(a, sms, s) : pick_gate<T, VEC, true, false>(a, sms, s);
+  return a.post ? pick_gate<T, VEC, false, true>(a, sms, s) : pick_gate<T, VEC, false, false>(a, sms, s);
 }
 
 }  // namespace
@@ -895,11 +628,7 @@ cudaError_t pick(const NormGradArgs& a, int layer, int sms, cudaStream_t s) {
 template <>
 cudaError_t launch_norm_grad<ECHO_ELEM>(NormGradArgs a, int layer, bool vec, int sms, cudaStream_t s) {
   using T = ECHO_ELEM;
-  if (vec) {
-    if (layer) return a.post ? pick_stream<T, true, true>(a, sms, s) : pick_stream<T, true, false>(a, sms, s);
-    return a.post ? pick_stream<T, false, true>(a, sms, s) : pick_stream<T, false, false>(a, sms, s);
-  }
-  return a.width <= 8 * kThreads ? pick<T, 1, 8>(a, layer, sms, s) : pick<T, 1, 16>(a, layer, sms, s);
+  return vec ? pick_norm<T, 16 / sizeof(T)>(a, layer, sms, s) : pick_norm<T, 1>(a, layer, sms, s);
 }
 
 }  // namespace echo

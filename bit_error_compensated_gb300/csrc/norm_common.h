@@ -73,13 +73,13 @@ template <typename T>
 cudaError_t launch_norm(const NormArgs& a, int layer, bool vec, int sms, cudaStream_t s);
 template <typename T>
 cudaError_t launch_norm_grad(NormGradArgs a, int layer, bool vec, int sms, cudaStream_t s);
-// Threads that norm_grad_stream_kernel gives a row of `cols` columns of a block.
+// Threads that the backward kernel gives a row of `cols` columns of a block.
 inline int norm_grad_threads(int cols) { return ((cols + 7) / 8 + 31) / 32 * 32; }
-// Workers (row ranges with their own partial sums) a backward call may have at most.
+// Workers (row ranges with their own partial sums) a backward call may have at
+// most: 16 warps an SM.
 inline int64_t norm_grad_max_workers(int width, int sms) {
   const int threads = norm_grad_threads(width < 4096 ? width : 4096);
-  const int stream = 1024 / threads > 1 ? 1024 / threads : 1, plain = width <= 2048 ? 8 : 2;
-  return (int64_t)sms * (stream > plain ? stream : plain);
+  return (int64_t)sms * (512 / threads > 1 ? 512 / threads : 1);
 }
 
 }  // namespace echo
