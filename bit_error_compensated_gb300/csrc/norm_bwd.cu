@@ -26,7 +26,7 @@
 namespace echo {
 namespace {
 
-constexpr int kMaxCluster = 8;         // ECHO_NORM_MAX_WIDTH / 2048
+constexpr int kMaxCluster = 4;         // ECHO_NORM_MAX_WIDTH / (8 * kStreamThreads)
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return (uint32_t)__cvta_generic_to_shared(p);
@@ -39,8 +39,7 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
 // past a row's warps stay 0).  Two sets of slots in turn, as a set is written
 // again only behind the next sum's barrier.
 constexpr int kStreamThreads = 512;
-constexpr int kStreamSlots = 64;       // 16 warps of one block, or 8 of each of 8
-static_assert(kStreamSlots >= kStreamThreads / 32 && kStreamSlots >= 8 * kMaxCluster, "a slot for every warp");
+constexpr int kStreamSlots = kStreamThreads / 32 * kMaxCluster;
 
 struct StreamSums {
   float (*slots)[3][kStreamSlots];     // [2]
@@ -87,13 +86,16 @@ struct StreamSums {
   }
 };
 
-// Rows ahead in the ring of asynchronous copies: 128 KB at 4096 columns.
-template <typename T> constexpr int rows_ahead() { return sizeof(T) == 2 ? 4 : 2; }
+// Rows ahead in the ring of asynchronous copies: 128 KB for a full block.  E:
+// elements of a row a thread has, 8 or 16.
+template <typename T, int E> constexpr int rows_ahead() { return 64 / (E * (int)sizeof(T)); }
+// Asynchronous copies take 16 bytes, or an fp32 element.
+template <typename T, int VEC> constexpr bool has_ring() { return VEC * sizeof(T) >= 4; }
 // 16-byte pieces of shared memory a thread has: the ring's (x, y, dr, dh) and
 // its columns' fp32 parameters (mul, w, and for layer norms add).
-template <typename T, int VEC, bool LAYER>
+template <typename T, int E, int VEC, bool LAYER>
 constexpr int grad_pieces() {
-  return (VEC == 1 ? 0 : rows_ahead<T>() * 4 * (8 * (int)sizeof(T) / 16)) + (LAYER ? 6 : 4);
+  return (has_ring<T, VEC>() ? rows_ahead<T, E>() * 4 * (E * (int)sizeof(T) / 16) : 0) + (LAYER ? 3 : 2) * (E / 4);
 }
 // Warps an SM: at 128 registers a thread.  (64 and twice the warps spill, and
 // take 143 us where this takes GRAD_US, 8192 x 4096 bf16.)
@@ -101,10 +103,11 @@ constexpr int kStreamWarps = 16;
 
 // GATE: 0 none, or one row for all; 1 a row of gates, 2 a gate, for each row
 // or several.
-template <typename T, int VEC, bool LAYER, bool POST, int GATE>
+template <typename T, int E, int VEC, bool LAYER, bool POST, int GATE>
 __global__ void __launch_bounds__(kStreamThreads, 1)
 norm_grad_kernel(const NormGradArgs a, int blocks, int block_cols) {
-  constexpr int NV = 8 / VEC, kAhead = VEC == 1 ? 1 : rows_ahead<T>();
+  constexpr int NV = E / VEC, kAhead = has_ring<T, VEC>() ? rows_ahead<T, E>() : 1;
+  constexpr bool RING = has_ring<T, VEC>();
   constexpr bool SUM0 = LAYER && POST;                  // sum D is needed (db_post, dgate)
   extern __shared__ __align__(16) uint8_t room[];
   __shared__ __align__(16) float slots[2][3][kStreamSlots];
@@ -130,9 +133,10 @@ norm_grad_kernel(const NormGradArgs a, int blocks, int block_cols) {
 
   const int64_t row0 = worker * a.span;
   const int64_t row1 = row0 + a.span < a.rows ? row0 + a.span : a.rows;
-  const uint32_t piece = 16u * all_threads;
-  const uint32_t mine = smem_u32(room) + 16u * me, slot_bytes = 4 * NV * piece;
-  const uint32_t params = VEC == 1 ? smem_u32(room) + 4u * me : mine + kAhead * slot_bytes;
+  constexpr uint32_t kBytes = VEC * sizeof(T);          // of a piece in the ring
+  const uint32_t piece = 16u * all_threads, ring_piece = kBytes * all_threads, slot_bytes = 4 * NV * ring_piece;
+  const uint32_t mine = smem_u32(room) + kBytes * me;
+  const uint32_t params = smem_u32(room) + (RING ? kAhead * slot_bytes : 0u) + (VEC == 1 ? 4u : 16u) * me;
   auto start = [&](const void* p, int64_t ld) {
     return static_cast<const char*>(p) + (row0 * ld + my_col) * (int64_t)sizeof(T);
   };
@@ -142,28 +146,33 @@ norm_grad_kernel(const NormGradArgs a, int blocks, int block_cols) {
                           a.ld_dh * (int64_t)sizeof(T)};
   // Whole pieces wait in the ring; single elements, which asynchronous copies
   // do not take, in registers.
-  T held[VEC == 1 ? 4 : 1][VEC == 1 ? NV : 1];
+  T held[RING ? 1 : 4][RING ? 1 : NV];
   int64_t fetch = row0;
   auto fetch_array = [&](int k, uint32_t slot) {
     if (fetch < row1 && there[k]) {
 #pragma unroll
       for (int j = 0; j < NV; ++j)
         if (in[j]) {
-          if constexpr (VEC == 1) held[k][j] = *reinterpret_cast<const T*>(from[k] + j * threads * (int)sizeof(T));
-          else copy16_async(mine + slot * slot_bytes + (4 * j + k) * piece, from[k] + 16 * j * threads);
+          const char* at = from[k] + j * threads * (int)kBytes;
+          const uint32_t to = mine + slot * slot_bytes + (4 * j + k) * ring_piece;
+          if constexpr (!RING) held[k][j] = *reinterpret_cast<const T*>(at);
+          else if constexpr (VEC == 1) copy4_async(to, at);
+          else copy16_async(to, at);
         }
     }
     from[k] += far[k];
   };
   auto take = [&](int k, int j, uint32_t slot, float (&v)[VEC]) {
-    if constexpr (VEC == 1) v[0] = to_float(held[k][j]);
-    else to_floats<T, VEC>(load_shared16<T, VEC>(mine + slot * slot_bytes + (4 * j + k) * piece), v);
+    const uint32_t at = mine + slot * slot_bytes + (4 * j + k) * ring_piece;
+    if constexpr (!RING) v[0] = to_float(held[k][j]);
+    else if constexpr (VEC == 1) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[0]) : "r"(at) : "memory");
+    else to_floats<T, VEC>(load_shared16<T, VEC>(at), v);
   };
 #pragma unroll
   for (int s = 0; s < kAhead; ++s) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) fetch_array(k, s);
-    if (VEC > 1) copies_commit();
+    if (RING) copies_commit();
     ++fetch;
   }
 
@@ -172,24 +181,24 @@ norm_grad_kernel(const NormGradArgs a, int blocks, int block_cols) {
   // and w of the norm of r.
   auto put = [&](int at, int j, const float (&v)[VEC]) {
     if constexpr (VEC == 1) {
-      asm volatile("st.shared.f32 [%0], %1;" :: "r"(params + (uint32_t)(at * 8 + j) * (piece / 4)), "f"(v[0]) : "memory");
+      asm volatile("st.shared.f32 [%0], %1;" :: "r"(params + (uint32_t)(at * E + j) * (piece / 4)), "f"(v[0]) : "memory");
     } else {
 #pragma unroll
       for (int i = 0; i < VEC; i += 4)
         asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};"
-                     :: "r"(params + (uint32_t)(at * 2 + j * (VEC / 4) + i / 4) * piece), "f"(v[i]), "f"(v[i + 1]),
+                     :: "r"(params + (uint32_t)(at * (E / 4) + j * (VEC / 4) + i / 4) * piece), "f"(v[i]), "f"(v[i + 1]),
                         "f"(v[i + 2]), "f"(v[i + 3]) : "memory");
     }
   };
   auto get = [&](int at, int j, float (&v)[VEC]) {
     if constexpr (VEC == 1) {
-      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[0]) : "r"(params + (uint32_t)(at * 8 + j) * (piece / 4)) : "memory");
+      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[0]) : "r"(params + (uint32_t)(at * E + j) * (piece / 4)) : "memory");
     } else {
 #pragma unroll
       for (int i = 0; i < VEC; i += 4)
         asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
                      : "=f"(v[i]), "=f"(v[i + 1]), "=f"(v[i + 2]), "=f"(v[i + 3])
-                     : "r"(params + (uint32_t)(at * 2 + j * (VEC / 4) + i / 4) * piece) : "memory");
+                     : "r"(params + (uint32_t)(at * (E / 4) + j * (VEC / 4) + i / 4) * piece) : "memory");
     }
   };
 #pragma unroll
@@ -262,7 +271,7 @@ norm_grad_kernel(const NormGradArgs a, int blocks, int block_cols) {
       load_param<T, 1>(a.gate, a.params_f32, gate_row, one);
       gate = one[0];
     }
-    if (VEC > 1) copies_wait<kAhead - 1>();
+    if (RING) copies_wait<kAhead - 1>();
     float hat1[NV][VEC], hat2[NV][VEC], g[NV][VEC];     // g: dh w, then f
     float s[LAYER ? 2 : 1] = {};
 #pragma unroll
@@ -322,7 +331,7 @@ norm_grad_kernel(const NormGradArgs a, int blocks, int block_cols) {
         for (int i = 0; i < VEC; ++i) g[j][i] = 0.f;
       }
     }
-    if (VEC == 1) {                     // what has been read makes room for the next row's
+    if (!RING) {                        // what has been read makes room for the next row's
       fetch_array(0, 0);
       fetch_array(1, 0);
       fetch_array(3, 0);
@@ -387,7 +396,7 @@ norm_grad_kernel(const NormGradArgs a, int blocks, int block_cols) {
         }
       }
     }
-    if (VEC == 1) {
+    if (!RING) {
       fetch_array(2, 0);
     } else {                            // this thread has read its pieces of the slot
 #pragma unroll
@@ -470,7 +479,7 @@ norm_grad_kernel(const NormGradArgs a, int blocks, int block_cols) {
       }
     }
   }
-  if (VEC > 1) copies_wait<0>();
+  if (RING) copies_wait<0>();
 
   if (worker < a.workers) {
 #pragma unroll
@@ -491,8 +500,9 @@ norm_grad_kernel(const NormGradArgs a, int blocks, int block_cols) {
 }
 
 // Adds the workers' column sums: blockIdx.y 0..3 a parameter each, 4 the gate
-// (with folded sums), or its rows that more than one worker shares.
-constexpr int kFinishRows = 32;
+// (with folded sums), or from 4 on its rows that more than one worker shares,
+// spread over the workers whose ranges begin inside one.
+constexpr int kFinishRows = 32, kMaxGateBlocks = 32;
 
 template <typename T>
 __global__ void __launch_bounds__(32 * kFinishRows)
@@ -545,12 +555,14 @@ norm_grad_finish(const NormGradArgs a) {
   if (!a.dgate || col >= cols) return;
   // Worker b's range begins inside a gate row that began in worker b - 1's:
   // that one's second slot and the first slots of all that follow are its sum.
-  for (int64_t b = 1 + threadIdx.y; b < a.workers; b += kFinishRows) {
+  for (int64_t b = 1 + threadIdx.y + (int64_t)kFinishRows * (which - 4); b < a.workers;
+       b += (int64_t)kFinishRows * (gridDim.y - 4)) {
     const int64_t g = b * a.span / a.gate_span, begin = g * a.gate_span, end = begin + a.gate_span;
     if (begin == b * a.span || begin < (b - 1) * a.span) continue;
+    const int64_t last = (end + a.span - 1) / a.span < a.workers ? (end + a.span - 1) / a.span : a.workers;
     float s = a.gate_partial[(2 * (b - 1) + 1) * cols + col];
-    for (int64_t w = b; w < a.workers && w * a.span < end; ++w)
-      s += a.gate_partial[2 * w * cols + col];
+#pragma unroll 8
+    for (int64_t w = b; w < last; ++w) s += a.gate_partial[2 * w * cols + col];
     put(a.dgate, g * cols + col, s);
   }
 }
@@ -561,7 +573,9 @@ cudaError_t launch_finish(const NormGradArgs& a, cudaStream_t s) {
   for (int k = 0; k < 4; ++k) any = any || a.dparam[k];
   if (!any) return cudaSuccess;
   cudaLaunchConfig_t fin = {};
-  fin.gridDim = dim3((unsigned)((a.width + 31) / 32), 5);
+  const int64_t gate_blocks = (a.workers + kFinishRows - 1) / kFinishRows;
+  fin.gridDim = dim3((unsigned)((a.width + 31) / 32),
+                     4 + (a.folded || !a.dgate ? 1 : (unsigned)(gate_blocks < kMaxGateBlocks ? gate_blocks : kMaxGateBlocks)));
   fin.blockDim = dim3(32, kFinishRows);
   fin.stream = s;
   cudaLaunchAttribute overlapped = overlapped_launch();
@@ -570,20 +584,18 @@ cudaError_t launch_finish(const NormGradArgs& a, cudaStream_t s) {
   return cudaLaunchKernelEx(&fin, norm_grad_finish<T>, a);
 }
 
-template <typename T, int VEC, bool LAYER, bool POST, int GATE>
+template <typename T, int E, int VEC, bool LAYER, bool POST, int GATE>
 cudaError_t launch_stream(NormGradArgs a, int sms, cudaStream_t s) {
-  // Past 4096 columns, blocks of 2048: two clusters an SM, so that one works
-  // while the other's barrier is on its way.
-  const int blocks = a.width <= 8 * kStreamThreads ? 1 : (a.width + 2047) / 2048;
+  const int blocks = (a.width + E * kStreamThreads - 1) / (E * kStreamThreads);
   const int block_cols = ((a.width + blocks - 1) / blocks + 7) / 8 * 8;
-  const int threads = norm_grad_threads(block_cols);
+  const int threads = norm_grad_threads(block_cols, E);
   const int rows = threads < 128 ? 128 / threads : 1;
-  const int smem = grad_pieces<T, VEC, LAYER>() * 16 * threads * rows;
+  const int smem = grad_pieces<T, E, VEC, LAYER>() * 16 * threads * rows;
   static OncePerDevice prepared;
   cudaError_t e = prepared.run([] {
-    return cudaFuncSetAttribute(norm_grad_kernel<T, VEC, LAYER, POST, GATE>,
+    return cudaFuncSetAttribute(norm_grad_kernel<T, E, VEC, LAYER, POST, GATE>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                grad_pieces<T, VEC, LAYER>() * 16 * kStreamThreads);
+                                grad_pieces<T, E, VEC, LAYER>() * 16 * kStreamThreads);
   });
   if (e != cudaSuccess) return e;
   int at_once = kStreamWarps * 32 / (threads * rows);          // by registers; by shared memory
@@ -606,21 +618,22 @@ cudaError_t launch_stream(NormGradArgs a, int sms, cudaStream_t s) {
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = blocks > 1 ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, norm_grad_kernel<T, VEC, LAYER, POST, GATE>, a, blocks, block_cols);
+  e = cudaLaunchKernelEx(&cfg, norm_grad_kernel<T, E, VEC, LAYER, POST, GATE>, a, blocks, block_cols);
   return e != cudaSuccess ? e : launch_finish<T>(a, s);
 }
 
-template <typename T, int VEC, bool LAYER, bool POST>
+template <typename T, int E, int VEC, bool LAYER, bool POST>
 cudaError_t pick_gate(const NormGradArgs& a, int sms, cudaStream_t s) {
-  if (!a.gate || (!a.gate_scalar && a.gate_span >= a.rows)) return launch_stream<T, VEC, LAYER, POST, 0>(a, sms, s);
-  return a.gate_scalar ? launch_stream<T, VEC, LAYER, POST, 2>(a, sms, s)
-                       : launch_stream<T, VEC, LAYER, POST, 1>(a, sms, s);
+  if (!a.gate || (!a.gate_scalar && a.gate_span >= a.rows))
+    return launch_stream<T, E, VEC, LAYER, POST, 0>(a, sms, s);
+  return a.gate_scalar ? launch_stream<T, E, VEC, LAYER, POST, 2>(a, sms, s)
+                       : launch_stream<T, E, VEC, LAYER, POST, 1>(a, sms, s);
 }
 
-template <typename T, int VEC>
+template <typename T, int E, int VEC>
 cudaError_t pick_norm(const NormGradArgs& a, int layer, int sms, cudaStream_t s) {
-  if (layer) return a.post ? pick_gate<T, VEC, true, true>(a, sms, s) : pick_gate<T, VEC, true, false>(a, sms, s);
-  return a.post ? pick_gate<T, VEC, false, true>(a, sms, s) : pick_gate<T, VEC, false, false>(a, sms, s);
+  if (layer) return a.post ? pick_gate<T, E, VEC, true, true>(a, sms, s) : pick_gate<T, E, VEC, true, false>(a, sms, s);
+  return a.post ? pick_gate<T, E, VEC, false, true>(a, sms, s) : pick_gate<T, E, VEC, false, false>(a, sms, s);
 }
 
 }  // namespace
@@ -628,7 +641,13 @@ cudaError_t pick_norm(const NormGradArgs& a, int layer, int sms, cudaStream_t s)
 template <>
 cudaError_t launch_norm_grad<ECHO_ELEM>(NormGradArgs a, int layer, bool vec, int sms, cudaStream_t s) {
   using T = ECHO_ELEM;
-  return vec ? pick_norm<T, 16 / sizeof(T)>(a, layer, sms, s) : pick_norm<T, 1>(a, layer, sms, s);
+  constexpr int V = 16 / sizeof(T);
+  // 16 elements a thread leave no registers to spare, but a cluster's barrier
+  // costs more: it waits for the copies and stores in flight, microseconds a
+  // row (4096 x 8192 bf16 as clusters of two 176 us, as one block W8192_US).
+  // Single elements need more registers still, and take the cluster.
+  if (!vec) return pick_norm<T, 8, 1>(a, layer, sms, s);
+  return a.width <= 8 * kStreamThreads ? pick_norm<T, 8, V>(a, layer, sms, s) : pick_norm<T, 16, V>(a, layer, sms, s);
 }
 
 }  // namespace echo

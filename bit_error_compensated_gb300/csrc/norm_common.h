@@ -73,12 +73,13 @@ template <typename T>
 cudaError_t launch_norm(const NormArgs& a, int layer, bool vec, int sms, cudaStream_t s);
 template <typename T>
 cudaError_t launch_norm_grad(NormGradArgs a, int layer, bool vec, int sms, cudaStream_t s);
-// Threads that the backward kernel gives a row of `cols` columns of a block.
-inline int norm_grad_threads(int cols) { return ((cols + 7) / 8 + 31) / 32 * 32; }
+// Threads that the backward kernel gives a row of `cols` columns of a block, at
+// `each` elements a thread.
+inline int norm_grad_threads(int cols, int each) { return ((cols + each - 1) / each + 31) / 32 * 32; }
 // Workers (row ranges with their own partial sums) a backward call may have at
 // most: 16 warps an SM.
 inline int64_t norm_grad_max_workers(int width, int sms) {
-  const int threads = norm_grad_threads(width < 4096 ? width : 4096);
+  const int threads = width <= 4096 ? norm_grad_threads(width, 8) : 256;
   return (int64_t)sms * (512 / threads > 1 ? 512 / threads : 1);
 }
 
