@@ -103,11 +103,11 @@ int check_product(int64_t ranks, int64_t tokens, int64_t channels, int64_t depth
   return clear_of(out, ranks, tokens, channels, size, in, n) ? ECHO_OK : ECHO_ERR_ARG;
 }
 
-int check_workspace(int64_t ranks, int64_t tokens, int64_t depth, const void* workspace, size_t bytes) {
-  const size_t need = product_workspace(ranks, tokens, depth);
+int check_workspace(const ProductArgs& p, size_t bytes) {
+  const size_t need = product_workspace(p).bytes();
   if (need == 0) return ECHO_OK;
-  if (workspace == nullptr || bytes < need) return ECHO_ERR_TOO_LARGE;
-  return on_boundary(workspace, 16) ? ECHO_OK : ECHO_ERR_ALIGN;
+  if (p.wide == nullptr || bytes < need) return ECHO_ERR_TOO_LARGE;
+  return on_boundary(p.wide, 16) ? ECHO_OK : ECHO_ERR_ALIGN;
 }
 
 QuantArgs quant_args(int64_t ranks, int64_t tokens, int64_t depth, const echo_matrix* x,
@@ -164,15 +164,19 @@ int echo_matmul_int8(int64_t ranks, int64_t tokens, int64_t channels, int64_t de
   ECHO_TRY(check_product(ranks, tokens, channels, depth, a, a_scales, a_scale_stride, w, w_scales,
                          w_scale_stride, out_dtype, out));
   if (tokens == 0 || channels == 0) return ECHO_OK;
-  ECHO_TRY(check_workspace(a->rank_stride == 0 ? 1 : ranks, tokens, depth, workspace, workspace_bytes));
-  ECHO_OPS_CUDA(launch_product(product_args(ranks, tokens, channels, depth, a, a_scales, a_scale_stride, w,
-                                            w_scales, w_scale_stride, out_dtype, out, workspace),
-                               false, static_cast<cudaStream_t>(stream)));
+  const ProductArgs p = product_args(ranks, tokens, channels, depth, a, a_scales, a_scale_stride, w, w_scales,
+                                     w_scale_stride, out_dtype, out, workspace);
+  ECHO_TRY(check_workspace(p, workspace_bytes));
+  ECHO_OPS_CUDA(launch_product(p, false, static_cast<cudaStream_t>(stream)));
   return ECHO_OK;
 }
 
-size_t echo_matmul_workspace_bytes(int64_t ranks, int64_t tokens, int64_t depth) {
-  return check_sizes(ranks, tokens, 0, depth) == ECHO_OK ? product_workspace(ranks, tokens, depth) : 0;
+size_t echo_matmul_workspace_bytes(int64_t ranks, int64_t tokens, int64_t channels, int64_t depth,
+                                   const echo_matrix* a, const echo_matrix* w) {
+  if (check_sizes(ranks, tokens, channels, depth) != ECHO_OK || a == nullptr || w == nullptr) return 0;
+  const echo_matrix none = {nullptr, 0, 0};
+  return product_workspace(product_args(ranks, tokens, channels, depth, a, nullptr, 0, w, nullptr, 0, ECHO_F32,
+                                        &none, nullptr)).bytes();
 }
 
 int echo_matmul_status(void* stream, int* status) {
@@ -208,14 +212,14 @@ int echo_linear_int8(int64_t ranks, int64_t tokens, int64_t channels, int64_t de
     for (int i = 0; i < n; ++i)
       if (overlaps(scales, given[i])) return ECHO_ERR_ARG;
   }
-  const bool many = channels > 0 && product_workspace(ranks, tokens, depth) > 0;
-  if (many) ECHO_TRY(check_workspace(ranks, tokens, depth, workspace, workspace_bytes));
+  const ProductArgs p = product_args(ranks, tokens, channels, depth, codes, a_scales, tokens, w, w_scales,
+                                     w_scale_stride, dtype, out, workspace);
+  ECHO_TRY(check_workspace(p, workspace_bytes));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool many = product_workspace(p).tokens > 0;
   ECHO_OPS_CUDA(launch_quantize(quant_args(ranks, tokens, depth, x, codes, a_scales, many ? workspace : nullptr),
                                 dtype, s));
-  if (channels == 0) return ECHO_OK;
-  ECHO_OPS_CUDA(launch_product(product_args(ranks, tokens, channels, depth, codes, a_scales, tokens, w,
-                                            w_scales, w_scale_stride, dtype, out, workspace), true, s));
+  if (channels > 0) ECHO_OPS_CUDA(launch_product(p, true, s));
   return ECHO_OK;
 }
 

@@ -29,7 +29,7 @@ struct ProductArgs {
   int64_t ld_out, rank_out;
   int64_t ranks, tokens, channels, depth;
   int out_dtype;
-  uint8_t* wide;                 // the tokens' codes as f16 (int8_load.h): many tokens only
+  uint8_t* wide;                 // workspace: the tokens' codes as f16 (int8_load.h), many tokens only
 };
 
 // Products of more tokens than this run in tiles (int8_pair.cu), from f16
@@ -37,7 +37,17 @@ struct ProductArgs {
 constexpr int64_t kFewTokens = 64;
 // Ranks of the tokens' codes: one where all share them.
 inline int64_t token_ranks(const ProductArgs& p) { return p.rank_a == 0 ? 1 : p.ranks; }
-size_t product_workspace(int64_t ranks, int64_t tokens, int64_t depth);
+// Whether a matrix' rows of codes all start on 16-byte boundaries.
+inline bool rows_aligned(const void* data, int64_t ld, int64_t rank_stride, int64_t rows, int64_t ranks) {
+  return on_boundary(data, 16) && (rows == 1 || ld % 16 == 0) && (ranks == 1 || rank_stride % 16 == 0);
+}
+// The workspace of a product of many tokens: their f16 codes, then a copy of
+// the channels' codes if their rows are not aligned (TMA takes no others).
+struct Workspace {
+  size_t tokens = 0, channels = 0;
+  size_t bytes() const { return tokens + channels; }
+};
+Workspace product_workspace(const ProductArgs& p);
 
 // The value of an exact sum: fp32 products by the token's, then the channel's
 // scale, in this order everywhere, so that every kernel gives the same bits.
@@ -45,16 +55,16 @@ __device__ __forceinline__ float scaled_sum(int sum, float token, float channel)
   return __fmul_rn(__fmul_rn(__int2float_rn(sum), token), channel);
 }
 
-// What a call's addresses and distances allow.
 struct ProductLayout {
-  bool aligned;                  // rows of codes start on 16-byte boundaries
-  bool wide;                     // rows of out do
+  bool wide;                     // rows of out start on 16-byte boundaries
   int sms;
 };
 
 cudaError_t launch_quantize(const QuantArgs& a, int dtype, cudaStream_t s);
 // The f16 codes of tokens that are in int8 already.
-cudaError_t launch_widen(const ProductArgs& p, bool aligned, cudaStream_t s);
+cudaError_t launch_widen(const ProductArgs& p, cudaStream_t s);
+// Copies the channels' codes to rows of `ld` bytes, aligned, rank after rank.
+cudaError_t launch_realign(const ProductArgs& p, int8_t* to, int64_t ld, cudaStream_t s);
 // `quantized`: this call's quantizer ran just before, and has left the tokens'
 // f16 codes in the workspace where the product needs them.
 cudaError_t launch_product(const ProductArgs& a, bool quantized, cudaStream_t s);

@@ -188,7 +188,7 @@ __device__ __forceinline__ void store_results(const ProductArgs& p, int64_t rank
   }
 }
 
-template <typename T, int BN, bool ALIGNED>
+template <typename T, int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide_out,
                     const __grid_constant__ CUtensorMap codes_map) {
@@ -313,7 +313,7 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide_out,
         wait_on(landed + 8 * slot, phase, &give_up);
         give_up = 1;
       }
-    } else if (ALIGNED && warp == kIssuer + 2 && lane == 0) {
+    } else if (warp == kIssuer + 2 && lane == 0) {
       // The channels' copies, a slot for each group of turners.
       int64_t g = 0;
       bool ok = true;
@@ -352,27 +352,16 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide_out,
     int stage = group;
     bool ok = true;
     for (int tile = pair; tile < tiles.total && ok; tile += pairs, stage -= stages) {
-      const Place at = place_of(tiles, tile);
       for (; stage < stages; stage += kGroups) {
         uint4 held[kPieces];
-        if (ALIGNED) {
-          ok = __all_sync(0xFFFFFFFFu, wait_on(codes_full + 8 * group, codes_phase, &give_up));
-          if (!ok) break;
-          codes_phase ^= 1;
+        ok = __all_sync(0xFFFFFFFFu, wait_on(codes_full + 8 * group, codes_phase, &give_up));
+        if (!ok) break;
+        codes_phase ^= 1;
 #pragma unroll
-          for (int i = 0; i < kPieces; ++i)             // two pieces of each eighth row
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(held[i].x), "=r"(held[i].y), "=r"(held[i].z), "=r"(held[i].w)
-                         : "r"((i & 1 ? from1 : from0) + (i >> 1) * 1024) : "memory");
-        } else {
-#pragma unroll
-          for (int i = 0; i < kPieces; ++i) {           // rows past the last repeat it: dropped
-            const int64_t c = (int64_t)at.col * BN + half * (BN / 2) + r0 + 8 * (i >> 1);
-            const int8_t* row = p.w + at.rank * p.rank_w + (c < p.channels ? c : p.channels - 1) * p.ld_w;
-            const int64_t k = (int64_t)stage * kStageDepth + 16 * (seg0 + 4 * (i & 1));
-            held[i] = k < p.depth ? load_codes<false>(row, k, p.depth) : make_uint4(0, 0, 0, 0);
-          }
-        }
+        for (int i = 0; i < kPieces; ++i)               // two pieces of each eighth row
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(held[i].x), "=r"(held[i].y), "=r"(held[i].z), "=r"(held[i].w)
+                       : "r"((i & 1 ? from1 : from0) + (i >> 1) * 1024) : "memory");
         ok = __all_sync(0xFFFFFFFFu, wait_on(empty + 8 * slot, phase ^ 1u, &give_up));
         if (!ok) break;
         const uint32_t base = ring + slot * stage_bytes<BN>() + put;
@@ -390,10 +379,8 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide_out,
                        :: "r"(to ^ 16u), "r"(h[4]), "r"(h[5]), "r"(h[6]), "r"(h[7]) : "memory");
         }
         fence_proxy_async();
-        if (ALIGNED) {                  // only now: a copy can overtake loads that no one has used yet
-          __syncwarp();
-          if (lane == 0) arrive_here(codes_free + 8 * group);
-        }
+        __syncwarp();                   // only now: a copy can overtake loads that no one has used yet
+        if (lane == 0) arrive_here(codes_free + 8 * group);
         if (warp % kGroupWarps == 0)    // one warp vouches for the tokens' copy too
           ok = __all_sync(0xFFFFFFFFu, wait_on(landed + 8 * slot, phase, &give_up));
         if (!ok) break;
@@ -491,16 +478,16 @@ cudaError_t channels_map(const ProductArgs& p, CUtensorMap* map) {
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <typename T, int BN, bool ALIGNED>
+template <typename T, int BN>
 cudaError_t launch(const ProductArgs& p, const ProductLayout& l, cudaStream_t s) {
   static OncePerDevice prepared;
   cudaError_t e = prepared.run([] {
-    return cudaFuncSetAttribute(product_pair_kernel<T, BN, ALIGNED>,
+    return cudaFuncSetAttribute(product_pair_kernel<T, BN>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<BN>());
   });
   if (e != cudaSuccess) return e;
   CUtensorMap map = {};
-  if (ALIGNED && (e = channels_map<BN>(p, &map)) != cudaSuccess) return e;
+  if ((e = channels_map<BN>(p, &map)) != cudaSuccess) return e;
   Tiles t;
   t.rows = (int)((p.tokens + 255) / 256);
   t.cols = (int)((p.channels + BN - 1) / BN);
@@ -516,14 +503,14 @@ cudaError_t launch(const ProductArgs& p, const ProductLayout& l, cudaStream_t s)
   cudaLaunchAttribute overlapped = overlapped_launch();
   cfg.attrs = &overlapped;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, product_pair_kernel<T, BN, ALIGNED>, p, t, (int)l.wide, map);
+  return cudaLaunchKernelEx(&cfg, product_pair_kernel<T, BN>, p, t, (int)l.wide, map);
 }
 
 }  // namespace
 
 template <>
 cudaError_t launch_pair<ECHO_ELEM>(const ProductArgs& p, const ProductLayout& l, cudaStream_t s) {
-  return l.aligned ? launch<ECHO_ELEM, 256, true>(p, l, s) : launch<ECHO_ELEM, 256, false>(p, l, s);
+  return launch<ECHO_ELEM, 256>(p, l, s);
 }
 
 template <>

@@ -3,23 +3,35 @@
 
 namespace echo {
 
-size_t product_workspace(int64_t ranks, int64_t tokens, int64_t depth) {
-  if (tokens <= kFewTokens || depth == 0) return 0;
-  return (size_t)(ranks * wide_blocks(tokens) * wide_blocks(depth)) * kBlockBytes;
+Workspace product_workspace(const ProductArgs& p) {
+  Workspace w;
+  if (p.tokens <= kFewTokens || p.depth == 0 || p.channels == 0) return w;
+  w.tokens = (size_t)(token_ranks(p) * wide_blocks(p.tokens) * wide_blocks(p.depth)) * kBlockBytes;
+  if (!rows_aligned(p.w, p.ld_w, p.rank_w, p.channels, p.ranks))
+    w.channels = (size_t)((p.rank_w == 0 ? 1 : p.ranks) * p.channels) * (size_t)((p.depth + 15) / 16 * 16);
+  return w;
 }
 
-cudaError_t launch_product(const ProductArgs& p, bool quantized, cudaStream_t s) {
+cudaError_t launch_product(const ProductArgs& given, bool quantized, cudaStream_t s) {
+  ProductArgs p = given;
   ProductLayout l;
   cudaError_t e = device_sms(&l.sms);
   if (e != cudaSuccess) return e;
+  const bool w_aligned = rows_aligned(p.w, p.ld_w, p.rank_w, p.channels, p.ranks);
+  if (p.tokens <= kFewTokens || p.depth == 0)
+    return launch_few(p, w_aligned && rows_aligned(p.a, p.ld_a, p.rank_a, p.tokens, p.ranks), quantized, s);
   const int64_t size = elem_size(p.out_dtype);
-  l.aligned = on_boundary(p.a, 16) && on_boundary(p.w, 16) && (p.tokens == 1 || p.ld_a % 16 == 0) &&
-              (p.channels == 1 || p.ld_w % 16 == 0) &&
-              (p.ranks == 1 || (p.rank_a % 16 == 0 && p.rank_w % 16 == 0));
   l.wide = on_boundary(p.out, 16) && (p.tokens == 1 || p.ld_out * size % 16 == 0) &&
            (p.ranks == 1 || p.rank_out * size % 16 == 0);
-  if (p.tokens <= kFewTokens || p.depth == 0) return launch_few(p, l.aligned, quantized, s);
-  if (!quantized && (e = launch_widen(p, l.aligned, s)) != cudaSuccess) return e;
+  if (!quantized && (e = launch_widen(p, s)) != cudaSuccess) return e;
+  if (!w_aligned) {
+    int8_t* copy = reinterpret_cast<int8_t*>(p.wide + product_workspace(given).tokens);
+    const int64_t ld = (p.depth + 15) / 16 * 16;
+    if ((e = launch_realign(p, copy, ld, s)) != cudaSuccess) return e;
+    p.w = copy;
+    p.ld_w = ld;
+    if (p.rank_w != 0) p.rank_w = p.channels * ld;
+  }
   return p.out_dtype == ECHO_F32    ? launch_pair<float>(p, l, s)
          : p.out_dtype == ECHO_BF16 ? launch_pair<__nv_bfloat16>(p, l, s) : launch_pair<__half>(p, l, s);
 }

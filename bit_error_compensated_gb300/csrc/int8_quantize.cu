@@ -97,6 +97,19 @@ widen_kernel(const ProductArgs p) {
   *reinterpret_cast<uint4*>(base + wide_offset(rank, token, k + 8, p.tokens, p.depth)) = make_uint4(h[4], h[5], h[6], h[7]);
 }
 
+// Channels' codes into rows that start on 16-byte boundaries, a thread 16 of a row.
+__global__ void __launch_bounds__(256)
+realign_kernel(const ProductArgs p, int8_t* to, int64_t ld) {
+  pdl_wait();
+  pdl_trigger();
+  const int64_t pieces = ld / 16, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t row = i / pieces, k = (i - row * pieces) * 16;
+  const int64_t rank = row / p.channels, channel = row - rank * p.channels;
+  if (rank >= (p.rank_w == 0 ? 1 : p.ranks)) return;
+  *reinterpret_cast<uint4*>(to + row * ld + k) =
+      load_codes<false>(p.w + rank * p.rank_w + channel * p.ld_w, k, p.depth);
+}
+
 template <typename T, int VEC>
 cudaError_t launch(const QuantArgs& a, cudaStream_t s) {
   int64_t threads = (a.depth + 2 * VEC - 1) / (2 * VEC);
@@ -123,7 +136,7 @@ cudaError_t pick(const QuantArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_widen(const ProductArgs& p, bool aligned, cudaStream_t s) {
+cudaError_t launch_widen(const ProductArgs& p, cudaStream_t s) {
   const int64_t pieces = token_ranks(p) * p.tokens * wide_blocks(p.depth) * (kBlockCodes / 16);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((pieces + 255) / 256));
@@ -132,7 +145,20 @@ cudaError_t launch_widen(const ProductArgs& p, bool aligned, cudaStream_t s) {
   cudaLaunchAttribute overlapped = overlapped_launch();
   cfg.attrs = &overlapped;
   cfg.numAttrs = 1;
-  return aligned ? cudaLaunchKernelEx(&cfg, widen_kernel<true>, p) : cudaLaunchKernelEx(&cfg, widen_kernel<false>, p);
+  return rows_aligned(p.a, p.ld_a, p.rank_a, p.tokens, p.ranks) ? cudaLaunchKernelEx(&cfg, widen_kernel<true>, p)
+                                                                : cudaLaunchKernelEx(&cfg, widen_kernel<false>, p);
+}
+
+cudaError_t launch_realign(const ProductArgs& p, int8_t* to, int64_t ld, cudaStream_t s) {
+  const int64_t pieces = (p.rank_w == 0 ? 1 : p.ranks) * p.channels * (ld / 16);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((pieces + 255) / 256));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute overlapped = overlapped_launch();
+  cfg.attrs = &overlapped;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, realign_kernel, p, to, ld);
 }
 
 cudaError_t launch_quantize(const QuantArgs& a, int dtype, cudaStream_t s) {

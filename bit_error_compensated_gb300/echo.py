@@ -89,7 +89,7 @@ _SIGS = {
     "echo_quantize_tokens": (_i32, [_i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp]),
     "echo_matmul_int8": (_i32, [_i64, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _i32, _vp,
                                 _vp, _sz, _vp]),
-    "echo_matmul_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "echo_matmul_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _vp, _vp]),
     "echo_matmul_status": (_i32, [_vp, ctypes.POINTER(_i32)]),
     "echo_linear_int8": (_i32, [_i64, _i64, _i64, _i64, _i32, _vp, _vp, _vp, _i64, _vp, _vp, _vp,
                                 _vp, _sz, _vp]),
@@ -583,12 +583,11 @@ def _check_product(tokens_of, what: str, dtype, scales, w, w_scales, out, device
     return ranks, tokens, channels, depth
 
 
-def _workspace(ranks: int, tokens: int, depth: int, device, stream) -> tuple:
-    """(tensor or None, address, bytes) of a product's workspace, from torch's
+def _workspace(nbytes: int, device, stream) -> tuple:
+    """(tensor or None, address) of a product's workspace, from torch's
     allocator: ordered by the stream that the call runs on."""
-    nbytes = _lib.echo_matmul_workspace_bytes(ranks, tokens, depth)
     if nbytes == 0:
-        return None, None, 0
+        return None, None
     import torch
     buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
     if stream is not None:
@@ -597,11 +596,12 @@ def _workspace(ranks: int, tokens: int, depth: int, device, stream) -> tuple:
         if stream != torch.cuda.current_stream():
             stream.wait_stream(torch.cuda.current_stream())   # the memory's last use lies on this one
             buf.record_stream(stream)
-    return buf, buf.data_ptr(), nbytes
+    return buf, buf.data_ptr()
 
 
-def echo_matmul_workspace_bytes(ranks: int, tokens: int, depth: int) -> int:
-    return int(_lib.echo_matmul_workspace_bytes(ranks, tokens, depth))
+def echo_matmul_workspace_bytes(ranks: int, tokens: int, channels: int, depth: int, codes, w) -> int:
+    """codes, w: the tensors of the call."""
+    return int(_lib.echo_matmul_workspace_bytes(ranks, tokens, channels, depth, _matrix(codes), _matrix(w)))
 
 
 def echo_quantize_tokens(x, codes, scales, stream=None) -> None:
@@ -628,13 +628,13 @@ def echo_matmul_int8(codes, scales, w, w_scales, out, stream=None) -> None:
     import torch
     device = _call_device(out)
     ranks, tokens, channels, depth = _check_product(codes, "codes", torch.int8, scales, w, w_scales, out, device)
-    stride = codes.stride()
-    own = len(stride) == 3               # each rank has its own tokens, unless they are expanded
-    keep, at, nbytes = (None, None, 0)
+    a, wm = _matrix(codes), _matrix(w)
+    keep, at, nbytes = None, None, 0
     if tokens > _FEW_TOKENS:
-        keep, at, nbytes = _workspace(ranks if own and stride[0] else 1, tokens, depth, out.device, stream)
-    status = _lib.echo_matmul_int8(ranks, tokens, channels, depth, _matrix(codes), scales.data_ptr(),
-                                   tokens if own else 0, _matrix(w), w_scales.data_ptr(),
+        nbytes = _lib.echo_matmul_workspace_bytes(ranks, tokens, channels, depth, a, wm)
+        keep, at = _workspace(nbytes, out.device, stream)
+    status = _lib.echo_matmul_int8(ranks, tokens, channels, depth, a, scales.data_ptr(),
+                                   tokens if len(codes.shape) == 3 else 0, wm, w_scales.data_ptr(),
                                    w_scales.stride()[0] if len(w_scales.shape) == 2 else 0,
                                    _dtype_code(out.dtype), _matrix(out), at, nbytes, _stream(stream))
     if status:
@@ -658,13 +658,15 @@ def echo_linear_int8(x, w, w_scales, out, codes, scales, stream=None) -> None:
     if len(shape) != len(out.shape):
         raise ValueError(f"x: shape {tuple(shape)}, expected the {len(out.shape)} dimensions of out")
     _expect(x, "x", out.dtype, codes.shape, device)
-    keep, at, nbytes = (None, None, 0)
+    a, wm = _matrix(codes), _matrix(w)
+    keep, at, nbytes = None, None, 0
     if tokens > _FEW_TOKENS:
-        keep, at, nbytes = _workspace(ranks, tokens, depth, out.device, stream)
-    status = _lib.echo_linear_int8(ranks, tokens, channels, depth, _dtype_code(x.dtype), _matrix(x), _matrix(w),
+        nbytes = _lib.echo_matmul_workspace_bytes(ranks, tokens, channels, depth, a, wm)
+        keep, at = _workspace(nbytes, out.device, stream)
+    status = _lib.echo_linear_int8(ranks, tokens, channels, depth, _dtype_code(x.dtype), _matrix(x), wm,
                                    w_scales.data_ptr(),
                                    w_scales.stride()[0] if len(w_scales.shape) == 2 else 0,
-                                   _matrix(codes), scales.data_ptr(), _matrix(out), at, nbytes, _stream(stream))
+                                   a, scales.data_ptr(), _matrix(out), at, nbytes, _stream(stream))
     if status:
         raise EchoError(status, "echo_linear_int8")
 

@@ -537,11 +537,14 @@ int echo_matmul_int8(int64_t ranks, int64_t tokens, int64_t channels, int64_t de
 
 /*
  * echo_matmul_workspace_bytes -- bytes of the device workspace that
- * echo_matmul_int8 and echo_linear_int8 need for these sizes (2 a code of the
- * tokens, whose f16 forms it holds during the call, rows and columns rounded
- * up to 128; 0 for few tokens).  Ranks that share their tokens count as one.
+ * echo_matmul_int8 (of a) and echo_linear_int8 (a: its codes) need: for more
+ * than 64 tokens 2 a code of theirs, whose f16 forms it holds during the call
+ * (rows and columns rounded up to 128, ranks that share their tokens once),
+ * and 1 a code of w (depth rounded up to 16) if the rows of w do not all start
+ * on 16-byte boundaries.  0 for fewer tokens, or sizes that the calls refuse.
  */
-size_t echo_matmul_workspace_bytes(int64_t ranks, int64_t tokens, int64_t depth);
+size_t echo_matmul_workspace_bytes(int64_t ranks, int64_t tokens, int64_t channels, int64_t depth,
+                                   const echo_matrix* a, const echo_matrix* w);
 
 /*
  * echo_matmul_status -- read and clear the current device's status word of the
