@@ -34,7 +34,7 @@ struct ProductArgs {
 
 // Products of more tokens than this run in tiles (int8_pair.cu), from f16
 // codes in a workspace.
-constexpr int64_t kFewTokens = 64;
+constexpr int64_t kFewTokens = 32;
 // Ranks of the tokens' codes: one where all share them.
 inline int64_t token_ranks(const ProductArgs& p) { return p.rank_a == 0 ? 1 : p.ranks; }
 // Whether a matrix' rows of codes all start on 16-byte boundaries.

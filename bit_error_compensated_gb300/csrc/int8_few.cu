@@ -1,6 +1,6 @@
 // int8_few.cu -- echo_matmul_int8 for few tokens (include/echo.h): decode.
 //
-// The channels' codes are read once per 64 tokens and everything else is
+// The channels' codes are read once (per 32 tokens) and everything else is
 // small, so the kernel streams them: a block takes 16 (or 32) channels, its
 // warps take windows of 64 codes in turn, and each thread's 16-byte loads go
 // straight into the operand registers of a matrix instruction.  (A sum does
@@ -191,8 +191,7 @@ cudaError_t launch(const ProductArgs& p, bool aligned, bool early, cudaStream_t 
 cudaError_t launch_few(const ProductArgs& p, bool aligned, bool early, cudaStream_t s) {
   if (p.tokens <= 8) return launch<1, 1, 4>(p, aligned, early, s);
   if (p.tokens <= 16) return launch<2, 1, 4>(p, aligned, early, s);
-  if (p.tokens <= 32) return launch<4, 2, 2>(p, aligned, early, s);
-  return launch<8, 2, 2>(p, aligned, early, s);
+  return launch<4, 2, 2>(p, aligned, early, s);
 }
 
 }  // namespace echo

@@ -25,6 +25,11 @@
 // of int8 codes written and read, 32 KB of their f16 written and read): 1280
 // cycles at 128 bytes a cycle, for 1024 of matrix instructions.
 //
+// Where there are fewer tiles than pairs of SMs, SPLIT pairs in a cluster share
+// a tile's depth.  Their sums are int32, so their order does not matter: each
+// pair writes those of the columns that it does not own into the owner's
+// shared memory (the ring is free by then), and the owner adds and stores.
+//
 // Every wait is bounded; one that gives up ends the call with a status
 // (echo_matmul_status).
 #include <cuda.h>
@@ -113,19 +118,19 @@ __device__ __forceinline__ void arrive_here(uint32_t bar) {
 // memory, which this SM's own matrix unit reads and the proxy fence before the
 // arrival has made visible to it; copies that have landed there; and loads
 // from TMEM that have returned.
-__device__ __forceinline__ void arrive_first(uint32_t bar) {
+__device__ __forceinline__ void arrive_first(uint32_t bar, uint32_t first_rank) {
   asm volatile(
       "{\n\t.reg .b32 at;\n\t"
-      "mapa.shared::cluster.u32 at, %0, 0;\n\t"
+      "mapa.shared::cluster.u32 at, %0, %1;\n\t"
       "mbarrier.arrive.shared::cluster.b64 _, [at];\n\t}"
-      :: "r"(bar) : "memory");
+      :: "r"(bar), "r"(first_rank) : "memory");
 }
 
 // All matrix instructions issued so far will arrive on `bar` of both blocks.
-__device__ __forceinline__ void commit_pair(uint32_t bar) {
+__device__ __forceinline__ void commit_pair(uint32_t bar, uint32_t first_rank) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-      " [%0], %1;" :: "r"(bar), "h"((uint16_t)3) : "memory");
+      " [%0], %1;" :: "r"(bar), "h"((uint16_t)(3u << first_rank)) : "memory");
 }
 
 __device__ __forceinline__ bool elect_one() {
@@ -188,8 +193,8 @@ __device__ __forceinline__ void store_results(const ProductArgs& p, int64_t rank
   }
 }
 
-template <typename T, int BN>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+template <typename T, int BN, int SPLIT>
+__global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(kThreads, 1)
 product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide_out,
                     const __grid_constant__ CUtensorMap codes_map) {
   constexpr int kCols = BN / 2;                         // of a chunk's sums, a taker's
@@ -205,8 +210,12 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide_out,
                  sums_full = codes_free + 8 * kGroups, sums_empty = sums_full + 16, last = sums_empty + 16;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int half = (int)(blockIdx.x & 1);               // of the pair
-  const int pair = (int)(blockIdx.x >> 1), pairs = (int)(gridDim.x >> 1);
-  const int stages = (int)wide_blocks(p.depth);         // of a tile
+  const int split = SPLIT == 1 ? 0 : (int)(blockIdx.x >> 1) % SPLIT;      // of the tile's depth, this pair's
+  const uint32_t first_rank = 2 * split;                // in the cluster, of the pair's first block
+  const int pair = (int)(blockIdx.x / (2 * SPLIT)), pairs = (int)(gridDim.x / (2 * SPLIT));   // (or cluster)
+  const int tile_stages = (int)wide_blocks(p.depth);    // at least SPLIT
+  const int first_stage = tile_stages * split / SPLIT;  // of a tile, this pair's
+  const int stages = tile_stages * (split + 1) / SPLIT - first_stage;
   const int least = (stages + kChunkStages - 1) / kChunkStages;           // chunks, as even as can be
   const int chunk_stages = (stages + least - 1) / least, chunks = (stages + chunk_stages - 1) / chunk_stages;
   const int mine = pair < tiles.total ? (tiles.total - 1 - pair) / pairs + 1 : 0;
@@ -273,15 +282,15 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide_out,
               for (int k = 0; k < kStageDepth / 16; ++k)        // 16 codes: 32 bytes on
                 mma_pair(d, da + (k / 4) * (kAtomA >> 4) + 2 * (k % 4),
                          db + (k / 4) * (kAtomB >> 4) + 2 * (k % 4), kInstr, s > 0 || k > 0);
-              commit_pair(empty + 8 * slot);
+              commit_pair(empty + 8 * slot, first_rank);
             }
             next();
           }
-          if (one && ok) commit_pair(sums_full + 8 * b);
+          if (one && ok) commit_pair(sums_full + 8 * b, first_rank);
         }
       }
       if (!ok && one) {                // instructions still running end before TMEM is freed
-        commit_pair(last);
+        commit_pair(last, first_rank);
         give_up = 0;
         wait_on(last, 0, &give_up);
         give_up = 1;
@@ -296,7 +305,8 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide_out,
         const Place at = place_of(tiles, tile);
         int64_t row = (int64_t)at.row * 2 + half;
         row = row < blocks ? row : blocks - 1;          // past the last token: its results are dropped
-        const uint8_t* from = p.wide + ((p.rank_a == 0 ? 0 : at.rank) * blocks + row) * stages * kBlockBytes;
+        const uint8_t* from =
+            p.wide + (((p.rank_a == 0 ? 0 : at.rank) * blocks + row) * tile_stages + first_stage) * kBlockBytes;
         for (int s = 0; s < stages; ++s, from += kBlockBytes) {
           ok = wait_on(empty + 8 * slot, phase ^ 1u, &give_up);
           if (!ok) break;
@@ -324,7 +334,7 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide_out,
           ok = wait_on(codes_free + 8 * (uint32_t)(g & 1), (uint32_t)((g >> 1) & 1) ^ 1u, &give_up);
           if (!ok) break;
           mbar_expect_tx(bar, code_bytes<BN>());
-          load_box(codes + (uint32_t)(g & 1) * code_bytes<BN>(), &codes_map, s * kStageDepth,
+          load_box(codes + (uint32_t)(g & 1) * code_bytes<BN>(), &codes_map, (first_stage + s) * kStageDepth,
                    at.col * BN + half * (BN / 2), p.rank_w == 0 ? 0 : at.rank, bar);
         }
       }
@@ -336,6 +346,10 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide_out,
       }
     }
     __syncwarp();
+    if (SPLIT > 1) {                   // the takers' exchange
+      cluster_sync();
+      cluster_sync();
+    }
   } else if (warp >= kTakers) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kTurnerRegs));
     // This thread's pieces: 16 codes from 16 * seg of a row.  Eight lanes
@@ -385,7 +399,7 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide_out,
           ok = __all_sync(0xFFFFFFFFu, wait_on(landed + 8 * slot, phase, &give_up));
         if (!ok) break;
         __syncwarp();
-        if (lane == 0) arrive_first(full + 8 * slot);
+        if (lane == 0) arrive_first(full + 8 * slot, first_rank);
         slot += kGroups;
         if (slot >= kStages) {
           slot -= kStages;
@@ -394,6 +408,11 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide_out,
       }
     }
     if (!ok && lane == 0) atomicOr(&g_gave_up, 1);
+    __syncwarp();
+    if (SPLIT > 1) {
+      cluster_sync();
+      cluster_sync();
+    }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kTakerRegs));
     int sum[kCols];
@@ -418,21 +437,58 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide_out,
         }
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncwarp();
-        if (lane == 0) arrive_first(sums_empty + 8 * b);
+        if (lane == 0) arrive_first(sums_empty + 8 * b, first_rank);
+      }
+      const int r = (warp & 3) * 32 + lane, col0 = (warp >> 2) * kCols;     // in the block's tile
+      if (SPLIT > 1) {
+        constexpr int kOwn = BN / SPLIT;                // columns of a pair
+        __syncwarp();
+        cluster_sync();                                 // every ring is free
+#pragma unroll
+        for (int j = 0; j < kCols; j += 4) {
+          const int owner = (col0 + j) / kOwn;
+          if (owner == split) continue;
+          const int from = split < owner ? split : split - 1;
+          const uint32_t to = ring + (uint32_t)((from * (kOwn / 4) + (col0 + j - owner * kOwn) / 4) * kRows + r) * 16u;
+          asm volatile(
+              "{\n\t.reg .b32 at;\n\t"
+              "mapa.shared::cluster.u32 at, %0, %1;\n\t"
+              "st.shared::cluster.v4.b32 [at], {%2, %3, %4, %5};\n\t}"
+              :: "r"(to), "r"(2 * owner + half), "r"(sum[j]), "r"(sum[j + 1]), "r"(sum[j + 2]), "r"(sum[j + 3])
+              : "memory");
+        }
+        __syncwarp();
+        cluster_sync();
+#pragma unroll
+        for (int j = 0; j < kCols; j += 4) {
+          if ((col0 + j) / kOwn != split) continue;
+#pragma unroll
+          for (int from = 0; from < SPLIT - 1; ++from) {
+            int v[4];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                         : "r"(ring + (uint32_t)((from * (kOwn / 4) + (col0 + j - split * kOwn) / 4) * kRows + r) * 16u)
+                         : "memory");
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[j + i] += v[i];
+          }
+        }
       }
       if (!ok) break;
       const Place at = place_of(tiles, tile);
-      const int64_t t = (int64_t)at.row * 256 + half * kRows + (warp & 3) * 32 + lane;
-      const int64_t c0 = (int64_t)at.col * BN + (warp >> 2) * kCols;
+      const int64_t t = (int64_t)at.row * 256 + half * kRows + r;
+      const int64_t c0 = (int64_t)at.col * BN + col0;
       if (t < p.tokens) {
         T* row = static_cast<T*>(p.out) + at.rank * p.rank_out + t * p.ld_out;
         const float token = __ldg(p.a_scales + at.rank * p.rank_a_scales + t);
 #pragma unroll
         for (int j = 0; j < kCols; j += 16)
-          if (c0 + j < p.channels) store_results<T>(p, at.rank, row, c0 + j, sum + j, token, wide_out);
+          if (c0 + j < p.channels && (SPLIT == 1 || (col0 + j) / (BN / SPLIT) == split))
+            store_results<T>(p, at.rank, row, c0 + j, sum + j, token, wide_out);
       }
     }
     if (!ok && lane == 0) atomicOr(&g_gave_up, 1);
+    __syncwarp();
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
@@ -478,16 +534,35 @@ cudaError_t channels_map(const ProductArgs& p, CUtensorMap* map) {
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <typename T, int BN>
-cudaError_t launch(const ProductArgs& p, const ProductLayout& l, cudaStream_t s) {
+template <typename T, int BN, int SPLIT>
+cudaError_t launch(const ProductArgs& p, const Tiles& t, const CUtensorMap& map, const ProductLayout& l, cudaStream_t s) {
   static OncePerDevice prepared;
   cudaError_t e = prepared.run([] {
-    return cudaFuncSetAttribute(product_pair_kernel<T, BN>,
+    return cudaFuncSetAttribute(product_pair_kernel<T, BN, SPLIT>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<BN>());
   });
   if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  const int pairs = l.sms / 2;
+  cfg.gridDim = dim3((unsigned)(2 * SPLIT * (SPLIT > 1 || t.total < pairs ? t.total : pairs)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem_bytes<BN>();
+  cfg.stream = s;
+  cudaLaunchAttribute overlapped = overlapped_launch();
+  cfg.attrs = &overlapped;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, product_pair_kernel<T, BN, SPLIT>, p, t, (int)l.wide, map);
+}
+
+}  // namespace
+
+template <>
+cudaError_t launch_pair<ECHO_ELEM>(const ProductArgs& p, const ProductLayout& l, cudaStream_t s) {
+  constexpr int BN = 256;
+  using T = ECHO_ELEM;
   CUtensorMap map = {};
-  if ((e = channels_map<BN>(p, &map)) != cudaSuccess) return e;
+  cudaError_t e = channels_map<BN>(p, &map);
+  if (e != cudaSuccess) return e;
   Tiles t;
   t.rows = (int)((p.tokens + 255) / 256);
   t.cols = (int)((p.channels + BN - 1) / BN);
@@ -495,22 +570,12 @@ cudaError_t launch(const ProductArgs& p, const ProductLayout& l, cudaStream_t s)
   if (total > 0x7FFFFFFF) return cudaErrorInvalidValue;       // past any memory's results
   t.per_rank = t.rows * t.cols;
   t.total = (int)total;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(2 * (t.total < l.sms / 2 ? t.total : l.sms / 2)));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem_bytes<BN>();
-  cfg.stream = s;
-  cudaLaunchAttribute overlapped = overlapped_launch();
-  cfg.attrs = &overlapped;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, product_pair_kernel<T, BN>, p, t, (int)l.wide, map);
-}
-
-}  // namespace
-
-template <>
-cudaError_t launch_pair<ECHO_ELEM>(const ProductArgs& p, const ProductLayout& l, cudaStream_t s) {
-  return launch<ECHO_ELEM, 256>(p, l, s);
+  // Pairs that share a tile's depth: as many as there are pairs for, while
+  // each has two stages at least.  256 x 4096 x 4096: SPLIT_US.
+  const int64_t pairs = l.sms / 2, stages = wide_blocks(p.depth);
+  if (total * 4 <= pairs && stages >= 8) return launch<T, BN, 4>(p, t, map, l, s);
+  if (total * 2 <= pairs && stages >= 4) return launch<T, BN, 2>(p, t, map, l, s);
+  return launch<T, BN, 1>(p, t, map, l, s);
 }
 
 template <>

@@ -57,7 +57,7 @@ _NORM_PARAMS = struct.Struct("4q")        # echo_norm_params: w_post, b_post, w_
 _NORM_IO = struct.Struct("16q")           # echo_norm_io
 _NORM_GRAD_IO = struct.Struct("18q")      # echo_norm_grad_io
 _MATRIX = struct.Struct("3q")             # echo_matrix: data, ld, rank_stride
-_FEW_TOKENS = 64                          # up to here no product needs a workspace
+_FEW_TOKENS = 32                          # up to here no product needs a workspace
 
 _SIGS = {
     "echo_plan": (_i32, [_i32, _i64, _i32, _i32, ctypes.POINTER(_vp)]),

@@ -538,7 +538,7 @@ int echo_matmul_int8(int64_t ranks, int64_t tokens, int64_t channels, int64_t de
 /*
  * echo_matmul_workspace_bytes -- bytes of the device workspace that
  * echo_matmul_int8 (of a) and echo_linear_int8 (a: its codes) need: for more
- * than 64 tokens 2 a code of theirs, whose f16 forms it holds during the call
+ * than 32 tokens 2 a code of theirs, whose f16 forms it holds during the call
  * (rows and columns rounded up to 128, ranks that share their tokens once),
  * and 1 a code of w (depth rounded up to 16) if the rows of w do not all start
  * on 16-byte boundaries.  0 for fewer tokens, or sizes that the calls refuse.
