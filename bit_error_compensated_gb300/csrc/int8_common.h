@@ -51,12 +51,12 @@ Workspace product_workspace(const ProductArgs& p);
 
 // The value of an exact sum: fp32 products by the token's, then the channel's
 // scale, in this order everywhere, so that every kernel gives the same bits.
-__device__ __forceinline__ float scaled_sum(int sum, float token, float channel) {
-  return __fmul_rn(__fmul_rn(__int2float_rn(sum), token), channel);
+__device__ __forceinline__ float scaled_sum(float sum, float token, float channel) {
+  return __fmul_rn(__fmul_rn(sum, token), channel);
 }
 
 struct ProductLayout {
-  bool wide;                     // rows of out start on 16-byte boundaries
+  bool wide;                     // rows of out start on 32-byte boundaries
   int sms;
 };
 

@@ -164,7 +164,7 @@ product_few_kernel(const ProductArgs p, const int early) {
   for (int i = threadIdx.x; i < kRows * kCols; i += 32 * kWarps) {
     const int64_t c = c0 + i % kRows, t = t0 + i / kRows;
     if (c >= p.channels || t >= p.tokens) continue;
-    const float v = scaled_sum(total[i], p.a_scales[rank * p.rank_a_scales + t], p.w_scales[rank * p.rank_w_scales + c]);
+    const float v = scaled_sum(__int2float_rn(total[i]), p.a_scales[rank * p.rank_a_scales + t], p.w_scales[rank * p.rank_w_scales + c]);
     const int64_t at = rank * p.rank_out + t * p.ld_out + c;
     if (p.out_dtype == ECHO_F32) static_cast<float*>(p.out)[at] = v;
     else if (p.out_dtype == ECHO_BF16) static_cast<__nv_bfloat16*>(p.out)[at] = from_float<__nv_bfloat16>(v);

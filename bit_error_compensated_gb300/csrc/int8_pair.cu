@@ -49,7 +49,7 @@ constexpr int kIssuer = kTakers + kTurners;     // the first of the issuing warp
 constexpr int kThreads = 32 * (kIssuer + 4);    // five warpgroups; of the last, three warps work
 // Registers: the block starts with 96 a thread (five warpgroups of 480 in
 // all); a taker holds up to 128 sums, a turner a stage's codes.
-constexpr int kTakerRegs = 160, kTurnerRegs = 64, kIssuerRegs = 32;
+constexpr int kTakerRegs = 168, kTurnerRegs = 56, kIssuerRegs = 32;
 static_assert(2 * kTakerRegs + 2 * kTurnerRegs + kIssuerRegs <= 5 * 96,
               "a split above the launch's registers never ends");
 
@@ -172,28 +172,31 @@ __device__ __forceinline__ void cluster_sync() {
                "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// 16 results of one token, from channel c.
+// 16 results of one token, from channel c, of exact sums.  The scales of the
+// 128 channels from c - at lie four in each lane.  `wide`: 16 results of a row
+// are aligned.
 template <typename T>
-__device__ __forceinline__ void store_results(const ProductArgs& p, int64_t rank, T* row, int64_t c,
-                                              const int* sum, float token, bool wide) {
-  const float* scales = p.w_scales + rank * p.rank_w_scales + c;
+__device__ __forceinline__ void store_results(const ProductArgs& p, T* row, int64_t c, int at, float (&sum)[16],
+                                              float token, const float (&scales)[4], bool there, bool wide) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    sum[i] = scaled_sum(sum[i], token, __shfl_sync(0xFFFFFFFFu, scales[i % 4], (at + i) / 4));
+  if (!there) return;
   if (wide && c + 16 <= p.channels) {
-    constexpr int N = 16 / sizeof(T);
+    const Pack<T, 16> out = from_floats<T, 16>(sum);
 #pragma unroll
-    for (int j = 0; j < 16; j += N) {
-      float v[N];
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = scaled_sum(sum[j + i], token, __ldg(scales + j + i));
-      store_floats<T, N>(row + c + j, v);
-    }
+    for (int i = 0; i < (int)sizeof(out) / 32; ++i)
+      store32(reinterpret_cast<uint8_t*>(row + c) + 32 * i, reinterpret_cast<const uint32_t(*)[8]>(&out)[i]);
   } else {
 #pragma unroll
     for (int i = 0; i < 16; ++i)
-      if (c + i < p.channels) row[c + i] = from_float<T>(scaled_sum(sum[i], token, __ldg(scales + i)));
+      if (c + i < p.channels) row[c + i] = from_float<T>(sum[i]);
   }
 }
 
-template <typename T, int BN, int SPLIT>
+// ONE: a tile is one chunk (depth up to 1024), whose sums are stored as they
+// come; SPLIT is 1.
+template <typename T, int BN, int SPLIT, bool ONE>
 __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(kThreads, 1)
 product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide_out,
                     const __grid_constant__ CUtensorMap codes_map) {
@@ -380,7 +383,8 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide_out,
         if (!ok) break;
         const uint32_t base = ring + slot * stage_bytes<BN>() + put;
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
+        for (int n = 0; n < kPieces; ++n) {
+          const int i = kPieces - 1 - n;                // the last loaded first:
           const uint32_t to = base + (i >> 1) * 1024 + (i & 1 ? kAtomB : 0);
           uint32_t h[8];
           codes_to_f16(held[i].x, h[0], h[1]);
@@ -391,10 +395,12 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide_out,
                        :: "r"(to), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
           asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
                        :: "r"(to ^ 16u), "r"(h[4]), "r"(h[5]), "r"(h[6]), "r"(h[7]) : "memory");
+          if (n == 0) {                 // where it has arrived, all have, and the slot can be filled
+            __syncwarp();               // again (a copy overtakes loads that no one has used yet)
+            if (lane == 0) arrive_here(codes_free + 8 * group);
+          }
         }
         fence_proxy_async();
-        __syncwarp();                   // only now: a copy can overtake loads that no one has used yet
-        if (lane == 0) arrive_here(codes_free + 8 * group);
         if (warp % kGroupWarps == 0)    // one warp vouches for the tokens' copy too
           ok = __all_sync(0xFFFFFFFFu, wait_on(landed + 8 * slot, phase, &give_up));
         if (!ok) break;
@@ -415,32 +421,53 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide_out,
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kTakerRegs));
-    int sum[kCols];
+    int sum[ONE ? 1 : kCols];
     uint32_t chunk = 0;
     bool ok = true;
     const uint32_t my_tmem = tmem + ((uint32_t)(warp & 3) << 21) + (uint32_t)(warp >> 2) * kCols;
     for (int tile = pair; tile < tiles.total && ok; tile += pairs) {
+      const Place at = place_of(tiles, tile);
+      const int r = (warp & 3) * 32 + lane, col0 = (warp >> 2) * kCols;     // in the block's tile
+      const int64_t t = (int64_t)at.row * 256 + half * kRows + r;
+      const int64_t c0 = (int64_t)at.col * BN + col0;
+      const bool there = t < p.tokens;
+      // Read now, used after the sums: a lane's four channels' scales, its token's.
+      float scales[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        scales[i] = c0 + 4 * lane + i < p.channels
+                        ? __ldg(p.w_scales + at.rank * p.rank_w_scales + c0 + 4 * lane + i) : 0.f;
+      const float token = there ? __ldg(p.a_scales + at.rank * p.rank_a_scales + t) : 0.f;
+      T* row = static_cast<T*>(p.out) + at.rank * p.rank_out + (there ? t : 0) * p.ld_out;
       for (int c = 0; c < chunks; ++c, ++chunk) {
         const uint32_t b = chunk & 1;
         ok = __all_sync(0xFFFFFFFFu, wait_on(sums_full + 8 * b, (chunk >> 1) & 1, &give_up));
         if (!ok) break;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        if constexpr (ONE) {
+#pragma unroll 1
+          for (int j = 0; j < kCols; j += 16) {         // rolled: code that runs once a tile is fetched each time
+            float v[16];
+            tmem_load16(my_tmem + b * BN + j, v);
+            if (c0 + j < p.channels) store_results<T>(p, row, c0 + j, j, v, token, scales, there, wide_out);
+          }
+        } else {
 #pragma unroll
-        for (int j = 0; j < kCols; j += 16) {
-          float v[16];
-          tmem_load16(my_tmem + b * BN + j, v);
+          for (int j = 0; j < kCols; j += 16) {
+            float v[16];
+            tmem_load16(my_tmem + b * BN + j, v);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int x = __float2int_rn(v[i]);
-            sum[j + i] = c == 0 ? x : sum[j + i] + x;
+            for (int i = 0; i < 16; ++i) {
+              const int x = __float2int_rn(v[i]);
+              sum[j + i] = c == 0 ? x : sum[j + i] + x;
+            }
           }
         }
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncwarp();
         if (lane == 0) arrive_first(sums_empty + 8 * b, first_rank);
       }
-      const int r = (warp & 3) * 32 + lane, col0 = (warp >> 2) * kCols;     // in the block's tile
-      if (SPLIT > 1) {
+      if constexpr (SPLIT > 1) {
         constexpr int kOwn = BN / SPLIT;                // columns of a pair
         __syncwarp();
         cluster_sync();                                 // every ring is free
@@ -475,16 +502,15 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide_out,
         }
       }
       if (!ok) break;
-      const Place at = place_of(tiles, tile);
-      const int64_t t = (int64_t)at.row * 256 + half * kRows + r;
-      const int64_t c0 = (int64_t)at.col * BN + col0;
-      if (t < p.tokens) {
-        T* row = static_cast<T*>(p.out) + at.rank * p.rank_out + t * p.ld_out;
-        const float token = __ldg(p.a_scales + at.rank * p.rank_a_scales + t);
+      if constexpr (!ONE) {
 #pragma unroll
-        for (int j = 0; j < kCols; j += 16)
-          if (c0 + j < p.channels && (SPLIT == 1 || (col0 + j) / (BN / SPLIT) == split))
-            store_results<T>(p, at.rank, row, c0 + j, sum + j, token, wide_out);
+        for (int j = 0; j < kCols; j += 16) {
+          if (SPLIT > 1 && (col0 + j) / (BN / SPLIT) != split) continue;
+          float v[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = __int2float_rn(sum[j + i]);
+          if (c0 + j < p.channels) store_results<T>(p, row, c0 + j, j, v, token, scales, there, wide_out);
+        }
       }
     }
     if (!ok && lane == 0) atomicOr(&g_gave_up, 1);
@@ -534,11 +560,11 @@ cudaError_t channels_map(const ProductArgs& p, CUtensorMap* map) {
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <typename T, int BN, int SPLIT>
+template <typename T, int BN, int SPLIT, bool ONE>
 cudaError_t launch(const ProductArgs& p, const Tiles& t, const CUtensorMap& map, const ProductLayout& l, cudaStream_t s) {
   static OncePerDevice prepared;
   cudaError_t e = prepared.run([] {
-    return cudaFuncSetAttribute(product_pair_kernel<T, BN, SPLIT>,
+    return cudaFuncSetAttribute(product_pair_kernel<T, BN, SPLIT, ONE>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<BN>());
   });
   if (e != cudaSuccess) return e;
@@ -551,7 +577,7 @@ cudaError_t launch(const ProductArgs& p, const Tiles& t, const CUtensorMap& map,
   cudaLaunchAttribute overlapped = overlapped_launch();
   cfg.attrs = &overlapped;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, product_pair_kernel<T, BN, SPLIT>, p, t, (int)l.wide, map);
+  return cudaLaunchKernelEx(&cfg, product_pair_kernel<T, BN, SPLIT, ONE>, p, t, (int)l.wide, map);
 }
 
 }  // namespace
@@ -573,9 +599,9 @@ cudaError_t launch_pair<ECHO_ELEM>(const ProductArgs& p, const ProductLayout& l,
   // Pairs that share a tile's depth: as many as there are pairs for, while
   // each has two stages at least.  256 x 4096 x 4096: SPLIT_US.
   const int64_t pairs = l.sms / 2, stages = wide_blocks(p.depth);
-  if (total * 4 <= pairs && stages >= 8) return launch<T, BN, 4>(p, t, map, l, s);
-  if (total * 2 <= pairs && stages >= 4) return launch<T, BN, 2>(p, t, map, l, s);
-  return launch<T, BN, 1>(p, t, map, l, s);
+  if (total * 4 <= pairs && stages >= 8) return launch<T, BN, 4, false>(p, t, map, l, s);
+  if (total * 2 <= pairs && stages >= 4) return launch<T, BN, 2, false>(p, t, map, l, s);
+  return stages <= kChunkStages ? launch<T, BN, 1, true>(p, t, map, l, s) : launch<T, BN, 1, false>(p, t, map, l, s);
 }
 
 template <>

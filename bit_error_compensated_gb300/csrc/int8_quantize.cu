@@ -17,8 +17,7 @@ template <typename T, int VEC>
 __global__ void __launch_bounds__(1024)
 quantize_kernel(const QuantArgs a) {
   __shared__ uint32_t maxima[32];
-  const int64_t row = blockIdx.x;
-  const int64_t rank = row / a.tokens, token = row - rank * a.tokens;
+  const int64_t token = blockIdx.x, rank = blockIdx.y;
   const T* x = static_cast<const T*>(a.x) + rank * a.rank_x + token * a.ld_x;
   int8_t* codes = a.codes + rank * a.rank_codes + token * a.ld_codes;
   const int64_t step = (int64_t)blockDim.x * VEC;
@@ -71,20 +70,18 @@ quantize_kernel(const QuantArgs a) {
   if (a.wide)                          // zeros up to the last block's end
     for (int64_t c = a.depth + threadIdx.x; c < wide_blocks(a.depth) * kBlockCodes; c += blockDim.x)
       *reinterpret_cast<uint16_t*>(a.wide + wide_offset(rank, token, c & ~(int64_t)7, a.tokens, a.depth) + 2 * (c & 7)) = 0;
-  if (threadIdx.x == 0) a.scales[row] = __fdiv_rn(top, 127.f);
+  if (threadIdx.x == 0) a.scales[rank * a.tokens + token] = __fdiv_rn(top, 127.f);
 }
 
-// Codes that are in int8 already, as f16: a thread turns 16 of a row.
+// Codes that are in int8 already, as f16: a thread turns 16 of a row (x, z: the
+// token and its rank).
 template <bool ALIGNED>
 __global__ void __launch_bounds__(256)
 widen_kernel(const ProductArgs p) {
   pdl_wait();
   pdl_trigger();
-  const int64_t pieces = wide_blocks(p.depth) * (kBlockCodes / 16);
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t row = i / pieces, k = (i - row * pieces) * 16;
-  const int64_t rank = row / p.tokens, token = row - rank * p.tokens;
-  if (rank >= (p.rank_a == 0 ? 1 : p.ranks)) return;
+  const int64_t k = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 16, token = blockIdx.x, rank = blockIdx.z;
+  if (k >= wide_blocks(p.depth) * kBlockCodes) return;
   const uint4 v = k < p.depth ? load_codes<ALIGNED>(p.a + rank * p.rank_a + token * p.ld_a, k, p.depth)
                               : make_uint4(0, 0, 0, 0);
   uint32_t h[8];
@@ -102,11 +99,9 @@ __global__ void __launch_bounds__(256)
 realign_kernel(const ProductArgs p, int8_t* to, int64_t ld) {
   pdl_wait();
   pdl_trigger();
-  const int64_t pieces = ld / 16, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t row = i / pieces, k = (i - row * pieces) * 16;
-  const int64_t rank = row / p.channels, channel = row - rank * p.channels;
-  if (rank >= (p.rank_w == 0 ? 1 : p.ranks)) return;
-  *reinterpret_cast<uint4*>(to + row * ld + k) =
+  const int64_t k = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 16, channel = blockIdx.x, rank = blockIdx.z;
+  if (k >= ld) return;
+  *reinterpret_cast<uint4*>(to + (rank * p.channels + channel) * ld + k) =
       load_codes<false>(p.w + rank * p.rank_w + channel * p.ld_w, k, p.depth);
 }
 
@@ -115,7 +110,7 @@ cudaError_t launch(const QuantArgs& a, cudaStream_t s) {
   int64_t threads = (a.depth + 2 * VEC - 1) / (2 * VEC);
   threads = threads > 1024 ? 1024 : threads < 32 ? 32 : (threads + 31) / 32 * 32;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.ranks * a.tokens));
+  cfg.gridDim = dim3((unsigned)a.tokens, (unsigned)a.ranks);
   cfg.blockDim = dim3((unsigned)threads);
   cfg.stream = s;
   cudaLaunchAttribute overlapped = overlapped_launch();
@@ -137,9 +132,9 @@ cudaError_t pick(const QuantArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_widen(const ProductArgs& p, cudaStream_t s) {
-  const int64_t pieces = token_ranks(p) * p.tokens * wide_blocks(p.depth) * (kBlockCodes / 16);
+  const int64_t pieces = wide_blocks(p.depth) * (kBlockCodes / 16);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((pieces + 255) / 256));
+  cfg.gridDim = dim3((unsigned)p.tokens, (unsigned)((pieces + 255) / 256), (unsigned)token_ranks(p));
   cfg.blockDim = dim3(256);
   cfg.stream = s;
   cudaLaunchAttribute overlapped = overlapped_launch();
@@ -150,9 +145,8 @@ cudaError_t launch_widen(const ProductArgs& p, cudaStream_t s) {
 }
 
 cudaError_t launch_realign(const ProductArgs& p, int8_t* to, int64_t ld, cudaStream_t s) {
-  const int64_t pieces = (p.rank_w == 0 ? 1 : p.ranks) * p.channels * (ld / 16);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((pieces + 255) / 256));
+  cfg.gridDim = dim3((unsigned)p.channels, (unsigned)((ld / 16 + 255) / 256), (unsigned)(p.rank_w == 0 ? 1 : p.ranks));
   cfg.blockDim = dim3(256);
   cfg.stream = s;
   cudaLaunchAttribute overlapped = overlapped_launch();

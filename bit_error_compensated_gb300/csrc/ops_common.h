@@ -119,6 +119,13 @@ __device__ __forceinline__ void store_floats(T* p, const float (&v)[N]) {
   store_pack<T, N>(p, from_floats<T, N>(v));
 }
 
+// 32 bytes, a whole sector, in one store (32-byte aligned).
+__device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+               :: "l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 // Copies of 16 bytes into shared memory that a thread reads back itself (no
 // barrier between): in flight while it works, without registers.
 __device__ __forceinline__ void copy16_async(uint32_t to, const void* from) {
