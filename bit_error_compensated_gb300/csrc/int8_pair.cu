@@ -167,30 +167,72 @@ __device__ __forceinline__ void load_box(uint32_t to, const CUtensorMap* map, in
       :: "r"(to), "l"(map), "r"(k), "r"(c), "r"(rank), "r"(bar) : "memory");
 }
 
+// Among the takers' warps.
+__device__ __forceinline__ void takers_sync() {
+  asm volatile("bar.sync 1, %0;" :: "n"(32 * kTakers) : "memory");
+}
+
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
                "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// 16 results of one token, from channel c, of exact sums.  The scales of the
-// 128 channels from c - at lie four in each lane.  `wide`: 16 results of a row
-// are aligned.
+// 16 exact sums of this lane's token times its scale and the channels' (in
+// shared memory), as out's type, into half (fp32: all) of 16 words.
 template <typename T>
-__device__ __forceinline__ void store_results(const ProductArgs& p, T* row, int64_t c, int at, float (&sum)[16],
-                                              float token, const float (&scales)[4], bool there, bool wide) {
+__device__ __forceinline__ void scale_sums(float (&sum)[16], uint32_t scales, float token, uint32_t* words) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
-    sum[i] = scaled_sum(sum[i], token, __shfl_sync(0xFFFFFFFFu, scales[i % 4], (at + i) / 4));
-  if (!there) return;
-  if (wide && c + 16 <= p.channels) {
-    const Pack<T, 16> out = from_floats<T, 16>(sum);
+  for (int i = 0; i < 16; i += 4) {
+    float w[4];
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(w[0]), "=f"(w[1]), "=f"(w[2]), "=f"(w[3]) : "r"(scales + 4 * i) : "memory");
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(out) / 32; ++i)
-      store32(reinterpret_cast<uint8_t*>(row + c) + 32 * i, reinterpret_cast<const uint32_t(*)[8]>(&out)[i]);
-  } else {
+    for (int k = 0; k < 4; ++k) sum[i + k] = scaled_sum(sum[i + k], token, w[k]);
+  }
+  const Pack<T, 16> out = from_floats<T, 16>(sum);
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (c + i < p.channels) row[c + i] = from_float<T>(sum[i]);
+  for (int i = 0; i < (int)sizeof(out) / 4; ++i) words[i] = reinterpret_cast<const uint32_t*>(&out)[i];
+}
+
+// Each lane has UNITS times 32 bytes of its own token's row; after this it has
+// unit lane % UNITS of the rows of its UNITS lanes (in order), so that these
+// store a row's UNITS * 32 bytes together.  A store takes its time by the lines
+// it touches: STORE_US.
+template <int UNITS>
+__device__ __forceinline__ void exchange_units(uint32_t (&w)[8 * UNITS], int lane) {
+#pragma unroll
+  for (int step = 1; step < UNITS; step *= 2) {
+    const bool high = lane & step;
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u) {
+      if (u & step) continue;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        uint32_t &a = w[8 * u + k], &b = w[8 * (u + step) + k];
+        const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, high ? a : b, step);
+        if (high) a = got;
+        else b = got;
+      }
+    }
+  }
+}
+
+// Unit lane % UNITS, at channel c, of UNITS rows from token t.
+template <typename T, int UNITS>
+__device__ __forceinline__ void store_units(const ProductArgs& p, T* out, int64_t t, int64_t c,
+                                            const uint32_t (&w)[8 * UNITS], bool wide) {
+  constexpr int kUnit = 32 / sizeof(T);
+#pragma unroll
+  for (int i = 0; i < UNITS; ++i) {
+    if (t + i >= p.tokens) break;
+    T* to = out + (t + i) * p.ld_out + c;
+    if (wide && c + kUnit <= p.channels) {
+      store32(to, reinterpret_cast<const uint32_t(*)[8]>(w)[i]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kUnit; ++e)
+        if (c + e < p.channels) to[e] = reinterpret_cast<const T*>(w)[i * kUnit + e];
+    }
   }
 }
 
@@ -201,12 +243,16 @@ __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(kThreads, 1)
 product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide_out,
                     const __grid_constant__ CUtensorMap codes_map) {
   constexpr int kCols = BN / 2;                         // of a chunk's sums, a taker's
+  // Units that lanes exchange before a store: with 128 sums in registers two
+  // are what fits.
+  constexpr int kUnits = ONE ? 4 : 2, kLine = kUnits * 32 / (int)sizeof(T);
   constexpr uint32_t kAtomA = kRows * 128, kAtomB = BN / 2 * 128;         // 64 codes of every row
   constexpr uint32_t kInstr = (1u << 4) | ((uint32_t)(BN / 8) << 17) | (16u << 24);  // f16, fp32 sums, 256 x BN
   extern __shared__ uint8_t raw[];
   __shared__ __align__(8) uint64_t bars[3 * kStages + 2 * kGroups + 5];
   __shared__ uint32_t tmem_at;
   __shared__ volatile int give_up;
+  __shared__ __align__(16) float channel_scales[BN];
   const uint32_t ring = (smem_addr(raw) + 1023u) & ~1023u, codes = ring + kStages * stage_bytes<BN>();
   const uint32_t full = smem_addr(bars), landed = full + 8 * kStages, empty = landed + 8 * kStages,
                  codes_full = empty + 8 * kStages, codes_free = codes_full + 8 * kGroups,
@@ -431,14 +477,17 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide_out,
       const int64_t t = (int64_t)at.row * 256 + half * kRows + r;
       const int64_t c0 = (int64_t)at.col * BN + col0;
       const bool there = t < p.tokens;
-      // Read now, used after the sums: a lane's four channels' scales, its token's.
-      float scales[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        scales[i] = c0 + 4 * lane + i < p.channels
-                        ? __ldg(p.w_scales + at.rank * p.rank_w_scales + c0 + 4 * lane + i) : 0.f;
+      // Read now, used after the sums: a channel's scale, this thread's token's.
+      static_assert(BN == 32 * kTakers, "a channel each");
+      const float channel = (int64_t)at.col * BN + tid < p.channels
+                                ? __ldg(p.w_scales + at.rank * p.rank_w_scales + (int64_t)at.col * BN + tid) : 0.f;
       const float token = there ? __ldg(p.a_scales + at.rank * p.rank_a_scales + t) : 0.f;
-      T* row = static_cast<T*>(p.out) + at.rank * p.rank_out + (there ? t : 0) * p.ld_out;
+      T* out = static_cast<T*>(p.out) + at.rank * p.rank_out;
+      const int64_t t0 = t - lane % kUnits, u0 = c0 + lane % kUnits * (kLine / kUnits);   // of the units this lane stores
+      takers_sync();                   // the last tile's scales have been used
+      channel_scales[tid] = channel;
+      takers_sync();
+      const uint32_t my_scales = smem_addr(channel_scales) + 4 * col0;
       for (int c = 0; c < chunks; ++c, ++chunk) {
         const uint32_t b = chunk & 1;
         ok = __all_sync(0xFFFFFFFFu, wait_on(sums_full + 8 * b, (chunk >> 1) & 1, &give_up));
@@ -446,10 +495,16 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide_out,
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         if constexpr (ONE) {
 #pragma unroll 1
-          for (int j = 0; j < kCols; j += 16) {         // rolled: code that runs once a tile is fetched each time
-            float v[16];
-            tmem_load16(my_tmem + b * BN + j, v);
-            if (c0 + j < p.channels) store_results<T>(p, row, c0 + j, j, v, token, scales, there, wide_out);
+          for (int j = 0; j < kCols; j += kLine) {      // rolled: code that runs once a tile is fetched each time
+            uint32_t words[8 * kUnits];
+#pragma unroll
+            for (int n = 0; n < kLine; n += 16) {
+              float v[16];
+              tmem_load16(my_tmem + b * BN + j + n, v);
+              scale_sums<T>(v, my_scales + 4 * (j + n), token, words + n * sizeof(T) / 4);
+            }
+            exchange_units<kUnits>(words, lane);
+            store_units<T, kUnits>(p, out, t0, u0 + j, words, wide_out);
           }
         } else {
 #pragma unroll
@@ -504,12 +559,18 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide_out,
       if (!ok) break;
       if constexpr (!ONE) {
 #pragma unroll
-        for (int j = 0; j < kCols; j += 16) {
+        for (int j = 0; j < kCols; j += kLine) {
           if (SPLIT > 1 && (col0 + j) / (BN / SPLIT) != split) continue;
-          float v[16];
+          uint32_t words[8 * kUnits];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = __int2float_rn(sum[j + i]);
-          if (c0 + j < p.channels) store_results<T>(p, row, c0 + j, j, v, token, scales, there, wide_out);
+          for (int n = 0; n < kLine; n += 16) {
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = __int2float_rn(sum[j + n + i]);
+            scale_sums<T>(v, my_scales + 4 * (j + n), token, words + n * sizeof(T) / 4);
+          }
+          exchange_units<kUnits>(words, lane);
+          store_units<T, kUnits>(p, out, t0, u0 + j, words, wide_out);
         }
       }
     }
