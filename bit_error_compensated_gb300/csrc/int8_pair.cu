@@ -622,24 +622,55 @@ cudaError_t channels_map(const ProductArgs& p, CUtensorMap* map) {
 }
 
 template <typename T, int BN, int SPLIT, bool ONE>
-cudaError_t launch(const ProductArgs& p, const Tiles& t, const CUtensorMap& map, const ProductLayout& l, cudaStream_t s) {
-  static OncePerDevice prepared;
-  cudaError_t e = prepared.run([] {
-    return cudaFuncSetAttribute(product_pair_kernel<T, BN, SPLIT, ONE>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<BN>());
-  });
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  const int pairs = l.sms / 2;
-  cfg.gridDim = dim3((unsigned)(2 * SPLIT * (SPLIT > 1 || t.total < pairs ? t.total : pairs)));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem_bytes<BN>();
-  cfg.stream = s;
-  cudaLaunchAttribute overlapped = overlapped_launch();
-  cfg.attrs = &overlapped;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, product_pair_kernel<T, BN, SPLIT, ONE>, p, t, (int)l.wide, map);
-}
+struct Launch {
+  static cudaError_t prepare() {
+    static OncePerDevice prepared;
+    return prepared.run([] {
+      return cudaFuncSetAttribute(product_pair_kernel<T, BN, SPLIT, ONE>,
+                                  cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<BN>());
+    });
+  }
+  static cudaLaunchConfig_t config(int clusters, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * SPLIT * clusters));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem_bytes<BN>();
+    cfg.stream = s;
+    return cfg;
+  }
+  // Clusters that can run at once on the current device: clusters lie inside
+  // a GPC, so fewer large ones fit than its SMs would hold.
+  static cudaError_t at_once(int* clusters) {
+    static std::atomic<int> known[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    *clusters = known[dev & 63].load(std::memory_order_relaxed);
+    if (*clusters) return cudaSuccess;
+    if ((e = prepare()) != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = config(1, nullptr);
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = 2 * SPLIT;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(clusters, product_pair_kernel<T, BN, SPLIT, ONE>, &cfg);
+    if (e == cudaSuccess) known[dev & 63].store(*clusters, std::memory_order_relaxed);
+    return e;
+  }
+  static cudaError_t run(const ProductArgs& p, const Tiles& t, const CUtensorMap& map, const ProductLayout& l,
+                         cudaStream_t s) {
+    cudaError_t e = prepare();
+    if (e != cudaSuccess) return e;
+    const int pairs = l.sms / 2;
+    cudaLaunchConfig_t cfg = config(SPLIT > 1 || t.total < pairs ? t.total : pairs, s);
+    cudaLaunchAttribute overlapped = overlapped_launch();
+    cfg.attrs = &overlapped;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, product_pair_kernel<T, BN, SPLIT, ONE>, p, t, (int)l.wide, map);
+  }
+};
 
 }  // namespace
 
@@ -657,12 +688,20 @@ cudaError_t launch_pair<ECHO_ELEM>(const ProductArgs& p, const ProductLayout& l,
   if (total > 0x7FFFFFFF) return cudaErrorInvalidValue;       // past any memory's results
   t.per_rank = t.rows * t.cols;
   t.total = (int)total;
-  // Pairs that share a tile's depth: as many as there are pairs for, while
-  // each has two stages at least.  256 x 4096 x 4096: SPLIT_US.
-  const int64_t pairs = l.sms / 2, stages = wide_blocks(p.depth);
-  if (total * 4 <= pairs && stages >= 8) return launch<T, BN, 4, false>(p, t, map, l, s);
-  if (total * 2 <= pairs && stages >= 4) return launch<T, BN, 2, false>(p, t, map, l, s);
-  return stages <= kChunkStages ? launch<T, BN, 1, true>(p, t, map, l, s) : launch<T, BN, 1, false>(p, t, map, l, s);
+  // Pairs that share a tile's depth, where the clusters all run at once and
+  // each pair has two stages at least.  SPLIT_US.
+  const int64_t stages = wide_blocks(p.depth);
+  int room = 0;
+  if (total * 2 <= l.sms / 2 && stages >= 8) {
+    if ((e = Launch<T, BN, 4, false>::at_once(&room)) != cudaSuccess) return e;
+    if (total <= room) return Launch<T, BN, 4, false>::run(p, t, map, l, s);
+  }
+  if (total * 2 <= l.sms / 2 && stages >= 4) {
+    if ((e = Launch<T, BN, 2, false>::at_once(&room)) != cudaSuccess) return e;
+    if (total <= room) return Launch<T, BN, 2, false>::run(p, t, map, l, s);
+  }
+  return stages <= kChunkStages ? Launch<T, BN, 1, true>::run(p, t, map, l, s)
+                                : Launch<T, BN, 1, false>::run(p, t, map, l, s);
 }
 
 template <>
