@@ -8,13 +8,15 @@
 // sums over the row's threads, the variance in a second pass over the
 // registers (no cancellation).  It is bound by those bytes.
 //
-// norm_stream_kernel takes rows of 16-byte pieces up to 8192 elements.  A
+// norm_stream_kernel takes rows up to 8192 elements.  A
 // 16-bit element leaves an SM only 3.4 of its four instructions a cycle's
 // worth of time (32 KB a row of 4096 at the memory's rate are 1400 cycles), so
 // what can be done once is: a thread keeps its eight columns' parameters in
 // registers over all its rows, the scale, a shared gate and the post norm's
 // weight multiplied into one factor.  Rows come through a ring of asynchronous
-// copies, several ahead.  norm_kernel takes any other row.
+// copies, several ahead (16-bit rows that are not made of 16-byte pieces, which
+// such copies do not take, element by element through registers, one ahead).
+// norm_kernel takes longer rows.
 #include "norm_common.h"
 
 namespace echo {
@@ -232,13 +234,17 @@ norm_kernel(const NormArgs a) {
 
 // Rows ahead in the ring of asynchronous copies: 64 (fp32: 96) bytes a thread.
 template <typename T> constexpr int rows_ahead() { return sizeof(T) == 2 ? 4 : 3; }
+// Asynchronous copies take 16 bytes, or an fp32 element.
+template <typename T, int VEC> constexpr bool has_ring() { return VEC * sizeof(T) >= 4; }
 
 // GATE: 0 none, or one row for all (multiplied into `mul` and `add`); 1 a row
 // of gates, 2 a gate, for each row or several.
-template <typename T, int NV, bool LAYER, bool POST, int GATE>
+template <typename T, int VEC, bool LAYER, bool POST, int GATE>
 __global__ void __launch_bounds__(1024)
 norm_stream_kernel(const NormArgs a) {
-  constexpr int VEC = 16 / sizeof(T), kAhead = rows_ahead<T>();
+  constexpr bool RING = has_ring<T, VEC>();
+  constexpr int NV = 8 / VEC, kAhead = RING ? rows_ahead<T>() : 1;
+  constexpr uint32_t kBytes = VEC * sizeof(T);          // of a piece in the ring
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ __align__(16) uint32_t slots[2][kMaxWarps];
   const int tid = threadIdx.x, threads = blockDim.x;
@@ -253,31 +259,43 @@ norm_stream_kernel(const NormArgs a) {
 #pragma unroll
   for (int j = 0; j < NV; ++j) in[j] = (j * threads + tid) * VEC < a.width;
   // This thread's pieces of the ring: x and y of piece j of slot s.
-  const uint32_t piece = 16u * threads * blockDim.y, slot_bytes = 2 * NV * piece;
-  const uint32_t mine = (uint32_t)__cvta_generic_to_shared(ring) + 16u * (threadIdx.y * threads + tid);
+  const uint32_t piece = kBytes * threads * blockDim.y, slot_bytes = 2 * NV * piece;
+  const uint32_t mine = (uint32_t)__cvta_generic_to_shared(ring) + kBytes * (threadIdx.y * threads + tid);
   pdl_wait();
   pdl_trigger();
 
-  const char* from_x = static_cast<const char*>(a.x) + row * a.ld_x * sizeof(T) + 16 * tid;
-  const char* from_y = static_cast<const char*>(a.y) + row * a.ld_y * sizeof(T) + 16 * tid;
-  const int64_t far_x = step * a.ld_x * sizeof(T), far_y = step * a.ld_y * sizeof(T);
+  const char* from[2] = {static_cast<const char*>(a.x) + row * a.ld_x * sizeof(T) + kBytes * tid,
+                         static_cast<const char*>(a.y) + row * a.ld_y * sizeof(T) + kBytes * tid};
+  const int64_t far[2] = {step * a.ld_x * (int64_t)sizeof(T), step * a.ld_y * (int64_t)sizeof(T)};
+  T held[RING ? 1 : 2][RING ? 1 : NV];
   int64_t fetch = row;
-  auto copy_row = [&](uint32_t slot) {
-    if (fetch < a.rows) {
+  auto fetch_array = [&](int k, uint32_t slot) {
+    if (fetch < a.rows && (k == 0 || a.y)) {
 #pragma unroll
       for (int j = 0; j < NV; ++j)
         if (in[j]) {
-          copy16_async(mine + slot * slot_bytes + 2 * j * piece, from_x + 16 * j * threads);
-          if (a.y) copy16_async(mine + slot * slot_bytes + (2 * j + 1) * piece, from_y + 16 * j * threads);
+          const char* at = from[k] + j * threads * (int)kBytes;
+          const uint32_t to = mine + slot * slot_bytes + (2 * j + k) * piece;
+          if constexpr (!RING) held[k][j] = *reinterpret_cast<const T*>(at);
+          else if constexpr (VEC == 1) copy4_async(to, at);
+          else copy16_async(to, at);
         }
     }
-    copies_commit();
-    fetch += step;
-    from_x += far_x;
-    from_y += far_y;
+    from[k] += far[k];
+  };
+  auto take = [&](int k, int j, uint32_t slot, float (&v)[VEC]) {
+    const uint32_t at = mine + slot * slot_bytes + (2 * j + k) * piece;
+    if constexpr (!RING) v[0] = to_float(held[k][j]);
+    else if constexpr (VEC == 1) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[0]) : "r"(at) : "memory");
+    else to_floats<T, VEC>(load_shared16<T, VEC>(at), v);
   };
 #pragma unroll
-  for (int s = 0; s < kAhead; ++s) copy_row(s);
+  for (int s = 0; s < kAhead; ++s) {
+    fetch_array(0, s);
+    fetch_array(1, s);
+    if (RING) copies_commit();
+    fetch += step;
+  }
 
   // The columns' parameters: n = hat1 * mul + add (times the row's gate), h = hat2 * w + b.
   float mul[NV][VEC], add[LAYER ? NV : 1][VEC], w[NV][VEC], b[LAYER ? NV : 1][VEC];
@@ -313,15 +331,15 @@ norm_stream_kernel(const NormArgs a) {
     gate_step = step / a.gate_span;
     gate_rest = step - gate_step * a.gate_span;
   }
-  char* to_r = static_cast<char*>(a.r) + row * a.ld_r * sizeof(T) + 16 * tid;
-  char* to_h = static_cast<char*>(a.h) + row * a.ld_h * sizeof(T) + 16 * tid;
+  char* to_r = static_cast<char*>(a.r) + row * a.ld_r * sizeof(T) + kBytes * tid;
+  char* to_h = static_cast<char*>(a.h) + row * a.ld_h * sizeof(T) + kBytes * tid;
   const int64_t far_r = step * a.ld_r * sizeof(T), far_h = step * a.ld_h * sizeof(T);
   uint32_t slot = 0;
 
   // All rows of a block take the same number of turns, as its sums' barriers need.
   for (int64_t base = row - threadIdx.y; base < a.rows; base += step, row += step) {
     const bool active = row < a.rows;
-    copies_wait<kAhead - 1>();
+    if (RING) copies_wait<kAhead - 1>();
     float v[NV][VEC];      // y, then r, then h; 0 outside the row
     float mean1 = 0.f, rstd1 = 1.f, mean2 = 0.f, rstd2 = 1.f;
     auto centre = [&](float& mean) {
@@ -348,12 +366,13 @@ norm_stream_kernel(const NormArgs a) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       if (a.y && active && in[j]) {
-        to_floats<T, VEC>(load_shared16<T, VEC>(mine + slot * slot_bytes + (2 * j + 1) * piece), v[j]);
+        take(1, j, slot, v[j]);
       } else {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) v[j][i] = 0.f;
       }
     }
+    if (!RING) fetch_array(1, 0);       // what has been read makes room for the next row's
     if (POST) rstd1 = centre(mean1);
     float factor = rstd1, gate = 1.f;
     if (GATE == 2 && active) {
@@ -366,7 +385,7 @@ norm_stream_kernel(const NormArgs a) {
     for (int j = 0; j < NV; ++j) {
       if (!active || !in[j]) continue;
       float x[VEC];
-      to_floats<T, VEC>(load_shared16<T, VEC>(mine + slot * slot_bytes + 2 * j * piece), x);
+      take(0, j, slot, x);
       if (a.y) {
         float g[VEC];
         if (GATE == 1) load_param<T, VEC>(a.gate, a.params_f32, gate_row * a.width + (j * threads + tid) * VEC, g);
@@ -382,10 +401,15 @@ norm_stream_kernel(const NormArgs a) {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) v[j][i] = x[i];
       }
-      if (a.r) store_floats<T, VEC>(reinterpret_cast<T*>(to_r + 16 * j * threads), v[j]);
+      if (a.r) store_floats<T, VEC>(reinterpret_cast<T*>(to_r) + j * threads * VEC, v[j]);
     }
-    copy_row(slot);                     // this thread has read its pieces of the slot
-    slot = slot == kAhead - 1 ? 0 : slot + 1;
+    fetch_array(0, slot);               // this thread has read its pieces of the slot
+    if (RING) {
+      fetch_array(1, slot);
+      copies_commit();
+      slot = slot == kAhead - 1 ? 0 : slot + 1;
+    }
+    fetch += step;
     if (a.h || a.codes || a.stats) rstd2 = centre(mean2);
     if (a.h || a.codes) {
       uint32_t amax = __float_as_uint(kTinyAmax);
@@ -395,7 +419,7 @@ norm_stream_kernel(const NormArgs a) {
 #pragma unroll
         for (int i = 0; i < VEC; ++i)
           v[j][i] = LAYER ? fmaf(v[j][i] * rstd2, w[j][i], b[j][i]) : v[j][i] * rstd2 * w[j][i];
-        if (a.h) store_floats<T, VEC>(reinterpret_cast<T*>(to_h + 16 * j * threads), v[j]);
+        if (a.h) store_floats<T, VEC>(reinterpret_cast<T*>(to_h) + j * threads * VEC, v[j]);
         if (a.codes)
 #pragma unroll
           for (int i = 0; i < VEC; ++i) amax = max(amax, abs_bits(v[j][i]));
@@ -411,7 +435,8 @@ norm_stream_kernel(const NormArgs a) {
           for (int i = 0; i < VEC; ++i) q.v[i] = (int8_t)quantize_code(v[j][i], inv);
           int8_t* to = a.codes + row * a.ld_codes + (j * threads + tid) * VEC;
           if constexpr (VEC == 8) *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(&q);
-          else *reinterpret_cast<uint32_t*>(to) = *reinterpret_cast<const uint32_t*>(&q);
+          else if constexpr (VEC == 4) *reinterpret_cast<uint32_t*>(to) = *reinterpret_cast<const uint32_t*>(&q);
+          else *to = q.v[0];
         }
         if (tid == 0 && active) a.scales[row] = __fdiv_rn(top, 127.f);
       }
@@ -429,7 +454,7 @@ norm_stream_kernel(const NormArgs a) {
       }
     }
   }
-  copies_wait<0>();
+  if (RING) copies_wait<0>();
 }
 
 template <typename T, int VEC, int NV>
@@ -449,21 +474,21 @@ cudaError_t launch(const NormArgs& a, int layer, int sms, cudaStream_t s) {
                : cudaLaunchKernelEx(&cfg, norm_kernel<T, VEC, NV, false>, a);
 }
 
-template <typename T, bool LAYER, bool POST, int GATE>
+template <typename T, int VEC, bool LAYER, bool POST, int GATE>
 cudaError_t launch_stream(const NormArgs& a, int sms, cudaStream_t s) {
-  constexpr int VEC = 16 / sizeof(T), NV = 8 / VEC, kAhead = rows_ahead<T>();
+  constexpr int kRing = has_ring<T, VEC>() ? rows_ahead<T>() * 2 * 8 * (int)sizeof(T) : 0;   // bytes a thread
   const int threads = ((a.width + 7) / 8 + 31) / 32 * 32;
   const int rows = threads < 128 ? 128 / threads : 1;
-  const int smem = kAhead * 2 * NV * 16 * threads * rows;
+  const int smem = kRing * threads * rows;
   static OncePerDevice prepared;
   cudaError_t e = prepared.run([] {
-    return cudaFuncSetAttribute(norm_stream_kernel<T, NV, LAYER, POST, GATE>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, kAhead * 2 * NV * 16 * 1024);
+    return cudaFuncSetAttribute(norm_stream_kernel<T, VEC, LAYER, POST, GATE>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, kRing * 1024);
   });
   if (e != cudaSuccess) return e;
   const int64_t blocks = (a.rows + rows - 1) / rows;
   int at_once = 1024 / (threads * rows);               // by registers; and by shared memory
-  if (at_once > 200 * 1024 / smem) at_once = 200 * 1024 / smem;
+  if (smem > 0 && at_once > 200 * 1024 / smem) at_once = 200 * 1024 / smem;
   if (at_once < 1) at_once = 1;
   const int64_t most = (int64_t)sms * at_once;
   cudaLaunchConfig_t cfg = {};
@@ -474,13 +499,20 @@ cudaError_t launch_stream(const NormArgs& a, int sms, cudaStream_t s) {
   cudaLaunchAttribute overlapped = overlapped_launch();
   cfg.attrs = &overlapped;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, norm_stream_kernel<T, NV, LAYER, POST, GATE>, a);
+  return cudaLaunchKernelEx(&cfg, norm_stream_kernel<T, VEC, LAYER, POST, GATE>, a);
 }
 
-template <typename T, bool LAYER, bool POST>
-cudaError_t pick_stream(const NormArgs& a, int sms, cudaStream_t s) {
-  if (!a.gate || (!a.gate_scalar && a.gate_span >= a.rows)) return launch_stream<T, LAYER, POST, 0>(a, sms, s);
-  return a.gate_scalar ? launch_stream<T, LAYER, POST, 2>(a, sms, s) : launch_stream<T, LAYER, POST, 1>(a, sms, s);
+template <typename T, int VEC, bool LAYER, bool POST>
+cudaError_t pick_gate(const NormArgs& a, int sms, cudaStream_t s) {
+  if (!a.gate || (!a.gate_scalar && a.gate_span >= a.rows)) return launch_stream<T, VEC, LAYER, POST, 0>(a, sms, s);
+  return a.gate_scalar ? launch_stream<T, VEC, LAYER, POST, 2>(a, sms, s)
+                       : launch_stream<T, VEC, LAYER, POST, 1>(a, sms, s);
+}
+
+template <typename T, int VEC>
+cudaError_t pick_norm(const NormArgs& a, int layer, int sms, cudaStream_t s) {
+  if (layer) return a.post ? pick_gate<T, VEC, true, true>(a, sms, s) : pick_gate<T, VEC, true, false>(a, sms, s);
+  return a.post ? pick_gate<T, VEC, false, true>(a, sms, s) : pick_gate<T, VEC, false, false>(a, sms, s);
 }
 
 }  // namespace
@@ -489,13 +521,8 @@ template <>
 cudaError_t launch_norm<ECHO_ELEM>(const NormArgs& a, int layer, bool vec, int sms, cudaStream_t s) {
   using T = ECHO_ELEM;
   constexpr int V = 16 / sizeof(T);
-  if (!vec) {
-    if (a.width <= 4096) return launch<T, 1, 4>(a, layer, sms, s);
-    return a.width <= 8192 ? launch<T, 1, 8>(a, layer, sms, s) : launch<T, 1, 16>(a, layer, sms, s);
-  }
-  if (a.width > 8192) return launch<T, V, 16 / V>(a, layer, sms, s);
-  if (layer) return a.post ? pick_stream<T, true, true>(a, sms, s) : pick_stream<T, true, false>(a, sms, s);
-  return a.post ? pick_stream<T, false, true>(a, sms, s) : pick_stream<T, false, false>(a, sms, s);
+  if (a.width > 8192) return vec ? launch<T, V, 16 / V>(a, layer, sms, s) : launch<T, 1, 16>(a, layer, sms, s);
+  return vec ? pick_norm<T, V>(a, layer, sms, s) : pick_norm<T, 1>(a, layer, sms, s);
 }
 
 }  // namespace echo

@@ -350,9 +350,15 @@ def echo_plan_destroy(plan: Plan) -> None:
 # cheap test of each tensor (_fits); only a tensor that fails it goes through
 # _refuse, which says what is wrong.
 
+_CODES = {}                                   # torch.dtype -> ECHO_*, filled by the first call
+
+
 def _dtype_code(dtype) -> int:
-    import torch
-    code = {torch.float32: ECHO_F32, torch.bfloat16: ECHO_BF16, torch.float16: ECHO_F16}.get(dtype)
+    code = _CODES.get(dtype)
+    if code is None:
+        import torch
+        _CODES.update({torch.float32: ECHO_F32, torch.bfloat16: ECHO_BF16, torch.float16: ECHO_F16})
+        code = _CODES.get(dtype)
     if code is None:
         raise ValueError(f"dtype {dtype}, expected float32, bfloat16 or float16")
     return code
@@ -553,6 +559,17 @@ def _matrix(t) -> bytes:
     return _MATRIX.pack(t.data_ptr(), stride[1], stride[0] if t.shape[0] > 1 else 0)
 
 
+def _expect_matrix(t, what: str, dtype, shape, device) -> bytes:
+    """_expect and _matrix of a two- or three-dimensional shape in one."""
+    stride = t.stride()
+    if not (t.dtype is dtype and t.shape == shape and t.get_device() == device
+            and (stride[-1] == 1 or shape[-1] <= 1)):
+        _refuse(t, what, dtype, shape, device)
+    if len(stride) == 2:
+        return _MATRIX.pack(t.data_ptr(), stride[0], 0)
+    return _MATRIX.pack(t.data_ptr(), stride[1], stride[0] if shape[0] > 1 else 0)
+
+
 def _batch(t, what: str) -> tuple:
     """(ranks, rows, columns) of a two- or three-dimensional tensor."""
     shape = t.shape
@@ -564,23 +581,21 @@ def _batch(t, what: str) -> tuple:
 
 
 def _check_product(tokens_of, what: str, dtype, scales, w, w_scales, out, device: int) -> tuple:
-    """(ranks, tokens, channels, depth) of a product whose tensors fit: out
-    [ranks][tokens][channels] or without ranks, the tokens' tensor and scales,
-    w and w_scales each with the ranks' dimension or without it."""
+    """(ranks, tokens, channels, depth, and the matrices of the tokens' tensor,
+    w and out) of a product whose tensors fit: out [ranks][tokens][channels] or
+    without ranks, the tokens' tensor and scales, w and w_scales each with the
+    ranks' dimension or without it."""
     import torch
     ranks, tokens, channels = _batch(out, "out")
     depth = w.shape[-1]
-    if len(tokens_of.shape) == 3:
-        _expect(tokens_of, what, dtype, (ranks, tokens, depth), device)
-        _expect_contiguous(scales, "scales", torch.float32, (ranks, tokens), device)
-    else:
-        _expect(tokens_of, what, dtype, (tokens, depth), device)
-        _expect_contiguous(scales, "scales", torch.float32, (tokens,), device)
-    _expect(w, "w", torch.int8, (ranks, channels, depth) if len(w.shape) == 3 else (channels, depth), device)
+    own = len(tokens_of.shape) == 3
+    a = _expect_matrix(tokens_of, what, dtype, (ranks, tokens, depth) if own else (tokens, depth), device)
+    _expect_contiguous(scales, "scales", torch.float32, (ranks, tokens) if own else (tokens,), device)
+    wm = _expect_matrix(w, "w", torch.int8,
+                        (ranks, channels, depth) if len(w.shape) == 3 else (channels, depth), device)
     _expect(w_scales, "w_scales", torch.float32,
             (ranks, channels) if len(w_scales.shape) == 2 else (channels,), device)
-    _expect(out, "out", out.dtype, out.shape, device)
-    return ranks, tokens, channels, depth
+    return ranks, tokens, channels, depth, a, wm, _expect_matrix(out, "out", out.dtype, out.shape, device)
 
 
 def _workspace(nbytes: int, device, stream) -> tuple:
@@ -627,8 +642,8 @@ def echo_matmul_int8(codes, scales, w, w_scales, out, stream=None) -> None:
     them (codes and scales both)."""
     import torch
     device = _call_device(out)
-    ranks, tokens, channels, depth = _check_product(codes, "codes", torch.int8, scales, w, w_scales, out, device)
-    a, wm = _matrix(codes), _matrix(w)
+    ranks, tokens, channels, depth, a, wm, om = _check_product(codes, "codes", torch.int8, scales, w, w_scales,
+                                                               out, device)
     keep, at, nbytes = None, None, 0
     if tokens > _FEW_TOKENS:
         nbytes = _lib.echo_matmul_workspace_bytes(ranks, tokens, channels, depth, a, wm)
@@ -636,7 +651,7 @@ def echo_matmul_int8(codes, scales, w, w_scales, out, stream=None) -> None:
     status = _lib.echo_matmul_int8(ranks, tokens, channels, depth, a, scales.data_ptr(),
                                    tokens if len(codes.shape) == 3 else 0, wm, w_scales.data_ptr(),
                                    w_scales.stride()[0] if len(w_scales.shape) == 2 else 0,
-                                   _dtype_code(out.dtype), _matrix(out), at, nbytes, _stream(stream))
+                                   _dtype_code(out.dtype), om, at, nbytes, _stream(stream))
     if status:
         raise EchoError(status, "echo_matmul_int8")
 
@@ -653,20 +668,19 @@ def echo_linear_int8(x, w, w_scales, out, codes, scales, stream=None) -> None:
     and scales are the caller's buffers for the quantized tokens."""
     import torch
     device = _call_device(out)
-    ranks, tokens, channels, depth = _check_product(codes, "codes", torch.int8, scales, w, w_scales, out, device)
-    shape = x.shape
-    if len(shape) != len(out.shape):
-        raise ValueError(f"x: shape {tuple(shape)}, expected the {len(out.shape)} dimensions of out")
-    _expect(x, "x", out.dtype, codes.shape, device)
-    a, wm = _matrix(codes), _matrix(w)
+    ranks, tokens, channels, depth, a, wm, om = _check_product(codes, "codes", torch.int8, scales, w, w_scales,
+                                                               out, device)
+    if len(x.shape) != len(out.shape):
+        raise ValueError(f"x: shape {tuple(x.shape)}, expected the {len(out.shape)} dimensions of out")
+    xm = _expect_matrix(x, "x", out.dtype, codes.shape, device)
     keep, at, nbytes = None, None, 0
     if tokens > _FEW_TOKENS:
         nbytes = _lib.echo_matmul_workspace_bytes(ranks, tokens, channels, depth, a, wm)
         keep, at = _workspace(nbytes, out.device, stream)
-    status = _lib.echo_linear_int8(ranks, tokens, channels, depth, _dtype_code(x.dtype), _matrix(x), wm,
+    status = _lib.echo_linear_int8(ranks, tokens, channels, depth, _dtype_code(x.dtype), xm, wm,
                                    w_scales.data_ptr(),
                                    w_scales.stride()[0] if len(w_scales.shape) == 2 else 0,
-                                   a, scales.data_ptr(), _matrix(out), at, nbytes, _stream(stream))
+                                   a, scales.data_ptr(), om, at, nbytes, _stream(stream))
     if status:
         raise EchoError(status, "echo_linear_int8")
 
