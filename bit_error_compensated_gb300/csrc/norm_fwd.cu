@@ -239,8 +239,9 @@ template <typename T, int VEC> constexpr bool has_ring() { return VEC * sizeof(T
 
 // GATE: 0 none, or one row for all (multiplied into `mul` and `add`); 1 a row
 // of gates, 2 a gate, for each row or several.
-template <typename T, int VEC, bool LAYER, bool POST, int GATE>
-__global__ void __launch_bounds__(1024)
+// MOST: threads of a block, at most; it sets the registers a thread may use.
+template <typename T, int VEC, bool LAYER, bool POST, int GATE, int MOST>
+__global__ void __launch_bounds__(MOST)
 norm_stream_kernel(const NormArgs a) {
   constexpr bool RING = has_ring<T, VEC>();
   constexpr int NV = 8 / VEC, kAhead = RING ? rows_ahead<T>() : 1;
@@ -474,20 +475,20 @@ cudaError_t launch(const NormArgs& a, int layer, int sms, cudaStream_t s) {
                : cudaLaunchKernelEx(&cfg, norm_kernel<T, VEC, NV, false>, a);
 }
 
-template <typename T, int VEC, bool LAYER, bool POST, int GATE>
-cudaError_t launch_stream(const NormArgs& a, int sms, cudaStream_t s) {
+template <typename T, int VEC, bool LAYER, bool POST, int GATE, int MOST>
+cudaError_t launch_most(const NormArgs& a, int sms, cudaStream_t s) {
   constexpr int kRing = has_ring<T, VEC>() ? rows_ahead<T>() * 2 * 8 * (int)sizeof(T) : 0;   // bytes a thread
   const int threads = ((a.width + 7) / 8 + 31) / 32 * 32;
   const int rows = threads < 128 ? 128 / threads : 1;
   const int smem = kRing * threads * rows;
   static OncePerDevice prepared;
   cudaError_t e = prepared.run([] {
-    return cudaFuncSetAttribute(norm_stream_kernel<T, VEC, LAYER, POST, GATE>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, kRing * 1024);
+    return cudaFuncSetAttribute(norm_stream_kernel<T, VEC, LAYER, POST, GATE, MOST>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, kRing * MOST);
   });
   if (e != cudaSuccess) return e;
   const int64_t blocks = (a.rows + rows - 1) / rows;
-  int at_once = 1024 / (threads * rows);               // by registers; and by shared memory
+  int at_once = MOST / (threads * rows);               // by registers; and by shared memory
   if (smem > 0 && at_once > 200 * 1024 / smem) at_once = 200 * 1024 / smem;
   if (at_once < 1) at_once = 1;
   const int64_t most = (int64_t)sms * at_once;
@@ -499,7 +500,18 @@ cudaError_t launch_stream(const NormArgs& a, int sms, cudaStream_t s) {
   cudaLaunchAttribute overlapped = overlapped_launch();
   cfg.attrs = &overlapped;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, norm_stream_kernel<T, VEC, LAYER, POST, GATE>, a);
+  return cudaLaunchKernelEx(&cfg, norm_stream_kernel<T, VEC, LAYER, POST, GATE, MOST>, a);
+}
+
+// RMS norms of 16-byte pieces need 64 registers, and are left 32 warps an SM;
+// layer norms keep two more parameters a column, single elements more
+// addresses, and spill there: up to 4096 columns they get 128 registers
+// (8192 x 4096 bf16, layer norms: LAYER_US).
+template <typename T, int VEC, bool LAYER, bool POST, int GATE>
+cudaError_t launch_stream(const NormArgs& a, int sms, cudaStream_t s) {
+  if constexpr (LAYER || VEC == 1)
+    if (a.width <= 4096) return launch_most<T, VEC, LAYER, POST, GATE, 512>(a, sms, s);
+  return launch_most<T, VEC, LAYER, POST, GATE, 1024>(a, sms, s);
 }
 
 template <typename T, int VEC, bool LAYER, bool POST>
