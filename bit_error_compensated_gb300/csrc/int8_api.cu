@@ -15,11 +15,12 @@ using namespace echo;
 
 // Sizes whose products stay far inside 64 bits (and grids inside CUDA's limits).
 constexpr int64_t kMaxExtent = (int64_t)1 << 40;
+constexpr int64_t kMaxRows = ECHO_MATMUL_MAX_ROWS;
 
 int check_sizes(int64_t ranks, int64_t tokens, int64_t channels, int64_t depth) {
   if (ranks < 1 || ranks > ECHO_MAX_RANKS) return ECHO_ERR_ARG;
   if (tokens < 0 || channels < 0 || depth < 0) return ECHO_ERR_SHAPE;
-  if (tokens > (1 << 22) || channels > (1 << 22)) return ECHO_ERR_UNSUPPORTED;
+  if (tokens > kMaxRows || channels > kMaxRows) return ECHO_ERR_UNSUPPORTED;
   if (depth > ECHO_MATMUL_MAX_DEPTH) return ECHO_ERR_UNSUPPORTED;
   return ECHO_OK;
 }

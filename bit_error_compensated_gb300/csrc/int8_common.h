@@ -56,7 +56,7 @@ __device__ __forceinline__ float scaled_sum(float sum, float token, float channe
 }
 
 struct ProductLayout {
-  bool wide;                     // rows of out start on 32-byte boundaries
+  int out_align;                 // rows of out start on multiples of 32, 16, 4 or (1) fewer bytes
   int sms;
 };
 

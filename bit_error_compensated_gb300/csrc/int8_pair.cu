@@ -217,17 +217,27 @@ __device__ __forceinline__ void exchange_units(uint32_t (&w)[8 * UNITS], int lan
   }
 }
 
-// Unit lane % UNITS, at channel c, of UNITS rows from token t.
+// Unit lane % UNITS, at channel c, of UNITS rows from token t.  `align`: the
+// bytes on whose multiples out's rows start (32, 16, 4 or fewer).
 template <typename T, int UNITS>
 __device__ __forceinline__ void store_units(const ProductArgs& p, T* out, int64_t t, int64_t c,
-                                            const uint32_t (&w)[8 * UNITS], bool wide) {
+                                            const uint32_t (&w)[8 * UNITS], int align) {
   constexpr int kUnit = 32 / sizeof(T);
 #pragma unroll
   for (int i = 0; i < UNITS; ++i) {
     if (t + i >= p.tokens) break;
     T* to = out + (t + i) * p.ld_out + c;
-    if (wide && c + kUnit <= p.channels) {
+    const bool whole = c + kUnit <= p.channels;
+    if (whole && align == 32) {
       store32(to, reinterpret_cast<const uint32_t(*)[8]>(w)[i]);
+    } else if (whole && align == 16) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        reinterpret_cast<uint4*>(to)[e] = make_uint4(w[8 * i + 4 * e], w[8 * i + 4 * e + 1], w[8 * i + 4 * e + 2],
+                                                     w[8 * i + 4 * e + 3]);
+    } else if (whole && align == 4) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) reinterpret_cast<uint32_t*>(to)[e] = w[8 * i + e];
     } else {
 #pragma unroll
       for (int e = 0; e < kUnit; ++e)
@@ -240,7 +250,7 @@ __device__ __forceinline__ void store_units(const ProductArgs& p, T* out, int64_
 // come; SPLIT is 1.
 template <typename T, int BN, int SPLIT, bool ONE>
 __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(kThreads, 1)
-product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide_out,
+product_pair_kernel(const ProductArgs p, const Tiles tiles, const int out_align,
                     const __grid_constant__ CUtensorMap codes_map) {
   constexpr int kCols = BN / 2;                         // of a chunk's sums, a taker's
   // Units that lanes exchange before a store: with 128 sums in registers two
@@ -504,7 +514,7 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide_out,
               scale_sums<T>(v, my_scales + 4 * (j + n), token, words + n * sizeof(T) / 4);
             }
             exchange_units<kUnits>(words, lane);
-            store_units<T, kUnits>(p, out, t0, u0 + j, words, wide_out);
+            store_units<T, kUnits>(p, out, t0, u0 + j, words, out_align);
           }
         } else {
 #pragma unroll
@@ -570,7 +580,7 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int wide_out,
             scale_sums<T>(v, my_scales + 4 * (j + n), token, words + n * sizeof(T) / 4);
           }
           exchange_units<kUnits>(words, lane);
-          store_units<T, kUnits>(p, out, t0, u0 + j, words, wide_out);
+          store_units<T, kUnits>(p, out, t0, u0 + j, words, out_align);
         }
       }
     }
@@ -668,7 +678,7 @@ struct Launch {
     cudaLaunchAttribute overlapped = overlapped_launch();
     cfg.attrs = &overlapped;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, product_pair_kernel<T, BN, SPLIT, ONE>, p, t, (int)l.wide, map);
+    return cudaLaunchKernelEx(&cfg, product_pair_kernel<T, BN, SPLIT, ONE>, p, t, l.out_align, map);
   }
 };
 

@@ -21,8 +21,10 @@ cudaError_t launch_product(const ProductArgs& given, bool quantized, cudaStream_
   if (p.tokens <= kFewTokens || p.depth == 0)
     return launch_few(p, w_aligned && rows_aligned(p.a, p.ld_a, p.rank_a, p.tokens, p.ranks), quantized, s);
   const int64_t size = elem_size(p.out_dtype);
-  l.wide = on_boundary(p.out, 32) && (p.tokens == 1 || p.ld_out * size % 32 == 0) &&
-           (p.ranks == 1 || p.rank_out * size % 32 == 0);
+  for (l.out_align = 32; l.out_align > 1; l.out_align = l.out_align == 32 ? 16 : l.out_align == 16 ? 4 : 1)
+    if (on_boundary(p.out, l.out_align) && (p.tokens == 1 || p.ld_out * size % l.out_align == 0) &&
+        (p.ranks == 1 || p.rank_out * size % l.out_align == 0))
+      break;
   if (!quantized && (e = launch_widen(p, s)) != cudaSuccess) return e;
   if (!w_aligned) {
     int8_t* copy = reinterpret_cast<int8_t*>(p.wide + product_workspace(given).tokens);

@@ -46,6 +46,7 @@ ECHO_F16 = 2
 ECHO_NORM_RMS = 0
 ECHO_NORM_LAYER = 1
 ECHO_NORM_MAX_WIDTH = 16384
+ECHO_MATMUL_MAX_ROWS = 1048576
 ECHO_MATMUL_MAX_DEPTH = 131071
 
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t

@@ -499,6 +499,11 @@ typedef struct {
   int64_t rank_stride;     /* 0: every rank reads the same matrix (inputs only) */
 } echo_matrix;
 
+/* Limits of the calls below (ECHO_ERR_UNSUPPORTED above): tokens and channels,
+ * and depth; ranks are 1..ECHO_MAX_RANKS (ECHO_ERR_ARG). */
+#define ECHO_MATMUL_MAX_ROWS  1048576
+#define ECHO_MATMUL_MAX_DEPTH 131071
+
 /*
  * echo_quantize_tokens -- x[ranks][tokens][depth] to int8, one scale a token:
  *     amax = max over the row of |x|, at least 2^-110
@@ -528,7 +533,6 @@ int echo_quantize_tokens(int64_t ranks, int64_t tokens, int64_t depth, int dtype
  * Laid out like echo_allreduce's inputs, out + p * rank_stride is rank p's
  * partial tensor.
  */
-#define ECHO_MATMUL_MAX_DEPTH 131071
 int echo_matmul_int8(int64_t ranks, int64_t tokens, int64_t channels, int64_t depth,
                      const echo_matrix* a, const float* a_scales, int64_t a_scale_stride,
                      const echo_matrix* w, const float* w_scales, int64_t w_scale_stride,
