@@ -489,7 +489,8 @@ cudaError_t launch_most(const NormArgs& a, int sms, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int64_t blocks = (a.rows + rows - 1) / rows;
   int at_once = MOST / (threads * rows);               // by registers; and by shared memory
-  if (smem > 0 && at_once > 200 * 1024 / smem) at_once = 200 * 1024 / smem;
+  if constexpr (kRing > 0)
+    if (at_once > 200 * 1024 / smem) at_once = 200 * 1024 / smem;
   if (at_once < 1) at_once = 1;
   const int64_t most = (int64_t)sms * at_once;
   cudaLaunchConfig_t cfg = {};
