@@ -97,8 +97,8 @@ template <typename T, int E, int VEC, bool LAYER>
 constexpr int grad_pieces() {
   return (has_ring<T, VEC>() ? rows_ahead<T, E>() * 4 * (E * (int)sizeof(T) / 16) : 0) + (LAYER ? 3 : 2) * (E / 4);
 }
-// Warps an SM: at 128 registers a thread.  (64 and twice the warps spill, and
-// take 143 us where this takes GRAD_US, 8192 x 4096 bf16.)
+// Warps an SM: at 128 registers a thread.  (64 and twice the warps spill:
+// 143 us with 8 elements a thread, where this takes 92, 8192 x 4096 bf16.)
 constexpr int kStreamWarps = 16;
 
 // GATE: 0 none, or one row for all; 1 a row of gates, 2 a gate, for each row
@@ -622,18 +622,35 @@ cudaError_t launch_stream(NormGradArgs a, int sms, cudaStream_t s) {
   return e != cudaSuccess ? e : launch_finish<T>(a, s);
 }
 
-template <typename T, int E, int VEC, bool LAYER, bool POST>
-cudaError_t pick_gate(const NormGradArgs& a, int sms, cudaStream_t s) {
-  if (!a.gate || (!a.gate_scalar && a.gate_span >= a.rows))
-    return launch_stream<T, E, VEC, LAYER, POST, 0>(a, sms, s);
-  return a.gate_scalar ? launch_stream<T, E, VEC, LAYER, POST, 2>(a, sms, s)
-                       : launch_stream<T, E, VEC, LAYER, POST, 1>(a, sms, s);
+// Elements a thread: 16 halve what a row costs a warp besides its elements,
+// and fit 128 registers where a thread keeps two sums a column (8192 x 4096
+// bf16, RMS: 80 us, with 8: 92); with three or more (layer norms, a row of
+// gates) they spill (RMS, 128 gate rows: 185 us, with 8: 114), as does a row
+// of single elements.  Past 4096 columns 16 stay the lesser evil: 8 would need
+// a cluster, whose barrier waits for the copies and stores in flight,
+// microseconds a row (4096 x 8192 bf16, RMS: 91 us, as clusters of two 176).
+template <typename T, int VEC, bool LAYER, bool POST, int GATE>
+cudaError_t pick_elements(const NormGradArgs& a, int sms, cudaStream_t s) {
+  if constexpr (VEC > 1 && !LAYER && GATE != 1) {
+    return launch_stream<T, 16, VEC, LAYER, POST, GATE>(a, sms, s);
+  } else {
+    if constexpr (VEC > 1)
+      if (a.width > 8 * kStreamThreads) return launch_stream<T, 16, VEC, LAYER, POST, GATE>(a, sms, s);
+    return launch_stream<T, 8, VEC, LAYER, POST, GATE>(a, sms, s);
+  }
 }
 
-template <typename T, int E, int VEC>
+template <typename T, int VEC, bool LAYER, bool POST>
+cudaError_t pick_gate(const NormGradArgs& a, int sms, cudaStream_t s) {
+  if (!a.gate || (!a.gate_scalar && a.gate_span >= a.rows)) return pick_elements<T, VEC, LAYER, POST, 0>(a, sms, s);
+  return a.gate_scalar ? pick_elements<T, VEC, LAYER, POST, 2>(a, sms, s)
+                       : pick_elements<T, VEC, LAYER, POST, 1>(a, sms, s);
+}
+
+template <typename T, int VEC>
 cudaError_t pick_norm(const NormGradArgs& a, int layer, int sms, cudaStream_t s) {
-  if (layer) return a.post ? pick_gate<T, E, VEC, true, true>(a, sms, s) : pick_gate<T, E, VEC, true, false>(a, sms, s);
-  return a.post ? pick_gate<T, E, VEC, false, true>(a, sms, s) : pick_gate<T, E, VEC, false, false>(a, sms, s);
+  if (layer) return a.post ? pick_gate<T, VEC, true, true>(a, sms, s) : pick_gate<T, VEC, true, false>(a, sms, s);
+  return a.post ? pick_gate<T, VEC, false, true>(a, sms, s) : pick_gate<T, VEC, false, false>(a, sms, s);
 }
 
 }  // namespace
@@ -641,13 +658,7 @@ cudaError_t pick_norm(const NormGradArgs& a, int layer, int sms, cudaStream_t s)
 template <>
 cudaError_t launch_norm_grad<ECHO_ELEM>(NormGradArgs a, int layer, bool vec, int sms, cudaStream_t s) {
   using T = ECHO_ELEM;
-  constexpr int V = 16 / sizeof(T);
-  // 16 elements a thread leave no registers to spare, but a cluster's barrier
-  // costs more: it waits for the copies and stores in flight, microseconds a
-  // row (4096 x 8192 bf16 as clusters of two 176 us, as one block W8192_US).
-  // Single elements need more registers still, and take the cluster.
-  if (!vec) return pick_norm<T, 8, 1>(a, layer, sms, s);
-  return a.width <= 8 * kStreamThreads ? pick_norm<T, 8, V>(a, layer, sms, s) : pick_norm<T, 16, V>(a, layer, sms, s);
+  return vec ? pick_norm<T, 16 / sizeof(T)>(a, layer, sms, s) : pick_norm<T, 1>(a, layer, sms, s);
 }
 
 }  // namespace echo

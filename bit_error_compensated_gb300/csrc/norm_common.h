@@ -79,7 +79,7 @@ inline int norm_grad_threads(int cols, int each) { return ((cols + each - 1) / e
 // Workers (row ranges with their own partial sums) a backward call may have at
 // most: 16 warps an SM.
 inline int64_t norm_grad_max_workers(int width, int sms) {
-  const int threads = width <= 4096 ? norm_grad_threads(width, 8) : 256;
+  const int threads = width <= 4096 ? norm_grad_threads(width, 16) : 256;     // at least
   return (int64_t)sms * (512 / threads > 1 ? 512 / threads : 1);
 }
 

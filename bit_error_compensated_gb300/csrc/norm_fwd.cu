@@ -232,19 +232,20 @@ norm_kernel(const NormArgs a) {
   }
 }
 
-// Rows ahead in the ring of asynchronous copies: 64 (fp32: 96) bytes a thread.
-template <typename T> constexpr int rows_ahead() { return sizeof(T) == 2 ? 4 : 3; }
+// Rows ahead in the ring of asynchronous copies.
+template <typename T, int E> constexpr int rows_ahead() { return sizeof(T) == 2 ? 4 : 3; }
 // Asynchronous copies take 16 bytes, or an fp32 element.
 template <typename T, int VEC> constexpr bool has_ring() { return VEC * sizeof(T) >= 4; }
 
 // GATE: 0 none, or one row for all (multiplied into `mul` and `add`); 1 a row
 // of gates, 2 a gate, for each row or several.
-// MOST: threads of a block, at most; it sets the registers a thread may use.
-template <typename T, int VEC, bool LAYER, bool POST, int GATE, int MOST>
+// E: elements a thread; MOST: threads of a block, at most, which sets the
+// registers a thread may use.
+template <typename T, int E, int VEC, bool LAYER, bool POST, int GATE, int MOST>
 __global__ void __launch_bounds__(MOST)
 norm_stream_kernel(const NormArgs a) {
   constexpr bool RING = has_ring<T, VEC>();
-  constexpr int NV = 8 / VEC, kAhead = RING ? rows_ahead<T>() : 1;
+  constexpr int NV = E / VEC, kAhead = RING ? rows_ahead<T, E>() : 1;
   constexpr uint32_t kBytes = VEC * sizeof(T);          // of a piece in the ring
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ __align__(16) uint32_t slots[2][kMaxWarps];
@@ -475,15 +476,15 @@ cudaError_t launch(const NormArgs& a, int layer, int sms, cudaStream_t s) {
                : cudaLaunchKernelEx(&cfg, norm_kernel<T, VEC, NV, false>, a);
 }
 
-template <typename T, int VEC, bool LAYER, bool POST, int GATE, int MOST>
+template <typename T, int E, int VEC, bool LAYER, bool POST, int GATE, int MOST>
 cudaError_t launch_most(const NormArgs& a, int sms, cudaStream_t s) {
-  constexpr int kRing = has_ring<T, VEC>() ? rows_ahead<T>() * 2 * 8 * (int)sizeof(T) : 0;   // bytes a thread
-  const int threads = ((a.width + 7) / 8 + 31) / 32 * 32;
+  constexpr int kRing = has_ring<T, VEC>() ? rows_ahead<T, E>() * 2 * E * (int)sizeof(T) : 0;   // bytes a thread
+  const int threads = ((a.width + E - 1) / E + 31) / 32 * 32;
   const int rows = threads < 128 ? 128 / threads : 1;
   const int smem = kRing * threads * rows;
   static OncePerDevice prepared;
   cudaError_t e = prepared.run([] {
-    return cudaFuncSetAttribute(norm_stream_kernel<T, VEC, LAYER, POST, GATE, MOST>,
+    return cudaFuncSetAttribute(norm_stream_kernel<T, E, VEC, LAYER, POST, GATE, MOST>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kRing * MOST);
   });
   if (e != cudaSuccess) return e;
@@ -501,7 +502,7 @@ cudaError_t launch_most(const NormArgs& a, int sms, cudaStream_t s) {
   cudaLaunchAttribute overlapped = overlapped_launch();
   cfg.attrs = &overlapped;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, norm_stream_kernel<T, VEC, LAYER, POST, GATE, MOST>, a);
+  return cudaLaunchKernelEx(&cfg, norm_stream_kernel<T, E, VEC, LAYER, POST, GATE, MOST>, a);
 }
 
 // RMS norms of 16-byte pieces need 64 registers, and are left 32 warps an SM;
@@ -510,9 +511,12 @@ cudaError_t launch_most(const NormArgs& a, int sms, cudaStream_t s) {
 // (8192 x 4096 bf16, layer norms: LAYER_US).
 template <typename T, int VEC, bool LAYER, bool POST, int GATE>
 cudaError_t launch_stream(const NormArgs& a, int sms, cudaStream_t s) {
-  if constexpr (LAYER || VEC == 1)
-    if (a.width <= 4096) return launch_most<T, VEC, LAYER, POST, GATE, 512>(a, sms, s);
-  return launch_most<T, VEC, LAYER, POST, GATE, 1024>(a, sms, s);
+  if constexpr (LAYER || VEC == 1) {
+    if (a.width <= 4096) return launch_most<T, 8, VEC, LAYER, POST, GATE, 512>(a, sms, s);
+    return launch_most<T, 8, VEC, LAYER, POST, GATE, 1024>(a, sms, s);
+  } else {
+    return launch_most<T, 16, VEC, LAYER, POST, GATE, 512>(a, sms, s);
+  }
 }
 
 template <typename T, int VEC, bool LAYER, bool POST>
