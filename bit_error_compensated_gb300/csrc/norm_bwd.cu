@@ -103,7 +103,8 @@ constexpr int kStreamWarps = 16;
 
 // GATE: 0 none, or one row for all; 1 a row of gates, 2 a gate, for each row
 // or several.
-template <typename T, int E, int VEC, bool LAYER, bool POST, int GATE>
+// FULL: x, y, dr, dh, dx and dy are all there.
+template <typename T, int E, int VEC, bool LAYER, bool POST, int GATE, bool FULL>
 __global__ void __launch_bounds__(kStreamThreads, 1)
 norm_grad_kernel(const NormGradArgs a, int blocks, int block_cols) {
   constexpr int NV = E / VEC, kAhead = has_ring<T, VEC>() ? rows_ahead<T, E>() : 1;
@@ -141,7 +142,9 @@ norm_grad_kernel(const NormGradArgs a, int blocks, int block_cols) {
     return static_cast<const char*>(p) + (row0 * ld + my_col) * (int64_t)sizeof(T);
   };
   const char* from[4] = {start(a.x, a.ld_x), start(a.y, a.ld_y), start(a.dr, a.ld_dr), start(a.dh, a.ld_dh)};
-  const bool there[4] = {true, a.y != nullptr, a.dr != nullptr, a.dh != nullptr};
+  const bool has_y = FULL || a.y, has_dr = FULL || a.dr, has_dh = FULL || a.dh, has_dx = FULL || a.dx,
+             has_dy = FULL || a.dy;
+  const bool there[4] = {true, has_y, has_dr, has_dh};
   const int64_t far[4] = {a.ld_x * (int64_t)sizeof(T), a.ld_y * (int64_t)sizeof(T), a.ld_dr * (int64_t)sizeof(T),
                           a.ld_dh * (int64_t)sizeof(T)};
   // Whole pieces wait in the ring; single elements, which asynchronous copies
@@ -283,7 +286,7 @@ norm_grad_kernel(const NormGradArgs a, int blocks, int block_cols) {
       }
       float x[VEC], m[VEC];
       take(0, j, slot, x);
-      if (a.y) {
+      if (has_y) {
         take(1, j, slot, hat1[j]);
         if (POST)
 #pragma unroll
@@ -314,7 +317,7 @@ norm_grad_kernel(const NormGradArgs a, int blocks, int block_cols) {
       }
 #pragma unroll
       for (int i = 0; i < VEC; ++i) hat2[j][i] = LAYER ? (x[i] - st.z) * st.w : x[i] * st.w;
-      if (a.dh) {
+      if (has_dh) {
         float w[VEC];
         take(3, j, slot, g[j]);
         get(1, j, w);
@@ -336,7 +339,7 @@ norm_grad_kernel(const NormGradArgs a, int blocks, int block_cols) {
       fetch_array(1, 0);
       fetch_array(3, 0);
     }
-    if (a.dh) {
+    if (has_dh) {
       sums.all(s);
 #pragma unroll
       for (float& v : s) v *= inv_width;
@@ -347,7 +350,7 @@ norm_grad_kernel(const NormGradArgs a, int blocks, int block_cols) {
     for (int j = 0; j < NV; ++j) {
       if (!active || !in[j]) continue;
       float d[VEC];
-      if (a.dr) {
+      if (has_dr) {
         take(2, j, slot, d);
       } else {
 #pragma unroll
@@ -358,8 +361,8 @@ norm_grad_kernel(const NormGradArgs a, int blocks, int block_cols) {
         const float back = fmaf(-s[0], hat2[j][i], LAYER ? g[j][i] - s[LAYER ? 1 : 0] : g[j][i]);
         d[i] = fmaf(st.w, back, d[i]);
       }
-      if (a.dx) store_floats<T, VEC>(reinterpret_cast<T*>(to_dx) + j * threads * VEC, d);
-      if (!a.y) continue;
+      if (has_dx) store_floats<T, VEC>(reinterpret_cast<T*>(to_dx) + j * threads * VEC, d);
+      if (!has_y) continue;
       float m[VEC];
       get(0, j, m);
       if (GATE == 1) {
@@ -410,7 +413,7 @@ norm_grad_kernel(const NormGradArgs a, int blocks, int block_cols) {
       t[0] *= inv_width;
       if (LAYER) t[LAYER ? 1 : 0] *= inv_width;
     }
-    if (a.dy) {
+    if (has_dy) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         if (!active || !in[j]) continue;
@@ -584,7 +587,7 @@ cudaError_t launch_finish(const NormGradArgs& a, cudaStream_t s) {
   return cudaLaunchKernelEx(&fin, norm_grad_finish<T>, a);
 }
 
-template <typename T, int E, int VEC, bool LAYER, bool POST, int GATE>
+template <typename T, int E, int VEC, bool LAYER, bool POST, int GATE, bool FULL>
 cudaError_t launch_stream(NormGradArgs a, int sms, cudaStream_t s) {
   const int blocks = (a.width + E * kStreamThreads - 1) / (E * kStreamThreads);
   const int block_cols = ((a.width + blocks - 1) / blocks + 7) / 8 * 8;
@@ -593,7 +596,7 @@ cudaError_t launch_stream(NormGradArgs a, int sms, cudaStream_t s) {
   const int smem = grad_pieces<T, E, VEC, LAYER>() * 16 * threads * rows;
   static OncePerDevice prepared;
   cudaError_t e = prepared.run([] {
-    return cudaFuncSetAttribute(norm_grad_kernel<T, E, VEC, LAYER, POST, GATE>,
+    return cudaFuncSetAttribute(norm_grad_kernel<T, E, VEC, LAYER, POST, GATE, FULL>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 grad_pieces<T, E, VEC, LAYER>() * 16 * kStreamThreads);
   });
@@ -618,7 +621,7 @@ cudaError_t launch_stream(NormGradArgs a, int sms, cudaStream_t s) {
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = blocks > 1 ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, norm_grad_kernel<T, E, VEC, LAYER, POST, GATE>, a, blocks, block_cols);
+  e = cudaLaunchKernelEx(&cfg, norm_grad_kernel<T, E, VEC, LAYER, POST, GATE, FULL>, a, blocks, block_cols);
   return e != cudaSuccess ? e : launch_finish<T>(a, s);
 }
 
@@ -632,11 +635,12 @@ cudaError_t launch_stream(NormGradArgs a, int sms, cudaStream_t s) {
 template <typename T, int VEC, bool LAYER, bool POST, int GATE>
 cudaError_t pick_elements(const NormGradArgs& a, int sms, cudaStream_t s) {
   if constexpr (VEC > 1 && !LAYER && GATE != 1) {
-    return launch_stream<T, 16, VEC, LAYER, POST, GATE>(a, sms, s);
+    return a.y && a.dr && a.dh && a.dx && a.dy ? launch_stream<T, 16, VEC, LAYER, POST, GATE, true>(a, sms, s)
+                                               : launch_stream<T, 16, VEC, LAYER, POST, GATE, false>(a, sms, s);
   } else {
     if constexpr (VEC > 1)
-      if (a.width > 8 * kStreamThreads) return launch_stream<T, 16, VEC, LAYER, POST, GATE>(a, sms, s);
-    return launch_stream<T, 8, VEC, LAYER, POST, GATE>(a, sms, s);
+      if (a.width > 8 * kStreamThreads) return launch_stream<T, 16, VEC, LAYER, POST, GATE, false>(a, sms, s);
+    return launch_stream<T, 8, VEC, LAYER, POST, GATE, false>(a, sms, s);
   }
 }
 

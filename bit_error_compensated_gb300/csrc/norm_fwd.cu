@@ -505,16 +505,21 @@ cudaError_t launch_most(const NormArgs& a, int sms, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, norm_stream_kernel<T, E, VEC, LAYER, POST, GATE, MOST>, a);
 }
 
-// RMS norms of 16-byte pieces need 64 registers, and are left 32 warps an SM;
-// layer norms keep two more parameters a column, single elements more
-// addresses, and spill there: up to 4096 columns they get 128 registers
-// (8192 x 4096 bf16, layer norms: LAYER_US).
+// Elements and registers a thread.  RMS norms of 16-byte pieces: 16 elements
+// at 128 registers, which halve what a row costs a warp besides its elements
+// (8192 x 4096 bf16: 52 us, with 8 at 64 registers 54; a gate a token 54, 65),
+// but 8 where there are no more rows than blocks, and one row's latency is
+// the time (1 x 4096: 2.7 us, 3.5 with 16).  Layer norms keep two more
+// parameters a column, single elements more addresses: 8 elements, at 128
+// registers as far as blocks of 512 threads reach (1001 x 1537 fp32, layer
+// norms: 12 us, at 64 registers 15).
 template <typename T, int VEC, bool LAYER, bool POST, int GATE>
 cudaError_t launch_stream(const NormArgs& a, int sms, cudaStream_t s) {
   if constexpr (LAYER || VEC == 1) {
     if (a.width <= 4096) return launch_most<T, 8, VEC, LAYER, POST, GATE, 512>(a, sms, s);
     return launch_most<T, 8, VEC, LAYER, POST, GATE, 1024>(a, sms, s);
   } else {
+    if (a.rows <= 2 * sms) return launch_most<T, 8, VEC, LAYER, POST, GATE, 1024>(a, sms, s);
     return launch_most<T, 16, VEC, LAYER, POST, GATE, 512>(a, sms, s);
   }
 }
