@@ -103,7 +103,8 @@ constexpr int kStreamWarps = 16;
 
 // GATE: 0 none, or one row for all; 1 a row of gates, 2 a gate, for each row
 // or several.
-// FULL: x, y, dr, dh, dx and dy are all there.
+// FULL: x, y, dr, dh, dx and dy are all there (8192 x 4096 bf16: 74 us, with
+// the branches 80).
 template <typename T, int E, int VEC, bool LAYER, bool POST, int GATE, bool FULL>
 __global__ void __launch_bounds__(kStreamThreads, 1)
 norm_grad_kernel(const NormGradArgs a, int blocks, int block_cols) {

@@ -240,8 +240,8 @@ template <typename T, int VEC> constexpr bool has_ring() { return VEC * sizeof(T
 // GATE: 0 none, or one row for all (multiplied into `mul` and `add`); 1 a row
 // of gates, 2 a gate, for each row or several.
 // E: elements a thread; MOST: threads of a block, at most, which sets the
-// registers a thread may use.
-template <typename T, int E, int VEC, bool LAYER, bool POST, int GATE, int MOST>
+// registers a thread may use.  FULL: y, r and h are there, codes are not.
+template <typename T, int E, int VEC, bool LAYER, bool POST, int GATE, int MOST, bool FULL>
 __global__ void __launch_bounds__(MOST)
 norm_stream_kernel(const NormArgs a) {
   constexpr bool RING = has_ring<T, VEC>();
@@ -257,6 +257,7 @@ norm_stream_kernel(const NormArgs a) {
   __syncthreads();
   RowReduce red{slots, (int)threadIdx.y * 4, threads / 32, tid >> 5, tid & 31, 0};
   const float inv_width = 1.0f / (float)a.width;
+  const bool has_y = FULL || a.y, has_r = FULL || a.r, has_h = FULL || a.h, has_codes = !FULL && a.codes;
   bool in[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) in[j] = (j * threads + tid) * VEC < a.width;
@@ -272,7 +273,7 @@ norm_stream_kernel(const NormArgs a) {
   T held[RING ? 1 : 2][RING ? 1 : NV];
   int64_t fetch = row;
   auto fetch_array = [&](int k, uint32_t slot) {
-    if (fetch < a.rows && (k == 0 || a.y)) {
+    if (fetch < a.rows && (k == 0 || has_y)) {
 #pragma unroll
       for (int j = 0; j < NV; ++j)
         if (in[j]) {
@@ -367,7 +368,7 @@ norm_stream_kernel(const NormArgs a) {
     };
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      if (a.y && active && in[j]) {
+      if (has_y && active && in[j]) {
         take(1, j, slot, v[j]);
       } else {
 #pragma unroll
@@ -388,7 +389,7 @@ norm_stream_kernel(const NormArgs a) {
       if (!active || !in[j]) continue;
       float x[VEC];
       take(0, j, slot, x);
-      if (a.y) {
+      if (has_y) {
         float g[VEC];
         if (GATE == 1) load_param<T, VEC>(a.gate, a.params_f32, gate_row * a.width + (j * threads + tid) * VEC, g);
 #pragma unroll
@@ -403,7 +404,7 @@ norm_stream_kernel(const NormArgs a) {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) v[j][i] = x[i];
       }
-      if (a.r) store_floats<T, VEC>(reinterpret_cast<T*>(to_r) + j * threads * VEC, v[j]);
+      if (has_r) store_floats<T, VEC>(reinterpret_cast<T*>(to_r) + j * threads * VEC, v[j]);
     }
     fetch_array(0, slot);               // this thread has read its pieces of the slot
     if (RING) {
@@ -412,8 +413,8 @@ norm_stream_kernel(const NormArgs a) {
       slot = slot == kAhead - 1 ? 0 : slot + 1;
     }
     fetch += step;
-    if (a.h || a.codes || a.stats) rstd2 = centre(mean2);
-    if (a.h || a.codes) {
+    if (has_h || has_codes || a.stats) rstd2 = centre(mean2);
+    if (has_h || has_codes) {
       uint32_t amax = __float_as_uint(kTinyAmax);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
@@ -421,12 +422,12 @@ norm_stream_kernel(const NormArgs a) {
 #pragma unroll
         for (int i = 0; i < VEC; ++i)
           v[j][i] = LAYER ? fmaf(v[j][i] * rstd2, w[j][i], b[j][i]) : v[j][i] * rstd2 * w[j][i];
-        if (a.h) store_floats<T, VEC>(reinterpret_cast<T*>(to_h) + j * threads * VEC, v[j]);
-        if (a.codes)
+        if (has_h) store_floats<T, VEC>(reinterpret_cast<T*>(to_h) + j * threads * VEC, v[j]);
+        if (has_codes)
 #pragma unroll
           for (int i = 0; i < VEC; ++i) amax = max(amax, abs_bits(v[j][i]));
       }
-      if (a.codes) {
+      if (has_codes) {
         const float top = __uint_as_float(red.all(amax, MaxBits()));
         const float inv = __fdiv_rn(127.f, top);
 #pragma unroll
@@ -476,7 +477,7 @@ cudaError_t launch(const NormArgs& a, int layer, int sms, cudaStream_t s) {
                : cudaLaunchKernelEx(&cfg, norm_kernel<T, VEC, NV, false>, a);
 }
 
-template <typename T, int E, int VEC, bool LAYER, bool POST, int GATE, int MOST>
+template <typename T, int E, int VEC, bool LAYER, bool POST, int GATE, int MOST, bool FULL>
 cudaError_t launch_most(const NormArgs& a, int sms, cudaStream_t s) {
   constexpr int kRing = has_ring<T, VEC>() ? rows_ahead<T, E>() * 2 * E * (int)sizeof(T) : 0;   // bytes a thread
   const int threads = ((a.width + E - 1) / E + 31) / 32 * 32;
@@ -484,7 +485,7 @@ cudaError_t launch_most(const NormArgs& a, int sms, cudaStream_t s) {
   const int smem = kRing * threads * rows;
   static OncePerDevice prepared;
   cudaError_t e = prepared.run([] {
-    return cudaFuncSetAttribute(norm_stream_kernel<T, E, VEC, LAYER, POST, GATE, MOST>,
+    return cudaFuncSetAttribute(norm_stream_kernel<T, E, VEC, LAYER, POST, GATE, MOST, FULL>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kRing * MOST);
   });
   if (e != cudaSuccess) return e;
@@ -502,7 +503,7 @@ cudaError_t launch_most(const NormArgs& a, int sms, cudaStream_t s) {
   cudaLaunchAttribute overlapped = overlapped_launch();
   cfg.attrs = &overlapped;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, norm_stream_kernel<T, E, VEC, LAYER, POST, GATE, MOST>, a);
+  return cudaLaunchKernelEx(&cfg, norm_stream_kernel<T, E, VEC, LAYER, POST, GATE, MOST, FULL>, a);
 }
 
 // Elements and registers a thread.  RMS norms of 16-byte pieces: 16 elements
@@ -516,11 +517,12 @@ cudaError_t launch_most(const NormArgs& a, int sms, cudaStream_t s) {
 template <typename T, int VEC, bool LAYER, bool POST, int GATE>
 cudaError_t launch_stream(const NormArgs& a, int sms, cudaStream_t s) {
   if constexpr (LAYER || VEC == 1) {
-    if (a.width <= 4096) return launch_most<T, 8, VEC, LAYER, POST, GATE, 512>(a, sms, s);
-    return launch_most<T, 8, VEC, LAYER, POST, GATE, 1024>(a, sms, s);
+    if (a.width <= 4096) return launch_most<T, 8, VEC, LAYER, POST, GATE, 512, false>(a, sms, s);
+    return launch_most<T, 8, VEC, LAYER, POST, GATE, 1024, false>(a, sms, s);
   } else {
-    if (a.rows <= 2 * sms) return launch_most<T, 8, VEC, LAYER, POST, GATE, 1024>(a, sms, s);
-    return launch_most<T, 16, VEC, LAYER, POST, GATE, 512>(a, sms, s);
+    if (a.rows <= 2 * sms) return launch_most<T, 8, VEC, LAYER, POST, GATE, 1024, false>(a, sms, s);
+    return a.y && a.r && a.h && !a.codes ? launch_most<T, 16, VEC, LAYER, POST, GATE, 512, true>(a, sms, s)
+                                         : launch_most<T, 16, VEC, LAYER, POST, GATE, 512, false>(a, sms, s);
   }
 }
 
