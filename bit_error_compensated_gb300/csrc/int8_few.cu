@@ -12,6 +12,11 @@
 // f16 in registers (int8_load.h) and the f16 instruction does 1023.  Its fp32
 // sums are exact for 1024 codes; after those, and at the end, a warp adds its
 // sums to the block's in shared memory as int32, whose order does not matter.
+//
+// One GB300, channels x depth, GPU time a call: 1 x 4096 x 4096 in 5.8 us (2.9
+// TB/s: of its 2.5 us of bytes and 2.2 of a launch, the rest is one wave of
+// blocks finding its first codes), 8 x 14336 x 4096 in 10.7 us (5.5 TB/s), 16
+// in 17, 32 in 24 (bound by turning codes: registers hold eight warps an SM).
 #include "int8_load.h"
 
 namespace echo {

@@ -25,6 +25,11 @@
 // of int8 codes written and read, 32 KB of their f16 written and read): 1280
 // cycles at 128 bytes a cycle, for 1024 of matrix instructions.
 //
+// One GB300: 8192 x 14336 x 4096 in 508 us, 1895 TFLOP/s of products (bound by
+// the matrix instructions: cuBLAS' f16 product reaches 1920); 4 x 2048 x 4096
+// x 1024 in 57 us, 1210 (one chunk a tile: its 128 KB of results take the
+// takers as long as its products take the tensor cores).
+//
 // Where there are fewer tiles than pairs of SMs, SPLIT pairs in a cluster share
 // a tile's depth.  Their sums are int32, so their order does not matter: each
 // pair writes those of the columns that it does not own into the owner's
@@ -196,8 +201,9 @@ __device__ __forceinline__ void scale_sums(float (&sum)[16], uint32_t scales, fl
 
 // Each lane has UNITS times 32 bytes of its own token's row; after this it has
 // unit lane % UNITS of the rows of its UNITS lanes (in order), so that these
-// store a row's UNITS * 32 bytes together.  A store takes its time by the lines
-// it touches: STORE_US.
+// store a row's UNITS * 32 bytes together: a store takes its time by the lines
+// it touches, and lanes that each store their own row touch 32 (4 x 2048 x
+// 4096 x 1024: 61 us, exchanged 57).
 template <int UNITS>
 __device__ __forceinline__ void exchange_units(uint32_t (&w)[8 * UNITS], int lane) {
 #pragma unroll
@@ -699,7 +705,8 @@ cudaError_t launch_pair<ECHO_ELEM>(const ProductArgs& p, const ProductLayout& l,
   t.per_rank = t.rows * t.cols;
   t.total = (int)total;
   // Pairs that share a tile's depth, where the clusters all run at once and
-  // each pair has two stages at least.  SPLIT_US.
+  // each pair has two stages at least.  256 x 4096 x 4096, 16 tiles: alone
+  // 25 us, two to a tile 21; four do not fit at once, and take 34.
   const int64_t stages = wide_blocks(p.depth);
   int room = 0;
   if (total * 2 <= l.sms / 2 && stages >= 8) {

@@ -21,6 +21,11 @@
 // row; and with one gate row for all, or while a gate row lasts, only
 // A = sum D a (and sum D) are kept, of which dw_post is scale gate A and dgate
 // is scale (w_post A + b_post sum D).
+//
+// One GB300, bf16, RMS: 8192 x 4096 in 74 us, 5.4 TB/s, 0.80 of the copy rate,
+// both kernels; 32768 x 4096 with a gate a token 340 us (a third row sum).
+// Layer norms 109 us (twice the sums, eight elements a thread).  Bound by
+// instructions and the row sums' latency at 16 warps an SM.
 #include "norm_common.h"
 
 namespace echo {
