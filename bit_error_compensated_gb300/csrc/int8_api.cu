@@ -192,6 +192,12 @@ int echo_matmul_status(void* stream, int* status) {
   return ECHO_OK;
 }
 
+int echo_debug_hold_product(int on) {
+  if (on != 0 && on != 1) return ECHO_ERR_ARG;
+  set_product_hold(on);
+  return ECHO_OK;
+}
+
 int echo_linear_int8(int64_t ranks, int64_t tokens, int64_t channels, int64_t depth, int dtype,
                      const echo_matrix* x, const echo_matrix* w, const float* w_scales,
                      int64_t w_scale_stride, const echo_matrix* codes, float* a_scales,

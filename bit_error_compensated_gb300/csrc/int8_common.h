@@ -59,6 +59,7 @@ __device__ __forceinline__ float scaled_sum(float sum, float token, float channe
 struct ProductLayout {
   int out_align;                 // rows of out start on multiples of 32, 16, 4 or (1) fewer bytes
   int sms;
+  int hold;                      // echo_debug_hold_product
 };
 
 cudaError_t launch_quantize(const QuantArgs& a, int dtype, cudaStream_t s);
@@ -69,6 +70,8 @@ cudaError_t launch_realign(const ProductArgs& p, int8_t* to, int64_t ld, cudaStr
 // `quantized`: this call's quantizer ran just before, and has left the tokens'
 // f16 codes in the workspace where the product needs them.
 cudaError_t launch_product(const ProductArgs& a, bool quantized, cudaStream_t s);
+// Test hook: whether later products of many tokens hold a report back.
+void set_product_hold(int on);
 // `early`: the kernel before is this call's quantizer, see int8_few.cu.
 cudaError_t launch_few(const ProductArgs& p, bool aligned, bool early, cudaStream_t s);
 // One instantiation per type of out (the sources are compiled once for each).

@@ -69,6 +69,7 @@ __device__ int g_gave_up;
 
 struct Tiles {
   int rows, cols, per_rank, total;      // of 256 tokens, BN channels
+  int hold;                             // test hook: the first block never reports a stage
 };
 
 struct Place {
@@ -172,9 +173,14 @@ __device__ __forceinline__ void load_box(uint32_t to, const CUtensorMap* map, in
       :: "r"(to), "l"(map), "r"(k), "r"(c), "r"(rank), "r"(bar) : "memory");
 }
 
-// Among the takers' warps.
-__device__ __forceinline__ void takers_sync() {
-  asm volatile("bar.sync 1, %0;" :: "n"(32 * kTakers) : "memory");
+// Among the takers' warps; whether all of them are fine.
+__device__ __forceinline__ bool takers_all(bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all) : "r"((uint32_t)ok), "n"(32 * kTakers) : "memory");
+  return all != 0;
 }
 
 __device__ __forceinline__ void cluster_sync() {
@@ -467,7 +473,7 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int out_align,
           ok = __all_sync(0xFFFFFFFFu, wait_on(landed + 8 * slot, phase, &give_up));
         if (!ok) break;
         __syncwarp();
-        if (lane == 0) arrive_first(full + 8 * slot, first_rank);
+        if (lane == 0 && !(tiles.hold && blockIdx.x == 0 && warp == kTakers)) arrive_first(full + 8 * slot, first_rank);
         slot += kGroups;
         if (slot >= kStages) {
           slot -= kStages;
@@ -487,7 +493,11 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int out_align,
     uint32_t chunk = 0;
     bool ok = true;
     const uint32_t my_tmem = tmem + ((uint32_t)(warp & 3) << 21) + (uint32_t)(warp >> 2) * kCols;
-    for (int tile = pair; tile < tiles.total && ok; tile += pairs) {
+    for (int tile = pair; tile < tiles.total; tile += pairs) {
+      // The last tile's scales have been used; and if a warp has given up, all
+      // leave here, so that no one waits for it at the barriers.
+      ok = takers_all(ok);
+      if (!ok) break;
       const Place at = place_of(tiles, tile);
       const int r = (warp & 3) * 32 + lane, col0 = (warp >> 2) * kCols;     // in the block's tile
       const int64_t t = (int64_t)at.row * 256 + half * kRows + r;
@@ -500,9 +510,8 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int out_align,
       const float token = there ? __ldg(p.a_scales + at.rank * p.rank_a_scales + t) : 0.f;
       T* out = static_cast<T*>(p.out) + at.rank * p.rank_out;
       const int64_t t0 = t - lane % kUnits, u0 = c0 + lane % kUnits * (kLine / kUnits);   // of the units this lane stores
-      takers_sync();                   // the last tile's scales have been used
       channel_scales[tid] = channel;
-      takers_sync();
+      takers_all(true);
       const uint32_t my_scales = smem_addr(channel_scales) + 4 * col0;
       for (int c = 0; c < chunks; ++c, ++chunk) {
         const uint32_t b = chunk & 1;
@@ -572,10 +581,10 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int out_align,
           }
         }
       }
-      if (!ok) break;
       if constexpr (!ONE) {
 #pragma unroll
         for (int j = 0; j < kCols; j += kLine) {
+          if (!ok) break;
           if (SPLIT > 1 && (col0 + j) / (BN / SPLIT) != split) continue;
           uint32_t words[8 * kUnits];
 #pragma unroll
@@ -601,7 +610,7 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int out_align,
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(2 * BN) : "memory");
 }
 
-// The driver's encoder of tensor maps, looked up once.
+// CUDA's encoder of tensor maps, looked up once.
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -704,6 +713,7 @@ cudaError_t launch_pair<ECHO_ELEM>(const ProductArgs& p, const ProductLayout& l,
   if (total > 0x7FFFFFFF) return cudaErrorInvalidValue;       // past any memory's results
   t.per_rank = t.rows * t.cols;
   t.total = (int)total;
+  t.hold = l.hold;
   // Pairs that share a tile's depth, where the clusters all run at once and
   // each pair has two stages at least.  256 x 4096 x 4096, 16 tiles: alone
   // 25 us, two to a tile 21; four do not fit at once, and take 34.

@@ -12,9 +12,16 @@ Workspace product_workspace(const ProductArgs& p) {
   return w;
 }
 
+namespace {
+std::atomic<int> g_hold{0};
+}
+
+void set_product_hold(int on) { g_hold.store(on, std::memory_order_relaxed); }
+
 cudaError_t launch_product(const ProductArgs& given, bool quantized, cudaStream_t s) {
   ProductArgs p = given;
   ProductLayout l;
+  l.hold = g_hold.load(std::memory_order_relaxed);
   cudaError_t e = device_sms(&l.sms);
   if (e != cudaSuccess) return e;
   const bool w_aligned = rows_aligned(p.w, p.ld_w, p.rank_w, p.channels, p.ranks);

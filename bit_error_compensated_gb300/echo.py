@@ -92,6 +92,7 @@ _SIGS = {
                                 _vp, _sz, _vp]),
     "echo_matmul_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _vp, _vp]),
     "echo_matmul_status": (_i32, [_vp, ctypes.POINTER(_i32)]),
+    "echo_debug_hold_product": (_i32, [_i32]),
     "echo_linear_int8": (_i32, [_i64, _i64, _i64, _i64, _i32, _vp, _vp, _vp, _i64, _vp, _vp, _vp,
                                 _vp, _sz, _vp]),
     "echo_strerror": (ctypes.c_char_p, [_i32]),
@@ -661,6 +662,10 @@ def echo_matmul_status(stream=None) -> int:
     st = _i32(0)
     _check(_lib.echo_matmul_status(_stream(stream), ctypes.byref(st)), "echo_matmul_status")
     return st.value
+
+
+def echo_debug_hold_product(on: bool) -> None:
+    _check(_lib.echo_debug_hold_product(1 if on else 0), "echo_debug_hold_product")
 
 
 def echo_linear_int8(x, w, w_scales, out, codes, scales, stream=None) -> None:

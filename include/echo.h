@@ -559,6 +559,15 @@ size_t echo_matmul_workspace_bytes(int64_t ranks, int64_t tokens, int64_t channe
 int echo_matmul_status(void* stream, int* status);
 
 /*
+ * echo_debug_hold_product -- test hook for the bounded waits of the products:
+ * with on = 1, in every later product of more than 32 tokens one warp of the
+ * first block never reports its work, so the waits on it run until their bound
+ * and echo_matmul_status reports ECHO_ERR_TIMEOUT.  0 (the default) turns the
+ * hook off.  ECHO_ERR_ARG for other values.
+ */
+int echo_debug_hold_product(int on);
+
+/*
  * echo_linear_int8 -- echo_quantize_tokens of x into codes and a_scales
  * ([ranks][tokens], contiguous), then echo_matmul_int8: the same bits.  x and out have the type dtype.
  */

@@ -96,6 +96,7 @@ def test_product_arguments_are_checked_before_any_cuda_call(lib):
     assert status(tokens=33, workspace=base * 9, nbytes=100) == echo.ECHO_ERR_TOO_LARGE
     assert status(tokens=33, workspace=base * 9 + 8, nbytes=1 << 20) == echo.ECHO_ERR_ALIGN
     assert echo._lib.echo_matmul_status(None, None) == echo.ECHO_ERR_ARG
+    assert echo._lib.echo_debug_hold_product(2) == echo.ECHO_ERR_ARG
 
 
 def test_workspace_bytes():

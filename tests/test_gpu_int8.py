@@ -295,3 +295,27 @@ def test_refusals():
             ("shape", echo.echo_linear_int8, (x, w, sw, out, a[:4], sa))):
         with pytest.raises(ValueError, match=word):
             call(*args)
+
+
+@pytest.mark.parametrize("shape", [(300, 5000, 1024), (300, 5000, 2048), (256, 512, 2048)])
+def test_a_wait_that_runs_out_ends_the_call(shape):
+    """One block never reports its work (the hold hook): every wait on it gives
+    up after its second, the call ends, the status says so, and the next call
+    is exact again.  Shapes of each form: one chunk, several, a shared tile."""
+    from bit_error_compensated_gb300 import echo
+    M, N, K = shape
+    gen = gen_of(M)
+    a, w = codes_of(gen, M, K), codes_of(gen, N, K)
+    sa, sw = torch.rand(M, generator=gen, device="cuda"), torch.rand(N, generator=gen, device="cuda")
+    out = torch.empty(M, N, device="cuda")
+    assert echo.echo_matmul_status() == echo.ECHO_OK
+    echo.echo_debug_hold_product(True)
+    try:
+        echo.echo_matmul_int8(a, sa, w, sw, out)
+        assert echo.echo_matmul_status() == echo.ECHO_ERR_TIMEOUT
+    finally:
+        echo.echo_debug_hold_product(False)
+    assert echo.echo_matmul_status() == echo.ECHO_OK
+    echo.echo_matmul_int8(a, sa, w, sw, out)
+    same_bits(out, want_product(a, sa, w, sw, F32))
+    assert echo.echo_matmul_status() == echo.ECHO_OK
