@@ -91,6 +91,17 @@ struct StreamSums {
   }
 };
 
+// A running sum that keeps what each addition rounds off (Kahan), for the few
+// sums that run over all rows or workers one after another.
+struct CarefulSum {
+  float sum = 0.f, lost = 0.f;
+  __device__ __forceinline__ void add(float v) {
+    const float y = __fsub_rn(v, lost), t = __fadd_rn(sum, y);
+    lost = __fsub_rn(__fsub_rn(t, sum), y);
+    sum = t;
+  }
+};
+
 // Rows ahead in the ring of asynchronous copies: 128 KB for a full block.  E:
 // elements of a row a thread has, 8 or 16.
 template <typename T, int E> constexpr int rows_ahead() { return 64 / (E * (int)sizeof(T)); }
@@ -253,7 +264,7 @@ norm_grad_kernel(const NormGradArgs a, int blocks, int block_cols) {
       if (GATE == 1 && SUM0) sum_bpost[j][i] = 0.f;
       if (LAYER) sum_bpre[j][i] = 0.f;
     }
-  float sum_scalar = 0.f;
+  CarefulSum sum_scalar;
   int64_t gate_row = 0, gate_left = 0;
   bool gate_whole = false;             // the gate row's first row is this worker's
   if (GATE != 0) {
@@ -437,7 +448,7 @@ norm_grad_kernel(const NormGradArgs a, int blocks, int block_cols) {
     // before its range goes to the worker's first slot, of one that goes on
     // behind it to the second, for norm_grad_finish.
     if (GATE != 0 && active) {
-      if (GATE == 2) sum_scalar += t[kScalar < (int)(sizeof(t) / sizeof(float)) ? kScalar : 0];
+      if (GATE == 2) sum_scalar.add(t[kScalar < (int)(sizeof(t) / sizeof(float)) ? kScalar : 0]);
       if (--gate_left == 0 || row + 1 == row1) {
         const bool direct = gate_whole && gate_left == 0;
         const int64_t cols = GATE == 1 ? a.width : 1;
@@ -474,11 +485,11 @@ norm_grad_kernel(const NormGradArgs a, int blocks, int block_cols) {
           }
         } else {
           if (a.dgate && tid == 0 && part == 0) {
-            if (!direct) part_of[0] = sum_scalar;
-            else if (a.params_f32) static_cast<float*>(a.dgate)[gate_row] = sum_scalar;
-            else static_cast<T*>(a.dgate)[gate_row] = from_float<T>(sum_scalar);
+            if (!direct) part_of[0] = sum_scalar.sum;
+            else if (a.params_f32) static_cast<float*>(a.dgate)[gate_row] = sum_scalar.sum;
+            else static_cast<T*>(a.dgate)[gate_row] = from_float<T>(sum_scalar.sum);
           }
-          sum_scalar = 0.f;
+          sum_scalar = CarefulSum();
         }
         if (gate_left == 0) {
           ++gate_row;
@@ -540,8 +551,9 @@ norm_grad_finish(const NormGradArgs a) {
     part[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
     if (threadIdx.y == 0) {
-      s = part[0][threadIdx.x];
-      for (int i = 1; i < kFinishRows; ++i) s += part[i][threadIdx.x];
+      CarefulSum all;
+      for (int i = 0; i < kFinishRows; ++i) all.add(part[i][threadIdx.x]);
+      s = all.sum;
     }
     return s;
   };
@@ -574,10 +586,11 @@ norm_grad_finish(const NormGradArgs a) {
     const int64_t g = b * a.span / a.gate_span, begin = g * a.gate_span, end = begin + a.gate_span;
     if (begin == b * a.span || begin < (b - 1) * a.span) continue;
     const int64_t last = (end + a.span - 1) / a.span < a.workers ? (end + a.span - 1) / a.span : a.workers;
-    float s = a.gate_partial[(2 * (b - 1) + 1) * cols + col];
+    CarefulSum s;
+    s.add(a.gate_partial[(2 * (b - 1) + 1) * cols + col]);
 #pragma unroll 8
-    for (int64_t w = b; w < last; ++w) s += a.gate_partial[2 * w * cols + col];
-    put(a.dgate, g * cols + col, s);
+    for (int64_t w = b; w < last; ++w) s.add(a.gate_partial[2 * w * cols + col]);
+    put(a.dgate, g * cols + col, s.sum);
   }
 }
 

@@ -173,6 +173,26 @@ def test_gate_without_its_gradient(gate):
     assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
 
 
+@pytest.mark.parametrize("rows", [40000, 65000])
+def test_gradient_of_a_gate_that_all_rows_share(rows):
+    """One scalar gate for every row.  A row's term is exact (16 values of 20
+    bits), so what is left is the sum over rows: compensated twice, within a
+    worker and over the workers, at most two unit roundoffs of 2^-24 each.  A
+    plain running sum is up to 3e-6 to 8e-6 off on these terms."""
+    from bit_error_compensated_gb300 import echo
+    width, value = 16, 1 + 2 ** -17 + 2 ** -19
+    x = torch.zeros(rows, width, device="cuda")
+    y, dr = torch.full_like(x, value), torch.ones_like(x)
+    gate, dgate = torch.ones(1, 1, device="cuda"), torch.empty(1, 1, device="cuda")
+    v = {"x": x, "y": y, "gate": gate}
+    p = {"w_pre": torch.ones(width, device="cuda")}
+    plan, params, _, _, stats, _, _ = call_forward(v, p, width, F32, F32, RMS, False, 1.0)
+    echo.echo_norm_backward(plan, params, x, y, stats, dr, None, torch.empty_like(x),
+                            torch.empty_like(x), gate=gate, dgate=dgate)
+    exact = rows * width * value
+    assert abs(dgate.double().item() - exact) <= 2 ** -22 * exact
+
+
 @pytest.mark.parametrize("kind,post", list(itertools.product([RMS, LAYER], [True, False])))
 def test_gradient_against_differences(kind, post):
     """The derivative along a random direction of every input at once, by
