@@ -73,7 +73,7 @@ cudaError_t launch_product(const ProductArgs& a, bool quantized, cudaStream_t s)
 // Test hook: whether later products of many tokens hold a report back.
 void set_product_hold(int on);
 // `early`: the kernel before is this call's quantizer, see int8_few.cu.
-cudaError_t launch_few(const ProductArgs& p, bool aligned, bool early, cudaStream_t s);
+cudaError_t launch_few(const ProductArgs& p, bool aligned, bool early, int sms, cudaStream_t s);
 // One instantiation per type of out (the sources are compiled once for each).
 template <typename T>
 cudaError_t launch_pair(const ProductArgs& p, const ProductLayout& l, cudaStream_t s);

@@ -13,9 +13,8 @@
 // sums are exact for 1024 codes; after those, and at the end, a warp adds its
 // sums to the block's in shared memory as int32, whose order does not matter.
 //
-// One GB300, channels x depth, GPU time a call: 1 x 4096 x 4096 in 5.8 us (2.9
-// TB/s: of its 2.5 us of bytes and 2.2 of a launch, the rest is one wave of
-// blocks finding its first codes), 8 x 14336 x 4096 in 10.7 us (5.5 TB/s), 16
+// One GB300, GPU time a call: 1 x 4096 x 4096 in 4.6 us (3.6 TB/s: its 2.5 us
+// of bytes and about 2.2 of a launch), 8 x 14336 x 4096 in 10.7 us (5.5 TB/s), 16
 // in 17, 32 in 24 (bound by turning codes: registers hold eight warps an SM).
 #include "int8_load.h"
 
@@ -193,8 +192,14 @@ cudaError_t launch(const ProductArgs& p, bool aligned, bool early, cudaStream_t 
 
 }  // namespace
 
-cudaError_t launch_few(const ProductArgs& p, bool aligned, bool early, cudaStream_t s) {
-  if (p.tokens <= 8) return launch<1, 1, 4>(p, aligned, early, s);
+cudaError_t launch_few(const ProductArgs& p, bool aligned, bool early, int sms, cudaStream_t s) {
+  // Eight windows at once leave registers for two blocks an SM: with no more
+  // blocks than that, a block's time is its loads' latency (1 x 4096 x 4096:
+  // 4.6 us, with four 5.8); with more, three blocks an SM keep more loads in
+  // flight (8 x 6144 x 4096: 6.3 us, with eight 7.0).
+  if (p.tokens <= 8)
+    return (p.channels + 15) / 16 * p.ranks <= 2 * sms ? launch<1, 1, 8>(p, aligned, early, s)
+                                                       : launch<1, 1, 4>(p, aligned, early, s);
   if (p.tokens <= 16) return launch<2, 1, 4>(p, aligned, early, s);
   return launch<4, 2, 2>(p, aligned, early, s);
 }

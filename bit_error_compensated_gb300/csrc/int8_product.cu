@@ -26,7 +26,7 @@ cudaError_t launch_product(const ProductArgs& given, bool quantized, cudaStream_
   if (e != cudaSuccess) return e;
   const bool w_aligned = rows_aligned(p.w, p.ld_w, p.rank_w, p.channels, p.ranks);
   if (p.tokens <= kFewTokens || p.depth == 0)
-    return launch_few(p, w_aligned && rows_aligned(p.a, p.ld_a, p.rank_a, p.tokens, p.ranks), quantized, s);
+    return launch_few(p, w_aligned && rows_aligned(p.a, p.ld_a, p.rank_a, p.tokens, p.ranks), quantized, l.sms, s);
   const int64_t size = elem_size(p.out_dtype);
   for (l.out_align = 32; l.out_align > 1; l.out_align = l.out_align == 32 ? 16 : l.out_align == 16 ? 4 : 1)
     if (on_boundary(p.out, l.out_align) && (p.tokens == 1 || p.ld_out * size % l.out_align == 0) &&

@@ -569,7 +569,9 @@ int echo_debug_hold_product(int on);
 
 /*
  * echo_linear_int8 -- echo_quantize_tokens of x into codes and a_scales
- * ([ranks][tokens], contiguous), then echo_matmul_int8: the same bits.  x and out have the type dtype.
+ * ([ranks][tokens], contiguous), then echo_matmul_int8: the same bits.  x and out have the type dtype;
+ * workspace as for echo_matmul_int8, with the codes as its a.  codes and a_scales
+ * must not overlap x, w or w_scales (ECHO_ERR_ARG).
  */
 int echo_linear_int8(int64_t ranks, int64_t tokens, int64_t channels, int64_t depth, int dtype,
                      const echo_matrix* x, const echo_matrix* w, const float* w_scales,
