@@ -205,13 +205,13 @@ __device__ __forceinline__ void scale_sums(float (&sum)[16], uint32_t scales, fl
   for (int i = 0; i < (int)sizeof(out) / 4; ++i) words[i] = reinterpret_cast<const uint32_t*>(&out)[i];
 }
 
-// Each lane has UNITS times 32 bytes of its own token's row; after this it has
-// unit lane % UNITS of the rows of its UNITS lanes (in order), so that these
-// store a row's UNITS * 32 bytes together: a store takes its time by the lines
-// it touches, and lanes that each store their own row touch 32 (4 x 2048 x
-// 4096 x 1024: 61 us, exchanged 57).
-template <int UNITS>
-__device__ __forceinline__ void exchange_units(uint32_t (&w)[8 * UNITS], int lane) {
+// Each lane has UNITS units of WORDS words of its own token's row; after this it
+// has unit lane % UNITS of the rows of its UNITS lanes (in order), so that these
+// store a row's part together: a store takes its time by the lines it touches,
+// and lanes that each store their own row touch 32 (4 x 2048 x 4096 x 1024:
+// 61 us, units of 32 bytes exchanged 57).
+template <int UNITS, int WORDS>
+__device__ __forceinline__ void exchange_units(uint32_t (&w)[WORDS * UNITS], int lane) {
 #pragma unroll
   for (int step = 1; step < UNITS; step *= 2) {
     const bool high = lane & step;
@@ -219,8 +219,8 @@ __device__ __forceinline__ void exchange_units(uint32_t (&w)[8 * UNITS], int lan
     for (int u = 0; u < UNITS; ++u) {
       if (u & step) continue;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        uint32_t &a = w[8 * u + k], &b = w[8 * (u + step) + k];
+      for (int k = 0; k < WORDS; ++k) {
+        uint32_t &a = w[WORDS * u + k], &b = w[WORDS * (u + step) + k];
         const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, high ? a : b, step);
         if (high) a = got;
         else b = got;
@@ -229,31 +229,60 @@ __device__ __forceinline__ void exchange_units(uint32_t (&w)[8 * UNITS], int lan
   }
 }
 
-// Unit lane % UNITS, at channel c, of UNITS rows from token t.  `align`: the
-// bytes on whose multiples out's rows start (32, 16, 4 or fewer).
-template <typename T, int UNITS>
-__device__ __forceinline__ void store_units(const ProductArgs& p, T* out, int64_t t, int64_t c,
-                                            const uint32_t (&w)[8 * UNITS], int align) {
-  constexpr int kUnit = 32 / sizeof(T);
+// Stores the lanes' rows, 8 UNITS words of each from channel c, of which the
+// first lane's is token t - lane.  `align`: the bytes on whose multiples out's
+// rows start (32, 16, 4 or fewer).  Rows on 16 bytes go in units of 32 bytes;
+// others, where a unit takes 16 stores that each touch a sector, BY_WORD with a
+// row's words from neighbouring lanes (9578 x 7999 x 512: 528 us in units, 115
+// by word).  A kernel that holds 128 sums a thread has no registers for that
+// second way (8192 x 14336 x 4096: 490 us without it, 680 with) and less to win,
+// as it stores once in several chunks (4 x 544 x 1587 x 8192: 144 us, 130).
+template <typename T, int UNITS, bool BY_WORD>
+__device__ __forceinline__ void store_rows(const ProductArgs& p, T* out, int64_t t, int64_t c, int lane,
+                                           uint32_t (&w)[8 * UNITS], int align) {
+  if (!BY_WORD || align >= 16) {
+    constexpr int kUnit = 32 / sizeof(T);
+    exchange_units<UNITS, 8>(w, lane);
+    t -= lane % UNITS;
+    c += lane % UNITS * kUnit;
 #pragma unroll
-  for (int i = 0; i < UNITS; ++i) {
-    if (t + i >= p.tokens) break;
-    T* to = out + (t + i) * p.ld_out + c;
-    const bool whole = c + kUnit <= p.channels;
-    if (whole && align == 32) {
-      store32(to, reinterpret_cast<const uint32_t(*)[8]>(w)[i]);
-    } else if (whole && align == 16) {
+    for (int i = 0; i < UNITS; ++i) {
+      if (t + i >= p.tokens) break;
+      T* to = out + (t + i) * p.ld_out + c;
+      const bool whole = c + kUnit <= p.channels;
+      if (whole && align == 32) {
+        store32(to, reinterpret_cast<const uint32_t(*)[8]>(w)[i]);
+      } else if (whole && align == 16) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        reinterpret_cast<uint4*>(to)[e] = make_uint4(w[8 * i + 4 * e], w[8 * i + 4 * e + 1], w[8 * i + 4 * e + 2],
-                                                     w[8 * i + 4 * e + 3]);
-    } else if (whole && align == 4) {
+        for (int e = 0; e < 2; ++e)
+          reinterpret_cast<uint4*>(to)[e] = make_uint4(w[8 * i + 4 * e], w[8 * i + 4 * e + 1], w[8 * i + 4 * e + 2],
+                                                       w[8 * i + 4 * e + 3]);
+      } else if (!BY_WORD && whole && align == 4) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) reinterpret_cast<uint32_t*>(to)[e] = w[8 * i + e];
-    } else {
+        for (int e = 0; e < 8; ++e) reinterpret_cast<uint32_t*>(to)[e] = w[8 * i + e];
+      } else {
 #pragma unroll
-      for (int e = 0; e < kUnit; ++e)
-        if (c + e < p.channels) to[e] = reinterpret_cast<const T*>(w)[i * kUnit + e];
+        for (int e = 0; e < kUnit; ++e)
+          if (c + e < p.channels) to[e] = reinterpret_cast<const T*>(w)[i * kUnit + e];
+      }
+    }
+  } else {
+    constexpr int kWords = 8 * UNITS, kWord = 4 / sizeof(T);
+    exchange_units<kWords, 1>(w, lane);
+    t -= lane % kWords;
+    c += lane % kWords * kWord;
+    if (c >= p.channels) return;
+    T* to = out + t * p.ld_out + c;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i, to += p.ld_out) {
+      if (t + i >= p.tokens) break;
+      if (align == 4 && c + kWord <= p.channels) {
+        *reinterpret_cast<uint32_t*>(to) = w[i];
+      } else {
+#pragma unroll
+        for (int e = 0; e < kWord; ++e)
+          if (c + e < p.channels) to[e] = reinterpret_cast<const T*>(w)[i * kWord + e];
+      }
     }
   }
 }
@@ -509,7 +538,6 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int out_align,
                                 ? __ldg(p.w_scales + at.rank * p.rank_w_scales + (int64_t)at.col * BN + tid) : 0.f;
       const float token = there ? __ldg(p.a_scales + at.rank * p.rank_a_scales + t) : 0.f;
       T* out = static_cast<T*>(p.out) + at.rank * p.rank_out;
-      const int64_t t0 = t - lane % kUnits, u0 = c0 + lane % kUnits * (kLine / kUnits);   // of the units this lane stores
       channel_scales[tid] = channel;
       takers_all(true);
       const uint32_t my_scales = smem_addr(channel_scales) + 4 * col0;
@@ -528,8 +556,7 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int out_align,
               tmem_load16(my_tmem + b * BN + j + n, v);
               scale_sums<T>(v, my_scales + 4 * (j + n), token, words + n * sizeof(T) / 4);
             }
-            exchange_units<kUnits>(words, lane);
-            store_units<T, kUnits>(p, out, t0, u0 + j, words, out_align);
+            store_rows<T, kUnits, ONE>(p, out, t, c0 + j, lane, words, out_align);
           }
         } else {
 #pragma unroll
@@ -594,8 +621,7 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int out_align,
             for (int i = 0; i < 16; ++i) v[i] = __int2float_rn(sum[j + n + i]);
             scale_sums<T>(v, my_scales + 4 * (j + n), token, words + n * sizeof(T) / 4);
           }
-          exchange_units<kUnits>(words, lane);
-          store_units<T, kUnits>(p, out, t0, u0 + j, words, out_align);
+          store_rows<T, kUnits, ONE>(p, out, t, c0 + j, lane, words, out_align);
         }
       }
     }
