@@ -165,6 +165,25 @@ def test_strides_and_alignment(tokens, pad, offset):
     assert (flat[:offset] == 7).all() and (rest == 7).all()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("tokens,channels,depth", [(33, 513, 1024), (257, 259, 17), (300, 516, 640), (511, 1022, 96),
+                                                   (290, 130, 1025), (700, 65, 2000)])
+@pytest.mark.parametrize("pad,offset", [(0, 0), (1, 1), (2, 2), (5, 4), (8, 0)])
+def test_results_in_rows_of_any_place(dtype, tokens, channels, depth, pad, offset):
+    """Rows of results that start on any element, and nothing written beside them."""
+    from bit_error_compensated_gb300 import echo
+    gen, ld = gen_of(tokens + channels), channels + pad
+    a, w = codes_of(gen, 2, tokens, depth), codes_of(gen, 2, channels, depth)
+    sa = torch.rand(2, tokens, generator=gen, device="cuda") * 0.01
+    sw = torch.rand(2, channels, generator=gen, device="cuda") * 0.01
+    base = torch.full((offset + 2 * tokens * ld + 64,), 7.0, dtype=dtype, device="cuda")
+    rows = base[offset:offset + 2 * tokens * ld].view(2, tokens, ld)
+    echo.echo_matmul_int8(a, sa, w, sw, rows[..., :channels])
+    same_bits(rows[..., :channels].clone(), want_product(a, sa, w, sw, dtype))
+    rows[..., :channels] = 7.0
+    assert bool((base == 7.0).all())
+
+
 @pytest.mark.parametrize("tokens", [3, 50, 300])
 def test_operands_shared_by_the_ranks(tokens):
     from bit_error_compensated_gb300 import echo
