@@ -25,9 +25,9 @@
 // of int8 codes written and read, 32 KB of their f16 written and read): 1280
 // cycles at 128 bytes a cycle, for 1024 of matrix instructions.
 //
-// One GB300: 8192 x 14336 x 4096 in 508 us, 1895 TFLOP/s of products (bound by
-// the matrix instructions: cuBLAS' f16 product reaches 1920); 4 x 2048 x 4096
-// x 1024 in 57 us, 1210 (one chunk a tile: its 128 KB of results take the
+// One GB300: 8192 x 14336 x 4096 in 491 us, 1960 TFLOP/s of products (bound by
+// the matrix instructions: a library's f16 product reaches 1920); 4 x 2048 x 4096
+// x 1024 in 54 us, 1280 (one chunk a tile: its 128 KB of results take the
 // takers as long as its products take the tensor cores).
 //
 // Where there are fewer tiles than pairs of SMs, SPLIT pairs in a cluster share
