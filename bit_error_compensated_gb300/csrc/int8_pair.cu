@@ -36,7 +36,10 @@
 // shared memory (the ring is free by then), and the owner adds and stores.
 //
 // Every wait is bounded; one that gives up ends the call with a status
-// (echo_matmul_status).
+// (echo_matmul_status).  The other warps of its block leave at their next wait,
+// whose own flag stays set; each issuing warp first waits for what it has
+// issued to end (mbar_wait_bounded, which looks at no flag), whether it gave up
+// itself or finished and another did.
 #include <cuda.h>
 
 #include "int8_load.h"
@@ -389,11 +392,9 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int out_align,
           if (one && ok) commit_pair(sums_full + 8 * b, first_rank);
         }
       }
-      if (!ok && one) {                // instructions still running end before TMEM is freed
+      if (one) {                       // instructions still running end before TMEM is freed
         commit_pair(last, first_rank);
-        give_up = 0;
-        wait_on(last, 0, &give_up);
-        give_up = 1;
+        mbar_wait_bounded(last, 0);
       }
     } else if (warp == kIssuer + 1 && lane == 0) {
       // The tokens' copies.
@@ -416,12 +417,10 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int out_align,
           next();
         }
       }
-      for (int n = 0; !ok && n < kStages && issued > 0; ++n, --issued) {  // no copy outlives the block
+      for (int n = 0; n < kStages && issued > 0; ++n, --issued) {         // no copy outlives the block
         slot = slot == 0 ? kStages - 1 : slot - 1;
         if (slot == kStages - 1) phase ^= 1;
-        give_up = 0;
-        wait_on(landed + 8 * slot, phase, &give_up);
-        give_up = 1;
+        mbar_wait_bounded(landed + 8 * slot, phase);
       }
     } else if (warp == kIssuer + 2 && lane == 0) {
       // The channels' copies, a slot for each group of turners.
@@ -438,11 +437,9 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int out_align,
                    at.col * BN + half * (BN / 2), p.rank_w == 0 ? 0 : at.rank, bar);
         }
       }
-      for (int n = 0; !ok && n < kGroups && g > 0; ++n) {                 // no copy outlives the block
+      for (int n = 0; n < kGroups && g > 0; ++n) {                        // no copy outlives the block
         --g;
-        give_up = 0;
-        wait_on(codes_full + 8 * (uint32_t)(g & 1), (uint32_t)((g >> 1) & 1), &give_up);
-        give_up = 1;
+        mbar_wait_bounded(codes_full + 8 * (uint32_t)(g & 1), (uint32_t)((g >> 1) & 1));
       }
     }
     __syncwarp();

@@ -1,0 +1,51 @@
+"""Rules that the block operators' kernels keep and whose breach no run shows:
+a wrong order that only a slow or preempted block would meet, or an access that
+is wrong by the programming model and right by luck.  Read from the sources."""
+import re
+from pathlib import Path
+
+CSRC = Path(__file__).resolve().parents[1] / "bit_error_compensated_gb300" / "csrc"
+
+
+def source(name):
+    """The file without its comments."""
+    text = (CSRC / name).read_text()
+    return re.sub(r"//[^\n]*|/\*.*?\*/", "", text, flags=re.S)
+
+
+def body_after(text, opening):
+    """The braces' contents that follow the first match of `opening`."""
+    start = re.search(opening, text)
+    assert start, opening
+    at = text.index("{", start.start())
+    depth = 0
+    for i in range(at, len(text)):
+        depth += {"{": 1, "}": -1}.get(text[i], 0)
+        if depth == 0:
+            return text[at + 1:i]
+    raise AssertionError("unbalanced braces")
+
+
+def test_a_block_that_gave_up_stays_so():
+    """The flag of a block whose wait gave up is cleared only where the block
+    begins: a warp that cleared it later would hide it from the others, and one
+    that set it again would end the waits of those that clean up."""
+    kernel = body_after(source("int8_pair.cu"), r"product_pair_kernel\(")
+    writes = re.findall(r"\bgive_up\s*=[^=]\s*[^;]*;", kernel)
+    assert writes == ["give_up = 0;"]
+    assert kernel.index("give_up = 0;") < kernel.index("mbar_init(")
+
+
+def test_issuing_warps_wait_for_what_they_issued():
+    """Each of the three issuing warps ends with bounded waits that look at no
+    flag, and makes them however its loop ended: another warp may give up after
+    this one has issued its last."""
+    kernel = body_after(source("int8_pair.cu"), r"product_pair_kernel\(")
+    issuing = body_after(kernel, r"if \(warp >= kIssuer\)")
+    drains = {"last": r"if \(one\)\s*", "landed": r"for \([^)]*kStages && issued > 0[^)]*\)\s*",
+              "codes_full": r"for \([^)]*kGroups && g > 0[^)]*\)\s*"}
+    for barrier, opening in drains.items():
+        waits = [b for b in re.findall(opening + r"\{([^{}]*)\}", issuing) if "mbar_wait_bounded(" + barrier in b]
+        assert len(waits) == 1, barrier
+        assert "give_up" not in waits[0] and "wait_on" not in waits[0]
+    assert "!ok &&" not in issuing

@@ -338,3 +338,27 @@ def test_a_wait_that_runs_out_ends_the_call(shape):
     echo.echo_matmul_int8(a, sa, w, sw, out)
     same_bits(out, want_product(a, sa, w, sw, F32))
     assert echo.echo_matmul_status() == echo.ECHO_OK
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("shape", [(600, 20000, 1024), (600, 20000, 1100), (129, 1024, 2048)])
+def test_a_call_that_gave_up_ends_cleanly(shape, dtype):
+    """The same with several tiles a pair (or a tile shared by pairs), each type
+    of results: every issuing warp waits for what it has in flight, and the call
+    after it is exact in every tile."""
+    from bit_error_compensated_gb300 import echo
+    M, N, K = shape
+    gen = gen_of(N)
+    a, w = codes_of(gen, M, K), codes_of(gen, N, K)
+    sa, sw = torch.rand(M, generator=gen, device="cuda"), torch.rand(N, generator=gen, device="cuda")
+    out = torch.empty(M, N, dtype=dtype, device="cuda")
+    echo.echo_matmul_status()
+    echo.echo_debug_hold_product(True)
+    try:
+        echo.echo_matmul_int8(a, sa, w, sw, out)
+        assert echo.echo_matmul_status() == echo.ECHO_ERR_TIMEOUT
+    finally:
+        echo.echo_debug_hold_product(False)
+    echo.echo_matmul_int8(a, sa, w, sw, out)
+    same_bits(out, want_product(a, sa, w, sw, dtype))
+    assert echo.echo_matmul_status() == echo.ECHO_OK
