@@ -133,6 +133,7 @@ product_few_kernel(const ProductArgs p, const int early) {
       for (int i = 0; i < OCTETS; ++i)
         tokens[d][i] = k < p.depth ? load_codes<ALIGNED>(a[i], k, p.depth) : make_uint4(0, 0, 0, 0);
     }
+    __syncwarp();                      // a row's ragged end parts the lanes; matrix instructions want them together
 #pragma unroll
     for (int d = 0; d < DEEP; ++d) {
       if constexpr (kInteger) {

@@ -155,8 +155,11 @@ __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uin
       :: "r"(d), "l"(a), "l"(b), "r"(desc), "r"(add) : "memory");
 }
 
+// (.aligned: lanes that store rows and columns past the last ones leave a
+// store early, so a warp's are brought together first.)
 __device__ __forceinline__ void tmem_load16(uint32_t at, float (&v)[16]) {
   uint32_t r[16];
+  __syncwarp();
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
       "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
@@ -184,11 +187,6 @@ __device__ __forceinline__ bool takers_all(bool ok) {
       "barrier.cta.red.and.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(all) : "r"((uint32_t)ok), "n"(32 * kTakers) : "memory");
   return all != 0;
-}
-
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
-               "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // 16 exact sums of this lane's token times its scale and the channels' (in
@@ -348,7 +346,7 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int out_align,
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
-  cluster_sync();
+  cluster_barrier();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = tmem_at;
   pdl_wait();
@@ -442,10 +440,9 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int out_align,
         mbar_wait_bounded(codes_full + 8 * (uint32_t)(g & 1), (uint32_t)((g >> 1) & 1));
       }
     }
-    __syncwarp();
     if (SPLIT > 1) {                   // the takers' exchange
-      cluster_sync();
-      cluster_sync();
+      cluster_barrier();
+      cluster_barrier();
     }
   } else if (warp >= kTakers) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kTurnerRegs));
@@ -508,10 +505,9 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int out_align,
       }
     }
     if (!ok && lane == 0) atomicOr(&g_gave_up, 1);
-    __syncwarp();
     if (SPLIT > 1) {
-      cluster_sync();
-      cluster_sync();
+      cluster_barrier();
+      cluster_barrier();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kTakerRegs));
@@ -573,8 +569,7 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int out_align,
       }
       if constexpr (SPLIT > 1) {
         constexpr int kOwn = BN / SPLIT;                // columns of a pair
-        __syncwarp();
-        cluster_sync();                                 // every ring is free
+        cluster_barrier();                              // every ring is free
 #pragma unroll
         for (int j = 0; j < kCols; j += 4) {
           const int owner = (col0 + j) / kOwn;
@@ -588,8 +583,7 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int out_align,
               :: "r"(to), "r"(2 * owner + half), "r"(sum[j]), "r"(sum[j + 1]), "r"(sum[j + 2]), "r"(sum[j + 3])
               : "memory");
         }
-        __syncwarp();
-        cluster_sync();
+        cluster_barrier();
 #pragma unroll
         for (int j = 0; j < kCols; j += 4) {
           if ((col0 + j) / kOwn != split) continue;
@@ -627,7 +621,7 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int out_align,
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
-  cluster_sync();
+  cluster_barrier();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   if (warp == kIssuer)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(2 * BN) : "memory");

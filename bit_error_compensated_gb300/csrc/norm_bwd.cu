@@ -69,8 +69,7 @@ struct StreamSums {
           asm volatile("st.shared::cluster.f32 [%0], %1;" :: "r"(at), "f"(v[k]) : "memory");
         }
       }
-      asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
-                   "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+      cluster_barrier();
     } else {
       if (lane == 0)
 #pragma unroll
@@ -140,9 +139,7 @@ norm_grad_kernel(const NormGradArgs a, int blocks, int block_cols) {
                   tid & 31, blocks, 0};
   for (int i = me; i < 6 * kStreamSlots; i += all_threads) (&slots[0][0][0])[i] = 0.f;
   __syncthreads();
-  if (blocks > 1)                      // every block's slots are ready before the first is written
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
-                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (blocks > 1) cluster_barrier();   // every block's slots are ready before the first is written
   const float inv_width = 1.0f / (float)a.width;
   bool in[NV];
 #pragma unroll
@@ -516,9 +513,7 @@ norm_grad_kernel(const NormGradArgs a, int blocks, int block_cols) {
     }
   }
   // No block of a cluster may end while another can still write to its slots.
-  if (blocks > 1)
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
-                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (blocks > 1) cluster_barrier();
 }
 
 // Adds the workers' column sums: blockIdx.y 0..3 a parameter each (with folded

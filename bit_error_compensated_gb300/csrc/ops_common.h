@@ -148,6 +148,15 @@ __device__ __forceinline__ Pack<T, N> load_shared16(uint32_t at) {
   return *reinterpret_cast<const Pack<T, N>*>(&v);
 }
 
+// A barrier of all threads of a cluster.  Its instructions are .aligned: the
+// lanes of a warp, which may have taken different branches on their way here,
+// have to be together.
+__device__ __forceinline__ void cluster_barrier() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
+               "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // See overlapped_launch below.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() {

@@ -49,3 +49,22 @@ def test_issuing_warps_wait_for_what_they_issued():
         assert len(waits) == 1, barrier
         assert "give_up" not in waits[0] and "wait_on" not in waits[0]
     assert "!ok &&" not in issuing
+
+
+def test_warps_are_together_at_aligned_instructions():
+    """A cluster's barrier, a load from tensor memory and a warp's matrix
+    instruction ask that all lanes of a warp execute them together, and all
+    three stand behind branches that part them.  So the barrier exists once,
+    behind a __syncwarp, the load's function begins with one, and one stands
+    between the loads of codes and the products of them."""
+    files = ["ops_common.h", "norm_common.h", "norm_fwd.cu", "norm_bwd.cu", "int8_common.h", "int8_load.h",
+             "int8_few.cu", "int8_quantize.cu", "int8_pair.cu"]
+    assert sum(source(f).count("barrier.cluster.arrive") for f in files) == 1
+    for name, opening, instruction in (("ops_common.h", r"void cluster_barrier\(\)", "barrier.cluster.arrive"),
+                                       ("int8_pair.cu", r"void tmem_load16\(", "tcgen05.ld")):
+        body = body_after(source(name), opening)
+        assert 0 <= body.find("__syncwarp();") < body.index(instruction)
+    assert source("int8_pair.cu").count("tcgen05.ld") == 1
+    few = body_after(source("int8_few.cu"), r"product_few_kernel\(")
+    loads, sync, products = (few.rindex("load_codes<"), few.rindex("__syncwarp();"), few.index("mma(sum"))
+    assert loads < sync < products
