@@ -10,17 +10,18 @@ namespace echo {
 // of 16).  ALIGNED: rows start on 16-byte boundaries, so all but a ragged last
 // piece is one load.  Otherwise a piece inside the row is put together from
 // the aligned words around it, all of them inside the row too, and only a
-// row's ends go byte by byte.
+// row's ends go byte by byte.  `row` is pinned behind the wait if the kernel
+// before may write the codes.
 template <bool ALIGNED>
 __device__ __forceinline__ uint4 load_codes(const int8_t* row, int64_t k, int64_t depth) {
   const int8_t* p = row + k;
-  if (ALIGNED && k + 16 <= depth) return __ldg(reinterpret_cast<const uint4*>(p));
+  if (ALIGNED && k + 16 <= depth) return load_free16(p);
   if (!ALIGNED && k >= 3 && k + 19 <= depth) {
     uint4 v;
     const uint32_t shift = (uint32_t)((uintptr_t)p & 3) * 8;
     const uint32_t* w = reinterpret_cast<const uint32_t*>((uintptr_t)p & ~(uintptr_t)3);
-    const uint32_t a = __ldg(w), b = __ldg(w + 1), c = __ldg(w + 2), d = __ldg(w + 3);
-    const uint32_t e = shift ? __ldg(w + 4) : 0;
+    const uint32_t a = load_free4(w), b = load_free4(w + 1), c = load_free4(w + 2), d = load_free4(w + 3);
+    const uint32_t e = shift ? load_free4(w + 4) : 0;
     v.x = __funnelshift_r(a, b, shift);
     v.y = __funnelshift_r(b, c, shift);
     v.z = __funnelshift_r(c, d, shift);
@@ -30,8 +31,8 @@ __device__ __forceinline__ uint4 load_codes(const int8_t* row, int64_t k, int64_
   uint64_t low = 0, high = 0;
 #pragma unroll 1
   for (int i = 0; i < 8; ++i) {
-    if (k + i < depth) low |= (uint64_t)(uint8_t)__ldg(p + i) << (8 * i);
-    if (k + i + 8 < depth) high |= (uint64_t)(uint8_t)__ldg(p + i + 8) << (8 * i);
+    if (k + i < depth) low |= (uint64_t)(uint8_t)p[i] << (8 * i);
+    if (k + i + 8 < depth) high |= (uint64_t)(uint8_t)p[i + 8] << (8 * i);
   }
   return make_uint4((uint32_t)low, (uint32_t)(low >> 32), (uint32_t)high, (uint32_t)(high >> 32));
 }

@@ -528,8 +528,8 @@ product_pair_kernel(const ProductArgs p, const Tiles tiles, const int out_align,
       // Read now, used after the sums: a channel's scale, this thread's token's.
       static_assert(BN == 32 * kTakers, "a channel each");
       const float channel = (int64_t)at.col * BN + tid < p.channels
-                                ? __ldg(p.w_scales + at.rank * p.rank_w_scales + (int64_t)at.col * BN + tid) : 0.f;
-      const float token = there ? __ldg(p.a_scales + at.rank * p.rank_a_scales + t) : 0.f;
+                                ? p.w_scales[at.rank * p.rank_w_scales + (int64_t)at.col * BN + tid] : 0.f;
+      const float token = there ? p.a_scales[at.rank * p.rank_a_scales + t] : 0.f;
       T* out = static_cast<T*>(p.out) + at.rank * p.rank_out;
       channel_scales[tid] = channel;
       takers_all(true);

@@ -82,7 +82,7 @@ widen_kernel(const ProductArgs p) {
   pdl_trigger();
   const int64_t k = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 16, token = blockIdx.x, rank = blockIdx.z;
   if (k >= wide_blocks(p.depth) * kBlockCodes) return;
-  const uint4 v = k < p.depth ? load_codes<ALIGNED>(p.a + rank * p.rank_a + token * p.ld_a, k, p.depth)
+  const uint4 v = k < p.depth ? load_codes<ALIGNED>(pinned(p.a + rank * p.rank_a + token * p.ld_a), k, p.depth)
                               : make_uint4(0, 0, 0, 0);
   uint32_t h[8];
   codes_to_f16(v.x, h[0], h[1]);
@@ -102,7 +102,7 @@ realign_kernel(const ProductArgs p, int8_t* to, int64_t ld) {
   const int64_t k = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 16, channel = blockIdx.x, rank = blockIdx.z;
   if (k >= ld) return;
   *reinterpret_cast<uint4*>(to + (rank * p.channels + channel) * ld + k) =
-      load_codes<false>(p.w + rank * p.rank_w + channel * p.ld_w, k, p.depth);
+      load_codes<false>(pinned(p.w + rank * p.rank_w + channel * p.ld_w), k, p.depth);
 }
 
 template <typename T, int VEC>

@@ -157,10 +157,40 @@ __device__ __forceinline__ void cluster_barrier() {
                "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// See overlapped_launch below.
+// See overlapped_launch below.  What a kernel reads of the one before, it reads
+// behind the wait by ordinary loads: the read-only path (__ldg) is for memory
+// that nothing writes while the kernel's blocks exist.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Ordinary loads of what nothing writes once the kernel is past its wait: the
+// compiler may place them anywhere behind the point where their pointer was
+// pinned, across other memory operations, as registers allow.
+template <typename T>
+__device__ __forceinline__ const T* pinned(const T* p) {
+  asm volatile("" : "+l"(p) :: "memory");
+  return p;
+}
+__device__ __forceinline__ uint4 load_free16(const void* p) {
+  uint4 v;
+  asm("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+// Zeros where the 16 bytes are not `there`, without a branch.
+__device__ __forceinline__ uint4 load_free16(const void* p, bool there) {
+  uint4 v;
+  asm("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+      "@p ld.global.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w) : "l"(p), "r"((uint32_t)there));
+  return v;
+}
+__device__ __forceinline__ uint32_t load_free4(const void* p) {
+  uint32_t v;
+  asm("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
 }
 
 // The smallest amax a quantized row is scaled by.

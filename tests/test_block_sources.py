@@ -66,5 +66,26 @@ def test_warps_are_together_at_aligned_instructions():
         assert 0 <= body.find("__syncwarp();") < body.index(instruction)
     assert source("int8_pair.cu").count("tcgen05.ld") == 1
     few = body_after(source("int8_few.cu"), r"product_few_kernel\(")
-    loads, sync, products = (few.rindex("load_codes<"), few.rindex("__syncwarp();"), few.index("mma(sum"))
+    loads, sync, products = (few.rindex("load(tokens"), few.rindex("__syncwarp();"), few.index("mma(sum"))
     assert loads < sync < products
+
+
+def test_no_read_only_loads_of_what_the_kernel_before_writes():
+    """Blocks of these kernels are in place while the kernel before still runs
+    (programmatic launches), so its results are not read-only data for them:
+    no __ldg, no ld.global.nc.  Loads that the compiler may move (not volatile)
+    start from pointers that were pinned behind the wait; the channels' codes,
+    which the kernel before does not write, may be read ahead of it."""
+    for path in sorted(CSRC.glob("int8_*")) + sorted(CSRC.glob("norm_*")) + [CSRC / "ops_common.h"]:
+        text = source(path.name)
+        assert "__ldg" not in text and "global.nc" not in text, path.name
+        for kernel in re.finditer(r"__global__", text):
+            body = body_after(text[kernel.start():], r"__global__")
+            assert "pdl_wait();" in body, path.name
+    for name, pointers in (("norm_bwd.cu", ["stats"]), ("int8_few.cu", ["w[i]", "a[i]"])):
+        text = source(name)
+        for p in pointers:
+            assert text.index("pdl_wait();") < text.index(p + " = pinned("), p
+    early = body_after(source("int8_few.cu"), r"product_few_kernel\(")
+    assert re.findall(r"\bload\([^)]*\);", early[:early.index("pdl_wait();")]) == ["load(codes, w, warp);"]
+    assert source("int8_quantize.cu").count("load_codes<") == source("int8_quantize.cu").count(">(pinned(") == 2
