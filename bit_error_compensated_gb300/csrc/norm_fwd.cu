@@ -164,7 +164,9 @@ norm_kernel(const NormArgs a) {
     };
 
     if (a.post) rstd1 = centre(mean1);
-    float factor = a.scale * rstd1;
+    // A layer norm's bias is added to the scaled row as it is: divided by rstd
+    // first, it would be lost where the variance overflows and rstd is 0.
+    float factor = LAYER ? a.scale : a.scale * rstd1;
     if (a.gate && a.gate_scalar && active) {
       float g[1];
       load_param<T, 1>(a.gate, a.params_f32, gate_row, g);
@@ -175,14 +177,11 @@ norm_kernel(const NormArgs a) {
       if (!active || !in[j]) continue;
       if (a.y) {
         if (a.post) {
-          scale_by<T, VEC>(a.w_post, a.params_f32, col(j), v[j]);
-          if (LAYER && a.b_post) {             // n / rstd, so that one factor is left
-            const float std1 = 1.f / rstd1;
-            float b[VEC];
-            load_param<T, VEC>(a.b_post, a.params_f32, col(j), b);
+          if (LAYER)
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) v[j][i] += b[i] * std1;
-          }
+            for (int i = 0; i < VEC; ++i) v[j][i] *= rstd1;
+          scale_by<T, VEC>(a.w_post, a.params_f32, col(j), v[j]);
+          if (LAYER) shift_by<T, VEC>(a.b_post, a.params_f32, col(j), v[j]);
         }
         if (a.gate && !a.gate_scalar)
           scale_by<T, VEC>(a.gate, a.params_f32, gate_row * a.width + col(j), v[j]);

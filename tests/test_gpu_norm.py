@@ -411,3 +411,18 @@ def test_refusals():
     assert e.value.status == echo.ECHO_ERR_ARG
     with pytest.raises(ValueError, match="dgate"):
         echo.echo_norm_backward(plan, None, x, y, stats, h, h.clone(), r, dgate=torch.ones(1, 256, dtype=BF16, device="cuda"))
+
+
+@pytest.mark.parametrize("width", [256, 4096, 8192, 8200, 12288, 12289, 16384])
+def test_a_variance_that_overflows(width):
+    """Finite rows whose variance passes fp32's range have 1/deviation 0: the
+    normalised row is 0 and the bias is left, at every width."""
+    v, p = make(5, width, F32, F32, LAYER, True, (5, 1), width)
+    v["y"].mul_(1e25)
+    assert v["y"].isfinite().all()
+    plan, params, r, h, stats, _, _ = call_forward(v, p, width, F32, F32, LAYER, True, 0.5)
+    assert (stats[:, 1] == 0).all()
+    want = v["x"].double() + 0.5 * v["gate"].double() * p["b_post"].double()
+    # two products and a sum
+    assert ((r.double() - want).abs() <= 3 * 2.0 ** -24 * (v["x"].double().abs() + want.abs())).all()
+    assert h.isfinite().all()
