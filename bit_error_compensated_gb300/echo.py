@@ -170,12 +170,13 @@ def _state_dtypes(fmt: int):
     return ((torch.float32,), (torch.bfloat16,), (torch.float16,))[fmt]
 
 
-def _stream(stream) -> int | None:
+def _stream(stream, device=None) -> int | None:
+    """The raw stream; of the current device (its number, where the caller has it) if None."""
     if stream is None:
         import torch
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         if raw is not None:                       # without making a Stream object: 0.1 us, not 3
-            return raw(torch.cuda.current_device())
+            return raw(torch.cuda.current_device() if device is None else device)
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -442,17 +443,28 @@ def echo_norm_plan_destroy(plan: NormPlan) -> None:
 class NormParams:
     """The weights and biases of a plan's norms (or their gradients), checked
     once: contiguous tensors of `width` elements of the plan's param_dtype, or
-    None.  Keeps the tensors; their addresses are taken once."""
+    None.  Keeps the tensors.  A call reads their addresses again (0.1 us each),
+    and where one has changed (a module was moved, .data assigned) checks the
+    tensors anew: it reads what they hold now, or raises ValueError."""
 
-    __slots__ = ("_keep", "_plan", "_packed")
+    __slots__ = ("_all", "_there", "_at", "_plan", "_packed")
 
     def __init__(self, plan: NormPlan, w_post=None, b_post=None, w_pre=None, b_pre=None):
-        self._keep = (w_post, b_post, w_pre, b_pre)
+        self._all = (w_post, b_post, w_pre, b_pre)
+        self._there = tuple(t for t in self._all if t is not None)
         self._plan = plan
-        for t, what in zip(self._keep, ("w_post", "b_post", "w_pre", "b_pre")):
+        self._check()
+
+    def _check(self) -> None:
+        plan = self._plan
+        self._at = None                           # a call after a refusal checks again
+        for t, what in zip(self._all, ("w_post", "b_post", "w_pre", "b_pre")):
             if t is not None:
                 _expect_contiguous(t, what, plan.param_dtype, (plan.width,), plan.device)
-        self._packed = _NORM_PARAMS.pack(*[0 if t is None else t.data_ptr() for t in self._keep])
+                if t.data_ptr() == 0:
+                    raise ValueError(f"{what}: the tensor's storage was freed")
+        self._packed = _NORM_PARAMS.pack(*[0 if t is None else t.data_ptr() for t in self._all])
+        self._at = [t.data_ptr() for t in self._there]
 
 
 def _packed_params(plan: NormPlan, params):
@@ -460,6 +472,8 @@ def _packed_params(plan: NormPlan, params):
         return None
     if params._plan is not plan:
         raise ValueError("these parameters were checked for another plan")
+    if [t.data_ptr() for t in params._there] != params._at:
+        params._check()
     return params._packed
 
 
@@ -520,7 +534,7 @@ def echo_norm(plan: NormPlan, params: NormParams | None, x, y=None, r=None, h=No
     at_gate, gate_rows, gate_cols = _norm_gate(plan, gate, None, rows)
     io = _NORM_IO.pack(rows, x.data_ptr(), x.stride()[0], at_y, ld_y, at_gate, gate_rows, gate_cols,
                        at_r, ld_r, at_h, ld_h, at_codes, ld_codes, at_scales, at_stats)
-    status = _lib.echo_norm(plan.handle, _packed_params(plan, params), io, _stream(stream))
+    status = _lib.echo_norm(plan.handle, _packed_params(plan, params), io, _stream(stream, device))
     if status:
         raise EchoError(status, "echo_norm")
 
@@ -548,7 +562,7 @@ def echo_norm_backward(plan: NormPlan, params: NormParams | None, x, y, stats, d
     io = _NORM_GRAD_IO.pack(rows, *at[:4], *gate_args, 0 if stats is None else stats.data_ptr(), *at[4:],
                             0 if dgate is None else dgate.data_ptr())
     status = _lib.echo_norm_backward(plan.handle, _packed_params(plan, params), io,
-                                     _packed_params(plan, grads), _stream(stream))
+                                     _packed_params(plan, grads), _stream(stream, device))
     if status:
         raise EchoError(status, "echo_norm_backward")
 
@@ -632,7 +646,7 @@ def echo_quantize_tokens(x, codes, scales, stream=None) -> None:
     _expect(codes, "codes", torch.int8, shape, device)
     _expect_contiguous(scales, "scales", torch.float32, shape[:-1], device)
     status = _lib.echo_quantize_tokens(ranks, tokens, depth, dtype, _matrix(x), _matrix(codes),
-                                       scales.data_ptr(), _stream(stream))
+                                       scales.data_ptr(), _stream(stream, device))
     if status:
         raise EchoError(status, "echo_quantize_tokens")
 
@@ -653,7 +667,7 @@ def echo_matmul_int8(codes, scales, w, w_scales, out, stream=None) -> None:
     status = _lib.echo_matmul_int8(ranks, tokens, channels, depth, a, scales.data_ptr(),
                                    tokens if len(codes.shape) == 3 else 0, wm, w_scales.data_ptr(),
                                    w_scales.stride()[0] if len(w_scales.shape) == 2 else 0,
-                                   _dtype_code(out.dtype), om, at, nbytes, _stream(stream))
+                                   _dtype_code(out.dtype), om, at, nbytes, _stream(stream, device))
     if status:
         raise EchoError(status, "echo_matmul_int8")
 
@@ -686,7 +700,7 @@ def echo_linear_int8(x, w, w_scales, out, codes, scales, stream=None) -> None:
     status = _lib.echo_linear_int8(ranks, tokens, channels, depth, _dtype_code(x.dtype), xm, wm,
                                    w_scales.data_ptr(),
                                    w_scales.stride()[0] if len(w_scales.shape) == 2 else 0,
-                                   a, scales.data_ptr(), om, at, nbytes, _stream(stream))
+                                   a, scales.data_ptr(), om, at, nbytes, _stream(stream, device))
     if status:
         raise EchoError(status, "echo_linear_int8")
 

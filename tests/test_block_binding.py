@@ -141,3 +141,30 @@ def test_tensors_have_to_be_on_the_gpu():
         echo.echo_quantize_tokens(torch.zeros(4), codes, scales)
     with pytest.raises(ValueError, match="float32, bfloat16 or float16"):
         echo.echo_quantize_tokens(x.double(), codes, scales)
+
+
+def test_parameters_that_move_are_read_where_they_are():
+    """A tensor whose memory is another one since it was checked (module.to, an
+    assignment to .data) is checked and packed anew by the next call; one that
+    no longer fits, or whose memory is gone, is refused.  (The device number -1
+    stands for the CPU.)"""
+    from bit_error_compensated_gb300 import echo
+    plan = echo.NormPlan(0, 16, torch.float32, torch.float32, 0, True, -1)
+    w, b = torch.zeros(16), torch.ones(16)
+    params = echo.NormParams(plan, w_pre=w, w_post=b)
+    packed = lambda: echo._NORM_PARAMS.unpack(echo._packed_params(plan, params))          # noqa: E731
+    assert packed() == (b.data_ptr(), 0, w.data_ptr(), 0)
+    was, w.data = w.detach(), torch.ones(16)
+    assert w.data_ptr() != was.data_ptr()
+    assert packed() == (b.data_ptr(), 0, w.data_ptr(), 0)
+    for bad, word in ((torch.ones(16, dtype=torch.float16), "dtype"), (torch.ones(15), "shape"),
+                      (torch.ones(32)[::2], "contiguous")):
+        good, w.data = w.detach(), bad
+        for _ in range(2):
+            with pytest.raises(ValueError, match="w_pre: .*" + word):
+                packed()
+        w.data = good
+        assert packed() == (b.data_ptr(), 0, w.data_ptr(), 0)
+    w.untyped_storage().resize_(0)
+    with pytest.raises(ValueError, match="w_pre: .*freed"):
+        packed()

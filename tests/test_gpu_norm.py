@@ -426,3 +426,23 @@ def test_a_variance_that_overflows(width):
     # two products and a sum
     assert ((r.double() - want).abs() <= 3 * 2.0 ** -24 * (v["x"].double().abs() + want.abs())).all()
     assert h.isfinite().all()
+
+
+def test_parameters_that_were_assigned_anew():
+    """A call uses what its parameters hold then, not what they held when they
+    were first checked; on another device or of another type they are refused."""
+    from bit_error_compensated_gb300 import echo
+    v, p = make(20, 512, BF16, F32, RMS, True, None, 12)
+    plan, params, r, h, *_ = call_forward(v, p, 512, BF16, F32, RMS, True, 1.0)
+    old = p["w_pre"].detach()
+    p["w_pre"].data = 2 * old
+    h2 = torch.empty_like(h)
+    echo.echo_norm(plan, params, v["x"], v["y"], None, h2)
+    assert torch.equal(h2, 2 * h)                       # twice the weight: an exact factor
+    for other, word in ((old.cpu(), "CUDA device"), (old.bfloat16(), "dtype")):
+        p["w_pre"].data = other
+        with pytest.raises(ValueError, match=word):
+            echo.echo_norm(plan, params, v["x"], v["y"], None, h2)
+    p["w_pre"].data = old
+    echo.echo_norm(plan, params, v["x"], v["y"], None, h2)
+    assert torch.equal(h2, h)
