@@ -43,7 +43,7 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
 // block) and everyone adds the slots in the same order, four at a time (those
 // past a row's warps stay 0).  Two sets of slots in turn, as a set is written
 // again only behind the next sum's barrier.
-constexpr int kStreamThreads = 512;
+constexpr int kStreamThreads = kNormGradThreads;
 constexpr int kStreamSlots = kStreamThreads / 32 * kMaxCluster;
 
 struct StreamSums {
@@ -114,9 +114,6 @@ template <typename T, int E, int VEC, bool LAYER>
 constexpr int grad_pieces() {
   return (has_ring<T, VEC>() ? rows_ahead<T, E>() * 4 * (E * (int)sizeof(T) / 16) : 0) + (LAYER ? 3 : 2) * (E / 4);
 }
-// Warps an SM: at 128 registers a thread.  (64 and twice the warps spill:
-// 143 us with 8 elements a thread, where this takes 92, 8192 x 4096 bf16.)
-constexpr int kStreamWarps = 16;
 
 // GATE: 0 none, or one row for all; 1 a row of gates, 2 a gate, for each row
 // or several.
@@ -625,10 +622,8 @@ cudaError_t launch_finish(const NormGradArgs& a, cudaStream_t s) {
 
 template <typename T, int E, int VEC, bool LAYER, bool POST, int GATE, bool FULL>
 cudaError_t launch_stream(NormGradArgs a, int sms, cudaStream_t s) {
-  const int blocks = (a.width + E * kStreamThreads - 1) / (E * kStreamThreads);
-  const int block_cols = ((a.width + blocks - 1) / blocks + 7) / 8 * 8;
-  const int threads = norm_grad_threads(block_cols, E);
-  const int rows = threads < 128 ? 128 / threads : 1;
+  const NormGradShape shape(a.width, E);
+  const int blocks = shape.blocks, block_cols = shape.block_cols, threads = shape.threads, rows = shape.rows;
   const int smem = grad_pieces<T, E, VEC, LAYER>() * 16 * threads * rows;
   static OncePerDevice prepared;
   cudaError_t e = prepared.run([] {
@@ -637,11 +632,7 @@ cudaError_t launch_stream(NormGradArgs a, int sms, cudaStream_t s) {
                                 grad_pieces<T, E, VEC, LAYER>() * 16 * kStreamThreads);
   });
   if (e != cudaSuccess) return e;
-  int at_once = kStreamWarps * 32 / (threads * rows);          // by registers; by shared memory
-  if (at_once > 216 * 1024 / smem) at_once = 216 * 1024 / smem;
-  if (at_once < 1) at_once = 1;
-  int64_t most = (int64_t)(at_once * sms / blocks) * rows;
-  if (most < 1) most = 1;
+  const int64_t most = shape.workers(sms, 216 * 1024 / smem);
   a.span = (a.rows + most - 1) / most;
   a.workers = (a.rows + a.span - 1) / a.span;
   a.folded = GATE == 0;

@@ -76,11 +76,34 @@ cudaError_t launch_norm_grad(NormGradArgs a, int layer, bool vec, int sms, cudaS
 // Threads that the backward kernel gives a row of `cols` columns of a block, at
 // `each` elements a thread.
 inline int norm_grad_threads(int cols, int each) { return ((cols + each - 1) / each + 31) / 32 * 32; }
-// Workers (row ranges with their own partial sums) a backward call may have at
-// most: 16 warps an SM.
+// Threads of a block, at most, and of an SM: at 128 registers a thread.  (64 and
+// twice the threads spill: 143 us with 8 elements a thread, where this takes 92,
+// 8192 x 4096 bf16.)
+constexpr int kNormGradThreads = 512;
+// How the backward kernel lays rows on blocks, at `each` elements a thread: a
+// row's columns over `blocks`, or `rows` narrow rows on one.
+struct NormGradShape {
+  int blocks, block_cols, threads, rows;
+  NormGradShape(int width, int each) {
+    blocks = (width + each * kNormGradThreads - 1) / (each * kNormGradThreads);
+    block_cols = ((width + blocks - 1) / blocks + 7) / 8 * 8;
+    threads = norm_grad_threads(block_cols, each);
+    rows = threads < 128 ? 128 / threads : 1;
+  }
+  // Workers (row ranges with their own partial sums) of a call, where an SM
+  // holds the blocks that registers let it and at most `room`.
+  int64_t workers(int sms, int room) const {
+    int at_once = kNormGradThreads / (threads * rows);
+    at_once = at_once > room ? room : at_once;
+    const int64_t most = (int64_t)((at_once < 1 ? 1 : at_once) * sms / blocks) * rows;
+    return most < 1 ? 1 : most;
+  }
+};
+// Workers a backward call may have at most, whichever form it takes.
 inline int64_t norm_grad_max_workers(int width, int sms) {
-  const int threads = width <= 4096 ? norm_grad_threads(width, 16) : 256;     // at least
-  return (int64_t)sms * (512 / threads > 1 ? 512 / threads : 1);
+  const int64_t a = NormGradShape(width, 8).workers(sms, kNormGradThreads);
+  const int64_t b = NormGradShape(width, 16).workers(sms, kNormGradThreads);
+  return a > b ? a : b;
 }
 
 }  // namespace echo

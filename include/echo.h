@@ -405,7 +405,9 @@ typedef struct echo_norm_plan_s* echo_norm_plan_t;
  *   post         1: with the norm after the block, 0: without
  *   eps, scale   finite, eps >= 0
  * Allocates (cudaMalloc, on the current device) the workspace of
- * echo_norm_backward: the plan serves one stream at a time.
+ * echo_norm_backward, six fp32 sums a column for each row range that its blocks
+ * take at once (30 MB at the most, on 152 SMs): the plan serves one stream at a
+ * time.
  */
 int echo_norm_plan(int64_t width, int dtype, int param_dtype, int kind, int post,
                    float eps, float scale, echo_norm_plan_t* out);

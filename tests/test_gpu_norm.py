@@ -446,3 +446,16 @@ def test_parameters_that_were_assigned_anew():
     p["w_pre"].data = old
     echo.echo_norm(plan, params, v["x"], v["y"], None, h2)
     assert torch.equal(h2, h)
+
+
+@pytest.mark.parametrize("width", [1, 96, 1024, 4096, 4097, 8192, 12288, 16384])
+def test_a_plan_allocates_what_its_calls_can_use(width):
+    """Six fp32 sums for each of the columns that the device's threads hold at
+    once: 512 threads an SM, 16 columns each (and the allocator's 2 MB)."""
+    from bit_error_compensated_gb300 import echo
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    torch.cuda.synchronize()
+    before = torch.cuda.mem_get_info()[0]
+    plans = [echo.echo_norm_plan(width, BF16) for _ in range(4)]
+    used = (before - torch.cuda.mem_get_info()[0]) / len(plans)
+    assert used <= 6 * 4 * sms * 512 * 16 + (1 << 21)
