@@ -184,10 +184,16 @@ int echo_matmul_status(void* stream, int* status) {
   if (status == nullptr) return ECHO_ERR_ARG;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   int word[3] = {0, 0, 0};
-  ECHO_OPS_CUDA(take_gave_up<float>(word, s));
-  ECHO_OPS_CUDA(take_gave_up<__nv_bfloat16>(word + 1, s));
-  ECHO_OPS_CUDA(take_gave_up<__half>(word + 2, s));
+  ECHO_OPS_CUDA(read_gave_up<float>(word, s));
+  ECHO_OPS_CUDA(read_gave_up<__nv_bfloat16>(word + 1, s));
+  ECHO_OPS_CUDA(read_gave_up<__half>(word + 2, s));
   ECHO_OPS_CUDA(cudaStreamSynchronize(s));
+  // Only a word that was set is cleared: one that a product on another stream
+  // sets right now is the next call's to report.
+  if (word[0]) ECHO_OPS_CUDA(clear_gave_up<float>(s));
+  if (word[1]) ECHO_OPS_CUDA(clear_gave_up<__nv_bfloat16>(s));
+  if (word[2]) ECHO_OPS_CUDA(clear_gave_up<__half>(s));
+  if (word[0] | word[1] | word[2]) ECHO_OPS_CUDA(cudaStreamSynchronize(s));
   *status = word[0] | word[1] | word[2] ? ECHO_ERR_TIMEOUT : ECHO_OK;
   return ECHO_OK;
 }

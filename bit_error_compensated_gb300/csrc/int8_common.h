@@ -77,8 +77,9 @@ cudaError_t launch_few(const ProductArgs& p, bool aligned, bool early, int sms, 
 // One instantiation per type of out (the sources are compiled once for each).
 template <typename T>
 cudaError_t launch_pair(const ProductArgs& p, const ProductLayout& l, cudaStream_t s);
-// Reads and clears the word that a wait that gave up has set.
-template <typename T> cudaError_t take_gave_up(int* word, cudaStream_t s);
+// Reads, and clears, the word that a wait that gave up has set.
+template <typename T> cudaError_t read_gave_up(int* word, cudaStream_t s);
+template <typename T> cudaError_t clear_gave_up(cudaStream_t s);
 
 }  // namespace echo
 

@@ -749,12 +749,17 @@ cudaError_t launch_pair<ECHO_ELEM>(const ProductArgs& p, const ProductLayout& l,
 }
 
 template <>
-cudaError_t take_gave_up<ECHO_ELEM>(int* word, cudaStream_t s) {
+cudaError_t read_gave_up<ECHO_ELEM>(int* word, cudaStream_t s) {
   void* at = nullptr;
-  cudaError_t e = cudaGetSymbolAddress(&at, g_gave_up);
-  if (e == cudaSuccess) e = cudaMemcpyAsync(word, at, sizeof(int), cudaMemcpyDeviceToHost, s);
-  if (e == cudaSuccess) e = cudaMemsetAsync(at, 0, sizeof(int), s);
-  return e;
+  const cudaError_t e = cudaGetSymbolAddress(&at, g_gave_up);
+  return e == cudaSuccess ? cudaMemcpyAsync(word, at, sizeof(int), cudaMemcpyDeviceToHost, s) : e;
+}
+
+template <>
+cudaError_t clear_gave_up<ECHO_ELEM>(cudaStream_t s) {
+  void* at = nullptr;
+  const cudaError_t e = cudaGetSymbolAddress(&at, g_gave_up);
+  return e == cudaSuccess ? cudaMemsetAsync(at, 0, sizeof(int), s) : e;
 }
 
 }  // namespace echo

@@ -89,3 +89,15 @@ def test_no_read_only_loads_of_what_the_kernel_before_writes():
     early = body_after(source("int8_few.cu"), r"product_few_kernel\(")
     assert re.findall(r"\bload\([^)]*\);", early[:early.index("pdl_wait();")]) == ["load(codes, w, warp);"]
     assert source("int8_quantize.cu").count("load_codes<") == source("int8_quantize.cu").count(">(pinned(") == 2
+
+
+def test_a_report_that_was_not_read_is_not_cleared():
+    """A product on another stream may set its word between this call's read
+    and its clearing: only words that were read as set are cleared."""
+    body = body_after(source("int8_api.cu"), r"int echo_matmul_status\(")
+    read = body.index("cudaStreamSynchronize")
+    for i, t in enumerate(("float", "__nv_bfloat16", "__half")):
+        clear = re.search(rf"if \(word\[{i}\]\) ECHO_OPS_CUDA\(clear_gave_up<{t}>\(s\)\);", body)
+        assert clear and clear.start() > read
+    assert body.count("clear_gave_up") == 3 and "cudaMemsetAsync" not in body
+    assert "cudaMemsetAsync" not in body_after(source("int8_pair.cu"), r"read_gave_up<")
