@@ -492,14 +492,21 @@ const char* echo_strerror(int status) {
   switch (status) {
     case ECHO_OK: return "ok";
     case ECHO_ERR_ARG: return "invalid argument";
-    case ECHO_ERR_SHAPE: return "n must be a non-negative multiple of P*g";
-    case ECHO_ERR_UNSUPPORTED: return "unsupported configuration (bits must be 4 or 8, g must be 64, 128 or 256)";
-    case ECHO_ERR_ALIGN: return "device pointer not 16-byte aligned (32 for a compensator state)";
+    case ECHO_ERR_SHAPE: 
+      return "wrong size: a call's n must be a non-negative multiple of P*g; a matrix needs sizes of at least 0, rows at "
+             "least its columns apart, and a gate whose rows divide its own";
+    case ECHO_ERR_UNSUPPORTED: 
+      return "unsupported configuration: a call's bits must be 4 or 8 and g 64, 128 or 256; a norm's width at most "
+             "ECHO_NORM_MAX_WIDTH; a product's sizes at most ECHO_MATMUL_MAX_*; element types ECHO_F32, BF16 or F16";
+    case ECHO_ERR_ALIGN: 
+      return "device pointer not aligned: a call's to 16 bytes (32 for a compensator state), a norm's stats and a "
+             "product's workspace to 16, other tensors to their element";
     case ECHO_ERR_CUDA: return cudaGetErrorString(g_last_cuda);
     case ECHO_ERR_OVERFLOW: return "non-finite input or fp16 step overflow in some group";
     case ECHO_ERR_TIMEOUT: return "a device-side wait gave up";
     case ECHO_ERR_TOO_LARGE:
-      return "problem needs more receive-slot space than the fixed no-allocation area holds";
+      return "problem needs more space than it has: receive slots of the fixed no-allocation area, or the workspace "
+             "given to a product";
     default: return "unknown status";
   }
 }

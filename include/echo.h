@@ -58,10 +58,16 @@ extern "C" {
 #define ECHO_OK              0
 #define ECHO_ERR_ARG         1  /* NULL pointer, P outside 1..ECHO_MAX_RANKS, g < 1,
                                    aliasing other than out[p] == in[p], wrong device */
-#define ECHO_ERR_SHAPE       2  /* n < 0, or n not a multiple of P*g */
-#define ECHO_ERR_UNSUPPORTED 3  /* bits not 4 or 8, or g not 64, 128 or 256 */
+#define ECHO_ERR_SHAPE       2  /* n < 0, or n not a multiple of P*g; a matrix of negative
+                                   size or with rows closer than its columns; a gate
+                                   whose rows do not divide the call's */
+#define ECHO_ERR_UNSUPPORTED 3  /* bits not 4 or 8, or g not 64, 128 or 256; sizes beyond
+                                   ECHO_NORM_MAX_WIDTH or ECHO_MATMUL_MAX_*; an element
+                                   type other than ECHO_F32, ECHO_BF16, ECHO_F16 */
 #define ECHO_ERR_ALIGN       4  /* an input or output not 16-byte aligned, or a
-                                   compensator state not 32-byte aligned */
+                                   compensator state not 32-byte aligned; a norm's or a
+                                   product's tensor off its element, stats or workspace
+                                   off 16 bytes */
 #define ECHO_ERR_CUDA        5  /* a CUDA runtime call failed */
 #define ECHO_ERR_OVERFLOW    6  /* (status word) a non-finite input or an fp16 step overflow */
 #define ECHO_ERR_TIMEOUT     7  /* (status word) a device-side wait gave up */

@@ -168,3 +168,14 @@ def test_parameters_that_move_are_read_where_they_are():
     w.untyped_storage().resize_(0)
     with pytest.raises(ValueError, match="w_pre: .*freed"):
         packed()
+
+
+def test_texts_of_errors_name_the_operators():
+    """The text of a status says what it means for a norm and a product too."""
+    from bit_error_compensated_gb300 import echo
+    for status, words in ((echo.ECHO_ERR_SHAPE, ("multiple of P*g", "rows", "gate")),
+                          (echo.ECHO_ERR_UNSUPPORTED, ("bits", "width", "product", "types")),
+                          (echo.ECHO_ERR_ALIGN, ("aligned", "stats", "workspace")),
+                          (echo.ECHO_ERR_TOO_LARGE, ("no-allocation", "workspace"))):
+        text = echo.echo_strerror(status)
+        assert all(w in text for w in words), text
