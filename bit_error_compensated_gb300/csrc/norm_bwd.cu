@@ -656,17 +656,27 @@ cudaError_t launch_stream(NormGradArgs a, int sms, cudaStream_t s) {
 // and fit 128 registers where a thread keeps two sums a column (8192 x 4096
 // bf16, RMS: 80 us, with 8: 92); with three or more (layer norms, a row of
 // gates) they spill (RMS, 128 gate rows: 185 us, with 8: 114), as does a row
-// of single elements.  Past 4096 columns 16 stay the lesser evil: 8 would need
-// a cluster, whose barrier waits for the copies and stores in flight,
-// microseconds a row (4096 x 8192 bf16, RMS: 91 us, as clusters of two 176).
+// of single elements.  Past 4096 columns 8 need a cluster, whose barrier waits
+// for the copies and stores in flight, so that 16 can be the lesser evil in
+// spite of their spills.  In us with 16, with 8:
+//   4096 x 8192, no gate or a scalar, RMS (no spills): bf16 76, 176
+//   4096 x 8192, layer norms: bf16 195, 204; fp32 275, 229
+//   4096 x 8192, layer norms, a row of gates: bf16 257, 235; fp32 302, 289
+//   4096 x 8192, RMS, a row of gates: bf16 180, 206; fp32 239, 249
+//     and without the norm after the block: bf16 152, 128; fp32 197, 166
+//   4096 x 8200 (two blocks, three), layer norms: bf16 268, 495; fp32 385, 555
+//   2048 x 12288, layer norms, a row of gates: bf16 257, 361; fp32 306, 427
+// So 8 up to 8192 columns, the most that two blocks hold, for fp32 layer norms
+// and for a row of gates where there are layer norms or no norm after the block.
 template <typename T, int VEC, bool LAYER, bool POST, int GATE>
 cudaError_t pick_elements(const NormGradArgs& a, int sms, cudaStream_t s) {
   if constexpr (VEC > 1 && !LAYER && GATE != 1) {
     return a.y && a.dr && a.dh && a.dx && a.dy ? launch_stream<T, 16, VEC, LAYER, POST, GATE, true>(a, sms, s)
                                                : launch_stream<T, 16, VEC, LAYER, POST, GATE, false>(a, sms, s);
   } else {
+    constexpr bool kPair = (LAYER && sizeof(T) == 4) || (GATE == 1 && (LAYER || !POST));
     if constexpr (VEC > 1)
-      if (a.width > 8 * kStreamThreads) return launch_stream<T, 16, VEC, LAYER, POST, GATE, false>(a, sms, s);
+      if (a.width > (kPair ? 16 : 8) * kStreamThreads) return launch_stream<T, 16, VEC, LAYER, POST, GATE, false>(a, sms, s);
     return launch_stream<T, 8, VEC, LAYER, POST, GATE, false>(a, sms, s);
   }
 }

@@ -459,3 +459,17 @@ def test_a_plan_allocates_what_its_calls_can_use(width):
     plans = [echo.echo_norm_plan(width, BF16) for _ in range(4)]
     used = (before - torch.cuda.mem_get_info()[0]) / len(plans)
     assert used <= 6 * 4 * sms * 512 * 16 + (1 << 21)
+
+
+@pytest.mark.parametrize("width", [4104, 5120, 8000, 8192])
+@pytest.mark.parametrize("dtype,kind,post,gate", [
+    (F32, LAYER, True, None), (F32, LAYER, True, "token"), (F32, LAYER, False, None), (F32, RMS, True, "sequence"),
+    (BF16, LAYER, True, "sequence"), (F16, LAYER, False, "sequence"), (BF16, RMS, False, "sequence"),
+    (F32, RMS, False, "sequence"), (BF16, LAYER, True, None), (F16, RMS, True, "sequence")])
+def test_rows_of_two_blocks(width, dtype, kind, post, gate):
+    """Aligned rows past 4096 columns, which one block or a cluster of two takes."""
+    rows = 333
+    gate = {None: None, "token": (rows, 1), "sequence": (9, width)}[gate]
+    v, p = make(rows, width, dtype, F32, kind, post, gate, width)
+    plan, params, stats = check_forward(v, p, width, dtype, F32, kind, post, 0.5)
+    check_backward(v, p, plan, params, stats, width, F32, kind, post, 0.5)
