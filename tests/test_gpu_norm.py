@@ -473,3 +473,122 @@ def test_rows_of_two_blocks(width, dtype, kind, post, gate):
     v, p = make(rows, width, dtype, F32, kind, post, gate, width)
     plan, params, stats = check_forward(v, p, width, dtype, F32, kind, post, 0.5)
     check_backward(v, p, plan, params, stats, width, F32, kind, post, 0.5)
+
+
+# Rows enough that every block (and every worker of the backward call) goes
+# several times round its ring of rows, with a ragged last turn.  On 152 SMs a
+# forward block of 4096 columns takes 9 or 10 rows (16 elements a thread) or 18
+# to 19, and its ring holds 4 at most; a worker 10 or 19.
+MANY = 2744
+
+
+def check_many_rows(rows):
+    """That there are as many: an SM holds two rows of 4096 columns at most."""
+    assert rows >= 9 * 2 * torch.cuda.get_device_properties(0).multi_processor_count
+
+
+def gate_of(name, rows, width):
+    return {"none": None, "all": (1, width), "sequence": (rows // 49, width), "scalar": (1, 1), "token": (rows, 1)}[name]
+
+
+@pytest.mark.parametrize("codes", [False, True])
+@pytest.mark.parametrize("gate", ["none", "all", "sequence", "token"])
+@pytest.mark.parametrize("post", [True, False])
+@pytest.mark.parametrize("kind", [RMS, LAYER])
+@pytest.mark.parametrize("dtype,width", [(BF16, 4096), (F16, 4096), (F32, 4096), (BF16, 4095), (F32, 4095), (BF16, 8192)])
+def test_forward_many_rows_a_block(dtype, width, kind, post, gate, codes):
+    """Distinct rows through every slot of the ring, many times; without codes
+    this is the form that training and prefill take."""
+    check_many_rows(MANY)
+    v, p = make(MANY, width, dtype, F32, kind, post, gate_of(gate, MANY, width), width + post)
+    if codes:
+        check_forward(v, p, width, dtype, F32, kind, post, 0.5)
+        return
+    _, _, r, h, stats, _, _ = call_forward(v, p, width, dtype, F32, kind, post, 0.5)
+    want_r, want_h, want_stats, err_r, err_h = ref.forward(
+        kind, post, EPS, 0.5, dbl(v["x"]), dbl(v["y"]), dbl(v["gate"]), {k: t.double() for k, t in p.items()})
+    ref.within(r, want_r, err_r, "r")
+    ref.within(h, want_h, err_h, "h")
+
+
+@pytest.mark.parametrize("rows,width,dtype,kind", [(700, 12288, BF16, RMS), (700, 9001, F32, LAYER),
+                                                   (700, 16384, F16, LAYER), (460, 10000, F32, RMS)])
+def test_forward_many_wide_rows_a_block(rows, width, dtype, kind):
+    v, p = make(rows, width, dtype, F32, kind, True, (rows // 20, width), width)
+    check_forward(v, p, width, dtype, F32, kind, True, 0.5)
+
+
+@pytest.mark.parametrize("width", [4096, 4095, 1001])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("kind", [RMS, LAYER])
+def test_in_place_many_rows(dtype, width, kind):
+    """Every tensor that may be written in place, the rows ahead of it in flight."""
+    from bit_error_compensated_gb300 import echo
+    check_many_rows(MANY)
+    v, p = make(MANY, width, dtype, F32, kind, True, (56, width), 3 + width)
+    plan, params, r, h, stats, _, _ = call_forward(v, p, width, dtype, F32, kind, True, 1.0)
+    x2, y2 = v["x"].clone(), v["y"].clone()
+    echo.echo_norm(plan, params, x2, y2, x2, y2, gate=v["gate"])
+    assert torch.equal(x2, r) and torch.equal(y2, h)
+    dx, dy = torch.empty_like(r), torch.empty_like(r)
+    echo.echo_norm_backward(plan, params, v["x"], v["y"], stats, v["dr"], v["dh"], dx, dy, gate=v["gate"])
+    for to_dx, to_dy in (("dr", "dh"), ("dh", "dr"), ("dr", "y"), ("dh", "y"), (None, "dr"), ("dr", None)):
+        t = {k: v[k].clone() for k in ("dr", "dh", "y")}
+        dx2 = t[to_dx] if to_dx else torch.empty_like(r)
+        dy2 = t[to_dy] if to_dy else torch.empty_like(r)
+        echo.echo_norm_backward(plan, params, v["x"], t["y"], stats, t["dr"], t["dh"], dx2, dy2, gate=v["gate"])
+        assert torch.equal(dx2, dx) and torch.equal(dy2, dy), (to_dx, to_dy)
+
+
+def check_gradients(v, p, plan, params, stats, width, kind, post, scale, full=True):
+    """All gradients, the gate's too, twice the same bits and within their
+    bounds; not `full`: without that of x."""
+    from bit_error_compensated_gb300 import echo
+    got = {"x": like(v["x"]) if full else None, "y": like(v["x"])}
+    d = {k: torch.full_like(t, float("nan")) for k, t in p.items()}
+    got["gate"] = None if v["gate"] is None else torch.full_like(v["gate"], float("nan"))
+    grads, first = echo.NormParams(plan, **d), None
+    got.update(d)
+    got = {k: t for k, t in got.items() if t is not None}
+    for _ in range(2):
+        echo.echo_norm_backward(plan, params, v["x"], v["y"], stats, v["dr"], v["dh"], got.get("x"), got["y"], grads,
+                                gate=v["gate"], dgate=got.get("gate"))
+        if first is None:
+            first = {k: t.clone() for k, t in got.items()}
+            for t in d.values():
+                t.fill_(float("nan"))
+            if "gate" in got:
+                got["gate"].fill_(float("nan"))
+    for k, t in got.items():
+        assert torch.equal(first[k], t), f"d{k}: a repeated call gives other bits"
+    want = ref.backward(kind, post, EPS, scale, dbl(v["x"]), dbl(v["y"]), dbl(v["gate"]),
+                        {k: t.double() for k, t in p.items()}, dbl(v["dr"]), dbl(v["dh"]))
+    for k, t in got.items():
+        ref.within(t, *want[k], f"d{k}")
+
+
+@pytest.mark.parametrize("full", [True, False])
+@pytest.mark.parametrize("gate", ["none", "all", "sequence", "scalar", "token"])
+@pytest.mark.parametrize("post", [True, False])
+@pytest.mark.parametrize("kind", [RMS, LAYER])
+@pytest.mark.parametrize("dtype,width", [(BF16, 4096), (F32, 4096), (F16, 4095), (F32, 4095)])
+def test_backward_many_rows_a_worker(dtype, width, kind, post, gate, full):
+    """Distinct rows many times round a worker's ring."""
+    check_many_rows(MANY)
+    v, p = make(MANY, width, dtype, F32, kind, post, gate_of(gate, MANY, width), width + 7)
+    plan, params, _, _, stats, _, _ = call_forward(v, p, width, dtype, F32, kind, post, 0.5)
+    check_gradients(v, p, plan, params, stats, width, kind, post, 0.5, full)
+
+
+@pytest.mark.parametrize("rows,span", [(2744, 1), (2744, 7), (2744, 8), (2744, 14), (2744, 49), (2744, 343), (2744, 1372),
+                                       (2740, 5), (2740, 10), (2740, 20), (2755, 19), (2755, 95), (2744, 2744)])
+@pytest.mark.parametrize("cols", ["width", 1])
+@pytest.mark.parametrize("kind", [RMS, LAYER])
+@pytest.mark.parametrize("dtype,width", [(BF16, 4096), (F32, 4096), (F32, 4095)])
+def test_gate_rows_across_workers_of_many_rows(dtype, width, kind, cols, rows, span):
+    """Gate rows that begin and end inside a worker's rows (10 with 16 elements a
+    thread, 19 with 8), at their ends, and that many workers share."""
+    check_many_rows(rows)
+    v, p = make(rows, width, dtype, F32, kind, True, (rows // span, width if cols == "width" else 1), span)
+    plan, params, _, _, stats, _, _ = call_forward(v, p, width, dtype, F32, kind, True, 1.0)
+    check_gradients(v, p, plan, params, stats, width, kind, True, 1.0)
