@@ -362,3 +362,57 @@ def test_a_call_that_gave_up_ends_cleanly(shape, dtype):
     echo.echo_matmul_int8(a, sa, w, sw, out)
     same_bits(out, want_product(a, sa, w, sw, dtype))
     assert echo.echo_matmul_status() == echo.ECHO_OK
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("shape", [(1, 1500, 7000, 1024), (1, 1500, 7000, 2048), (1, 1500, 7001, 1100), (2, 1030, 5136, 640),
+                                   (1, 2600, 5000, 3000), (1, 9000, 600, 512), (3, 700, 5003, 1300), (1, 1025, 6144, 4096)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_product_of_several_tiles_a_pair(shape, dtype):
+    """More tiles than pairs of SMs: a pair goes on to a second and third one,
+    in one chunk and in several."""
+    from bit_error_compensated_gb300 import echo
+    P, M, N, K = shape
+    pairs = torch.cuda.get_device_properties(0).multi_processor_count // 2
+    assert P * ((M + 255) // 256) * ((N + 255) // 256) > pairs
+    gen = gen_of(M + N + K)
+    a, w = codes_of(gen, P, M, K), codes_of(gen, P, N, K)
+    sa, sw = torch.rand(P, M, generator=gen, device="cuda"), torch.rand(P, N, generator=gen, device="cuda") * 1e-3
+    out = torch.full((P, M, N), float("nan"), dtype=dtype, device="cuda")
+    want = want_product(a, sa, w, sw, dtype)
+    for _ in range(3):
+        echo.echo_matmul_int8(a, sa, w, sw, out)
+        same_bits(out, want)
+        out.fill_(float("nan"))
+    assert echo.echo_matmul_status() == echo.ECHO_OK
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("shape", [(1, 8, 6144, 4096), (1, 5, 7000, 2051), (4, 3, 2000, 1024), (1, 1, 9000, 515),
+                                   (1, 8, 14336, 1040), (1, 1, 4096, 8192)], ids=lambda s: "x".join(map(str, s)))
+def test_product_of_few_tokens_and_many_channels(shape, dtype):
+    """Up to 8 tokens with more blocks of 16 channels than two an SM, and depths
+    of several turns of a block's warps."""
+    from bit_error_compensated_gb300 import echo
+    P, M, N, K = shape
+    gen = gen_of(M + N + K)
+    a, w = codes_of(gen, P, M, K), codes_of(gen, P, N, K)
+    sa, sw = torch.rand(P, M, generator=gen, device="cuda"), torch.rand(P, N, generator=gen, device="cuda") * 1e-3
+    out = torch.full((P, M, N), float("nan"), dtype=dtype, device="cuda")
+    echo.echo_matmul_int8(a, sa, w, sw, out)
+    same_bits(out, want_product(a, sa, w, sw, dtype))
+
+
+@pytest.mark.parametrize("tokens", [1, 12, 30, 100, 700])
+@pytest.mark.parametrize("P,N,K", [(4, 520, 1024), (2, 300, 1040), (4, 260, 1000), (3, 4100, 512), (2, 300, 333)])
+def test_weights_that_are_slices_of_one_matrix(tokens, P, N, K):
+    """A row-parallel layer's weights as the ranks' columns of one matrix: rows
+    lie farther apart than ranks, on 16 bytes or on any."""
+    from bit_error_compensated_gb300 import echo
+    gen = gen_of(tokens + N)
+    w = codes_of(gen, N, P * K).view(N, P, K).transpose(0, 1)
+    a = codes_of(gen, tokens, P * K).view(tokens, P, K).transpose(0, 1)
+    sa, sw = torch.rand(P, tokens, generator=gen, device="cuda"), torch.rand(P, N, generator=gen, device="cuda")
+    out = torch.full((tokens, P, N), float("nan"), dtype=BF16, device="cuda").transpose(0, 1)
+    echo.echo_matmul_int8(a, sa, w, sw, out)
+    same_bits(out, want_product(a, sa, w, sw, BF16))
