@@ -33,8 +33,10 @@ struct ProductArgs {
 };
 
 // Products of more tokens than this run in tiles (int8_pair.cu), from f16
-// codes in a workspace: 32 tokens x 4096 x 4096 take 10 us here and 21 in
-// tiles; a form for 64 took 17 (tiles 21) and 51 at 14336 channels (tiles 29).
+// codes in a workspace, which those of fewer (int8_few.cu) do not need.  Both
+// product_workspace and launch_product go by it.  Depth 4096, 4096 and 14336
+// channels: tiles take 21 and 26 us for 33 to 96 tokens, these kernels 8 and 23
+// for 32, 14 and 43 for 48, 22 and 67 for 96.
 constexpr int64_t kFewTokens = 32;
 // Ranks of the tokens' codes: one where all share them.
 inline int64_t token_ranks(const ProductArgs& p) { return p.rank_a == 0 ? 1 : p.ranks; }

@@ -13,9 +13,11 @@
 // sums are exact for 1024 codes; after those, and at the end, a warp adds its
 // sums to the block's in shared memory as int32, whose order does not matter.
 //
-// One GB300, GPU time a call: 1 x 4096 x 4096 in 4.6 us (3.6 TB/s: its 2.5 us
-// of bytes and about 2.2 of a launch), 8 x 14336 x 4096 in 10.7 us (5.5 TB/s), 16
-// in 17, 32 in 24 (bound by turning codes: registers hold eight warps an SM).
+// One GB300, GPU time a call: 1 x 4096 x 4096 in 4.4 us (3.8 TB/s: its 2.5 us
+// of bytes and about 2.2 of a launch), 8 x 14336 x 4096 in 9.9 us (6.0 TB/s), 16
+// in 15, 32 in 23.  The last are bound by latency: 136 registers a thread leave
+// eight warps an SM, whose loads and products take turns (memory, matrix pipe and
+// issue slots are each busy less than a third of the time).
 #include "int8_load.h"
 
 namespace echo {
@@ -208,8 +210,9 @@ cudaError_t launch(const ProductArgs& p, bool aligned, bool early, cudaStream_t 
 cudaError_t launch_few(const ProductArgs& p, bool aligned, bool early, int sms, cudaStream_t s) {
   // Eight windows at once leave registers for two blocks an SM: with no more
   // blocks than that, a block's time is its loads' latency (1 x 4096 x 4096:
-  // 4.6 us, with four 5.8); with more, three blocks an SM keep more loads in
-  // flight (8 x 6144 x 4096: 6.3 us, with eight 7.0).
+  // 4.4 us, with four 5.5; 300 blocks, 1 x 4800 x 4096: 4.5, 5.5); with more,
+  // three blocks an SM keep more loads in flight (8 x 6144 x 4096: 5.9 us, with
+  // eight 6.4; 8 x 14336 x 4096: 9.9, 11.1).
   if (p.tokens <= 8)
     return (p.channels + 15) / 16 * p.ranks <= 2 * sms ? launch<1, 1, 8>(p, aligned, early, s)
                                                        : launch<1, 1, 4>(p, aligned, early, s);

@@ -21,19 +21,20 @@
 //   3  issue: matrix instructions (first block), the tokens' copies, the
 //      channels' copies.
 // TMEM holds two chunks' sums, so one is taken out while the next is computed.
-// Shared memory moves 160 KB a stage (32 KB of tokens written and read, 16 KB
-// of int8 codes written and read, 32 KB of their f16 written and read): 1280
-// cycles at 128 bytes a cycle, for 1024 of matrix instructions.
+// A stage takes 1000 to 1100 cycles, 1024 of which its matrix instructions need.
 //
-// One GB300: 8192 x 14336 x 4096 in 491 us, 1960 TFLOP/s of products (bound by
-// the matrix instructions: a library's f16 product reaches 1920); 4 x 2048 x 4096
-// x 1024 in 54 us, 1280 (one chunk a tile: its 128 KB of results take the
-// takers as long as its products take the tensor cores).
+// One GB300: 8192 x 14336 x 4096 in 491 to 506 us, 1900 to 1960 TFLOP/s of
+// products (bound by the matrix instructions: a library's f16 product reaches
+// 1920); 4 x 2048 x 4096 x 1024 in 54 us, 1280 (one chunk a tile: its 128 KB of
+// results take the takers as long as its products take the tensor cores).
+// Where tiles are few the machine is not full: a tile is always 256 x 256, so 64
+// x 4096 x 4096 takes the 21 us of 256 tokens, of 2.5 us of bytes.
 //
 // Where there are fewer tiles than pairs of SMs, SPLIT pairs in a cluster share
 // a tile's depth.  Their sums are int32, so their order does not matter: each
 // pair writes those of the columns that it does not own into the owner's
-// shared memory (the ring is free by then), and the owner adds and stores.
+// shared memory (the ring is free by then), and the owner adds and stores.  (With
+// that exchange beside 128 sums, 136 to 316 bytes a thread are spilled.)
 //
 // Every wait is bounded; one that gives up ends the call with a status
 // (echo_matmul_status).  The other warps of its block leave at their next wait,

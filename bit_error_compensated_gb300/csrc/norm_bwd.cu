@@ -24,8 +24,10 @@
 //
 // One GB300, bf16, RMS: 8192 x 4096 in 71 us, 5.7 TB/s, 0.84 of the copy rate,
 // both kernels; 32768 x 4096 with a gate a token 343 us (a third row sum).
-// Layer norms 109 us (twice the sums, eight elements a thread).  Bound by
-// instructions and the row sums' latency at 16 warps an SM.
+// Layer norms 109 us (twice the sums, eight elements a thread); 8192 x 12288 391
+// us, layer norms 694 (clusters of two, spills).  Bound by instructions (scalar
+// arithmetic: 679 a warp and row of 16 elements a thread, issue slots 59% busy)
+// and the row sums' latency at 16 warps an SM.
 #include "norm_common.h"
 
 namespace echo {

@@ -15,12 +15,16 @@
 // weight multiplied into one factor.  Rows come through a ring of asynchronous
 // copies, several ahead (16-bit rows that are not made of 16-byte pieces, which
 // such copies do not take, element by element through registers, one ahead).
-// norm_kernel takes longer rows.
+// norm_kernel takes longer rows: 1024 threads an SM at 64 registers hold x, the
+// next x and y and the row, of which 170 to 300 bytes a thread are spilled.
 //
 // One GB300, 8192 x 4096 bf16, RMS: 47 us, 5.7 TB/s, 0.84 of the copy rate;
 // what is left are the two sums' round trips through shuffles and barriers
 // (short scoreboard 1.7 of 6 cycles an instruction, issue 60%).  fp32, same
-// rows: 95 us, 5.6 TB/s.  One row: 2.7 us, a launch and one trip to memory.
+// rows: 94 us, 5.7 TB/s.  One row: 2.7 us, a launch and one trip to memory.
+// Layer norms (four sums, eight elements a thread): 96 us, fp32 108.  Longer
+// rows: 8192 x 12288 bf16 369 us, layer norms 397, 2.2 and 2.0 TB/s (spills, and
+// no ring); 4096 x 16384 239 and 259.
 #include "norm_common.h"
 
 namespace echo {
