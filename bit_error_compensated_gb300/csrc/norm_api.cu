@@ -103,6 +103,7 @@ int echo_norm_plan(int64_t width, int dtype, int param_dtype, int kind, int post
   }
   if (e != cudaSuccess) {
     echo_norm_plan_destroy(p);
+    cudaGetLastError();                // the caller's next check is not this call's
     return note_cuda_error(e);
   }
   *out = p;
