@@ -13,7 +13,9 @@ _BINDING_NAMES = (
     "COMP_DEFAULT", "echo_norm_plan", "echo_norm_plan_destroy", "echo_norm", "echo_norm_backward",
     "echo_quantize_tokens", "echo_matmul_int8", "echo_matmul_status",
     "echo_matmul_workspace_bytes",
-    "echo_linear_int8", "NormPlan", "NormParams",
+    "echo_linear_int8", "NormPlan", "NormParams", "Cache", "CacheBatch", "echo_cache_append",
+    "echo_cache_read", "echo_attention", "echo_attention_workspace_bytes", "echo_quantize_weights",
+    "echo_linear_int4", "echo_serving_status",
 )
 
 

@@ -1,0 +1,201 @@
+// attn_common.h -- how echo_attention's work is cut (attn_*.cu): rows of
+// queries into units, the keys that a unit sees into tiles, and the tiles of
+// all units into one even range for each block.
+#pragma once
+
+#include "serve_common.h"
+
+namespace echo {
+
+constexpr float kLog2E = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLowest = -3.4028234663852886e38f;      // a maximum before any key
+constexpr float kNone = -INFINITY;
+
+// Rows of queries that share a head of the cache: row r of a sequence is query
+// head r % group of its token r / group.  A unit is R consecutive rows of one
+// sequence and head, its tiles are the TILE keys at a time from the first to
+// the last that any of its rows sees (one tile at least, so that every row is
+// somebody's to write).
+struct Unit {
+  int sequence, head, first, rows;       // rows of queries [first, first + rows)
+  int tile, tiles;
+};
+
+// Keys [from, to) that the row at a place sees.
+__device__ __forceinline__ int keys_to(const AttentionArgs& a, const Sequence& s, int place) {
+  if (!a.causal) return s.keys;
+  return place + 1 < 0 ? 0 : (place + 1 < s.keys ? place + 1 : s.keys);
+}
+__device__ __forceinline__ int keys_from(const AttentionArgs& a, int place) {
+  return a.window && place >= a.window ? place - a.window + 1 : 0;
+}
+
+template <int R, int TILE>
+__device__ __forceinline__ void unit_tiles(const AttentionArgs& a, const Sequence& s, int j, int* tile, int* tiles) {
+  const int rows = s.rows * a.group, last = (j + 1) * R < rows ? (j + 1) * R : rows;
+  const int from = keys_from(a, s.place + j * R / a.group) / TILE;
+  const int to = (keys_to(a, s, s.place + (last - 1) / a.group) + TILE - 1) / TILE;
+  *tile = from;
+  *tiles = to > from ? to - from : 1;
+}
+template <int R>
+__device__ __forceinline__ int units_of(const AttentionArgs& a, const Sequence& s) {
+  return (s.rows * a.group + R - 1) / R;
+}
+// Tiles of all units of a sequence and one head.
+template <int R, int TILE>
+__device__ __forceinline__ int64_t sequence_tiles(const AttentionArgs& a, const Sequence& s) {
+  int64_t n = 0;
+  for (int j = 0; j < units_of<R>(a, s); ++j) {
+    int tile, tiles;
+    unit_tiles<R, TILE>(a, s, j, &tile, &tiles);
+    n += tiles;
+  }
+  return n;
+}
+
+// A block's range of the tiles of all units, which are ordered by sequence,
+// head, and rows: block c of n has tiles [c T / n, (c + 1) T / n) of T (n no
+// more than T), so that its first and its last unit may be shared with others.
+struct Range {
+  int64_t total, begin, end;             // tiles
+  int blocks;                            // that have any
+  int sequence;                          // that has `begin`
+  int64_t before;                        // tiles of the sequences before it
+};
+__device__ __forceinline__ int64_t range_begin(int64_t total, int block, int blocks) { return total * block / blocks; }
+// The block whose range has a tile (the last that begins at or before it).
+__device__ __forceinline__ int block_of(int64_t total, int64_t tile, int blocks) {
+  return (int)(((tile + 1) * blocks - 1) / total);
+}
+
+// Of a whole block of THREADS threads.  LEAST: tiles that a block has at least
+// where there are few.  `shared`: THREADS / 32 + 2 words of 8 bytes.
+template <int R, int TILE, int THREADS, int LEAST>
+__device__ __forceinline__ Range block_range(const AttentionArgs& a, int64_t* shared, int* bad) {
+  constexpr int kWarps = THREADS / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.batch.sequences;
+  Range r;
+  int64_t mine = 0, sum = 0;             // of the last sequence looked at, of all that this thread has
+  for (int i = tid; i < n; i += THREADS) {
+    mine = sequence_tiles<R, TILE>(a, sequence_of(a.batch, a.cache.page_shift, i, bad)) * a.cache.heads;
+    sum += mine;
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
+  if (lane == 0) shared[warp] = sum;
+  __syncthreads();
+  r.total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) r.total += shared[w];
+  r.blocks = r.total < (int64_t)gridDim.x * LEAST ? (int)((r.total + LEAST - 1) / LEAST) : (int)gridDim.x;
+  const int c = (int)blockIdx.x < r.blocks ? blockIdx.x : r.blocks;
+  r.begin = r.blocks ? range_begin(r.total, c, r.blocks) : 0;
+  r.end = c < r.blocks ? range_begin(r.total, c + 1, r.blocks) : r.begin;
+  r.sequence = 0;
+  r.before = 0;
+  if (r.begin == r.end) return r;        // the whole block
+  // The sequence that has `begin`: prefix sums of THREADS sequences at a time.
+  int64_t before = 0;
+  for (int i0 = 0; i0 < n; i0 += THREADS) {
+    const int i = i0 + tid;
+    if (n > THREADS) {
+      int ignored = 0;
+      mine = i < n ? sequence_tiles<R, TILE>(a, sequence_of(a.batch, a.cache.page_shift, i, &ignored)) * a.cache.heads : 0;
+    } else if (i >= n) {
+      mine = 0;
+    }
+    int64_t prefix = mine;               // inclusive, of the warp
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t other = __shfl_up_sync(kFull, prefix, off);
+      if (lane >= off) prefix += other;
+    }
+    __syncthreads();
+    if (lane == 31) shared[warp] = prefix;
+    __syncthreads();
+    int64_t block = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) prefix += shared[w];
+      block += shared[w];
+    }
+    if (before + prefix > r.begin && before + prefix - mine <= r.begin) {
+      shared[kWarps] = i;
+      shared[kWarps + 1] = before + prefix - mine;
+    }
+    before += block;
+    if (before > r.begin) break;
+  }
+  __syncthreads();
+  r.sequence = (int)shared[kWarps];
+  r.before = shared[kWarps + 1];
+  __syncthreads();
+  return r;
+}
+
+// Workspace: two slots a block, for the parts of its first and its last unit
+// (R rows of maximum, sum and D sums of values, fp32), and what to join.
+struct Join {
+  int blocks;                            // that share the unit: this one and the ones behind it; 0: none
+  int slot;                              // of this block's part
+  int row, head, first, rows;            // first token row of the sequence; the unit
+};
+__host__ __device__ inline int64_t slot_floats(int rows, int dim) { return (int64_t)rows * (dim + 2); }
+__host__ __device__ inline int64_t join_bytes(int blocks) { return ((int64_t)blocks * sizeof(Join) + 255) / 256 * 256; }
+inline int64_t workspace_bytes(int blocks, int rows, int dim) {
+  return join_bytes(blocks) + 2 * (int64_t)blocks * slot_floats(rows, dim) * 4;
+}
+__device__ __forceinline__ Join* joins(const AttentionArgs& a) { return reinterpret_cast<Join*>(a.partial); }
+__device__ __forceinline__ float* slot_at(const AttentionArgs& a, int blocks, int slot, int rows, int dim) {
+  return reinterpret_cast<float*>(reinterpret_cast<char*>(a.partial) + join_bytes(blocks)) + slot * slot_floats(rows, dim);
+}
+
+__device__ __forceinline__ float exp2_of(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float log2_of(float v) {
+  float r;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float reciprocal(float v) {
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// Query rows as f16, scaled by a power of two that takes the row's largest
+// element to [2^14, 2^15): bf16 values stay exact down to 2^-31 of it (f16's
+// subnormals begin 2^-29 below and hold 2^-39 of it).
+__device__ __forceinline__ float row_factor(uint32_t amax_bits) {
+  const int e = (int)(amax_bits >> 23);                  // biased
+  if (e == 255) return 1.0f;
+  return __uint_as_float((uint32_t)(127 + 14 + 127 - (e < 27 ? 27 : e)) << 23);
+}
+
+// One value of a result row in out's type.
+__device__ __forceinline__ void store_value(const AttentionArgs& a, int64_t at, float v) {
+  if (a.dtype == ECHO_BF16) static_cast<__nv_bfloat16*>(a.out.data)[at] = from_float<__nv_bfloat16>(v);
+  else static_cast<__half*>(a.out.data)[at] = from_float<__half>(v);
+}
+__device__ __forceinline__ void store_values4(const AttentionArgs& a, int64_t at, const float (&v)[4], bool vector) {
+  if (!vector) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) store_value(a, at + i, v[i]);
+  } else if (a.dtype == ECHO_BF16) {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out.data) + at) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  } else {
+    const __half2 lo = __floats2half2_rn(v[0], v[1]), hi = __floats2half2_rn(v[2], v[3]);
+    *reinterpret_cast<uint2*>(static_cast<__half*>(a.out.data) + at) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  }
+}
+// Whether rows of out take 8-byte stores.
+inline bool vector_rows(const HeadsArgs& h) { return on_boundary(h.data, 8) && h.ld % 4 == 0 && h.head_stride % 4 == 0; }
+
+}  // namespace echo

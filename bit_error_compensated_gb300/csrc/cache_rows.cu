@@ -1,0 +1,218 @@
+// cache_rows.cu -- echo_cache_append and echo_cache_read (include/echo.h).
+//
+// A head's row of a token is one group: head_dim / 16 lanes hold it, 16 values
+// each, so that a warp takes 8, 4 or 2 rows with 16-byte accesses and its
+// lanes' shuffles find a row's range.  A warp's rows belong to one token, whose
+// sequence its 32 lanes look for together.  Both kernels move bytes and little
+// else: a row of 128 in 16 bits is 256 bytes in and 68 out (4 bits).
+#include "serve_common.h"
+
+namespace echo {
+namespace {
+
+ECHO_STATUS_WORD
+
+constexpr int kWarps = 4;
+
+// Values [8 NL h + 8 q, + 8) of a row, h = 0, 1, as lane q of the row's NL.
+template <typename T, int NL>
+__device__ __forceinline__ void load_row(const T* row, int q, bool aligned, float (&v)[16]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const T* p = row + 8 * NL * h + 8 * q;
+    float f[8];
+    if (aligned) {
+      to_floats<T, 8>(load_pack<T, 8>(p), f);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = to_float(p[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[8 * h + i] = f[i];
+  }
+}
+
+// Which row of which token a lane works on: warps take a token's 2 * heads
+// rows in turn.
+struct Place {
+  int token, row;                // row: head, or heads + head of the values
+  bool there;
+};
+template <int NL>
+__device__ __forceinline__ Place place_of(int heads, int tokens, int lane) {
+  constexpr int kRows = 32 / NL;
+  const int each = (2 * heads + kRows - 1) / kRows;      // warps a token
+  const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  Place p;
+  p.token = (int)(w / each);
+  p.row = (int)(w % each) * kRows + lane / NL;
+  p.there = p.token < tokens && p.row < 2 * heads;
+  return p;
+}
+
+// What only a look at all starts shows.
+__device__ __forceinline__ void check_starts(const BatchArgs& b) {
+  if (blockIdx.x != 0) return;
+  bool bad = false;
+  for (int i = threadIdx.x; i < b.sequences; i += 32 * kWarps)
+    bad |= b.starts[i] < 0 || b.starts[i + 1] < b.starts[i] || b.starts[i + 1] > b.tokens;
+  if (bad) report(kBadRows);
+}
+
+// The place of a token in its sequence, or -1, and whether it is a batch's at all.
+__device__ __forceinline__ bool token_place(const BatchArgs& b, int page_shift, int t, int lane, int* sequence,
+                                            int* place) {
+  const int i = sequence_at(b, t, lane);
+  if (i < 0 || i >= b.sequences) return false;
+  int bad = 0;
+  const Sequence s = sequence_of(b, page_shift, i, &bad);
+  if (t < s.row || t >= s.row + s.rows) return false;
+  *sequence = i;
+  *place = s.place + (t - s.row);
+  return true;
+}
+
+template <typename T, int NL>
+__global__ void __launch_bounds__(32 * kWarps) append_kernel(const RowsArgs a, const int aligned) {
+  pdl_wait();
+  pdl_trigger();
+  check_starts(a.batch);
+  const int lane = threadIdx.x & 31, q = lane % NL;
+  const Place p = place_of<NL>(a.cache.heads, a.batch.tokens, lane);
+  if (p.token >= a.batch.tokens) return;                 // the whole warp
+  float v[16] = {};
+  const bool value = p.row >= a.cache.heads;
+  const int head = p.row - (value ? a.cache.heads : 0);
+  if (p.there) {
+    const HeadsArgs& from = value ? a.v : a.k;
+    load_row<T, NL>(static_cast<const T*>(from.data) + p.token * from.ld + head * from.head_stride, q, aligned, v);
+  }
+  __syncwarp();
+  int sequence, place;
+  if (!token_place(a.batch, a.cache.page_shift, p.token, lane, &sequence, &place) || place < 0) return;
+  const int page = page_of(a.batch, a.cache, sequence, place);
+  if (page < 0) {
+    if (lane == 0) report(kBadPage);
+    return;
+  }
+  const float L = a.cache.bits == 4 ? 15.0f : 255.0f;
+  float lo, hi;
+  group_range<NL>(v, lo, hi);
+  if (!p.there) return;
+  const GroupStep g = group_step(lo, hi, L);
+  const int64_t at = group_index(a.cache, page, head, place) + (value ? (int64_t)a.cache.heads << a.cache.page_shift : 0);
+  if (q == 0) {
+    a.cache.meta[at] = g.meta;
+    if (!g.finite) report(kNaNGroup);
+  }
+  uint8_t* codes = a.cache.codes + at * (2 * NL * a.cache.bits);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t low = 0, high = 0;
+    const int first = 8 * NL * h + 8 * q;
+    if (a.cache.bits == 4) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) low |= group_code(v[8 * h + i], g, 15.0f) << (4 * i);
+      *reinterpret_cast<uint32_t*>(codes + first / 2) = low;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        low |= group_code(v[8 * h + i], g, 255.0f) << (8 * i);
+        high |= group_code(v[8 * h + 4 + i], g, 255.0f) << (8 * i);
+      }
+      *reinterpret_cast<uint2*>(codes + first) = make_uint2(low, high);
+    }
+  }
+}
+
+template <typename T, int NL>
+__global__ void __launch_bounds__(32 * kWarps) read_kernel(const RowsArgs a, const int aligned) {
+  pdl_wait();
+  pdl_trigger();
+  check_starts(a.batch);
+  const int lane = threadIdx.x & 31, q = lane % NL;
+  const Place p = place_of<NL>(a.cache.heads, a.batch.tokens, lane);
+  if (p.token >= a.batch.tokens) return;                 // the whole warp
+  int sequence, place;
+  if (!token_place(a.batch, a.cache.page_shift, p.token, lane, &sequence, &place)) return;
+  const int page = place < 0 ? -1 : page_of(a.batch, a.cache, sequence, place);
+  if (page < 0 && place >= 0 && lane == 0) report(kBadPage);
+  const bool value = p.row >= a.cache.heads;
+  const int head = p.row - (value ? a.cache.heads : 0);
+  const HeadsArgs& into = value ? a.v : a.k;
+  if (!p.there || into.data == nullptr) return;
+  float s = 0.0f, z = 0.0f;
+  uint32_t word[4] = {};
+  if (page >= 0) {
+    const int64_t at = group_index(a.cache, page, head, place) + (value ? (int64_t)a.cache.heads << a.cache.page_shift : 0);
+    const uint32_t meta = a.cache.meta[at];
+    const uint8_t* codes = a.cache.codes + at * (2 * NL * a.cache.bits);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int first = 8 * NL * h + 8 * q;
+      if (a.cache.bits == 4) {
+        word[2 * h] = *reinterpret_cast<const uint32_t*>(codes + first / 2);
+      } else {
+        const uint2 two = *reinterpret_cast<const uint2*>(codes + first);
+        word[2 * h] = two.x;
+        word[2 * h + 1] = two.y;
+      }
+    }
+    s = meta_step(meta);
+    z = meta_zero(meta);
+  }
+  T* row = static_cast<T*>(into.data) + p.token * into.ld + head * into.head_stride;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t c = a.cache.bits == 4 ? (word[2 * h] >> (4 * i)) & 15u : (word[2 * h + i / 4] >> (8 * (i % 4))) & 255u;
+      v[i] = __fmul_rn(s, __fsub_rn((float)c, z));       // exact: 11 and 9 bits
+    }
+    T* to = row + 8 * NL * h + 8 * q;
+    if (aligned) {
+      store_floats<T, 8>(to, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) to[i] = from_float<T>(v[i]);
+    }
+  }
+}
+
+template <typename T, int NL>
+cudaError_t launch(const RowsArgs& a, bool append, cudaStream_t s) {
+  constexpr int kRows = 32 / NL;
+  const int64_t each = (2 * a.cache.heads + kRows - 1) / kRows;
+  bool aligned = true;
+  for (const HeadsArgs* h : {&a.k, &a.v})
+    aligned = aligned && on_boundary(h->data, 16) && h->ld % (16 / sizeof(T)) == 0 && h->head_stride % (16 / sizeof(T)) == 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((each * a.batch.tokens + kWarps - 1) / kWarps));
+  cfg.blockDim = dim3(32 * kWarps);
+  cfg.stream = s;
+  cudaLaunchAttribute overlapped = overlapped_launch();
+  cfg.attrs = &overlapped;
+  cfg.numAttrs = 1;
+  return append ? cudaLaunchKernelEx(&cfg, append_kernel<T, NL>, a, (int)aligned)
+                : cudaLaunchKernelEx(&cfg, read_kernel<T, NL>, a, (int)aligned);
+}
+template <typename T>
+cudaError_t launch(const RowsArgs& a, bool append, cudaStream_t s) {
+  if (a.cache.head_dim == 64) return launch<T, 4>(a, append, s);
+  if (a.cache.head_dim == 128) return launch<T, 8>(a, append, s);
+  return launch<T, 16>(a, append, s);
+}
+cudaError_t launch(const RowsArgs& a, int dtype, bool append, cudaStream_t s) {
+  if (dtype == ECHO_F32) return launch<float>(a, append, s);
+  if (dtype == ECHO_BF16) return launch<__nv_bfloat16>(a, append, s);
+  return launch<__half>(a, append, s);
+}
+
+}  // namespace
+
+cudaError_t launch_append(const RowsArgs& a, int dtype, cudaStream_t s) { return launch(a, dtype, true, s); }
+cudaError_t launch_read(const RowsArgs& a, int dtype, cudaStream_t s) { return launch(a, dtype, false, s); }
+StatusWord rows_status() { return {read_status, clear_status_bits}; }
+
+}  // namespace echo

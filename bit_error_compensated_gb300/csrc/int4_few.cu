@@ -1,0 +1,285 @@
+// int4_few.cu -- echo_linear_int4 (include/echo.h): few tokens with 4-bit
+// weights.
+//
+// The weights are read once for 32 tokens and streamed: a block takes 16 (or
+// 32) channels, its warps take windows of their depth in turn, and a thread's
+// loads are the operands of matrix instructions: as long as weights and tokens
+// are cut the same way, the codes that a thread has of a row can be any of the
+// instruction's places.  A code behind the bits of 128 (bf16) or 1024 (f16) is
+// that number plus the code; taking off that number plus the zero point leaves
+// code - z, exact.  Products are exact, a window's sums (of one group) are
+// multiplied by the group's step in fp32 and added up.  fp32 tokens are three
+// bf16 numbers each, which hold all their bits.
+#include "serve_common.h"
+
+namespace echo {
+namespace {
+
+constexpr int kWarps = 8;
+
+template <typename T> struct Codes {                     // f16 tokens
+  static constexpr uint32_t kBase = 0x64006400u;
+  static __device__ __forceinline__ uint32_t base_and(float z) {         // 1024 + z, twice
+    const __half2 h = __float2half2_rn(1024.0f + z);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  static __device__ __forceinline__ uint32_t less(uint32_t a, uint32_t b) {
+    const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&d);
+  }
+  static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t* lo, const uint32_t* hi, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3},{%4,%5,%6,%7},{%8,%9},{%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(lo[0]), "r"(hi[0]), "r"(lo[1]), "r"(hi[1]), "r"(b0), "r"(b1));
+  }
+};
+struct CodesBf16 {
+  static constexpr uint32_t kBase = 0x43004300u;
+  static __device__ __forceinline__ uint32_t base_and(float z) {
+    const __nv_bfloat162 h = __float2bfloat162_rn(128.0f + z);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  static __device__ __forceinline__ uint32_t less(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&d);
+  }
+  static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t* lo, const uint32_t* hi, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3},{%4,%5,%6,%7},{%8,%9},{%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(lo[0]), "r"(hi[0]), "r"(lo[1]), "r"(hi[1]), "r"(b0), "r"(b1));
+  }
+};
+template <> struct Codes<__nv_bfloat16> : CodesBf16 {};
+template <> struct Codes<float> : CodesBf16 {};
+
+// Eight codes of a word, less the zero point, as pairs of elements (0, 4),
+// (1, 5), (2, 6), (3, 7).
+template <typename T>
+__device__ __forceinline__ void turn(uint32_t w, uint32_t zero, uint32_t (&h)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    h[i] = Codes<T>::less(((w >> (4 * i)) & 0x000F000Fu) | Codes<T>::kBase, zero);
+}
+
+// WORDS words of a row of `bytes` bytes from byte `at` (a multiple of 4 WORDS),
+// zeros behind its end.  ALIGNED: rows start on multiples of 4 WORDS bytes.
+template <int WORDS, bool ALIGNED>
+__device__ __forceinline__ void load_codes(const uint8_t* row, int64_t at, int64_t bytes, uint32_t (&w)[WORDS]) {
+  const uint8_t* p = row + at;
+  if (ALIGNED && at + 4 * WORDS <= bytes) {
+    if constexpr (WORDS == 4) {
+      const uint4 v = load_free16(p);
+      w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+    } else {
+      asm("ld.global.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+    }
+    return;
+  }
+  if (!ALIGNED && at >= 3 && at + 4 * WORDS + 3 <= bytes) {
+    // put together from the aligned words around it, all of them inside the row too
+    const uint32_t shift = (uint32_t)((uintptr_t)p & 3) * 8;
+    const uint32_t* from = reinterpret_cast<const uint32_t*>((uintptr_t)p & ~(uintptr_t)3);
+    uint32_t v[WORDS + 1];
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) v[i] = load_free4(from + i);
+    v[WORDS] = shift ? load_free4(from + WORDS) : 0;
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) w[i] = __funnelshift_r(v[i], v[i + 1], shift);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < WORDS; ++i) w[i] = 0;
+#pragma unroll
+  for (int i = 0; i < 4 * WORDS; ++i)
+    if (at + i < bytes) w[i / 4] |= (uint32_t)p[i] << (8 * (i % 4));
+}
+
+// Eight elements of a token's row from k, zeros behind its end, in the order of
+// turn's pairs: PARTS operands of four registers, whose sum they are.
+template <typename T> constexpr int parts() { return sizeof(T) == 4 ? 3 : 1; }
+template <typename T, bool ALIGNED>
+__device__ __forceinline__ void load_tokens(const T* row, int64_t k, int64_t depth, uint32_t (&h)[parts<T>()][4]) {
+  if constexpr (sizeof(T) == 2) {
+    uint32_t w[4] = {0, 0, 0, 0};
+    if (ALIGNED && k + 8 <= depth) {
+      const uint4 v = load_free16(row + k);
+      w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (k + i < depth) w[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(row)[k + i] << (16 * (i % 2));
+    }
+    h[0][0] = __byte_perm(w[0], w[2], 0x5410);
+    h[0][1] = __byte_perm(w[0], w[2], 0x7632);
+    h[0][2] = __byte_perm(w[1], w[3], 0x5410);
+    h[0][3] = __byte_perm(w[1], w[3], 0x7632);
+  } else {
+    float v[8];
+    if (ALIGNED && k + 8 <= depth) {
+      const uint4 a = load_free16(row + k), b = load_free16(row + k + 4);
+      v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y); v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
+      v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y); v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = k + i < depth ? row[k + i] : 0.0f;
+    }
+    // The upper 8 bits of the significand, the next, and the rest; an infinity is its own first part.
+#pragma unroll
+    for (int part = 0; part < 3; ++part)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = __float_as_uint(v[i]), hi = __float_as_uint(v[i + 4]);
+        h[part][i] = __byte_perm(lo, hi, 0x7632);
+        if (part < 2) {
+          const float rest = v[i] - __uint_as_float(lo & 0xFFFF0000u), rest4 = v[i + 4] - __uint_as_float(hi & 0xFFFF0000u);
+          v[i] = isfinite(v[i]) ? rest : 0.0f;
+          v[i + 4] = isfinite(v[i + 4]) ? rest4 : 0.0f;
+        }
+      }
+  }
+}
+
+// OCTETS: of tokens; TALL: 16-channel parts of a block; WORDS: of a row's
+// window, a thread's (a window is 32 WORDS codes of one group); DEEP: windows
+// loaded at once.
+template <typename T, int OCTETS, int TALL, int WORDS, int DEEP, bool ALIGNED>
+__global__ void __launch_bounds__(32 * kWarps) linear4_kernel(const Linear4Args p) {
+  constexpr int kRows = 16 * TALL, kCols = 8 * OCTETS, kWindow = 32 * WORDS, kParts = parts<T>();
+  __shared__ float total[kWarps][kCols][kRows + 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, quad = lane & 3;
+  const int64_t rank = blockIdx.z, c0 = (int64_t)blockIdx.x * kRows, t0 = (int64_t)blockIdx.y * kCols;
+  const int64_t bytes = (p.depth + 1) / 2;
+  pdl_wait();
+  pdl_trigger();
+  // Rows past the last channel or token repeat it: their results are dropped.
+  const uint8_t* codes[2 * TALL];
+  const uint32_t* meta[2 * TALL];
+#pragma unroll
+  for (int i = 0; i < 2 * TALL; ++i) {
+    const int64_t c = c0 + 8 * i + g < p.channels ? c0 + 8 * i + g : p.channels - 1;
+    codes[i] = pinned(p.codes + rank * p.rank_codes + c * p.ld_codes);
+    meta[i] = pinned(p.meta + rank * p.rank_meta + c * p.ld_meta);
+  }
+  const T* x[OCTETS];
+#pragma unroll
+  for (int i = 0; i < OCTETS; ++i) {
+    const int64_t t = t0 + 8 * i + g < p.tokens ? t0 + 8 * i + g : p.tokens - 1;
+    x[i] = pinned(static_cast<const T*>(p.x) + rank * p.rank_x + t * p.ld_x);
+  }
+  float sum[TALL][OCTETS][4];
+#pragma unroll
+  for (int r = 0; r < TALL; ++r)
+#pragma unroll
+    for (int o = 0; o < OCTETS; ++o)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[r][o][i] = 0.0f;
+
+  const int64_t windows = (p.depth + kWindow - 1) / kWindow;
+#pragma unroll 1
+  for (int64_t first = warp; first < windows; first += DEEP * kWarps) {
+    uint32_t w[DEEP][2 * TALL][WORDS], word[DEEP][2 * TALL];
+#pragma unroll
+    for (int d = 0; d < DEEP; ++d) {
+      const int64_t window = first + d * kWarps;
+      const bool there = window < windows;
+#pragma unroll
+      for (int i = 0; i < 2 * TALL; ++i) {
+        load_codes<WORDS, ALIGNED>(codes[i], there ? window * (kWindow / 2) + 4 * WORDS * quad : bytes, bytes, w[d][i]);
+        word[d][i] = there ? load_free4(meta[i] + window * kWindow / p.group) : 0;
+      }
+    }
+#pragma unroll
+    for (int d = 0; d < DEEP; ++d) {
+      const int64_t k = (first + d * kWarps) * kWindow + 8 * WORDS * quad;
+      if (first + d * kWarps >= windows) break;            // the whole warp
+      float part[TALL][OCTETS][4] = {};
+      uint32_t zero[2 * TALL];
+#pragma unroll
+      for (int i = 0; i < 2 * TALL; ++i) zero[i] = Codes<T>::base_and(meta_zero(word[d][i]));
+#pragma unroll
+      for (int n = 0; n < WORDS; ++n) {
+        uint32_t lo[TALL][4], hi[TALL][4];
+#pragma unroll
+        for (int r = 0; r < TALL; ++r) {
+          turn<T>(w[d][2 * r][n], zero[2 * r], lo[r]);
+          turn<T>(w[d][2 * r + 1][n], zero[2 * r + 1], hi[r]);
+        }
+#pragma unroll
+        for (int o = 0; o < OCTETS; ++o) {
+          uint32_t b[kParts][4];
+          load_tokens<T, ALIGNED>(x[o], k + 8 * n, p.depth, b);
+          __syncwarp();                                    // a row's ragged end parts the lanes; matrix instructions want them together
+#pragma unroll
+          for (int q = 0; q < kParts; ++q)
+#pragma unroll
+            for (int r = 0; r < TALL; ++r) {
+              Codes<T>::mma(part[r][o], lo[r], hi[r], b[q][0], b[q][1]);
+              Codes<T>::mma(part[r][o], lo[r] + 2, hi[r] + 2, b[q][2], b[q][3]);
+            }
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < TALL; ++r) {
+        const float s0 = meta_step(word[d][2 * r]), s1 = meta_step(word[d][2 * r + 1]);
+#pragma unroll
+        for (int o = 0; o < OCTETS; ++o)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sum[r][o][i] = fmaf(part[r][o][i], i < 2 ? s0 : s1, sum[r][o][i]);
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < TALL; ++r)
+#pragma unroll
+    for (int o = 0; o < OCTETS; ++o)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) total[warp][8 * o + 2 * quad + (i & 1)][16 * r + g + 8 * (i >> 1)] = sum[r][o][i];
+  __syncthreads();
+  for (int i = threadIdx.x; i < kRows * kCols; i += 32 * kWarps) {
+    const int64_t c = c0 + i % kRows, t = t0 + i / kRows;
+    if (c >= p.channels || t >= p.tokens) continue;
+    float v = 0.0f;
+#pragma unroll
+    for (int n = 0; n < kWarps; ++n) v += total[n][i / kRows][i % kRows];
+    static_cast<T*>(p.out)[rank * p.rank_out + t * p.ld_out + c] = from_float<T>(v);
+  }
+}
+
+template <typename T, int OCTETS, int TALL, int WORDS, int DEEP>
+cudaError_t launch(const Linear4Args& p, cudaStream_t s) {
+  const int64_t in16 = 16 / (int64_t)sizeof(T);
+  const bool aligned = on_boundary(p.codes, 16) && (p.channels == 1 || p.ld_codes % 16 == 0) &&
+                       (p.ranks == 1 || p.rank_codes % 16 == 0) && on_boundary(p.x, 16) &&
+                       (p.tokens == 1 || p.ld_x % in16 == 0) && (p.ranks == 1 || p.rank_x % in16 == 0);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((p.channels + 16 * TALL - 1) / (16 * TALL)),
+                     (unsigned)((p.tokens + 8 * OCTETS - 1) / (8 * OCTETS)), (unsigned)p.ranks);
+  cfg.blockDim = dim3(32 * kWarps);
+  cfg.stream = s;
+  cudaLaunchAttribute overlapped = overlapped_launch();
+  cfg.attrs = &overlapped;
+  cfg.numAttrs = 1;
+  return aligned ? cudaLaunchKernelEx(&cfg, linear4_kernel<T, OCTETS, TALL, WORDS, DEEP, true>, p)
+                 : cudaLaunchKernelEx(&cfg, linear4_kernel<T, OCTETS, TALL, WORDS, DEEP, false>, p);
+}
+template <typename T, int WORDS>
+cudaError_t launch(const Linear4Args& p, cudaStream_t s) {
+  if (p.tokens <= 8) return launch<T, 1, 1, WORDS, 4>(p, s);
+  if (p.tokens <= 16) return launch<T, 2, 1, WORDS, 4>(p, s);
+  return launch<T, 4, 2, WORDS, 2>(p, s);
+}
+template <typename T>
+cudaError_t launch(const Linear4Args& p, cudaStream_t s) {
+  return p.group == 64 ? launch<T, 2>(p, s) : launch<T, 4>(p, s);
+}
+
+}  // namespace
+
+cudaError_t launch_linear4(const Linear4Args& p, int sms, cudaStream_t s) {
+  (void)sms;
+  if (p.dtype == ECHO_F32) return launch<float>(p, s);
+  if (p.dtype == ECHO_BF16) return launch<__nv_bfloat16>(p, s);
+  return launch<__half>(p, s);
+}
+
+}  // namespace echo

@@ -1,0 +1,104 @@
+// int4_quantize.cu -- echo_quantize_weights (include/echo.h): weights to 4-bit
+// codes in groups along their depth.
+//
+// group / 16 lanes hold a group, 16 values each, as in the all-reduce's push;
+// a warp takes 8, 4 or 2 groups of a row that follow each other.  The kernel is
+// bound by the weights that it reads: 2 bytes in and 0.53 out in 16 bits.
+#include "serve_common.h"
+
+namespace echo {
+namespace {
+
+ECHO_STATUS_WORD
+
+constexpr int kWarps = 8;
+
+template <typename T, int NL>
+__global__ void __launch_bounds__(32 * kWarps) quantize_weights_kernel(const WeightsArgs a, const int aligned) {
+  constexpr int kGroups = 32 / NL, kGroup = 16 * NL;
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, q = lane % NL;
+  const int64_t groups = (a.depth + kGroup - 1) / kGroup, each = (groups + kGroups - 1) / kGroups;   // warps a row
+  const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int64_t row = w / each;
+  if (row >= a.ranks * a.channels) return;               // the whole warp
+  const int64_t rank = row / a.channels, channel = row - rank * a.channels;
+  const int64_t group = w % each * kGroups + lane / NL, k0 = group * kGroup;
+  const T* from = static_cast<const T*>(a.w) + rank * a.rank_w + channel * a.ld_w + k0;
+  const int64_t here = a.depth - k0;                     // values of this group, if fewer than all
+  float v[16] = {};
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int first = 8 * NL * h + 8 * q;
+    if (aligned && first + 8 <= here) {
+      float f[8];
+      to_floats<T, 8>(load_pack<T, 8>(from + first), f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[8 * h + i] = f[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (first + i < here) v[8 * h + i] = to_float(from[first + i]);
+    }
+  }
+  __syncwarp();
+  float lo, hi;
+  group_range<NL>(v, lo, hi);
+  if (here <= 0) return;
+  const GroupStep g = group_step(lo, hi, 15.0f);
+  if (q == 0) {
+    a.meta[rank * a.rank_meta + channel * a.ld_meta + group] = g.meta;
+    if (!g.finite) report(kNaNGroup);
+  }
+  uint8_t* to = a.codes + rank * a.rank_codes + channel * a.ld_codes + k0 / 2;
+  const bool words = ((uintptr_t)to & 3) == 0;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int first = 8 * NL * h + 8 * q;
+    uint32_t codes = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (first + i < here) codes |= group_code(v[8 * h + i], g, 15.0f) << (4 * i);
+    if (words && first + 8 <= here) {
+      *reinterpret_cast<uint32_t*>(to + first / 2) = codes;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; i += 2)
+        if (first + i < here) to[(first + i) / 2] = (uint8_t)(codes >> (4 * i));
+    }
+  }
+}
+
+template <typename T, int NL>
+cudaError_t launch(const WeightsArgs& a, cudaStream_t s) {
+  constexpr int kGroups = 32 / NL, kGroup = 16 * NL;
+  const int64_t groups = (a.depth + kGroup - 1) / kGroup, warps = (groups + kGroups - 1) / kGroups * a.ranks * a.channels;
+  const int64_t in16 = 16 / (int64_t)sizeof(T);
+  const bool aligned = on_boundary(a.w, 16) && (a.channels == 1 || a.ld_w % in16 == 0) && (a.ranks == 1 || a.rank_w % in16 == 0);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((warps + kWarps - 1) / kWarps));
+  cfg.blockDim = dim3(32 * kWarps);
+  cfg.stream = s;
+  cudaLaunchAttribute overlapped = overlapped_launch();
+  cfg.attrs = &overlapped;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, quantize_weights_kernel<T, NL>, a, (int)aligned);
+}
+template <typename T>
+cudaError_t launch(const WeightsArgs& a, cudaStream_t s) {
+  if (a.group == 64) return launch<T, 4>(a, s);
+  if (a.group == 128) return launch<T, 8>(a, s);
+  return launch<T, 16>(a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_weights(const WeightsArgs& a, int dtype, cudaStream_t s) {
+  if (dtype == ECHO_F32) return launch<float>(a, s);
+  if (dtype == ECHO_BF16) return launch<__nv_bfloat16>(a, s);
+  return launch<__half>(a, s);
+}
+StatusWord weights_status() { return {read_status, clear_status_bits}; }
+
+}  // namespace echo

@@ -1,0 +1,220 @@
+// serve_common.h -- shared by the operators of a serving step (cache_*.cu,
+// attn_*.cu, int4_*.cu): launch arguments, a batch's geometry, and the group
+// quantizer with exact quotients.  The operators are described in
+// include/echo.h.
+#pragma once
+
+#include "ops_common.h"
+#include "quant.cuh"
+
+namespace echo {
+
+// Bits of the status words.
+constexpr int kBadPage = 1, kBadRows = 2, kNaNGroup = 4, kGaveUp = 8;
+
+struct CacheArgs {
+  uint8_t* codes;
+  uint32_t* meta;
+  int64_t pages;
+  int heads, head_dim, bits;
+  int page_shift;                // log2 of page_size
+};
+
+struct BatchArgs {
+  const int32_t* starts;
+  const int32_t* lengths;
+  const int32_t* table;
+  int64_t ld_table;
+  int sequences, tokens, table_pages;
+};
+
+struct HeadsArgs {
+  void* data;
+  int64_t ld, head_stride;
+};
+
+struct RowsArgs {
+  CacheArgs cache;
+  BatchArgs batch;
+  HeadsArgs k, v;                // data nullptr: not read back
+};
+
+struct AttentionArgs {
+  CacheArgs cache;
+  BatchArgs batch;
+  HeadsArgs q, out;
+  float* lse;
+  int heads, group;              // query heads, and to a head of the cache
+  int dtype;
+  float scale;
+  int causal;
+  int window;                    // 0: none
+  float* partial;                // workspace
+};
+
+struct WeightsArgs {
+  const void* w;
+  int64_t ld_w, rank_w;
+  uint8_t* codes;
+  int64_t ld_codes, rank_codes;
+  uint32_t* meta;
+  int64_t ld_meta, rank_meta;
+  int64_t ranks, channels, depth;
+  int group;
+};
+
+struct Linear4Args {
+  const void* x;
+  int64_t ld_x, rank_x;
+  const uint8_t* codes;
+  int64_t ld_codes, rank_codes;
+  const uint32_t* meta;
+  int64_t ld_meta, rank_meta;
+  void* out;
+  int64_t ld_out, rank_out;
+  int64_t ranks, tokens, channels, depth;
+  int group, dtype;
+};
+
+cudaError_t launch_append(const RowsArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_read(const RowsArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_attention(const AttentionArgs& a, int sms, cudaStream_t s);
+int64_t attention_bytes(int head_dim, int sms);        // of its workspace
+cudaError_t launch_quantize_weights(const WeightsArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_linear4(const Linear4Args& a, int sms, cudaStream_t s);
+
+// Each translation unit whose kernels report has a status word of its own:
+// read copies it to the host on a stream, clear takes the bits that were read
+// off it (one that a kernel sets meanwhile is the next call's to report).
+struct StatusWord {
+  cudaError_t (*read)(int* word, cudaStream_t s);
+  cudaError_t (*clear)(int bits, cudaStream_t s);
+};
+StatusWord rows_status();
+StatusWord attn_few_status();
+StatusWord weights_status();
+
+#define ECHO_STATUS_WORD                                                              \
+  __device__ int g_status;                                                            \
+  __global__ void clear_status(int bits) { atomicAnd(&g_status, ~bits); }             \
+  cudaError_t read_status(int* word, cudaStream_t s) {                                \
+    return cudaMemcpyFromSymbolAsync(word, g_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s); \
+  }                                                                                   \
+  cudaError_t clear_status_bits(int bits, cudaStream_t s) {                           \
+    clear_status<<<1, 1, 0, s>>>(bits);                                               \
+    return cudaGetLastError();                                                        \
+  }                                                                                   \
+  __device__ __forceinline__ void report(int bits) { atomicOr(&g_status, bits); }
+
+// ------------------------------------------------------------------ batches
+// One sequence of a batch: its rows of the token tensors and its tokens in the
+// cache, as far as the arrays make sense.
+struct Sequence {
+  int row, rows;                 // first of its rows, and how many
+  int length;                    // as given (0 if negative)
+  int keys;                      // of these, that the table has room for
+  int place;                     // of its first row, may be negative
+};
+__device__ __forceinline__ Sequence sequence_of(const BatchArgs& b, int page_shift, int i, int* bad) {
+  Sequence s;
+  const int first = b.starts[i], last = b.starts[i + 1], length = b.lengths[i];
+  if (last < first || first < 0 || last > b.tokens) *bad |= kBadRows;
+  const int from = first < 0 ? 0 : first, to = last > b.tokens ? b.tokens : last;
+  s.row = from;
+  s.rows = to > from ? to - from : 0;
+  s.length = length < 0 ? 0 : length;
+  const int64_t room = (int64_t)b.table_pages << page_shift;
+  s.keys = s.length < room ? s.length : (int)room;
+  if (s.rows > 0 && s.length > room) *bad |= kBadPage;
+  // row `first` is at length - (last - first), whether or not it exists
+  const int64_t place = (int64_t)s.length - ((int64_t)last - from);
+  s.place = place < -(1 << 30) ? -(1 << 30) : (int)place;
+  return s;
+}
+
+// The sequence whose rows hold row t (as far as starts rise), -1 or
+// `sequences` where none does; of a whole warp, 32 probes a step.
+__device__ __forceinline__ int sequence_at(const BatchArgs& b, int t, int lane) {
+  int lo = 0, n = b.sequences + 1;
+  for (;;) {
+    const int step = (n + 31) / 32, at = lane * step;
+    const bool below = at < n && b.starts[lo + at] <= t;
+    const int k = __popc(__ballot_sync(kFull, below));
+    if (k == 0) return lo - 1;
+    if (step == 1) return lo + k - 1;
+    lo += (k - 1) * step;
+    n = n - (k - 1) * step < step ? n - (k - 1) * step : step;
+  }
+}
+
+// The page of a place, or -1 (reported) if the table or the cache has none.
+__device__ __forceinline__ int page_of(const BatchArgs& b, const CacheArgs& c, int sequence, int place) {
+  const int at = place >> c.page_shift;
+  if (at >= b.table_pages) return -1;
+  const int page = b.table[(int64_t)sequence * b.ld_table + at];
+  return page >= 0 && page < c.pages ? page : -1;
+}
+
+// Where the groups of a page's place begin, in groups: keys, or values `heads << page_shift` later.
+__device__ __forceinline__ int64_t group_index(const CacheArgs& c, int page, int head, int place) {
+  return ((((int64_t)page * 2 * c.heads + head) << c.page_shift) + (place & ((1 << c.page_shift) - 1)));
+}
+
+// ------------------------------------------------------------------- groups
+// The least fp16 number s with s * L >= hi - lo, exactly: from the rounded
+// quotient, which is off by one step at most.  s * L has 19 bits, so it is
+// exact in fp32; hi - lo is d + e exactly, and s * L - d is exact because the
+// two are near each other.
+__device__ __forceinline__ bool covers(unsigned short s, float L, float d, float e) {
+  return __fsub_rn(__fmul_rn(__half2float(__ushort_as_half(s)), L), d) >= e;
+}
+struct GroupStep {
+  float s, inv, zf;
+  uint32_t meta;
+  bool finite;
+};
+// rint(v / s) with the quotient exact, for |v / s| < 256 and inv = fl(1 / s):
+// where the product with inv lies near a half, v is compared with s times that
+// half, which has 21 bits at most and so is exact.
+__device__ __forceinline__ float exact_rint(float v, float s, float inv) {
+  const float t = __fmul_rn(v, inv), r = rint_small(t);
+  if (fabsf(__fsub_rn(t, r)) < kFastRintLimit) return r;
+  const float low = floorf(t), half = __fmul_rn(s, __fadd_rn(low, 0.5f));
+  if (v != half) return v > half ? __fadd_rn(low, 1.0f) : low;
+  return rintf(__fadd_rn(low, 0.5f));
+}
+__device__ __forceinline__ GroupStep group_step(float lo, float hi, float L) {
+  GroupStep g;
+  const float d = __fsub_rn(hi, lo), b = -lo, bb = __fsub_rn(d, hi);
+  const float err = __fadd_rn(__fsub_rn(hi, __fsub_rn(d, bb)), __fsub_rn(b, bb));   // hi - lo is d + err
+  unsigned short s = __half_as_ushort(__float2half_ru(__fdiv_rn(d, L)));
+  g.finite = isfinite(d) && s < 0x7C00;
+  if (g.finite) {
+    if (!covers(s, L, d, err)) ++s;
+    else if (s > 0 && covers(s - 1, L, d, err)) --s;
+    if (s == 0) s = 0x3C00;      // 1, only for a group of zeros
+    g.finite = s < 0x7C00;
+  }
+  g.s = __half2float(__ushort_as_half(s));
+  g.inv = __frcp_rn(g.s);
+  g.zf = 0.0f;
+  g.meta = 0x7E00u;              // a step of NaN
+  if (g.finite) {
+    g.zf = fminf(fmaxf(exact_rint(-lo, g.s, g.inv), 0.0f), L);
+    g.meta = (uint32_t)s | ((uint32_t)__half_as_ushort(__float2half_rn(g.zf)) << 16);
+  }
+  return g;
+}
+__device__ __forceinline__ uint32_t group_code(float v, const GroupStep& g, float L) {
+  if (!g.finite) return 0;
+  const float c = __fadd_rn(exact_rint(v, g.s, g.inv), g.zf);
+  return (uint32_t)__float2int_rn(fminf(fmaxf(c, 0.0f), L));
+}
+__device__ __forceinline__ float meta_step(uint32_t meta) {
+  return __half2float(__ushort_as_half((unsigned short)(meta & 0xFFFFu)));
+}
+__device__ __forceinline__ float meta_zero(uint32_t meta) {
+  return __half2float(__ushort_as_half((unsigned short)(meta >> 16)));
+}
+
+}  // namespace echo

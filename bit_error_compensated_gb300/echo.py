@@ -48,6 +48,8 @@ ECHO_NORM_LAYER = 1
 ECHO_NORM_MAX_WIDTH = 16384
 ECHO_MATMUL_MAX_ROWS = 1048576
 ECHO_MATMUL_MAX_DEPTH = 131071
+ECHO_CACHE_MAX_HEADS = 1024
+ECHO_BATCH_MAX_TOKENS = 1048576
 
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
 
@@ -58,6 +60,9 @@ _NORM_PARAMS = struct.Struct("4q")        # echo_norm_params: w_post, b_post, w_
 _NORM_IO = struct.Struct("16q")           # echo_norm_io
 _NORM_GRAD_IO = struct.Struct("18q")      # echo_norm_grad_io
 _MATRIX = struct.Struct("3q")             # echo_matrix: data, ld, rank_stride
+_CACHE = struct.Struct("7q")              # echo_cache
+_BATCH = struct.Struct("7q")              # echo_batch
+_HEADS = struct.Struct("3q")              # echo_heads: data, ld, head_stride
 _FEW_TOKENS = 32                          # up to here no product needs a workspace
 
 _SIGS = {
@@ -95,6 +100,13 @@ _SIGS = {
     "echo_debug_hold_product": (_i32, [_i32]),
     "echo_linear_int8": (_i32, [_i64, _i64, _i64, _i64, _i32, _vp, _vp, _vp, _i64, _vp, _vp, _vp,
                                 _vp, _sz, _vp]),
+    "echo_cache_append": (_i32, [_vp, _vp, _i32, _vp, _vp, _vp]),
+    "echo_cache_read": (_i32, [_vp, _vp, _i32, _vp, _vp, _vp]),
+    "echo_attention": (_i32, [_vp, _vp, _i64, _i32, _vp, _vp, ctypes.c_float, _i32, _i64, _vp, _vp, _sz, _vp]),
+    "echo_attention_workspace_bytes": (_sz, [_vp, _vp, _i64]),
+    "echo_quantize_weights": (_i32, [_i64, _i64, _i64, _i32, _i64, _vp, _vp, _vp, _vp]),
+    "echo_linear_int4": (_i32, [_i64, _i64, _i64, _i64, _i32, _i64, _vp, _vp, _vp, _vp, _vp]),
+    "echo_serving_status": (_i32, [_vp, ctypes.POINTER(_i32)]),
     "echo_strerror": (ctypes.c_char_p, [_i32]),
 }
 for _name, (_res, _args) in _SIGS.items():
@@ -703,6 +715,242 @@ def echo_linear_int8(x, w, w_scales, out, codes, scales, stream=None) -> None:
                                    a, scales.data_ptr(), om, at, nbytes, _stream(stream, device))
     if status:
         raise EchoError(status, "echo_linear_int8")
+
+
+# ---------------------------------------------------------------------------
+# A serving step between two all-reduces: the cache, the attention over it, and
+# products of few tokens with 4-bit weights.
+
+class Cache:
+    """A paged cache of keys and values in 4- or 8-bit groups (include/echo.h):
+    codes uint8 [pages][2][heads][page_size][head_dim * bits / 8] and meta int32
+    [pages][2][heads][page_size], contiguous tensors on one device, made here
+    (zeros, on the current device) where they are not given.  A call reads their
+    addresses again, and checks the tensors anew where one has changed."""
+
+    __slots__ = ("pages", "page_size", "heads", "head_dim", "bits", "device", "codes", "meta", "_at", "_packed")
+
+    def __init__(self, pages: int, page_size: int, heads: int, head_dim: int, bits: int, codes=None, meta=None):
+        import torch
+        for v, what, known in ((page_size, "page_size", (16, 32, 64, 128, 256)), (head_dim, "head_dim", (64, 128, 256)),
+                               (bits, "bits", (4, 8))):
+            if v not in known:
+                raise ValueError(f"{what}: {v}, expected one of {known}")
+        if pages < 0 or not 1 <= heads <= ECHO_CACHE_MAX_HEADS:
+            raise ValueError(f"pages {pages}, heads {heads}: expected pages >= 0 and heads in 1..{ECHO_CACHE_MAX_HEADS}")
+        self.pages, self.page_size, self.heads, self.head_dim, self.bits = pages, page_size, heads, head_dim, bits
+        if (codes is None) != (meta is None):
+            raise ValueError("codes and meta belong together")
+        if codes is None:
+            codes = torch.zeros(self._shape(True), dtype=torch.uint8, device="cuda")
+            meta = torch.zeros(self._shape(False), dtype=torch.int32, device="cuda")
+        self.codes, self.meta = codes, meta
+        self._check()
+
+    def _shape(self, codes: bool) -> tuple:
+        shape = (self.pages, 2, self.heads, self.page_size)
+        return shape + (self.head_dim * self.bits // 8,) if codes else shape
+
+    def _check(self) -> None:
+        import torch
+        self._at = None                           # a call after a refusal checks again
+        if not self.codes.is_cuda:
+            raise ValueError("codes: tensor must be on a CUDA device")
+        self.device = self.codes.get_device()
+        _expect_contiguous(self.codes, "codes", torch.uint8, self._shape(True), self.device)
+        _expect_contiguous(self.meta, "meta", torch.int32, self._shape(False), self.device)
+        at = (self.codes.data_ptr(), self.meta.data_ptr())
+        if self.pages and 0 in at:
+            raise ValueError("the cache's storage was freed")
+        self._packed = _CACHE.pack(*at, self.pages, self.page_size, self.heads, self.head_dim, self.bits)
+        self._at = at
+
+    def _pack(self) -> bytes:
+        if (self.codes.data_ptr(), self.meta.data_ptr()) != self._at:
+            self._check()
+        return self._packed
+
+
+class CacheBatch:
+    """New tokens of several sequences (include/echo.h): starts int32 [sequences
+    + 1], lengths int32 [sequences], both contiguous, and table int32
+    [sequences][pages] (rows at any distance), on the cache's device.  The
+    kernels read what the tensors hold when they run; a call reads the tensors'
+    addresses again, and checks them anew where one has changed."""
+
+    __slots__ = ("starts", "lengths", "table", "sequences", "device", "_at", "_rest", "_packed")
+
+    def __init__(self, starts, lengths, table):
+        self.starts, self.lengths, self.table = starts, lengths, table
+        self._check()
+
+    def _check(self) -> None:
+        import torch
+        self._at = None
+        if not self.table.is_cuda:
+            raise ValueError("table: tensor must be on a CUDA device")
+        self.device = self.table.get_device()
+        if self.table.dim() != 2:
+            raise ValueError(f"table: shape {tuple(self.table.shape)}, expected (sequences, pages)")
+        self.sequences, pages = self.table.shape
+        _expect(self.table, "table", torch.int32, (self.sequences, pages), self.device)
+        _expect_contiguous(self.lengths, "lengths", torch.int32, (self.sequences,), self.device)
+        _expect_contiguous(self.starts, "starts", torch.int32, (self.sequences + 1,), self.device)
+        at = (self.starts.data_ptr(), self.lengths.data_ptr(), self.table.data_ptr())
+        if self.sequences and (0 in at[:2] or (pages and at[2] == 0)):
+            raise ValueError("the batch's storage was freed")
+        self._rest = (pages, self.table.stride(0) if self.sequences > 1 else pages)
+        self._packed = {}
+        self._at = at
+
+    def _pack(self, tokens: int) -> bytes:
+        if (self.starts.data_ptr(), self.lengths.data_ptr(), self.table.data_ptr()) != self._at:
+            self._check()
+        packed = self._packed.get(tokens)
+        if packed is None:
+            if len(self._packed) > 64:            # token counts of steps past
+                self._packed.clear()
+            packed = self._packed[tokens] = _BATCH.pack(self.sequences, tokens, *self._at, *self._rest)
+        return packed
+
+
+def _expect_heads(t, what: str, dtype, shape, device) -> bytes:
+    """A [tokens][heads][head_dim] tensor, tokens and heads at any distance."""
+    stride = t.stride()
+    if not (t.dtype is dtype and t.shape == shape and t.get_device() == device
+            and (stride[-1] == 1 or shape[-1] <= 1)):
+        _refuse(t, what, dtype, shape, device)
+    return _HEADS.pack(t.data_ptr(), stride[0], stride[1])
+
+
+def _serving_device(cache: Cache, batch: CacheBatch, t) -> int:
+    import torch
+    device = torch.cuda.current_device() if t.is_cuda else -1
+    if device < 0:
+        raise ValueError("tensor must be on a CUDA device")
+    for owner, what in ((cache, "cache"), (batch, "batch")):
+        if owner.device != device:
+            raise ValueError(f"the {what} belongs to cuda:{owner.device}, but the current device is cuda:{device}")
+    return device
+
+
+def _cache_rows(fn, call: str, cache: Cache, batch: CacheBatch, k, v, stream) -> None:
+    first = v if k is None else k
+    if first is None:
+        raise ValueError("k or v is needed")
+    if first.dim() != 3:
+        raise ValueError(f"k, v: shape {tuple(first.shape)}, expected (tokens, {cache.heads}, {cache.head_dim})")
+    packed = cache._pack()
+    shape, dtype = (first.shape[0], cache.heads, cache.head_dim), first.dtype
+    rows = batch._pack(shape[0])
+    code, device = _dtype_code(dtype), _serving_device(cache, batch, first)
+    at = [None if t is None else _expect_heads(t, what, dtype, shape, device) for t, what in ((k, "k"), (v, "v"))]
+    status = fn(packed, rows, code, *at, _stream(stream, device))
+    if status:
+        raise EchoError(status, call)
+
+
+def echo_cache_append(cache: Cache, batch: CacheBatch, k, v, stream=None) -> None:
+    """Quantizes k and v, [tokens][heads][head_dim] of one dtype (tokens and
+    heads at any distance), into the places of the batch's tokens."""
+    if k is None or v is None:
+        raise ValueError("k and v are both needed")
+    _cache_rows(_lib.echo_cache_append, "echo_cache_append", cache, batch, k, v, stream)
+
+
+def echo_cache_read(cache: Cache, batch: CacheBatch, k=None, v=None, stream=None) -> None:
+    """Writes what the cache holds for the batch's tokens to k and v (either may
+    be None), [tokens][heads][head_dim] of one dtype."""
+    _cache_rows(_lib.echo_cache_read, "echo_cache_read", cache, batch, k, v, stream)
+
+
+def echo_attention_workspace_bytes(cache: Cache, batch: CacheBatch, tokens: int, heads: int) -> int:
+    return int(_lib.echo_attention_workspace_bytes(cache._pack(), batch._pack(tokens), heads))
+
+
+def echo_attention(cache: Cache, batch: CacheBatch, q, out, scale: float | None = None, causal: bool = True,
+                   window: int = 0, lse=None, stream=None) -> None:
+    """The batch's tokens attend over their sequences' pages: q, out
+    [tokens][heads][head_dim] in bf16 or fp16 (tokens and heads at any distance),
+    heads a multiple of the cache's; scale 1 / sqrt(head_dim) if None; window:
+    the last tokens that a token sees (0: all up to itself); lse fp32
+    [tokens][heads], contiguous, or None."""
+    import torch
+    if q.dim() != 3:
+        raise ValueError(f"q: shape {tuple(q.shape)}, expected (tokens, heads, {cache.head_dim})")
+    packed, (tokens, heads, _) = cache._pack(), q.shape
+    rows = batch._pack(tokens)
+    shape, dtype = (tokens, heads, cache.head_dim), q.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        raise ValueError(f"q: dtype {dtype}, expected torch.bfloat16 or torch.float16")
+    if heads < 1 or heads % cache.heads:
+        raise ValueError(f"q: {heads} heads, expected a multiple of the cache's {cache.heads}")
+    device = _serving_device(cache, batch, q)
+    at_q = _expect_heads(q, "q", dtype, shape, device)
+    at_out = _expect_heads(out, "out", dtype, shape, device)
+    at_lse = None
+    if lse is not None:
+        _expect_contiguous(lse, "lse", torch.float32, (tokens, heads), device)
+        at_lse = lse.data_ptr()
+    nbytes = _lib.echo_attention_workspace_bytes(packed, rows, heads)
+    keep, at = _workspace(nbytes, q.device, stream)
+    status = _lib.echo_attention(packed, rows, heads, _dtype_code(dtype), at_q, at_out,
+                                 cache.head_dim ** -0.5 if scale is None else scale, int(causal), window, at_lse, at,
+                                 nbytes, _stream(stream, device))
+    if status:
+        raise EchoError(status, "echo_attention")
+
+
+def _weight_shapes(ranks: int | None, channels: int, depth: int, group: int) -> tuple:
+    if group not in (64, 128, 256):
+        raise ValueError(f"group: {group}, expected 64, 128 or 256")
+    of = () if ranks is None else (ranks,)
+    return of + (channels, (depth + 1) // 2), of + (channels, (depth + group - 1) // group)
+
+
+def echo_quantize_weights(w, codes, meta, group: int = 128, stream=None) -> None:
+    """w [ranks][channels][depth] (or without ranks) to 4-bit codes uint8
+    [...][channels][(depth + 1) / 2] and words int32 [...][channels][groups]."""
+    import torch
+    ranks, channels, depth = _batch(w, "w")
+    device = _call_device(w)
+    dtype = _dtype_code(w.dtype)
+    shapes = _weight_shapes(ranks if len(w.shape) == 3 else None, channels, depth, group)
+    wm = _expect_matrix(w, "w", w.dtype, w.shape, device)
+    cm = _expect_matrix(codes, "codes", torch.uint8, shapes[0], device)
+    mm = _expect_matrix(meta, "meta", torch.int32, shapes[1], device)
+    status = _lib.echo_quantize_weights(ranks, channels, depth, dtype, group, wm, cm, mm, _stream(stream, device))
+    if status:
+        raise EchoError(status, "echo_quantize_weights")
+
+
+def echo_linear_int4(x, codes, meta, out, group: int = 128, stream=None) -> None:
+    """out[p][t][c] = sum_k x[p][t][k] w[p][c][k] for weights from
+    echo_quantize_weights: x [ranks][tokens][depth] and out
+    [ranks][tokens][channels] of one dtype, or both without ranks; x, and codes
+    and meta together, may lack the ranks' dimension where all ranks share them."""
+    import torch
+    device = _call_device(out)
+    ranks, tokens, channels = _batch(out, "out")
+    depth = x.shape[-1]
+    own_x, own_w = len(x.shape) == 3, len(codes.shape) == 3
+    shapes = _weight_shapes(ranks if own_w else None, channels, depth, group)
+    xm = _expect_matrix(x, "x", out.dtype, (ranks, tokens, depth) if own_x else (tokens, depth), device)
+    cm = _expect_matrix(codes, "codes", torch.uint8, shapes[0], device)
+    mm = _expect_matrix(meta, "meta", torch.int32, shapes[1], device)
+    om = _expect_matrix(out, "out", out.dtype, out.shape, device)
+    status = _lib.echo_linear_int4(ranks, tokens, channels, depth, _dtype_code(out.dtype), group, xm, cm, mm, om,
+                                   _stream(stream, device))
+    if status:
+        raise EchoError(status, "echo_linear_int4")
+
+
+def echo_serving_status(stream=None) -> int:
+    """Reads and clears the status of the cache's, the attention's and the
+    weight quantizer's calls on the current device (synchronizes the stream)."""
+    st = _i32(0)
+    _check(_lib.echo_serving_status(_stream(stream), ctypes.byref(st)), "echo_serving_status")
+    return st.value
 
 
 def echo_strerror(status: int) -> str:

@@ -57,10 +57,13 @@ extern "C" {
 /* Status codes. */
 #define ECHO_OK              0
 #define ECHO_ERR_ARG         1  /* NULL pointer, P outside 1..ECHO_MAX_RANKS, g < 1,
-                                   aliasing other than out[p] == in[p], wrong device */
+                                   aliasing other than out[p] == in[p], wrong device;
+                                   (status word) a page outside its cache or table */
 #define ECHO_ERR_SHAPE       2  /* n < 0, or n not a multiple of P*g; a matrix of negative
                                    size or with rows closer than its columns; a gate
-                                   whose rows do not divide the call's */
+                                   whose rows do not divide the call's; query heads that
+                                   are no multiple of the cache's; (status word) rows of a
+                                   batch past its tokens, or falling starts */
 #define ECHO_ERR_UNSUPPORTED 3  /* bits not 4 or 8, or g not 64, 128 or 256; sizes beyond
                                    ECHO_NORM_MAX_WIDTH or ECHO_MATMUL_MAX_*; an element
                                    type other than ECHO_F32, ECHO_BF16, ECHO_F16 */
@@ -69,7 +72,8 @@ extern "C" {
                                    product's tensor off its element, stats or workspace
                                    off 16 bytes */
 #define ECHO_ERR_CUDA        5  /* a CUDA runtime call failed */
-#define ECHO_ERR_OVERFLOW    6  /* (status word) a non-finite input or an fp16 step overflow */
+#define ECHO_ERR_OVERFLOW    6  /* (status word) a non-finite input or an fp16 step overflow,
+                                   in a call or in a group of a cache or of weights */
 #define ECHO_ERR_TIMEOUT     7  /* (status word) a device-side wait gave up */
 #define ECHO_ERR_TOO_LARGE   8  /* echo_allreduce_noalloc: beyond its fixed scratch area;
                                    a product: its workspace is too small */
@@ -586,6 +590,151 @@ int echo_linear_int8(int64_t ranks, int64_t tokens, int64_t channels, int64_t de
                      int64_t w_scale_stride, const echo_matrix* codes, float* a_scales,
                      const echo_matrix* out, void* workspace, size_t workspace_bytes,
                      void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * What a serving step does between two all-reduces: the ranks' heads attend
+ * over a cache that is kept in the library's 4- or 8-bit groups, and few tokens
+ * are multiplied with weights in the same 4-bit groups.  Status codes, streams
+ * and ownership are as above; all calls only enqueue work on `stream`, and none
+ * allocates.  Only echo_serving_status synchronizes.
+ *
+ * A group of values v with b-bit codes holds
+ *     lo = min(0, min v), hi = max(0, max v)
+ *     s  = the least fp16 number with s * (2^b - 1) >= hi - lo (1 if all are 0)
+ *     z  = clamp(rint(-lo / s), 0, 2^b - 1)
+ *     code = clamp(rint(v / s) + z, 0, 2^b - 1),  which stands for s * (code - z)
+ * with quotients rounded as exact numbers (ties to even), which for 16-bit
+ * values is what the all-reduce's quantizer gives.  A group with a non-finite
+ * value, or whose s would be beyond fp16, gets codes 0, z 0 and a step of NaN,
+ * so that all its values read as NaN, and sets the status word to
+ * ECHO_ERR_OVERFLOW.  A meta word holds s in its low half and z (an fp16
+ * number) in its high half; 4-bit codes lie as in echo_wire_layout (element 2i
+ * in the low nibble of byte i).
+ * ---------------------------------------------------------------------------
+ */
+
+/* A paged cache of keys and values: a page holds page_size tokens of every
+ * head, a token's head_dim values of a head are one group.  Both arrays are the
+ * caller's, 16-byte aligned and contiguous:
+ *   codes  [pages][2][heads][page_size][head_dim * bits / 8], keys first
+ *   meta   [pages][2][heads][page_size]
+ * head_dim 64, 128 or 256, bits 4 or 8, page_size 16, 32, 64, 128 or 256, heads
+ * 1..ECHO_CACHE_MAX_HEADS (ECHO_ERR_UNSUPPORTED otherwise). */
+#define ECHO_CACHE_MAX_HEADS 1024
+typedef struct {
+  void* codes;
+  void* meta;
+  int64_t pages, page_size, heads, head_dim, bits;
+} echo_cache;
+
+/* New tokens of several sequences, packed: sequence i has the rows starts[i]
+ * to starts[i + 1] - 1 of the calls' token tensors, and these are its last
+ * tokens: row starts[i] + j is the token at place
+ * lengths[i] - (starts[i + 1] - starts[i]) + j of the sequence, whose place p
+ * lies in the page table[i][p / page_size].  The arrays are device memory, read
+ * by the kernels, so a captured call follows their contents.  Rows outside
+ * starts[0]..starts[sequences] are left as they are, and tokens before a
+ * sequence's begin (lengths[i] less than its rows) are not written, read as
+ * zeros and attend to nothing.  What the arrays hold is checked on the device:
+ * rows past `tokens` and falling starts are left out and set the status word to
+ * ECHO_ERR_SHAPE, and pages that are not in the cache (or in the table), whose
+ * tokens are not written, read as zeros and are hidden from attention, set it
+ * to ECHO_ERR_ARG. */
+#define ECHO_BATCH_MAX_TOKENS 1048576
+typedef struct {
+  int64_t sequences, tokens;   /* tokens: rows of the token tensors */
+  const int32_t* starts;       /* [sequences + 1], rising */
+  const int32_t* lengths;      /* [sequences] */
+  const int32_t* table;        /* [sequences][table_pages] */
+  int64_t table_pages;
+  int64_t ld_table;            /* from one sequence's row to the next, >= table_pages */
+} echo_batch;
+
+/* [tokens][heads][head_dim] values: element (t, h, i) at
+ * data + t * ld + h * head_stride + i (in elements). */
+typedef struct {
+  void* data;
+  int64_t ld;
+  int64_t head_stride;
+} echo_heads;
+
+/*
+ * echo_cache_append -- quantizes the keys and values of a batch's tokens into
+ * their places in the cache.  k and v hold the cache's heads and have the type
+ * dtype.  No two rows of a batch may have the same place.
+ */
+int echo_cache_append(const echo_cache* cache, const echo_batch* batch, int dtype,
+                      const echo_heads* k, const echo_heads* v, void* stream);
+
+/*
+ * echo_cache_read -- the inverse: writes the values that the cache holds for a
+ * batch's tokens to k and v, rounded to dtype (either may be NULL: not read).
+ * To read whole sequences give them as many rows as they have tokens.
+ */
+int echo_cache_read(const echo_cache* cache, const echo_batch* batch, int dtype,
+                    const echo_heads* k, const echo_heads* v, void* stream);
+
+/*
+ * echo_attention -- a batch's tokens attend over their sequences' pages:
+ *     out[t][h] = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale * q[t][h] . k_j)
+ * with the keys and values of head h / (heads / cache->heads) at the places j
+ * that token t sees: all up to its own place p with causal = 1 (of these the
+ * last `window` if window > 0), all of the sequence with causal = 0 (window 0).
+ * The tokens' own keys and values have to be in the cache.  A token that sees
+ * nothing gets zeros.
+ *   heads  of q and out, a multiple of the cache's
+ *   dtype  ECHO_BF16 or ECHO_F16 (ECHO_ERR_UNSUPPORTED for others)
+ *   lse    [tokens][heads] fp32, log of the sum of w (-infinity for a token that
+ *          sees nothing); NULL: not written
+ *   workspace  16-byte-aligned device memory of at least
+ *          echo_attention_workspace_bytes bytes, overlapping nothing else
+ *          (ECHO_ERR_TOO_LARGE if NULL or smaller); one call at a time
+ * Codes less their zero point are exact in the 16-bit operands of the matrix
+ * instructions, sums, maxima and steps are fp32, and w_j times v's step is
+ * rounded to 11 bits.  A repeated call gives the same bits; another batch may
+ * split a sequence differently and round differently.
+ */
+int echo_attention(const echo_cache* cache, const echo_batch* batch, int64_t heads, int dtype,
+                   const echo_heads* q, const echo_heads* out, float scale, int causal,
+                   int64_t window, float* lse, void* workspace, size_t workspace_bytes,
+                   void* stream);
+
+/* Bytes of echo_attention's workspace, 0 for sizes that it refuses. */
+size_t echo_attention_workspace_bytes(const echo_cache* cache, const echo_batch* batch,
+                                      int64_t heads);
+
+/*
+ * echo_quantize_weights -- w[ranks][channels][depth] to 4-bit codes in groups of
+ * `group` (64, 128 or 256) along the depth, the last group of a row shorter if
+ * depth is no multiple.
+ *   codes  bytes, rows of (depth + 1) / 2 (the last nibble of an odd row is 0)
+ *   meta   32-bit words, rows of (depth + group - 1) / group
+ */
+int echo_quantize_weights(int64_t ranks, int64_t channels, int64_t depth, int dtype, int64_t group,
+                          const echo_matrix* w, const echo_matrix* codes, const echo_matrix* meta,
+                          void* stream);
+
+/*
+ * echo_linear_int4 -- for each rank p, token t, channel c:
+ *     out[p][t][c] = sum over k of x[p][t][k] * s[p][c][k / group] * (code[p][c][k] - z[p][c][k / group])
+ * x and out have the type dtype; products are exact, their sums are fp32, a
+ * group's sum is multiplied by its step in fp32.  Limits as for
+ * echo_matmul_int8.  It reads the weights once for each 32 tokens and is meant
+ * for few; out must not overlap the inputs nor one rank's rows another's.
+ */
+int echo_linear_int4(int64_t ranks, int64_t tokens, int64_t channels, int64_t depth, int dtype,
+                     int64_t group, const echo_matrix* x, const echo_matrix* codes,
+                     const echo_matrix* meta, const echo_matrix* out, void* stream);
+
+/*
+ * echo_serving_status -- read and clear the current device's status word of the
+ * calls above: synchronizes `stream`, then writes ECHO_OK or, the first that
+ * holds, ECHO_ERR_TIMEOUT (a device-side wait of echo_attention gave up, after
+ * 1 s; that call's results are unspecified), ECHO_ERR_ARG, ECHO_ERR_SHAPE (see
+ * echo_batch) or ECHO_ERR_OVERFLOW (a group that is NaN was written).
+ */
+int echo_serving_status(void* stream, int* status);
 
 /* A static description of a status code; for ECHO_ERR_CUDA, of the last CUDA
  * error seen by the library in this thread. */
