@@ -27,7 +27,7 @@ GROUPS = (64, 128, 256)
 TYPES = (0, 1, 2)
 SOURCES = [(src, None) for src in ("echo_api.cu", "echo_noalloc.cu", "norm_api.cu", "int8_api.cu",
                                    "int8_quantize.cu", "int8_product.cu", "int8_few.cu", "serve_api.cu",
-                                   "cache_rows.cu", "attn_few.cu", "int4_quantize.cu", "int4_few.cu")] + [
+                                   "cache_rows.cu", "attn_few.cu", "attn_many.cu", "int4_quantize.cu", "int4_few.cu")] + [
     (src, (f"_g{g}", f"-DECHO_G={g}"))
     for src in ("k_push.cu", "k_reduce.cu", "k_gather.cu", "k_call.cu", "k_tile.cu")
     for g in GROUPS] + [

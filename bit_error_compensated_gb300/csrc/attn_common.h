@@ -134,6 +134,58 @@ __device__ __forceinline__ Range block_range(const AttentionArgs& a, int64_t* sh
   return r;
 }
 
+// Walks the units of a block's range: `unit` is the one at hand, the block has
+// `take` of its tiles from its tile `in` on.  Every thread walks for itself.
+template <int R, int TILE>
+struct Walk {
+  int64_t at, end;
+  Sequence s;
+  Unit unit;
+  int j, in, take;
+
+  __device__ __forceinline__ void start(const AttentionArgs& a, const Range& r, int* bad) {
+    at = r.begin;
+    end = r.end;
+    if (at >= end) return;
+    unit.sequence = r.sequence;
+    s = sequence_of(a.batch, a.cache.page_shift, r.sequence, bad);
+    const int64_t each = sequence_tiles<R, TILE>(a, s);
+    unit.head = (int)((at - r.before) / each);
+    int64_t left = at - r.before - unit.head * each;
+    for (j = 0;; ++j) {
+      unit_tiles<R, TILE>(a, s, j, &unit.tile, &unit.tiles);
+      if (left < unit.tiles) break;
+      left -= unit.tiles;
+    }
+    in = (int)left;
+    enter(a);
+  }
+  __device__ __forceinline__ bool more() const { return at < end; }
+  __device__ __forceinline__ bool whole() const { return in == 0 && take == unit.tiles; }
+  __device__ __forceinline__ void next(const AttentionArgs& a, int* bad) {
+    at += take;
+    if (at >= end) return;               // else the unit has been walked to its end
+    in = 0;
+    if (++j == units_of<R>(a, s)) {
+      j = 0;
+      if (++unit.head == a.cache.heads) {
+        unit.head = 0;
+        do s = sequence_of(a.batch, a.cache.page_shift, ++unit.sequence, bad);
+        while (s.rows == 0);
+      }
+    }
+    unit_tiles<R, TILE>(a, s, j, &unit.tile, &unit.tiles);
+    enter(a);
+  }
+
+ private:
+  __device__ __forceinline__ void enter(const AttentionArgs& a) {
+    unit.first = j * R;
+    unit.rows = s.rows * a.group - unit.first < R ? s.rows * a.group - unit.first : R;
+    take = unit.tiles - in < end - at ? unit.tiles - in : (int)(end - at);
+  }
+};
+
 // Workspace: two slots a block, for the parts of its first and its last unit
 // (R rows of maximum, sum and D sums of values, fp32), and what to join.
 struct Join {
@@ -149,6 +201,19 @@ inline int64_t workspace_bytes(int blocks, int rows, int dim) {
 __device__ __forceinline__ Join* joins(const AttentionArgs& a) { return reinterpret_cast<Join*>(a.partial); }
 __device__ __forceinline__ float* slot_at(const AttentionArgs& a, int blocks, int slot, int rows, int dim) {
   return reinterpret_cast<float*>(reinterpret_cast<char*>(a.partial) + join_bytes(blocks)) + slot * slot_floats(rows, dim);
+}
+
+// Block c's part of the unit at hand: in slot 2 c if the unit has the block's
+// first tile, else in slot 2 c + 1.
+template <int R, int TILE>
+__device__ __forceinline__ int slot_of(const Walk<R, TILE>& w, const Range& r) {
+  return 2 * (int)blockIdx.x + (w.at - w.in > r.begin ? 1 : 0);
+}
+// The first part's block names the others that have parts of the unit.
+template <int R, int TILE>
+__device__ __forceinline__ void name_parts(const AttentionArgs& a, const Walk<R, TILE>& w, const Range& r) {
+  const int last = block_of(r.total, w.at + w.unit.tiles - 1, r.blocks);
+  joins(a)[blockIdx.x] = {last - (int)blockIdx.x + 1, slot_of(w, r), w.s.row, w.unit.head, w.unit.first, w.unit.rows};
 }
 
 __device__ __forceinline__ float exp2_of(float v) {
@@ -197,5 +262,11 @@ __device__ __forceinline__ void store_values4(const AttentionArgs& a, int64_t at
 }
 // Whether rows of out take 8-byte stores.
 inline bool vector_rows(const HeadsArgs& h) { return on_boundary(h.data, 8) && h.ld % 4 == 0 && h.head_stride % 4 == 0; }
+
+// Joins the parts of units that several blocks of a kernel before have had.
+cudaError_t launch_join(const AttentionArgs& a, int blocks, int rows, cudaStream_t s);
+// attn_many.cu; attn_few.cu has the rest.
+cudaError_t launch_attention_many(const AttentionArgs& a, int sms, cudaStream_t s);
+int64_t attention_many_bytes(int head_dim, int sms);
 
 }  // namespace echo

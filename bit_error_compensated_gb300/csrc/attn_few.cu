@@ -162,33 +162,12 @@ __global__ void __launch_bounds__(kThreads) attention_few_kernel(const Attention
   int bad = 0;
   const Range range = block_range<kRows, kTile, kThreads, kLeast>(a, shared, &bad);
   const int heads = a.cache.heads, page_size = 1 << a.cache.page_shift;
-  int64_t before = range.before;
-  int i = range.sequence;
-  for (int64_t at = range.begin; at < range.end;) {
-    // The unit that has tile `at`, and this block's part of it.
-    const Sequence s = sequence_of(a.batch, a.cache.page_shift, i, &bad);
-    const int64_t each = sequence_tiles<kRows, kTile>(a, s);
-    if (at >= before + each * heads) {
-      before += each * heads;
-      ++i;
-      continue;
-    }
-    Unit u;
-    u.sequence = i;
-    u.head = (int)((at - before) / each);
-    int64_t in = at - before - u.head * each;              // of the head's tiles
-    int j = 0;
-    for (;; ++j) {
-      unit_tiles<kRows, kTile>(a, s, j, &u.tile, &u.tiles);
-      if (in < u.tiles) break;
-      in -= u.tiles;
-    }
-    u.first = j * kRows;
-    u.rows = s.rows * a.group - u.first < kRows ? s.rows * a.group - u.first : kRows;
-    const int64_t left = range.end - at;
-    const int tiles = u.tiles - in < left ? u.tiles - (int)in : (int)left;
-    const bool whole = in == 0 && tiles == u.tiles;
-
+  Walk<kRows, kTile> walk;
+  for (walk.start(a, range, &bad); walk.more(); walk.next(a, &bad)) {
+    const Sequence& s = walk.s;
+    const Unit& u = walk.unit;
+    const int tiles = walk.take;
+    const bool whole = walk.whole();
     __syncthreads();                                       // the last unit's sums have been read
     if (a.dtype == ECHO_BF16) load_queries<__nv_bfloat16, D, BITS>(a, s, u, query, factor);
     else load_queries<__half, D, BITS>(a, s, u, query, factor);
@@ -217,12 +196,12 @@ __global__ void __launch_bounds__(kThreads) attention_few_kernel(const Attention
 #pragma unroll
       for (int k = 0; k < 4; ++k) sums[c][k] = 0.0f;
 
-    const int key0 = (u.tile + (int)in) * kTile + kStep * warp;            // of this warp's first step
+    const int key0 = (u.tile + walk.in) * kTile + kStep * warp;            // of this warp's first step
     const int64_t values_on = (int64_t)heads << a.cache.page_shift;        // groups from a key's to its value's
     uint32_t missing = 0;                                  // stages without a page
     auto look_up = [&](int t) {
       const int key = key0 + t * kTile;
-      return t < tiles && key < end ? page_of(a.batch, a.cache, i, key) : -1;
+      return t < tiles && key < end ? page_of(a.batch, a.cache, u.sequence, key) : -1;
     };
     auto issue = [&](int t, int page, int stage) {
       const int key = key0 + t * kTile;
@@ -431,10 +410,7 @@ __global__ void __launch_bounds__(kThreads) attention_few_kernel(const Attention
         for (int e = 0; e < 2; ++e) row[(8 * (c / kPiece) + 2 * quad + e) * kPiece + c % kPiece] = sums[c][2 * h + e];
     }
     __syncthreads();
-    // Block c's part of a unit goes to slot 2 c if the unit has the block's
-    // first tile, else to slot 2 c + 1.
-    const int slot = 2 * (int)blockIdx.x + (at - in > range.begin ? 1 : 0);
-    float* const part = slot_at(a, gridDim.x, slot, kRows, D);
+    float* const part = slot_at(a, gridDim.x, slot_of(walk, range), kRows, D);
     for (int n = tid; n < u.rows * (D / 4); n += kThreads) {
       const int r = n / (D / 4), d = n % (D / 4) * 4;
       float top = most[0][r], sum = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -465,11 +441,7 @@ __global__ void __launch_bounds__(kThreads) attention_few_kernel(const Attention
         }
       }
     }
-    if (!whole && in == 0 && tid == 0) {                   // the first part's block names the others
-      const int last = block_of(range.total, at + u.tiles - 1, range.blocks);
-      joins(a)[blockIdx.x] = {last - (int)blockIdx.x + 1, slot, s.row, u.head, u.first, u.rows};
-    }
-    at += tiles;
+    if (!whole && walk.in == 0 && tid == 0) name_parts(a, walk, range);
   }
   if (bad) report(bad);
 }
@@ -509,18 +481,9 @@ __global__ void __launch_bounds__(128) attention_join_kernel(const AttentionArgs
   }
 }
 
-cudaError_t launch_join(const AttentionArgs& a, int blocks, int rows, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)blocks, (unsigned)(rows / 4));
-  cfg.blockDim = dim3(128);
-  cfg.stream = s;
-  cudaLaunchAttribute overlapped = overlapped_launch();
-  cfg.attrs = &overlapped;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attention_join_kernel, a, blocks, rows, (int)vector_rows(a.out));
-}
-
 constexpr int kBlocksPerSm = 2;
+// Up to as many rows a sequence this kernel runs, for more attn_many.cu's.
+constexpr int64_t kFewRows = 64;
 
 template <int D, int BITS>
 cudaError_t launch(const AttentionArgs& a, int sms, cudaStream_t s) {
@@ -545,13 +508,30 @@ cudaError_t launch(const AttentionArgs& a, int sms, cudaStream_t s) {
 
 }  // namespace
 
+cudaError_t launch_join(const AttentionArgs& a, int blocks, int rows, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks, (unsigned)(rows / 4));
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cudaLaunchAttribute overlapped = overlapped_launch();
+  cfg.attrs = &overlapped;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attention_join_kernel, a, blocks, rows, (int)vector_rows(a.out));
+}
+
 cudaError_t launch_attention(const AttentionArgs& a, int sms, cudaStream_t s) {
+  // Rows of an average sequence; which kernel runs changes no result beyond rounding.
+  const int64_t rows = (int64_t)a.batch.tokens * a.group / a.batch.sequences;
+  if (rows > kFewRows) return launch_attention_many(a, sms, s);
   const bool four = a.cache.bits == 4;
   if (a.cache.head_dim == 64) return four ? launch<64, 4>(a, sms, s) : launch<64, 8>(a, sms, s);
   if (a.cache.head_dim == 128) return four ? launch<128, 4>(a, sms, s) : launch<128, 8>(a, sms, s);
   return four ? launch<256, 4>(a, sms, s) : launch<256, 8>(a, sms, s);
 }
-int64_t attention_bytes(int head_dim, int sms) { return workspace_bytes(kBlocksPerSm * sms, kRows, head_dim); }
+int64_t attention_bytes(int head_dim, int sms) {
+  const int64_t few = workspace_bytes(kBlocksPerSm * sms, kRows, head_dim), many = attention_many_bytes(head_dim, sms);
+  return few > many ? few : many;
+}
 StatusWord attn_few_status() { return {read_status, clear_status_bits}; }
 
 }  // namespace echo

@@ -1,0 +1,771 @@
+// attn_many.cu -- echo_attention for many rows a sequence (include/echo.h):
+// prompts, chunks of them, on the tensor cores.
+//
+// A block takes NT tiles of 128 rows of queries (two for rows of 64 and 128,
+// one of 256) and KT keys at a time.  Scores and sums of values are matrix
+// instructions with fp32 sums in TMEM:
+//     S[128][KT] = Q K^T        Q and K in shared memory,
+//     O[128][D] += P V          P in TMEM, in the place of S, V in shared memory,
+// where K and V hold codes less their zero points, exact in f16.  Warps of the
+// block:
+//   4 a tile of rows   take S out of TMEM, turn scores into weights and put P
+//                      back: p = exp(score + log s_v - m), see attn_few.cu, so
+//                      that no value is multiplied by its step;
+//   4 for the keys, 4 for the values
+//                      turn a tile's codes, loaded one tile ahead;
+//   1 issues the matrix instructions.
+// The maximum m of a row is raised only when a score passes it by 2^8, so O in
+// TMEM is rescaled a few times a row, and the weights are made in one pass over
+// S on the assumption that it is not (made again where it was).  While one
+// tile's weights are made, the tensor cores work for the other (with one tile
+// of rows: on the next tile's scores).
+//
+// A lane has two neighbouring keys of every eight and four rows of the warp's
+// 32: a quarter of the keys' steps are read by each lane, and P's pairs go back
+// as they are.
+//
+// Every wait is bounded; one that gives up ends the call with a status
+// (echo_serving_status): the block's other warps leave at their next wait, and
+// the issuing one first waits for what it has issued.
+#include "attn_common.h"
+#include "tensor.cuh"
+
+namespace echo {
+namespace {
+
+ECHO_STATUS_WORD
+
+constexpr int kRowTile = 128;
+constexpr int kSlots = 4;                               // of steps: tiles whose weights are being made, or are next
+// Registers: the block starts with 96 a thread (five warpgroups of 480 in all).
+constexpr int kWarpsWeights = 8, kWarpsKeys = 4, kWarpsValues = 4;
+constexpr int kIssuer = kWarpsWeights + kWarpsKeys + kWarpsValues, kThreads = 32 * (kIssuer + 4);
+constexpr int kWeightRegs = 168, kTurnRegs = 56, kIssueRegs = 32;
+static_assert(2 * kWeightRegs + 2 * kTurnRegs + kIssueRegs <= 5 * 96, "a split above the launch's registers never ends");
+constexpr float kAhead = 8.0f;
+
+template <int D, int BITS>
+struct Many {
+  static constexpr int NT = D == 256 ? 1 : 2;            // tiles of rows
+  static constexpr int KT = D == 256 ? 64 : 128;         // keys of a tile
+  static constexpr int kRows = NT * kRowTile;
+  static constexpr int kRowBytes = D * BITS / 8;
+  static constexpr int kQuery = kRowTile * D * 2;        // bytes of a tile of rows
+  static constexpr int kStage = KT * D * 2;              // of a tile of keys, or values
+  static constexpr int kSteps = 3 * KT * 4;              // keys' steps, values' log steps and reciprocals
+  static constexpr int kBytes = NT * kQuery + 4 * kStage + kSlots * kSteps + 1024;
+  static constexpr int kSums = NT == 2 ? 256 : 128;      // TMEM column of O; S before it
+};
+
+// Values of V for the instruction's B operand: D contiguous, a row a key.  128-
+// byte swizzle: 64 elements of eight rows are 1024 bytes, rows' eights follow
+// each other, 64 elements on are KT rows on.
+template <int KT>
+__device__ __forceinline__ uint64_t value_desc(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)(KT * 128 / 16) << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ void mma_shared(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      :: "r"(d), "l"(a), "l"(b), "r"(desc), "r"(add) : "memory");
+}
+__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      :: "r"(d), "r"(a), "l"(b), "r"(desc), "r"(add) : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(bar) : "memory");
+}
+
+// 16 rows x 32 columns of TMEM: v[4 n + k] is row lane / 4 (+ 8 for k >= 2),
+// column 8 n + 2 (lane % 4) + k % 2.  (.aligned: hidden keys part the lanes.)
+__device__ __forceinline__ void tmem_load(uint32_t at, float (&v)[16]) {
+  uint32_t r[16];
+  __syncwarp();
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(at) : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_loaded(float (&v)[16]) {
+  // the registers are inputs and outputs, so that none is used before the wait
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+               :: "memory");
+}
+__device__ __forceinline__ void tmem_store(uint32_t at, const float (&v)[16]) {
+  __syncwarp();
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+      :: "r"(at), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
+         "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]) : "memory");
+}
+// 16 rows x 16 columns: w[2 n + k] is row lane / 4 + 8 k, column 4 n + lane % 4.
+__device__ __forceinline__ void tmem_store_pairs(uint32_t at, const uint32_t* w) {
+  __syncwarp();
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+      :: "r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
+}
+__device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {         // a in the low half
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 shared_pair(uint32_t at) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void store_shared16(uint32_t at, const uint32_t (&h)[4]) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" :: "r"(at), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
+}
+
+// The barriers, as offsets from the first one's address.
+template <int NT>
+struct Bars {
+  static constexpr int kQuery = 0;                       // NT tiles of rows are in shared memory
+  static constexpr int kKeys = kQuery + 8, kKeysFree = kKeys + 16;
+  static constexpr int kValues = kKeysFree + 16, kValuesFree = kValues + 16;
+  static constexpr int kSteps = kValuesFree + 16;        // steps of a slot
+  static constexpr int kScores = kSteps + 8 * kSlots;    // by tile of rows, or by buffer
+  static constexpr int kWeights = kScores + 16;          // by tile of rows
+  static constexpr int kSums = kWeights + 16;            // a unit's sums are complete, by tile of rows
+  static constexpr int kLast = kSums + 16;
+  static constexpr int kCount = kLast / 8 + 1;
+};
+
+// Eight codes of a word (4 bits) as (0, 4), (1, 5), (2, 6), (3, 7), or of two
+// (8 bits) in order, less the zero point.  low: 1024 + z, high: -(64 + z), twice.
+__device__ __forceinline__ uint32_t less(uint32_t v, uint32_t z) {
+  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&v), *reinterpret_cast<const __half2*>(&z));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+__device__ __forceinline__ uint32_t less_high(uint32_t v, uint32_t z) {
+  const __half2 d = __hfma2(*reinterpret_cast<const __half2*>(&v), __float2half2_rn(0.0625f), *reinterpret_cast<const __half2*>(&z));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+__device__ __forceinline__ void turn4(uint32_t w, uint32_t low, uint32_t high, uint32_t (&h)[4]) {
+  const uint32_t up = w >> 8;
+  h[0] = less((w & 0x000F000Fu) | 0x64006400u, low);
+  h[1] = less_high((w & 0x00F000F0u) | 0x64006400u, high);
+  h[2] = less((up & 0x000F000Fu) | 0x64006400u, low);
+  h[3] = less_high((up & 0x00F000F0u) | 0x64006400u, high);
+}
+__device__ __forceinline__ void turn8(uint32_t a, uint32_t b, uint32_t low, uint32_t (&h)[4]) {
+  h[0] = less(__byte_perm(a, 0x64646464u, 0x4140), low);
+  h[1] = less(__byte_perm(a, 0x64646464u, 0x4342), low);
+  h[2] = less(__byte_perm(b, 0x64646464u, 0x4140), low);
+  h[3] = less(__byte_perm(b, 0x64646464u, 0x4342), low);
+}
+// Where element e of eight lies among them.
+template <int BITS>
+__device__ __forceinline__ constexpr int spot(int e) { return BITS == 4 ? 2 * (e & 3) + (e >> 2) : e; }
+
+// The rows of tile t of a unit into shared memory, as the A operand (K-major);
+// a warp takes 32 of them.  They are scaled by one power of two, from the
+// largest of them, that takes f16's range into account; a row that is 2^-16 of
+// it or less has one of its own, and what its scores then have to be multiplied
+// by goes to `apart` (1 for the others).  A row with a non-finite element is
+// made NaN.  Returns the inverse of the warp's factor, and whether any row is
+// apart.
+constexpr int kSpread = 16;
+template <typename T, int D, int BITS>
+__device__ __forceinline__ float load_rows(const AttentionArgs& a, const Sequence& s, const Unit& u, int t, uint8_t* query,
+                                           float* apart, bool* any_apart) {
+  const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+  constexpr int kAtOnce = 4;
+  auto load = [&](int i, float (&v)[kAtOnce][D / 32]) {
+#pragma unroll
+    for (int n = 0; n < kAtOnce; ++n) {
+      const int r = t * kRowTile + warp * 32 + i + n, row = u.first + r;
+      const T* from = static_cast<const T*>(a.q.data);
+      if (r < u.rows)
+        from += (int64_t)(s.row + row / a.group) * a.q.ld + (int64_t)(u.head * a.group + row % a.group) * a.q.head_stride;
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) v[n][k] = r < u.rows ? to_float(from[lane + 32 * k]) : 0.0f;
+    }
+  };
+  uint32_t mine = 0;                                       // the largest |element| of row `lane`
+#pragma unroll 1
+  for (int i = 0; i < 32; i += kAtOnce) {
+    float v[kAtOnce][D / 32];
+    load(i, v);
+#pragma unroll
+    for (int n = 0; n < kAtOnce; ++n) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) top = max(top, abs_bits(v[n][k]));
+      top = __reduce_max_sync(kFull, top);
+      if (lane == i + n) mine = top;
+    }
+  }
+  const bool finite = mine < 0x7F800000u;
+  const uint32_t most = __reduce_max_sync(kFull, finite ? mine : 0u);
+  const float factor = row_factor(most);
+  const bool own = finite && mine != 0 && (int)(most >> 23) - (int)(mine >> 23) > kSpread;
+  const float my_factor = own ? row_factor(mine) : factor;
+  *any_apart = __any_sync(kFull, own);
+  apart[t * kRowTile + warp * 32 + lane] = factor / my_factor;            // powers of two
+#pragma unroll 1
+  for (int i = 0; i < 32; i += kAtOnce) {
+    float v[kAtOnce][D / 32];
+    load(i, v);
+#pragma unroll
+    for (int n = 0; n < kAtOnce; ++n) {
+      const int r = warp * 32 + i + n;
+      const float f = __shfl_sync(kFull, my_factor, i + n);
+      const bool bad = __shfl_sync(kFull, (int)!finite, i + n) != 0;
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) {
+        const int e = lane + 32 * k, chunk = e >> 3;
+        const int at = (chunk >> 3) * (kRowTile * 128) + r * 128 + (((chunk & 7) ^ (r & 7)) << 4) + 2 * spot<BITS>(e & 7);
+        *reinterpret_cast<__half*>(query + at) = bad ? __ushort_as_half(0x7E00) : __float2half_rn(v[n][k] * f);
+      }
+    }
+  }
+  __syncwarp();
+  return 1.0f / factor;
+}
+
+template <int D, int BITS>
+__global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const AttentionArgs a, const int wide_out) {
+  using S = Many<D, BITS>;
+  constexpr int NT = S::NT, KT = S::KT;
+  using B = Bars<NT>;
+  extern __shared__ uint8_t raw[];
+  __shared__ __align__(8) uint64_t bars[B::kCount];
+  __shared__ int64_t shared[kThreads / 32 + 2];
+  __shared__ float apart[S::kRows];
+  __shared__ int2 seen[S::kRows];                        // keys [x, y) that a row sees
+  __shared__ uint32_t tmem_at;
+  __shared__ volatile int give_up;
+  uint8_t* const base_ptr = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
+  const uint32_t query = smem_addr(base_ptr), keys = query + NT * S::kQuery, values = keys + 2 * S::kStage,
+                 steps = values + 2 * S::kStage, bar = smem_addr(bars);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    give_up = 0;
+    mbar_init(bar + B::kQuery, 4 * NT);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar + B::kKeys + 8 * i, kWarpsKeys);
+      mbar_init(bar + B::kKeysFree + 8 * i, 1);
+      mbar_init(bar + B::kValues + 8 * i, kWarpsValues);
+      mbar_init(bar + B::kValuesFree + 8 * i, 1);
+      mbar_init(bar + B::kScores + 8 * i, 1);
+      mbar_init(bar + B::kWeights + 8 * i, 4);
+      mbar_init(bar + B::kSums + 8 * i, 1);
+    }
+    for (int i = 0; i < kSlots; ++i) mbar_init(bar + B::kSteps + 8 * i, kWarpsKeys + kWarpsValues);
+    mbar_init(bar + B::kLast, 1);
+    fence_barrier_init();
+  }
+  if (warp == kIssuer) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" :: "r"(smem_addr(&tmem_at)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = tmem_at;
+  pdl_wait();
+  pdl_trigger();
+  if (tid == 0) joins(a)[blockIdx.x].blocks = 0;
+  int bad = 0;
+  const Range range = block_range<S::kRows, KT, kThreads, 1>(a, shared, &bad);
+  Walk<S::kRows, KT> walk;
+  walk.start(a, range, &bad);
+  bool ok = true;
+
+  if (warp >= kIssuer) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kIssueRegs));
+    if (warp == kIssuer) {
+      const bool one = elect_one();
+      constexpr uint32_t kInstrS = (1u << 4) | ((uint32_t)(KT / 8) << 17) | (8u << 24);                  // f16, fp32 sums
+      constexpr uint32_t kInstrO = (1u << 4) | (1u << 16) | ((uint32_t)(D / 8) << 17) | (8u << 24);      // B with D contiguous
+      auto wait = [&](uint32_t b, uint32_t parity) {
+        ok = ok && __all_sync(0xFFFFFFFFu, wait_on(b, parity, &give_up));
+        fence_after();
+        return ok;
+      };
+      auto score = [&](int t, uint32_t i, uint32_t to) {               // S of tile i and rows' tile t
+        const uint64_t da = smem_desc(query + t * S::kQuery), db = smem_desc(keys + (i & 1) * S::kStage);
+        if (one) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            mma_shared(to, da + (k / 4) * (kRowTile * 128 / 16) + 2 * (k % 4), db + (k / 4) * (KT * 128 / 16) + 2 * (k % 4),
+                       kInstrS, k > 0);
+        }
+      };
+      auto weigh = [&](int t, uint32_t i, uint32_t from, bool add) {   // O of rows' tile t
+        const uint64_t db = value_desc<KT>(values + (i & 1) * S::kStage);
+        if (one) {
+#pragma unroll
+          for (int k = 0; k < KT / 16; ++k)
+            mma_tmem(tmem + S::kSums + t * D, from + 8 * k, db + k * (16 * 128 / 16), kInstrO, add || k > 0);
+        }
+      };
+      auto tell = [&](uint32_t b) {
+        if (one) commit(b);
+      };
+      uint32_t i = 0, unit = 0;                            // tiles, units so far
+      for (; walk.more() && ok; walk.next(a, &bad), ++unit) {
+        const int n = walk.take;
+        if (!wait(bar + B::kQuery, unit & 1)) break;
+        if (!wait(bar + B::kKeys + 8 * (i & 1), (i >> 1) & 1)) break;
+        if constexpr (NT == 2) {
+          for (int t = 0; t < 2; ++t) {
+            score(t, i, tmem + t * KT);
+            tell(bar + B::kScores + 8 * t);
+          }
+          tell(bar + B::kKeysFree + 8 * (i & 1));
+          for (int k = 0; k < n && ok; ++k, ++i) {
+            const bool last = k + 1 == n;
+            for (int t = 0; t < 2 && ok; ++t) {
+              if (!wait(bar + B::kWeights + 8 * t, i & 1)) break;
+              if (t == 0 && !wait(bar + B::kValues + 8 * (i & 1), (i >> 1) & 1)) break;
+              weigh(t, i, tmem + t * KT, k > 0);
+              if (last) {
+                tell(bar + B::kSums + 8 * t);
+              } else {
+                if (t == 0 && !wait(bar + B::kKeys + 8 * ((i + 1) & 1), ((i + 1) >> 1) & 1)) break;
+                score(t, i + 1, tmem + t * KT);
+                tell(bar + B::kScores + 8 * t);
+              }
+            }
+            if (!ok) break;
+            tell(bar + B::kValuesFree + 8 * (i & 1));
+            if (!last) tell(bar + B::kKeysFree + 8 * ((i + 1) & 1));
+          }
+        } else {
+          score(0, i, tmem + (i & 1) * KT);
+          tell(bar + B::kScores + 8 * (i & 1));
+          tell(bar + B::kKeysFree + 8 * (i & 1));
+          for (int k = 0; k < n && ok; ++k, ++i) {
+            const bool last = k + 1 == n;
+            if (!last) {
+              if (!wait(bar + B::kKeys + 8 * ((i + 1) & 1), ((i + 1) >> 1) & 1)) break;
+              score(0, i + 1, tmem + ((i + 1) & 1) * KT);
+              tell(bar + B::kScores + 8 * ((i + 1) & 1));
+              tell(bar + B::kKeysFree + 8 * ((i + 1) & 1));
+            }
+            if (!wait(bar + B::kWeights, i & 1)) break;
+            if (!wait(bar + B::kValues + 8 * (i & 1), (i >> 1) & 1)) break;
+            weigh(0, i, tmem + (i & 1) * KT, k > 0);
+            tell(bar + B::kValuesFree + 8 * (i & 1));
+            if (last) tell(bar + B::kSums);
+          }
+        }
+      }
+      if (one) {                                           // instructions still running end before TMEM is freed
+        commit(bar + B::kLast);
+        mbar_wait_bounded(bar + B::kLast, 0);
+      }
+      __syncwarp();
+    }
+  } else if (warp >= kWarpsWeights) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kTurnRegs));
+    // Keys, or values: a thread has a row of a tile (of KT 64, half of one).
+    const bool value = warp >= kWarpsWeights + kWarpsKeys;
+    constexpr int kParts = 128 / KT, kPieces = S::kRowBytes / 16 / kParts, kChunks = 128 / BITS / 8;   // of 16 bytes; of eight codes, a piece
+    const int mine = tid & 127, r = mine % KT, part = mine / KT;
+    const uint32_t stages = value ? values : keys, full = bar + (value ? B::kValues : B::kKeys),
+                   empty = bar + (value ? B::kValuesFree : B::kKeysFree);
+    const int64_t on = value ? (int64_t)a.cache.heads << a.cache.page_shift : 0;
+    uint4 w[kPieces];
+    uint32_t meta = 0;
+    bool there = false;
+    // A row's page is looked up two tiles ahead, its codes are loaded one ahead.
+    Walk<S::kRows, KT> far = walk;                         // the unit of the page that is looked up next
+    int far_k = 0, page = -1, page_key = 0, page_head = 0;
+    bool page_there = false;
+    auto look_up = [&]() {
+      page_there = false;
+      if (!far.more()) return;
+      page_key = (far.unit.tile + far.in + far_k) * KT + r;
+      page_head = far.unit.head;
+      page = -1;
+      if (page_key < far.s.keys) {
+        page = page_of(a.batch, a.cache, far.unit.sequence, page_key);
+        page_there = page >= 0;
+        if (page < 0) bad |= kBadPage;
+      }
+      if (++far_k == far.take) {
+        far_k = 0;
+        far.next(a, &bad);
+      }
+    };
+    auto load = [&]() {
+      there = page_there;
+      if (there) {
+        const int64_t group = group_index(a.cache, page, page_head, page_key) + on;
+        const uint4* from = reinterpret_cast<const uint4*>(a.cache.codes + group * S::kRowBytes) + part * kPieces;
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p) w[p] = from[p];
+        meta = a.cache.meta[group];
+      }
+    };
+    look_up();
+    load();
+    look_up();
+    uint32_t i = 0;
+    for (; walk.more() && ok; walk.next(a, &bad)) {
+      for (int k = 0; k < walk.take; ++k, ++i) {
+        // A key that is not there has codes of 0, less 0, and a weight of 0.
+        if (!there) {
+          meta = 0;
+#pragma unroll
+          for (int p = 0; p < kPieces; ++p) w[p] = make_uint4(0, 0, 0, 0);
+        }
+        const float step = meta_step(meta);
+        const uint32_t slot = steps + (i & (kSlots - 1)) * S::kSteps + 4 * r;
+        ok = __all_sync(0xFFFFFFFFu, wait_on(empty + 8 * (i & 1), ((i >> 1) & 1) ^ 1u, &give_up));
+        if (!ok) break;
+        if (part == 0) {
+          if (!value) {
+            asm volatile("st.shared.f32 [%0], %1;" :: "r"(slot), "f"(step) : "memory");
+          } else {
+            // (of a NaN the log spreads it; its weight adds nothing to the sum for rows that do not see it)
+            const float log = there ? log2_of(step) : kNone, per = there && step == step ? reciprocal(step) : 0.0f;
+            asm volatile("st.shared.f32 [%0], %1;" :: "r"(slot + 4 * KT), "f"(log) : "memory");
+            asm volatile("st.shared.f32 [%0], %1;" :: "r"(slot + 8 * KT), "f"(per) : "memory");
+          }
+        }
+        __syncwarp();
+        if (lane == 0) arrive_here(bar + B::kSteps + 8 * (i & (kSlots - 1)));
+        const uint32_t zs = __byte_perm(meta, meta, 0x3232);
+        const __half2 z = *reinterpret_cast<const __half2*>(&zs);
+        const __half2 z_low = __hadd2(z, __float2half2_rn(1024.0f)), z_high = __hneg2(__hadd2(z, __float2half2_rn(64.0f)));
+        const uint32_t low = *reinterpret_cast<const uint32_t*>(&z_low), high = *reinterpret_cast<const uint32_t*>(&z_high);
+        const uint32_t to = stages + (i & 1) * S::kStage + r * 128;
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p) {
+          const uint32_t words[4] = {w[p].x, w[p].y, w[p].z, w[p].w};
+#pragma unroll
+          for (int n = 0; n < kChunks; ++n) {
+            uint32_t h[4];
+            if constexpr (BITS == 4) turn4(words[n], low, high, h);
+            else turn8(words[2 * n], words[2 * n + 1], low, h);
+            const int chunk = (part * kPieces + p) * kChunks + n;
+            store_shared16(to + (chunk >> 3) * (KT * 128) + (((chunk & 7) ^ (r & 7)) << 4), h);
+          }
+        }
+        load();
+        look_up();
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) arrive_here(full + 8 * (i & 1));
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kWeightRegs));
+    const int t = warp >> 2;                               // tile of rows
+    if (t < NT) {
+      const int g = lane >> 2, quad = lane & 3;
+      const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);          // this warp's 32 rows
+      const uint32_t sums = lanes + S::kSums + t * D;
+      uint32_t i = 0, unit = 0;
+      float scale = 0.0f, next_scale = 0.0f;               // of the warp's scores
+      bool any_apart = false, next_apart = false;
+      auto take_rows = [&]() {
+        uint8_t* const to = base_ptr + t * S::kQuery;
+        const float back = a.dtype == ECHO_BF16
+                               ? load_rows<__nv_bfloat16, D, BITS>(a, walk.s, walk.unit, t, to, apart, &next_apart)
+                               : load_rows<__half, D, BITS>(a, walk.s, walk.unit, t, to, apart, &next_apart);
+        next_scale = a.scale * kLog2E * back;
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) arrive_here(bar + B::kQuery);
+      };
+      if (walk.more()) take_rows();
+      while (walk.more() && ok) {
+        // This lane's rows: g, g + 8, g + 16, g + 24 of the warp's.
+        float m[4], l[4];
+        scale = next_scale;
+        any_apart = next_apart;
+        const int first = t * kRowTile + 32 * (warp & 3);                  // of the unit's rows, the warp's first
+        {
+          const int r = first + lane, place = walk.s.place + (walk.unit.first + r) / a.group;
+          seen[r] = r < walk.unit.rows ? make_int2(keys_from(a, place), keys_to(a, walk.s, place)) : make_int2(0, 0);
+          __syncwarp();
+        }
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          m[h] = kLowest;
+          l[h] = 0.0f;
+        }
+        int all_from = 0, all_to = 0;                      // keys that all rows of the warp see
+        if (first < walk.unit.rows) {
+          const int end = first + 32 < walk.unit.rows ? first + 31 : walk.unit.rows - 1;
+          all_from = keys_from(a, walk.s.place + (walk.unit.first + end) / a.group);
+          all_to = keys_to(a, walk.s, walk.s.place + (walk.unit.first + first) / a.group);
+        }
+        int key = (walk.unit.tile + walk.in) * KT;
+        for (int k = 0; k < walk.take; ++k, ++i, key += KT) {
+          const uint32_t buffer = NT == 2 ? (uint32_t)t : i & 1;
+          ok = __all_sync(0xFFFFFFFFu, wait_on(bar + B::kSteps + 8 * (i & (kSlots - 1)), (i / kSlots) & 1, &give_up) &&
+                                           wait_on(bar + B::kScores + 8 * buffer, NT == 2 ? i & 1 : (i >> 1) & 1, &give_up));
+          if (!ok) break;
+          fence_after();
+          const uint32_t s_at = lanes + buffer * KT, slot = steps + (i & (kSlots - 1)) * S::kSteps + 8 * quad;
+          const bool inside = key >= all_from && key + KT <= all_to;
+          uint32_t p[4][KT / 8];                           // weights of a row, pairs of keys
+          // Scores of 32 keys from c: u = s * scale * step_k + log step_v.
+          auto scores = [&](int c, float (&v)[2][16]) {
+            tmem_load(s_at + c, v[0]);
+            tmem_load(s_at + (16u << 16) + c, v[1]);
+            tmem_loaded(v[0]);
+            tmem_loaded(v[1]);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              float2 ks = shared_pair(slot + 4 * (c + 8 * n));
+              const float2 log = shared_pair(slot + 4 * (KT + c + 8 * n));
+              mul2(ks.x, ks.y, ks.x, ks.y, scale, scale);
+#pragma unroll
+              for (int h = 0; h < 4; ++h) {
+                float &v0 = v[h >> 1][4 * n + 2 * (h & 1)], &v1 = v[h >> 1][4 * n + 2 * (h & 1) + 1];
+                if (any_apart) {
+                  const float f = apart[first + g + 8 * h];
+                  mul2(v0, v1, v0, v1, f, f);
+                }
+                fma2(v0, v1, v0, v1, ks.x, ks.y, log.x, log.y);
+                if (!inside) {
+                  const int at = key + c + 8 * n + 2 * quad;
+                  const int2 see = seen[first + g + 8 * h];
+                  if (at < see.x || at >= see.y) v0 = kNone;
+                  if (at + 1 < see.x || at + 1 >= see.y) v1 = kNone;
+                }
+              }
+            }
+          };
+          bool raise = k == 0;
+          float sum[4][2];
+          for (;;) {
+            if (raise) {                                   // the rows' maxima first
+              float top[4] = {m[0], m[1], m[2], m[3]};
+#pragma unroll 1
+              for (int c = 0; c < KT; c += 32) {
+                float v[2][16];
+                scores(c, v);
+#pragma unroll
+                for (int h = 0; h < 4; ++h)
+#pragma unroll
+                  for (int n = 0; n < 4; ++n)
+                    top[h] = fmaxf(top[h], fmaxf(v[h >> 1][4 * n + 2 * (h & 1)], v[h >> 1][4 * n + 2 * (h & 1) + 1]));
+              }
+              float f[4];
+#pragma unroll
+              for (int h = 0; h < 4; ++h) {
+                top[h] = fmaxf(top[h], __shfl_xor_sync(kFull, top[h], 1));
+                top[h] = fmaxf(top[h], __shfl_xor_sync(kFull, top[h], 2));
+                f[h] = exp2_of(m[h] - top[h]);
+                m[h] = top[h];
+                l[h] *= f[h];
+              }
+              if (k > 0) {
+                if (NT == 1) {                             // (with two tiles of rows the scores came after the sums)
+                  ok = __all_sync(0xFFFFFFFFu, wait_on(bar + B::kValuesFree + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1, &give_up));
+                  if (!ok) break;
+                  fence_after();
+                }
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32)
+#pragma unroll
+                  for (int h = 0; h < 2; ++h) {
+                    float v[16];
+                    tmem_load(sums + ((uint32_t)h << 20) + c, v);
+                    tmem_loaded(v);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[e] *= f[2 * h + ((e >> 1) & 1)];
+                    tmem_store(sums + ((uint32_t)h << 20) + c, v);
+                  }
+              }
+            }
+            float top[4];
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              sum[h][0] = sum[h][1] = 0.0f;
+              top[h] = m[h];
+            }
+#pragma unroll
+            for (int c = 0; c < KT; c += 32) {
+              float v[2][16];
+              scores(c, v);
+#pragma unroll
+              for (int n = 0; n < 4; ++n) {
+                const float2 per = shared_pair(slot + 4 * (2 * KT + c + 8 * n));
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                  float v0 = v[h >> 1][4 * n + 2 * (h & 1)], v1 = v[h >> 1][4 * n + 2 * (h & 1) + 1];
+                  top[h] = max3(top[h], v0, v1);
+                  sub2(v0, v1, v0, v1, m[h], m[h]);
+                  v0 = exp2_of(v0);
+                  v1 = exp2_of(v1);
+                  fma2(sum[h][0], sum[h][1], v0, v1, per.x, per.y, sum[h][0], sum[h][1]);
+                  p[h][c / 8 + n] = pack_f16(v0, v1);
+                }
+              }
+            }
+            if (raise) break;
+            raise = __any_sync(kFull, top[0] - m[0] > kAhead || top[1] - m[1] > kAhead || top[2] - m[2] > kAhead ||
+                                          top[3] - m[3] > kAhead);
+            if (!raise) break;
+          }
+          if (!ok) break;
+#pragma unroll
+          for (int h = 0; h < 4; ++h) l[h] += sum[h][0] + sum[h][1];
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int c = 0; c < KT / 8; c += 4) {
+              uint32_t w[8];
+#pragma unroll
+              for (int n = 0; n < 4; ++n) {
+                w[2 * n] = p[2 * half][c + n];
+                w[2 * n + 1] = p[2 * half + 1][c + n];
+              }
+              tmem_store_pairs(s_at + ((uint32_t)half << 20) + 4 * c, w);
+            }
+          tmem_stored();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_here(bar + B::kWeights + 8 * t);
+        }
+        if (!ok) break;
+        // The next unit's rows (this one's have been used), then this one's sums.
+        const Walk<S::kRows, KT> done = walk;
+        walk.next(a, &bad);
+        if (walk.more()) take_rows();
+        ok = __all_sync(0xFFFFFFFFu, wait_on(bar + B::kSums + 8 * t, unit & 1, &give_up));
+        if (!ok) break;
+        ++unit;
+        fence_after();
+        const bool whole = done.whole();
+        float* const part = slot_at(a, gridDim.x, slot_of(done, range), S::kRows, D);
+        float per[4];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          l[h] += __shfl_xor_sync(kFull, l[h], 1);
+          l[h] += __shfl_xor_sync(kFull, l[h], 2);
+          per[h] = l[h] == 0.0f ? 0.0f : 1.0f / l[h];
+          const int r = first + g + 8 * h, row = done.unit.first + r;
+          if (quad == 0 && r < done.unit.rows) {
+            if (!whole) {
+              part[S::kRows * D + r] = m[h];
+              part[S::kRows * D + S::kRows + r] = l[h];
+            } else if (a.lse) {
+              const int64_t at = (int64_t)(done.s.row + row / a.group) * a.heads + done.unit.head * a.group + row % a.group;
+              a.lse[at] = l[h] == 0.0f ? kNone : (m[h] + log2_of(l[h])) * kLn2;
+            }
+          }
+        }
+        if (!whole && done.in == 0 && tid == 0) name_parts(a, done, range);
+#pragma unroll 1
+        for (int h = 0; h < 4; ++h) {
+          const int r = first + g + 8 * h, row = done.unit.first + r;
+          const bool there = r < done.unit.rows;
+          const float f = h == 0 ? per[0] : h == 1 ? per[1] : h == 2 ? per[2] : per[3];
+          const int64_t out = (done.s.row + row / a.group) * a.out.ld +
+                              (int64_t)(done.unit.head * a.group + row % a.group) * a.out.head_stride;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            float v[16];
+            tmem_load(sums + ((uint32_t)(h >> 1) << 20) + c, v);
+            tmem_loaded(v);
+            // Of the row's four eights this lane has a pair each; after the
+            // exchange it has all of the eight of its own number.
+            float e[8];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)                    // the pairs of lane `q` of the four
+#pragma unroll
+              for (int b = 0; b < 2; ++b) {
+                float mine[4];
+#pragma unroll
+                for (int n = 0; n < 4; ++n) mine[n] = h & 1 ? v[4 * n + 2 + b] : v[4 * n + b];
+                // lane `quad` wants eight `quad` of lane q
+                float got = 0.0f;
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                  const float x = __shfl_sync(kFull, mine[n], (lane & ~3) | q);
+                  if (quad == n) got = x;
+                }
+                const int place = 2 * q + b;               // in the eight, as TMEM has it
+                e[BITS == 4 ? (place & 1) * 4 + (place >> 1) : place] = got;
+              }
+            if (there) {
+              const int d = c + 8 * quad;
+              if (whole) {
+#pragma unroll
+                for (int n = 0; n < 8; ++n) e[n] *= f;
+                if (wide_out) {
+                  if (a.dtype == ECHO_BF16) store_floats<__nv_bfloat16, 8>(static_cast<__nv_bfloat16*>(a.out.data) + out + d, e);
+                  else store_floats<__half, 8>(static_cast<__half*>(a.out.data) + out + d, e);
+                } else {
+#pragma unroll
+                  for (int n = 0; n < 8; ++n) store_value(a, out + d + n, e[n]);
+                }
+              } else {
+                *reinterpret_cast<float4*>(part + r * D + d) = make_float4(e[0], e[1], e[2], e[3]);
+                *reinterpret_cast<float4*>(part + r * D + d + 4) = make_float4(e[4], e[5], e[6], e[7]);
+              }
+            }
+          }
+        }
+        fence_before();
+      }
+    }
+  }
+  if (!ok) bad |= kGaveUp;
+  if (bad) report(bad);
+  __syncthreads();
+  if (warp == kIssuer) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" :: "r"(tmem));
+  }
+}
+
+template <int D, int BITS>
+cudaError_t launch(const AttentionArgs& a, int sms, cudaStream_t s) {
+  using S = Many<D, BITS>;
+  static OncePerDevice once;
+  const cudaError_t e = once.run([] {
+    return cudaFuncSetAttribute(attention_many_kernel<D, BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
+  });
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)sms);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = S::kBytes;
+  cfg.stream = s;
+  cudaLaunchAttribute overlapped = overlapped_launch();
+  cfg.attrs = &overlapped;
+  cfg.numAttrs = 1;
+  const bool wide = on_boundary(a.out.data, 16) && a.out.ld % 8 == 0 && a.out.head_stride % 8 == 0;
+  const cudaError_t e2 = cudaLaunchKernelEx(&cfg, attention_many_kernel<D, BITS>, a, (int)wide);
+  return e2 != cudaSuccess ? e2 : launch_join(a, sms, S::kRows, s);
+}
+
+}  // namespace
+
+cudaError_t launch_attention_many(const AttentionArgs& a, int sms, cudaStream_t s) {
+  const bool four = a.cache.bits == 4;
+  if (a.cache.head_dim == 64) return four ? launch<64, 4>(a, sms, s) : launch<64, 8>(a, sms, s);
+  if (a.cache.head_dim == 128) return four ? launch<128, 4>(a, sms, s) : launch<128, 8>(a, sms, s);
+  return four ? launch<256, 4>(a, sms, s) : launch<256, 8>(a, sms, s);
+}
+int64_t attention_many_bytes(int head_dim, int sms) { return workspace_bytes(sms, head_dim == 256 ? 128 : 256, head_dim); }
+StatusWord attn_many_status() { return {read_status, clear_status_bits}; }
+
+}  // namespace echo

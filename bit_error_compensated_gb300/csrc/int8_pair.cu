@@ -44,7 +44,7 @@
 #include <cuda.h>
 
 #include "int8_load.h"
-#include "tma.cuh"
+#include "tensor.cuh"
 
 namespace echo {
 namespace {
@@ -92,36 +92,6 @@ __device__ __forceinline__ Place place_of(const Tiles& t, int tile) {
   return p;
 }
 
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
-  // K-major, 128-byte swizzle: rows of 128 bytes in groups of eight, 1024 bytes apart
-  return (uint64_t)((addr >> 4) & 0x3FFF) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
-}
-
-__device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* give_up) {
-  uint64_t began = 0;
-  for (;;) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done) : "r"(bar), "r"(parity) : "memory");
-    if (done) return true;
-    if (*give_up) return false;
-    const uint64_t t = global_ns();
-    if (began == 0) began = t;
-    else if (t - began > kWaitLimitNs) {
-      *give_up = 1;
-      return false;
-    }
-  }
-}
-
-// Arrives on a barrier of this block.
-__device__ __forceinline__ void arrive_here(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
-}
-
 // Arrives on a barrier of the pair's first block, without a release to the
 // cluster (which waits for everything the SM has in flight, over a thousand
 // cycles).  What the arrival reports needs none: rows in this block's shared
@@ -141,12 +111,6 @@ __device__ __forceinline__ void commit_pair(uint32_t bar, uint32_t first_rank) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
       " [%0], %1;" :: "r"(bar), "h"((uint16_t)(3u << first_rank)) : "memory");
-}
-
-__device__ __forceinline__ bool elect_one() {
-  uint32_t is;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(is));
-  return is != 0;
 }
 
 __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, uint32_t add) {

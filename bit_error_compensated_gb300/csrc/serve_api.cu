@@ -281,7 +281,7 @@ int echo_linear_int4(int64_t ranks, int64_t tokens, int64_t channels, int64_t de
 int echo_serving_status(void* stream, int* status) {
   if (status == nullptr) return ECHO_ERR_ARG;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const StatusWord words[] = {rows_status(), attn_few_status(), weights_status()};
+  const StatusWord words[] = {rows_status(), attn_few_status(), attn_many_status(), weights_status()};
   constexpr int kWords = sizeof(words) / sizeof(words[0]);
   int word[kWords] = {};
   for (int i = 0; i < kWords; ++i) ECHO_OPS_CUDA(words[i].read(&word[i], s));

@@ -92,6 +92,7 @@ struct StatusWord {
 };
 StatusWord rows_status();
 StatusWord attn_few_status();
+StatusWord attn_many_status();
 StatusWord weights_status();
 
 #define ECHO_STATUS_WORD                                                              \
