@@ -42,14 +42,35 @@ template <int R>
 __device__ __forceinline__ int units_of(const AttentionArgs& a, const Sequence& s) {
   return (s.rows * a.group + R - 1) / R;
 }
-// Tiles of all units of a sequence and one head.
+// Tiles of all units of a sequence and one head, for each lane's own sequence
+// (rows 0: none); of a whole warp, whose lanes share the units where there are
+// many.
 template <int R, int TILE>
-__device__ __forceinline__ int64_t sequence_tiles(const AttentionArgs& a, const Sequence& s) {
+__device__ __forceinline__ int64_t sequence_tiles(const AttentionArgs& a, const Sequence& s, int lane) {
+  const int units = units_of<R>(a, s);
   int64_t n = 0;
-  for (int j = 0; j < units_of<R>(a, s); ++j) {
-    int tile, tiles;
-    unit_tiles<R, TILE>(a, s, j, &tile, &tiles);
-    n += tiles;
+  const bool many = units > 4;
+  if (!many)
+    for (int j = 0; j < units; ++j) {
+      int tile, tiles;
+      unit_tiles<R, TILE>(a, s, j, &tile, &tiles);
+      n += tiles;
+    }
+  for (uint32_t left = __ballot_sync(kFull, many); left; left &= left - 1) {
+    const int owner = __ffs(left) - 1;
+    Sequence of = s;
+    of.rows = __shfl_sync(kFull, s.rows, owner);
+    of.keys = __shfl_sync(kFull, s.keys, owner);
+    of.place = __shfl_sync(kFull, s.place, owner);
+    int64_t sum = 0;
+    for (int j = lane; j < units_of<R>(a, of); j += 32) {
+      int tile, tiles;
+      unit_tiles<R, TILE>(a, of, j, &tile, &tiles);
+      sum += tiles;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
+    if (lane == owner) n = sum;
   }
   return n;
 }
@@ -62,6 +83,7 @@ struct Range {
   int blocks;                            // that have any
   int sequence;                          // that has `begin`
   int64_t before;                        // tiles of the sequences before it
+  int64_t each;                          // tiles of a head of that sequence
 };
 __device__ __forceinline__ int64_t range_begin(int64_t total, int block, int blocks) { return total * block / blocks; }
 // The block whose range has a tile (the last that begins at or before it).
@@ -70,15 +92,20 @@ __device__ __forceinline__ int block_of(int64_t total, int64_t tile, int blocks)
 }
 
 // Of a whole block of THREADS threads.  LEAST: tiles that a block has at least
-// where there are few.  `shared`: THREADS / 32 + 2 words of 8 bytes.
+// where there are few.  `shared`: THREADS / 32 + 3 words of 8 bytes.
 template <int R, int TILE, int THREADS, int LEAST>
 __device__ __forceinline__ Range block_range(const AttentionArgs& a, int64_t* shared, int* bad) {
   constexpr int kWarps = THREADS / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.batch.sequences;
   Range r;
-  int64_t mine = 0, sum = 0;             // of the last sequence looked at, of all that this thread has
-  for (int i = tid; i < n; i += THREADS) {
-    mine = sequence_tiles<R, TILE>(a, sequence_of(a.batch, a.cache.page_shift, i, bad)) * a.cache.heads;
+  int64_t mine = 0, sum = 0;             // tiles of the last sequence looked at, of all that this thread has
+  auto tiles_of = [&](int i, int* report) {
+    Sequence s = {0, 0, 0, 0, 0};
+    if (i < n) s = sequence_of(a.batch, a.cache.page_shift, i, report);
+    return sequence_tiles<R, TILE>(a, s, lane) * a.cache.heads;
+  };
+  for (int i0 = 0; i0 < n; i0 += THREADS) {
+    mine = tiles_of(i0 + tid, bad);
     sum += mine;
   }
 #pragma unroll
@@ -94,17 +121,14 @@ __device__ __forceinline__ Range block_range(const AttentionArgs& a, int64_t* sh
   r.end = c < r.blocks ? range_begin(r.total, c + 1, r.blocks) : r.begin;
   r.sequence = 0;
   r.before = 0;
+  r.each = 1;
   if (r.begin == r.end) return r;        // the whole block
   // The sequence that has `begin`: prefix sums of THREADS sequences at a time.
   int64_t before = 0;
   for (int i0 = 0; i0 < n; i0 += THREADS) {
     const int i = i0 + tid;
-    if (n > THREADS) {
-      int ignored = 0;
-      mine = i < n ? sequence_tiles<R, TILE>(a, sequence_of(a.batch, a.cache.page_shift, i, &ignored)) * a.cache.heads : 0;
-    } else if (i >= n) {
-      mine = 0;
-    }
+    int ignored = 0;
+    if (n > THREADS) mine = tiles_of(i, &ignored);
     int64_t prefix = mine;               // inclusive, of the warp
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -123,6 +147,7 @@ __device__ __forceinline__ Range block_range(const AttentionArgs& a, int64_t* sh
     if (before + prefix > r.begin && before + prefix - mine <= r.begin) {
       shared[kWarps] = i;
       shared[kWarps + 1] = before + prefix - mine;
+      shared[kWarps + 2] = mine / a.cache.heads;
     }
     before += block;
     if (before > r.begin) break;
@@ -130,12 +155,14 @@ __device__ __forceinline__ Range block_range(const AttentionArgs& a, int64_t* sh
   __syncthreads();
   r.sequence = (int)shared[kWarps];
   r.before = shared[kWarps + 1];
+  r.each = shared[kWarps + 2];
   __syncthreads();
   return r;
 }
 
 // Walks the units of a block's range: `unit` is the one at hand, the block has
-// `take` of its tiles from its tile `in` on.  Every thread walks for itself.
+// `take` of its tiles from its tile `in` on.  Every thread walks for itself, its
+// warp together.
 template <int R, int TILE>
 struct Walk {
   int64_t at, end;
@@ -149,14 +176,30 @@ struct Walk {
     if (at >= end) return;
     unit.sequence = r.sequence;
     s = sequence_of(a.batch, a.cache.page_shift, r.sequence, bad);
-    const int64_t each = sequence_tiles<R, TILE>(a, s);
-    unit.head = (int)((at - r.before) / each);
-    int64_t left = at - r.before - unit.head * each;
-    for (j = 0;; ++j) {
-      unit_tiles<R, TILE>(a, s, j, &unit.tile, &unit.tiles);
-      if (left < unit.tiles) break;
-      left -= unit.tiles;
+    unit.head = (int)((at - r.before) / r.each);
+    int64_t left = at - r.before - unit.head * r.each;
+    // The unit that has this tile: a warp's lanes look at 32 at a time.
+    const int lane = threadIdx.x & 31, units = units_of<R>(a, s);
+    for (j = 0;; j += 32) {
+      int tile = 0, tiles = 0;
+      if (j + lane < units) unit_tiles<R, TILE>(a, s, j + lane, &tile, &tiles);
+      int64_t prefix = tiles;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int64_t other = __shfl_up_sync(kFull, prefix, off);
+        if (lane >= off) prefix += other;
+      }
+      const uint32_t past = __ballot_sync(kFull, prefix > left);
+      if (past == 0 && j + 32 < units) {
+        left -= __shfl_sync(kFull, prefix, 31);
+        continue;
+      }
+      const int k = past ? __ffs(past) - 1 : 0;
+      left -= __shfl_sync(kFull, prefix - tiles, k);
+      j += k;
+      break;
     }
+    unit_tiles<R, TILE>(a, s, j, &unit.tile, &unit.tiles);
     in = (int)left;
     enter(a);
   }

@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kThreads) attention_few_kernel(const Attention
   using S = Shape<D, BITS>;
   constexpr int kCols = D / 8;                             // tiles of 8 columns
   extern __shared__ __align__(128) uint8_t raw[];
-  __shared__ int64_t shared[kWarps + 4];
+  __shared__ int64_t shared[kWarps + 3];
   __shared__ float factor[kRows], most[kWarps][kRows], weight[kWarps][kRows];
   uint8_t* const query = raw + (S::kBytes - S::kQuery);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, quad = lane & 3;

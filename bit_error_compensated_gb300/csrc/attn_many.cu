@@ -16,8 +16,7 @@
 //   1 issues the matrix instructions.
 // The maximum m of a row is raised only when a score passes it by 2^8, so O in
 // TMEM is rescaled a few times a row, and the weights are made in one pass over
-// S on the assumption that it is not (made again where it was).  While one
-// tile's weights are made, the tensor cores work for the other (with one tile
+// S.  While one tile's weights are made, the tensor cores work for the other (with one tile
 // of rows: on the next tile's scores).
 //
 // A lane has two neighbouring keys of every eight and four rows of the warp's
@@ -64,21 +63,28 @@ template <int KT>
 __device__ __forceinline__ uint64_t value_desc(uint32_t addr) {
   return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)(KT * 128 / 16) << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
 }
-__device__ __forceinline__ void mma_shared(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, uint32_t add) {
+// One lane issues (`one`), but its warp stays together, and what the
+// instructions take is known to be uniform: an instruction whose operands have
+// to be moved to uniform registers first takes longer to issue than to run.
+__device__ __forceinline__ void mma_shared(uint32_t one, uint32_t d, uint64_t a, uint64_t b, uint32_t desc, uint32_t add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-      :: "r"(d), "l"(a), "l"(b), "r"(desc), "r"(add) : "memory");
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      :: "r"(d), "l"(a), "l"(b), "r"(desc), "r"(add), "r"(one) : "memory");
 }
-__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, uint32_t add) {
+__device__ __forceinline__ void mma_tmem(uint32_t one, uint32_t d, uint32_t a, uint64_t b, uint32_t desc, uint32_t add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-      :: "r"(d), "r"(a), "l"(b), "r"(desc), "r"(add) : "memory");
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      :: "r"(d), "r"(a), "l"(b), "r"(desc), "r"(add), "r"(one) : "memory");
 }
-__device__ __forceinline__ void commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(bar) : "memory");
+__device__ __forceinline__ void commit(uint32_t one, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+      :: "r"(bar), "r"(one) : "memory");
 }
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __reduce_max_sync(kFull, v); }
 
 // 16 rows x 32 columns of TMEM: v[4 n + k] is row lane / 4 (+ 8 for k >= 2),
 // column 8 n + 2 (lane % 4) + k % 2.  (.aligned: hidden keys part the lanes.)
@@ -101,6 +107,11 @@ __device__ __forceinline__ void tmem_loaded(float (&v)[16]) {
                  "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
                :: "memory");
 }
+__device__ __forceinline__ void tmem_loaded(float (&v)[16], float (&u)[16]) {
+  tmem_loaded(v);
+  asm volatile("" : "+f"(u[0]), "+f"(u[1]), "+f"(u[2]), "+f"(u[3]), "+f"(u[4]), "+f"(u[5]), "+f"(u[6]), "+f"(u[7]),
+                    "+f"(u[8]), "+f"(u[9]), "+f"(u[10]), "+f"(u[11]), "+f"(u[12]), "+f"(u[13]), "+f"(u[14]), "+f"(u[15]));
+}
 __device__ __forceinline__ void tmem_store(uint32_t at, const float (&v)[16]) {
   __syncwarp();
   asm volatile(
@@ -115,6 +126,13 @@ __device__ __forceinline__ void tmem_store_pairs(uint32_t at, const uint32_t* w)
   asm volatile(
       "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
       :: "r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
+}
+__device__ __forceinline__ void tmem_load_pairs(uint32_t at, uint32_t (&w)[8]) {
+  __syncwarp();
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x128b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7]) : "r"(at) : "memory");
 }
 __device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -141,7 +159,7 @@ struct Bars {
   static constexpr int kValues = kKeysFree + 16, kValuesFree = kValues + 16;
   static constexpr int kSteps = kValuesFree + 16;        // steps of a slot
   static constexpr int kScores = kSteps + 8 * kSlots;    // by tile of rows, or by buffer
-  static constexpr int kWeights = kScores + 16;          // by tile of rows
+  static constexpr int kWeights = kScores + 16;          // the same
   static constexpr int kSums = kWeights + 16;            // a unit's sums are complete, by tile of rows
   static constexpr int kLast = kSums + 16;
   static constexpr int kCount = kLast / 8 + 1;
@@ -170,10 +188,6 @@ __device__ __forceinline__ void turn8(uint32_t a, uint32_t b, uint32_t low, uint
   h[2] = less(__byte_perm(b, 0x64646464u, 0x4140), low);
   h[3] = less(__byte_perm(b, 0x64646464u, 0x4342), low);
 }
-// Where element e of eight lies among them.
-template <int BITS>
-__device__ __forceinline__ constexpr int spot(int e) { return BITS == 4 ? 2 * (e & 3) + (e >> 2) : e; }
-
 // The rows of tile t of a unit into shared memory, as the A operand (K-major);
 // a warp takes 32 of them.  They are scaled by one power of two, from the
 // largest of them, that takes f16's range into account; a row that is 2^-16 of
@@ -183,77 +197,95 @@ __device__ __forceinline__ constexpr int spot(int e) { return BITS == 4 ? 2 * (e
 // apart.
 constexpr int kSpread = 16;
 template <typename T, int D, int BITS>
-__device__ __forceinline__ float load_rows(const AttentionArgs& a, const Sequence& s, const Unit& u, int t, uint8_t* query,
-                                           float* apart, bool* any_apart) {
+__device__ __forceinline__ float load_rows(const AttentionArgs& a, const Sequence& s, const Unit& u, int t, uint32_t query,
+                                           float* apart, bool* any_apart, bool aligned) {
   const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
-  constexpr int kAtOnce = 4;
-  auto load = [&](int i, float (&v)[kAtOnce][D / 32]) {
-#pragma unroll
-    for (int n = 0; n < kAtOnce; ++n) {
-      const int r = t * kRowTile + warp * 32 + i + n, row = u.first + r;
-      const T* from = static_cast<const T*>(a.q.data);
-      if (r < u.rows)
-        from += (int64_t)(s.row + row / a.group) * a.q.ld + (int64_t)(u.head * a.group + row % a.group) * a.q.head_stride;
-#pragma unroll
-      for (int k = 0; k < D / 32; ++k) v[n][k] = r < u.rows ? to_float(from[lane + 32 * k]) : 0.0f;
-    }
+  constexpr int kChunks = D / 8, kAtOnce = 32 / kChunks == 0 ? 1 : 32 / kChunks;      // of a row, of eight elements; rows a step
+  constexpr int kSteps = 32 * kChunks / 32;
+  // A lane's chunks, one a step, come to where they stay, element by element as
+  // they lie in memory; then they are read twice, for the largest and to be turned.
+  auto row_of = [&](int n) { return kChunks <= 32 ? n * kAtOnce + lane / kChunks : n; };
+  const int chunk = lane % kChunks;
+  auto spot_of = [&](int n) {
+    const int r = warp * 32 + row_of(n);
+    return query + (chunk >> 3) * (kRowTile * 128) + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
   };
-  uint32_t mine = 0;                                       // the largest |element| of row `lane`
-#pragma unroll 1
-  for (int i = 0; i < 32; i += kAtOnce) {
-    float v[kAtOnce][D / 32];
-    load(i, v);
+  static_assert(kChunks <= 32, "a row is one step's at most");
+#pragma unroll 4
+  for (int n = 0; n < kSteps; ++n) {
+    const int r = t * kRowTile + warp * 32 + row_of(n), row = u.first + r;
+    if (r < u.rows) {
+      const T* from = static_cast<const T*>(a.q.data) + (int64_t)(s.row + row / a.group) * a.q.ld +
+                      (int64_t)(u.head * a.group + row % a.group) * a.q.head_stride + 8 * chunk;
+      if (aligned) {
+        copy16_async(spot_of(n), from);
+      } else {
+        uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int n = 0; n < kAtOnce; ++n) {
-      uint32_t top = 0;
-#pragma unroll
-      for (int k = 0; k < D / 32; ++k) top = max(top, abs_bits(v[n][k]));
-      top = __reduce_max_sync(kFull, top);
-      if (lane == i + n) mine = top;
+        for (int e = 0; e < 8; ++e) w[e / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(from)[e] << (16 * (e % 2));
+        store_shared16(spot_of(n), w);
+      }
+    } else {
+      const uint32_t none[4] = {0, 0, 0, 0};
+      store_shared16(spot_of(n), none);
     }
   }
+  copies_commit();
+  copies_wait<0>();
+  uint32_t most = 0;                                       // the largest |element| of the warp's finite rows
+  uint32_t mine = 0;                                       // of row `lane`
+#pragma unroll 4
+  for (int n = 0; n < kSteps; ++n) {
+    float v[8];
+    to_floats<T, 8>(load_shared16<T, 8>(spot_of(n)), v);
+    uint32_t top = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = max(top, abs_bits(v[e]));
+#pragma unroll
+    for (int off = kChunks / 2; off > 0; off >>= 1) top = max(top, __shfl_xor_sync(kFull, top, off));
+    // lane k of this step's row: hand the row's largest to the lane of its number
+    const int first = n * kAtOnce;
+    const uint32_t got = __shfl_sync(kFull, top, ((lane - first) & (kAtOnce - 1)) * kChunks);
+    if (lane >= first && lane < first + kAtOnce) mine = got;
+  }
   const bool finite = mine < 0x7F800000u;
-  const uint32_t most = __reduce_max_sync(kFull, finite ? mine : 0u);
+  most = __reduce_max_sync(kFull, finite ? mine : 0u);
   const float factor = row_factor(most);
   const bool own = finite && mine != 0 && (int)(most >> 23) - (int)(mine >> 23) > kSpread;
   const float my_factor = own ? row_factor(mine) : factor;
   *any_apart = __any_sync(kFull, own);
   apart[t * kRowTile + warp * 32 + lane] = factor / my_factor;            // powers of two
-#pragma unroll 1
-  for (int i = 0; i < 32; i += kAtOnce) {
-    float v[kAtOnce][D / 32];
-    load(i, v);
+#pragma unroll 4
+  for (int n = 0; n < kSteps; ++n) {
+    const float f = __shfl_sync(kFull, my_factor, row_of(n));
+    const bool bad = __shfl_sync(kFull, (int)!finite, row_of(n)) != 0;
+    float v[8];
+    to_floats<T, 8>(load_shared16<T, 8>(spot_of(n)), v);
+    uint32_t h[4];
 #pragma unroll
-    for (int n = 0; n < kAtOnce; ++n) {
-      const int r = warp * 32 + i + n;
-      const float f = __shfl_sync(kFull, my_factor, i + n);
-      const bool bad = __shfl_sync(kFull, (int)!finite, i + n) != 0;
-#pragma unroll
-      for (int k = 0; k < D / 32; ++k) {
-        const int e = lane + 32 * k, chunk = e >> 3;
-        const int at = (chunk >> 3) * (kRowTile * 128) + r * 128 + (((chunk & 7) ^ (r & 7)) << 4) + 2 * spot<BITS>(e & 7);
-        *reinterpret_cast<__half*>(query + at) = bad ? __ushort_as_half(0x7E00) : __float2half_rn(v[n][k] * f);
-      }
+    for (int i = 0; i < 4; ++i) {                          // places 2 i and 2 i + 1
+      const int e0 = BITS == 4 ? i : 2 * i, e1 = BITS == 4 ? i + 4 : 2 * i + 1;
+      h[i] = bad ? 0x7E007E00u : pack_f16(v[e0] * f, v[e1] * f);
     }
+    store_shared16(spot_of(n), h);
   }
   __syncwarp();
   return 1.0f / factor;
 }
 
 template <int D, int BITS>
-__global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const AttentionArgs a, const int wide_out) {
+__global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const AttentionArgs a, const int wide_out, const int wide_in) {
   using S = Many<D, BITS>;
   constexpr int NT = S::NT, KT = S::KT;
   using B = Bars<NT>;
   extern __shared__ uint8_t raw[];
   __shared__ __align__(8) uint64_t bars[B::kCount];
-  __shared__ int64_t shared[kThreads / 32 + 2];
+  __shared__ int64_t shared[kThreads / 32 + 3];
   __shared__ float apart[S::kRows];
   __shared__ int2 seen[S::kRows];                        // keys [x, y) that a row sees
   __shared__ uint32_t tmem_at;
   __shared__ volatile int give_up;
-  uint8_t* const base_ptr = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
-  const uint32_t query = smem_addr(base_ptr), keys = query + NT * S::kQuery, values = keys + 2 * S::kStage,
+  const uint32_t query = (smem_addr(raw) + 1023u) & ~1023u, keys = query + NT * S::kQuery, values = keys + 2 * S::kStage,
                  steps = values + 2 * S::kStage, bar = smem_addr(bars);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -292,7 +324,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
   if (warp >= kIssuer) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kIssueRegs));
     if (warp == kIssuer) {
-      const bool one = elect_one();
+      const uint32_t one = elect_one();
+      const uint32_t tm = uniform(tmem);
       constexpr uint32_t kInstrS = (1u << 4) | ((uint32_t)(KT / 8) << 17) | (8u << 24);                  // f16, fp32 sums
       constexpr uint32_t kInstrO = (1u << 4) | (1u << 16) | ((uint32_t)(D / 8) << 17) | (8u << 24);      // B with D contiguous
       auto wait = [&](uint32_t b, uint32_t parity) {
@@ -302,46 +335,40 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
       };
       auto score = [&](int t, uint32_t i, uint32_t to) {               // S of tile i and rows' tile t
         const uint64_t da = smem_desc(query + t * S::kQuery), db = smem_desc(keys + (i & 1) * S::kStage);
-        if (one) {
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            mma_shared(to, da + (k / 4) * (kRowTile * 128 / 16) + 2 * (k % 4), db + (k / 4) * (KT * 128 / 16) + 2 * (k % 4),
-                       kInstrS, k > 0);
-        }
+        for (int k = 0; k < D / 16; ++k)
+          mma_shared(one, to, da + (k / 4) * (kRowTile * 128 / 16) + 2 * (k % 4), db + (k / 4) * (KT * 128 / 16) + 2 * (k % 4),
+                     kInstrS, k > 0);
       };
       auto weigh = [&](int t, uint32_t i, uint32_t from, bool add) {   // O of rows' tile t
         const uint64_t db = value_desc<KT>(values + (i & 1) * S::kStage);
-        if (one) {
 #pragma unroll
-          for (int k = 0; k < KT / 16; ++k)
-            mma_tmem(tmem + S::kSums + t * D, from + 8 * k, db + k * (16 * 128 / 16), kInstrO, add || k > 0);
-        }
+        for (int k = 0; k < KT / 16; ++k)
+          mma_tmem(one, tm + S::kSums + t * D, from + 8 * k, db + k * (16 * 128 / 16), kInstrO, add || k > 0);
       };
-      auto tell = [&](uint32_t b) {
-        if (one) commit(b);
-      };
+      auto tell = [&](uint32_t b) { commit(one, b); };
       uint32_t i = 0, unit = 0;                            // tiles, units so far
-      for (; walk.more() && ok; walk.next(a, &bad), ++unit) {
-        const int n = walk.take;
+      for (; __any_sync(kFull, walk.more()) && ok; walk.next(a, &bad), ++unit) {
+        const uint32_t n = uniform(walk.take);
         if (!wait(bar + B::kQuery, unit & 1)) break;
         if (!wait(bar + B::kKeys + 8 * (i & 1), (i >> 1) & 1)) break;
         if constexpr (NT == 2) {
           for (int t = 0; t < 2; ++t) {
-            score(t, i, tmem + t * KT);
+            score(t, i, tm + t * KT);
             tell(bar + B::kScores + 8 * t);
           }
           tell(bar + B::kKeysFree + 8 * (i & 1));
-          for (int k = 0; k < n && ok; ++k, ++i) {
+          for (uint32_t k = 0; k < n && ok; ++k, ++i) {
             const bool last = k + 1 == n;
             for (int t = 0; t < 2 && ok; ++t) {
               if (!wait(bar + B::kWeights + 8 * t, i & 1)) break;
               if (t == 0 && !wait(bar + B::kValues + 8 * (i & 1), (i >> 1) & 1)) break;
-              weigh(t, i, tmem + t * KT, k > 0);
+              weigh(t, i, tm + t * KT, k > 0);
               if (last) {
                 tell(bar + B::kSums + 8 * t);
               } else {
                 if (t == 0 && !wait(bar + B::kKeys + 8 * ((i + 1) & 1), ((i + 1) >> 1) & 1)) break;
-                score(t, i + 1, tmem + t * KT);
+                score(t, i + 1, tm + t * KT);
                 tell(bar + B::kScores + 8 * t);
               }
             }
@@ -350,27 +377,27 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
             if (!last) tell(bar + B::kKeysFree + 8 * ((i + 1) & 1));
           }
         } else {
-          score(0, i, tmem + (i & 1) * KT);
+          score(0, i, tm + (i & 1) * KT);
           tell(bar + B::kScores + 8 * (i & 1));
           tell(bar + B::kKeysFree + 8 * (i & 1));
-          for (int k = 0; k < n && ok; ++k, ++i) {
+          for (uint32_t k = 0; k < n && ok; ++k, ++i) {
             const bool last = k + 1 == n;
             if (!last) {
               if (!wait(bar + B::kKeys + 8 * ((i + 1) & 1), ((i + 1) >> 1) & 1)) break;
-              score(0, i + 1, tmem + ((i + 1) & 1) * KT);
+              score(0, i + 1, tm + ((i + 1) & 1) * KT);
               tell(bar + B::kScores + 8 * ((i + 1) & 1));
               tell(bar + B::kKeysFree + 8 * ((i + 1) & 1));
             }
-            if (!wait(bar + B::kWeights, i & 1)) break;
+            if (!wait(bar + B::kWeights + 8 * (i & 1), (i >> 1) & 1)) break;
             if (!wait(bar + B::kValues + 8 * (i & 1), (i >> 1) & 1)) break;
-            weigh(0, i, tmem + (i & 1) * KT, k > 0);
+            weigh(0, i, tm + (i & 1) * KT, k > 0);
             tell(bar + B::kValuesFree + 8 * (i & 1));
             if (last) tell(bar + B::kSums);
           }
         }
       }
       if (one) {                                           // instructions still running end before TMEM is freed
-        commit(bar + B::kLast);
+        commit(1, bar + B::kLast);
         mbar_wait_bounded(bar + B::kLast, 0);
       }
       __syncwarp();
@@ -388,23 +415,23 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
     uint32_t meta = 0;
     bool there = false;
     // A row's page is looked up two tiles ahead, its codes are loaded one ahead.
-    Walk<S::kRows, KT> far = walk;                         // the unit of the page that is looked up next
-    int far_k = 0, page = -1, page_key = 0, page_head = 0;
+    int ahead = 0, page = -1, page_key = 0, page_head = 0; // tiles into the unit of the page that is looked up next
+    const uint32_t n = (uint32_t)(range.end - range.begin);
     bool page_there = false;
     auto look_up = [&]() {
       page_there = false;
-      if (!far.more()) return;
-      page_key = (far.unit.tile + far.in + far_k) * KT + r;
-      page_head = far.unit.head;
+      if (!walk.more()) return;
+      page_key = (walk.unit.tile + walk.in + ahead) * KT + r;
+      page_head = walk.unit.head;
       page = -1;
-      if (page_key < far.s.keys) {
-        page = page_of(a.batch, a.cache, far.unit.sequence, page_key);
+      if (page_key < walk.s.keys) {
+        page = page_of(a.batch, a.cache, walk.unit.sequence, page_key);
         page_there = page >= 0;
         if (page < 0) bad |= kBadPage;
       }
-      if (++far_k == far.take) {
-        far_k = 0;
-        far.next(a, &bad);
+      if (++ahead == walk.take) {
+        ahead = 0;
+        walk.next(a, &bad);
       }
     };
     auto load = [&]() {
@@ -420,54 +447,51 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
     look_up();
     load();
     look_up();
-    uint32_t i = 0;
-    for (; walk.more() && ok; walk.next(a, &bad)) {
-      for (int k = 0; k < walk.take; ++k, ++i) {
-        // A key that is not there has codes of 0, less 0, and a weight of 0.
-        if (!there) {
-          meta = 0;
+    for (uint32_t i = 0; i < n; ++i) {
+      // A key that is not there has codes of 0, less 0, and a weight of 0.
+      if (!there) {
+        meta = 0;
 #pragma unroll
-          for (int p = 0; p < kPieces; ++p) w[p] = make_uint4(0, 0, 0, 0);
-        }
-        const float step = meta_step(meta);
-        const uint32_t slot = steps + (i & (kSlots - 1)) * S::kSteps + 4 * r;
-        ok = __all_sync(0xFFFFFFFFu, wait_on(empty + 8 * (i & 1), ((i >> 1) & 1) ^ 1u, &give_up));
-        if (!ok) break;
-        if (part == 0) {
-          if (!value) {
-            asm volatile("st.shared.f32 [%0], %1;" :: "r"(slot), "f"(step) : "memory");
-          } else {
-            // (of a NaN the log spreads it; its weight adds nothing to the sum for rows that do not see it)
-            const float log = there ? log2_of(step) : kNone, per = there && step == step ? reciprocal(step) : 0.0f;
-            asm volatile("st.shared.f32 [%0], %1;" :: "r"(slot + 4 * KT), "f"(log) : "memory");
-            asm volatile("st.shared.f32 [%0], %1;" :: "r"(slot + 8 * KT), "f"(per) : "memory");
-          }
-        }
-        __syncwarp();
-        if (lane == 0) arrive_here(bar + B::kSteps + 8 * (i & (kSlots - 1)));
-        const uint32_t zs = __byte_perm(meta, meta, 0x3232);
-        const __half2 z = *reinterpret_cast<const __half2*>(&zs);
-        const __half2 z_low = __hadd2(z, __float2half2_rn(1024.0f)), z_high = __hneg2(__hadd2(z, __float2half2_rn(64.0f)));
-        const uint32_t low = *reinterpret_cast<const uint32_t*>(&z_low), high = *reinterpret_cast<const uint32_t*>(&z_high);
-        const uint32_t to = stages + (i & 1) * S::kStage + r * 128;
-#pragma unroll
-        for (int p = 0; p < kPieces; ++p) {
-          const uint32_t words[4] = {w[p].x, w[p].y, w[p].z, w[p].w};
-#pragma unroll
-          for (int n = 0; n < kChunks; ++n) {
-            uint32_t h[4];
-            if constexpr (BITS == 4) turn4(words[n], low, high, h);
-            else turn8(words[2 * n], words[2 * n + 1], low, h);
-            const int chunk = (part * kPieces + p) * kChunks + n;
-            store_shared16(to + (chunk >> 3) * (KT * 128) + (((chunk & 7) ^ (r & 7)) << 4), h);
-          }
-        }
-        load();
-        look_up();
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) arrive_here(full + 8 * (i & 1));
+        for (int p = 0; p < kPieces; ++p) w[p] = make_uint4(0, 0, 0, 0);
       }
+      const float step = meta_step(meta);
+      const uint32_t slot = steps + (i & (kSlots - 1)) * S::kSteps + 4 * r;
+      ok = __all_sync(0xFFFFFFFFu, wait_on(empty + 8 * (i & 1), ((i >> 1) & 1) ^ 1u, &give_up));
+      if (!ok) break;
+      if (part == 0) {
+        if (!value) {
+          asm volatile("st.shared.f32 [%0], %1;" :: "r"(slot), "f"(step) : "memory");
+        } else {
+          // (of a NaN the log spreads it; its weight adds nothing to the sum for rows that do not see it)
+          const float log = there ? log2_of(step) : kNone, per = there && step == step ? reciprocal(step) : 0.0f;
+          asm volatile("st.shared.f32 [%0], %1;" :: "r"(slot + 4 * KT), "f"(log) : "memory");
+          asm volatile("st.shared.f32 [%0], %1;" :: "r"(slot + 8 * KT), "f"(per) : "memory");
+        }
+      }
+      __syncwarp();
+      if (lane == 0) arrive_here(bar + B::kSteps + 8 * (i & (kSlots - 1)));
+      const uint32_t zs = __byte_perm(meta, meta, 0x3232);
+      const __half2 z = *reinterpret_cast<const __half2*>(&zs);
+      const __half2 z_low = __hadd2(z, __float2half2_rn(1024.0f)), z_high = __hneg2(__hadd2(z, __float2half2_rn(64.0f)));
+      const uint32_t low = *reinterpret_cast<const uint32_t*>(&z_low), high = *reinterpret_cast<const uint32_t*>(&z_high);
+      const uint32_t to = stages + (i & 1) * S::kStage + r * 128;
+#pragma unroll
+      for (int p = 0; p < kPieces; ++p) {
+        const uint32_t words[4] = {w[p].x, w[p].y, w[p].z, w[p].w};
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          uint32_t h[4];
+          if constexpr (BITS == 4) turn4(words[c], low, high, h);
+          else turn8(words[2 * c], words[2 * c + 1], low, h);
+          const int chunk = (part * kPieces + p) * kChunks + c;
+          store_shared16(to + (chunk >> 3) * (KT * 128) + (((chunk & 7) ^ (r & 7)) << 4), h);
+        }
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) arrive_here(full + 8 * (i & 1));
+      load();                          // behind the fence, which would wait for it
+      look_up();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kWeightRegs));
@@ -480,10 +504,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
       float scale = 0.0f, next_scale = 0.0f;               // of the warp's scores
       bool any_apart = false, next_apart = false;
       auto take_rows = [&]() {
-        uint8_t* const to = base_ptr + t * S::kQuery;
+        const uint32_t to = query + t * S::kQuery;
         const float back = a.dtype == ECHO_BF16
-                               ? load_rows<__nv_bfloat16, D, BITS>(a, walk.s, walk.unit, t, to, apart, &next_apart)
-                               : load_rows<__half, D, BITS>(a, walk.s, walk.unit, t, to, apart, &next_apart);
+                               ? load_rows<__nv_bfloat16, D, BITS>(a, walk.s, walk.unit, t, to, apart, &next_apart, wide_in)
+                               : load_rows<__half, D, BITS>(a, walk.s, walk.unit, t, to, apart, &next_apart, wide_in);
         next_scale = a.scale * kLog2E * back;
         fence_proxy_async();
         __syncwarp();
@@ -492,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
       if (walk.more()) take_rows();
       while (walk.more() && ok) {
         // This lane's rows: g, g + 8, g + 16, g + 24 of the warp's.
-        float m[4], l[4];
+        float m[4], l[4][2];
         scale = next_scale;
         any_apart = next_apart;
         const int first = t * kRowTile + 32 * (warp & 3);                  // of the unit's rows, the warp's first
@@ -504,9 +528,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
           m[h] = kLowest;
-          l[h] = 0.0f;
+          l[h][0] = l[h][1] = 0.0f;
         }
-        int all_from = 0, all_to = 0;                      // keys that all rows of the warp see
+        int all_from = 0, all_to = 0x7FFFFFFF;             // keys that all rows of the warp see
         if (first < walk.unit.rows) {
           const int end = first + 32 < walk.unit.rows ? first + 31 : walk.unit.rows - 1;
           all_from = keys_from(a, walk.s.place + (walk.unit.first + end) / a.group);
@@ -521,127 +545,124 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
           fence_after();
           const uint32_t s_at = lanes + buffer * KT, slot = steps + (i & (kSlots - 1)) * S::kSteps + 8 * quad;
           const bool inside = key >= all_from && key + KT <= all_to;
-          uint32_t p[4][KT / 8];                           // weights of a row, pairs of keys
-          // Scores of 32 keys from c: u = s * scale * step_k + log step_v.
-          auto scores = [&](int c, float (&v)[2][16]) {
-            tmem_load(s_at + c, v[0]);
-            tmem_load(s_at + (16u << 16) + c, v[1]);
-            tmem_loaded(v[0]);
-            tmem_loaded(v[1]);
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-              float2 ks = shared_pair(slot + 4 * (c + 8 * n));
-              const float2 log = shared_pair(slot + 4 * (KT + c + 8 * n));
-              mul2(ks.x, ks.y, ks.x, ks.y, scale, scale);
-#pragma unroll
-              for (int h = 0; h < 4; ++h) {
-                float &v0 = v[h >> 1][4 * n + 2 * (h & 1)], &v1 = v[h >> 1][4 * n + 2 * (h & 1) + 1];
-                if (any_apart) {
-                  const float f = apart[first + g + 8 * h];
-                  mul2(v0, v1, v0, v1, f, f);
-                }
-                fma2(v0, v1, v0, v1, ks.x, ks.y, log.x, log.y);
-                if (!inside) {
-                  const int at = key + c + 8 * n + 2 * quad;
-                  const int2 see = seen[first + g + 8 * h];
-                  if (at < see.x || at >= see.y) v0 = kNone;
-                  if (at + 1 < see.x || at + 1 >= see.y) v1 = kNone;
-                }
-              }
-            }
-          };
-          bool raise = k == 0;
-          float sum[4][2];
-          for (;;) {
-            if (raise) {                                   // the rows' maxima first
-              float top[4] = {m[0], m[1], m[2], m[3]};
-#pragma unroll 1
-              for (int c = 0; c < KT; c += 32) {
-                float v[2][16];
-                scores(c, v);
-#pragma unroll
-                for (int h = 0; h < 4; ++h)
-#pragma unroll
-                  for (int n = 0; n < 4; ++n)
-                    top[h] = fmaxf(top[h], fmaxf(v[h >> 1][4 * n + 2 * (h & 1)], v[h >> 1][4 * n + 2 * (h & 1) + 1]));
-              }
-              float f[4];
-#pragma unroll
-              for (int h = 0; h < 4; ++h) {
-                top[h] = fmaxf(top[h], __shfl_xor_sync(kFull, top[h], 1));
-                top[h] = fmaxf(top[h], __shfl_xor_sync(kFull, top[h], 2));
-                f[h] = exp2_of(m[h] - top[h]);
-                m[h] = top[h];
-                l[h] *= f[h];
-              }
-              if (k > 0) {
-                if (NT == 1) {                             // (with two tiles of rows the scores came after the sums)
-                  ok = __all_sync(0xFFFFFFFFu, wait_on(bar + B::kValuesFree + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1, &give_up));
-                  if (!ok) break;
-                  fence_after();
-                }
-#pragma unroll 1
-                for (int c = 0; c < D; c += 32)
-#pragma unroll
-                  for (int h = 0; h < 2; ++h) {
-                    float v[16];
-                    tmem_load(sums + ((uint32_t)h << 20) + c, v);
-                    tmem_loaded(v);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) v[e] *= f[2 * h + ((e >> 1) & 1)];
-                    tmem_store(sums + ((uint32_t)h << 20) + c, v);
-                  }
-              }
-            }
-            float top[4];
+          // Raises the rows' maxima to `top` and scales what was made with the
+          // old ones: the sums, and this tile's weights of the keys before c.
+          auto raise = [&](float (&top)[4], int c) {
+            float f[4];
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
-              sum[h][0] = sum[h][1] = 0.0f;
-              top[h] = m[h];
+              top[h] = fmaxf(top[h], __shfl_xor_sync(kFull, top[h], 1));
+              top[h] = fmaxf(top[h], __shfl_xor_sync(kFull, top[h], 2));
+              f[h] = exp2_of(m[h] - top[h]);
+              m[h] = top[h];
+              l[h][0] *= f[h];
+              l[h][1] *= f[h];
             }
+            if (k > 0) {
+              if (NT == 1) {                               // (with two tiles of rows the scores came after the sums)
+                ok = ok && __all_sync(0xFFFFFFFFu, wait_on(bar + B::kValuesFree + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1, &give_up));
+                fence_after();
+              }
+#pragma unroll 1
+              for (int d = 0; d < D; d += 32)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  float v[16];
+                  tmem_load(sums + ((uint32_t)h << 20) + d, v);
+                  tmem_loaded(v);
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) v[e] *= f[2 * h + ((e >> 1) & 1)];
+                  tmem_store(sums + ((uint32_t)h << 20) + d, v);
+                }
+            }
+            if (c > 0) tmem_stored();
+#pragma unroll 1
+            for (int d = 0; d < c / 2; d += 16)            // (pairs, read and written as 8 words of two rows)
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                uint32_t w[8];
+                tmem_load_pairs(s_at + ((uint32_t)half << 20) + d, w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const float2 two = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
+                  w[e] = pack_f16(two.x * f[2 * half + (e & 1)], two.y * f[2 * half + (e & 1)]);
+                }
+                tmem_store_pairs(s_at + ((uint32_t)half << 20) + d, w);
+              }
+          };
+          // Weights of the tile's keys, 32 at a time: u = s * scale * step_k + log
+          // step_v, p = exp(u - m).  PLAIN: every row sees all, none is apart (a
+          // branch a pair would leave the compiler nothing to interleave).
+          auto weights = [&](auto plain) {
+            constexpr bool kPlain = decltype(plain)::value;
+            float v[2][2][16];                             // of this and of the next keys, by 16 rows
+            float f[4];
+            int2 see[4];
+            if (!kPlain) {
+#pragma unroll
+              for (int h = 0; h < 4; ++h) {
+                f[h] = apart[first + g + 8 * h];
+                see[h] = seen[first + g + 8 * h];
+              }
+            }
+            tmem_load(s_at, v[0][0]);
+            tmem_load(s_at + (16u << 16), v[0][1]);
 #pragma unroll
             for (int c = 0; c < KT; c += 32) {
-              float v[2][16];
-              scores(c, v);
+              float(&now)[2][16] = v[(c / 32) & 1];
+              tmem_loaded(now[0], now[1]);
+              if (c + 32 < KT) {
+                tmem_load(s_at + c + 32, v[(c / 32 + 1) & 1][0]);
+                tmem_load(s_at + (16u << 16) + c + 32, v[(c / 32 + 1) & 1][1]);
+              }
+              float top[4] = {m[0], m[1], m[2], m[3]};
+#pragma unroll
+              for (int n = 0; n < 4; ++n) {
+                float2 ks = shared_pair(slot + 4 * (c + 8 * n));
+                const float2 log = shared_pair(slot + 4 * (KT + c + 8 * n));
+                mul2(ks.x, ks.y, ks.x, ks.y, scale, scale);
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                  float &v0 = now[h >> 1][4 * n + 2 * (h & 1)], &v1 = now[h >> 1][4 * n + 2 * (h & 1) + 1];
+                  if (!kPlain) mul2(v0, v1, v0, v1, f[h], f[h]);
+                  fma2(v0, v1, v0, v1, ks.x, ks.y, log.x, log.y);
+                  if (!kPlain) {
+                    const int at = key + c + 8 * n + 2 * quad;
+                    v0 = at < see[h].x || at >= see[h].y ? kNone : v0;
+                    v1 = at + 1 < see[h].x || at + 1 >= see[h].y ? kNone : v1;
+                  }
+                  top[h] = max3(top[h], v0, v1);
+                }
+              }
+              if (__any_sync(kFull, top[0] - m[0] > kAhead || top[1] - m[1] > kAhead || top[2] - m[2] > kAhead ||
+                                        top[3] - m[3] > kAhead))
+                raise(top, c);
+              uint32_t w[2][8];
 #pragma unroll
               for (int n = 0; n < 4; ++n) {
                 const float2 per = shared_pair(slot + 4 * (2 * KT + c + 8 * n));
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
-                  float v0 = v[h >> 1][4 * n + 2 * (h & 1)], v1 = v[h >> 1][4 * n + 2 * (h & 1) + 1];
-                  top[h] = max3(top[h], v0, v1);
+                  float v0 = now[h >> 1][4 * n + 2 * (h & 1)], v1 = now[h >> 1][4 * n + 2 * (h & 1) + 1];
                   sub2(v0, v1, v0, v1, m[h], m[h]);
                   v0 = exp2_of(v0);
                   v1 = exp2_of(v1);
-                  fma2(sum[h][0], sum[h][1], v0, v1, per.x, per.y, sum[h][0], sum[h][1]);
-                  p[h][c / 8 + n] = pack_f16(v0, v1);
+                  fma2(l[h][0], l[h][1], v0, v1, per.x, per.y, l[h][0], l[h][1]);
+                  w[h >> 1][2 * n + (h & 1)] = pack_f16(v0, v1);
                 }
               }
+              // (in the place of scores that have been read: those of half as many keys)
+              tmem_store_pairs(s_at + c / 2, w[0]);
+              tmem_store_pairs(s_at + (16u << 16) + c / 2, w[1]);
             }
-            if (raise) break;
-            raise = __any_sync(kFull, top[0] - m[0] > kAhead || top[1] - m[1] > kAhead || top[2] - m[2] > kAhead ||
-                                          top[3] - m[3] > kAhead);
-            if (!raise) break;
-          }
+          };
+          if (inside && !any_apart) weights(std::true_type());
+          else weights(std::false_type());
           if (!ok) break;
-#pragma unroll
-          for (int h = 0; h < 4; ++h) l[h] += sum[h][0] + sum[h][1];
-#pragma unroll
-          for (int half = 0; half < 2; ++half)
-#pragma unroll
-            for (int c = 0; c < KT / 8; c += 4) {
-              uint32_t w[8];
-#pragma unroll
-              for (int n = 0; n < 4; ++n) {
-                w[2 * n] = p[2 * half][c + n];
-                w[2 * n + 1] = p[2 * half + 1][c + n];
-              }
-              tmem_store_pairs(s_at + ((uint32_t)half << 20) + 4 * c, w);
-            }
           tmem_stored();
           fence_before();
           __syncwarp();
-          if (lane == 0) arrive_here(bar + B::kWeights + 8 * t);
+          if (lane == 0) arrive_here(bar + B::kWeights + 8 * buffer);
         }
         if (!ok) break;
         // The next unit's rows (this one's have been used), then this one's sums.
@@ -657,17 +678,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
         float per[4];
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
-          l[h] += __shfl_xor_sync(kFull, l[h], 1);
-          l[h] += __shfl_xor_sync(kFull, l[h], 2);
-          per[h] = l[h] == 0.0f ? 0.0f : 1.0f / l[h];
+          float sum = l[h][0] + l[h][1];
+          sum += __shfl_xor_sync(kFull, sum, 1);
+          sum += __shfl_xor_sync(kFull, sum, 2);
+          per[h] = sum == 0.0f ? 0.0f : 1.0f / sum;
           const int r = first + g + 8 * h, row = done.unit.first + r;
           if (quad == 0 && r < done.unit.rows) {
             if (!whole) {
               part[S::kRows * D + r] = m[h];
-              part[S::kRows * D + S::kRows + r] = l[h];
+              part[S::kRows * D + S::kRows + r] = sum;
             } else if (a.lse) {
               const int64_t at = (int64_t)(done.s.row + row / a.group) * a.heads + done.unit.head * a.group + row % a.group;
-              a.lse[at] = l[h] == 0.0f ? kNone : (m[h] + log2_of(l[h])) * kLn2;
+              a.lse[at] = sum == 0.0f ? kNone : (m[h] + log2_of(sum)) * kLn2;
             }
           }
         }
@@ -685,25 +707,29 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
             tmem_load(sums + ((uint32_t)(h >> 1) << 20) + c, v);
             tmem_loaded(v);
             // Of the row's four eights this lane has a pair each; after the
-            // exchange it has all of the eight of its own number.
+            // exchange it has all pairs of the eight of its own number.
             float e[8];
 #pragma unroll
-            for (int q = 0; q < 4; ++q)                    // the pairs of lane `q` of the four
+            for (int b = 0; b < 2; ++b) {
+              float x[4];
 #pragma unroll
-              for (int b = 0; b < 2; ++b) {
-                float mine[4];
+              for (int n = 0; n < 4; ++n) x[n] = h & 1 ? v[4 * n + 2 + b] : v[4 * n + b];
 #pragma unroll
-                for (int n = 0; n < 4; ++n) mine[n] = h & 1 ? v[4 * n + 2 + b] : v[4 * n + b];
-                // lane `quad` wants eight `quad` of lane q
-                float got = 0.0f;
+              for (int step = 1; step < 4; step *= 2)
 #pragma unroll
                 for (int n = 0; n < 4; ++n) {
-                  const float x = __shfl_sync(kFull, mine[n], (lane & ~3) | q);
-                  if (quad == n) got = x;
+                  if (n & step) continue;
+                  const bool high = quad & step;
+                  const float got = __shfl_xor_sync(kFull, high ? x[n] : x[n + step], step);
+                  if (high) x[n] = got;
+                  else x[n + step] = got;
                 }
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
                 const int place = 2 * q + b;               // in the eight, as TMEM has it
-                e[BITS == 4 ? (place & 1) * 4 + (place >> 1) : place] = got;
+                e[BITS == 4 ? (place & 1) * 4 + (place >> 1) : place] = x[q];
               }
+            }
             if (there) {
               const int d = c + 8 * quad;
               if (whole) {
@@ -752,8 +778,8 @@ cudaError_t launch(const AttentionArgs& a, int sms, cudaStream_t s) {
   cudaLaunchAttribute overlapped = overlapped_launch();
   cfg.attrs = &overlapped;
   cfg.numAttrs = 1;
-  const bool wide = on_boundary(a.out.data, 16) && a.out.ld % 8 == 0 && a.out.head_stride % 8 == 0;
-  const cudaError_t e2 = cudaLaunchKernelEx(&cfg, attention_many_kernel<D, BITS>, a, (int)wide);
+  auto wide = [](const HeadsArgs& h) { return (int)(on_boundary(h.data, 16) && h.ld % 8 == 0 && h.head_stride % 8 == 0); };
+  const cudaError_t e2 = cudaLaunchKernelEx(&cfg, attention_many_kernel<D, BITS>, a, wide(a.out), wide(a.q));
   return e2 != cudaSuccess ? e2 : launch_join(a, sms, S::kRows, s);
 }
 
