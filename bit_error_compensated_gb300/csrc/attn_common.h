@@ -38,6 +38,11 @@ __device__ __forceinline__ void unit_tiles(const AttentionArgs& a, const Sequenc
   *tile = from;
   *tiles = to > from ? to - from : 1;
 }
+// The unit that is walked j-th of `units`: first, last, second, last but one and
+// so on.  In a prompt the first units see few keys and the last many, and each
+// costs its rows' loads and stores besides its tiles: so all blocks have about
+// as many.
+__device__ __forceinline__ int unit_at(int j, int units) { return j & 1 ? units - 1 - (j >> 1) : j >> 1; }
 template <int R>
 __device__ __forceinline__ int units_of(const AttentionArgs& a, const Sequence& s) {
   return (s.rows * a.group + R - 1) / R;
@@ -168,7 +173,7 @@ struct Walk {
   int64_t at, end;
   Sequence s;
   Unit unit;
-  int j, in, take;
+  int j, in, take;                       // units of the head before, tiles of the unit before, tiles of it that are the block's
 
   __device__ __forceinline__ void start(const AttentionArgs& a, const Range& r, int* bad) {
     at = r.begin;
@@ -182,7 +187,7 @@ struct Walk {
     const int lane = threadIdx.x & 31, units = units_of<R>(a, s);
     for (j = 0;; j += 32) {
       int tile = 0, tiles = 0;
-      if (j + lane < units) unit_tiles<R, TILE>(a, s, j + lane, &tile, &tiles);
+      if (j + lane < units) unit_tiles<R, TILE>(a, s, unit_at(j + lane, units), &tile, &tiles);
       int64_t prefix = tiles;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -199,7 +204,6 @@ struct Walk {
       j += k;
       break;
     }
-    unit_tiles<R, TILE>(a, s, j, &unit.tile, &unit.tiles);
     in = (int)left;
     enter(a);
   }
@@ -217,13 +221,14 @@ struct Walk {
         while (s.rows == 0);
       }
     }
-    unit_tiles<R, TILE>(a, s, j, &unit.tile, &unit.tiles);
     enter(a);
   }
 
  private:
   __device__ __forceinline__ void enter(const AttentionArgs& a) {
-    unit.first = j * R;
+    const int u = unit_at(j, units_of<R>(a, s));
+    unit_tiles<R, TILE>(a, s, u, &unit.tile, &unit.tiles);
+    unit.first = u * R;
     unit.rows = s.rows * a.group - unit.first < R ? s.rows * a.group - unit.first : R;
     take = unit.tiles - in < end - at ? unit.tiles - in : (int)(end - at);
   }

@@ -211,12 +211,18 @@ __device__ __forceinline__ float load_rows(const AttentionArgs& a, const Sequenc
     return query + (chunk >> 3) * (kRowTile * 128) + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
   };
   static_assert(kChunks <= 32, "a row is one step's at most");
-#pragma unroll 4
+  const T* my_row = nullptr;                               // row `lane`
+  {
+    const int r = t * kRowTile + warp * 32 + lane, row = u.first + r;
+    if (r < u.rows)
+      my_row = static_cast<const T*>(a.q.data) + (int64_t)(s.row + row / a.group) * a.q.ld +
+               (int64_t)(u.head * a.group + row % a.group) * a.q.head_stride;
+  }
+#pragma unroll 2
   for (int n = 0; n < kSteps; ++n) {
-    const int r = t * kRowTile + warp * 32 + row_of(n), row = u.first + r;
-    if (r < u.rows) {
-      const T* from = static_cast<const T*>(a.q.data) + (int64_t)(s.row + row / a.group) * a.q.ld +
-                      (int64_t)(u.head * a.group + row % a.group) * a.q.head_stride + 8 * chunk;
+    const T* from = reinterpret_cast<const T*>(__shfl_sync(kFull, reinterpret_cast<unsigned long long>(my_row), row_of(n)));
+    if (from != nullptr) {
+      from += 8 * chunk;
       if (aligned) {
         copy16_async(spot_of(n), from);
       } else {
@@ -234,7 +240,7 @@ __device__ __forceinline__ float load_rows(const AttentionArgs& a, const Sequenc
   copies_wait<0>();
   uint32_t most = 0;                                       // the largest |element| of the warp's finite rows
   uint32_t mine = 0;                                       // of row `lane`
-#pragma unroll 4
+#pragma unroll 2
   for (int n = 0; n < kSteps; ++n) {
     float v[8];
     to_floats<T, 8>(load_shared16<T, 8>(spot_of(n)), v);
@@ -255,7 +261,7 @@ __device__ __forceinline__ float load_rows(const AttentionArgs& a, const Sequenc
   const float my_factor = own ? row_factor(mine) : factor;
   *any_apart = __any_sync(kFull, own);
   apart[t * kRowTile + warp * 32 + lane] = factor / my_factor;            // powers of two
-#pragma unroll 4
+#pragma unroll 2
   for (int n = 0; n < kSteps; ++n) {
     const float f = __shfl_sync(kFull, my_factor, row_of(n));
     const bool bad = __shfl_sync(kFull, (int)!finite, row_of(n)) != 0;
@@ -406,27 +412,30 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kTurnRegs));
     // Keys, or values: a thread has a row of a tile (of KT 64, half of one).
     const bool value = warp >= kWarpsWeights + kWarpsKeys;
-    constexpr int kParts = 128 / KT, kPieces = S::kRowBytes / 16 / kParts, kChunks = 128 / BITS / 8;   // of 16 bytes; of eight codes, a piece
-    const int mine = tid & 127, r = mine % KT, part = mine / KT;
+    // For loads a row's pieces of 16 bytes are neighbouring lanes', 32 * kWide of
+    // which a warp takes at once; page and meta word of a row come from its lane.
+    constexpr int kWarpRows = KT / 4, kPieces = S::kRowBytes / 16;         // rows of a warp; pieces of a row
+    constexpr int kWide = 32 / kPieces;                                    // rows at once
+    constexpr int kLoads = kWarpRows / kWide, kChunks = 16 / BITS;         // loads; eights of codes of a piece
+    const int row0 = (warp & 3) * kWarpRows, r = row0 + lane;              // this lane's row, if it has one
+    const bool row_lane = lane < kWarpRows;
+    const int piece = lane % kPieces, in_row = lane / kPieces;
     const uint32_t stages = value ? values : keys, full = bar + (value ? B::kValues : B::kKeys),
                    empty = bar + (value ? B::kValuesFree : B::kKeysFree);
     const int64_t on = value ? (int64_t)a.cache.heads << a.cache.page_shift : 0;
-    uint4 w[kPieces];
-    uint32_t meta = 0;
+    uint4 w[kLoads];
+    uint32_t meta = 0;                                     // of this lane's row
     bool there = false;
     // A row's page is looked up two tiles ahead, its codes are loaded one ahead.
     int ahead = 0, page = -1, page_key = 0, page_head = 0; // tiles into the unit of the page that is looked up next
     const uint32_t n = (uint32_t)(range.end - range.begin);
-    bool page_there = false;
     auto look_up = [&]() {
-      page_there = false;
-      if (!walk.more()) return;
+      page = -1;
+      if (!__any_sync(kFull, walk.more())) return;
       page_key = (walk.unit.tile + walk.in + ahead) * KT + r;
       page_head = walk.unit.head;
-      page = -1;
-      if (page_key < walk.s.keys) {
+      if (row_lane && page_key < walk.s.keys) {
         page = page_of(a.batch, a.cache, walk.unit.sequence, page_key);
-        page_there = page >= 0;
         if (page < 0) bad |= kBadPage;
       }
       if (++ahead == walk.take) {
@@ -434,38 +443,37 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
         walk.next(a, &bad);
       }
     };
+    // Rows that are not there have codes of 0, less 0.
     auto load = [&]() {
-      there = page_there;
-      if (there) {
-        const int64_t group = group_index(a.cache, page, page_head, page_key) + on;
-        const uint4* from = reinterpret_cast<const uint4*>(a.cache.codes + group * S::kRowBytes) + part * kPieces;
+      there = page >= 0;
+      const int64_t group = there ? group_index(a.cache, page, page_head, page_key) + on : -1;
+      meta = 0;
+      if (there) meta = a.cache.meta[group];
 #pragma unroll
-        for (int p = 0; p < kPieces; ++p) w[p] = from[p];
-        meta = a.cache.meta[group];
+      for (int p = 0; p < kLoads; ++p) {
+        const int64_t of = __shfl_sync(kFull, group, p * kWide + in_row);
+        w[p] = make_uint4(0, 0, 0, 0);
+        if (of >= 0) w[p] = reinterpret_cast<const uint4*>(a.cache.codes + of * S::kRowBytes)[piece];
       }
     };
     look_up();
     load();
     look_up();
     for (uint32_t i = 0; i < n; ++i) {
-      // A key that is not there has codes of 0, less 0, and a weight of 0.
-      if (!there) {
-        meta = 0;
-#pragma unroll
-        for (int p = 0; p < kPieces; ++p) w[p] = make_uint4(0, 0, 0, 0);
-      }
       const float step = meta_step(meta);
-      const uint32_t slot = steps + (i & (kSlots - 1)) * S::kSteps + 4 * r;
       ok = __all_sync(0xFFFFFFFFu, wait_on(empty + 8 * (i & 1), ((i >> 1) & 1) ^ 1u, &give_up));
       if (!ok) break;
-      if (part == 0) {
+      // A value that is not there has a log of -infinity, so that its weight is 0,
+      // which adds 0 to the sum.  So does a NaN to the sums of rows that do not
+      // see it; its log spreads it to those that do.
+      if (row_lane) {
+        const uint32_t at = steps + (i & (kSlots - 1)) * S::kSteps + 4 * r;
         if (!value) {
-          asm volatile("st.shared.f32 [%0], %1;" :: "r"(slot), "f"(step) : "memory");
+          asm volatile("st.shared.f32 [%0], %1;" :: "r"(at), "f"(step) : "memory");
         } else {
-          // (of a NaN the log spreads it; its weight adds nothing to the sum for rows that do not see it)
           const float log = there ? log2_of(step) : kNone, per = there && step == step ? reciprocal(step) : 0.0f;
-          asm volatile("st.shared.f32 [%0], %1;" :: "r"(slot + 4 * KT), "f"(log) : "memory");
-          asm volatile("st.shared.f32 [%0], %1;" :: "r"(slot + 8 * KT), "f"(per) : "memory");
+          asm volatile("st.shared.f32 [%0], %1;" :: "r"(at + 4 * KT), "f"(log) : "memory");
+          asm volatile("st.shared.f32 [%0], %1;" :: "r"(at + 8 * KT), "f"(per) : "memory");
         }
       }
       __syncwarp();
@@ -473,18 +481,41 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
       const uint32_t zs = __byte_perm(meta, meta, 0x3232);
       const __half2 z = *reinterpret_cast<const __half2*>(&zs);
       const __half2 z_low = __hadd2(z, __float2half2_rn(1024.0f)), z_high = __hneg2(__hadd2(z, __float2half2_rn(64.0f)));
-      const uint32_t low = *reinterpret_cast<const uint32_t*>(&z_low), high = *reinterpret_cast<const uint32_t*>(&z_high);
-      const uint32_t to = stages + (i & 1) * S::kStage + r * 128;
+      const uint32_t my_low = *reinterpret_cast<const uint32_t*>(&z_low), my_high = *reinterpret_cast<const uint32_t*>(&z_high);
+      const uint32_t to = stages + (i & 1) * S::kStage;
+      // A piece's eights are stored in an order by piece, so that eight lanes that
+      // store together (one, two or four rows) meet no bank twice.
+      constexpr int kAtom = 8 / kChunks;                   // pieces of a row's 128 bytes
+      const int turn = (piece / kAtom * (kPieces / kAtom == 2 && kChunks == 4 ? 2 : 1)) & (kChunks - 1);
 #pragma unroll
-      for (int p = 0; p < kPieces; ++p) {
-        const uint32_t words[4] = {w[p].x, w[p].y, w[p].z, w[p].w};
+      for (int p = 0; p < kLoads; ++p) {
+        const int row = p * kWide + in_row;
+        const uint32_t low = __shfl_sync(kFull, my_low, row);
+        const uint32_t high = BITS == 4 ? __shfl_sync(kFull, my_high, row) : 0;
+        const uint32_t at = to + (row0 + row) * 128;
+        uint32_t words[4] = {w[p].x, w[p].y, w[p].z, w[p].w};
+        if constexpr (BITS == 4) {
+          if (turn & 2) {
+            uint32_t x = words[0];
+            words[0] = words[2], words[2] = x, x = words[1], words[1] = words[3], words[3] = x;
+          }
+          if (turn & 1) {
+            uint32_t x = words[0];
+            words[0] = words[1], words[1] = x, x = words[2], words[2] = words[3], words[3] = x;
+          }
+        } else {
+          if (turn & 1) {
+            uint32_t x = words[0];
+            words[0] = words[2], words[2] = x, x = words[1], words[1] = words[3], words[3] = x;
+          }
+        }
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
           uint32_t h[4];
           if constexpr (BITS == 4) turn4(words[c], low, high, h);
           else turn8(words[2 * c], words[2 * c + 1], low, h);
-          const int chunk = (part * kPieces + p) * kChunks + c;
-          store_shared16(to + (chunk >> 3) * (KT * 128) + (((chunk & 7) ^ (r & 7)) << 4), h);
+          const int chunk = piece * kChunks + (c ^ turn);
+          store_shared16(at + (chunk >> 3) * (KT * 128) + (((chunk & 7) ^ ((row0 + row) & 7)) << 4), h);
         }
       }
       fence_proxy_async();
@@ -607,13 +638,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
             }
             tmem_load(s_at, v[0][0]);
             tmem_load(s_at + (16u << 16), v[0][1]);
+#pragma unroll 1                                           // (code that is fetched again costs as much as its work)
+            for (int c0 = 0; c0 < KT; c0 += 64)
 #pragma unroll
-            for (int c = 0; c < KT; c += 32) {
-              float(&now)[2][16] = v[(c / 32) & 1];
+            for (int odd = 0; odd < 2; ++odd) {
+              const int c = c0 + 32 * odd;
+              float(&now)[2][16] = v[odd];
               tmem_loaded(now[0], now[1]);
               if (c + 32 < KT) {
-                tmem_load(s_at + c + 32, v[(c / 32 + 1) & 1][0]);
-                tmem_load(s_at + (16u << 16) + c + 32, v[(c / 32 + 1) & 1][1]);
+                tmem_load(s_at + c + 32, v[odd ^ 1][0]);
+                tmem_load(s_at + (16u << 16) + c + 32, v[odd ^ 1][1]);
               }
               float top[4] = {m[0], m[1], m[2], m[3]};
 #pragma unroll
@@ -694,57 +728,66 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
           }
         }
         if (!whole && done.in == 0 && tid == 0) name_parts(a, done, range);
+        // Two rows of 32 columns at a time, in a rolled loop: code that runs once a
+        // unit is fetched each time.
 #pragma unroll 1
-        for (int h = 0; h < 4; ++h) {
-          const int r = first + g + 8 * h, row = done.unit.first + r;
-          const bool there = r < done.unit.rows;
-          const float f = h == 0 ? per[0] : h == 1 ? per[1] : h == 2 ? per[2] : per[3];
-          const int64_t out = (done.s.row + row / a.group) * a.out.ld +
-                              (int64_t)(done.unit.head * a.group + row % a.group) * a.out.head_stride;
+        for (int half = 0; half < 2; ++half) {
+          const float per0 = half ? per[2] : per[0], per1 = half ? per[3] : per[1];
+          int64_t out[2];
+          bool there[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int r = first + g + 16 * half + 8 * h, row = done.unit.first + r;
+            there[h] = r < done.unit.rows;
+            out[h] = (done.s.row + row / a.group) * a.out.ld +
+                     (int64_t)(done.unit.head * a.group + row % a.group) * a.out.head_stride + 8 * quad;
+          }
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             float v[16];
-            tmem_load(sums + ((uint32_t)(h >> 1) << 20) + c, v);
+            tmem_load(sums + ((uint32_t)half << 20) + c, v);
             tmem_loaded(v);
-            // Of the row's four eights this lane has a pair each; after the
-            // exchange it has all pairs of the eight of its own number.
-            float e[8];
+            // Of a row's four eights this lane has a pair each; after the exchange
+            // it has all pairs of the eight of its own number.
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              float x[4];
+            for (int h = 0; h < 2; ++h) {
+              float e[8];
 #pragma unroll
-              for (int n = 0; n < 4; ++n) x[n] = h & 1 ? v[4 * n + 2 + b] : v[4 * n + b];
+              for (int b = 0; b < 2; ++b) {
+                float x[4];
 #pragma unroll
-              for (int step = 1; step < 4; step *= 2)
+                for (int n = 0; n < 4; ++n) x[n] = v[4 * n + 2 * h + b];
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                  if (n & step) continue;
-                  const bool high = quad & step;
-                  const float got = __shfl_xor_sync(kFull, high ? x[n] : x[n + step], step);
-                  if (high) x[n] = got;
-                  else x[n + step] = got;
+                for (int step = 1; step < 4; step *= 2)
+#pragma unroll
+                  for (int n = 0; n < 4; ++n) {
+                    if (n & step) continue;
+                    const bool high = quad & step;
+                    const float got = __shfl_xor_sync(kFull, high ? x[n] : x[n + step], step);
+                    x[n] = high ? got : x[n];
+                    x[n + step] = high ? x[n + step] : got;
+                  }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  const int place = 2 * q + b;             // in the eight, as TMEM has it
+                  e[BITS == 4 ? (place & 1) * 4 + (place >> 1) : place] = x[q];
                 }
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const int place = 2 * q + b;               // in the eight, as TMEM has it
-                e[BITS == 4 ? (place & 1) * 4 + (place >> 1) : place] = x[q];
               }
-            }
-            if (there) {
-              const int d = c + 8 * quad;
+              if (!there[h]) continue;
               if (whole) {
 #pragma unroll
-                for (int n = 0; n < 8; ++n) e[n] *= f;
+                for (int n = 0; n < 8; ++n) e[n] *= h ? per1 : per0;
                 if (wide_out) {
-                  if (a.dtype == ECHO_BF16) store_floats<__nv_bfloat16, 8>(static_cast<__nv_bfloat16*>(a.out.data) + out + d, e);
-                  else store_floats<__half, 8>(static_cast<__half*>(a.out.data) + out + d, e);
+                  if (a.dtype == ECHO_BF16) store_floats<__nv_bfloat16, 8>(static_cast<__nv_bfloat16*>(a.out.data) + out[h] + c, e);
+                  else store_floats<__half, 8>(static_cast<__half*>(a.out.data) + out[h] + c, e);
                 } else {
 #pragma unroll
-                  for (int n = 0; n < 8; ++n) store_value(a, out + d + n, e[n]);
+                  for (int n = 0; n < 8; ++n) store_value(a, out[h] + c + n, e[n]);
                 }
               } else {
-                *reinterpret_cast<float4*>(part + r * D + d) = make_float4(e[0], e[1], e[2], e[3]);
-                *reinterpret_cast<float4*>(part + r * D + d + 4) = make_float4(e[4], e[5], e[6], e[7]);
+                float* const to_part = part + (first + g + 16 * half + 8 * h) * D + c + 8 * quad;
+                *reinterpret_cast<float4*>(to_part) = make_float4(e[0], e[1], e[2], e[3]);
+                *reinterpret_cast<float4*>(to_part + 4) = make_float4(e[4], e[5], e[6], e[7]);
               }
             }
           }
