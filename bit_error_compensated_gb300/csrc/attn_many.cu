@@ -426,17 +426,21 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
     uint4 w[kLoads];
     uint32_t meta = 0;                                     // of this lane's row
     bool there = false;
-    // A row's page is looked up two tiles ahead, its codes are loaded one ahead.
-    int ahead = 0, page = -1, page_key = 0, page_head = 0; // tiles into the unit of the page that is looked up next
+    // A row's page is looked up two tiles ahead (and looked at one ahead: a use
+    // right away would wait for it), its codes are loaded one ahead.
+    int ahead = 0, page = 0, page_key = 0, page_head = 0;  // tiles into the unit of the page that is looked up next
+    enum { kNoKey, kNoPage, kPage };
+    int found = kNoKey;
     const uint32_t n = (uint32_t)(range.end - range.begin);
     auto look_up = [&]() {
-      page = -1;
+      found = kNoKey;
       if (!__any_sync(kFull, walk.more())) return;
       page_key = (walk.unit.tile + walk.in + ahead) * KT + r;
       page_head = walk.unit.head;
       if (row_lane && page_key < walk.s.keys) {
-        page = page_of(a.batch, a.cache, walk.unit.sequence, page_key);
-        if (page < 0) bad |= kBadPage;
+        const int at = page_key >> a.cache.page_shift;
+        found = at < a.batch.table_pages ? kPage : kNoPage;
+        if (found == kPage) page = a.batch.table[(int64_t)walk.unit.sequence * a.batch.ld_table + at];
       }
       if (++ahead == walk.take) {
         ahead = 0;
@@ -445,7 +449,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
     };
     // Rows that are not there have codes of 0, less 0.
     auto load = [&]() {
-      there = page >= 0;
+      there = found == kPage && page >= 0 && page < a.cache.pages;
+      if (found != kNoKey && !there) bad |= kBadPage;
       const int64_t group = there ? group_index(a.cache, page, page_head, page_key) + on : -1;
       meta = 0;
       if (there) meta = a.cache.meta[group];
@@ -553,7 +558,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
         const int first = t * kRowTile + 32 * (warp & 3);                  // of the unit's rows, the warp's first
         {
           const int r = first + lane, place = walk.s.place + (walk.unit.first + r) / a.group;
-          seen[r] = r < walk.unit.rows ? make_int2(keys_from(a, place), keys_to(a, walk.s, place)) : make_int2(0, 0);
+          // (rows past the last see all: one that sees nothing has no maximum)
+          seen[r] = r < walk.unit.rows ? make_int2(keys_from(a, place), keys_to(a, walk.s, place)) : make_int2(0, 0x7FFFFFFF);
           __syncwarp();
         }
 #pragma unroll
