@@ -26,6 +26,8 @@ ECHO_STATUS_WORD
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps, kRows = 16, kStep = 16, kTile = kStep * kWarps;
 constexpr int kLeast = 2;                // tiles of a block: fewer parts to join where a batch is small
+// Blocks an SM: what registers allow (of rows of 256, sums alone take 128 a thread).
+template <int D> __host__ __device__ constexpr int few_blocks() { return D == 256 ? 2 : 3; }
 constexpr float kAhead = 8.0f;           // a score may pass the maximum by this much, as a power of two
 
 template <int D, int BITS>
@@ -78,12 +80,12 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {         // a in
 // Codes less their zero points (of two rows, for values) as pairs of f16.
 // `low` is 1024 + z, `high` 64 + z, twice.
 struct Zero {
-  uint32_t low, high;
+  uint32_t low, high, base;              // base: 1024, twice
 };
-__device__ __forceinline__ Zero zero_of(uint32_t zs) {     // two fp16 zero points
+__device__ __forceinline__ Zero zero_of(uint32_t zs, uint32_t base) {     // two fp16 zero points
   const __half2 z = *reinterpret_cast<const __half2*>(&zs);
   const __half2 low = __hadd2(z, __float2half2_rn(1024.0f)), high = __hneg2(__hadd2(z, __float2half2_rn(64.0f)));
-  return {*reinterpret_cast<const uint32_t*>(&low), *reinterpret_cast<const uint32_t*>(&high)};
+  return {*reinterpret_cast<const uint32_t*>(&low), *reinterpret_cast<const uint32_t*>(&high), base};
 }
 __device__ __forceinline__ uint32_t less_low(uint32_t v, const Zero& z) {
   const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&v), *reinterpret_cast<const __half2*>(&z.low));
@@ -95,13 +97,13 @@ __device__ __forceinline__ uint32_t less_high(uint32_t v, const Zero& z) {
   return *reinterpret_cast<const uint32_t*>(&d);
 }
 __device__ __forceinline__ uint32_t low_codes(uint32_t w, const Zero& z) {        // at bits 0 and 16
-  return less_low((w & 0x000F000Fu) | 0x64006400u, z);
+  return less_low(masked<0x000F000Fu>(w, z.base), z);
 }
 __device__ __forceinline__ uint32_t high_codes(uint32_t w, const Zero& z) {       // at bits 4 and 20
-  return less_high((w & 0x00F000F0u) | 0x64006400u, z);
+  return less_high(masked<0x00F000F0u>(w, z.base), z);
 }
 __device__ __forceinline__ uint32_t byte_codes(uint32_t w, uint32_t bytes, const Zero& z) {
-  return less_low(__byte_perm(w, 0x64646464u, bytes), z);
+  return less_low(__byte_perm(w, z.base, bytes), z);
 }
 
 // Loads the unit's rows as operands: for each matrix instruction and lane, the
@@ -147,7 +149,7 @@ __device__ __forceinline__ void load_queries(const AttentionArgs& a, const Seque
 }
 
 template <int D, int BITS>
-__global__ void __launch_bounds__(kThreads) attention_few_kernel(const AttentionArgs a, const int vector_out) {
+__global__ void __launch_bounds__(kThreads, few_blocks<D>()) attention_few_kernel(const AttentionArgs a, const int vector_out) {
   using S = Shape<D, BITS>;
   constexpr int kCols = D / 8;                             // tiles of 8 columns
   extern __shared__ __align__(128) uint8_t raw[];
@@ -156,6 +158,7 @@ __global__ void __launch_bounds__(kThreads) attention_few_kernel(const Attention
   uint8_t* const query = raw + (S::kBytes - S::kQuery);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, quad = lane & 3;
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(raw) + warp * S::kStages * S::kStage;
+  const uint32_t base1024 = unknown(0x64006400u);
   pdl_wait();
   pdl_trigger();
   if (tid == 0) joins(a)[blockIdx.x].blocks = 0;
@@ -256,7 +259,7 @@ __global__ void __launch_bounds__(kThreads) attention_few_kernel(const Attention
           }
           uint32_t word;
           load_words<4>(meta + (8 * n + g) * 4, &word);
-          const Zero z = zero_of(__byte_perm(word, word, 0x3232));
+          const Zero z = zero_of(__byte_perm(word, word, 0x3232), base1024);
 #pragma unroll
           for (int k = 0; k < kWords; ++k) {
             if constexpr (BITS == 4) {
@@ -267,7 +270,7 @@ __global__ void __launch_bounds__(kThreads) attention_few_kernel(const Attention
               mma_f16(scores[n], q1.x, q1.y, q1.z, q1.w, low_codes(high, z), high_codes(high, z));
             } else {
               const uint4 q0 = reinterpret_cast<const uint4*>(query)[k * 32 + lane];
-              mma_f16(scores[n], q0.x, q0.y, q0.z, q0.w, byte_codes(w[k], 0x4140, z), byte_codes(w[k], 0x4342, z));
+              mma_f16(scores[n], q0.x, q0.y, q0.z, q0.w, byte_codes(w[k], 0x5150, z), byte_codes(w[k], 0x5352, z));
             }
           }
         }
@@ -348,8 +351,8 @@ __global__ void __launch_bounds__(kThreads) attention_few_kernel(const Attention
         __syncwarp();                                      // hidden keys part the lanes; matrix instructions want them together
         // Values: columns of eight lanes' pieces, keys' pairs side by side.
         constexpr int kPieceWords = S::kValuePiece / 4, kPieces = S::kRowBytes / (8 * S::kValuePiece);
-        const Zero zx = zero_of(__byte_perm(vmeta[0][0], vmeta[0][1], 0x7632));
-        const Zero zy = zero_of(__byte_perm(vmeta[1][0], vmeta[1][1], 0x7632));
+        const Zero zx = zero_of(__byte_perm(vmeta[0][0], vmeta[0][1], 0x7632), base1024);
+        const Zero zy = zero_of(__byte_perm(vmeta[1][0], vmeta[1][1], 0x7632), base1024);
         const uint32_t values = base + kStep * S::kRowBytes;
 #pragma unroll
         for (int piece = 0; piece < kPieces; ++piece) {
@@ -375,8 +378,8 @@ __global__ void __launch_bounds__(kThreads) attention_few_kernel(const Attention
                 add(out[4 * half + 2], low_codes(x >> 8, zx), low_codes(y >> 8, zy));
                 add(out[4 * half + 3], high_codes(x >> 8, zx), high_codes(y >> 8, zy));
               } else {
-                add(out[2 * half], byte_codes(x, 0x4240, zx), byte_codes(y, 0x4240, zy));
-                add(out[2 * half + 1], byte_codes(x, 0x4341, zx), byte_codes(y, 0x4341, zy));
+                add(out[2 * half], byte_codes(x, 0x5250, zx), byte_codes(y, 0x5250, zy));
+                add(out[2 * half + 1], byte_codes(x, 0x5351, zx), byte_codes(y, 0x5351, zy));
               }
             }
           }
@@ -481,7 +484,6 @@ __global__ void __launch_bounds__(128) attention_join_kernel(const AttentionArgs
   }
 }
 
-constexpr int kBlocksPerSm = 2;
 // Up to as many rows a sequence this kernel runs, for more attn_many.cu's.
 constexpr int64_t kFewRows = 64;
 
@@ -493,7 +495,7 @@ cudaError_t launch(const AttentionArgs& a, int sms, cudaStream_t s) {
     return cudaFuncSetAttribute(attention_few_kernel<D, BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
   });
   if (e != cudaSuccess) return e;
-  const int blocks = kBlocksPerSm * sms;
+  const int blocks = few_blocks<D>() * sms;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3(kThreads);
@@ -529,7 +531,7 @@ cudaError_t launch_attention(const AttentionArgs& a, int sms, cudaStream_t s) {
   return four ? launch<256, 4>(a, sms, s) : launch<256, 8>(a, sms, s);
 }
 int64_t attention_bytes(int head_dim, int sms) {
-  const int64_t few = workspace_bytes(kBlocksPerSm * sms, kRows, head_dim), many = attention_many_bytes(head_dim, sms);
+  const int64_t few = workspace_bytes((head_dim == 256 ? few_blocks<256>() : few_blocks<128>()) * sms, kRows, head_dim), many = attention_many_bytes(head_dim, sms);
   return few > many ? few : many;
 }
 StatusWord attn_few_status() { return {read_status, clear_status_bits}; }

@@ -175,18 +175,18 @@ __device__ __forceinline__ uint32_t less_high(uint32_t v, uint32_t z) {
   const __half2 d = __hfma2(*reinterpret_cast<const __half2*>(&v), __float2half2_rn(0.0625f), *reinterpret_cast<const __half2*>(&z));
   return *reinterpret_cast<const uint32_t*>(&d);
 }
-__device__ __forceinline__ void turn4(uint32_t w, uint32_t low, uint32_t high, uint32_t (&h)[4]) {
+__device__ __forceinline__ void turn4(uint32_t w, uint32_t base, uint32_t low, uint32_t high, uint32_t (&h)[4]) {
   const uint32_t up = w >> 8;
-  h[0] = less((w & 0x000F000Fu) | 0x64006400u, low);
-  h[1] = less_high((w & 0x00F000F0u) | 0x64006400u, high);
-  h[2] = less((up & 0x000F000Fu) | 0x64006400u, low);
-  h[3] = less_high((up & 0x00F000F0u) | 0x64006400u, high);
+  h[0] = less(masked<0x000F000Fu>(w, base), low);
+  h[1] = less_high(masked<0x00F000F0u>(w, base), high);
+  h[2] = less(masked<0x000F000Fu>(up, base), low);
+  h[3] = less_high(masked<0x00F000F0u>(up, base), high);
 }
-__device__ __forceinline__ void turn8(uint32_t a, uint32_t b, uint32_t low, uint32_t (&h)[4]) {
-  h[0] = less(__byte_perm(a, 0x64646464u, 0x4140), low);
-  h[1] = less(__byte_perm(a, 0x64646464u, 0x4342), low);
-  h[2] = less(__byte_perm(b, 0x64646464u, 0x4140), low);
-  h[3] = less(__byte_perm(b, 0x64646464u, 0x4342), low);
+__device__ __forceinline__ void turn8(uint32_t a, uint32_t b, uint32_t base, uint32_t low, uint32_t (&h)[4]) {
+  h[0] = less(__byte_perm(a, base, 0x5150), low);
+  h[1] = less(__byte_perm(a, base, 0x5352), low);
+  h[2] = less(__byte_perm(b, base, 0x5150), low);
+  h[3] = less(__byte_perm(b, base, 0x5352), low);
 }
 // The rows of tile t of a unit into shared memory, as the A operand (K-major);
 // a warp takes 32 of them.  They are scaled by one power of two, from the
@@ -412,6 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kTurnRegs));
     // Keys, or values: a thread has a row of a tile (of KT 64, half of one).
     const bool value = warp >= kWarpsWeights + kWarpsKeys;
+    const uint32_t base1024 = unknown(0x64006400u);
     // For loads a row's pieces of 16 bytes are neighbouring lanes', 32 * kWide of
     // which a warp takes at once; page and meta word of a row come from its lane.
     constexpr int kWarpRows = KT / 4, kPieces = S::kRowBytes / 16;         // rows of a warp; pieces of a row
@@ -517,8 +518,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
           uint32_t h[4];
-          if constexpr (BITS == 4) turn4(words[c], low, high, h);
-          else turn8(words[2 * c], words[2 * c + 1], low, h);
+          if constexpr (BITS == 4) turn4(words[c], base1024, low, high, h);
+          else turn8(words[2 * c], words[2 * c + 1], base1024, low, h);
           const int chunk = piece * kChunks + (c ^ turn);
           store_shared16(at + (chunk >> 3) * (KT * 128) + (((chunk & 7) ^ ((row0 + row) & 7)) << 4), h);
         }

@@ -55,10 +55,9 @@ template <> struct Codes<float> : CodesBf16 {};
 // Eight codes of a word, less the zero point, as pairs of elements (0, 4),
 // (1, 5), (2, 6), (3, 7).
 template <typename T>
-__device__ __forceinline__ void turn(uint32_t w, uint32_t zero, uint32_t (&h)[4]) {
+__device__ __forceinline__ void turn(uint32_t w, uint32_t base, uint32_t zero, uint32_t (&h)[4]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    h[i] = Codes<T>::less(((w >> (4 * i)) & 0x000F000Fu) | Codes<T>::kBase, zero);
+  for (int i = 0; i < 4; ++i) h[i] = Codes<T>::less(masked<0x000F000Fu>(w >> (4 * i), base), zero);
 }
 
 // WORDS words of a row of `bytes` bytes from byte `at` (a multiple of 4 WORDS),
@@ -149,6 +148,7 @@ __global__ void __launch_bounds__(32 * kWarps) linear4_kernel(const Linear4Args 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, quad = lane & 3;
   const int64_t rank = blockIdx.z, c0 = (int64_t)blockIdx.x * kRows, t0 = (int64_t)blockIdx.y * kCols;
   const int64_t bytes = (p.depth + 1) / 2;
+  const uint32_t base = unknown(Codes<T>::kBase);
   pdl_wait();
   pdl_trigger();
   // Rows past the last channel or token repeat it: their results are dropped.
@@ -201,8 +201,8 @@ __global__ void __launch_bounds__(32 * kWarps) linear4_kernel(const Linear4Args 
         uint32_t lo[TALL][4], hi[TALL][4];
 #pragma unroll
         for (int r = 0; r < TALL; ++r) {
-          turn<T>(w[d][2 * r][n], zero[2 * r], lo[r]);
-          turn<T>(w[d][2 * r + 1][n], zero[2 * r + 1], hi[r]);
+          turn<T>(w[d][2 * r][n], base, zero[2 * r], lo[r]);
+          turn<T>(w[d][2 * r + 1][n], base, zero[2 * r + 1], hi[r]);
         }
 #pragma unroll
         for (int o = 0; o < OCTETS; ++o) {

@@ -218,4 +218,20 @@ __device__ __forceinline__ float meta_zero(uint32_t meta) {
   return __half2float(__ushort_as_half((unsigned short)(meta >> 16)));
 }
 
+
+// (w & MASK) | base in one instruction: an instruction takes one constant, so
+// the base is a register that the compiler does not know (it made two of them,
+// and the codes' turning bounds these kernels).
+__device__ __forceinline__ uint32_t unknown(uint32_t v) {
+  uint32_t r;
+  asm("mov.b32 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t masked(uint32_t w, uint32_t base) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "n"(MASK), "r"(base));
+  return r;
+}
+
 }  // namespace echo
