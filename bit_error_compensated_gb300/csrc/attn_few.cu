@@ -1,22 +1,26 @@
 // attn_few.cu -- echo_attention for few rows a sequence (include/echo.h):
 // decode, drafted tokens.
 //
-// Every key is read once for 16 rows, so the kernel streams codes: each warp
-// copies 16 keys and values at a time into a ring of its own (asynchronous
-// copies, no barrier between warps) and feeds them to matrix instructions of 16
-// rows.  A code c behind the bits of 1024 is the f16 number 1024 + c (of 4 bits
-// at bit 4: 1024 + 16 c), from which one instruction for two codes takes c - z,
-// exactly; steps are multiplied into scores and weights in fp32.  (f16 holds
-// c * 2^-24 as it stands, as a subnormal, but the matrix instructions align
-// their sums by exponents that leave such a number 14 bits.)  The step s of a
-// value goes into the weight, p_j = exp(score_j + log s_j - m), whose running
-// maximum m then bounds p_j by 2^8 whatever the steps are (it is raised only
-// when a score passes it by 2^8), so that p_j has 11 bits in f16; the sum of
-// weights takes p_j / s_j.
+// Every key is read once for R = 8, 16 or 32 rows, so the kernel streams codes:
+// each warp copies 32 keys and values at a time into a ring of its own
+// (asynchronous copies, no barrier between warps) and feeds them to matrix
+// instructions whose 16 rows are keys, or columns of the values, and whose 8
+// columns are rows of queries:
+//     S^T[keys][rows] = K Q^T,    O^T[columns][rows] += V^T P^T
+// (the other way round half of an instruction is idle where a head of the cache
+// serves 8 queries or fewer).  A code c behind the bits of 1024 is the f16
+// number 1024 + c (of 4 bits at bit 4: 1024 + 16 c), from which one instruction
+// for two codes takes c - z, exactly; steps are multiplied into scores and
+// weights in fp32.  (f16 holds c * 2^-24 as it stands, as a subnormal, but the
+// matrix instructions align their sums by exponents that leave such a number 14
+// bits.)  The step s of a value goes into the weight, p_j = exp(score_j + log
+// s_j - m), whose running maximum m then bounds p_j by 2^8 whatever the steps
+// are (it is raised only when a score passes it by 2^8), so that p_j has 11 bits
+// in f16; the sum of weights takes p_j / s_j.
 //
 // Blocks take equal shares of the batch's tiles (attn_common.h); four warps
-// take a tile's 64 keys and join at the unit's end, and parts of units that
-// several blocks have had are joined by a second kernel.
+// take a tile's keys and join at the unit's end, and parts of units that several
+// blocks have had are joined by a second kernel.
 #include "attn_common.h"
 
 namespace echo {
@@ -24,24 +28,30 @@ namespace {
 
 ECHO_STATUS_WORD
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps, kRows = 16, kStep = 16, kTile = kStep * kWarps;
-constexpr int kLeast = 2;                // tiles of a block: fewer parts to join where a batch is small
-// Blocks an SM: what registers allow (of rows of 256, sums alone take 128 a thread).
-template <int D> __host__ __device__ constexpr int few_blocks() { return D == 256 ? 2 : 3; }
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kLeast = 1;                // tiles of a block
 constexpr float kAhead = 8.0f;           // a score may pass the maximum by this much, as a power of two
 
-template <int D, int BITS>
-struct Shape {
+// NR: eights of rows.
+template <int D, int BITS, int NR>
+struct Few {
+  static constexpr int kRows = 8 * NR;
   static constexpr int kRowBytes = D * BITS / 8;
+  static constexpr int kStep = kRowBytes >= 256 ? 16 : 32;                 // keys of a warp at once
+  static constexpr int kTile = kStep * kWarps;
   static constexpr int kStage = 2 * kStep * kRowBytes + 2 * kStep * 4;     // keys, values, meta of both
-  static constexpr int kStages = kRowBytes >= 256 ? 3 : 4;
+  static constexpr int kStages = kRowBytes >= 128 ? 2 : 3;
   static constexpr int kRing = kWarps * kStages * kStage;
-  static constexpr int kJoin = kWarps * kRows * D * 4;   // the warps' sums, in the ring's place
-  static constexpr int kQuery = D / 16 * 32 * 16;        // rows as the instructions' operands
+  static constexpr int kPitch = D + 4;                   // floats from row to row of the warps' sums
+  static constexpr int kJoin = kWarps * kRows * kPitch * 4;                // which take the ring's place
+  static constexpr int kQuery = D / 16 * NR * 32 * 8;    // rows as the instructions' operands
   static constexpr int kBytes = (kRing > kJoin ? kRing : kJoin) + kQuery;
   static constexpr int kKeyPiece = kRowBytes / 4 < 16 ? kRowBytes / 4 : 16;      // bytes a thread takes at once
   static constexpr int kValuePiece = kRowBytes / 8 < 16 ? kRowBytes / 8 : 16;
   static constexpr int kPerWord = 32 / BITS;
+  // Blocks an SM: what registers (sums take D * NR / 4 a thread) and shared memory allow.
+  static constexpr int kByRegs = D * NR <= 128 ? 4 : D * NR <= 256 ? 3 : 2, kBySmem = 227 * 1024 / (kBytes + 2560);
+  static constexpr int kBlocks = kByRegs < kBySmem ? kByRegs : kBySmem;
 };
 
 // Where 16-byte piece `piece` of row r lies in a stage: turned so that the lanes
@@ -59,7 +69,7 @@ __device__ __forceinline__ int value_at(int at, int piece) {     // at: value_ro
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3},{%4,%5,%6,%7},{%8,%9},{%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3},{%4,%5,%6,%7},{%8,%9},{%0,%1,%2,%3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -71,6 +81,12 @@ __device__ __forceinline__ void load_words(uint32_t at, uint32_t* w) {
     asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at) : "memory");
   else
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(at) : "memory");
+}
+// 8 x 8 halves, a lane's two in row lane / 4, with rows and columns exchanged.
+__device__ __forceinline__ uint32_t transposed(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
 }
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {         // a in the low half
   const __half2 h = __floats2half2_rn(a, b);
@@ -106,18 +122,18 @@ __device__ __forceinline__ uint32_t byte_codes(uint32_t w, uint32_t bytes, const
   return less_low(__byte_perm(w, z.base, bytes), z);
 }
 
-// Loads the unit's rows as operands: for each matrix instruction and lane, the
-// four registers in a row.  Element e of a row meets the code that the lane
+// Loads the unit's rows as operands: for each matrix instruction, eight of rows
+// and lane, its two registers.  Element e of a row meets the code that the lane
 // of its quarter finds at the same place of its words.  The rows' factors go to
 // shared memory (NaN for a row with a non-finite element).
-template <typename T, int D, int BITS>
+template <typename T, int D, int BITS, int NR>
 __device__ __forceinline__ void load_queries(const AttentionArgs& a, const Sequence& s, const Unit& u, uint8_t* query,
                                              float* factor) {
-  using S = Shape<D, BITS>;
+  using S = Few<D, BITS, NR>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-#pragma unroll
-  for (int i = 0; i < kRows / kWarps; ++i) {
-    const int r = warp * (kRows / kWarps) + i, row = u.first + r;
+#pragma unroll 2
+  for (int i = 0; i < S::kRows / kWarps; ++i) {
+    const int r = warp * (S::kRows / kWarps) + i, row = u.first + r;
     float v[D / 32];
     uint32_t top = 0;
     if (r < u.rows) {
@@ -141,20 +157,22 @@ __device__ __forceinline__ void load_queries(const AttentionArgs& a, const Seque
       const int word = (piece >> 2) * (S::kKeyPiece / 4) + in / S::kPerWord, c = in % S::kPerWord;
       const int instruction = BITS == 4 ? 2 * word + ((c >> 1) & 1) : word;
       const int half = BITS == 4 ? c >> 2 : c & 1, second = BITS == 4 ? c & 1 : c >> 1;
-      const int at = ((instruction * 32 + (r & 7) * 4 + quad) * 4 + 2 * second + (r >> 3)) * 4 + 2 * half;
+      const int at = ((instruction * NR + (r >> 3)) * 32 + (r & 7) * 4 + quad) * 8 + 4 * second + 2 * half;
       *reinterpret_cast<__half*>(query + at) = __float2half_rn(v[k] * f);
     }
     if (lane == 0) factor[r] = top < 0x7F800000u ? a.scale * kLog2E / f : __int_as_float(0x7FC00000);
   }
 }
 
-template <int D, int BITS>
-__global__ void __launch_bounds__(kThreads, few_blocks<D>()) attention_few_kernel(const AttentionArgs a, const int vector_out) {
-  using S = Shape<D, BITS>;
-  constexpr int kCols = D / 8;                             // tiles of 8 columns
+template <int D, int BITS, int NR>
+__global__ void __launch_bounds__(kThreads, (Few<D, BITS, NR>::kBlocks)) attention_few_kernel(const AttentionArgs a, const int vector_out) {
+  using S = Few<D, BITS, NR>;
+  constexpr int kRows = S::kRows, kStep = S::kStep, kTile = S::kTile, kSubs = kStep / 16;
+  constexpr int kPairs = D / 16;                           // of columns that a thread has of O^T
   extern __shared__ __align__(128) uint8_t raw[];
   __shared__ int64_t shared[kWarps + 3];
   __shared__ float factor[kRows], most[kWarps][kRows], weight[kWarps][kRows];
+  __shared__ int2 seen[kRows];                             // keys [x, y) that a row sees
   uint8_t* const query = raw + (S::kBytes - S::kQuery);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, quad = lane & 3;
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(raw) + warp * S::kStages * S::kStage;
@@ -171,71 +189,91 @@ __global__ void __launch_bounds__(kThreads, few_blocks<D>()) attention_few_kerne
     const Unit& u = walk.unit;
     const int tiles = walk.take;
     const bool whole = walk.whole();
+
     __syncthreads();                                       // the last unit's sums have been read
-    if (a.dtype == ECHO_BF16) load_queries<__nv_bfloat16, D, BITS>(a, s, u, query, factor);
-    else load_queries<__half, D, BITS>(a, s, u, query, factor);
-    __syncthreads();
-    const bool tall = u.rows > 8;
-    float row_scale[2];
-    int from[2], to[2];                                    // keys that rows g and g + 8 see
-    int all_from = 0, all_to = 0x7FFFFFFF, end = 0;        // that all rows see, and where the last that any sees ends
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = g + 8 * h, place = s.place + (u.first + r) / a.group;
-      row_scale[h] = factor[r];
-      from[h] = r < u.rows ? keys_from(a, place) : 0;
-      to[h] = r < u.rows ? keys_to(a, s, place) : 0;
+    if (a.dtype == ECHO_BF16) load_queries<__nv_bfloat16, D, BITS, NR>(a, s, u, query, factor);
+    else load_queries<__half, D, BITS, NR>(a, s, u, query, factor);
+    if (tid < kRows) {
+      const int place = s.place + (u.first + tid) / a.group;
+      // (rows past the last see all, so that they ask for nothing by themselves)
+      seen[tid] = tid < u.rows ? make_int2(keys_from(a, place), keys_to(a, s, place)) : make_int2(0, 0x7FFFFFFF);
     }
-    {
-      const int first = s.place + u.first / a.group, last = s.place + (u.first + u.rows - 1) / a.group;
-      all_to = keys_to(a, s, first);
-      all_from = keys_from(a, last);
-      end = keys_to(a, s, last);
+    // Keys that all rows see, and where the last that any sees ends.
+    const int first_place = s.place + u.first / a.group, last_place = s.place + (u.first + u.rows - 1) / a.group;
+    const int all_to = keys_to(a, s, first_place), all_from = keys_from(a, last_place), end = keys_to(a, s, last_place);
+    __syncthreads();
+    float row_scale[NR][2];                                // of rows 8 o + 2 quad and the next
+#pragma unroll
+    for (int o = 0; o < NR; ++o)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) row_scale[o][e] = factor[8 * o + 2 * quad + e];
+    uint2 held[NR == 1 ? D / 16 : 1];                      // one eight of rows stays in registers
+    if constexpr (NR == 1) {
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) held[k] = reinterpret_cast<const uint2*>(query)[k * 32 + lane];
     }
 
-    float sums[kCols][4], m[2] = {kLowest, kLowest}, l[2] = {0.0f, 0.0f};
+    float sums[kPairs][NR][4], m[NR][2], l[NR][2];
 #pragma unroll
-    for (int c = 0; c < kCols; ++c)
+    for (int o = 0; o < NR; ++o) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) sums[c][k] = 0.0f;
+      for (int c = 0; c < kPairs; ++c)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sums[c][o][k] = 0.0f;
+      m[o][0] = m[o][1] = kLowest;
+      l[o][0] = l[o][1] = 0.0f;
+    }
 
     const int key0 = (u.tile + walk.in) * kTile + kStep * warp;            // of this warp's first step
     const int64_t values_on = (int64_t)heads << a.cache.page_shift;        // groups from a key's to its value's
-    uint32_t missing = 0;                                  // stages without a page
-    auto look_up = [&](int t) {
-      const int key = key0 + t * kTile;
-      return t < tiles && key < end ? page_of(a.batch, a.cache, u.sequence, key) : -1;
+    uint32_t missing = 0;                                  // 16 keys of a stage without a page, a bit each
+    // The pages of a step's sixteens of keys (the same one where a page is larger).
+    struct Pages {
+      int of[kSubs];
     };
-    auto issue = [&](int t, int page, int stage) {
-      const int key = key0 + t * kTile;
-      missing &= ~(1u << stage);
-      if (page >= 0) {
-        const int64_t group = group_index(a.cache, page, u.head, key & (page_size - 1));
-        const uint8_t* codes = a.cache.codes + group * S::kRowBytes;
-        const uint32_t base = ring + stage * S::kStage;
-        constexpr int kPieces = S::kRowBytes / 16;         // of a row; a stage's rows have 32 lanes' worth of them or more
+    auto look_up = [&](int t) {
+      Pages p;
 #pragma unroll
-        for (int n = 0; n < kPieces * kStep / 32; ++n) {
-          const int piece = lane + 32 * n, r = piece / kPieces, p = piece % kPieces;
-          copy16_async(base + key_at<S::kRowBytes>(r, p), codes + piece * 16);
-          copy16_async(base + kStep * S::kRowBytes + value_at<S::kRowBytes>(value_row(r), p),
-                       codes + values_on * S::kRowBytes + piece * 16);
+      for (int sub = 0; sub < kSubs; ++sub) {
+        const int key = key0 + t * kTile + 16 * sub;
+        p.of[sub] = t < tiles && key < end ? page_of(a.batch, a.cache, u.sequence, key) : -1;
+      }
+      return p;
+    };
+    auto issue = [&](int t, const Pages& pages, int stage) {
+#pragma unroll
+      for (int sub = 0; sub < kSubs; ++sub) {
+        const int key = key0 + t * kTile + 16 * sub, page = pages.of[sub];
+        const uint32_t bit = 1u << (stage * kSubs + sub);
+        missing &= ~bit;
+        if (page >= 0) {
+          const int64_t group = group_index(a.cache, page, u.head, key & (page_size - 1));
+          const uint8_t* codes = a.cache.codes + group * S::kRowBytes + 16 * lane;
+          const uint8_t* value_codes = codes + values_on * S::kRowBytes;
+          const uint32_t base = ring + stage * S::kStage + sub * 16 * S::kRowBytes;
+          constexpr int kPieces = S::kRowBytes / 16;       // of a row; 16 rows have 32 lanes' worth of them or more
+#pragma unroll
+          for (int n = 0; n < kPieces * 16 / 32; ++n) {
+            const int piece = lane + 32 * n, r = piece / kPieces, p = piece % kPieces;
+            copy16_async(base + key_at<S::kRowBytes>(r, p), codes + 512 * n);
+            copy16_async(base + kStep * S::kRowBytes + value_at<S::kRowBytes>(value_row(r), p), value_codes + 512 * n);
+          }
+          if (lane < 8)
+            copy16_async(ring + stage * S::kStage + 2 * kStep * S::kRowBytes + (lane < 4 ? 0 : 4 * kStep) + 64 * sub + 16 * (lane & 3),
+                         a.cache.meta + group + (lane < 4 ? 0 : values_on) + 4 * (lane & 3));
+        } else {
+          missing |= bit;
+          if (t < tiles && key < end) bad |= kBadPage;
         }
-        if (lane < 8)
-          copy16_async(base + 2 * kStep * S::kRowBytes + 16 * lane,
-                       a.cache.meta + group + (lane < 4 ? 0 : values_on) + 4 * (lane & 3));
-      } else if (t < tiles && key < end) {
-        missing |= 1u << stage;
-        bad |= kBadPage;
       }
       copies_commit();
     };
-    int page = look_up(0);
+    Pages pages = look_up(0);
 #pragma unroll 1
     for (int t = 0; t < S::kStages - 1; ++t) {
-      const int next = look_up(t + 1);
-      issue(t, page, t);
-      page = next;
+      const Pages next = look_up(t + 1);
+      issue(t, pages, t);
+      pages = next;
     }
     int stage = 0, ahead = S::kStages - 1;
 #pragma unroll 1
@@ -243,152 +281,208 @@ __global__ void __launch_bounds__(kThreads, few_blocks<D>()) attention_few_kerne
       const int key = key0 + t * kTile;
       copies_wait<S::kStages - 2>();
       __syncwarp();
-      if (key < end && !(missing >> stage & 1)) {          // the whole warp
+      const uint32_t absent = missing >> (stage * kSubs) & ((1u << kSubs) - 1);
+      if (key < end && absent != (1u << kSubs) - 1) {      // the whole warp
         const uint32_t base = ring + stage * S::kStage, meta = base + 2 * kStep * S::kRowBytes;
-        float scores[2][4];
+        // S^T of keys 16 sub + g (+ 8) and rows 8 o + 2 quad (+ 1).
+        float scores[kSubs][NR][4];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
+        for (int sub = 0; sub < kSubs; ++sub)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) scores[n][k] = 0.0f;
-          constexpr int kWords = S::kRowBytes / 16, kPieceWords = S::kKeyPiece / 4;      // a thread's, of a row and at once
-          uint32_t w[kWords];
+          for (int o = 0; o < NR; ++o)
 #pragma unroll
-          for (int p = 0; p < kWords / kPieceWords; ++p) {
-            const int byte = (4 * p + quad) * S::kKeyPiece;
-            load_words<S::kKeyPiece>(base + key_at<S::kRowBytes>(8 * n + g, byte / 16) + byte % 16, w + p * kPieceWords);
-          }
-          uint32_t word;
-          load_words<4>(meta + (8 * n + g) * 4, &word);
-          const Zero z = zero_of(__byte_perm(word, word, 0x3232), base1024);
+            for (int k = 0; k < 4; ++k) scores[sub][o][k] = 0.0f;
+        uint32_t vmeta[kSubs][2], kmeta[kSubs][2];
+        Zero z[kSubs][2];
 #pragma unroll
-          for (int k = 0; k < kWords; ++k) {
-            if constexpr (BITS == 4) {
-              const uint4 q0 = reinterpret_cast<const uint4*>(query)[2 * k * 32 + lane];
-              const uint4 q1 = reinterpret_cast<const uint4*>(query)[(2 * k + 1) * 32 + lane];
-              const uint32_t high = w[k] >> 8;
-              mma_f16(scores[n], q0.x, q0.y, q0.z, q0.w, low_codes(w[k], z), high_codes(w[k], z));
-              mma_f16(scores[n], q1.x, q1.y, q1.z, q1.w, low_codes(high, z), high_codes(high, z));
-            } else {
-              const uint4 q0 = reinterpret_cast<const uint4*>(query)[k * 32 + lane];
-              mma_f16(scores[n], q0.x, q0.y, q0.z, q0.w, byte_codes(w[k], 0x5150, z), byte_codes(w[k], 0x5352, z));
-            }
-          }
-        }
-        // This thread's keys: 2 quad and 2 quad + 1 of each eight.
-        uint32_t vmeta[2][2];
-        const bool inside = key >= all_from && key + kStep <= all_to;      // every row sees all 16
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          uint32_t kmeta[2];
-          load_words<8>(meta + (8 * n + 2 * quad) * 4, kmeta);
-          load_words<8>(meta + (kStep + 8 * n + 2 * quad) * 4, vmeta[n]);
-          float ks[2], steps[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            ks[e] = meta_step(kmeta[e]);
-            steps[e] = log2_of(meta_step(vmeta[n][e]));
-          }
+        for (int sub = 0; sub < kSubs; ++sub)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            if (h == 1 && !tall) break;
-            float *s0 = &scores[n][2 * h], *s1 = s0 + 1;
-            mul2(*s0, *s1, *s0, *s1, row_scale[h], row_scale[h]);
-            fma2(*s0, *s1, *s0, *s1, ks[0], ks[1], steps[0], steps[1]);
+            load_words<4>(meta + (16 * sub + 8 * h + g) * 4, &kmeta[sub][h]);
+            load_words<4>(meta + (kStep + 16 * sub + 8 * h + g) * 4, &vmeta[sub][h]);
+            z[sub][h] = zero_of(__byte_perm(kmeta[sub][h], kmeta[sub][h], 0x3232), base1024);
           }
-        }
-        if (!inside) {
+        {
+          constexpr int kPieceWords = S::kKeyPiece / 4, kPieces = S::kRowBytes / (4 * S::kKeyPiece);
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
+          for (int p = 0; p < kPieces; ++p) {
+            const int byte = (4 * p + quad) * S::kKeyPiece;
+            uint32_t w[kSubs][2][kPieceWords];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int k = key + 8 * n + 2 * quad + e;
-              if (k >= end) vmeta[n][e] = 0x00003C00u;     // whatever lies there must not meet a weight of 0
+            for (int sub = 0; sub < kSubs; ++sub)
 #pragma unroll
               for (int h = 0; h < 2; ++h)
-                if (k < from[h] || k >= to[h]) scores[n][2 * h + e] = kNone;
+                load_words<S::kKeyPiece>(base + key_at<S::kRowBytes>(16 * sub + 8 * h + g, byte / 16) + byte % 16, w[sub][h]);
+#pragma unroll
+            for (int k = 0; k < kPieceWords; ++k)
+#pragma unroll
+              for (int part = 0; part < (BITS == 4 ? 2 : 1); ++part) {
+                const int instruction = BITS == 4 ? 2 * (p * kPieceWords + k) + part : p * kPieceWords + k;
+                uint2 q[NR];
+#pragma unroll
+                for (int o = 0; o < NR; ++o) {
+                  if constexpr (NR == 1) q[o] = held[instruction];
+                  else q[o] = reinterpret_cast<const uint2*>(query)[(instruction * NR + o) * 32 + lane];
+                }
+#pragma unroll
+                for (int sub = 0; sub < kSubs; ++sub) {
+                  uint32_t c[2][2];                        // of key g, g + 8: first and second pair
+#pragma unroll
+                  for (int h = 0; h < 2; ++h) {
+                    const uint32_t v = w[sub][h][k];
+                    if constexpr (BITS == 4) {
+                      c[h][0] = low_codes(part ? v >> 8 : v, z[sub][h]);
+                      c[h][1] = high_codes(part ? v >> 8 : v, z[sub][h]);
+                    } else {
+                      c[h][0] = byte_codes(v, 0x5150, z[sub][h]);
+                      c[h][1] = byte_codes(v, 0x5352, z[sub][h]);
+                    }
+                  }
+#pragma unroll
+                  for (int o = 0; o < NR; ++o) mma_f16(scores[sub][o], c[0][0], c[1][0], c[0][1], c[1][1], q[o].x, q[o].y);
+                }
+              }
+          }
+        }
+        const bool inside = key >= all_from && key + kStep <= all_to && absent == 0;     // every row sees all
+        float per[kSubs][2];                               // 1 / step of the values
+#pragma unroll
+        for (int sub = 0; sub < kSubs; ++sub)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float ks = meta_step(kmeta[sub][h]), vs = meta_step(vmeta[sub][h]);
+            const float log = log2_of(vs);
+            per[sub][h] = reciprocal(vs);
+#pragma unroll
+            for (int o = 0; o < NR; ++o) {
+              float &s0 = scores[sub][o][2 * h], &s1 = scores[sub][o][2 * h + 1];
+              mul2(s0, s1, s0, s1, row_scale[o][0], row_scale[o][1]);
+              fma2(s0, s1, s0, s1, ks, ks, log, log);
+            }
+          }
+        if (!inside) {
+#pragma unroll
+          for (int sub = 0; sub < kSubs; ++sub)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int k = key + 16 * sub + 8 * h + g;
+              // Whatever lies where no key is must not meet a weight of 0, nor may
+              // a NaN that a row does not see reach its sum: the weight adds 0.
+              const bool there = k < end && !(absent >> sub & 1);
+              if (!there || !(per[sub][h] > 0.0f)) per[sub][h] = 0.0f;
+#pragma unroll
+              for (int o = 0; o < NR; ++o)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const int2 see = seen[8 * o + 2 * quad + e];
+                  if (!there || k < see.x || k >= see.y) scores[sub][o][2 * h + e] = kNone;
+                }
             }
         }
         // The maxima, where a score has passed them by far.
-        float top[2];
-        top[0] = fmaxf(fmaxf(scores[0][0], scores[0][1]), fmaxf(scores[1][0], scores[1][1]));
-        top[1] = tall ? fmaxf(fmaxf(scores[0][2], scores[0][3]), fmaxf(scores[1][2], scores[1][3])) : kLowest;
-        if (__any_sync(kFull, top[0] - kAhead > m[0] || top[1] - kAhead > m[1])) {
+        float top[NR][2];
+        bool passed = false;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            top[h] = fmaxf(top[h], __shfl_xor_sync(kFull, top[h], 1));
-            top[h] = fmaxf(top[h], __shfl_xor_sync(kFull, top[h], 2));
-            top[h] = fmaxf(top[h], m[h]);
-            const float f = exp2_of(m[h] - top[h]);
-            m[h] = top[h];
-            l[h] *= f;
+        for (int o = 0; o < NR; ++o)
 #pragma unroll
-            for (int c = 0; c < kCols; ++c) {
-              sums[c][2 * h] *= f;
-              sums[c][2 * h + 1] *= f;
+          for (int e = 0; e < 2; ++e) {
+            top[o][e] = m[o][e];
+#pragma unroll
+            for (int sub = 0; sub < kSubs; ++sub) top[o][e] = max3(top[o][e], scores[sub][o][e], scores[sub][o][2 + e]);
+            passed |= top[o][e] - m[o][e] > kAhead;
+          }
+        if (__any_sync(kFull, passed)) {
+#pragma unroll
+          for (int o = 0; o < NR; ++o) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float v = top[o][e];
+#pragma unroll
+              for (int off = 4; off < 32; off <<= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, off));
+              top[o][e] = exp2_of(m[o][e] - v);
+              m[o][e] = v;
+              l[o][e] *= top[o][e];
+            }
+#pragma unroll
+            for (int c = 0; c < kPairs; ++c) {
+              mul2(sums[c][o][0], sums[c][o][1], sums[c][o][0], sums[c][o][1], top[o][0], top[o][1]);
+              mul2(sums[c][o][2], sums[c][o][3], sums[c][o][2], sums[c][o][3], top[o][0], top[o][1]);
             }
           }
         }
-        uint32_t p[2][2] = {{0, 0}, {0, 0}};               // weights of [keys' eight][rows' eight]
+        uint32_t p[kSubs][NR][2];                          // P^T as operands: keys 2 quad (+ 1) of each eight, row g
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          float per[2];
+        for (int sub = 0; sub < kSubs; ++sub)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) per[e] = reciprocal(meta_step(vmeta[n][e]));
+          for (int o = 0; o < NR; ++o)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (h == 1 && !tall) break;
-            const float p0 = exp2_of(scores[n][2 * h] - m[h]), p1 = exp2_of(scores[n][2 * h + 1] - m[h]);
-            if (inside) {
-              l[h] = fmaf(p0, per[0], l[h]);
-              l[h] = fmaf(p1, per[1], l[h]);
-            } else {                                       // a hidden key's step may be anything
-              if (scores[n][2 * h] != kNone) l[h] = fmaf(p0, per[0], l[h]);
-              if (scores[n][2 * h + 1] != kNone) l[h] = fmaf(p1, per[1], l[h]);
+            for (int h = 0; h < 2; ++h) {
+              float p0 = scores[sub][o][2 * h], p1 = scores[sub][o][2 * h + 1];
+              sub2(p0, p1, p0, p1, m[o][0], m[o][1]);
+              p0 = exp2_of(p0);
+              p1 = exp2_of(p1);
+              fma2(l[o][0], l[o][1], p0, p1, per[sub][h], per[sub][h], l[o][0], l[o][1]);
+              p[sub][o][h] = pack_f16(p0, p1);
             }
-            p[n][h] = pack_f16(p0, p1);
-          }
-        }
         __syncwarp();                                      // hidden keys part the lanes; matrix instructions want them together
-        // Values: columns of eight lanes' pieces, keys' pairs side by side.
+#pragma unroll
+        for (int sub = 0; sub < kSubs; ++sub)
+#pragma unroll
+          for (int o = 0; o < NR; ++o)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) p[sub][o][h] = transposed(p[sub][o][h]);
+        // Values: a lane has its piece of every eighth of a row; pairs of keys side by side.
         constexpr int kPieceWords = S::kValuePiece / 4, kPieces = S::kRowBytes / (8 * S::kValuePiece);
-        const Zero zx = zero_of(__byte_perm(vmeta[0][0], vmeta[0][1], 0x7632), base1024);
-        const Zero zy = zero_of(__byte_perm(vmeta[1][0], vmeta[1][1], 0x7632), base1024);
         const uint32_t values = base + kStep * S::kRowBytes;
 #pragma unroll
-        for (int piece = 0; piece < kPieces; ++piece) {
-          const int byte = (8 * piece + g) * S::kValuePiece;
-          uint32_t w[4][kPieceWords];                      // keys 2 quad, 2 quad + 1, and 8 on
+        for (int sub = 0; sub < kSubs; ++sub) {
+          Zero zv[2];
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            load_words<S::kValuePiece>(
-                values + value_at<S::kRowBytes>(8 * (k >> 1) + 4 * (k & 1) + quad, byte / 16) + byte % 16, w[k]);
+          for (int h = 0; h < 2; ++h) {
+            uint32_t two[2];
+            load_words<8>(meta + (kStep + 16 * sub + 8 * h + 2 * quad) * 4, two);
+            if (!inside) {                                 // (as above: no NaN where no key is)
 #pragma unroll
-          for (int k = 0; k < kPieceWords; ++k) {
-            float(*out)[4] = &sums[(piece * kPieceWords + k) * S::kPerWord];
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const uint32_t x = __byte_perm(w[0][k], w[1][k], half ? 0x7632 : 0x5410);
-              const uint32_t y = __byte_perm(w[2][k], w[3][k], half ? 0x7632 : 0x5410);
-              auto add = [&](float(&to)[4], uint32_t b0, uint32_t b1) {
-                mma_f16(to, p[0][0], p[0][1], p[1][0], p[1][1], b0, b1);
-              };
-              if constexpr (BITS == 4) {
-                add(out[4 * half], low_codes(x, zx), low_codes(y, zy));
-                add(out[4 * half + 1], high_codes(x, zx), high_codes(y, zy));
-                add(out[4 * half + 2], low_codes(x >> 8, zx), low_codes(y >> 8, zy));
-                add(out[4 * half + 3], high_codes(x >> 8, zx), high_codes(y >> 8, zy));
-              } else {
-                add(out[2 * half], byte_codes(x, 0x5250, zx), byte_codes(y, 0x5250, zy));
-                add(out[2 * half + 1], byte_codes(x, 0x5351, zx), byte_codes(y, 0x5351, zy));
-              }
+              for (int e = 0; e < 2; ++e)
+                if (key + 16 * sub + 8 * h + 2 * quad + e >= end || (absent >> sub & 1)) two[e] = 0;
             }
+            zv[h] = zero_of(__byte_perm(two[0], two[1], 0x7632), base1024);
+          }
+#pragma unroll
+          for (int piece = 0; piece < kPieces; ++piece) {
+            const int byte = (8 * piece + g) * S::kValuePiece;
+            uint32_t w[4][kPieceWords];                    // keys 2 quad, 2 quad + 1, and 8 on
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              load_words<S::kValuePiece>(
+                  values + value_at<S::kRowBytes>(16 * sub + 8 * (k >> 1) + 4 * (k & 1) + quad, byte / 16) + byte % 16, w[k]);
+#pragma unroll
+            for (int k = 0; k < kPieceWords; ++k)
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                const uint32_t x = __byte_perm(w[0][k], w[1][k], half ? 0x7632 : 0x5410);
+                const uint32_t y = __byte_perm(w[2][k], w[3][k], half ? 0x7632 : 0x5410);
+                const int pair = (piece * kPieceWords + k) * (S::kPerWord / 2) + (BITS == 4 ? 2 * half : half);
+                auto add = [&](int at, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+                  for (int o = 0; o < NR; ++o) mma_f16(sums[at][o], a0, a1, a2, a3, p[sub][o][0], p[sub][o][1]);
+                };
+                if constexpr (BITS == 4) {
+                  add(pair, low_codes(x, zv[0]), high_codes(x, zv[0]), low_codes(y, zv[1]), high_codes(y, zv[1]));
+                  add(pair + 1, low_codes(x >> 8, zv[0]), high_codes(x >> 8, zv[0]), low_codes(y >> 8, zv[1]),
+                      high_codes(y >> 8, zv[1]));
+                } else {
+                  add(pair, byte_codes(x, 0x5250, zv[0]), byte_codes(x, 0x5351, zv[0]), byte_codes(y, 0x5250, zv[1]),
+                      byte_codes(y, 0x5351, zv[1]));
+                }
+              }
           }
         }
       }
       __syncwarp();                                        // before the stage is overwritten
-      const int next = look_up(t + S::kStages);
-      issue(t + S::kStages - 1, page, ahead);
-      page = next;
+      const Pages next = look_up(t + S::kStages);
+      issue(t + S::kStages - 1, pages, ahead);
+      pages = next;
       stage = stage + 1 == S::kStages ? 0 : stage + 1;
       ahead = ahead + 1 == S::kStages ? 0 : ahead + 1;
     }
@@ -398,20 +492,23 @@ __global__ void __launch_bounds__(kThreads, few_blocks<D>()) attention_few_kerne
     // The warps' sums.
     float* const join = reinterpret_cast<float*>(raw);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      l[h] += __shfl_xor_sync(kFull, l[h], 1);
-      l[h] += __shfl_xor_sync(kFull, l[h], 2);
-      if (quad == 0) {
-        most[warp][g + 8 * h] = m[h];
-        weight[warp][g + 8 * h] = l[h];
+    for (int o = 0; o < NR; ++o)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * o + 2 * quad + e;
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) l[o][e] += __shfl_xor_sync(kFull, l[o][e], off);
+        if (g == 0) {
+          most[warp][r] = m[o][e];
+          weight[warp][r] = l[o][e];
+        }
+        float* row = join + (warp * kRows + r) * S::kPitch;
+        constexpr int kPiece = S::kValuePiece * 8 / BITS;  // elements
+#pragma unroll
+        for (int c = 0; c < kPairs; ++c)
+          *reinterpret_cast<float2*>(row + (8 * (2 * c / kPiece) + g) * kPiece + 2 * c % kPiece) =
+              make_float2(sums[c][o][e], sums[c][o][2 + e]);
       }
-      float* row = join + (warp * kRows + g + 8 * h) * D;
-      constexpr int kPiece = S::kValuePiece * 8 / BITS;    // elements
-#pragma unroll
-      for (int c = 0; c < kCols; ++c)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) row[(8 * (c / kPiece) + 2 * quad + e) * kPiece + c % kPiece] = sums[c][2 * h + e];
-    }
     __syncthreads();
     float* const part = slot_at(a, gridDim.x, slot_of(walk, range), kRows, D);
     for (int n = tid; n < u.rows * (D / 4); n += kThreads) {
@@ -422,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, few_blocks<D>()) attention_few_kerne
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float f = exp2_of(most[w][r] - top);
-        const float4 four = *reinterpret_cast<const float4*>(join + (w * kRows + r) * D + d);
+        const float4 four = *reinterpret_cast<const float4*>(join + (w * kRows + r) * S::kPitch + d);
         sum = fmaf(weight[w][r], f, sum);
         v[0] = fmaf(four.x, f, v[0]);
         v[1] = fmaf(four.y, f, v[1]);
@@ -484,18 +581,15 @@ __global__ void __launch_bounds__(128) attention_join_kernel(const AttentionArgs
   }
 }
 
-// Up to as many rows a sequence this kernel runs, for more attn_many.cu's.
-constexpr int64_t kFewRows = 64;
-
-template <int D, int BITS>
+template <int D, int BITS, int NR>
 cudaError_t launch(const AttentionArgs& a, int sms, cudaStream_t s) {
-  using S = Shape<D, BITS>;
+  using S = Few<D, BITS, NR>;
   static OncePerDevice once;
   const cudaError_t e = once.run([] {
-    return cudaFuncSetAttribute(attention_few_kernel<D, BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
+    return cudaFuncSetAttribute(attention_few_kernel<D, BITS, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
   });
   if (e != cudaSuccess) return e;
-  const int blocks = few_blocks<D>() * sms;
+  const int blocks = S::kBlocks * sms;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3(kThreads);
@@ -504,8 +598,30 @@ cudaError_t launch(const AttentionArgs& a, int sms, cudaStream_t s) {
   cudaLaunchAttribute overlapped = overlapped_launch();
   cfg.attrs = &overlapped;
   cfg.numAttrs = 1;
-  const cudaError_t e2 = cudaLaunchKernelEx(&cfg, attention_few_kernel<D, BITS>, a, (int)vector_rows(a.out));
-  return e2 != cudaSuccess ? e2 : launch_join(a, blocks, kRows, s);
+  const cudaError_t e2 = cudaLaunchKernelEx(&cfg, attention_few_kernel<D, BITS, NR>, a, (int)vector_rows(a.out));
+  return e2 != cudaSuccess ? e2 : launch_join(a, blocks, S::kRows, s);
+}
+template <int D, int NR>
+cudaError_t launch(const AttentionArgs& a, int sms, cudaStream_t s) {
+  return a.cache.bits == 4 ? launch<D, 4, NR>(a, sms, s) : launch<D, 8, NR>(a, sms, s);
+}
+template <int D>
+cudaError_t launch(const AttentionArgs& a, int64_t rows, int sms, cudaStream_t s) {
+  if (rows <= 8) return launch<D, 1>(a, sms, s);
+  // (sums of 32 rows of 256 do not fit registers)
+  if (rows <= 16 || D == 256) return launch<D, 2>(a, sms, s);
+  return launch<D, D == 256 ? 2 : 4>(a, sms, s);
+}
+template <int D, int NR>
+int64_t bytes(int sms) {
+  constexpr int kMost = Few<D, 4, NR>::kBlocks > Few<D, 8, NR>::kBlocks ? Few<D, 4, NR>::kBlocks : Few<D, 8, NR>::kBlocks;
+  return workspace_bytes(kMost * sms, 8 * NR, D);
+}
+template <int D>
+int64_t bytes(int sms) {
+  const int64_t one = bytes<D, 1>(sms), two = bytes<D, 2>(sms), four = bytes<D, D == 256 ? 2 : 4>(sms);
+  const int64_t most = one > two ? one : two;
+  return most > four ? most : four;
 }
 
 }  // namespace
@@ -521,17 +637,20 @@ cudaError_t launch_join(const AttentionArgs& a, int blocks, int rows, cudaStream
   return cudaLaunchKernelEx(&cfg, attention_join_kernel, a, blocks, rows, (int)vector_rows(a.out));
 }
 
+// Up to as many rows a sequence this file's kernels run, for more attn_many.cu's.
+constexpr int64_t kFewRows = 64;
+
 cudaError_t launch_attention(const AttentionArgs& a, int sms, cudaStream_t s) {
-  // Rows of an average sequence; which kernel runs changes no result beyond rounding.
-  const int64_t rows = (int64_t)a.batch.tokens * a.group / a.batch.sequences;
+  // Rows of an average sequence, rounded up; which kernel runs changes no result beyond rounding.
+  const int64_t rows = ((int64_t)a.batch.tokens * a.group + a.batch.sequences - 1) / a.batch.sequences;
   if (rows > kFewRows) return launch_attention_many(a, sms, s);
-  const bool four = a.cache.bits == 4;
-  if (a.cache.head_dim == 64) return four ? launch<64, 4>(a, sms, s) : launch<64, 8>(a, sms, s);
-  if (a.cache.head_dim == 128) return four ? launch<128, 4>(a, sms, s) : launch<128, 8>(a, sms, s);
-  return four ? launch<256, 4>(a, sms, s) : launch<256, 8>(a, sms, s);
+  if (a.cache.head_dim == 64) return launch<64>(a, rows, sms, s);
+  if (a.cache.head_dim == 128) return launch<128>(a, rows, sms, s);
+  return launch<256>(a, rows, sms, s);
 }
 int64_t attention_bytes(int head_dim, int sms) {
-  const int64_t few = workspace_bytes((head_dim == 256 ? few_blocks<256>() : few_blocks<128>()) * sms, kRows, head_dim), many = attention_many_bytes(head_dim, sms);
+  const int64_t few = head_dim == 64 ? bytes<64>(sms) : head_dim == 128 ? bytes<128>(sms) : bytes<256>(sms);
+  const int64_t many = attention_many_bytes(head_dim, sms);
   return few > many ? few : many;
 }
 StatusWord attn_few_status() { return {read_status, clear_status_bits}; }
