@@ -89,11 +89,16 @@ struct Range {
   int sequence;                          // that has `begin`
   int64_t before;                        // tiles of the sequences before it
   int64_t each;                          // tiles of a head of that sequence
+  Sequence s;                            // that sequence
 };
-__device__ __forceinline__ int64_t range_begin(int64_t total, int block, int blocks) { return total * block / blocks; }
+// total * block / blocks; in 32 bits where they do (a division in 64 takes five times as long).
+__device__ __forceinline__ int64_t divided(int64_t a, int64_t b) {
+  return (uint64_t)(a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+__device__ __forceinline__ int64_t range_begin(int64_t total, int block, int blocks) { return divided(total * block, blocks); }
 // The block whose range has a tile (the last that begins at or before it).
 __device__ __forceinline__ int block_of(int64_t total, int64_t tile, int blocks) {
-  return (int)(((tile + 1) * blocks - 1) / total);
+  return (int)divided((tile + 1) * blocks - 1, total);
 }
 
 // Of a whole block of THREADS threads.  LEAST: tiles that a block has at least
@@ -103,6 +108,39 @@ __device__ __forceinline__ Range block_range(const AttentionArgs& a, int64_t* sh
   constexpr int kWarps = THREADS / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.batch.sequences;
   Range r;
+  r.s = {0, 0, 0, 0, 0};
+  auto divide = [&]() {
+    r.blocks = r.total < (int64_t)gridDim.x * LEAST ? (int)((r.total + LEAST - 1) / LEAST) : (int)gridDim.x;
+    const int c = (int)blockIdx.x < r.blocks ? blockIdx.x : r.blocks;
+    r.begin = r.blocks ? range_begin(r.total, c, r.blocks) : 0;
+    r.end = c < r.blocks ? range_begin(r.total, c + 1, r.blocks) : r.begin;
+    r.sequence = 0;
+    r.before = 0;
+    r.each = 1;
+  };
+  if (n <= 32) {                         // each warp for itself, a lane a sequence
+    if (lane < n) r.s = sequence_of(a.batch, a.cache.page_shift, lane, bad);
+    const int64_t each = sequence_tiles<R, TILE>(a, r.s, lane), mine = each * a.cache.heads;
+    int64_t prefix = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t other = __shfl_up_sync(kFull, prefix, off);
+      if (lane >= off) prefix += other;
+    }
+    r.total = __shfl_sync(kFull, prefix, 31);
+    divide();
+    if (r.begin == r.end) return r;
+    const int owner = __ffs(__ballot_sync(kFull, prefix > r.begin)) - 1;
+    r.sequence = owner;
+    r.before = __shfl_sync(kFull, prefix - mine, owner);
+    r.each = __shfl_sync(kFull, each, owner);
+    r.s.row = __shfl_sync(kFull, r.s.row, owner);
+    r.s.rows = __shfl_sync(kFull, r.s.rows, owner);
+    r.s.length = __shfl_sync(kFull, r.s.length, owner);
+    r.s.keys = __shfl_sync(kFull, r.s.keys, owner);
+    r.s.place = __shfl_sync(kFull, r.s.place, owner);
+    return r;
+  }
   int64_t mine = 0, sum = 0;             // tiles of the last sequence looked at, of all that this thread has
   auto tiles_of = [&](int i, int* report) {
     Sequence s = {0, 0, 0, 0, 0};
@@ -120,13 +158,7 @@ __device__ __forceinline__ Range block_range(const AttentionArgs& a, int64_t* sh
   r.total = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) r.total += shared[w];
-  r.blocks = r.total < (int64_t)gridDim.x * LEAST ? (int)((r.total + LEAST - 1) / LEAST) : (int)gridDim.x;
-  const int c = (int)blockIdx.x < r.blocks ? blockIdx.x : r.blocks;
-  r.begin = r.blocks ? range_begin(r.total, c, r.blocks) : 0;
-  r.end = c < r.blocks ? range_begin(r.total, c + 1, r.blocks) : r.begin;
-  r.sequence = 0;
-  r.before = 0;
-  r.each = 1;
+  divide();
   if (r.begin == r.end) return r;        // the whole block
   // The sequence that has `begin`: prefix sums of THREADS sequences at a time.
   int64_t before = 0;
@@ -161,6 +193,8 @@ __device__ __forceinline__ Range block_range(const AttentionArgs& a, int64_t* sh
   r.sequence = (int)shared[kWarps];
   r.before = shared[kWarps + 1];
   r.each = shared[kWarps + 2];
+  int ignored = 0;
+  r.s = sequence_of(a.batch, a.cache.page_shift, r.sequence, &ignored);
   __syncthreads();
   return r;
 }
@@ -175,13 +209,13 @@ struct Walk {
   Unit unit;
   int j, in, take;                       // units of the head before, tiles of the unit before, tiles of it that are the block's
 
-  __device__ __forceinline__ void start(const AttentionArgs& a, const Range& r, int* bad) {
+  __device__ __forceinline__ void start(const AttentionArgs& a, const Range& r) {
     at = r.begin;
     end = r.end;
     if (at >= end) return;
     unit.sequence = r.sequence;
-    s = sequence_of(a.batch, a.cache.page_shift, r.sequence, bad);
-    unit.head = (int)((at - r.before) / r.each);
+    s = r.s;
+    unit.head = (int)divided(at - r.before, r.each);
     int64_t left = at - r.before - unit.head * r.each;
     // The unit that has this tile: a warp's lanes look at 32 at a time.
     const int lane = threadIdx.x & 31, units = units_of<R>(a, s);

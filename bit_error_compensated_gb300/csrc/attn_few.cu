@@ -184,13 +184,72 @@ __global__ void __launch_bounds__(kThreads, (Few<D, BITS, NR>::kBlocks)) attenti
   const Range range = block_range<kRows, kTile, kThreads, kLeast>(a, shared, &bad);
   const int heads = a.cache.heads, page_size = 1 << a.cache.page_shift;
   Walk<kRows, kTile> walk;
-  for (walk.start(a, range, &bad); walk.more(); walk.next(a, &bad)) {
+  for (walk.start(a, range); walk.more(); walk.next(a, &bad)) {
     const Sequence& s = walk.s;
     const Unit& u = walk.unit;
     const int tiles = walk.take;
     const bool whole = walk.whole();
 
     __syncthreads();                                       // the last unit's sums have been read
+    // Keys that all rows see, and where the last that any sees ends.
+    const int first_place = s.place + u.first / a.group, last_place = s.place + (u.first + u.rows - 1) / a.group;
+    const int all_to = keys_to(a, s, first_place), all_from = keys_from(a, last_place), end = keys_to(a, s, last_place);
+    const int key0 = (u.tile + walk.in) * kTile + kStep * warp;            // of this warp's first step
+    const int64_t values_on = (int64_t)heads << a.cache.page_shift;        // groups from a key's to its value's
+    uint32_t missing = 0;                                  // 16 keys of a stage without a page, a bit each
+    // The pages of a step's sixteens of keys (the same one where a page is larger),
+    // as the table has them: what is there is looked at a step later, since a use
+    // right away would wait for it.
+    struct Pages {
+      int of[kSubs];
+    };
+    auto look_up = [&](int t) {
+      Pages p;
+#pragma unroll
+      for (int sub = 0; sub < kSubs; ++sub) {
+        const int key = key0 + t * kTile + 16 * sub;
+        const int at = key >> a.cache.page_shift;
+        p.of[sub] = -1;
+        if (t < tiles && key < end && at < a.batch.table_pages)
+          p.of[sub] = a.batch.table[(int64_t)u.sequence * a.batch.ld_table + at];
+      }
+      return p;
+    };
+    auto issue = [&](int t, const Pages& pages, int stage) {
+#pragma unroll
+      for (int sub = 0; sub < kSubs; ++sub) {
+        const int key = key0 + t * kTile + 16 * sub, page = pages.of[sub];
+        const uint32_t bit = 1u << (stage * kSubs + sub);
+        missing &= ~bit;
+        if (page >= 0 && page < a.cache.pages) {
+          const int64_t group = group_index(a.cache, page, u.head, key & (page_size - 1));
+          const uint8_t* codes = a.cache.codes + group * S::kRowBytes + 16 * lane;
+          const uint8_t* value_codes = codes + values_on * S::kRowBytes;
+          const uint32_t base = ring + stage * S::kStage + sub * 16 * S::kRowBytes;
+          constexpr int kPieces = S::kRowBytes / 16;       // of a row; 16 rows have 32 lanes' worth of them or more
+#pragma unroll
+          for (int n = 0; n < kPieces * 16 / 32; ++n) {
+            const int piece = lane + 32 * n, r = piece / kPieces, p = piece % kPieces;
+            copy16_async(base + key_at<S::kRowBytes>(r, p), codes + 512 * n);
+            copy16_async(base + kStep * S::kRowBytes + value_at<S::kRowBytes>(value_row(r), p), value_codes + 512 * n);
+          }
+          if (lane < 8)
+            copy16_async(ring + stage * S::kStage + 2 * kStep * S::kRowBytes + (lane < 4 ? 0 : 4 * kStep) + 64 * sub + 16 * (lane & 3),
+                         a.cache.meta + group + (lane < 4 ? 0 : values_on) + 4 * (lane & 3));
+        } else {
+          missing |= bit;
+          if (t < tiles && key < end) bad |= kBadPage;
+        }
+      }
+      copies_commit();
+    };
+    // (the first copies are under way before the rows are loaded)
+    Pages pages = look_up(0);
+#pragma unroll 1
+    for (int t = 0; t < S::kStages - 1; ++t) {
+      issue(t, pages, t);
+      pages = look_up(t + 1);
+    }
     if (a.dtype == ECHO_BF16) load_queries<__nv_bfloat16, D, BITS, NR>(a, s, u, query, factor);
     else load_queries<__half, D, BITS, NR>(a, s, u, query, factor);
     if (tid < kRows) {
@@ -198,9 +257,6 @@ __global__ void __launch_bounds__(kThreads, (Few<D, BITS, NR>::kBlocks)) attenti
       // (rows past the last see all, so that they ask for nothing by themselves)
       seen[tid] = tid < u.rows ? make_int2(keys_from(a, place), keys_to(a, s, place)) : make_int2(0, 0x7FFFFFFF);
     }
-    // Keys that all rows see, and where the last that any sees ends.
-    const int first_place = s.place + u.first / a.group, last_place = s.place + (u.first + u.rows - 1) / a.group;
-    const int all_to = keys_to(a, s, first_place), all_from = keys_from(a, last_place), end = keys_to(a, s, last_place);
     __syncthreads();
     float row_scale[NR][2];                                // of rows 8 o + 2 quad and the next
 #pragma unroll
@@ -224,57 +280,6 @@ __global__ void __launch_bounds__(kThreads, (Few<D, BITS, NR>::kBlocks)) attenti
       l[o][0] = l[o][1] = 0.0f;
     }
 
-    const int key0 = (u.tile + walk.in) * kTile + kStep * warp;            // of this warp's first step
-    const int64_t values_on = (int64_t)heads << a.cache.page_shift;        // groups from a key's to its value's
-    uint32_t missing = 0;                                  // 16 keys of a stage without a page, a bit each
-    // The pages of a step's sixteens of keys (the same one where a page is larger).
-    struct Pages {
-      int of[kSubs];
-    };
-    auto look_up = [&](int t) {
-      Pages p;
-#pragma unroll
-      for (int sub = 0; sub < kSubs; ++sub) {
-        const int key = key0 + t * kTile + 16 * sub;
-        p.of[sub] = t < tiles && key < end ? page_of(a.batch, a.cache, u.sequence, key) : -1;
-      }
-      return p;
-    };
-    auto issue = [&](int t, const Pages& pages, int stage) {
-#pragma unroll
-      for (int sub = 0; sub < kSubs; ++sub) {
-        const int key = key0 + t * kTile + 16 * sub, page = pages.of[sub];
-        const uint32_t bit = 1u << (stage * kSubs + sub);
-        missing &= ~bit;
-        if (page >= 0) {
-          const int64_t group = group_index(a.cache, page, u.head, key & (page_size - 1));
-          const uint8_t* codes = a.cache.codes + group * S::kRowBytes + 16 * lane;
-          const uint8_t* value_codes = codes + values_on * S::kRowBytes;
-          const uint32_t base = ring + stage * S::kStage + sub * 16 * S::kRowBytes;
-          constexpr int kPieces = S::kRowBytes / 16;       // of a row; 16 rows have 32 lanes' worth of them or more
-#pragma unroll
-          for (int n = 0; n < kPieces * 16 / 32; ++n) {
-            const int piece = lane + 32 * n, r = piece / kPieces, p = piece % kPieces;
-            copy16_async(base + key_at<S::kRowBytes>(r, p), codes + 512 * n);
-            copy16_async(base + kStep * S::kRowBytes + value_at<S::kRowBytes>(value_row(r), p), value_codes + 512 * n);
-          }
-          if (lane < 8)
-            copy16_async(ring + stage * S::kStage + 2 * kStep * S::kRowBytes + (lane < 4 ? 0 : 4 * kStep) + 64 * sub + 16 * (lane & 3),
-                         a.cache.meta + group + (lane < 4 ? 0 : values_on) + 4 * (lane & 3));
-        } else {
-          missing |= bit;
-          if (t < tiles && key < end) bad |= kBadPage;
-        }
-      }
-      copies_commit();
-    };
-    Pages pages = look_up(0);
-#pragma unroll 1
-    for (int t = 0; t < S::kStages - 1; ++t) {
-      const Pages next = look_up(t + 1);
-      issue(t, pages, t);
-      pages = next;
-    }
     int stage = 0, ahead = S::kStages - 1;
 #pragma unroll 1
     for (int t = 0; t < tiles; ++t) {
@@ -546,38 +551,61 @@ __global__ void __launch_bounds__(kThreads, (Few<D, BITS, NR>::kBlocks)) attenti
   if (bad) report(bad);
 }
 
-// Joins the parts of the units that several blocks have had: a block for each
-// block of the first kernel, by four rows.
-__global__ void __launch_bounds__(128) attention_join_kernel(const AttentionArgs a, const int blocks, const int rows,
-                                                             const int vector_out) {
+// Joins the parts of the units that several blocks have had: blocks for each
+// block of the first kernel, which take the unit's rows in turn.  DIM / 4 threads
+// take a row's parts; where these are many, several such groups share them (one
+// after the other, the 76 parts of 32000 keys took 20 us), where they are few,
+// the groups take rows.
+constexpr int kJoiners = 256;
+template <int DIM>
+__global__ void __launch_bounds__(kJoiners) attention_join_kernel(const AttentionArgs a, const int blocks, const int rows,
+                                                                  const int vector_out) {
+  constexpr int kWide = DIM / 4, kGroups = kJoiners / kWide;
+  __shared__ float4 sums[kGroups][kWide];
+  __shared__ float most[kGroups], weight[kGroups];
   pdl_wait();
   pdl_trigger();
   const Join j = joins(a)[blockIdx.x];
   if (j.blocks == 0) return;
-  const int dim = a.cache.head_dim;
-  for (int n = blockIdx.y * 128 + threadIdx.x; n < j.rows * (dim / 4); n += 128 * gridDim.y) {
-    const int r = n / (dim / 4), d = n % (dim / 4) * 4;
-    float top = kLowest, sum = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-    for (int b = 0; b < j.blocks; ++b) {
-      const int slot = b == 0 ? j.slot : 2 * ((int)blockIdx.x + b);
-      const float* part = slot_at(a, blocks, slot, rows, dim);
-      const float m = part[rows * dim + r], l = part[rows * dim + rows + r];
-      const float4 four = *reinterpret_cast<const float4*>(part + r * dim + d);
+  const int lane = threadIdx.x % kWide, group = threadIdx.x / kWide;
+  const int wanted = j.blocks >= 16 ? 8 : j.blocks >= 6 ? 4 : 1, share = wanted < kGroups ? wanted : kGroups;
+  const int step = kGroups / share, mine = group % share;  // rows at once; this group's number among its row's
+  for (int r0 = blockIdx.y * step; r0 < j.rows; r0 += gridDim.y * step) {
+    const int r = r0 + group / share;
+    float top = kLowest, sum = 0.0f;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    auto join = [&](float m, float l, const float4& w) {
       const float t = fmaxf(top, m), f0 = exp2_of(top - t), f1 = exp2_of(m - t);
       sum = fmaf(l, f1, sum * f0);
-      v[0] = fmaf(four.x, f1, v[0] * f0);
-      v[1] = fmaf(four.y, f1, v[1] * f0);
-      v[2] = fmaf(four.z, f1, v[2] * f0);
-      v[3] = fmaf(four.w, f1, v[3] * f0);
+      v.x = fmaf(w.x, f1, v.x * f0);
+      v.y = fmaf(w.y, f1, v.y * f0);
+      v.z = fmaf(w.z, f1, v.z * f0);
+      v.w = fmaf(w.w, f1, v.w * f0);
       top = t;
+    };
+    if (r < j.rows)
+#pragma unroll 4
+      for (int b = mine; b < j.blocks; b += share) {
+        const float* part = slot_at(a, blocks, b == 0 ? j.slot : 2 * ((int)blockIdx.x + b), rows, DIM);
+        join(part[rows * DIM + r], part[rows * DIM + rows + r], reinterpret_cast<const float4*>(part + r * DIM)[lane]);
+      }
+    if (share > 1) {                                       // the whole block
+      __syncthreads();                                     // the row before has been read
+      sums[group][lane] = v;
+      if (lane == 0) {
+        most[group] = top;
+        weight[group] = sum;
+      }
+      __syncthreads();
+      if (mine != 0) continue;
+      for (int g = group + 1; g < group + share; ++g) join(most[g], weight[g], sums[g][lane]);
     }
+    if (r >= j.rows) continue;
     const int row = j.first + r, token = j.row + row / a.group, head = j.head * a.group + row % a.group;
     const float per = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] *= per;
-    store_values4(a, token * a.out.ld + head * a.out.head_stride + d, v, vector_out);
-    if (a.lse && d == 0) a.lse[(int64_t)token * a.heads + head] = sum == 0.0f ? kNone : (top + log2_of(sum)) * kLn2;
+    const float out[4] = {v.x * per, v.y * per, v.z * per, v.w * per};
+    store_values4(a, token * a.out.ld + head * a.out.head_stride + 4 * lane, out, vector_out);
+    if (a.lse && lane == 0) a.lse[(int64_t)token * a.heads + head] = sum == 0.0f ? kNone : (top + log2_of(sum)) * kLn2;
   }
 }
 
@@ -628,13 +656,17 @@ int64_t bytes(int sms) {
 
 cudaError_t launch_join(const AttentionArgs& a, int blocks, int rows, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)blocks, (unsigned)(rows / 4));
-  cfg.blockDim = dim3(128);
+  // (most of these find nothing to join: more of them, and they take as long as the joining)
+  cfg.gridDim = dim3((unsigned)blocks, rows <= 32 ? 4 : 16);
+  cfg.blockDim = dim3(kJoiners);
   cfg.stream = s;
   cudaLaunchAttribute overlapped = overlapped_launch();
   cfg.attrs = &overlapped;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attention_join_kernel, a, blocks, rows, (int)vector_rows(a.out));
+  const int vector = vector_rows(a.out);
+  if (a.cache.head_dim == 64) return cudaLaunchKernelEx(&cfg, attention_join_kernel<64>, a, blocks, rows, vector);
+  if (a.cache.head_dim == 128) return cudaLaunchKernelEx(&cfg, attention_join_kernel<128>, a, blocks, rows, vector);
+  return cudaLaunchKernelEx(&cfg, attention_join_kernel<256>, a, blocks, rows, vector);
 }
 
 // Up to as many rows a sequence this file's kernels run, for more attn_many.cu's.

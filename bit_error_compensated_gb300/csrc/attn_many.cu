@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
   int bad = 0;
   const Range range = block_range<S::kRows, KT, kThreads, 1>(a, shared, &bad);
   Walk<S::kRows, KT> walk;
-  walk.start(a, range, &bad);
+  walk.start(a, range);
   bool ok = true;
 
   if (warp >= kIssuer) {
