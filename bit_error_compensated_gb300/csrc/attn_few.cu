@@ -633,12 +633,32 @@ template <int D, int NR>
 cudaError_t launch(const AttentionArgs& a, int sms, cudaStream_t s) {
   return a.cache.bits == 4 ? launch<D, 4, NR>(a, sms, s) : launch<D, 8, NR>(a, sms, s);
 }
+// How many eights of rows a unit has: a unit's keys cost about as much as four
+// eights do by themselves, so the fewest of units * (4 + eights), among what
+// registers hold.
+template <int D>
+int eights(int64_t rows) {
+  const int known[] = {1, 2, 3, 4, 6}, most = D == 64 ? 5 : D == 128 ? 4 : 2;
+  int best = 1;
+  int64_t least = INT64_MAX;
+  for (int i = 0; i < most; ++i) {
+    const int64_t cost = (rows + 8 * known[i] - 1) / (8 * known[i]) * (4 + known[i]);
+    if (cost < least) {
+      least = cost;
+      best = known[i];
+    }
+  }
+  return best;
+}
 template <int D>
 cudaError_t launch(const AttentionArgs& a, int64_t rows, int sms, cudaStream_t s) {
-  if (rows <= 8) return launch<D, 1>(a, sms, s);
-  // (sums of 32 rows of 256 do not fit registers)
-  if (rows <= 16 || D == 256) return launch<D, 2>(a, sms, s);
-  return launch<D, D == 256 ? 2 : 4>(a, sms, s);
+  switch (eights<D>(rows)) {
+    case 1: return launch<D, 1>(a, sms, s);
+    case 2: return launch<D, 2>(a, sms, s);
+    case 3: return launch<D, D <= 128 ? 3 : 2>(a, sms, s);
+    case 4: return launch<D, D <= 128 ? 4 : 2>(a, sms, s);
+    default: return launch<D, D <= 64 ? 6 : 2>(a, sms, s);
+  }
 }
 template <int D, int NR>
 int64_t bytes(int sms) {
@@ -647,9 +667,11 @@ int64_t bytes(int sms) {
 }
 template <int D>
 int64_t bytes(int sms) {
-  const int64_t one = bytes<D, 1>(sms), two = bytes<D, 2>(sms), four = bytes<D, D == 256 ? 2 : 4>(sms);
-  const int64_t most = one > two ? one : two;
-  return most > four ? most : four;
+  int64_t most = 0;
+  for (int64_t n : {bytes<D, 1>(sms), bytes<D, 2>(sms), bytes<D, D <= 128 ? 3 : 2>(sms), bytes<D, D <= 128 ? 4 : 2>(sms),
+                    bytes<D, D <= 64 ? 6 : 2>(sms)})
+    most = n > most ? n : most;
+  return most;
 }
 
 }  // namespace

@@ -13,6 +13,7 @@ namespace {
 ECHO_STATUS_WORD
 
 constexpr int kWarps = 4;
+constexpr int64_t kManySteps = 4 * 152 * 16;      // of the machine's warps, see launch
 
 // Values [8 NL h + 8 q, + 8) of a row, h = 0, 1, as lane q of the row's NL.
 template <typename T, int NL>
@@ -32,21 +33,19 @@ __device__ __forceinline__ void load_row(const T* row, int q, bool aligned, floa
   }
 }
 
-// Which row of which token a lane works on: warps take a token's 2 * heads
-// rows in turn.
+// Which rows of which token a lane works on: warps take G steps of 32 / NL rows
+// of a token's 2 * heads.
 struct Place {
-  int token, row;                // row: head, or heads + head of the values
-  bool there;
+  int token, row;                // the first; row: head, or heads + head of the values
 };
-template <int NL>
-__device__ __forceinline__ Place place_of(int heads, int tokens, int lane) {
-  constexpr int kRows = 32 / NL;
+template <int NL, int G>
+__device__ __forceinline__ Place place_of(int heads, int lane) {
+  constexpr int kRows = 32 / NL * G;
   const int each = (2 * heads + kRows - 1) / kRows;      // warps a token
   const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   Place p;
   p.token = (int)(w / each);
   p.row = (int)(w % each) * kRows + lane / NL;
-  p.there = p.token < tokens && p.row < 2 * heads;
   return p;
 }
 
@@ -72,20 +71,23 @@ __device__ __forceinline__ bool token_place(const BatchArgs& b, int page_shift, 
   return true;
 }
 
-template <typename T, int NL>
+template <typename T, int NL, int G>
 __global__ void __launch_bounds__(32 * kWarps) append_kernel(const RowsArgs a, const int aligned) {
+  constexpr int kStep = 32 / NL;
   pdl_wait();
   pdl_trigger();
   check_starts(a.batch);
-  const int lane = threadIdx.x & 31, q = lane % NL;
-  const Place p = place_of<NL>(a.cache.heads, a.batch.tokens, lane);
+  const int lane = threadIdx.x & 31, q = lane % NL, heads = a.cache.heads;
+  const Place p = place_of<NL, G>(heads, lane);
   if (p.token >= a.batch.tokens) return;                 // the whole warp
-  float v[16] = {};
-  const bool value = p.row >= a.cache.heads;
-  const int head = p.row - (value ? a.cache.heads : 0);
-  if (p.there) {
-    const HeadsArgs& from = value ? a.v : a.k;
-    load_row<T, NL>(static_cast<const T*>(from.data) + p.token * from.ld + head * from.head_stride, q, aligned, v);
+  float v[G][16] = {};
+#pragma unroll
+  for (int i = 0; i < G; ++i) {
+    const int row = p.row + i * kStep;
+    if (row >= 2 * heads) continue;
+    const HeadsArgs& from = row >= heads ? a.v : a.k;
+    load_row<T, NL>(static_cast<const T*>(from.data) + p.token * from.ld + (row >= heads ? row - heads : row) * from.head_stride,
+                    q, aligned, v[i]);
   }
   __syncwarp();
   int sequence, place;
@@ -96,93 +98,105 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const RowsArgs a, c
     return;
   }
   const float L = a.cache.bits == 4 ? 15.0f : 255.0f;
-  float lo, hi;
-  group_range<NL>(v, lo, hi);
-  if (!p.there) return;
-  const GroupStep g = group_step(lo, hi, L);
-  const int64_t at = group_index(a.cache, page, head, place) + (value ? (int64_t)a.cache.heads << a.cache.page_shift : 0);
-  if (q == 0) {
-    a.cache.meta[at] = g.meta;
-    if (!g.finite) report(kNaNGroup);
-  }
-  uint8_t* codes = a.cache.codes + at * (2 * NL * a.cache.bits);
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t low = 0, high = 0;
-    const int first = 8 * NL * h + 8 * q;
-    if (a.cache.bits == 4) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) low |= group_code(v[8 * h + i], g, 15.0f) << (4 * i);
-      *reinterpret_cast<uint32_t*>(codes + first / 2) = low;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        low |= group_code(v[8 * h + i], g, 255.0f) << (8 * i);
-        high |= group_code(v[8 * h + 4 + i], g, 255.0f) << (8 * i);
-      }
-      *reinterpret_cast<uint2*>(codes + first) = make_uint2(low, high);
+  for (int i = 0; i < G; ++i) {
+    const int row = p.row + i * kStep;
+    if (p.row - lane / NL + i * kStep >= 2 * heads) break;               // the whole warp
+    float lo, hi;
+    group_range<NL>(v[i], lo, hi);
+    if (row >= 2 * heads) continue;
+    const GroupStep g = group_step(lo, hi, L);
+    // (the values' groups of a page follow its keys')
+    const int64_t at = group_index(a.cache, page, row, place);
+    if (q == 0) {
+      a.cache.meta[at] = g.meta;
+      if (!g.finite) report(kNaNGroup);
     }
+    uint8_t* codes = a.cache.codes + at * (2 * NL * a.cache.bits);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t low = 0, high = 0;
+      const int first = 8 * NL * h + 8 * q;
+      if (a.cache.bits == 4) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) low |= group_code(v[i][8 * h + k], g, 15.0f) << (4 * k);
+        *reinterpret_cast<uint32_t*>(codes + first / 2) = low;
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          low |= group_code(v[i][8 * h + k], g, 255.0f) << (8 * k);
+          high |= group_code(v[i][8 * h + 4 + k], g, 255.0f) << (8 * k);
+        }
+        *reinterpret_cast<uint2*>(codes + first) = make_uint2(low, high);
+      }
+    }
+    __syncwarp();
   }
 }
 
-template <typename T, int NL>
+template <typename T, int NL, int G>
 __global__ void __launch_bounds__(32 * kWarps) read_kernel(const RowsArgs a, const int aligned) {
+  constexpr int kStep = 32 / NL;
   pdl_wait();
   pdl_trigger();
   check_starts(a.batch);
-  const int lane = threadIdx.x & 31, q = lane % NL;
-  const Place p = place_of<NL>(a.cache.heads, a.batch.tokens, lane);
+  const int lane = threadIdx.x & 31, q = lane % NL, heads = a.cache.heads;
+  const Place p = place_of<NL, G>(heads, lane);
   if (p.token >= a.batch.tokens) return;                 // the whole warp
   int sequence, place;
   if (!token_place(a.batch, a.cache.page_shift, p.token, lane, &sequence, &place)) return;
   const int page = place < 0 ? -1 : page_of(a.batch, a.cache, sequence, place);
   if (page < 0 && place >= 0 && lane == 0) report(kBadPage);
-  const bool value = p.row >= a.cache.heads;
-  const int head = p.row - (value ? a.cache.heads : 0);
-  const HeadsArgs& into = value ? a.v : a.k;
-  if (!p.there || into.data == nullptr) return;
-  float s = 0.0f, z = 0.0f;
-  uint32_t word[4] = {};
-  if (page >= 0) {
-    const int64_t at = group_index(a.cache, page, head, place) + (value ? (int64_t)a.cache.heads << a.cache.page_shift : 0);
-    const uint32_t meta = a.cache.meta[at];
+  uint32_t word[G][4] = {}, meta[G] = {};
+#pragma unroll
+  for (int i = 0; i < G; ++i) {
+    const int row = p.row + i * kStep;
+    if (row >= 2 * heads || page < 0) continue;
+    const int64_t at = group_index(a.cache, page, row, place);
+    meta[i] = a.cache.meta[at];
     const uint8_t* codes = a.cache.codes + at * (2 * NL * a.cache.bits);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int first = 8 * NL * h + 8 * q;
       if (a.cache.bits == 4) {
-        word[2 * h] = *reinterpret_cast<const uint32_t*>(codes + first / 2);
+        word[i][2 * h] = *reinterpret_cast<const uint32_t*>(codes + first / 2);
       } else {
         const uint2 two = *reinterpret_cast<const uint2*>(codes + first);
-        word[2 * h] = two.x;
-        word[2 * h + 1] = two.y;
+        word[i][2 * h] = two.x;
+        word[i][2 * h + 1] = two.y;
       }
     }
-    s = meta_step(meta);
-    z = meta_zero(meta);
   }
-  T* row = static_cast<T*>(into.data) + p.token * into.ld + head * into.head_stride;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    float v[8];
+  for (int i = 0; i < G; ++i) {
+    const int row = p.row + i * kStep;
+    if (row >= 2 * heads) break;
+    const HeadsArgs& into = row >= heads ? a.v : a.k;
+    if (into.data == nullptr) continue;
+    const float s = meta_step(meta[i]), z = meta_zero(meta[i]);
+    T* to_row = static_cast<T*>(into.data) + p.token * into.ld + (row >= heads ? row - heads : row) * into.head_stride;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t c = a.cache.bits == 4 ? (word[2 * h] >> (4 * i)) & 15u : (word[2 * h + i / 4] >> (8 * (i % 4))) & 255u;
-      v[i] = __fmul_rn(s, __fsub_rn((float)c, z));       // exact: 11 and 9 bits
-    }
-    T* to = row + 8 * NL * h + 8 * q;
-    if (aligned) {
-      store_floats<T, 8>(to, v);
-    } else {
+    for (int h = 0; h < 2; ++h) {
+      float v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) to[i] = from_float<T>(v[i]);
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t c = a.cache.bits == 4 ? (word[i][2 * h] >> (4 * k)) & 15u : (word[i][2 * h + k / 4] >> (8 * (k % 4))) & 255u;
+        v[k] = __fmul_rn(s, __fsub_rn((float)c, z));     // exact: 11 and 9 bits
+      }
+      T* to = to_row + 8 * NL * h + 8 * q;
+      if (aligned) {
+        store_floats<T, 8>(to, v);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) to[k] = from_float<T>(v[k]);
+      }
     }
   }
 }
 
-template <typename T, int NL>
+template <typename T, int NL, int G>
 cudaError_t launch(const RowsArgs& a, bool append, cudaStream_t s) {
-  constexpr int kRows = 32 / NL;
+  constexpr int kRows = 32 / NL * G;
   const int64_t each = (2 * a.cache.heads + kRows - 1) / kRows;
   bool aligned = true;
   for (const HeadsArgs* h : {&a.k, &a.v})
@@ -194,8 +208,16 @@ cudaError_t launch(const RowsArgs& a, bool append, cudaStream_t s) {
   cudaLaunchAttribute overlapped = overlapped_launch();
   cfg.attrs = &overlapped;
   cfg.numAttrs = 1;
-  return append ? cudaLaunchKernelEx(&cfg, append_kernel<T, NL>, a, (int)aligned)
-                : cudaLaunchKernelEx(&cfg, read_kernel<T, NL>, a, (int)aligned);
+  return append ? cudaLaunchKernelEx(&cfg, append_kernel<T, NL, G>, a, (int)aligned)
+                : cudaLaunchKernelEx(&cfg, read_kernel<T, NL, G>, a, (int)aligned);
+}
+// Where a step a warp would fill the machine several times over, a warp takes
+// four: a token's place is looked for once for them (three loads that wait for
+// each other), and their loads are in flight together.
+template <typename T, int NL>
+cudaError_t launch(const RowsArgs& a, bool append, cudaStream_t s) {
+  const int64_t steps = (int64_t)a.batch.tokens * ((2 * a.cache.heads + 32 / NL - 1) / (32 / NL));
+  return steps > kManySteps ? launch<T, NL, 4>(a, append, s) : launch<T, NL, 1>(a, append, s);
 }
 template <typename T>
 cudaError_t launch(const RowsArgs& a, bool append, cudaStream_t s) {
