@@ -115,18 +115,16 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const RowsArgs a, c
     uint8_t* codes = a.cache.codes + at * (2 * NL * a.cache.bits);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      uint32_t low = 0, high = 0;
       const int first = 8 * NL * h + 8 * q;
+      float eight[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) eight[k] = v[i][8 * h + k];
+      uint32_t low, high;
       if (a.cache.bits == 4) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) low |= group_code(v[i][8 * h + k], g, 15.0f) << (4 * k);
-        *reinterpret_cast<uint32_t*>(codes + first / 2) = low;
+        group_codes8<4>(eight, g, low, high);
+        *reinterpret_cast<uint32_t*>(codes + first / 2) = low | high << 16;
       } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          low |= group_code(v[i][8 * h + k], g, 255.0f) << (8 * k);
-          high |= group_code(v[i][8 * h + 4 + k], g, 255.0f) << (8 * k);
-        }
+        group_codes8<8>(eight, g, low, high);
         *reinterpret_cast<uint2*>(codes + first) = make_uint2(low, high);
       }
     }

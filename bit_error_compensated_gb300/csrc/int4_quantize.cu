@@ -56,10 +56,13 @@ __global__ void __launch_bounds__(32 * kWarps) quantize_weights_kernel(const Wei
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int first = 8 * NL * h + 8 * q;
-    uint32_t codes = 0;
+    float eight[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (first + i < here) codes |= group_code(v[8 * h + i], g, 15.0f) << (4 * i);
+    for (int i = 0; i < 8; ++i) eight[i] = v[8 * h + i];
+    uint32_t low, high;
+    group_codes8<4>(eight, g, low, high);
+    uint32_t codes = low | high << 16;
+    if (here - first < 8) codes &= here > first ? (1u << (4 * (here - first))) - 1 : 0;       // behind the row's end: 0
     if (words && first + 8 <= here) {
       *reinterpret_cast<uint32_t*>(to + first / 2) = codes;
     } else {

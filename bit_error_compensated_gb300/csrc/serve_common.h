@@ -206,10 +206,34 @@ __device__ __forceinline__ GroupStep group_step(float lo, float hi, float L) {
   }
   return g;
 }
-__device__ __forceinline__ uint32_t group_code(float v, const GroupStep& g, float L) {
-  if (!g.finite) return 0;
-  const float c = __fadd_rn(exact_rint(v, g.s, g.inv), g.zf);
-  return (uint32_t)__float2int_rn(fminf(fmaxf(c, 0.0f), L));
+// Codes of 8 values, packed as by pack8.  Quotients come from the product with
+// inv unless one of the 8 lies near a half.  v >= lo, so rint(v / s) >= -z
+// without a clamp (rint is monotonic and odd); only the upper one is applied.
+template <int BITS>
+__device__ __forceinline__ void group_codes8(const float (&v)[8], const GroupStep& g, uint32_t& w0, uint32_t& w1) {
+  constexpr float L = BITS == 4 ? 15.0f : 255.0f, M = 12582912.0f;        // 1.5 * 2^23, see rint_small
+  float t[8], r[8], e[8], c[8];
+  mul_ns<8>(t, v, g.inv);
+#pragma unroll
+  for (int k = 0; k < 8; k += 2) {
+    add2(r[k], r[k + 1], t[k], t[k + 1], M, M);
+    sub2(r[k], r[k + 1], r[k], r[k + 1], M, M);
+  }
+  sub_n<8>(e, t, r);
+  float off = max3(fabsf(e[0]), fabsf(e[1]), fabsf(e[2]));
+  off = max3(off, fabsf(e[3]), fabsf(e[4]));
+  off = max3(off, fabsf(e[5]), fabsf(e[6]));
+  off = fmaxf(off, fabsf(e[7]));
+  if (off >= kFastRintLimit)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) r[k] = exact_rint(v[k], g.s, g.inv);
+  const float most = __fsub_rn(L, g.zf);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) c[k] = fminf(r[k], most);
+#pragma unroll
+  for (int k = 0; k < 8; k += 2) add2(c[k], c[k + 1], c[k], c[k + 1], g.zf, g.zf);
+  pack8<BITS>(c, w0, w1);
+  if (!g.finite) w0 = w1 = 0;
 }
 __device__ __forceinline__ float meta_step(uint32_t meta) {
   return __half2float(__ushort_as_half((unsigned short)(meta & 0xFFFFu)));
