@@ -91,10 +91,6 @@ struct Range {
   int64_t each;                          // tiles of a head of that sequence
   Sequence s;                            // that sequence
 };
-// total * block / blocks; in 32 bits where they do (a division in 64 takes five times as long).
-__device__ __forceinline__ int64_t divided(int64_t a, int64_t b) {
-  return (uint64_t)(a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
-}
 __device__ __forceinline__ int64_t range_begin(int64_t total, int block, int blocks) { return divided(total * block, blocks); }
 // The block whose range has a tile (the last that begins at or before it).
 __device__ __forceinline__ int block_of(int64_t total, int64_t tile, int blocks) {

@@ -44,8 +44,8 @@ __device__ __forceinline__ Place place_of(int heads, int lane) {
   const int each = (2 * heads + kRows - 1) / kRows;      // warps a token
   const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   Place p;
-  p.token = (int)(w / each);
-  p.row = (int)(w % each) * kRows + lane / NL;
+  p.token = (int)divided(w, each);
+  p.row = (int)(w - (int64_t)p.token * each) * kRows + lane / NL;
   return p;
 }
 
@@ -215,7 +215,7 @@ cudaError_t launch(const RowsArgs& a, bool append, cudaStream_t s) {
 template <typename T, int NL>
 cudaError_t launch(const RowsArgs& a, bool append, cudaStream_t s) {
   const int64_t steps = (int64_t)a.batch.tokens * ((2 * a.cache.heads + 32 / NL - 1) / (32 / NL));
-  return steps > kManySteps ? launch<T, NL, 4>(a, append, s) : launch<T, NL, 1>(a, append, s);
+  return steps > kManySteps ? launch<T, NL, 2>(a, append, s) : launch<T, NL, 1>(a, append, s);
 }
 template <typename T>
 cudaError_t launch(const RowsArgs& a, bool append, cudaStream_t s) {

@@ -149,7 +149,7 @@ __device__ __forceinline__ void load_tokens(const T* row, int64_t k, int64_t dep
 // window, a thread's (a window is 32 WORDS codes of one group); DEEP: windows
 // loaded at once.
 template <typename T, int OCTETS, int TALL, int WORDS, int DEEP, bool ALIGNED>
-__global__ void __launch_bounds__(32 * kWarps) linear4_kernel(const Linear4Args p) {
+__global__ void __launch_bounds__(32 * kWarps, 4) linear4_kernel(const Linear4Args p) {
   constexpr int kRows = 16 * TALL, kCols = 8 * OCTETS, kWindow = 32 * WORDS, kParts = parts<T>();
   __shared__ float total[kWarps][kCols][kRows + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, quad = lane & 3;
@@ -195,6 +195,18 @@ __global__ void __launch_bounds__(32 * kWarps) linear4_kernel(const Linear4Args 
         word[d][i] = there ? load_free4(meta[i] + window * kWindow / p.group) : 0;
       }
     }
+    // The tokens' loads follow the codes', before any of them is used (16-bit
+    // ones: three parts of fp32 ones would not fit registers).
+    constexpr bool kEarly = sizeof(T) == 2;
+    uint32_t early[kEarly ? DEEP : 1][WORDS][OCTETS][kParts][4];
+    if constexpr (kEarly)
+#pragma unroll
+      for (int d = 0; d < DEEP; ++d)
+#pragma unroll
+        for (int n = 0; n < WORDS; ++n)
+#pragma unroll
+          for (int o = 0; o < OCTETS; ++o)
+            load_tokens<T, ALIGNED>(x[o], (first + d * kWarps) * kWindow + 8 * (WORDS * quad + n), p.depth, early[d][n][o]);
 #pragma unroll
     for (int d = 0; d < DEEP; ++d) {
       const int64_t k = (first + d * kWarps) * kWindow + 8 * WORDS * quad;
@@ -214,7 +226,12 @@ __global__ void __launch_bounds__(32 * kWarps) linear4_kernel(const Linear4Args 
 #pragma unroll
         for (int o = 0; o < OCTETS; ++o) {
           uint32_t b[kParts][4];
-          load_tokens<T, ALIGNED>(x[o], k + 8 * n, p.depth, b);
+          if constexpr (kEarly) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) b[0][i] = early[d][n][o][0][i];
+          } else {
+            load_tokens<T, ALIGNED>(x[o], k + 8 * n, p.depth, b);
+          }
           __syncwarp();                                    // a row's ragged end parts the lanes; matrix instructions want them together
 #pragma unroll
           for (int q = 0; q < kParts; ++q)
@@ -435,7 +452,7 @@ cudaError_t launch_tiled(const Linear4Args& p, int sms, cudaStream_t s) {
 }
 template <typename T, int WORDS>
 cudaError_t launch(const Linear4Args& p, int sms, cudaStream_t s) {
-  if (p.tokens <= 8) return launch_direct<T, 1, 1, WORDS, 4>(p, s);
+  if (p.tokens <= 8) return launch_direct<T, 1, 1, WORDS, 1>(p, s);
   if (p.tokens <= 16) return launch_tiled<T, 2, WORDS>(p, sms, s);
   return launch_tiled<T, sizeof(T) == 4 ? 2 : 4, WORDS>(p, sms, s);      // (three parts of fp32 tokens: 16 at once)
 }

@@ -13,70 +13,82 @@ ECHO_STATUS_WORD
 
 constexpr int kWarps = 8;
 
-template <typename T, int NL>
+// G: steps of 32 / NL groups, one after the other in a row, that a warp takes
+// (their loads are in flight together).
+template <typename T, int NL, int G>
 __global__ void __launch_bounds__(32 * kWarps) quantize_weights_kernel(const WeightsArgs a, const int aligned) {
   constexpr int kGroups = 32 / NL, kGroup = 16 * NL;
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, q = lane % NL;
-  const int64_t groups = (a.depth + kGroup - 1) / kGroup, each = (groups + kGroups - 1) / kGroups;   // warps a row
+  const int groups = (int)((a.depth + kGroup - 1) / kGroup), each = (groups + kGroups * G - 1) / (kGroups * G);   // warps a row
   const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int64_t row = w / each;
+  const int64_t row = divided(w, each);
   if (row >= a.ranks * a.channels) return;               // the whole warp
-  const int64_t rank = row / a.channels, channel = row - rank * a.channels;
-  const int64_t group = w % each * kGroups + lane / NL, k0 = group * kGroup;
-  const T* from = static_cast<const T*>(a.w) + rank * a.rank_w + channel * a.ld_w + k0;
-  const int64_t here = a.depth - k0;                     // values of this group, if fewer than all
-  float v[16] = {};
+  const int64_t rank = divided(row, a.channels), channel = row - rank * a.channels;
+  const int64_t group0 = (w - row * each) * kGroups * G + lane / NL;
+  const T* from = static_cast<const T*>(a.w) + rank * a.rank_w + channel * a.ld_w;
+  float v[G][16] = {};
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int first = 8 * NL * h + 8 * q;
-    if (aligned && first + 8 <= here) {
-      float f[8];
-      to_floats<T, 8>(load_pack<T, 8>(from + first), f);
+  for (int i = 0; i < G; ++i) {
+    const int64_t k0 = (group0 + i * kGroups) * kGroup, here = a.depth - k0;             // values of this group, if fewer than all
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[8 * h + i] = f[i];
-    } else {
+    for (int h = 0; h < 2; ++h) {
+      const int first = 8 * NL * h + 8 * q;
+      if (aligned && first + 8 <= here) {
+        float f[8];
+        to_floats<T, 8>(load_pack<T, 8>(from + k0 + first), f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (first + i < here) v[8 * h + i] = to_float(from[first + i]);
+        for (int k = 0; k < 8; ++k) v[i][8 * h + k] = f[k];
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (first + k < here) v[i][8 * h + k] = to_float(from[k0 + first + k]);
+      }
     }
   }
   __syncwarp();
-  float lo, hi;
-  group_range<NL>(v, lo, hi);
-  if (here <= 0) return;
-  const GroupStep g = group_step(lo, hi, 15.0f);
-  if (q == 0) {
-    a.meta[rank * a.rank_meta + channel * a.ld_meta + group] = g.meta;
-    if (!g.finite) report(kNaNGroup);
-  }
-  uint8_t* to = a.codes + rank * a.rank_codes + channel * a.ld_codes + k0 / 2;
-  const bool words = ((uintptr_t)to & 3) == 0;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int first = 8 * NL * h + 8 * q;
-    float eight[8];
+  for (int i = 0; i < G; ++i) {
+    const int64_t group = group0 + i * kGroups, k0 = group * kGroup, here = a.depth - k0;
+    float lo, hi;
+    group_range<NL>(v[i], lo, hi);
+    if (here > 0) {
+      const GroupStep g = group_step(lo, hi, 15.0f);
+      if (q == 0) {
+        a.meta[rank * a.rank_meta + channel * a.ld_meta + group] = g.meta;
+        if (!g.finite) report(kNaNGroup);
+      }
+      uint8_t* to = a.codes + rank * a.rank_codes + channel * a.ld_codes + k0 / 2;
+      const bool words = ((uintptr_t)to & 3) == 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) eight[i] = v[8 * h + i];
-    uint32_t low, high;
-    group_codes8<4>(eight, g, low, high);
-    uint32_t codes = low | high << 16;
-    if (here - first < 8) codes &= here > first ? (1u << (4 * (here - first))) - 1 : 0;       // behind the row's end: 0
-    if (words && first + 8 <= here) {
-      *reinterpret_cast<uint32_t*>(to + first / 2) = codes;
-    } else {
+      for (int h = 0; h < 2; ++h) {
+        const int first = 8 * NL * h + 8 * q;
+        float eight[8];
 #pragma unroll
-      for (int i = 0; i < 8; i += 2)
-        if (first + i < here) to[(first + i) / 2] = (uint8_t)(codes >> (4 * i));
+        for (int k = 0; k < 8; ++k) eight[k] = v[i][8 * h + k];
+        uint32_t low, high;
+        group_codes8<4>(eight, g, low, high);
+        uint32_t codes = low | high << 16;
+        if (here - first < 8) codes &= here > first ? (1u << (4 * (here - first))) - 1 : 0;     // behind the row's end: 0
+        if (words && first + 8 <= here) {
+          *reinterpret_cast<uint32_t*>(to + first / 2) = codes;
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; k += 2)
+            if (first + k < here) to[(first + k) / 2] = (uint8_t)(codes >> (4 * k));
+        }
+      }
     }
+    __syncwarp();
   }
 }
 
 template <typename T, int NL>
 cudaError_t launch(const WeightsArgs& a, cudaStream_t s) {
-  constexpr int kGroups = 32 / NL, kGroup = 16 * NL;
-  const int64_t groups = (a.depth + kGroup - 1) / kGroup, warps = (groups + kGroups - 1) / kGroups * a.ranks * a.channels;
+  constexpr int G = 1, kGroups = 32 / NL, kGroup = 16 * NL;
+  const int64_t groups = (a.depth + kGroup - 1) / kGroup;
+  const int64_t warps = (groups + kGroups * G - 1) / (kGroups * G) * a.ranks * a.channels;
   const int64_t in16 = 16 / (int64_t)sizeof(T);
   const bool aligned = on_boundary(a.w, 16) && (a.channels == 1 || a.ld_w % in16 == 0) && (a.ranks == 1 || a.rank_w % in16 == 0);
   cudaLaunchConfig_t cfg = {};
@@ -86,7 +98,7 @@ cudaError_t launch(const WeightsArgs& a, cudaStream_t s) {
   cudaLaunchAttribute overlapped = overlapped_launch();
   cfg.attrs = &overlapped;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, quantize_weights_kernel<T, NL>, a, (int)aligned);
+  return cudaLaunchKernelEx(&cfg, quantize_weights_kernel<T, NL, G>, a, (int)aligned);
 }
 template <typename T>
 cudaError_t launch(const WeightsArgs& a, cudaStream_t s) {

@@ -107,6 +107,12 @@ StatusWord weights_status();
   }                                                                                   \
   __device__ __forceinline__ void report(int bits) { atomicOr(&g_status, bits); }
 
+// a / b of no negative numbers, in 32 bits where they fit (a division in 64 takes
+// five times as long).
+__device__ __forceinline__ int64_t divided(int64_t a, int64_t b) {
+  return (uint64_t)(a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
 // ------------------------------------------------------------------ batches
 // One sequence of a batch: its rows of the token tensors and its tokens in the
 // cache, as far as the arrays make sense.
@@ -162,7 +168,7 @@ __device__ __forceinline__ int64_t group_index(const CacheArgs& c, int page, int
 }
 
 // ------------------------------------------------------------------- groups
-// The least fp16 number s with s * L >= hi - lo, exactly: from the rounded
+// The least fp16 number s with s * L >= hi - lo, exactly: from an approximate
 // quotient, which is off by one step at most.  s * L has 19 bits, so it is
 // exact in fp32; hi - lo is d + e exactly, and s * L - d is exact because the
 // two are near each other.
@@ -174,8 +180,9 @@ struct GroupStep {
   uint32_t meta;
   bool finite;
 };
-// rint(v / s) with the quotient exact, for |v / s| < 256 and inv = fl(1 / s):
-// where the product with inv lies near a half, v is compared with s times that
+// rint(v / s) with the quotient exact, for |v / s| < 256 and inv within 2^-23 of
+// 1 / s (so the product is within 256 * 3 * 2^-24 of the quotient, less than
+// 2^-13): where the product with inv lies near a half, v is compared with s times that
 // half, which has 21 bits at most and so is exact.
 __device__ __forceinline__ float exact_rint(float v, float s, float inv) {
   const float t = __fmul_rn(v, inv), r = rint_small(t);
@@ -188,7 +195,7 @@ __device__ __forceinline__ GroupStep group_step(float lo, float hi, float L) {
   GroupStep g;
   const float d = __fsub_rn(hi, lo), b = -lo, bb = __fsub_rn(d, hi);
   const float err = __fadd_rn(__fsub_rn(hi, __fsub_rn(d, bb)), __fsub_rn(b, bb));   // hi - lo is d + err
-  unsigned short s = __half_as_ushort(__float2half_ru(__fdiv_rn(d, L)));
+  unsigned short s = __half_as_ushort(__float2half_ru(__fmul_rn(d, 1.0f / L)));
   g.finite = isfinite(d) && s < 0x7C00;
   if (g.finite) {
     if (!covers(s, L, d, err)) ++s;
@@ -197,7 +204,7 @@ __device__ __forceinline__ GroupStep group_step(float lo, float hi, float L) {
     g.finite = s < 0x7C00;
   }
   g.s = __half2float(__ushort_as_half(s));
-  g.inv = __frcp_rn(g.s);
+  asm("rcp.approx.f32 %0, %1;" : "=f"(g.inv) : "f"(g.s));
   g.zf = 0.0f;
   g.meta = 0x7E00u;              // a step of NaN
   if (g.finite) {
