@@ -144,12 +144,12 @@ __device__ __forceinline__ void load_tokens(const T* row, int64_t k, int64_t dep
   }
 }
 
-// At most 8 tokens: each warp loads what it needs of them by itself.
+// Few tokens: each warp loads what it needs of them by itself.
 // OCTETS: of tokens; TALL: 16-channel parts of a block; WORDS: of a row's
 // window, a thread's (a window is 32 WORDS codes of one group); DEEP: windows
 // loaded at once.
 template <typename T, int OCTETS, int TALL, int WORDS, int DEEP, bool ALIGNED>
-__global__ void __launch_bounds__(32 * kWarps, 4) linear4_kernel(const Linear4Args p) {
+__global__ void __launch_bounds__(32 * kWarps, OCTETS * TALL == 1 ? 4 : OCTETS * TALL == 2 ? 3 : 2) linear4_kernel(const Linear4Args p) {
   constexpr int kRows = 16 * TALL, kCols = 8 * OCTETS, kWindow = 32 * WORDS, kParts = parts<T>();
   __shared__ float total[kWarps][kCols][kRows + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, quad = lane & 3;
@@ -429,12 +429,12 @@ cudaError_t launch_tiled(const Linear4Args& p, int sms, cudaStream_t s) {
                                                            cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
   });
   if (e != cudaSuccess) return e;
-  // The depth is shared by as many blocks, up to 8, as are needed for two an SM
-  // and leave each four windows.
+  // The depth is shared by as many blocks, up to 8, as all run at once (two an
+  // SM) and leave each four windows.
   const int64_t blocks = (p.channels + S::kChannels - 1) / S::kChannels, windows = (p.depth + S::kWindow - 1) / S::kWindow;
   const int64_t columns = (p.tokens + S::kCols - 1) / S::kCols;
   int split = 1;
-  while (split < 8 && blocks * columns * p.ranks * split < 2 * sms && windows >= 8 * split) split *= 2;
+  while (split < 8 && blocks * columns * p.ranks * split <= sms && windows >= 8 * split) split *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(blocks * split), (unsigned)columns, (unsigned)p.ranks);
   cfg.blockDim = dim3(32 * kWarps);
@@ -452,7 +452,17 @@ cudaError_t launch_tiled(const Linear4Args& p, int sms, cudaStream_t s) {
 }
 template <typename T, int WORDS>
 cudaError_t launch(const Linear4Args& p, int sms, cudaStream_t s) {
-  if (p.tokens <= 8) return launch_direct<T, 1, 1, WORDS, 1>(p, s);
+  // 32 channels a block halve the loads of the tokens' elements, if there are
+  // blocks enough (one token, 14336 x 4096: 11.4 us, with 16 channels 13.9; 7 x
+  // 1111 x 2051: 5.6 us with 16, 8.1 with 32).  Of 9 to 16 tokens those loads
+  // are as many as the codes' in each warp: it is only where the blocks all run
+  // at once that no shared memory is faster (16 x 4096 x 4096: 7.5 us, through
+  // shared memory 9.8; 16 x 14336 x 4096: 23, 21).
+  const int64_t blocks = (p.channels + 31) / 32 * p.ranks;
+  const bool many = blocks * 4 >= 3 * sms;
+  if (p.tokens <= 8) return many ? launch_direct<T, 1, 2, WORDS, 1>(p, s) : launch_direct<T, 1, 1, WORDS, 1>(p, s);
+  if (p.tokens <= 16 && blocks <= 2 * sms)
+    return many ? launch_direct<T, 2, 2, WORDS, 1>(p, s) : launch_direct<T, 2, 1, WORDS, 1>(p, s);
   if (p.tokens <= 16) return launch_tiled<T, 2, WORDS>(p, sms, s);
   return launch_tiled<T, sizeof(T) == 4 ? 2 : 4, WORDS>(p, sms, s);      // (three parts of fp32 tokens: 16 at once)
 }

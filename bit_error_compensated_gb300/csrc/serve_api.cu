@@ -189,21 +189,20 @@ int echo_attention(const echo_cache* cache, const echo_batch* batch, int64_t hea
   ECHO_TRY(check_heads(q, tokens, heads, dim, 2, false));
   ECHO_TRY(check_heads(out, tokens, heads, dim, 2, true));
   if (!on_boundary(lse, 4)) return ECHO_ERR_ALIGN;
+  Region r[9];
+  int n = add_cache(cache, r);
+  n += add_batch(batch, r + n);
+  r[n++] = of_heads(q, tokens, heads, dim, 2);
+  for (const Region& w : {of_heads(out, tokens, heads, dim, 2), region(lse, 1, tokens * heads, tokens * heads, 4)}) {
+    if (!clear_of_all(w, r, n)) return ECHO_ERR_ARG;
+    r[n++] = w;
+  }
   int sms = 0;
   ECHO_OPS_CUDA(device_sms(&sms));
   const size_t need = (size_t)attention_bytes((int)dim, sms);
   if (workspace == nullptr || workspace_bytes < need) return ECHO_ERR_TOO_LARGE;
   if (!on_boundary(workspace, 16)) return ECHO_ERR_ALIGN;
-  Region r[9];
-  int n = add_cache(cache, r);
-  n += add_batch(batch, r + n);
-  r[n++] = of_heads(q, tokens, heads, dim, 2);
-  const Region written[3] = {of_heads(out, tokens, heads, dim, 2), region(lse, 1, tokens * heads, tokens * heads, 4),
-                             region(workspace, 1, (int64_t)need, (int64_t)need, 1)};
-  for (const Region& w : written) {
-    if (!clear_of_all(w, r, n)) return ECHO_ERR_ARG;
-    r[n++] = w;
-  }
+  if (!clear_of_all(region(workspace, 1, (int64_t)need, (int64_t)need, 1), r, n)) return ECHO_ERR_ARG;
   AttentionArgs a;
   std::memset(&a, 0, sizeof(a));
   a.cache = cache_args(cache);
