@@ -341,6 +341,15 @@ __device__ __forceinline__ void store_values4(const AttentionArgs& a, int64_t at
 // Whether rows of out take 8-byte stores.
 inline bool vector_rows(const HeadsArgs& h) { return on_boundary(h.data, 8) && h.ld % 4 == 0 && h.head_stride % 4 == 0; }
 
+// Blocks that can have a tile, of `most`: a small batch is not waited for by
+// blocks that only find out that they have nothing to do.
+inline int useful_blocks(const AttentionArgs& a, int rows, int tile, int most) {
+  const int64_t units = a.cache.heads * (((int64_t)a.batch.tokens * a.group + rows - 1) / rows + a.batch.sequences);
+  const int64_t keys = (int64_t)a.batch.table_pages << a.cache.page_shift, tiles = keys / tile + 1;
+  if (units >= most || tiles >= most) return most;
+  return (int)(units * tiles < most ? units * tiles : most);
+}
+
 // Joins the parts of units that several blocks of a kernel before have had.
 cudaError_t launch_join(const AttentionArgs& a, int blocks, int rows, cudaStream_t s);
 // attn_many.cu; attn_few.cu has the rest.

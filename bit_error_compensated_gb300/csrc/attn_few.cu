@@ -617,7 +617,7 @@ cudaError_t launch(const AttentionArgs& a, int sms, cudaStream_t s) {
     return cudaFuncSetAttribute(attention_few_kernel<D, BITS, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
   });
   if (e != cudaSuccess) return e;
-  const int blocks = S::kBlocks * sms;
+  const int blocks = useful_blocks(a, S::kRows, S::kTile, S::kBlocks * sms);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3(kThreads);

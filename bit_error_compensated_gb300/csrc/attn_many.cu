@@ -821,7 +821,8 @@ cudaError_t launch(const AttentionArgs& a, int sms, cudaStream_t s) {
   });
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)sms);
+  const int blocks = useful_blocks(a, S::kRows, S::KT, sms);
+  cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = S::kBytes;
   cfg.stream = s;
@@ -830,7 +831,7 @@ cudaError_t launch(const AttentionArgs& a, int sms, cudaStream_t s) {
   cfg.numAttrs = 1;
   auto wide = [](const HeadsArgs& h) { return (int)(on_boundary(h.data, 16) && h.ld % 8 == 0 && h.head_stride % 8 == 0); };
   const cudaError_t e2 = cudaLaunchKernelEx(&cfg, attention_many_kernel<D, BITS>, a, wide(a.out), wide(a.q));
-  return e2 != cudaSuccess ? e2 : launch_join(a, sms, S::kRows, s);
+  return e2 != cudaSuccess ? e2 : launch_join(a, blocks, S::kRows, s);
 }
 
 }  // namespace
