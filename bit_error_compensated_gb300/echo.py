@@ -823,29 +823,37 @@ def _expect_heads(t, what: str, dtype, shape, device) -> bytes:
     return _HEADS.pack(t.data_ptr(), stride[0], stride[1])
 
 
-def _serving_device(cache: Cache, batch: CacheBatch, t) -> int:
+def _current_device() -> int:
+    """torch.cuda.current_device() without its checks, where torch has that."""
     import torch
-    device = torch.cuda.current_device() if t.is_cuda else -1
-    if device < 0:
+    raw = getattr(torch._C, "_cuda_getDevice", None)
+    return raw() if raw is not None and torch.cuda.is_initialized() else torch.cuda.current_device()
+
+
+def _serving_device(cache: Cache, batch: CacheBatch, t) -> int:
+    device = cache.device
+    if t.get_device() == device == batch.device and _current_device() == device:
+        return device
+    if not t.is_cuda:
         raise ValueError("tensor must be on a CUDA device")
+    current = _current_device()
     for owner, what in ((cache, "cache"), (batch, "batch")):
-        if owner.device != device:
-            raise ValueError(f"the {what} belongs to cuda:{owner.device}, but the current device is cuda:{device}")
-    return device
+        if owner.device != current:
+            raise ValueError(f"the {what} belongs to cuda:{owner.device}, but the current device is cuda:{current}")
+    raise ValueError(f"tensor on cuda:{t.get_device()}, but the call runs on cuda:{current}")
 
 
 def _cache_rows(fn, call: str, cache: Cache, batch: CacheBatch, k, v, stream) -> None:
     first = v if k is None else k
     if first is None:
         raise ValueError("k or v is needed")
-    if first.dim() != 3:
-        raise ValueError(f"k, v: shape {tuple(first.shape)}, expected (tokens, {cache.heads}, {cache.head_dim})")
-    packed = cache._pack()
-    shape, dtype = (first.shape[0], cache.heads, cache.head_dim), first.dtype
-    rows = batch._pack(shape[0])
+    shape, dtype = first.shape, first.dtype
+    if len(shape) != 3 or shape[1] != cache.heads or shape[2] != cache.head_dim:
+        raise ValueError(f"k, v: shape {tuple(shape)}, expected (tokens, {cache.heads}, {cache.head_dim})")
     code, device = _dtype_code(dtype), _serving_device(cache, batch, first)
-    at = [None if t is None else _expect_heads(t, what, dtype, shape, device) for t, what in ((k, "k"), (v, "v"))]
-    status = fn(packed, rows, code, *at, _stream(stream, device))
+    status = fn(cache._pack(), batch._pack(shape[0]), code,
+                None if k is None else _expect_heads(k, "k", dtype, shape, device),
+                None if v is None else _expect_heads(v, "v", dtype, shape, device), _stream(stream, device))
     if status:
         raise EchoError(status, call)
 
@@ -876,13 +884,12 @@ def echo_attention(cache: Cache, batch: CacheBatch, q, out, scale: float | None 
     the last tokens that a token sees (0: all up to itself); lse fp32
     [tokens][heads], contiguous, or None."""
     import torch
-    if q.dim() != 3:
-        raise ValueError(f"q: shape {tuple(q.shape)}, expected (tokens, heads, {cache.head_dim})")
-    packed, (tokens, heads, _) = cache._pack(), q.shape
-    rows = batch._pack(tokens)
-    shape, dtype = (tokens, heads, cache.head_dim), q.dtype
+    shape, dtype = q.shape, q.dtype
+    if len(shape) != 3 or shape[2] != cache.head_dim:
+        raise ValueError(f"q: shape {tuple(shape)}, expected (tokens, heads, {cache.head_dim})")
     if dtype is not torch.bfloat16 and dtype is not torch.float16:
         raise ValueError(f"q: dtype {dtype}, expected torch.bfloat16 or torch.float16")
+    tokens, heads, dim = shape
     if heads < 1 or heads % cache.heads:
         raise ValueError(f"q: {heads} heads, expected a multiple of the cache's {cache.heads}")
     device = _serving_device(cache, batch, q)
@@ -892,13 +899,25 @@ def echo_attention(cache: Cache, batch: CacheBatch, q, out, scale: float | None 
     if lse is not None:
         _expect_contiguous(lse, "lse", torch.float32, (tokens, heads), device)
         at_lse = lse.data_ptr()
-    nbytes = _lib.echo_attention_workspace_bytes(packed, rows, heads)
-    keep, at = _workspace(nbytes, q.device, stream)
-    status = _lib.echo_attention(packed, rows, heads, _dtype_code(dtype), at_q, at_out,
-                                 cache.head_dim ** -0.5 if scale is None else scale, int(causal), window, at_lse, at,
-                                 nbytes, _stream(stream, device))
+    packed, rows = cache._pack(), batch._pack(tokens)
+    nbytes = _attention_bytes.get((device, dim))             # the size depends on nothing else
+    if nbytes is None:
+        nbytes = _lib.echo_attention_workspace_bytes(packed, rows, heads)
+        if nbytes:
+            _attention_bytes[device, dim] = nbytes
+    if stream is None:
+        keep = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        at = keep.data_ptr()
+    else:
+        keep, at = _workspace(nbytes, q.device, stream)
+    status = _lib.echo_attention(packed, rows, heads, ECHO_BF16 if dtype is torch.bfloat16 else ECHO_F16, at_q, at_out,
+                                 dim ** -0.5 if scale is None else scale, causal, window, at_lse, at, nbytes,
+                                 _stream(stream, device))
     if status:
         raise EchoError(status, "echo_attention")
+
+
+_attention_bytes = {}                             # (device, head_dim) -> bytes
 
 
 def _weight_shapes(ranks: int | None, channels: int, depth: int, group: int) -> tuple:
@@ -930,7 +949,9 @@ def echo_linear_int4(x, codes, meta, out, group: int = 128, stream=None) -> None
     [ranks][tokens][channels] of one dtype, or both without ranks; x, and codes
     and meta together, may lack the ranks' dimension where all ranks share them."""
     import torch
-    device = _call_device(out)
+    device = out.get_device()
+    if device < 0 or device != _current_device():
+        device = _call_device(out)
     ranks, tokens, channels = _batch(out, "out")
     depth = x.shape[-1]
     own_x, own_w = len(x.shape) == 3, len(codes.shape) == 3
