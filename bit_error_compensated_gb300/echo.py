@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import struct
+import threading
 from pathlib import Path
 
 _LIB_PATH = Path(__file__).resolve().parent / "lib" / "libecho.so"
@@ -905,18 +906,33 @@ def echo_attention(cache: Cache, batch: CacheBatch, q, out, scale: float | None 
         nbytes = _lib.echo_attention_workspace_bytes(packed, rows, heads)
         if nbytes:
             _attention_bytes[device, dim] = nbytes
-    if stream is None:
-        keep = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        at = keep.data_ptr()
+    args = (packed, rows, heads, ECHO_BF16 if dtype is torch.bfloat16 else ECHO_F16, at_q, at_out,
+            dim ** -0.5 if scale is None else scale, causal, window, at_lse)
+    raw = _stream(stream, device)
+    if stream is None and not torch.cuda.is_current_stream_capturing():
+        with _workspace_lock:                                # a call's two kernels follow each other
+            status = _lib.echo_attention(*args, _kept_workspace(nbytes, device, raw), nbytes, raw)
     else:
         keep, at = _workspace(nbytes, q.device, stream)
-    status = _lib.echo_attention(packed, rows, heads, ECHO_BF16 if dtype is torch.bfloat16 else ECHO_F16, at_q, at_out,
-                                 dim ** -0.5 if scale is None else scale, causal, window, at_lse, at, nbytes,
-                                 _stream(stream, device))
+        status = _lib.echo_attention(*args, at, nbytes, raw)
     if status:
         raise EchoError(status, "echo_attention")
 
 
+def _kept_workspace(nbytes: int, device: int, raw: int) -> int:
+    """The address of the attention's workspace for a stream, which stays
+    allocated (40 MB at the most): with an allocation between one call's launches
+    and the next's, a call took 7 us longer.  Captured calls have their own."""
+    kept = _workspaces.get((device, raw))
+    if kept is None or kept[1] < nbytes:
+        import torch
+        buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        kept = _workspaces[device, raw] = (buf.data_ptr(), nbytes, buf)
+    return kept[0]
+
+
+_workspaces = {}                                  # (device, raw stream) -> (address, bytes, tensor)
+_workspace_lock = threading.Lock()
 _attention_bytes = {}                             # (device, head_dim) -> bytes
 
 
