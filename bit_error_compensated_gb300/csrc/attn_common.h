@@ -23,7 +23,7 @@ struct Unit {
 
 // Keys [from, to) that the row at a place sees.
 __device__ __forceinline__ int keys_to(const AttentionArgs& a, const Sequence& s, int place) {
-  if (!a.causal) return s.keys;
+  if (!a.causal) return place < 0 ? 0 : s.keys;
   return place + 1 < 0 ? 0 : (place + 1 < s.keys ? place + 1 : s.keys);
 }
 __device__ __forceinline__ int keys_from(const AttentionArgs& a, int place) {

@@ -26,10 +26,11 @@ int check_cache(const echo_cache* c) {
 
 bool empty(const echo_batch* b) { return b->sequences == 0 || b->tokens == 0; }
 
-int check_batch(const echo_batch* b) {
+int check_batch(const echo_batch* b, const echo_cache* c) {
   if (b == nullptr) return ECHO_ERR_ARG;
   if (b->sequences < 0 || b->tokens < 0 || b->table_pages < 0) return ECHO_ERR_SHAPE;
-  if (b->sequences > kMaxTokens || b->tokens > kMaxTokens || b->table_pages > INT_MAX) return ECHO_ERR_UNSUPPORTED;
+  if (b->sequences > kMaxTokens || b->tokens > kMaxTokens || b->table_pages > kMostPlaces / c->page_size)
+    return ECHO_ERR_UNSUPPORTED;
   if (empty(b)) return ECHO_OK;
   if (b->sequences > 1 && (b->ld_table < b->table_pages || b->ld_table > kMaxExtent)) return ECHO_ERR_SHAPE;
   if (b->starts == nullptr || b->lengths == nullptr || (b->table == nullptr && b->table_pages > 0)) return ECHO_ERR_ARG;
@@ -106,7 +107,7 @@ HeadsArgs heads_args(const echo_heads* h) {
 int check_rows(const echo_cache* c, const echo_batch* b, int dtype, const echo_heads* k, const echo_heads* v, bool read) {
   if (!known_dtype(dtype)) return ECHO_ERR_UNSUPPORTED;
   ECHO_TRY(check_cache(c));
-  ECHO_TRY(check_batch(b));
+  ECHO_TRY(check_batch(b, c));
   if (empty(b)) return ECHO_OK;
   const int size = elem_size(dtype);
   const echo_heads* both[2] = {k, v};
@@ -162,7 +163,7 @@ int echo_cache_read(const echo_cache* cache, const echo_batch* batch, int dtype,
 
 static int check_attention_sizes(const echo_cache* cache, const echo_batch* batch, int64_t heads) {
   ECHO_TRY(check_cache(cache));
-  ECHO_TRY(check_batch(batch));
+  ECHO_TRY(check_batch(batch, cache));
   if (heads < 1 || heads % cache->heads != 0) return ECHO_ERR_SHAPE;
   if (heads > INT_MAX / 2 || batch->tokens * heads > INT_MAX / 2) return ECHO_ERR_UNSUPPORTED;
   return ECHO_OK;
@@ -273,7 +274,15 @@ int echo_linear_int4(int64_t ranks, int64_t tokens, int64_t channels, int64_t de
   p.dtype = dtype;
   int sms = 0;
   ECHO_OPS_CUDA(device_sms(&sms));
-  ECHO_OPS_CUDA(launch_linear4(p, sms, static_cast<cudaStream_t>(stream)));
+  // (a launch has 65535 blocks of tokens at the most, of 8 to 32 each)
+  constexpr int64_t kTokens = 65535 * 8;
+  for (p.tokens = tokens; p.tokens > 0; p.tokens -= kTokens) {
+    Linear4Args some = p;
+    some.tokens = p.tokens < kTokens ? p.tokens : kTokens;
+    ECHO_OPS_CUDA(launch_linear4(some, sms, static_cast<cudaStream_t>(stream)));
+    p.x = static_cast<const char*>(p.x) + kTokens * p.ld_x * size;
+    p.out = static_cast<char*>(p.out) + kTokens * p.ld_out * size;
+  }
   return ECHO_OK;
 }
 

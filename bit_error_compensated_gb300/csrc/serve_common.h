@@ -9,6 +9,8 @@
 
 namespace echo {
 
+// Places that a table may have (sums of places stay inside 32 bits).
+constexpr int kMostPlaces = 1 << 30;
 // Bits of the status words.
 constexpr int kBadPage = 1, kBadRows = 2, kNaNGroup = 4, kGaveUp = 8;
 
@@ -118,7 +120,7 @@ __device__ __forceinline__ int64_t divided(int64_t a, int64_t b) {
 // cache, as far as the arrays make sense.
 struct Sequence {
   int row, rows;                 // first of its rows, and how many
-  int length;                    // as given (0 if negative)
+  int length;                    // as given (0 if negative, cut off far behind any table's end)
   int keys;                      // of these, that the table has room for
   int place;                     // of its first row, may be negative
 };
@@ -129,7 +131,7 @@ __device__ __forceinline__ Sequence sequence_of(const BatchArgs& b, int page_shi
   const int from = first < 0 ? 0 : first, to = last > b.tokens ? b.tokens : last;
   s.row = from;
   s.rows = to > from ? to - from : 0;
-  s.length = length < 0 ? 0 : length;
+  s.length = length < 0 ? 0 : length < kMostPlaces + (1 << 20) ? length : kMostPlaces + (1 << 20);
   const int64_t room = (int64_t)b.table_pages << page_shift;
   s.keys = s.length < room ? s.length : (int)room;
   if (s.rows > 0 && s.length > room) *bad |= kBadPage;

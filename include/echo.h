@@ -647,7 +647,7 @@ typedef struct {
   const int32_t* starts;       /* [sequences + 1], rising */
   const int32_t* lengths;      /* [sequences] */
   const int32_t* table;        /* [sequences][table_pages] */
-  int64_t table_pages;
+  int64_t table_pages;         /* times page_size 2^30 at the most (ECHO_ERR_UNSUPPORTED) */
   int64_t ld_table;            /* from one sequence's row to the next, >= table_pages */
 } echo_batch;
 

@@ -114,7 +114,7 @@ def attention(cache, q, starts, lengths, table, scale, causal=True, window=0):
             qs = q[row, h * group:(h + 1) * group].double().flatten(0, 1)
             at = place.repeat_interleave(group)[:, None]
             key = torch.arange(keys, device=q.device)
-            seen = held.there[None].expand(len(at), -1).clone()
+            seen = held.there[None] & (at >= 0)              # a token before the begin sees nothing
             if causal:
                 seen &= key <= at
                 if window:

@@ -149,3 +149,18 @@ def test_no_depth_and_no_tokens():
     codes, meta = (t[0] for t in buffers(1, 6, 64, 64))
     codes.zero_(), meta.zero_()
     echo.echo_linear_int4(torch.empty(0, 64, device="cuda"), codes, meta, torch.empty(0, 6, device="cuda"), group=64)
+
+
+def test_more_tokens_than_one_launch_takes():
+    from bit_error_compensated_gb300 import echo
+    g = gen(9)
+    tokens = 65535 * 8 + 5
+    x = torch.randn(tokens, 64, generator=g, device="cuda")
+    w = torch.randn(3, 64, generator=g, device="cuda")
+    codes, meta = (t[0] for t in buffers(1, 3, 64, 64))
+    echo.echo_quantize_weights(w, codes, meta, group=64)
+    out = torch.full((tokens, 3), 7.0, device="cuda")
+    echo.echo_linear_int4(x, codes, meta, out, group=64)
+    code, s, z = quantised(w, 64)
+    want, size = ref.linear4(x, code, s, z, 64)
+    assert ((out.double() - want).abs() <= 64 * 2.0 ** -23 * size).all()

@@ -267,6 +267,33 @@ SHAPES = [
 ]
 
 
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("counts,lengths,heads,group,dim", [
+    ([600], [5000], 1, 4, 256), ([700], [4000], 3, 5, 128), ([90] * 40, [130 + 7 * i for i in range(40)], 2, 4, 64),
+    ([1] * 33, [2000 + i for i in range(33)], 4, 8, 128), ([1, 500, 2], [9000, 500, 4000], 2, 6, 128)])
+def test_blocks_that_walk_several_units(bits, counts, lengths, heads, group, dim):
+    """Enough rows and keys that a block has whole units and parts of others one
+    after the other, and more sequences than a warp has lanes."""
+    g = gen(bits + group)
+    starts, table, pages = make_batch(counts, lengths, 64, g)
+    cache = full_cache(g, pages, 64, heads, dim, bits)
+    spoil_behind(cache, lengths, table)
+    q = values(g, starts[-1], heads * group, dim, dtype=torch.bfloat16)
+    check(cache, tensors(starts, lengths, table), q, starts, lengths, table)
+
+
+@pytest.mark.parametrize("new", [3, 200])
+def test_without_causal_order_tokens_before_the_begin_see_nothing(new):
+    from bit_error_compensated_gb300 import echo
+    g = gen(19)
+    starts, table, pages = make_batch([new], [new - 2], 16, g)
+    cache = full_cache(g, pages, 16, 1, 64, 4)
+    q = values(g, new, 2, 64, dtype=torch.float16)
+    out = torch.full_like(q, 7)
+    echo.echo_attention(cache, tensors(starts, [new - 2], table), q, out, causal=False)
+    assert torch.all(out[:2] == 0) and torch.all(out[2:].abs().amax(-1) > 0) and torch.all(out[2:] != 7)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, (len(s[0]), max(s[0]), max(s[1]), *s[2:]))))

@@ -58,7 +58,7 @@ BAD_CACHE = [(dict(head_dim=96), "UNSUPPORTED"), (dict(bits=3), "UNSUPPORTED"), 
              (dict(codes=MB + 8), "ALIGN"), (dict(meta=2 * MB + 4), "ALIGN")]
 BAD_BATCH = [(dict(sequences=-1), "SHAPE"), (dict(tokens=-1), "SHAPE"), (dict(pages=-1), "SHAPE"), (dict(ld=1), "SHAPE"),
              (dict(sequences=2 ** 20 + 1), "UNSUPPORTED"), (dict(tokens=2 ** 20 + 1), "UNSUPPORTED"),
-             (dict(pages=2 ** 31, ld=2 ** 31), "UNSUPPORTED"), (dict(starts=0), "ARG"), (dict(lengths=0), "ARG"),
+             (dict(pages=2 ** 26 + 1, ld=2 ** 27), "UNSUPPORTED"), (dict(starts=0), "ARG"), (dict(lengths=0), "ARG"),
              (dict(table=0), "ARG"), (dict(starts=3 * MB + 2), "ALIGN"), (dict(table=3 * MB + 129), "ALIGN")]
 
 
