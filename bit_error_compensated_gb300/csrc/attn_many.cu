@@ -8,7 +8,7 @@
 //     O[128][D] += P V          P in TMEM, in the place of S, V in shared memory,
 // where K and V hold codes less their zero points, exact in f16.  Warps of the
 // block:
-//   4 a tile of rows   take S out of TMEM, turn scores into weights and put P
+//   8 a tile of rows   take S out of TMEM, turn scores into weights and put P
 //                      back: p = exp(score + log s_v - m), see attn_few.cu, so
 //                      that no value is multiplied by its step;
 //   4 for the keys, 4 for the values
@@ -19,9 +19,18 @@
 // S.  While one tile's weights are made, the tensor cores work for the other (with one tile
 // of rows: on the next tile's scores).
 //
-// A lane has two neighbouring keys of every eight and four rows of the warp's
-// 32: a quarter of the keys' steps are read by each lane, and P's pairs go back
-// as they are.
+// A lane has two neighbouring keys of every eight and two rows of the warp's
+// 16, so a quarter of the keys' steps are read by each lane, P's pairs go back
+// as they are, and a row is one warp's alone.
+//
+// One GB300: 2048 tokens (32 heads to 8, of 128) over 32768 keys of 4 bits in
+// 1211 us, 936 TFLOP/s; a prompt of 8192 in 732 us, 750.  A tile of 256 rows and
+// 128 keys takes 5100 cycles, of which the matrix instructions need 2100.  What
+// it is nearest to is shared memory: operands take 1536 cycles of it, the
+// warps' accesses 3100 (steps 1600, codes turned 570, barriers, and loads of
+// codes from L2); issue slots are 59% busy.  Four warps a tile of rows, with four
+// rows a lane, load steps half as often and wait longer for each other: 1172 and
+// 735 us, and 107 for a prompt of 2048 (95).
 //
 // Every wait is bounded; one that gives up ends the call with a status
 // (echo_serving_status): the block's other warps leave at their next wait, and
@@ -36,11 +45,11 @@ ECHO_STATUS_WORD
 
 constexpr int kRowTile = 128;
 constexpr int kSlots = 4;                               // of steps: tiles whose weights are being made, or are next
-// Registers: the block starts with 96 a thread (five warpgroups of 480 in all).
-constexpr int kWarpsWeights = 8, kWarpsKeys = 4, kWarpsValues = 4;
+// Registers: the block starts with 72 a thread (seven warpgroups of 504 in all).
+constexpr int kWarpsWeights = 16, kWarpsKeys = 4, kWarpsValues = 4;
 constexpr int kIssuer = kWarpsWeights + kWarpsKeys + kWarpsValues, kThreads = 32 * (kIssuer + 4);
-constexpr int kWeightRegs = 168, kTurnRegs = 56, kIssueRegs = 32;
-static_assert(2 * kWeightRegs + 2 * kTurnRegs + kIssueRegs <= 5 * 96, "a split above the launch's registers never ends");
+constexpr int kWeightRegs = 88, kTurnRegs = 56, kIssueRegs = 40;
+static_assert(4 * kWeightRegs + 2 * kTurnRegs + kIssueRegs <= 7 * 72, "a split above the launch's registers never ends");
 constexpr float kAhead = 8.0f;
 
 template <int D, int BITS>
@@ -106,11 +115,6 @@ __device__ __forceinline__ void tmem_loaded(float (&v)[16]) {
                : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
                  "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
                :: "memory");
-}
-__device__ __forceinline__ void tmem_loaded(float (&v)[16], float (&u)[16]) {
-  tmem_loaded(v);
-  asm volatile("" : "+f"(u[0]), "+f"(u[1]), "+f"(u[2]), "+f"(u[3]), "+f"(u[4]), "+f"(u[5]), "+f"(u[6]), "+f"(u[7]),
-                    "+f"(u[8]), "+f"(u[9]), "+f"(u[10]), "+f"(u[11]), "+f"(u[12]), "+f"(u[13]), "+f"(u[14]), "+f"(u[15]));
 }
 __device__ __forceinline__ void tmem_store(uint32_t at, const float (&v)[16]) {
   __syncwarp();
@@ -189,7 +193,7 @@ __device__ __forceinline__ void turn8(uint32_t a, uint32_t b, uint32_t base, uin
   h[3] = less(__byte_perm(b, base, 0x5352), low);
 }
 // The rows of tile t of a unit into shared memory, as the A operand (K-major);
-// a warp takes 32 of them.  They are scaled by one power of two, from the
+// a warp takes 16 of them, from row0.  They are scaled by one power of two, from the
 // largest of them, that takes f16's range into account; a row that is 2^-16 of
 // it or less has one of its own, and what its scores then have to be multiplied
 // by goes to `apart` (1 for the others).  A row with a non-finite element is
@@ -197,24 +201,24 @@ __device__ __forceinline__ void turn8(uint32_t a, uint32_t b, uint32_t base, uin
 // apart.
 constexpr int kSpread = 16;
 template <typename T, int D, int BITS>
-__device__ __forceinline__ float load_rows(const AttentionArgs& a, const Sequence& s, const Unit& u, int t, uint32_t query,
-                                           float* apart, bool* any_apart, bool aligned) {
-  const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+__device__ __forceinline__ float load_rows(const AttentionArgs& a, const Sequence& s, const Unit& u, int t, int row0,
+                                           uint32_t query, float* apart, bool* any_apart, bool aligned) {
+  const int lane = threadIdx.x & 31;
   constexpr int kChunks = D / 8, kAtOnce = 32 / kChunks == 0 ? 1 : 32 / kChunks;      // of a row, of eight elements; rows a step
-  constexpr int kSteps = 32 * kChunks / 32;
+  constexpr int kSteps = 16 * kChunks / 32;
   // A lane's chunks, one a step, come to where they stay, element by element as
   // they lie in memory; then they are read twice, for the largest and to be turned.
   auto row_of = [&](int n) { return kChunks <= 32 ? n * kAtOnce + lane / kChunks : n; };
   const int chunk = lane % kChunks;
   auto spot_of = [&](int n) {
-    const int r = warp * 32 + row_of(n);
+    const int r = row0 + row_of(n);
     return query + (chunk >> 3) * (kRowTile * 128) + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
   };
   static_assert(kChunks <= 32, "a row is one step's at most");
   const T* my_row = nullptr;                               // row `lane`
   {
-    const int r = t * kRowTile + warp * 32 + lane, row = u.first + r;
-    if (r < u.rows)
+    const int r = t * kRowTile + row0 + lane, row = u.first + r;
+    if (lane < 16 && r < u.rows)
       my_row = static_cast<const T*>(a.q.data) + (int64_t)(s.row + row / a.group) * a.q.ld +
                (int64_t)(u.head * a.group + row % a.group) * a.q.head_stride;
   }
@@ -260,7 +264,7 @@ __device__ __forceinline__ float load_rows(const AttentionArgs& a, const Sequenc
   const bool own = finite && mine != 0 && (int)(most >> 23) - (int)(mine >> 23) > kSpread;
   const float my_factor = own ? row_factor(mine) : factor;
   *any_apart = __any_sync(kFull, own);
-  apart[t * kRowTile + warp * 32 + lane] = factor / my_factor;            // powers of two
+  if (lane < 16) apart[t * kRowTile + row0 + lane] = factor / my_factor;  // powers of two
 #pragma unroll 2
   for (int n = 0; n < kSteps; ++n) {
     const float f = __shfl_sync(kFull, my_factor, row_of(n));
@@ -296,14 +300,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     give_up = 0;
-    mbar_init(bar + B::kQuery, 4 * NT);
+    mbar_init(bar + B::kQuery, 8 * NT);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar + B::kKeys + 8 * i, kWarpsKeys);
       mbar_init(bar + B::kKeysFree + 8 * i, 1);
       mbar_init(bar + B::kValues + 8 * i, kWarpsValues);
       mbar_init(bar + B::kValuesFree + 8 * i, 1);
       mbar_init(bar + B::kScores + 8 * i, 1);
-      mbar_init(bar + B::kWeights + 8 * i, 4);
+      mbar_init(bar + B::kWeights + 8 * i, 8);
       mbar_init(bar + B::kSums + 8 * i, 1);
     }
     for (int i = 0; i < kSlots; ++i) mbar_init(bar + B::kSteps + 8 * i, kWarpsKeys + kWarpsValues);
@@ -532,10 +536,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kWeightRegs));
-    const int t = warp >> 2;                               // tile of rows
+    const int t = warp >> 3;                               // tile of rows
     if (t < NT) {
+      // Two warps have 16 each of the 32 rows that a warp of this number reaches.
+      const int row0 = 32 * (warp & 3) + 16 * ((warp >> 2) & 1);
       const int g = lane >> 2, quad = lane & 3;
-      const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);          // this warp's 32 rows
+      const uint32_t lanes = tmem + ((uint32_t)row0 << 16);
       const uint32_t sums = lanes + S::kSums + t * D;
       uint32_t i = 0, unit = 0;
       float scale = 0.0f, next_scale = 0.0f;               // of the warp's scores
@@ -543,8 +549,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
       auto take_rows = [&]() {
         const uint32_t to = query + t * S::kQuery;
         const float back = a.dtype == ECHO_BF16
-                               ? load_rows<__nv_bfloat16, D, BITS>(a, walk.s, walk.unit, t, to, apart, &next_apart, wide_in)
-                               : load_rows<__half, D, BITS>(a, walk.s, walk.unit, t, to, apart, &next_apart, wide_in);
+                               ? load_rows<__nv_bfloat16, D, BITS>(a, walk.s, walk.unit, t, row0, to, apart, &next_apart, wide_in)
+                               : load_rows<__half, D, BITS>(a, walk.s, walk.unit, t, row0, to, apart, &next_apart, wide_in);
         next_scale = a.scale * kLog2E * back;
         fence_proxy_async();
         __syncwarp();
@@ -552,25 +558,25 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
       };
       if (walk.more()) take_rows();
       while (walk.more() && ok) {
-        // This lane's rows: g, g + 8, g + 16, g + 24 of the warp's.
-        float m[4], l[4][2];
+        // This lane's rows: g and g + 8 of the warp's.
+        float m[2], l[2][2];
         scale = next_scale;
         any_apart = next_apart;
-        const int first = t * kRowTile + 32 * (warp & 3);                  // of the unit's rows, the warp's first
-        {
+        const int first = t * kRowTile + row0;             // of the unit's rows, the warp's first
+        if (lane < 16) {
           const int r = first + lane, place = walk.s.place + (walk.unit.first + r) / a.group;
           // (rows past the last see all: one that sees nothing has no maximum)
           seen[r] = r < walk.unit.rows ? make_int2(keys_from(a, place), keys_to(a, walk.s, place)) : make_int2(0, 0x7FFFFFFF);
-          __syncwarp();
         }
+        __syncwarp();
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
+        for (int h = 0; h < 2; ++h) {
           m[h] = kLowest;
           l[h][0] = l[h][1] = 0.0f;
         }
         int all_from = 0, all_to = 0x7FFFFFFF;             // keys that all rows of the warp see
         if (first < walk.unit.rows) {
-          const int end = first + 32 < walk.unit.rows ? first + 31 : walk.unit.rows - 1;
+          const int end = first + 16 < walk.unit.rows ? first + 15 : walk.unit.rows - 1;
           all_from = keys_from(a, walk.s.place + (walk.unit.first + end) / a.group);
           all_to = keys_to(a, walk.s, walk.s.place + (walk.unit.first + first) / a.group);
         }
@@ -585,10 +591,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
           const bool inside = key >= all_from && key + KT <= all_to;
           // Raises the rows' maxima to `top` and scales what was made with the
           // old ones: the sums, and this tile's weights of the keys before c.
-          auto raise = [&](float (&top)[4], int c) {
-            float f[4];
+          auto raise = [&](float (&top)[2], int c) {
+            float f[2];
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
+            for (int h = 0; h < 2; ++h) {
               top[h] = fmaxf(top[h], __shfl_xor_sync(kFull, top[h], 1));
               top[h] = fmaxf(top[h], __shfl_xor_sync(kFull, top[h], 2));
               f[h] = exp2_of(m[h] - top[h]);
@@ -602,100 +608,89 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
                 fence_after();
               }
 #pragma unroll 1
-              for (int d = 0; d < D; d += 32)
+              for (int d = 0; d < D; d += 32) {
+                float v[16];
+                tmem_load(sums + d, v);
+                tmem_loaded(v);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  float v[16];
-                  tmem_load(sums + ((uint32_t)h << 20) + d, v);
-                  tmem_loaded(v);
-#pragma unroll
-                  for (int e = 0; e < 16; ++e) v[e] *= f[2 * h + ((e >> 1) & 1)];
-                  tmem_store(sums + ((uint32_t)h << 20) + d, v);
-                }
+                for (int e = 0; e < 16; ++e) v[e] *= f[(e >> 1) & 1];
+                tmem_store(sums + d, v);
+              }
             }
             if (c > 0) tmem_stored();
 #pragma unroll 1
-            for (int d = 0; d < c / 2; d += 16)            // (pairs, read and written as 8 words of two rows)
+            for (int d = 0; d < c / 2; d += 16) {          // (pairs, read and written as 8 words of two rows)
+              uint32_t w[8];
+              tmem_load_pairs(s_at + d, w);
 #pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                uint32_t w[8];
-                tmem_load_pairs(s_at + ((uint32_t)half << 20) + d, w);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const float2 two = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
-                  w[e] = pack_f16(two.x * f[2 * half + (e & 1)], two.y * f[2 * half + (e & 1)]);
-                }
-                tmem_store_pairs(s_at + ((uint32_t)half << 20) + d, w);
+              for (int e = 0; e < 8; ++e) {
+                const float2 two = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
+                w[e] = pack_f16(two.x * f[e & 1], two.y * f[e & 1]);
               }
+              tmem_store_pairs(s_at + d, w);
+            }
           };
           // Weights of the tile's keys, 32 at a time: u = s * scale * step_k + log
           // step_v, p = exp(u - m).  PLAIN: every row sees all, none is apart (a
           // branch a pair would leave the compiler nothing to interleave).
           auto weights = [&](auto plain) {
             constexpr bool kPlain = decltype(plain)::value;
-            float v[2][2][16];                             // of this and of the next keys, by 16 rows
-            float f[4];
-            int2 see[4];
+            float v[2][16];                                // of these and of the next keys
+            float f[2];
+            int2 see[2];
             if (!kPlain) {
 #pragma unroll
-              for (int h = 0; h < 4; ++h) {
+              for (int h = 0; h < 2; ++h) {
                 f[h] = apart[first + g + 8 * h];
                 see[h] = seen[first + g + 8 * h];
               }
             }
-            tmem_load(s_at, v[0][0]);
-            tmem_load(s_at + (16u << 16), v[0][1]);
+            tmem_load(s_at, v[0]);
 #pragma unroll 1                                           // (code that is fetched again costs as much as its work)
             for (int c0 = 0; c0 < KT; c0 += 64)
 #pragma unroll
-            for (int odd = 0; odd < 2; ++odd) {
-              const int c = c0 + 32 * odd;
-              float(&now)[2][16] = v[odd];
-              tmem_loaded(now[0], now[1]);
-              if (c + 32 < KT) {
-                tmem_load(s_at + c + 32, v[odd ^ 1][0]);
-                tmem_load(s_at + (16u << 16) + c + 32, v[odd ^ 1][1]);
-              }
-              float top[4] = {m[0], m[1], m[2], m[3]};
+              for (int odd = 0; odd < 2; ++odd) {
+                const int c = c0 + 32 * odd;
+                float(&now)[16] = v[odd];
+                tmem_loaded(now);
+                if (c + 32 < KT) tmem_load(s_at + c + 32, v[odd ^ 1]);
+                float top[2] = {m[0], m[1]};
 #pragma unroll
-              for (int n = 0; n < 4; ++n) {
-                float2 ks = shared_pair(slot + 4 * (c + 8 * n));
-                const float2 log = shared_pair(slot + 4 * (KT + c + 8 * n));
-                mul2(ks.x, ks.y, ks.x, ks.y, scale, scale);
+                for (int n = 0; n < 4; ++n) {
+                  float2 ks = shared_pair(slot + 4 * (c + 8 * n));
+                  const float2 log = shared_pair(slot + 4 * (KT + c + 8 * n));
+                  mul2(ks.x, ks.y, ks.x, ks.y, scale, scale);
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                  float &v0 = now[h >> 1][4 * n + 2 * (h & 1)], &v1 = now[h >> 1][4 * n + 2 * (h & 1) + 1];
-                  if (!kPlain) mul2(v0, v1, v0, v1, f[h], f[h]);
-                  fma2(v0, v1, v0, v1, ks.x, ks.y, log.x, log.y);
-                  if (!kPlain) {
-                    const int at = key + c + 8 * n + 2 * quad;
-                    v0 = at < see[h].x || at >= see[h].y ? kNone : v0;
-                    v1 = at + 1 < see[h].x || at + 1 >= see[h].y ? kNone : v1;
+                  for (int h = 0; h < 2; ++h) {
+                    float &v0 = now[4 * n + 2 * h], &v1 = now[4 * n + 2 * h + 1];
+                    if (!kPlain) mul2(v0, v1, v0, v1, f[h], f[h]);
+                    fma2(v0, v1, v0, v1, ks.x, ks.y, log.x, log.y);
+                    if (!kPlain) {
+                      const int at = key + c + 8 * n + 2 * quad;
+                      v0 = at < see[h].x || at >= see[h].y ? kNone : v0;
+                      v1 = at + 1 < see[h].x || at + 1 >= see[h].y ? kNone : v1;
+                    }
+                    top[h] = max3(top[h], v0, v1);
                   }
-                  top[h] = max3(top[h], v0, v1);
                 }
-              }
-              if (__any_sync(kFull, top[0] - m[0] > kAhead || top[1] - m[1] > kAhead || top[2] - m[2] > kAhead ||
-                                        top[3] - m[3] > kAhead))
-                raise(top, c);
-              uint32_t w[2][8];
+                if (__any_sync(kFull, top[0] - m[0] > kAhead || top[1] - m[1] > kAhead)) raise(top, c);
+                uint32_t w[8];
 #pragma unroll
-              for (int n = 0; n < 4; ++n) {
-                const float2 per = shared_pair(slot + 4 * (2 * KT + c + 8 * n));
+                for (int n = 0; n < 4; ++n) {
+                  const float2 per = shared_pair(slot + 4 * (2 * KT + c + 8 * n));
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                  float v0 = now[h >> 1][4 * n + 2 * (h & 1)], v1 = now[h >> 1][4 * n + 2 * (h & 1) + 1];
-                  sub2(v0, v1, v0, v1, m[h], m[h]);
-                  v0 = exp2_of(v0);
-                  v1 = exp2_of(v1);
-                  fma2(l[h][0], l[h][1], v0, v1, per.x, per.y, l[h][0], l[h][1]);
-                  w[h >> 1][2 * n + (h & 1)] = pack_f16(v0, v1);
+                  for (int h = 0; h < 2; ++h) {
+                    float v0 = now[4 * n + 2 * h], v1 = now[4 * n + 2 * h + 1];
+                    sub2(v0, v1, v0, v1, m[h], m[h]);
+                    v0 = exp2_of(v0);
+                    v1 = exp2_of(v1);
+                    fma2(l[h][0], l[h][1], v0, v1, per.x, per.y, l[h][0], l[h][1]);
+                    w[2 * n + h] = pack_f16(v0, v1);
+                  }
                 }
+                // (in the place of scores that have been read: those of half as many keys)
+                tmem_store_pairs(s_at + c / 2, w);
               }
-              // (in the place of scores that have been read: those of half as many keys)
-              tmem_store_pairs(s_at + c / 2, w[0]);
-              tmem_store_pairs(s_at + (16u << 16) + c / 2, w[1]);
-            }
           };
           if (inside && !any_apart) weights(std::true_type());
           else weights(std::false_type());
@@ -716,43 +711,36 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
         fence_after();
         const bool whole = done.whole();
         float* const part = slot_at(a, gridDim.x, slot_of(done, range), S::kRows, D);
-        float per[4];
+        float per[2];
+        int64_t out[2];
+        bool there[2];
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
+        for (int h = 0; h < 2; ++h) {
           float sum = l[h][0] + l[h][1];
           sum += __shfl_xor_sync(kFull, sum, 1);
           sum += __shfl_xor_sync(kFull, sum, 2);
           per[h] = sum == 0.0f ? 0.0f : 1.0f / sum;
-          const int r = first + g + 8 * h, row = done.unit.first + r;
-          if (quad == 0 && r < done.unit.rows) {
+          const int r = first + g + 8 * h, row = done.unit.first + r, token = done.s.row + row / a.group;
+          const int head = done.unit.head * a.group + row % a.group;
+          there[h] = r < done.unit.rows;
+          out[h] = token * a.out.ld + head * a.out.head_stride + 8 * quad;
+          if (quad == 0 && there[h]) {
             if (!whole) {
               part[S::kRows * D + r] = m[h];
               part[S::kRows * D + S::kRows + r] = sum;
             } else if (a.lse) {
-              const int64_t at = (int64_t)(done.s.row + row / a.group) * a.heads + done.unit.head * a.group + row % a.group;
-              a.lse[at] = sum == 0.0f ? kNone : (m[h] + log2_of(sum)) * kLn2;
+              a.lse[(int64_t)token * a.heads + head] = sum == 0.0f ? kNone : (m[h] + log2_of(sum)) * kLn2;
             }
           }
         }
         if (!whole && done.in == 0 && tid == 0) name_parts(a, done, range);
         // Two rows of 32 columns at a time, in a rolled loop: code that runs once a
         // unit is fetched each time.
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          const float per0 = half ? per[2] : per[0], per1 = half ? per[3] : per[1];
-          int64_t out[2];
-          bool there[2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int r = first + g + 16 * half + 8 * h, row = done.unit.first + r;
-            there[h] = r < done.unit.rows;
-            out[h] = (done.s.row + row / a.group) * a.out.ld +
-                     (int64_t)(done.unit.head * a.group + row % a.group) * a.out.head_stride + 8 * quad;
-          }
+        {
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             float v[16];
-            tmem_load(sums + ((uint32_t)half << 20) + c, v);
+            tmem_load(sums + c, v);
             tmem_loaded(v);
             // Of a row's four eights this lane has a pair each; after the exchange
             // it has all pairs of the eight of its own number.
@@ -783,7 +771,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
               if (!there[h]) continue;
               if (whole) {
 #pragma unroll
-                for (int n = 0; n < 8; ++n) e[n] *= h ? per1 : per0;
+                for (int n = 0; n < 8; ++n) e[n] *= per[h];
                 if (wide_out) {
                   if (a.dtype == ECHO_BF16) store_floats<__nv_bfloat16, 8>(static_cast<__nv_bfloat16*>(a.out.data) + out[h] + c, e);
                   else store_floats<__half, 8>(static_cast<__half*>(a.out.data) + out[h] + c, e);
@@ -792,7 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
                   for (int n = 0; n < 8; ++n) store_value(a, out[h] + c + n, e[n]);
                 }
               } else {
-                float* const to_part = part + (first + g + 16 * half + 8 * h) * D + c + 8 * quad;
+                float* const to_part = part + (first + g + 8 * h) * D + c + 8 * quad;
                 *reinterpret_cast<float4*>(to_part) = make_float4(e[0], e[1], e[2], e[3]);
                 *reinterpret_cast<float4*>(to_part + 4) = make_float4(e[4], e[5], e[6], e[7]);
               }

@@ -3,8 +3,10 @@
 // A head's row of a token is one group: head_dim / 16 lanes hold it, 16 values
 // each, so that a warp takes 8, 4 or 2 rows with 16-byte accesses and its
 // lanes' shuffles find a row's range.  A warp's rows belong to one token, whose
-// sequence its 32 lanes look for together.  Both kernels move bytes and little
-// else: a row of 128 in 16 bits is 256 bytes in and 68 out (4 bits).
+// sequence its 32 lanes look for together.  A row of 128 in 16 bits is 256 bytes
+// in and 68 out (4 bits).  8192 tokens of 8 heads of 128, bf16: written in 18.9 us
+// (2.2 TB/s, bound by instructions: range, step, rounding), read in 10.6 (4.0
+// TB/s); 64 tokens in 3.3 and 2.4.
 #include "serve_common.h"
 
 namespace echo {

@@ -16,6 +16,11 @@
 // weights (32 x 14336 x 4096: 51 us).  A cluster's blocks share the depth where
 // channels are few, and add up their sums through each other's shared memory, in
 // the order of the blocks.
+//
+// One GB300, GPU time a call: 1 x 4096 x 4096 in 5.7 us (2.2 of them a launch),
+// 1, 8, 16, 32 x 14336 x 4096 in 11.5, 12.4, 21 and 31 us (2.7 to 1.0 TB/s): a
+// block's loads, products and sums take turns, and the tokens' elements are as
+// many bytes as the codes.
 #include "serve_common.h"
 
 namespace echo {
