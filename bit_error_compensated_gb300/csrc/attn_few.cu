@@ -1,7 +1,7 @@
 // attn_few.cu -- echo_attention for few rows a sequence (include/echo.h):
 // decode, drafted tokens.
 //
-// Every key is read once for R = 8, 16 or 32 rows, so the kernel streams codes:
+// Every key is read once for 8 to 48 rows, so the kernel streams codes:
 // each warp copies 32 keys and values at a time into a ring of its own
 // (asynchronous copies, no barrier between warps) and feeds them to matrix
 // instructions whose 16 rows are keys, or columns of the values, and whose 8
@@ -640,17 +640,18 @@ cudaError_t launch(const AttentionArgs& a, int sms, cudaStream_t s) {
 }
 // How many eights of rows a unit has: a unit's keys cost about as much as four
 // eights do by themselves, so the fewest of units * (4 + eights), among what
-// registers hold.
+// registers hold.  (35 rows of 64, 16 sequences up to 8000: 36 us with five
+// eights, 41 with six.)
 template <int D>
 int eights(int64_t rows) {
-  const int known[] = {1, 2, 3, 4, 6}, most = D == 64 ? 5 : D == 128 ? 4 : 2;
+  constexpr int kMost = D == 64 ? 6 : D == 128 ? 4 : 2;
   int best = 1;
   int64_t least = INT64_MAX;
-  for (int i = 0; i < most; ++i) {
-    const int64_t cost = (rows + 8 * known[i] - 1) / (8 * known[i]) * (4 + known[i]);
+  for (int n = 1; n <= kMost; ++n) {
+    const int64_t cost = (rows + 8 * n - 1) / (8 * n) * (4 + n);
     if (cost < least) {
       least = cost;
-      best = known[i];
+      best = n;
     }
   }
   return best;
@@ -662,6 +663,7 @@ cudaError_t launch(const AttentionArgs& a, int64_t rows, int sms, cudaStream_t s
     case 2: return launch<D, 2>(a, sms, s);
     case 3: return launch<D, D <= 128 ? 3 : 2>(a, sms, s);
     case 4: return launch<D, D <= 128 ? 4 : 2>(a, sms, s);
+    case 5: return launch<D, D <= 64 ? 5 : 2>(a, sms, s);
     default: return launch<D, D <= 64 ? 6 : 2>(a, sms, s);
   }
 }
@@ -674,7 +676,7 @@ template <int D>
 int64_t bytes(int sms) {
   int64_t most = 0;
   for (int64_t n : {bytes<D, 1>(sms), bytes<D, 2>(sms), bytes<D, D <= 128 ? 3 : 2>(sms), bytes<D, D <= 128 ? 4 : 2>(sms),
-                    bytes<D, D <= 64 ? 6 : 2>(sms)})
+                    bytes<D, D <= 64 ? 5 : 2>(sms), bytes<D, D <= 64 ? 6 : 2>(sms)})
     most = n > most ? n : most;
   return most;
 }
