@@ -4,9 +4,9 @@
 // each, so that a warp takes 8, 4 or 2 rows with 16-byte accesses and its
 // lanes' shuffles find a row's range.  A warp's rows belong to one token, whose
 // sequence its 32 lanes look for together.  A row of 128 in 16 bits is 256 bytes
-// in and 68 out (4 bits).  8192 tokens of 8 heads of 128, bf16: written in 18.9 us
-// (2.2 TB/s, bound by instructions: range, step, rounding), read in 10.6 (4.0
-// TB/s); 64 tokens in 3.3 and 2.4.
+// in and 68 out (4 bits).  8192 tokens of 8 heads of 128, bf16: written in 15.2 us
+// (2.7 TB/s, bound by instructions: range, step, rounding; 18.9 where every lane
+// finds its group's step), read in 10.6 to 11.4 (3.7 TB/s); 64 tokens in 3.1 and 2.4.
 #include "serve_common.h"
 
 namespace echo {
@@ -19,19 +19,16 @@ constexpr int64_t kManySteps = 4 * 152 * 16;      // of the machine's warps, see
 
 // Values [8 NL h + 8 q, + 8) of a row, h = 0, 1, as lane q of the row's NL.
 template <typename T, int NL>
-__device__ __forceinline__ void load_row(const T* row, int q, bool aligned, float (&v)[16]) {
+__device__ __forceinline__ void load_row(const T* row, int q, bool aligned, Pack<T, 8> (&v)[2]) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const T* p = row + 8 * NL * h + 8 * q;
-    float f[8];
     if (aligned) {
-      to_floats<T, 8>(load_pack<T, 8>(p), f);
+      v[h] = load_pack<T, 8>(p);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = to_float(p[i]);
+      for (int i = 0; i < 8; ++i) v[h].v[i] = p[i];
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[8 * h + i] = f[i];
   }
 }
 
@@ -82,11 +79,15 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const RowsArgs a, c
   const int lane = threadIdx.x & 31, q = lane % NL, heads = a.cache.heads;
   const Place p = place_of<NL, G>(heads, lane);
   if (p.token >= a.batch.tokens) return;                 // the whole warp
-  float v[G][16] = {};
+  Pack<T, 8> v[G][2];
 #pragma unroll
   for (int i = 0; i < G; ++i) {
     const int row = p.row + i * kStep;
-    if (row >= 2 * heads) continue;
+    if (row >= 2 * heads) {
+#pragma unroll
+      for (int k = 0; k < 16; ++k) v[i][k / 8].v[k % 8] = from_float<T>(0.0f);
+      continue;
+    }
     const HeadsArgs& from = row >= heads ? a.v : a.k;
     load_row<T, NL>(static_cast<const T*>(from.data) + p.token * from.ld + (row >= heads ? row - heads : row) * from.head_stride,
                     q, aligned, v[i]);
@@ -100,27 +101,29 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const RowsArgs a, c
     return;
   }
   const float L = a.cache.bits == 4 ? 15.0f : 255.0f;
+  float lo[G], hi[G];
+#pragma unroll
+  for (int i = 0; i < G; ++i) range_of<T>(v[i], lo[i], hi[i]);
+  const GroupStep mine = shared_step<NL, G>(lo, hi, q, L);
+  // (the values' groups of a page follow its keys')
+  if (q < G && p.row + q * kStep < 2 * heads) {
+    a.cache.meta[group_index(a.cache, page, p.row + q * kStep, place)] = mine.meta;
+    if (!mine.finite) report(kNaNGroup);
+  }
+  __syncwarp();
 #pragma unroll
   for (int i = 0; i < G; ++i) {
     const int row = p.row + i * kStep;
     if (p.row - lane / NL + i * kStep >= 2 * heads) break;               // the whole warp
-    float lo, hi;
-    group_range<NL>(v[i], lo, hi);
+    const GroupStep g = step_at<NL, G>(mine, i);
     if (row >= 2 * heads) continue;
-    const GroupStep g = group_step(lo, hi, L);
-    // (the values' groups of a page follow its keys')
     const int64_t at = group_index(a.cache, page, row, place);
-    if (q == 0) {
-      a.cache.meta[at] = g.meta;
-      if (!g.finite) report(kNaNGroup);
-    }
     uint8_t* codes = a.cache.codes + at * (2 * NL * a.cache.bits);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int first = 8 * NL * h + 8 * q;
       float eight[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) eight[k] = v[i][8 * h + k];
+      to_floats<T, 8>(v[i][h], eight);
       uint32_t low, high;
       if (a.cache.bits == 4) {
         group_codes8<4>(eight, g, low, high);
@@ -194,8 +197,8 @@ __global__ void __launch_bounds__(32 * kWarps) read_kernel(const RowsArgs a, con
   }
 }
 
-template <typename T, int NL, int G>
-cudaError_t launch(const RowsArgs& a, bool append, cudaStream_t s) {
+template <typename T, int NL, int G, bool APPEND>
+cudaError_t launch(const RowsArgs& a, cudaStream_t s) {
   constexpr int kRows = 32 / NL * G;
   const int64_t each = (2 * a.cache.heads + kRows - 1) / kRows;
   bool aligned = true;
@@ -208,16 +211,19 @@ cudaError_t launch(const RowsArgs& a, bool append, cudaStream_t s) {
   cudaLaunchAttribute overlapped = overlapped_launch();
   cfg.attrs = &overlapped;
   cfg.numAttrs = 1;
-  return append ? cudaLaunchKernelEx(&cfg, append_kernel<T, NL, G>, a, (int)aligned)
-                : cudaLaunchKernelEx(&cfg, read_kernel<T, NL, G>, a, (int)aligned);
+  if constexpr (APPEND) return cudaLaunchKernelEx(&cfg, append_kernel<T, NL, G>, a, (int)aligned);
+  else return cudaLaunchKernelEx(&cfg, read_kernel<T, NL, G>, a, (int)aligned);
 }
 // Where a step a warp would fill the machine several times over, a warp takes
-// four: a token's place is looked for once for them (three loads that wait for
-// each other), and their loads are in flight together.
+// two (if a token has as many): its place is looked for once for them (three loads
+// that wait for each other), their loads are in flight together, and lanes share
+// the finding of steps (four: 15.7 us for 8192 tokens, two 15.2).
 template <typename T, int NL>
 cudaError_t launch(const RowsArgs& a, bool append, cudaStream_t s) {
-  const int64_t steps = (int64_t)a.batch.tokens * ((2 * a.cache.heads + 32 / NL - 1) / (32 / NL));
-  return steps > kManySteps ? launch<T, NL, 2>(a, append, s) : launch<T, NL, 1>(a, append, s);
+  const int each = (2 * a.cache.heads + 32 / NL - 1) / (32 / NL);        // steps a token
+  const bool many = (int64_t)a.batch.tokens * each > kManySteps;
+  if (!append) return many && each > 1 ? launch<T, NL, 2, false>(a, s) : launch<T, NL, 1, false>(a, s);
+  return many && each > 1 ? launch<T, NL, 2, true>(a, s) : launch<T, NL, 1, true>(a, s);
 }
 template <typename T>
 cudaError_t launch(const RowsArgs& a, bool append, cudaStream_t s) {

@@ -2,10 +2,10 @@
 // codes in groups along their depth.
 //
 // group / 16 lanes hold a group, 16 values each, as in the all-reduce's push;
-// a warp takes 8, 4 or 2 groups of a row that follow each other.  14336 x 4096
-// bf16 take 55 us (2.7 TB/s): 437 instructions for 16 values a lane, issue slots
-// 77% busy, a quarter of them for the step that every lane of a group computes.
-// (Two steps of a row a warp, their loads in flight together: 63 us.)
+// a warp takes up to twice 8, 4 or 2 groups of a row that follow each other.
+// 14336 x 4096 bf16 take 41 us (3.6 TB/s), bound by instructions; with a step
+// that every lane of a group finds by itself, 55 us (437 instructions for 16
+// values a lane).
 #include "serve_common.h"
 
 namespace echo {
@@ -14,6 +14,7 @@ namespace {
 ECHO_STATUS_WORD
 
 constexpr int kWarps = 8;
+constexpr int64_t kManySteps = 4 * 152 * 16;      // of the machine's warps, see launch
 
 // G: steps of 32 / NL groups, one after the other in a row, that a warp takes
 // (their loads are in flight together).
@@ -30,7 +31,7 @@ __global__ void __launch_bounds__(32 * kWarps) quantize_weights_kernel(const Wei
   const int64_t rank = divided(row, a.channels), channel = row - rank * a.channels;
   const int64_t group0 = (w - row * each) * kGroups * G + lane / NL;
   const T* from = static_cast<const T*>(a.w) + rank * a.rank_w + channel * a.ld_w;
-  float v[G][16] = {};
+  Pack<T, 8> v[G][2];
 #pragma unroll
   for (int i = 0; i < G; ++i) {
     const int64_t k0 = (group0 + i * kGroups) * kGroup, here = a.depth - k0;             // values of this group, if fewer than all
@@ -38,37 +39,35 @@ __global__ void __launch_bounds__(32 * kWarps) quantize_weights_kernel(const Wei
     for (int h = 0; h < 2; ++h) {
       const int first = 8 * NL * h + 8 * q;
       if (aligned && first + 8 <= here) {
-        float f[8];
-        to_floats<T, 8>(load_pack<T, 8>(from + k0 + first), f);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[i][8 * h + k] = f[k];
+        v[i][h] = load_pack<T, 8>(from + k0 + first);
       } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (first + k < here) v[i][8 * h + k] = to_float(from[k0 + first + k]);
+        for (int k = 0; k < 8; ++k) v[i][h].v[k] = first + k < here ? from[k0 + first + k] : from_float<T>(0.0f);
       }
     }
   }
   __syncwarp();
+  float lo[G], hi[G];
+#pragma unroll
+  for (int i = 0; i < G; ++i) range_of<T>(v[i], lo[i], hi[i]);
+  const GroupStep mine = shared_step<NL, G>(lo, hi, q, 15.0f);
+  if (q < G && group0 + q * kGroups < groups) {
+    a.meta[rank * a.rank_meta + channel * a.ld_meta + group0 + q * kGroups] = mine.meta;
+    if (!mine.finite) report(kNaNGroup);
+  }
+  __syncwarp();
 #pragma unroll
   for (int i = 0; i < G; ++i) {
-    const int64_t group = group0 + i * kGroups, k0 = group * kGroup, here = a.depth - k0;
-    float lo, hi;
-    group_range<NL>(v[i], lo, hi);
+    const int64_t k0 = (group0 + i * kGroups) * kGroup, here = a.depth - k0;
+    const GroupStep g = step_at<NL, G>(mine, i);
     if (here > 0) {
-      const GroupStep g = group_step(lo, hi, 15.0f);
-      if (q == 0) {
-        a.meta[rank * a.rank_meta + channel * a.ld_meta + group] = g.meta;
-        if (!g.finite) report(kNaNGroup);
-      }
       uint8_t* to = a.codes + rank * a.rank_codes + channel * a.ld_codes + k0 / 2;
       const bool words = ((uintptr_t)to & 3) == 0;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int first = 8 * NL * h + 8 * q;
         float eight[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) eight[k] = v[i][8 * h + k];
+        to_floats<T, 8>(v[i][h], eight);
         uint32_t low, high;
         group_codes8<4>(eight, g, low, high);
         uint32_t codes = low | high << 16;
@@ -86,9 +85,9 @@ __global__ void __launch_bounds__(32 * kWarps) quantize_weights_kernel(const Wei
   }
 }
 
-template <typename T, int NL>
+template <typename T, int NL, int G>
 cudaError_t launch(const WeightsArgs& a, cudaStream_t s) {
-  constexpr int G = 1, kGroups = 32 / NL, kGroup = 16 * NL;
+  constexpr int kGroups = 32 / NL, kGroup = 16 * NL;
   const int64_t groups = (a.depth + kGroup - 1) / kGroup;
   const int64_t warps = (groups + kGroups * G - 1) / (kGroups * G) * a.ranks * a.channels;
   const int64_t in16 = 16 / (int64_t)sizeof(T);
@@ -101,6 +100,14 @@ cudaError_t launch(const WeightsArgs& a, cudaStream_t s) {
   cfg.attrs = &overlapped;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, quantize_weights_kernel<T, NL, G>, a, (int)aligned);
+}
+// Two steps a warp where one each would fill the machine several times over (four:
+// 43 us for 14336 x 4096, two 41, one 55).
+template <typename T, int NL>
+cudaError_t launch(const WeightsArgs& a, cudaStream_t s) {
+  constexpr int kSpan = 16 * 32;
+  const int64_t steps = (a.depth + kSpan - 1) / kSpan * a.ranks * a.channels;
+  return steps > kManySteps ? launch<T, NL, 2>(a, s) : launch<T, NL, 1>(a, s);
 }
 template <typename T>
 cudaError_t launch(const WeightsArgs& a, cudaStream_t s) {

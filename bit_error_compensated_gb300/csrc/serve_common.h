@@ -251,6 +251,70 @@ __device__ __forceinline__ float meta_zero(uint32_t meta) {
   return __half2float(__ushort_as_half((unsigned short)(meta >> 16)));
 }
 
+// Groups of which NL lanes have 16 values each.  A group's step takes more than a
+// hundred instructions, so a warp that has G steps of 32 / NL groups lets lane q
+// of NL find that of step q % G: lanes hand on half of their ranges at a time.
+//
+// The range of 16 values and 0.
+template <typename T>
+__device__ __forceinline__ void range_of(const Pack<T, 8> (&x)[2], float& lo, float& hi) {
+  if constexpr (sizeof(T) == 4) {
+    float v[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v[k] = x[k / 8].v[k % 8];
+    group_range<1>(v, lo, hi);
+  } else {
+    using Two = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+    const Two* a = reinterpret_cast<const Two*>(&x[0]);
+    const Two* b = reinterpret_cast<const Two*>(&x[1]);
+    Two low[4], high[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      low[k] = __hmin2_nan(a[k], b[k]);
+      high[k] = __hmax2_nan(a[k], b[k]);
+    }
+    const Two l = __hmin2_nan(__hmin2_nan(low[0], low[1]), __hmin2_nan(low[2], low[3]));
+    const Two h = __hmax2_nan(__hmax2_nan(high[0], high[1]), __hmax2_nan(high[2], high[3]));
+    lo = min3_nan(to_float(l.x), to_float(l.y), 0.0f);
+    hi = max3_nan(to_float(h.x), to_float(h.y), 0.0f);
+  }
+}
+// The step of step q % G's group, from the parts of all; of a whole warp.
+template <int NL, int G>
+__device__ __forceinline__ GroupStep shared_step(float (&lo)[G], float (&hi)[G], int q, float L) {
+  int n = G;
+#pragma unroll
+  for (int off = 1; off < NL; off <<= 1) {
+    if (n > 1) {                         // this lane keeps the steps whose next bit is its own
+      const bool odd = q & off;
+#pragma unroll
+      for (int j = 0; j < n / 2; ++j) {
+        const float l = __shfl_xor_sync(kFull, odd ? lo[2 * j] : lo[2 * j + 1], off);
+        const float h = __shfl_xor_sync(kFull, odd ? hi[2 * j] : hi[2 * j + 1], off);
+        lo[j] = min_nan(odd ? lo[2 * j + 1] : lo[2 * j], l);
+        hi[j] = max_nan(odd ? hi[2 * j + 1] : hi[2 * j], h);
+      }
+      n /= 2;
+    } else {
+      lo[0] = min_nan(lo[0], __shfl_xor_sync(kFull, lo[0], off));
+      hi[0] = max_nan(hi[0], __shfl_xor_sync(kFull, hi[0], off));
+    }
+  }
+  return group_step(lo[0], hi[0], L);
+}
+// Step i's, from the lane that has it; of a whole warp.
+template <int NL, int G>
+__device__ __forceinline__ GroupStep step_at(const GroupStep& mine, int i) {
+  if constexpr (G == 1) return mine;
+  const int from = (threadIdx.x & 31 & ~(NL - 1)) | i;
+  GroupStep g;
+  g.meta = __shfl_sync(kFull, mine.meta, from);
+  g.inv = __shfl_sync(kFull, mine.inv, from);
+  g.s = meta_step(g.meta);
+  g.zf = meta_zero(g.meta);
+  g.finite = (g.meta & 0x7FFFu) < 0x7C00u;
+  return g;
+}
 
 // (w & MASK) | base in one instruction: an instruction takes one constant, so
 // the base is a register that the compiler does not know (it made two of them,

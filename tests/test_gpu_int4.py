@@ -45,6 +45,33 @@ def test_weights_are_quantised_exactly(dtype, group, ranks, channels, depth):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("group", [64, 128, 256])
+@pytest.mark.parametrize("ranks,channels,depth", [(1, 10000, 72), (2, 2500, 1027), (1, 1250, 4096), (1, 1100, 4616)])
+def test_many_weights_are_quantised_exactly(dtype, group, ranks, channels, depth):
+    """As above, with so many that a warp has several steps of a row's, the last of
+    them in part or not at all, and groups that cannot be held among them."""
+    from bit_error_compensated_gb300 import echo
+    echo.echo_serving_status()
+    w = torch.randn(ranks, channels, depth, generator=gen(depth), device="cuda").to(DTYPES[dtype])
+    code, s, z = quantised(w, group)
+    bad = [(0, 5, 3, float("nan")), (ranks - 1, channels - 1, depth - 1, float("inf")), (0, channels // 2, depth // 2, float("-inf"))]
+    for p, c, k, x in bad:
+        w[p, c, k] = x
+    codes, meta = buffers(ranks, channels, depth, group)
+    echo.echo_quantize_weights(w, codes, meta, group=group)
+    assert echo.echo_serving_status() == echo.ECHO_ERR_OVERFLOW
+    want_codes, want_meta = ref.pack(code, 4), ref.words(s[..., None], z[..., None])
+    for p, c, k, _ in bad:
+        at = k // group
+        assert int(meta[p, c, at]) & 0x7FFF == 0x7E00
+        want_meta[p, c, at] = meta[p, c, at]
+        of = slice(at * group // 2, (at + 1) * group // 2)
+        assert not codes[p, c, of].any()                     # a group without a step has codes of 0
+        want_codes[p, c, of] = 0
+    assert torch.equal(codes, want_codes) and torch.equal(meta, want_meta)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("group", [64, 128, 256])
 @pytest.mark.parametrize("ranks,tokens,channels,depth", [
     (1, 1, 1, 1), (1, 1, 16, 128), (2, 3, 33, 257), (1, 8, 100, 1000), (1, 9, 64, 512), (4, 16, 48, 384),
     (1, 17, 40, 2051), (1, 32, 96, 4096), (2, 33, 31, 640), (1, 70, 65, 320), (1, 5, 130, 8192)])

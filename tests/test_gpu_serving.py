@@ -113,6 +113,37 @@ def test_rows_are_quantised_exactly_and_read_back(dtype, bits, dim, heads, page)
     assert echo.echo_serving_status() == 0
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("tokens,dim,heads", [(9800, 64, 1), (3300, 64, 9), (5000, 128, 3), (3300, 128, 5), (3300, 256, 3)])
+def test_many_rows_are_quantised_exactly(dtype, bits, tokens, dim, heads):
+    """As above, with so many rows that a warp has several steps of a token's, the
+    last of them in part or not at all, and groups that cannot be held among them."""
+    from bit_error_compensated_gb300 import echo
+    g = gen(dim + bits + heads)
+    page, pages = 64, (tokens + 63) // 64
+    cache = echo.Cache(pages, page, heads, dim, bits)
+    batch = tensors([0, tokens], [tokens], torch.arange(pages, dtype=torch.int32, device="cuda")[None])
+    k, v = (values(g, tokens, heads, dim).mul(10.0 ** torch.randint(-4, 4, (tokens, heads, 1), generator=g, device="cuda"))
+            .to(DTYPES[dtype]) for _ in range(2))
+    bad = [(0, 17, 0, float("nan")), (0, 500, heads - 1, float("inf")), (1, tokens - 1, heads // 2, float("-inf"))]
+    both = torch.stack((k, v))                               # as they are without those
+    code, s, z = ref.groups(both, bits)
+    for i, token, head, x in bad:
+        (k, v)[i][token, head, (7 * token) % dim] = x
+    echo.echo_cache_append(cache, batch, k, v)
+    assert echo.echo_serving_status() == echo.ECHO_ERR_OVERFLOW
+    rows = lambda t: t.permute(1, 0, 3, 2, *range(4, t.dim())).flatten(1, 2)[:, :tokens]     # noqa: E731  (pages' places in a row)
+    got_codes, got_meta = rows(cache.codes), rows(cache.meta)
+    want_codes, want_meta = ref.pack(code, bits), ref.words(s, z)
+    assert want_meta.shape == got_meta.shape and want_codes.shape == got_codes.shape
+    for i, token, head, _ in bad:
+        assert int(got_meta[i, token, head]) & 0x7FFF == 0x7E00
+        want_meta[i, token, head] = got_meta[i, token, head]
+        want_codes[i, token, head] = got_codes[i, token, head]
+    assert torch.equal(got_meta, want_meta) and torch.equal(got_codes, want_codes)
+
+
 @pytest.mark.parametrize("bits", [4, 8])
 def test_values_next_to_a_border_are_rounded_exactly(bits):
     """fp32 values a step of their own beside k + 1/2 steps of the group, and
