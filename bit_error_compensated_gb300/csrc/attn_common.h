@@ -310,6 +310,12 @@ __device__ __forceinline__ float reciprocal(float v) {
   return r;
 }
 
+// A value's step as its weight takes it.  A place that was never written may have
+// a step of 0 and codes of 0: its value adds nothing, but its weight counts.  With
+// a step far below fp16's least the weight's part of the sum is exact and its
+// product with the value rounds to nothing.  NaN stays NaN.
+__device__ __forceinline__ float value_step(uint32_t meta) { return max_nan(meta_step(meta), 0x1p-60f); }
+
 // Query rows as f16, scaled by a power of two that takes the row's largest
 // element to [2^14, 2^15): bf16 values stay exact down to 2^-31 of it (f16's
 // subnormals begin 2^-29 below and hold 2^-39 of it).

@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, (Few<D, BITS, NR>::kBlocks)) attenti
         for (int sub = 0; sub < kSubs; ++sub)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float ks = meta_step(kmeta[sub][h]), vs = meta_step(vmeta[sub][h]);
+            const float ks = meta_step(kmeta[sub][h]), vs = value_step(vmeta[sub][h]);
             const float log = log2_of(vs);
             per[sub][h] = reciprocal(vs);
 #pragma unroll
@@ -640,7 +640,7 @@ cudaError_t launch(const AttentionArgs& a, int sms, cudaStream_t s) {
 }
 // How many eights of rows a unit has: a unit's keys cost about as much as four
 // eights do by themselves, so the fewest of units * (4 + eights), among what
-// registers hold.  (35 rows of 64, 16 sequences up to 8000: 36 us with five
+// registers hold.  (35 rows of 64, 16 sequences up to 6000: 36 us with five
 // eights, 41 with six.)
 template <int D>
 int eights(int64_t rows) {

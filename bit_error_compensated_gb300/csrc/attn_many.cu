@@ -470,7 +470,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
     load();
     look_up();
     for (uint32_t i = 0; i < n; ++i) {
-      const float step = meta_step(meta);
       ok = __all_sync(0xFFFFFFFFu, wait_on(empty + 8 * (i & 1), ((i >> 1) & 1) ^ 1u, &give_up));
       if (!ok) break;
       // A value that is not there has a log of -infinity, so that its weight is 0,
@@ -479,9 +478,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
       if (row_lane) {
         const uint32_t at = steps + (i & (kSlots - 1)) * S::kSteps + 4 * r;
         if (!value) {
-          asm volatile("st.shared.f32 [%0], %1;" :: "r"(at), "f"(step) : "memory");
+          asm volatile("st.shared.f32 [%0], %1;" :: "r"(at), "f"(meta_step(meta)) : "memory");
         } else {
-          const float log = there ? log2_of(step) : kNone, per = there && step == step ? reciprocal(step) : 0.0f;
+          const float of = value_step(meta);
+          const float log = there ? log2_of(of) : kNone, per = there && of == of ? reciprocal(of) : 0.0f;
           asm volatile("st.shared.f32 [%0], %1;" :: "r"(at + 4 * KT), "f"(log) : "memory");
           asm volatile("st.shared.f32 [%0], %1;" :: "r"(at + 8 * KT), "f"(per) : "memory");
         }

@@ -608,7 +608,7 @@ int echo_linear_int8(int64_t ranks, int64_t tokens, int64_t channels, int64_t de
  * values is what the all-reduce's quantizer gives.  A group with a non-finite
  * value, or whose s would be beyond fp16, gets codes 0, z 0 and a step of NaN,
  * so that all its values read as NaN, and sets the status word to
- * ECHO_ERR_OVERFLOW.  A meta word holds s in its low half and z (an fp16
+ * ECHO_ERR_OVERFLOW.  Words and codes of 0 stand for values of 0.  A meta word holds s in its low half and z (an fp16
  * number) in its high half; 4-bit codes lie as in echo_wire_layout (element 2i
  * in the low nibble of byte i).
  * ---------------------------------------------------------------------------

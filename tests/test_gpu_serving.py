@@ -375,6 +375,28 @@ def test_no_key_and_fewer_keys_than_tokens(new, length):
         assert torch.all(out[:new - length] == 0) and torch.any(out[new - length] != 0)
 
 
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("new", [1, 80])
+def test_places_that_were_never_written_are_zeros(new, bits):
+    """A new cache holds words of 0, whose values are 0: their weights count, alone
+    and among written places."""
+    from bit_error_compensated_gb300 import echo
+    g = gen(new + bits)
+    counts, lengths = [new, new], [700, 333]
+    starts, table, pages = make_batch(counts, lengths, 64, g)
+    cache = full_cache(g, pages, 64, 2, 128, bits)
+    gone = torch.rand(pages, 1, 1, 64, generator=g, device="cuda") < 0.5
+    gone[table[1].long()] = True                             # all of the second sequence
+    gone = gone.expand(cache.meta.shape)
+    cache.meta[gone] = 0
+    cache.codes[gone] = 0
+    q = values(g, 2 * new, 8, 128, dtype=torch.bfloat16)
+    out = check(cache, tensors(starts, lengths, table), q, starts, lengths, table)
+    assert torch.all(out[new:] == 0) and torch.any(out[:new] != 0)
+    fresh = echo.Cache(pages, 64, 2, 128, bits)
+    assert torch.all(check(fresh, tensors(starts, lengths, table), q, starts, lengths, table) == 0)
+
+
 @pytest.mark.parametrize("new", [1, 70])
 def test_extreme_scales_of_queries_keys_and_values(new):
     """Rows of q from 2^-60 to 2^60 of each other, values' steps over six orders
