@@ -310,11 +310,37 @@ __device__ __forceinline__ float reciprocal(float v) {
   return r;
 }
 
-// A value's step as its weight takes it.  A place that was never written may have
-// a step of 0 and codes of 0: its value adds nothing, but its weight counts.  With
-// a step far below fp16's least the weight's part of the sum is exact and its
-// product with the value rounds to nothing.  NaN stays NaN.
+// What a weight is in f16.  A value's step s is f times a power of two S (value_scale)
+// with f from 1 to 2, or less or more than that where s is outside 2^-14 .. 2^6.  The
+// matrix instructions take P = w f 2^-m and V = (c - z) S, both in f16, and add
+// their products in fp32: (c - z) S is exact, P has 11 bits, and the sum of weights
+// takes P / f in fp32.  (With all of s in P a key of a large step and weight pushes
+// the other keys' weights below f16's least: a row of zeros has a step of 1 by
+// definition.)
+//
+// A row's m is a whole number, so that scaling by a difference of two of them
+// rounds nothing.  It is raised when a score passes it by kMostWeight, so weights
+// are 2^15 at the most, and then to AHEAD above the score less kMostWeight, so the
+// largest is 2^(14 - AHEAD) at the least.  11 bits are left to weights down to
+// 2^-14, those below have a step of 2^-24: of the largest weight, with AHEAD 4 and
+// 8, 2^-24 and 2^-20, and 2^-34 and 2^-30.
+constexpr float kMostWeight = 15.0f;
+template <int AHEAD>
+__device__ __forceinline__ float raised(float m, float top) { return fmaxf(m, ceilf(top) - (kMostWeight - AHEAD)); }
+
+// A value's step.  A place that was never written may have a step of 0 and codes
+// of 0: its value adds nothing, but its weight counts.  With a step far below fp16's
+// least the weight's part of the sum is exact and its product with the value rounds
+// to nothing.  NaN stays NaN.
 __device__ __forceinline__ float value_step(uint32_t meta) { return max_nan(meta_step(meta), 0x1p-60f); }
+// S as f16 bits, the step's power of two within 2^-14 .. 2^5: with it both 1024 + z
+// and a single code are f16 numbers that are no subnormals, which matrix
+// instructions would align like 2^-14.
+__device__ __forceinline__ uint32_t value_scale(uint32_t meta) { return min(max(meta & 0x7C00u, 0x0400u), 0x5000u); }
+// f = s / S, exactly.
+__device__ __forceinline__ float value_factor(uint32_t meta) {
+  return __fmul_rn(value_step(meta), __uint_as_float((127u + 15u << 23) - (value_scale(meta) << 13)));
+}
 
 // Query rows as f16, scaled by a power of two that takes the row's largest
 // element to [2^14, 2^15): bf16 values stay exact down to 2^-31 of it (f16's

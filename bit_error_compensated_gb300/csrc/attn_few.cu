@@ -13,17 +13,15 @@
 // for two codes takes c - z, exactly; steps are multiplied into scores and
 // weights in fp32.  (f16 holds c * 2^-24 as it stands, as a subnormal, but the
 // matrix instructions align their sums by exponents that leave such a number 14
-// bits.)  The step s of a value goes into the weight, p_j = exp(score_j + log
-// s_j - m), whose running maximum m then bounds p_j by 2^8 whatever the steps
-// are (it is raised only when a score passes it by 2^8), so that p_j has 11 bits
-// in f16; the sum of weights takes p_j / s_j.
+// bits.)  Of a value's step its power of two goes into the value and the rest, 1 to
+// 2, into the weight, which is f16 below a bound on its row (attn_common.h).
 //
 // Blocks take equal shares of the batch's tiles (attn_common.h); four warps
 // take a tile's keys and join at the unit's end, and parts of units that several
 // blocks have had are joined by a second kernel.
 //
 // One GB300, 32 heads to 8 of 128, GPU time a call: 64 ragged sequences up to
-// 16384, 4 bits, in 161 us (4.1 TB/s: bound by the instructions that turn
+// 16384, 4 bits, in 163 us (4.1 TB/s: bound by the instructions that turn
 // codes), 4 x 131072 of 8 bits in 178 (6.2 TB/s: memory); one token over 2000
 // keys in 9.7, 131000 in 46.
 #include "attn_common.h"
@@ -35,7 +33,7 @@ ECHO_STATUS_WORD
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kLeast = 1;                // tiles of a block
-constexpr float kAhead = 8.0f;           // a score may pass the maximum by this much, as a power of two
+constexpr int kAhead = 4;                // (8 is no faster)
 
 // NR: eights of rows.
 template <int D, int BITS, int NR>
@@ -46,7 +44,9 @@ struct Few {
   static constexpr int kTile = kStep * kWarps;
   static constexpr int kStage = 2 * kStep * kRowBytes + 2 * kStep * 4;     // keys, values, meta of both
   static constexpr int kStages = kRowBytes >= 128 ? 2 : 3;
-  static constexpr int kRing = kWarps * kStages * kStage;
+  static constexpr int kPairBytes = BITS == 4 ? 16 : 8;  // of what turns the codes of two values
+  static constexpr int kSteps = kStep * 8 + kStep / 2 * kPairBytes;        // a warp's, see prepare_values
+  static constexpr int kRing = kWarps * (kStages * kStage + kSteps);
   static constexpr int kPitch = D + 4;                   // floats from row to row of the warps' sums
   static constexpr int kJoin = kWarps * kRows * kPitch * 4;                // which take the ring's place
   static constexpr int kQuery = D / 16 * NR * 32 * 8;    // rows as the instructions' operands
@@ -55,7 +55,7 @@ struct Few {
   static constexpr int kValuePiece = kRowBytes / 8 < 16 ? kRowBytes / 8 : 16;
   static constexpr int kPerWord = 32 / BITS;
   // Blocks an SM: what registers (sums take D * NR / 4 a thread) and shared memory allow.
-  static constexpr int kByRegs = D * NR <= 128 ? 4 : D * NR <= 256 ? 3 : 2, kBySmem = 227 * 1024 / (kBytes + 2560);
+  static constexpr int kByRegs = D * NR <= 128 ? 4 : D * NR <= 256 ? 3 : 2, kBySmem = 227 * 1024 / (kBytes + 1152 + 44 * kRows);
   static constexpr int kBlocks = kByRegs < kBySmem ? kByRegs : kBySmem;
 };
 
@@ -98,16 +98,27 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {         // a in
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Codes less their zero points (of two rows, for values) as pairs of f16.
-// `low` is 1024 + z, `high` 64 + z, twice.
+// Codes less their zero points as pairs of f16: of a key, `low` is 1024 + z,
+// `high` - 64 - z, twice; of two values, - (1024 + z) S and - (64 + z) S.
 struct Zero {
   uint32_t low, high, base;              // base: 1024, twice
+};
+struct ScaledZero {
+  uint32_t low, scale, high, high_scale; // scale: S, high_scale: S / 16
+  uint32_t base;
 };
 __device__ __forceinline__ Zero zero_of(uint32_t zs, uint32_t base) {     // two fp16 zero points
   const __half2 z = *reinterpret_cast<const __half2*>(&zs);
   const __half2 low = __hadd2(z, __float2half2_rn(1024.0f)), high = __hneg2(__hadd2(z, __float2half2_rn(64.0f)));
   return {*reinterpret_cast<const uint32_t*>(&low), *reinterpret_cast<const uint32_t*>(&high), base};
 }
+__device__ __forceinline__ uint32_t scaled_sum(uint32_t v, uint32_t scale, uint32_t z) {
+  const __half2 d = __hfma2(*reinterpret_cast<const __half2*>(&v), *reinterpret_cast<const __half2*>(&scale),
+                            *reinterpret_cast<const __half2*>(&z));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+__device__ __forceinline__ uint32_t less_low(uint32_t v, const ScaledZero& z) { return scaled_sum(v, z.scale, z.low); }
+__device__ __forceinline__ uint32_t less_high(uint32_t v, const ScaledZero& z) { return scaled_sum(v, z.high_scale, z.high); }
 __device__ __forceinline__ uint32_t less_low(uint32_t v, const Zero& z) {
   const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&v), *reinterpret_cast<const __half2*>(&z.low));
   return *reinterpret_cast<const uint32_t*>(&d);
@@ -117,14 +128,46 @@ __device__ __forceinline__ uint32_t less_high(uint32_t v, const Zero& z) {
                             *reinterpret_cast<const __half2*>(&z.high));
   return *reinterpret_cast<const uint32_t*>(&d);
 }
-__device__ __forceinline__ uint32_t low_codes(uint32_t w, const Zero& z) {        // at bits 0 and 16
+template <typename Z>
+__device__ __forceinline__ uint32_t low_codes(uint32_t w, const Z& z) {           // at bits 0 and 16
   return less_low(masked<0x000F000Fu>(w, z.base), z);
 }
-__device__ __forceinline__ uint32_t high_codes(uint32_t w, const Zero& z) {       // at bits 4 and 20
+template <typename Z>
+__device__ __forceinline__ uint32_t high_codes(uint32_t w, const Z& z) {          // at bits 4 and 20
   return less_high(masked<0x00F000F0u>(w, z.base), z);
 }
-__device__ __forceinline__ uint32_t byte_codes(uint32_t w, uint32_t bytes, const Zero& z) {
+template <typename Z>
+__device__ __forceinline__ uint32_t byte_codes(uint32_t w, uint32_t bytes, const Z& z) {
   return less_low(__byte_perm(w, z.base, bytes), z);
+}
+
+// What a step's values are turned and weighted with, found once by the lane of
+// each value for all that need it: at `to`, log2 f and 1 / f of each (its weight
+// adds 0 to the sum of weights where no key is, or where f is NaN: whatever lies
+// there must not meet a weight of 0, nor may a NaN that a row does not see reach
+// its sum), then of each two a ScaledZero.
+template <typename S, int BITS>
+__device__ __forceinline__ void prepare_values(uint32_t metas, uint32_t to, bool there) {
+  const int lane = threadIdx.x & 31;
+  if (S::kStep == 32 || lane < S::kStep) {
+    uint32_t meta;
+    load_words<4>(metas + 4 * lane, &meta);
+    if (!there) meta = 0;
+    const float f = value_factor(meta), log = log2_of(f), per = there && f == f ? reciprocal(f) : 0.0f;
+    asm volatile("st.shared.v2.f32 [%0], {%1, %2};" :: "r"(to + 8 * lane), "f"(log), "f"(per) : "memory");
+    const uint32_t scale = value_scale(meta), scales = __byte_perm(scale, scale, 0x1010), zs = __byte_perm(meta, meta, 0x3232);
+    const __half2 zero = __hmul2(__hsub2(__floats2half2_rn(-1024.0f, -64.0f), *reinterpret_cast<const __half2*>(&zs)),
+                                 *reinterpret_cast<const __half2*>(&scales));
+    const uint32_t zeros = *reinterpret_cast<const uint32_t*>(&zero), at = to + 8 * S::kStep + S::kPairBytes * (lane >> 1) + 2 * (lane & 1);
+    asm volatile("st.shared.b16 [%0], %1;" :: "r"(at), "h"((unsigned short)zeros) : "memory");
+    asm volatile("st.shared.b16 [%0], %1;" :: "r"(at + 4), "h"((unsigned short)scale) : "memory");
+    if constexpr (BITS == 4) {
+      const __half sixteenth = __hmul(__ushort_as_half((unsigned short)scale), __float2half_rn(0.0625f));
+      asm volatile("st.shared.b16 [%0], %1;" :: "r"(at + 8), "h"((unsigned short)(zeros >> 16)) : "memory");
+      asm volatile("st.shared.b16 [%0], %1;" :: "r"(at + 12), "h"(__half_as_ushort(sixteenth)) : "memory");
+    }
+  }
+  __syncwarp();
 }
 
 // Loads the unit's rows as operands: for each matrix instruction, eight of rows
@@ -181,6 +224,7 @@ __global__ void __launch_bounds__(kThreads, (Few<D, BITS, NR>::kBlocks)) attenti
   uint8_t* const query = raw + (S::kBytes - S::kQuery);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, quad = lane & 3;
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(raw) + warp * S::kStages * S::kStage;
+  const uint32_t steps = (uint32_t)__cvta_generic_to_shared(raw) + kWarps * S::kStages * S::kStage + warp * S::kSteps;
   const uint32_t base1024 = unknown(0x64006400u);
   pdl_wait();
   pdl_trigger();
@@ -294,6 +338,7 @@ __global__ void __launch_bounds__(kThreads, (Few<D, BITS, NR>::kBlocks)) attenti
       const uint32_t absent = missing >> (stage * kSubs) & ((1u << kSubs) - 1);
       if (key < end && absent != (1u << kSubs) - 1) {      // the whole warp
         const uint32_t base = ring + stage * S::kStage, meta = base + 2 * kStep * S::kRowBytes;
+        prepare_values<S, BITS>(meta + 4 * kStep, steps, key + lane < end && !(absent >> (lane >> 4) & 1));
         // S^T of keys 16 sub + g (+ 8) and rows 8 o + 2 quad (+ 1).
         float scores[kSubs][NR][4];
 #pragma unroll
@@ -302,14 +347,13 @@ __global__ void __launch_bounds__(kThreads, (Few<D, BITS, NR>::kBlocks)) attenti
           for (int o = 0; o < NR; ++o)
 #pragma unroll
             for (int k = 0; k < 4; ++k) scores[sub][o][k] = 0.0f;
-        uint32_t vmeta[kSubs][2], kmeta[kSubs][2];
+        uint32_t kmeta[kSubs][2];
         Zero z[kSubs][2];
 #pragma unroll
         for (int sub = 0; sub < kSubs; ++sub)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             load_words<4>(meta + (16 * sub + 8 * h + g) * 4, &kmeta[sub][h]);
-            load_words<4>(meta + (kStep + 16 * sub + 8 * h + g) * 4, &vmeta[sub][h]);
             z[sub][h] = zero_of(__byte_perm(kmeta[sub][h], kmeta[sub][h], 0x3232), base1024);
           }
         {
@@ -355,14 +399,15 @@ __global__ void __launch_bounds__(kThreads, (Few<D, BITS, NR>::kBlocks)) attenti
           }
         }
         const bool inside = key >= all_from && key + kStep <= all_to && absent == 0;     // every row sees all
-        float per[kSubs][2];                               // 1 / step of the values
+        float per[kSubs][2];                               // 1 / f of the values
 #pragma unroll
         for (int sub = 0; sub < kSubs; ++sub)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float ks = meta_step(kmeta[sub][h]), vs = value_step(vmeta[sub][h]);
-            const float log = log2_of(vs);
-            per[sub][h] = reciprocal(vs);
+            uint32_t two[2];
+            load_words<8>(steps + 8 * (16 * sub + 8 * h + g), two);
+            const float ks = meta_step(kmeta[sub][h]), log = __uint_as_float(two[0]);
+            per[sub][h] = __uint_as_float(two[1]);
 #pragma unroll
             for (int o = 0; o < NR; ++o) {
               float &s0 = scores[sub][o][2 * h], &s1 = scores[sub][o][2 * h + 1];
@@ -376,10 +421,7 @@ __global__ void __launch_bounds__(kThreads, (Few<D, BITS, NR>::kBlocks)) attenti
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int k = key + 16 * sub + 8 * h + g;
-              // Whatever lies where no key is must not meet a weight of 0, nor may
-              // a NaN that a row does not see reach its sum: the weight adds 0.
               const bool there = k < end && !(absent >> sub & 1);
-              if (!there || !(per[sub][h] > 0.0f)) per[sub][h] = 0.0f;
 #pragma unroll
               for (int o = 0; o < NR; ++o)
 #pragma unroll
@@ -399,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, (Few<D, BITS, NR>::kBlocks)) attenti
             top[o][e] = m[o][e];
 #pragma unroll
             for (int sub = 0; sub < kSubs; ++sub) top[o][e] = max3(top[o][e], scores[sub][o][e], scores[sub][o][2 + e]);
-            passed |= top[o][e] - m[o][e] > kAhead;
+            passed |= top[o][e] - m[o][e] > kMostWeight;
           }
         if (__any_sync(kFull, passed)) {
 #pragma unroll
@@ -409,6 +451,7 @@ __global__ void __launch_bounds__(kThreads, (Few<D, BITS, NR>::kBlocks)) attenti
               float v = top[o][e];
 #pragma unroll
               for (int off = 4; off < 32; off <<= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, off));
+              v = raised<kAhead>(m[o][e], v);
               top[o][e] = exp2_of(m[o][e] - v);
               m[o][e] = v;
               l[o][e] *= top[o][e];
@@ -446,17 +489,18 @@ __global__ void __launch_bounds__(kThreads, (Few<D, BITS, NR>::kBlocks)) attenti
         const uint32_t values = base + kStep * S::kRowBytes;
 #pragma unroll
         for (int sub = 0; sub < kSubs; ++sub) {
-          Zero zv[2];
+          ScaledZero zv[2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            uint32_t two[2];
-            load_words<8>(meta + (kStep + 16 * sub + 8 * h + 2 * quad) * 4, two);
-            if (!inside) {                                 // (as above: no NaN where no key is)
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                if (key + 16 * sub + 8 * h + 2 * quad + e >= end || (absent >> sub & 1)) two[e] = 0;
+            uint32_t found[S::kPairBytes / 4];
+            load_words<S::kPairBytes>(steps + 8 * kStep + S::kPairBytes * (8 * sub + 4 * h + quad), found);
+            zv[h].low = found[0];
+            zv[h].scale = found[1];
+            if constexpr (BITS == 4) {
+              zv[h].high = found[2];
+              zv[h].high_scale = found[3];
             }
-            zv[h] = zero_of(__byte_perm(two[0], two[1], 0x7632), base1024);
+            zv[h].base = base1024;
           }
 #pragma unroll
           for (int piece = 0; piece < kPieces; ++piece) {

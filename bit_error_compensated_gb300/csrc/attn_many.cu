@@ -9,14 +9,14 @@
 // where K and V hold codes less their zero points, exact in f16.  Warps of the
 // block:
 //   8 a tile of rows   take S out of TMEM, turn scores into weights and put P
-//                      back: p = exp(score + log s_v - m), see attn_few.cu, so
-//                      that no value is multiplied by its step;
+//                      back (attn_common.h says what of a value's step is in
+//                      the weight and what in the value);
 //   4 for the keys, 4 for the values
 //                      turn a tile's codes, loaded one tile ahead;
 //   1 issues the matrix instructions.
-// The maximum m of a row is raised only when a score passes it by 2^8, so O in
-// TMEM is rescaled a few times a row, and the weights are made in one pass over
-// S.  While one tile's weights are made, the tensor cores work for the other (with one tile
+// What a row's weights are scaled by changes only when a score passes the ones
+// before by 2^kAhead, so O in TMEM is rescaled a few times a row, and the weights are
+// made in one pass over S.  While one tile's weights are made, the tensor cores work for the other (with one tile
 // of rows: on the next tile's scores).
 //
 // A lane has two neighbouring keys of every eight and two rows of the warp's
@@ -49,8 +49,9 @@ constexpr int kSlots = 4;                               // of steps: tiles whose
 constexpr int kWarpsWeights = 16, kWarpsKeys = 4, kWarpsValues = 4;
 constexpr int kIssuer = kWarpsWeights + kWarpsKeys + kWarpsValues, kThreads = 32 * (kIssuer + 4);
 constexpr int kWeightRegs = 88, kTurnRegs = 56, kIssueRegs = 40;
+// (4, as attn_few.cu has it for nothing: a prompt of 8192 in 779 us; 6: 757, 7: 746, 8: 735)
+constexpr int kAhead = 8;
 static_assert(4 * kWeightRegs + 2 * kTurnRegs + kIssueRegs <= 7 * 72, "a split above the launch's registers never ends");
-constexpr float kAhead = 8.0f;
 
 template <int D, int BITS>
 struct Many {
@@ -170,27 +171,30 @@ struct Bars {
 };
 
 // Eight codes of a word (4 bits) as (0, 4), (1, 5), (2, 6), (3, 7), or of two
-// (8 bits) in order, less the zero point.  low: 1024 + z, high: -(64 + z), twice.
-__device__ __forceinline__ uint32_t less(uint32_t v, uint32_t z) {
-  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&v), *reinterpret_cast<const __half2*>(&z));
+// (8 bits) in order, less the zero point, times S (1 for keys).  low: -(1024 + z)
+// S, high: -(64 + z) S, scale and high_scale S and S / 16, all twice.
+__device__ __forceinline__ uint32_t less(uint32_t v, uint32_t scale, uint32_t z) {
+  const __half2 d = __hfma2(*reinterpret_cast<const __half2*>(&v), *reinterpret_cast<const __half2*>(&scale),
+                            *reinterpret_cast<const __half2*>(&z));
   return *reinterpret_cast<const uint32_t*>(&d);
 }
-__device__ __forceinline__ uint32_t less_high(uint32_t v, uint32_t z) {
-  const __half2 d = __hfma2(*reinterpret_cast<const __half2*>(&v), __float2half2_rn(0.0625f), *reinterpret_cast<const __half2*>(&z));
+__device__ __forceinline__ uint32_t times_half(uint32_t a, float b) {
+  const __half2 d = __hmul2(*reinterpret_cast<const __half2*>(&a), __float2half2_rn(b));
   return *reinterpret_cast<const uint32_t*>(&d);
 }
-__device__ __forceinline__ void turn4(uint32_t w, uint32_t base, uint32_t low, uint32_t high, uint32_t (&h)[4]) {
+__device__ __forceinline__ void turn4(uint32_t w, uint32_t base, uint32_t scale, uint32_t low, uint32_t high_scale, uint32_t high,
+                                      uint32_t (&h)[4]) {
   const uint32_t up = w >> 8;
-  h[0] = less(masked<0x000F000Fu>(w, base), low);
-  h[1] = less_high(masked<0x00F000F0u>(w, base), high);
-  h[2] = less(masked<0x000F000Fu>(up, base), low);
-  h[3] = less_high(masked<0x00F000F0u>(up, base), high);
+  h[0] = less(masked<0x000F000Fu>(w, base), scale, low);
+  h[1] = less(masked<0x00F000F0u>(w, base), high_scale, high);
+  h[2] = less(masked<0x000F000Fu>(up, base), scale, low);
+  h[3] = less(masked<0x00F000F0u>(up, base), high_scale, high);
 }
-__device__ __forceinline__ void turn8(uint32_t a, uint32_t b, uint32_t base, uint32_t low, uint32_t (&h)[4]) {
-  h[0] = less(__byte_perm(a, base, 0x5150), low);
-  h[1] = less(__byte_perm(a, base, 0x5352), low);
-  h[2] = less(__byte_perm(b, base, 0x5150), low);
-  h[3] = less(__byte_perm(b, base, 0x5352), low);
+__device__ __forceinline__ void turn8(uint32_t a, uint32_t b, uint32_t base, uint32_t scale, uint32_t low, uint32_t (&h)[4]) {
+  h[0] = less(__byte_perm(a, base, 0x5150), scale, low);
+  h[1] = less(__byte_perm(a, base, 0x5352), scale, low);
+  h[2] = less(__byte_perm(b, base, 0x5150), scale, low);
+  h[3] = less(__byte_perm(b, base, 0x5352), scale, low);
 }
 // The rows of tile t of a unit into shared memory, as the A operand (K-major);
 // a warp takes 16 of them, from row0.  They are scaled by one power of two, from the
@@ -480,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
         if (!value) {
           asm volatile("st.shared.f32 [%0], %1;" :: "r"(at), "f"(meta_step(meta)) : "memory");
         } else {
-          const float of = value_step(meta);
+          const float of = value_factor(meta);
           const float log = there ? log2_of(of) : kNone, per = there && of == of ? reciprocal(of) : 0.0f;
           asm volatile("st.shared.f32 [%0], %1;" :: "r"(at + 4 * KT), "f"(log) : "memory");
           asm volatile("st.shared.f32 [%0], %1;" :: "r"(at + 8 * KT), "f"(per) : "memory");
@@ -488,10 +492,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
       }
       __syncwarp();
       if (lane == 0) arrive_here(bar + B::kSteps + 8 * (i & (kSlots - 1)));
-      const uint32_t zs = __byte_perm(meta, meta, 0x3232);
-      const __half2 z = *reinterpret_cast<const __half2*>(&zs);
-      const __half2 z_low = __hadd2(z, __float2half2_rn(1024.0f)), z_high = __hneg2(__hadd2(z, __float2half2_rn(64.0f)));
-      const uint32_t my_low = *reinterpret_cast<const uint32_t*>(&z_low), my_high = *reinterpret_cast<const uint32_t*>(&z_high);
+      // Of this lane's row: -(1024 + z) S and -(64 + z) S in one word, S in another
+      // (with 8 bits in the first one's upper half).
+      const uint32_t zs = __byte_perm(meta, meta, 0x3232), my_scale = value ? value_scale(meta) : 0x3C00u;
+      const uint32_t scales = __byte_perm(my_scale, my_scale, 0x1010);
+      const __half2 both = __hmul2(__hsub2(__floats2half2_rn(-1024.0f, -64.0f), *reinterpret_cast<const __half2*>(&zs)),
+                                   *reinterpret_cast<const __half2*>(&scales));
+      uint32_t my_zero = *reinterpret_cast<const uint32_t*>(&both);
+      if constexpr (BITS == 8) my_zero = __byte_perm(my_zero, my_scale, 0x5410);
       const uint32_t to = stages + (i & 1) * S::kStage;
       // A piece's eights are stored in an order by piece, so that eight lanes that
       // store together (one, two or four rows) meet no bank twice.
@@ -500,8 +508,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
 #pragma unroll
       for (int p = 0; p < kLoads; ++p) {
         const int row = p * kWide + in_row;
-        const uint32_t low = __shfl_sync(kFull, my_low, row);
-        const uint32_t high = BITS == 4 ? __shfl_sync(kFull, my_high, row) : 0;
+        const uint32_t zero = __shfl_sync(kFull, my_zero, row), low = __byte_perm(zero, zero, 0x1010),
+                       upper = __byte_perm(zero, zero, 0x3232);
+        const uint32_t scale = BITS == 4 ? __shfl_sync(kFull, scales, row) : upper;
+        const uint32_t high_scale = BITS == 4 ? times_half(scale, 0.0625f) : 0;
         const uint32_t at = to + (row0 + row) * 128;
         uint32_t words[4] = {w[p].x, w[p].y, w[p].z, w[p].w};
         if constexpr (BITS == 4) {
@@ -522,8 +532,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
           uint32_t h[4];
-          if constexpr (BITS == 4) turn4(words[c], base1024, low, high, h);
-          else turn8(words[2 * c], words[2 * c + 1], base1024, low, h);
+          if constexpr (BITS == 4) turn4(words[c], base1024, scale, low, high_scale, upper, h);
+          else turn8(words[2 * c], words[2 * c + 1], base1024, scale, low, h);
           const int chunk = piece * kChunks + (c ^ turn);
           store_shared16(at + (chunk >> 3) * (KT * 128) + (((chunk & 7) ^ ((row0 + row) & 7)) << 4), h);
         }
@@ -597,6 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
             for (int h = 0; h < 2; ++h) {
               top[h] = fmaxf(top[h], __shfl_xor_sync(kFull, top[h], 1));
               top[h] = fmaxf(top[h], __shfl_xor_sync(kFull, top[h], 2));
+              top[h] = raised<kAhead>(m[h], top[h]);
               f[h] = exp2_of(m[h] - top[h]);
               m[h] = top[h];
               l[h][0] *= f[h];
@@ -673,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
                     top[h] = max3(top[h], v0, v1);
                   }
                 }
-                if (__any_sync(kFull, top[0] - m[0] > kAhead || top[1] - m[1] > kAhead)) raise(top, c);
+                if (__any_sync(kFull, top[0] - m[0] > kMostWeight || top[1] - m[1] > kMostWeight)) raise(top, c);
                 uint32_t w[8];
 #pragma unroll
                 for (int n = 0; n < 4; ++n) {

@@ -690,10 +690,14 @@ int echo_cache_read(const echo_cache* cache, const echo_batch* batch, int dtype,
  *   workspace  16-byte-aligned device memory of at least
  *          echo_attention_workspace_bytes bytes, overlapping nothing else
  *          (ECHO_ERR_TOO_LARGE if NULL or smaller); one call at a time
- * Codes less their zero point are exact in the 16-bit operands of the matrix
- * instructions, sums, maxima and steps are fp32, and w_j times v's step is
- * rounded to 11 bits.  A repeated call gives the same bits; another batch may
- * split a sequence differently and round differently.
+ * Codes less their zero point, and values less what their step exceeds a power
+ * of two by (1 to 2, for steps from 2^-14 to 2^6), are exact in the 16-bit operands
+ * of the matrix instructions; sums, maxima and steps are fp32.  w_j times that
+ * rest is rounded to 11 bits; where it is below 2^-20 of the largest that a row
+ * has met, to a multiple of 2^-30 of that (2^-24 and 2^-34 in batches of at most
+ * 64 rows of queries a sequence and head of the cache, on average), and the sum of w_j has no
+ * part in this.  A repeated call gives the same bits; another batch may split a
+ * sequence differently and round differently.
  */
 int echo_attention(const echo_cache* cache, const echo_batch* batch, int64_t heads, int dtype,
                    const echo_heads* q, const echo_heads* out, float scale, int causal,
