@@ -248,23 +248,25 @@ __global__ void __launch_bounds__(kThreads, (Few<D, BITS, NR>::kBlocks)) attenti
     uint32_t missing = 0;                                  // 16 keys of a stage without a page, a bit each
     // The pages of a step's sixteens of keys (the same one where a page is larger),
     // as the table has them: what is there is looked at a step later, since a use
-    // right away would wait for it.
+    // right away would wait for it.  Pages wholly behind the rows' window (`from` in the
+    // first tile, 0 past it) may be gone.
+    auto wanted = [&](int t, int key, int from) { return t < tiles && key < end && key + 16 > from; };
     struct Pages {
       int of[kSubs];
     };
-    auto look_up = [&](int t) {
+    auto look_up = [&](int t, int from) {
       Pages p;
 #pragma unroll
       for (int sub = 0; sub < kSubs; ++sub) {
         const int key = key0 + t * kTile + 16 * sub;
         const int at = key >> a.cache.page_shift;
         p.of[sub] = -1;
-        if (t < tiles && key < end && at < a.batch.table_pages)
+        if (wanted(t, key, from) && at < a.batch.table_pages)
           p.of[sub] = a.batch.table[(int64_t)u.sequence * a.batch.ld_table + at];
       }
       return p;
     };
-    auto issue = [&](int t, const Pages& pages, int stage) {
+    auto issue = [&](int t, const Pages& pages, int stage, int from) {
 #pragma unroll
       for (int sub = 0; sub < kSubs; ++sub) {
         const int key = key0 + t * kTile + 16 * sub, page = pages.of[sub];
@@ -287,17 +289,18 @@ __global__ void __launch_bounds__(kThreads, (Few<D, BITS, NR>::kBlocks)) attenti
                          a.cache.meta + group + (lane < 4 ? 0 : values_on) + 4 * (lane & 3));
         } else {
           missing |= bit;
-          if (t < tiles && key < end) bad |= kBadPage;
+          if (wanted(t, key, from)) bad |= kBadPage;
         }
       }
       copies_commit();
     };
     // (the first copies are under way before the rows are loaded)
-    Pages pages = look_up(0);
+    const int from = keys_from(a, first_place);
+    Pages pages = look_up(0, from);
 #pragma unroll 1
     for (int t = 0; t < S::kStages - 1; ++t) {
-      issue(t, pages, t);
-      pages = look_up(t + 1);
+      issue(t, pages, t, t == 0 ? from : 0);
+      pages = look_up(t + 1, 0);
     }
     if (a.dtype == ECHO_BF16) load_queries<__nv_bfloat16, D, BITS, NR>(a, s, u, query, factor);
     else load_queries<__half, D, BITS, NR>(a, s, u, query, factor);
@@ -534,8 +537,8 @@ __global__ void __launch_bounds__(kThreads, (Few<D, BITS, NR>::kBlocks)) attenti
         }
       }
       __syncwarp();                                        // before the stage is overwritten
-      const Pages next = look_up(t + S::kStages);
-      issue(t + S::kStages - 1, pages, ahead);
+      const Pages next = look_up(t + S::kStages, 0);
+      issue(t + S::kStages - 1, pages, ahead, 0);
       pages = next;
       stage = stage + 1 == S::kStages ? 0 : stage + 1;
       ahead = ahead + 1 == S::kStages ? 0 : ahead + 1;

@@ -438,18 +438,19 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
     // A row's page is looked up two tiles ahead (and looked at one ahead: a use
     // right away would wait for it), its codes are loaded one ahead.
     int ahead = 0, page = 0, page_key = 0, page_head = 0;  // tiles into the unit of the page that is looked up next
-    enum { kNoKey, kNoPage, kPage };
-    int found = kNoKey;
     const uint32_t n = (uint32_t)(range.end - range.begin);
     auto look_up = [&]() {
-      found = kNoKey;
+      page_key = -1;                                       // no key for this lane
       if (!__any_sync(kFull, walk.more())) return;
       page_key = (walk.unit.tile + walk.in + ahead) * KT + r;
       page_head = walk.unit.head;
-      if (row_lane && page_key < walk.s.keys) {
+      if (!row_lane || page_key >= walk.s.keys) page_key = -1;
+      // (pages wholly behind the window of the unit's first row may be gone)
+      if (ahead == 0 && a.window && page_key < keys_from(a, walk.s.place + walk.unit.first / a.group)) page_key = -1;
+      if (page_key >= 0) {
         const int at = page_key >> a.cache.page_shift;
-        found = at < a.batch.table_pages ? kPage : kNoPage;
-        if (found == kPage) page = a.batch.table[(int64_t)walk.unit.sequence * a.batch.ld_table + at];
+        page = -1;
+        if (at < a.batch.table_pages) page = a.batch.table[(int64_t)walk.unit.sequence * a.batch.ld_table + at];
       }
       if (++ahead == walk.take) {
         ahead = 0;
@@ -458,8 +459,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
     };
     // Rows that are not there have codes of 0, less 0.
     auto load = [&]() {
-      there = found == kPage && page >= 0 && page < a.cache.pages;
-      if (found != kNoKey && !there) bad |= kBadPage;
+      there = page_key >= 0 && page >= 0 && page < a.cache.pages;
+      if (page_key >= 0 && !there) bad |= kBadPage;
       const int64_t group = there ? group_index(a.cache, page, page_head, page_key) + on : -1;
       meta = 0;
       if (there) meta = a.cache.meta[group];

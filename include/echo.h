@@ -681,6 +681,8 @@ int echo_cache_read(const echo_cache* cache, const echo_batch* batch, int dtype,
  * with the keys and values of head h / (heads / cache->heads) at the places j
  * that token t sees: all up to its own place p with causal = 1 (of these the
  * last `window` if window > 0), all of the sequence with causal = 0 (window 0).
+ * Pages wholly behind the windows of a sequence's tokens may be gone: nothing in
+ * them is read, and what the table holds for them is not looked at.
  * The tokens' own keys and values have to be in the cache.  A token that sees
  * nothing gets zeros.
  *   heads  of q and out, a multiple of the cache's
