@@ -186,14 +186,21 @@ def _state_dtypes(fmt: int):
 def _stream(stream, device=None) -> int | None:
     """The raw stream; of the current device (its number, where the caller has it) if None."""
     if stream is None:
-        import torch
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if raw is not None:                       # without making a Stream object: 0.1 us, not 3
-            return raw(torch.cuda.current_device() if device is None else device)
-        return torch.cuda.current_stream().cuda_stream
+        global _raw_stream
+        if _raw_stream is None:
+            import torch
+            # (where torch has it, without making a Stream object: 0.1 us, not 3)
+            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda n: torch.cuda.current_stream(n).cuda_stream)
+        if device is None:
+            import torch
+            device = torch.cuda.current_device()
+        return _raw_stream(device)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+_raw_stream = None
 
 
 class Plan:
@@ -722,24 +729,32 @@ def echo_linear_int8(x, w, w_scales, out, codes, scales, stream=None) -> None:
 # A serving step between two all-reduces: the cache, the attention over it, and
 # products of few tokens with 4-bit weights.
 
-class Cache:
+class _Described:
+    """Keeps a packed description of its tensors.  A call makes it anew, and checks
+    them, where an attribute was assigned since, or where a tensor's address or size
+    (the distance of a table's rows) has changed in place."""
+
+    __slots__ = ("_at", "_packed")
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        if name[0] != "_":
+            object.__setattr__(self, "_at", None)
+
+
+class Cache(_Described):
     """A paged cache of keys and values in 4- or 8-bit groups (include/echo.h):
     codes uint8 [pages][2][heads][page_size][head_dim * bits / 8] and meta int32
     [pages][2][heads][page_size], contiguous tensors on one device, made here
-    (zeros, on the current device) where they are not given.  A call reads their
-    addresses again, and checks the tensors anew where one has changed."""
+    (zeros, on the current device) where they are not given.  The attributes may be
+    assigned; what they are together is checked by the next call."""
 
-    __slots__ = ("pages", "page_size", "heads", "head_dim", "bits", "device", "codes", "meta", "_at", "_packed")
+    __slots__ = ("pages", "page_size", "heads", "head_dim", "bits", "device", "codes", "meta")
 
     def __init__(self, pages: int, page_size: int, heads: int, head_dim: int, bits: int, codes=None, meta=None):
         import torch
-        for v, what, known in ((page_size, "page_size", (16, 32, 64, 128, 256)), (head_dim, "head_dim", (64, 128, 256)),
-                               (bits, "bits", (4, 8))):
-            if v not in known:
-                raise ValueError(f"{what}: {v}, expected one of {known}")
-        if pages < 0 or not 1 <= heads <= ECHO_CACHE_MAX_HEADS:
-            raise ValueError(f"pages {pages}, heads {heads}: expected pages >= 0 and heads in 1..{ECHO_CACHE_MAX_HEADS}")
         self.pages, self.page_size, self.heads, self.head_dim, self.bits = pages, page_size, heads, head_dim, bits
+        self._check_sizes()
         if (codes is None) != (meta is None):
             raise ValueError("codes and meta belong together")
         if codes is None:
@@ -752,38 +767,58 @@ class Cache:
         shape = (self.pages, 2, self.heads, self.page_size)
         return shape + (self.head_dim * self.bits // 8,) if codes else shape
 
+    def _check_sizes(self) -> None:
+        for what, known in (("page_size", (16, 32, 64, 128, 256)), ("head_dim", (64, 128, 256)), ("bits", (4, 8))):
+            v = getattr(self, what)
+            if v not in known:
+                raise ValueError(f"{what}: {v}, expected one of {known}")
+        if self.pages < 0 or not 1 <= self.heads <= ECHO_CACHE_MAX_HEADS:
+            raise ValueError(f"pages {self.pages}, heads {self.heads}: "
+                             f"expected pages >= 0 and heads in 1..{ECHO_CACHE_MAX_HEADS}")
+
+    def _now(self) -> tuple:
+        codes, meta = self.codes, self.meta
+        return codes.data_ptr(), meta.data_ptr(), codes.numel(), meta.numel()
+
     def _check(self) -> None:
         import torch
         self._at = None                           # a call after a refusal checks again
+        self._check_sizes()
         if not self.codes.is_cuda:
             raise ValueError("codes: tensor must be on a CUDA device")
         self.device = self.codes.get_device()
         _expect_contiguous(self.codes, "codes", torch.uint8, self._shape(True), self.device)
         _expect_contiguous(self.meta, "meta", torch.int32, self._shape(False), self.device)
-        at = (self.codes.data_ptr(), self.meta.data_ptr())
-        if self.pages and 0 in at:
+        at = self._now()
+        if self.pages and 0 in at[:2]:
             raise ValueError("the cache's storage was freed")
-        self._packed = _CACHE.pack(*at, self.pages, self.page_size, self.heads, self.head_dim, self.bits)
+        self._packed = _CACHE.pack(*at[:2], self.pages, self.page_size, self.heads, self.head_dim, self.bits)
         self._at = at
 
     def _pack(self) -> bytes:
-        if (self.codes.data_ptr(), self.meta.data_ptr()) != self._at:
+        if self._at is None or self._now() != self._at:
             self._check()
         return self._packed
 
 
-class CacheBatch:
+class CacheBatch(_Described):
     """New tokens of several sequences (include/echo.h): starts int32 [sequences
     + 1], lengths int32 [sequences], both contiguous, and table int32
     [sequences][pages] (rows at any distance), on the cache's device.  The
-    kernels read what the tensors hold when they run; a call reads the tensors'
-    addresses again, and checks them anew where one has changed."""
+    kernels read what the tensors hold when they run.  The tensors may be assigned
+    (a step's first n of the largest batch's); whether they fit each other is
+    checked by the next call."""
 
-    __slots__ = ("starts", "lengths", "table", "sequences", "device", "_at", "_rest", "_packed")
+    __slots__ = ("starts", "lengths", "table", "sequences", "device", "_rest")
 
     def __init__(self, starts, lengths, table):
         self.starts, self.lengths, self.table = starts, lengths, table
         self._check()
+
+    def _now(self) -> tuple:
+        starts, lengths, table = self.starts, self.lengths, self.table
+        return (starts.data_ptr(), lengths.data_ptr(), table.data_ptr(), starts.numel(), lengths.numel(), table.numel(),
+                table.stride(0))
 
     def _check(self) -> None:
         import torch
@@ -797,7 +832,7 @@ class CacheBatch:
         _expect(self.table, "table", torch.int32, (self.sequences, pages), self.device)
         _expect_contiguous(self.lengths, "lengths", torch.int32, (self.sequences,), self.device)
         _expect_contiguous(self.starts, "starts", torch.int32, (self.sequences + 1,), self.device)
-        at = (self.starts.data_ptr(), self.lengths.data_ptr(), self.table.data_ptr())
+        at = self._now()
         if self.sequences and (0 in at[:2] or (pages and at[2] == 0)):
             raise ValueError("the batch's storage was freed")
         self._rest = (pages, self.table.stride(0) if self.sequences > 1 else pages)
@@ -805,13 +840,13 @@ class CacheBatch:
         self._at = at
 
     def _pack(self, tokens: int) -> bytes:
-        if (self.starts.data_ptr(), self.lengths.data_ptr(), self.table.data_ptr()) != self._at:
+        if self._at is None or self._now() != self._at:
             self._check()
         packed = self._packed.get(tokens)
         if packed is None:
             if len(self._packed) > 64:            # token counts of steps past
                 self._packed.clear()
-            packed = self._packed[tokens] = _BATCH.pack(self.sequences, tokens, *self._at, *self._rest)
+            packed = self._packed[tokens] = _BATCH.pack(self.sequences, tokens, *self._at[:3], *self._rest)
         return packed
 
 
@@ -825,10 +860,16 @@ def _expect_heads(t, what: str, dtype, shape, device) -> bytes:
 
 
 def _current_device() -> int:
-    """torch.cuda.current_device() without its checks, where torch has that."""
-    import torch
-    raw = getattr(torch._C, "_cuda_getDevice", None)
-    return raw() if raw is not None and torch.cuda.is_initialized() else torch.cuda.current_device()
+    """torch.cuda.current_device(), without its checks after the first call where torch has that."""
+    global _raw_device
+    if _raw_device is None:
+        import torch
+        torch.cuda.current_device()
+        _raw_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    return _raw_device()
+
+
+_raw_device = None
 
 
 def _serving_device(cache: Cache, batch: CacheBatch, t) -> int:
@@ -851,8 +892,9 @@ def _cache_rows(fn, call: str, cache: Cache, batch: CacheBatch, k, v, stream) ->
     shape, dtype = first.shape, first.dtype
     if len(shape) != 3 or shape[1] != cache.heads or shape[2] != cache.head_dim:
         raise ValueError(f"k, v: shape {tuple(shape)}, expected (tokens, {cache.heads}, {cache.head_dim})")
+    packed, rows = cache._pack(), batch._pack(shape[0])      # (which may find them on another device)
     code, device = _dtype_code(dtype), _serving_device(cache, batch, first)
-    status = fn(cache._pack(), batch._pack(shape[0]), code,
+    status = fn(packed, rows, code,
                 None if k is None else _expect_heads(k, "k", dtype, shape, device),
                 None if v is None else _expect_heads(v, "v", dtype, shape, device), _stream(stream, device))
     if status:
@@ -893,6 +935,7 @@ def echo_attention(cache: Cache, batch: CacheBatch, q, out, scale: float | None 
     tokens, heads, dim = shape
     if heads < 1 or heads % cache.heads:
         raise ValueError(f"q: {heads} heads, expected a multiple of the cache's {cache.heads}")
+    packed, rows = cache._pack(), batch._pack(tokens)        # (which may find them on another device)
     device = _serving_device(cache, batch, q)
     at_q = _expect_heads(q, "q", dtype, shape, device)
     at_out = _expect_heads(out, "out", dtype, shape, device)
@@ -900,7 +943,6 @@ def echo_attention(cache: Cache, batch: CacheBatch, q, out, scale: float | None 
     if lse is not None:
         _expect_contiguous(lse, "lse", torch.float32, (tokens, heads), device)
         at_lse = lse.data_ptr()
-    packed, rows = cache._pack(), batch._pack(tokens)
     nbytes = _attention_bytes.get((device, dim))             # the size depends on nothing else
     if nbytes is None:
         nbytes = _lib.echo_attention_workspace_bytes(packed, rows, heads)
