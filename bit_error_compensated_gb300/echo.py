@@ -953,7 +953,8 @@ def echo_attention(cache: Cache, batch: CacheBatch, q, out, scale: float | None 
     raw = _stream(stream, device)
     if stream is None and not torch.cuda.is_current_stream_capturing():
         with _workspace_lock:                                # a call's two kernels follow each other
-            status = _lib.echo_attention(*args, _kept_workspace(nbytes, device, raw), nbytes, raw)
+            kept = _kept_workspace(nbytes, device, raw)      # (until after the launches)
+            status = _lib.echo_attention(*args, kept[0], nbytes, raw)
     else:
         keep, at = _workspace(nbytes, q.device, stream)
         status = _lib.echo_attention(*args, at, nbytes, raw)
@@ -961,19 +962,30 @@ def echo_attention(cache: Cache, batch: CacheBatch, q, out, scale: float | None 
         raise EchoError(status, "echo_attention")
 
 
-def _kept_workspace(nbytes: int, device: int, raw: int) -> int:
-    """The address of the attention's workspace for a stream, which stays
-    allocated (40 MB at the most): with an allocation between one call's launches
-    and the next's, a call took 7 us longer.  Captured calls have their own."""
+def _kept_workspace(nbytes: int, device: int, raw: int) -> tuple:
+    """(address, bytes, tensor) of the attention's workspace for the current
+    stream, which stays allocated (40 MB at the most, for each of the last
+    _KEPT_STREAMS that had none): with an allocation between one call's launches
+    and the next's, a call took 7 us longer.  One that gives way goes back to its
+    stream's memory, behind what was launched there.  Captured calls have their
+    own, and so have streams that torch did not make: their handles may be
+    another stream's tomorrow, or in each thread."""
     kept = _workspaces.get((device, raw))
     if kept is None or kept[1] < nbytes:
         import torch
         buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        kept = _workspaces[device, raw] = (buf.data_ptr(), nbytes, buf)
-    return kept[0]
+        kept = buf.data_ptr(), nbytes, buf
+        if raw and torch.cuda.current_stream(device).stream_id == raw:
+            return kept
+        mine = [key for key in _workspaces if key[0] == device and key[1] != raw]
+        if len(mine) >= _KEPT_STREAMS:
+            del _workspaces[mine[0]]
+        _workspaces[device, raw] = kept
+    return kept
 
 
-_workspaces = {}                                  # (device, raw stream) -> (address, bytes, tensor)
+_KEPT_STREAMS = 4                                 # a device
+_workspaces = {}                                  # (device, raw stream) -> (address, bytes, tensor), oldest first
 _workspace_lock = threading.Lock()
 _attention_bytes = {}                             # (device, head_dim) -> bytes
 

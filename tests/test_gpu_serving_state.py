@@ -1,5 +1,7 @@
 """What the binding keeps between the serving calls: descriptions of a cache and
-a batch."""
+a batch, and the attention's workspaces."""
+import threading
+
 import pytest
 import torch
 
@@ -115,3 +117,91 @@ def test_a_cache_whose_tensors_change_is_checked_again():
     with pytest.raises(ValueError, match="bits"):
         cache.bits = 5
         attend(cache, batch, q)
+
+
+# ------------------------------------------------------------------ workspaces
+def work(seed, new=1, length=5000):
+    g = gen(seed)
+    counts, lengths = [new, new], [length, length // 3]
+    starts, table, pages = make_batch(counts, lengths, 64, g)
+    cache = full_cache(g, pages, 64, 4, 128, 4)
+    return cache, tensors(starts, lengths, table), values(g, 2 * new, 16, 128, dtype=torch.bfloat16)
+
+
+def test_eager_calls_on_two_streams_at_once():
+    """Parts of units that blocks share lie in the workspace between a call's two
+    kernels: streams that ran at once over one workspace would mix them."""
+    jobs = [work(21), work(22, new=80)]
+    want = [attend(*job) for job in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    outs = [[], []]
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    for _ in range(60):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                outs[i].append(attend(*jobs[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, want[i]) for o in outs[i])
+
+
+@pytest.mark.parametrize("shared", [False, True])
+def test_eager_calls_from_threads(shared):
+    """Four threads, each with a stream of its own or all with one: a call's two
+    kernels follow each other in either case."""
+    jobs = [work(31 + i, new=1 + 40 * (i % 2)) for i in range(4)]
+    want = [attend(*job) for job in jobs]
+    torch.cuda.synchronize()
+    one, bad = torch.cuda.Stream(), []
+
+    def turn(i):
+        try:
+            st = one if shared else torch.cuda.Stream()
+            with torch.cuda.stream(st):
+                outs = [attend(*jobs[i]) for _ in range(40)]
+            st.synchronize()
+            if not all(torch.equal(o, want[i]) for o in outs):
+                bad.append(i)
+        except Exception as e:                               # a thread's own would be lost
+            bad.append((i, e))
+
+    threads = [threading.Thread(target=turn, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert bad == []
+
+
+def test_kept_workspaces_are_few():
+    """A process that goes round many streams keeps the workspaces of a few."""
+    from bit_error_compensated_gb300 import echo
+    job = work(41)
+    want = attend(*job)
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream() for _ in range(14)], []
+    for _ in range(3):
+        for st in streams:
+            with torch.cuda.stream(st):
+                outs.append(attend(*job))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+    assert len(echo._workspaces) <= 4
+
+
+def test_streams_of_others_have_no_kept_workspace():
+    """A raw handle that torch did not make may be another stream's tomorrow."""
+    from bit_error_compensated_gb300 import echo
+    job = work(42)
+    want = attend(*job)
+    mine = torch.cuda.Stream()
+    other = torch.cuda.ExternalStream(mine.cuda_stream)
+    torch.cuda.synchronize()
+    before = set(echo._workspaces)
+    with torch.cuda.stream(other):
+        outs = [attend(*job) for _ in range(5)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+    assert set(echo._workspaces) == before
