@@ -198,8 +198,9 @@ __device__ __forceinline__ GroupStep group_step(float lo, float hi, float L) {
   const float d = __fsub_rn(hi, lo), b = -lo, bb = __fsub_rn(d, hi);
   const float err = __fadd_rn(__fsub_rn(hi, __fsub_rn(d, bb)), __fsub_rn(b, bb));   // hi - lo is d + err
   unsigned short s = __half_as_ushort(__float2half_ru(__fmul_rn(d, 1.0f / L)));
-  g.finite = isfinite(d) && s < 0x7C00;
+  g.finite = isfinite(d);
   if (g.finite) {
+    if (s > 0x7BFF) s = 0x7BFF;  // the quotient of 65504 L is beyond 65504 as fp32 has it
     if (!covers(s, L, d, err)) ++s;
     else if (s > 0 && covers(s - 1, L, d, err)) --s;
     if (s == 0) s = 0x3C00;      // 1, only for a group of zeros
