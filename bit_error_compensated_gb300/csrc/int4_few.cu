@@ -133,7 +133,11 @@ __device__ __forceinline__ void load_tokens(const T* row, int64_t k, int64_t dep
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = k + i < depth ? row[k + i] : 0.0f;
     }
-    // The upper 8 bits of the significand, the next, and the rest; an infinity is its own first part.
+    // The upper 8 bits of the significand, the next, and the rest; an infinity is
+    // its own first part, and so is a NaN once the sum has made it CUDA's (one with
+    // its bits set in the lower half only would leave an infinity).
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __fadd_rn(v[i], 0.0f);
 #pragma unroll
     for (int part = 0; part < 3; ++part)
 #pragma unroll
