@@ -98,14 +98,22 @@ __device__ __forceinline__ int block_of(int64_t total, int64_t tile, int blocks)
 }
 
 // Of a whole block of THREADS threads.  LEAST: tiles that a block has at least
-// where there are few.  `shared`: THREADS / 32 + 3 words of 8 bytes.
+// where there are few.  `shared`: THREADS / 16 + 3 words of 8 bytes.
+//
+// Starts that fall and rise again may give several sequences the same rows.  Where
+// these are more in sum than there are tokens, nothing is computed or counted: a
+// large batch's could keep the kernel busy for hours.
 template <int R, int TILE, int THREADS, int LEAST>
 __device__ __forceinline__ Range block_range(const AttentionArgs& a, int64_t* shared, int* bad) {
   constexpr int kWarps = THREADS / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.batch.sequences;
   Range r;
   r.s = {0, 0, 0, 0, 0};
-  auto divide = [&]() {
+  auto divide = [&](int64_t rows) {
+    if (rows > a.batch.tokens) {
+      *bad |= kBadRows;
+      r.total = 0;
+    }
     r.blocks = r.total < (int64_t)gridDim.x * LEAST ? (int)((r.total + LEAST - 1) / LEAST) : (int)gridDim.x;
     const int c = (int)blockIdx.x < r.blocks ? blockIdx.x : r.blocks;
     r.begin = r.blocks ? range_begin(r.total, c, r.blocks) : 0;
@@ -116,7 +124,8 @@ __device__ __forceinline__ Range block_range(const AttentionArgs& a, int64_t* sh
   };
   if (n <= 32) {                         // each warp for itself, a lane a sequence
     if (lane < n) r.s = sequence_of(a.batch, a.cache.page_shift, lane, bad);
-    const int64_t each = sequence_tiles<R, TILE>(a, r.s, lane), mine = each * a.cache.heads;
+    const int64_t rows = __reduce_add_sync(kFull, (uint32_t)r.s.rows);     // 32 times 2^20 at the most
+    const int64_t each = rows > a.batch.tokens ? 0 : sequence_tiles<R, TILE>(a, r.s, lane), mine = each * a.cache.heads;
     int64_t prefix = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -124,7 +133,7 @@ __device__ __forceinline__ Range block_range(const AttentionArgs& a, int64_t* sh
       if (lane >= off) prefix += other;
     }
     r.total = __shfl_sync(kFull, prefix, 31);
-    divide();
+    divide(rows);
     if (r.begin == r.end) return r;
     const int owner = __ffs(__ballot_sync(kFull, prefix > r.begin)) - 1;
     r.sequence = owner;
@@ -137,31 +146,44 @@ __device__ __forceinline__ Range block_range(const AttentionArgs& a, int64_t* sh
     r.s.place = __shfl_sync(kFull, r.s.place, owner);
     return r;
   }
-  int64_t mine = 0, sum = 0;             // tiles of the last sequence looked at, of all that this thread has
-  auto tiles_of = [&](int i, int* report) {
+  int64_t mine = 0, sum = 0, rows = 0;   // tiles of the last sequence looked at; tiles, and rows, of all that this thread has
+  auto tiles_of = [&](int i, int* report, int64_t* rows) {
     Sequence s = {0, 0, 0, 0, 0};
     if (i < n) s = sequence_of(a.batch, a.cache.page_shift, i, report);
+    *rows += s.rows;
+    if (__any_sync(kFull, *rows > a.batch.tokens)) return (int64_t)0;
     return sequence_tiles<R, TILE>(a, s, lane) * a.cache.heads;
   };
   for (int i0 = 0; i0 < n; i0 += THREADS) {
-    mine = tiles_of(i0 + tid, bad);
+    mine = tiles_of(i0 + tid, bad, &rows);
     sum += mine;
   }
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
-  if (lane == 0) shared[warp] = sum;
+  for (int off = 16; off > 0; off >>= 1) {
+    sum += __shfl_xor_sync(kFull, sum, off);
+    rows += __shfl_xor_sync(kFull, rows, off);
+  }
+  if (lane == 0) {
+    shared[warp] = sum;
+    shared[kWarps + 3 + warp] = rows;
+  }
   __syncthreads();
   r.total = 0;
+  int64_t all_rows = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) r.total += shared[w];
-  divide();
+  for (int w = 0; w < kWarps; ++w) {
+    r.total += shared[w];
+    all_rows += shared[kWarps + 3 + w];
+  }
+  divide(all_rows);
   if (r.begin == r.end) return r;        // the whole block
   // The sequence that has `begin`: prefix sums of THREADS sequences at a time.
   int64_t before = 0;
   for (int i0 = 0; i0 < n; i0 += THREADS) {
     const int i = i0 + tid;
     int ignored = 0;
-    if (n > THREADS) mine = tiles_of(i, &ignored);
+    int64_t these = 0;
+    if (n > THREADS) mine = tiles_of(i, &ignored, &these);
     int64_t prefix = mine;               // inclusive, of the warp
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {

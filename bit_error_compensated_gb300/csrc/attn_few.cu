@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, (Few<D, BITS, NR>::kBlocks)) attenti
   constexpr int kRows = S::kRows, kStep = S::kStep, kTile = S::kTile, kSubs = kStep / 16;
   constexpr int kPairs = D / 16;                           // of columns that a thread has of O^T
   extern __shared__ __align__(128) uint8_t raw[];
-  __shared__ int64_t shared[kWarps + 3];
+  __shared__ int64_t shared[2 * kWarps + 3];
   __shared__ float factor[kRows], most[kWarps][kRows], weight[kWarps][kRows];
   __shared__ int2 seen[kRows];                             // keys [x, y) that a row sees
   uint8_t* const query = raw + (S::kBytes - S::kQuery);

@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const Atten
   using B = Bars<NT>;
   extern __shared__ uint8_t raw[];
   __shared__ __align__(8) uint64_t bars[B::kCount];
-  __shared__ int64_t shared[kThreads / 32 + 3];
+  __shared__ int64_t shared[kThreads / 16 + 3];
   __shared__ float apart[S::kRows];
   __shared__ int2 seen[S::kRows];                        // keys [x, y) that a row sees
   __shared__ uint32_t tmem_at;

@@ -638,7 +638,9 @@ typedef struct {
  * sequence's begin (lengths[i] less than its rows) are not written, read as
  * zeros and attend to nothing.  What the arrays hold is checked on the device:
  * rows past `tokens` and falling starts are left out and set the status word to
- * ECHO_ERR_SHAPE, and pages that are not in the cache (or in the table), whose
+ * ECHO_ERR_SHAPE (where starts that fall and rise again give more rows in sum than
+ * there are tokens, the attention computes nothing; rows that two sequences have
+ * are either one's), and pages that are not in the cache (or in the table), whose
  * tokens are not written, read as zeros and are hidden from attention, set it
  * to ECHO_ERR_ARG. */
 #define ECHO_BATCH_MAX_TOKENS 1048576
