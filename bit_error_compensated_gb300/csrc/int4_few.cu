@@ -155,9 +155,8 @@ __device__ __forceinline__ void load_tokens(const T* row, int64_t k, int64_t dep
 
 // Few tokens: each warp loads what it needs of them by itself.
 // OCTETS: of tokens; TALL: 16-channel parts of a block; WORDS: of a row's
-// window, a thread's (a window is 32 WORDS codes of one group); DEEP: windows
-// loaded at once.
-template <typename T, int OCTETS, int TALL, int WORDS, int DEEP, bool ALIGNED>
+// window, a thread's (a window is 32 WORDS codes of one group).
+template <typename T, int OCTETS, int TALL, int WORDS, bool ALIGNED>
 __global__ void __launch_bounds__(32 * kWarps, OCTETS * TALL == 1 ? 4 : OCTETS * TALL == 2 ? 3 : 2) linear4_kernel(const Linear4Args p) {
   constexpr int kRows = 16 * TALL, kCols = 8 * OCTETS, kWindow = 32 * WORDS, kParts = parts<T>();
   __shared__ float total[kWarps][kCols][kRows + 1];
@@ -192,73 +191,61 @@ __global__ void __launch_bounds__(32 * kWarps, OCTETS * TALL == 1 ? 4 : OCTETS *
 
   const int64_t windows = (p.depth + kWindow - 1) / kWindow;
 #pragma unroll 1
-  for (int64_t first = warp; first < windows; first += DEEP * kWarps) {
-    uint32_t w[DEEP][2 * TALL][WORDS], word[DEEP][2 * TALL];
+  for (int64_t window = warp; window < windows; window += kWarps) {
+    uint32_t w[2 * TALL][WORDS], word[2 * TALL];
 #pragma unroll
-    for (int d = 0; d < DEEP; ++d) {
-      const int64_t window = first + d * kWarps;
-      const bool there = window < windows;
-#pragma unroll
-      for (int i = 0; i < 2 * TALL; ++i) {
-        load_codes<WORDS, ALIGNED>(codes[i], there ? window * (kWindow / 2) + 4 * WORDS * quad : bytes, bytes, w[d][i]);
-        word[d][i] = there ? load_free4(meta[i] + window * kWindow / p.group) : 0;
-      }
+    for (int i = 0; i < 2 * TALL; ++i) {
+      load_codes<WORDS, ALIGNED>(codes[i], window * (kWindow / 2) + 4 * WORDS * quad, bytes, w[i]);
+      word[i] = load_free4(meta[i] + window * kWindow / p.group);
     }
     // The tokens' loads follow the codes', before any of them is used (16-bit
     // ones: three parts of fp32 ones would not fit registers).
     constexpr bool kEarly = sizeof(T) == 2;
-    uint32_t early[kEarly ? DEEP : 1][WORDS][OCTETS][kParts][4];
+    const int64_t k = window * kWindow + 8 * WORDS * quad;
+    uint32_t early[kEarly ? WORDS : 1][OCTETS][kParts][4];
     if constexpr (kEarly)
 #pragma unroll
-      for (int d = 0; d < DEEP; ++d)
+      for (int n = 0; n < WORDS; ++n)
 #pragma unroll
-        for (int n = 0; n < WORDS; ++n)
+        for (int o = 0; o < OCTETS; ++o) load_tokens<T, ALIGNED>(x[o], k + 8 * n, p.depth, early[n][o]);
+    float part[TALL][OCTETS][4] = {};
+    uint32_t zero[2 * TALL];
 #pragma unroll
-          for (int o = 0; o < OCTETS; ++o)
-            load_tokens<T, ALIGNED>(x[o], (first + d * kWarps) * kWindow + 8 * (WORDS * quad + n), p.depth, early[d][n][o]);
+    for (int i = 0; i < 2 * TALL; ++i) zero[i] = Codes<T>::base_and(meta_zero(word[i]));
 #pragma unroll
-    for (int d = 0; d < DEEP; ++d) {
-      const int64_t k = (first + d * kWarps) * kWindow + 8 * WORDS * quad;
-      if (first + d * kWarps >= windows) break;            // the whole warp
-      float part[TALL][OCTETS][4] = {};
-      uint32_t zero[2 * TALL];
-#pragma unroll
-      for (int i = 0; i < 2 * TALL; ++i) zero[i] = Codes<T>::base_and(meta_zero(word[d][i]));
-#pragma unroll
-      for (int n = 0; n < WORDS; ++n) {
-        uint32_t lo[TALL][4], hi[TALL][4];
-#pragma unroll
-        for (int r = 0; r < TALL; ++r) {
-          turn<T>(w[d][2 * r][n], base, zero[2 * r], lo[r]);
-          turn<T>(w[d][2 * r + 1][n], base, zero[2 * r + 1], hi[r]);
-        }
-#pragma unroll
-        for (int o = 0; o < OCTETS; ++o) {
-          uint32_t b[kParts][4];
-          if constexpr (kEarly) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) b[0][i] = early[d][n][o][0][i];
-          } else {
-            load_tokens<T, ALIGNED>(x[o], k + 8 * n, p.depth, b);
-          }
-          __syncwarp();                                    // a row's ragged end parts the lanes; matrix instructions want them together
-#pragma unroll
-          for (int q = 0; q < kParts; ++q)
-#pragma unroll
-            for (int r = 0; r < TALL; ++r) {
-              Codes<T>::mma(part[r][o], lo[r], hi[r], b[q][0], b[q][1]);
-              Codes<T>::mma(part[r][o], lo[r] + 2, hi[r] + 2, b[q][2], b[q][3]);
-            }
-        }
-      }
+    for (int n = 0; n < WORDS; ++n) {
+      uint32_t lo[TALL][4], hi[TALL][4];
 #pragma unroll
       for (int r = 0; r < TALL; ++r) {
-        const float s0 = meta_step(word[d][2 * r]), s1 = meta_step(word[d][2 * r + 1]);
-#pragma unroll
-        for (int o = 0; o < OCTETS; ++o)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sum[r][o][i] = fmaf(part[r][o][i], i < 2 ? s0 : s1, sum[r][o][i]);
+        turn<T>(w[2 * r][n], base, zero[2 * r], lo[r]);
+        turn<T>(w[2 * r + 1][n], base, zero[2 * r + 1], hi[r]);
       }
+#pragma unroll
+      for (int o = 0; o < OCTETS; ++o) {
+        uint32_t b[kParts][4];
+        if constexpr (kEarly) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) b[0][i] = early[n][o][0][i];
+        } else {
+          load_tokens<T, ALIGNED>(x[o], k + 8 * n, p.depth, b);
+        }
+        __syncwarp();                                      // a row's ragged end parts the lanes; matrix instructions want them together
+#pragma unroll
+        for (int q = 0; q < kParts; ++q)
+#pragma unroll
+          for (int r = 0; r < TALL; ++r) {
+            Codes<T>::mma(part[r][o], lo[r], hi[r], b[q][0], b[q][1]);
+            Codes<T>::mma(part[r][o], lo[r] + 2, hi[r] + 2, b[q][2], b[q][3]);
+          }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < TALL; ++r) {
+      const float s0 = meta_step(word[2 * r]), s1 = meta_step(word[2 * r + 1]);
+#pragma unroll
+      for (int o = 0; o < OCTETS; ++o)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[r][o][i] = fmaf(part[r][o][i], i < 2 ? s0 : s1, sum[r][o][i]);
     }
   }
 #pragma unroll
@@ -414,7 +401,7 @@ bool rows_aligned(const Linear4Args& p) {
   return on_boundary(p.codes, 16) && (p.channels == 1 || p.ld_codes % 16 == 0) && (p.ranks == 1 || p.rank_codes % 16 == 0) &&
          on_boundary(p.x, 16) && (p.tokens == 1 || p.ld_x % in16 == 0) && (p.ranks == 1 || p.rank_x % in16 == 0);
 }
-template <typename T, int OCTETS, int TALL, int WORDS, int DEEP>
+template <typename T, int OCTETS, int TALL, int WORDS>
 cudaError_t launch_direct(const Linear4Args& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((p.channels + 16 * TALL - 1) / (16 * TALL)),
@@ -424,8 +411,8 @@ cudaError_t launch_direct(const Linear4Args& p, cudaStream_t s) {
   cudaLaunchAttribute overlapped = overlapped_launch();
   cfg.attrs = &overlapped;
   cfg.numAttrs = 1;
-  return rows_aligned<T>(p) ? cudaLaunchKernelEx(&cfg, linear4_kernel<T, OCTETS, TALL, WORDS, DEEP, true>, p)
-                            : cudaLaunchKernelEx(&cfg, linear4_kernel<T, OCTETS, TALL, WORDS, DEEP, false>, p);
+  return rows_aligned<T>(p) ? cudaLaunchKernelEx(&cfg, linear4_kernel<T, OCTETS, TALL, WORDS, true>, p)
+                            : cudaLaunchKernelEx(&cfg, linear4_kernel<T, OCTETS, TALL, WORDS, false>, p);
 }
 template <typename T, int OCTETS, int WORDS>
 cudaError_t launch_tiled(const Linear4Args& p, int sms, cudaStream_t s) {
@@ -469,9 +456,9 @@ cudaError_t launch(const Linear4Args& p, int sms, cudaStream_t s) {
   // and four ranks of 1024 deep 7.9, 10.1; 16 x 14336 x 4096: 23, 21).
   const int64_t blocks = (p.channels + 31) / 32 * p.ranks;
   const bool many = blocks * 4 >= 3 * sms;
-  if (p.tokens <= 8) return many ? launch_direct<T, 1, 2, WORDS, 1>(p, s) : launch_direct<T, 1, 1, WORDS, 1>(p, s);
+  if (p.tokens <= 8) return many ? launch_direct<T, 1, 2, WORDS>(p, s) : launch_direct<T, 1, 1, WORDS>(p, s);
   if (p.tokens <= 16 && p.ranks * p.channels * p.depth <= (int64_t)1 << 25)
-    return many ? launch_direct<T, 2, 2, WORDS, 1>(p, s) : launch_direct<T, 2, 1, WORDS, 1>(p, s);
+    return many ? launch_direct<T, 2, 2, WORDS>(p, s) : launch_direct<T, 2, 1, WORDS>(p, s);
   if (p.tokens <= 16) return launch_tiled<T, 2, WORDS>(p, sms, s);
   return launch_tiled<T, sizeof(T) == 4 ? 2 : 4, WORDS>(p, sms, s);      // (three parts of fp32 tokens: 16 at once)
 }
