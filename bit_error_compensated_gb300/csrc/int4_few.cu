@@ -451,13 +451,15 @@ cudaError_t launch(const Linear4Args& p, int sms, cudaStream_t s) {
   // 32 channels a block halve the loads of the tokens' elements, if there are
   // blocks enough (one token, 14336 x 4096: 11.4 us, with 16 channels 13.9; 7 x
   // 1111 x 2051: 5.6 us with 16, 8.1 with 32).  Of 9 to 16 tokens those loads
-  // are as many as the codes' in each warp, and of large weights they cost more
-  // than shared memory does (16 x 4096 x 4096: 7.5 us, through shared memory 9.8,
-  // and four ranks of 1024 deep 7.9, 10.1; 16 x 14336 x 4096: 23, 21).
+  // are as many as the codes' in each warp (in fp32 twice, and parts are made of
+  // them), and of large weights they cost more than shared memory does.  16 tokens,
+  // by themselves and through shared memory: 2^24 weights (4096 x 4096) 7.4 and
+  // 9.7 us, 2^25 12.2 and 13.6, 14336 x 4096 23.1 and 21.2; in fp32 2^20 (1024 x
+  // 1024) 4.6 and 9.3, 2^22 7.9 and 9.1, 2^24 14.6 and 12.6, 2^25 22.2 and 19.0.
   const int64_t blocks = (p.channels + 31) / 32 * p.ranks;
   const bool many = blocks * 4 >= 3 * sms;
   if (p.tokens <= 8) return many ? launch_direct<T, 1, 2, WORDS>(p, s) : launch_direct<T, 1, 1, WORDS>(p, s);
-  if (p.tokens <= 16 && p.ranks * p.channels * p.depth <= (int64_t)1 << 25)
+  if (p.tokens <= 16 && p.ranks * p.channels * p.depth <= (int64_t)1 << (sizeof(T) == 4 ? 23 : 25))
     return many ? launch_direct<T, 2, 2, WORDS>(p, s) : launch_direct<T, 2, 1, WORDS>(p, s);
   if (p.tokens <= 16) return launch_tiled<T, 2, WORDS>(p, sms, s);
   return launch_tiled<T, sizeof(T) == 4 ? 2 : 4, WORDS>(p, sms, s);      // (three parts of fp32 tokens: 16 at once)
