@@ -340,15 +340,15 @@ __device__ __forceinline__ float reciprocal(float v) {
 // the other keys' weights below f16's least: a row of zeros has a step of 1 by
 // definition.)
 //
-// A row's m is a whole number, so that scaling by a difference of two of them
-// rounds nothing.  It is raised when a score passes it by kMostWeight, so weights
-// are 2^15 at the most, and then to AHEAD above the score less kMostWeight, so the
-// largest is 2^(14 - AHEAD) at the least.  11 bits are left to weights down to
-// 2^-14, those below have a step of 2^-24: of the largest weight, with AHEAD 4 and
-// 8, 2^-24 and 2^-20, and 2^-34 and 2^-30.
+// A row's m is raised when a score passes it by kMostWeight, so weights are 2^15 at
+// the most, and then to AHEAD above the score less kMostWeight.  So the weight that
+// raises it is a power of two, 2^(15 - AHEAD), and exact: where one key has most of a
+// row, nothing is lost of it.  11 bits are left to weights down to 2^-14, those below
+// have a step of 2^-24: with AHEAD 4 and 8, 2^-25 and 2^-21, and 2^-35 and 2^-31, of
+// the largest.
 constexpr float kMostWeight = 15.0f;
 template <int AHEAD>
-__device__ __forceinline__ float raised(float m, float top) { return fmaxf(m, ceilf(top) - (kMostWeight - AHEAD)); }
+__device__ __forceinline__ float raised(float m, float top) { return fmaxf(m, top - (kMostWeight - AHEAD)); }
 
 // A value's step.  A place that was never written may have a step of 0 and codes
 // of 0: its value adds nothing, but its weight counts.  With a step far below fp16's

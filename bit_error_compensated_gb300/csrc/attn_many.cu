@@ -49,7 +49,7 @@ constexpr int kSlots = 4;                               // of steps: tiles whose
 constexpr int kWarpsWeights = 16, kWarpsKeys = 4, kWarpsValues = 4;
 constexpr int kIssuer = kWarpsWeights + kWarpsKeys + kWarpsValues, kThreads = 32 * (kIssuer + 4);
 constexpr int kWeightRegs = 88, kTurnRegs = 56, kIssueRegs = 40;
-// (4, as attn_few.cu has it for nothing: a prompt of 8192 in 779 us; 6: 757, 7: 746, 8: 735)
+// (4, as attn_few.cu has it for nothing: a prompt of 8192 takes 6% longer, 6: 3%, 7: 1%)
 constexpr int kAhead = 8;
 static_assert(4 * kWeightRegs + 2 * kTurnRegs + kIssueRegs <= 7 * 72, "a split above the launch's registers never ends");
 

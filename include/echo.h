@@ -697,10 +697,10 @@ int echo_cache_read(const echo_cache* cache, const echo_batch* batch, int dtype,
  * Codes less their zero point, and values less what their step exceeds a power
  * of two by (1 to 2, for steps from 2^-14 to 2^6), are exact in the 16-bit operands
  * of the matrix instructions; sums, maxima and steps are fp32.  w_j times that
- * rest is rounded to 11 bits; where it is below 2^-20 of the largest that a row
- * has met, to a multiple of 2^-30 of that (2^-24 and 2^-34 in batches of at most
- * 64 rows of queries a sequence and head of the cache, on average), and the sum of w_j has no
- * part in this.  A repeated call gives the same bits; another batch may split a
+ * rest is rounded to 11 bits; where it is below 2^-21 of the largest that a row
+ * has met, to a multiple of 2^-31 of that (2^-25 and 2^-35 in batches of at most
+ * 64 rows of queries a sequence and head of the cache, on average).  The sum of w_j
+ * has no part in this.  A repeated call gives the same bits; another batch may split a
  * sequence differently and round differently.
  */
 int echo_attention(const echo_cache* cache, const echo_batch* batch, int64_t heads, int dtype,

@@ -92,3 +92,28 @@ def test_a_row_of_zeros_under_a_dominant_key_leaves_the_row(bits, dim, new, lead
     exact, _, _ = ref.attention(cache, q, starts, lengths, table, 1.0)
     off = (out.double() - exact).norm(dim=-1) / exact.norm(dim=-1)
     assert off.max().item() <= 4 * (2.0 ** -12 + 2.0 ** (lead - below(new))) + 2.0 ** -9
+
+
+@pytest.mark.parametrize("lead", [17.1, 17.37, 17.6, 17.9])
+@pytest.mark.parametrize("bits,dim,new", [(8, 128, 1), (4, 64, 5), (8, 128, 90), (4, 256, 90)])
+def test_the_weight_of_a_dominant_key_is_exact(bits, dim, new, lead):
+    """One key of 2048, the first, has all but 2^(11 - lead) of the row: its weight is
+    a power of two, so that out is off by its own rounding, 2^-12 of what the others
+    add, and fp32's errors (an error of its own weight is in both sums; scores of 12
+    and the exponential are off by 2^-18, of the others' part; the sums' 2048
+    additions of parts of 2^-17 by 2^-23 each)."""
+    from bit_error_compensated_gb300 import echo
+    keys, page = 2048, 64
+    g = gen(int(10 * lead) + dim)
+    cache, table, q = one_loud_key(bits, dim, keys, 0, "zeros", lead, 0.0, int(10 * lead) + dim)
+    v = torch.randn(keys, dim, generator=g, device="cuda")
+    code, s, z = ref.groups(v, bits)
+    cache.codes[:, 1, 0] = ref.pack(code, bits).view(keys // page, page, -1)
+    cache.meta[:, 1, 0] = ref.words(s, z).view(keys // page, page)
+    q = q.half().expand(new, 1, dim).contiguous()
+    out = torch.full_like(q, 7)
+    echo.echo_attention(cache, tensors([0, new], [keys], table), q, out, scale=1.0, causal=False)
+    exact, _, _ = ref.attention(cache, q, [0, new], [keys], table, 1.0, causal=False)
+    size = (s * (code.double() - z)).abs().amax()
+    limit = ref.half_step(q.dtype) * exact.abs() * (1 + 2.0 ** -9) + 2.0 ** -12 * 2.0 ** (11 - lead) * size + 2.0 ** -20 * size
+    assert ((out.double() - exact).abs() <= limit).all()
