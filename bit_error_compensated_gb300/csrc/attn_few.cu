@@ -21,9 +21,9 @@
 // blocks have had are joined by a second kernel.
 //
 // One GB300, 32 heads to 8 of 128, GPU time a call: 64 ragged sequences up to
-// 16384, 4 bits, in 163 us (4.1 TB/s: bound by the instructions that turn
-// codes), 4 x 131072 of 8 bits in 178 (6.2 TB/s: memory); one token over 2000
-// keys in 9.7, 131000 in 46.
+// 16384, 4 bits, in 164 us (4.1 TB/s: bound by the instructions that turn
+// codes), 4 x 131072 of 8 bits in 180 (6.2 TB/s: memory); one token over 2000
+// keys in 10, 131000 in 47.
 #include "attn_common.h"
 
 namespace echo {
@@ -687,8 +687,9 @@ cudaError_t launch(const AttentionArgs& a, int sms, cudaStream_t s) {
 }
 // How many eights of rows a unit has: a unit's keys cost about as much as four
 // eights do by themselves, so the fewest of units * (4 + eights), among what
-// registers hold.  (35 rows of 64, 16 sequences up to 6000: 36 us with five
-// eights, 41 with six.)
+// registers hold.  (16 sequences of 8000 keys, 8 heads, 4 bits, one unit of 2, 3 and
+// 4 eights of rows of 128: 65, 76 and 92 us; of 2 to 6 eights of rows of 64: 49, 55,
+// 70, 76 and 88; of 128 two units of 3 and of 4: 121 and 147.)
 template <int D>
 int eights(int64_t rows) {
   constexpr int kMost = D == 64 ? 6 : D == 128 ? 4 : 2;
@@ -746,6 +747,9 @@ cudaError_t launch_join(const AttentionArgs& a, int blocks, int rows, cudaStream
 }
 
 // Up to as many rows a sequence this file's kernels run, for more attn_many.cu's.
+// 16 sequences of 8000 keys, 4 bits, here and there: 64 rows of 64 107 and 157 us, 96
+// 135 and 158, 128 193 and 160; of 128 147 and 176, 219 and 178, 270 and 180; of 256
+// (4 heads; 48 rows 141 and 158) 176 and 158, 254 and 160, 322 and 166.
 constexpr int64_t kFewRows = 64;
 
 cudaError_t launch_attention(const AttentionArgs& a, int sms, cudaStream_t s) {

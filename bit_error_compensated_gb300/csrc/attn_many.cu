@@ -24,13 +24,13 @@
 // as they are, and a row is one warp's alone.
 //
 // One GB300: 2048 tokens (32 heads to 8, of 128) over 32768 keys of 4 bits in
-// 1211 us, 936 TFLOP/s; a prompt of 8192 in 732 us, 750.  A tile of 256 rows and
+// 1217 us, 932 TFLOP/s; a prompt of 8192 in 741 us, 742.  A tile of 256 rows and
 // 128 keys takes 5100 cycles, of which the matrix instructions need 2100.  What
 // it is nearest to is shared memory: operands take 1536 cycles of it, the
 // warps' accesses 3100 (steps 1600, codes turned 570, barriers, and loads of
 // codes from L2); issue slots are 59% busy.  Four warps a tile of rows, with four
-// rows a lane, load steps half as often and wait longer for each other: 1172 and
-// 735 us, and 107 for a prompt of 2048 (95).
+// rows a lane, load steps half as often and wait longer for each other: when that
+// was measured 1172 us (1211), and 107 for a prompt of 2048 (95).
 //
 // Every wait is bounded; one that gives up ends the call with a status
 // (echo_serving_status): the block's other warps leave at their next wait, and
