@@ -796,7 +796,8 @@ class Cache(_Described):
         self._at = at
 
     def _pack(self) -> bytes:
-        if self._at is None or self._now() != self._at:
+        codes, meta = self.codes, self.meta       # (_now, without another call)
+        if (codes.data_ptr(), meta.data_ptr(), codes.numel(), meta.numel()) != self._at:
             self._check()
         return self._packed
 
@@ -840,7 +841,9 @@ class CacheBatch(_Described):
         self._at = at
 
     def _pack(self, tokens: int) -> bytes:
-        if self._at is None or self._now() != self._at:
+        starts, lengths, table = self.starts, self.lengths, self.table
+        if self._at is None or (starts.data_ptr(), lengths.data_ptr(), table.data_ptr(), starts.numel(), lengths.numel(),
+                                table.numel(), table.stride(0)) != self._at:
             self._check()
         packed = self._packed.get(tokens)
         if packed is None:
@@ -869,7 +872,16 @@ def _current_device() -> int:
     return _raw_device()
 
 
-_raw_device = None
+def _capturing() -> bool:
+    """Whether the current stream is being captured."""
+    global _raw_capturing
+    if _raw_capturing is None:
+        import torch
+        _raw_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
+    return _raw_capturing()
+
+
+_raw_device = _raw_capturing = None
 
 
 def _serving_device(cache: Cache, batch: CacheBatch, t) -> int:
@@ -926,12 +938,15 @@ def echo_attention(cache: Cache, batch: CacheBatch, q, out, scale: float | None 
     heads a multiple of the cache's; scale 1 / sqrt(head_dim) if None; window:
     the last tokens that a token sees (0: all up to itself); lse fp32
     [tokens][heads], contiguous, or None."""
-    import torch
     shape, dtype = q.shape, q.dtype
     if len(shape) != 3 or shape[2] != cache.head_dim:
         raise ValueError(f"q: shape {tuple(shape)}, expected (tokens, heads, {cache.head_dim})")
-    if dtype is not torch.bfloat16 and dtype is not torch.float16:
-        raise ValueError(f"q: dtype {dtype}, expected torch.bfloat16 or torch.float16")
+    code = _CODES.get(dtype)
+    if not code:                                             # fp32's is 0
+        import torch
+        if dtype is not torch.bfloat16 and dtype is not torch.float16:
+            raise ValueError(f"q: dtype {dtype}, expected torch.bfloat16 or torch.float16")
+        code = _dtype_code(dtype)
     tokens, heads, dim = shape
     if heads < 1 or heads % cache.heads:
         raise ValueError(f"q: {heads} heads, expected a multiple of the cache's {cache.heads}")
@@ -941,6 +956,7 @@ def echo_attention(cache: Cache, batch: CacheBatch, q, out, scale: float | None 
     at_out = _expect_heads(out, "out", dtype, shape, device)
     at_lse = None
     if lse is not None:
+        import torch
         _expect_contiguous(lse, "lse", torch.float32, (tokens, heads), device)
         at_lse = lse.data_ptr()
     nbytes = _attention_bytes.get((device, dim))             # the size depends on nothing else
@@ -948,10 +964,9 @@ def echo_attention(cache: Cache, batch: CacheBatch, q, out, scale: float | None 
         nbytes = _lib.echo_attention_workspace_bytes(packed, rows, heads)
         if nbytes:
             _attention_bytes[device, dim] = nbytes
-    args = (packed, rows, heads, ECHO_BF16 if dtype is torch.bfloat16 else ECHO_F16, at_q, at_out,
-            dim ** -0.5 if scale is None else scale, causal, window, at_lse)
+    args = (packed, rows, heads, code, at_q, at_out, dim ** -0.5 if scale is None else scale, causal, window, at_lse)
     raw = _stream(stream, device)
-    if stream is None and not torch.cuda.is_current_stream_capturing():
+    if stream is None and not _capturing():
         with _workspace_lock:                                # a call's two kernels follow each other
             kept = _kept_workspace(nbytes, device, raw)      # (until after the launches)
             status = _lib.echo_attention(*args, kept[0], nbytes, raw)
