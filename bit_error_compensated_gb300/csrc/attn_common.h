@@ -361,7 +361,7 @@ __device__ __forceinline__ float value_step(uint32_t meta) { return max_nan(meta
 __device__ __forceinline__ uint32_t value_scale(uint32_t meta) { return min(max(meta & 0x7C00u, 0x0400u), 0x5000u); }
 // f = s / S, exactly.
 __device__ __forceinline__ float value_factor(uint32_t meta) {
-  return __fmul_rn(value_step(meta), __uint_as_float((127u + 15u << 23) - (value_scale(meta) << 13)));
+  return __fmul_rn(value_step(meta), __uint_as_float(((127u + 15u) << 23) - (value_scale(meta) << 13)));
 }
 
 // Query rows as f16, scaled by a power of two that takes the row's largest

@@ -10,11 +10,11 @@
 // (the other way round half of an instruction is idle where a head of the cache
 // serves 8 queries or fewer).  A code c behind the bits of 1024 is the f16
 // number 1024 + c (of 4 bits at bit 4: 1024 + 16 c), from which one instruction
-// for two codes takes c - z, exactly; steps are multiplied into scores and
-// weights in fp32.  (f16 holds c * 2^-24 as it stands, as a subnormal, but the
-// matrix instructions align their sums by exponents that leave such a number 14
-// bits.)  Of a value's step its power of two goes into the value and the rest, 1 to
-// 2, into the weight, which is f16 below a bound on its row (attn_common.h).
+// for two codes takes c - z, exactly.  (f16 holds c * 2^-24 as it stands, as a
+// subnormal, but the matrix instructions align their sums by exponents that leave
+// such a number 14 bits.)  A key's step is multiplied into its score in fp32; of a
+// value's its power of two goes into the value and the rest, 1 to 2, into the
+// weight, which is f16 below a bound on its row (attn_common.h).
 //
 // Blocks take equal shares of the batch's tiles (attn_common.h); four warps
 // take a tile's keys and join at the unit's end, and parts of units that several
